@@ -235,6 +235,8 @@ def _plain_route(s):
     T, E = z.shape
     score = torch.softmax(z, -1) if s["score"] == "softmax" else torch.sigmoid(z)
     choice = score if s["bias_v"] is None else score + s["bias_v"].double()
+    # a masked expert is not chosen, whatever its bias
+    choice = choice.masked_fill(z == -math.inf, -math.inf)
     if s["groups"] > 1:
         G = s["groups"]
         by_group = choice.reshape(T, G, E // G)
@@ -243,7 +245,9 @@ def _plain_route(s):
         keep.scatter_(1, _stable_top(top, s["topk_groups"]), True)
         choice = by_group.masked_fill(~keep[..., None], -math.inf).reshape(T, E)
     ids = _stable_top(choice, s["k"])
-    w = torch.gather(score, 1, ids)
+    none = torch.gather(choice, 1, ids) == -math.inf
+    w = torch.gather(score, 1, ids).masked_fill(none, 0.0)
+    ids = ids.masked_fill(none, -1)
     if s["renormalize"]:
         w = w / (w.sum(-1, keepdim=True) + 1e-20)
     return {"ids": ids.to(torch.int32), "weights": (w * s["scale"]).float()}
@@ -392,6 +396,7 @@ def exact(case, seed):
         else:
             p = 1 / (1 + torch.exp(-z))
         c = p.clone() if s["bias_v"] is None else p + s["bias_v"].double()
+        c[torch.isneginf(z)] = -math.inf
         if s["groups"] > 1:
             G, n = s["groups"], s["E"] // s["groups"]
             c = c.reshape(T, G, n)
@@ -400,7 +405,10 @@ def exact(case, seed):
             c[torch.arange(T, device=z.device)[:, None], order[:, s["topk_groups"]:]] = -math.inf
             c = c.reshape(T, G * n)
         ids = torch.argsort(-c, dim=-1, stable=True)[:, :s["k"]]
-        w = p[torch.arange(T, device=z.device)[:, None], ids]
+        at = torch.arange(T, device=z.device)[:, None]
+        left = ~torch.isneginf(c[at, ids])
+        w = torch.where(left, p[at, ids], 0.0)
+        ids = torch.where(left, ids, -1)
         if s["renormalize"]:
             w = w / (w.sum(-1, keepdim=True) + 1e-20)
         return {"ids": ids.to(torch.int32), "weights": w * s["scale"]}
