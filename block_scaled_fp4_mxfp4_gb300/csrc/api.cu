@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "internal.h"
+#include "moe.h"
 #include "mxfp4.h"
 
 using namespace mxfp4;
@@ -81,6 +82,29 @@ bool encoder()
     });
     return g_encode != nullptr;
 }
+
+}  // namespace
+
+namespace mxfp4 {
+
+bool current_device_sms(int *sms) { return current_device(sms) == MXFP4_OK; }
+
+bool encode_map_2d(CUtensorMap *out, CUtensorMapDataType dtype, const void *base, uint64_t inner, uint64_t rows,
+                   uint64_t stride, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swz,
+                   CUtensorMapL2promotion promo)
+{
+    if (!encoder()) return false;
+    const cuuint64_t dims[2] = {inner, rows};
+    const cuuint64_t strides[1] = {stride};
+    const cuuint32_t box[2] = {box_inner, box_rows};
+    const cuuint32_t estr[2] = {1u, 1u};
+    return g_encode(out, dtype, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+                    promo, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace mxfp4
+
+namespace {
 
 struct MapKey {
     uintptr_t ptr;
@@ -838,8 +862,9 @@ mxfp4_status_t mxfp4_get_device_error(int *code)
     const int g = read_and_clear_gemm_error();
     const int f = read_and_clear_fused_error();
     const int pg = read_and_clear_gemm_pair_error();
-    if (g < 0 || f < 0 || pg < 0) return MXFP4_ERR_CUDA;
-    *code = g != 0 ? g : (f != 0 ? 16 + f : (pg != 0 ? 32 + pg : 0));
+    const int me = read_and_clear_moe_error();
+    if (g < 0 || f < 0 || pg < 0 || me < 0) return MXFP4_ERR_CUDA;
+    *code = g != 0 ? g : (f != 0 ? 16 + f : (pg != 0 ? 32 + pg : (me != 0 ? 48 + me : 0)));
     return MXFP4_OK;
 }
 

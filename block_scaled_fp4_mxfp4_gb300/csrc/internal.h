@@ -63,6 +63,15 @@ cudaError_t prepare_kernel(Kern kern, uint32_t smem_bytes, KernelOnce &once, int
     return cudaSuccess;
 }
 
+// ------------------------------------------------------------------ api.cu
+// The current device's SM count in *sms; false if it is not a GB300.
+bool current_device_sms(int *sms);
+// Encodes a 2-D tensor map (no caching): `inner` elements a row, `rows` rows
+// `stride` bytes apart, box {box_inner, box_rows}, zero fill out of bounds.
+bool encode_map_2d(CUtensorMap *out, CUtensorMapDataType dtype, const void *base, uint64_t inner, uint64_t rows,
+                   uint64_t stride, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swz,
+                   CUtensorMapL2promotion promo);
+
 // ---------------------------------------------------------------- quant.cu
 // Every quantization launch uses programmatic dependent launch and reads A
 // only after the preceding grid has completed. feeds_gemm: the next launch

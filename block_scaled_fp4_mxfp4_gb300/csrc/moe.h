@@ -1,0 +1,59 @@
+// Host-side interface between the mixture-of-experts C-ABI layer (moe_api.cu)
+// and its kernel translation units. Not part of the public ABI.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace mxfp4 {
+
+// ---------------------------------------------------- add_rmsnorm_quant.cu
+cudaError_t launch_add_rmsnorm_mxfp8(const void *X, int64_t ldx, const void *res, int64_t ldr, const void *w, bool f16,
+                                     float eps, int64_t M, int64_t K, void *H, int64_t ldh, void *Y, int64_t ldy,
+                                     void *Aq, int64_t ldq, void *sf, cudaStream_t stream);
+
+// ------------------------------------------------------------ moe_route.cu
+struct RouteParams {
+    const void *logits;
+    const float *bias;      // [E] or null
+    int32_t *ids;
+    float *weights;
+    int64_t ldl, T;
+    int E, k, groups, topk_groups, group_top;
+    int sigmoid, renorm;
+    float scale;
+};
+cudaError_t launch_moe_route(const RouteParams &p, int dtype, int num_sms, cudaStream_t stream);
+
+// ---------------------------------------------------------- moe_experts.cu
+// Workspace of one call, and the token tile its two products share.
+struct MoeLayout {
+    int nt;                 // tokens of a tile (columns of the accumulator)
+    int max_tiles;          // most token tiles T * k choices can need
+    int chunks;             // blocks of the placing kernel
+    size_t hist, off, tile0, src, pos, act, act_sf, y, total;
+};
+bool moe_layout(int64_t T, int k, int E, int64_t H, int64_t I, MoeLayout *out);
+
+struct MoeArgs {
+    const uint8_t *xq;
+    int64_t ldx;
+    const uint8_t *x_sf;
+    const int32_t *ids;
+    const float *weights;
+    const uint8_t *w13_sf, *w2_sf;
+    uint16_t *out;
+    int64_t ldo;
+    int64_t T;
+    int k, E, H, I;
+    uint8_t *ws;
+    CUtensorMap tm_x;       // Xq [T, H] u8, box {128, 1}: rows gathered by index
+    CUtensorMap tm_w13;     // [E * 2I, H] 4-bit, box {128, 64}, unpacked to a byte each
+    CUtensorMap tm_act;     // activations [rows, I] u8, box {128, 16}
+    CUtensorMap tm_w2;      // [E * H, I] 4-bit, box {128, 64}, unpacked
+};
+cudaError_t launch_moe_experts(const MoeArgs &a, const MoeLayout &l, cudaStream_t stream);
+int read_and_clear_moe_error();
+
+}  // namespace mxfp4

@@ -1,0 +1,725 @@
+// The experts' products of a mixture-of-experts layer (mxfp4_moe_experts):
+// MXFP8 activations x MXFP4 weights on the tensor cores (tcgen05.mma
+// kind::mxf8f6f4), for row counts that only the GPU knows.
+//
+// Mathematics, for token t and its choice j of expert e:
+//   act = MXFP8(silu(x_t G_e^T) * (x_t U_e^T)),  out_t = sum_j w_tj (act W2_e^T).
+//
+// Launches, each one starting while the last drains (programmatic dependent
+// launch):
+//   place    sorts the T * k choices by expert (counts in shared memory, prefix
+//            sums, ranks): row r of the sorted order comes from token src[r],
+//            choice i sits in row pos[i]; tile0[e] counts tiles of NT rows.
+//            More than kChunk choices take several blocks and a counting launch
+//            before it.
+//   product1 rows gathered by TMA from the unsorted activations; epilogue
+//            silu(g) * u, MXFP8, to the workspace in sorted order
+//   product2 act x W2^T, bf16 rows to the workspace
+//   combine  out_t = sum_j w_tj row[pos[t, j]], in the order of j: no atomics, so
+//            the result does not depend on the order of the sorted rows
+//
+// Both products swap the operands: the 128 rows of the MMA are weight rows, its
+// columns are tokens. Weights, which dominate the traffic of a small batch, fill
+// every row of the tensor core whatever the batch, and N follows the rows that an
+// expert has (a multiple of 16). Product 1 puts 64 rows of G and the 64 rows of U
+// of the same channels in one tile, so the epilogue has both of a channel.
+#include <algorithm>
+#include <cstring>
+
+#include "internal.h"
+#include "moe.h"
+#include "mxfp8_math.cuh"
+#include "ptx.cuh"
+
+namespace mxfp4 {
+
+__device__ int g_moe_error;
+
+namespace {
+
+constexpr int kMaxExperts = 512;
+constexpr int kPlaceThreads = 1024;
+constexpr int kPerThread = 8;
+constexpr int kChunk = kPlaceThreads * kPerThread;   // choices a placing block takes
+
+// ------------------------------------------------------------------ placing
+
+struct PlaceParams {
+    const int32_t *ids;
+    int *hist;      // [chunks][E], more than one chunk only
+    int *off;       // [E + 1] first sorted row of each expert
+    int *tile0;     // [E + 1] first token tile of each expert
+    int *src;       // [R] token of a sorted row
+    int *pos;       // [R] sorted row of a choice, -1: left out
+    int R, k, E, chunks, nt;
+};
+
+__global__ void __launch_bounds__(kPlaceThreads) moe_count_kernel(const PlaceParams p)
+{
+    __shared__ int cnt[kMaxExperts];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) cnt[e] = 0;
+    __syncthreads();
+    const int begin = blockIdx.x * kChunk;
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+        const int c = begin + i * kPlaceThreads + threadIdx.x;
+        if (c < p.R) {
+            const int e = p.ids[c];
+            if (e >= 0 && e < p.E) atomicAdd(&cnt[e], 1);
+        }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) p.hist[static_cast<size_t>(blockIdx.x) * p.E + e] = cnt[e];
+}
+
+__global__ void __launch_bounds__(kPlaceThreads) moe_place_kernel(const PlaceParams p)
+{
+    __shared__ int total[kMaxExperts];    // rows of an expert
+    __shared__ int next[kMaxExperts];     // rows of it before this block's; then the next free row
+    __shared__ int off[kMaxExperts + 1];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int tid = threadIdx.x, begin = blockIdx.x * kChunk;
+    int mine[kPerThread];
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+        const int c = begin + i * kPlaceThreads + tid;
+        const int e = c < p.R ? p.ids[c] : -1;
+        mine[i] = e >= 0 && e < p.E ? e : -1;
+    }
+    if (p.chunks == 1) {
+        for (int e = tid; e < p.E; e += blockDim.x) total[e] = next[e] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kPerThread; ++i)
+            if (mine[i] >= 0) atomicAdd(&total[mine[i]], 1);
+    } else {
+        for (int e = tid; e < p.E; e += blockDim.x) {
+            int all = 0, before = 0;
+            for (int c = 0; c < p.chunks; ++c) {
+                const int n = p.hist[static_cast<size_t>(c) * p.E + e];
+                all += n;
+                if (c < static_cast<int>(blockIdx.x)) before += n;
+            }
+            total[e] = all;
+            next[e] = before;
+        }
+    }
+    __syncthreads();
+    if (tid < 32) {
+        // prefix sums of rows and tiles: lane l takes experts [l * per, (l + 1) * per)
+        const int per = (p.E + 31) / 32;
+        int rows = 0, tiles = 0;
+        for (int i = 0; i < per; ++i) {
+            const int e = tid * per + i;
+            if (e < p.E) {
+                rows += total[e];
+                tiles += (total[e] + p.nt - 1) / p.nt;
+            }
+        }
+        int r0 = rows, t0 = tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int a = __shfl_up_sync(0xffffffffu, r0, o), b = __shfl_up_sync(0xffffffffu, t0, o);
+            if (tid >= o) {
+                r0 += a;
+                t0 += b;
+            }
+        }
+        const int all_rows = __shfl_sync(0xffffffffu, r0, 31), all_tiles = __shfl_sync(0xffffffffu, t0, 31);
+        r0 -= rows;
+        t0 -= tiles;
+        for (int i = 0; i < per; ++i) {
+            const int e = tid * per + i;
+            if (e < p.E) {
+                off[e] = r0;
+                if (blockIdx.x == 0) {
+                    p.off[e] = r0;
+                    p.tile0[e] = t0;
+                }
+                r0 += total[e];
+                t0 += (total[e] + p.nt - 1) / p.nt;
+            }
+        }
+        if (tid == 0 && blockIdx.x == 0) {
+            p.off[p.E] = all_rows;
+            p.tile0[p.E] = all_tiles;
+        }
+    }
+    __syncthreads();
+    for (int e = tid; e < p.E; e += blockDim.x) next[e] += off[e];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+        const int c = begin + i * kPlaceThreads + tid;
+        if (c < p.R) {
+            int r = -1;
+            if (mine[i] >= 0) {
+                r = atomicAdd(&next[mine[i]], 1);
+                p.src[r] = c / p.k;
+            }
+            p.pos[c] = r;
+        }
+    }
+}
+
+// ----------------------------------------------------------------- products
+
+struct ProductParams {
+    CUtensorMap tm_w;       // weights, unpacked on load: box 128 elements x 64 rows
+    CUtensorMap tm_t;       // tokens: product 1 gathers rows of Xq; product 2 loads 16-row boxes of act
+    const uint8_t *w_sf;    // blocked weight scales, one buffer an expert
+    const uint8_t *x_sf;    // product 1: blocked scales of Xq
+    uint8_t *act;           // [rows, I] E4M3 (product 1 writes, product 2 reads through tm_t)
+    uint8_t *act_sf;        // [tiles][I / 128][NT / 128 rounded up][512]
+    uint16_t *y;            // product 2: [rows, H] bf16
+    const int *off, *tile0, *src;
+    int E, H, I;
+    uint64_t wait_ns;
+};
+
+__host__ __device__ constexpr uint32_t tmem_pow2(uint32_t n)
+{
+    return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : n <= 256 ? 256 : 512;
+}
+
+template <int NT, int STAGES>
+struct ProductCfg {
+    static constexpr int NTB = (NT + 127) / 128;           // scale blocks of a token tile
+    static constexpr uint32_t W_BYTES = 128 * 128;         // 128 weight rows, a byte an element
+    static constexpr uint32_t T_BYTES = NT * 128;
+    static constexpr uint32_t SFW_OFF = W_BYTES + T_BYTES;
+    static constexpr uint32_t SFT_OFF = SFW_OFF + 512;
+    static constexpr uint32_t STAGE_BYTES = (SFT_OFF + NTB * 512 + 1023) / 1024 * 1024;
+    static constexpr int EPI_LD = 132;                     // floats of a staged column
+    static constexpr uint32_t EPI_BYTES = 32 * EPI_LD * 4;
+    static constexpr uint32_t TAB_BYTES = 2 * (kMaxExperts + 4) * 4;
+    static constexpr uint32_t BAR_BYTES = 512;
+    static constexpr uint32_t SMEM_BYTES = STAGES * STAGE_BYTES + EPI_BYTES + TAB_BYTES + BAR_BYTES + 1024;
+    static constexpr uint32_t SF_COLS = 4 + 4 * NTB;
+    static constexpr uint32_t TMEM_COLS = tmem_pow2(2 * NT + STAGES * SF_COLS);
+    static constexpr int LAG = STAGES / 2;                 // stages whose gathered scales are in flight
+    static_assert(NT % 32 == 0 && NT <= 256, "token tile");
+    static_assert(2 * NT + STAGES * SF_COLS <= 512, "TMEM budget");
+    static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+    static_assert((2 * STAGES + 6) * 8 + 32 <= BAR_BYTES, "barrier area");
+};
+
+// One unit of work: 128 weight rows x one token tile of an expert.
+struct Unit {
+    int e, m, tile, row0, rows;
+};
+
+// Units of one expert are consecutive, its token tiles innermost: the blocks that
+// work on the same weights at the same time read them from L2.
+__device__ __forceinline__ Unit decode_unit(int u, int mw, int E, int nt, const int *off, const int *tile0)
+{
+    Unit w;
+    const int q = u / mw;
+    int lo = 0, hi = E - 1;   // the last expert with tile0[e] <= q; it has tiles, since tile0[e + 1] > q
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (tile0[mid] <= q)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    w.e = lo;
+    const int t0 = tile0[lo], nj = tile0[lo + 1] - t0;
+    const int local = u - t0 * mw;
+    w.m = local / nj;
+    const int j = local - w.m * nj;
+    w.tile = t0 + j;
+    w.row0 = off[lo] + j * nt;
+    w.rows = min(nt, off[lo + 1] - w.row0);
+    return w;
+}
+
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// FIRST: product 1 (tokens x [G; U], SwiGLU, MXFP8), else product 2. Warps:
+//   0    loads: weights by TMA (lane 0), token rows by TMA (all lanes), and in
+//        product 2 the scales
+//   1    TMEM owner; lane 0 copies scales to TMEM and issues the MMAs
+//   2    product 1: scales of weights and gathered tokens (4 and 8 byte copies)
+//   4-7  epilogue of a finished tile while the next one's mainloop runs (two
+//        accumulators)
+template <bool FIRST, int NT, int STAGES>
+__global__ void __launch_bounds__(256, 1) moe_product_kernel(const __grid_constant__ ProductParams p)
+{
+    using Cfg = ProductCfg<NT, STAGES>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float *epi = reinterpret_cast<float *>(smem + STAGES * Cfg::STAGE_BYTES);
+    int *off = reinterpret_cast<int *>(smem + STAGES * Cfg::STAGE_BYTES + Cfg::EPI_BYTES);
+    int *tile0 = off + kMaxExperts + 4;
+    uint64_t *full = reinterpret_cast<uint64_t *>(tile0 + kMaxExperts + 4);
+    uint64_t *empty = full + STAGES;
+    uint64_t *accf = empty + STAGES;      // [2] accumulator complete
+    uint64_t *acc_empty = accf + 2;       // [2] accumulator drained
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    volatile int *epi_go = abort_flag + 1;   // [2]
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(full + s, FIRST ? 2 : 1);
+            mbar_init(empty + s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(accf + b, 1);
+            mbar_init(acc_empty + b, 128);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&p.tm_w);
+        tma_prefetch_desc(&p.tm_t);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, Cfg::TMEM_COLS);
+        tmem_relinquish();
+    }
+    grid_dependency_wait();
+    grid_launch_dependents();
+    for (int e = threadIdx.x; e <= p.E; e += blockDim.x) {
+        off[e] = __ldcg(p.off + e);
+        tile0[e] = __ldcg(p.tile0 + e);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem_sf = tmem + 2 * NT;
+    const int K = FIRST ? p.H : p.I;
+    const int kc = K >> 7;                                  // stages of a tile
+    const int mw = FIRST ? p.I >> 6 : p.H >> 7;             // weight tiles of an expert
+    const int wrows = FIRST ? 2 * p.I : p.H;                // weight rows of an expert
+    const int units = tile0[p.E] * mw;
+    int issued = 0;
+
+    if (warp == 0) {
+        const uint64_t pol_w = policy_evict_first(), pol_t = policy_evict_last();
+        int gs = 0;
+        bool ok = true;
+        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;   // one verdict for the warp
+            const Unit w = decode_unit(u, mw, p.E, NT, off, tile0);
+            const int n16 = (w.rows + 15) >> 4;
+            // weight rows of the two halves of the tile
+            const int r0 = w.e * wrows + w.m * (FIRST ? 64 : 128);
+            const int r1 = r0 + (FIRST ? p.I : 64);
+            int4 quad[(NT + 127) / 128];
+            if constexpr (FIRST) {
+                // this lane's rows 4 q .. 4 q + 3, q = lane and lane + 32; past the
+                // tile's last row, that row again (its columns are not stored)
+#pragma unroll
+                for (int i = 0; i < (NT + 127) / 128; ++i) {
+                    const int r = 4 * (lane + 32 * i);
+                    const int *s = p.src + w.row0;
+                    quad[i] = make_int4(__ldcg(s + min(r, w.rows - 1)), __ldcg(s + min(r + 1, w.rows - 1)),
+                                        __ldcg(s + min(r + 2, w.rows - 1)), __ldcg(s + min(r + 3, w.rows - 1)));
+                }
+            }
+            // an unpacking load counts the packed bytes it reads, 64 a row
+            const uint32_t bytes = Cfg::W_BYTES / 2 + n16 * 2048u + (FIRST ? 0u : 512u + Cfg::NTB * 512u);
+            for (int ks = 0; ks < kc; ++ks, ++gs) {
+                const int slot = gs % STAGES;
+                if (gs >= STAGES)
+                    ok = mbar_wait_warp(empty + slot, ((gs / STAGES) - 1) & 1, &g_moe_error, kErrWaitEmpty, p.wait_ns);
+                if (!ok) {
+                    *abort_flag = 1;
+                    break;
+                }
+                uint8_t *st = smem + slot * Cfg::STAGE_BYTES;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(full + slot, bytes);
+                    tma_load_2d(st, &p.tm_w, ks * 128, r0, full + slot, pol_w);
+                    tma_load_2d(st + 8192, &p.tm_w, ks * 128, r1, full + slot, pol_w);
+                }
+                __syncwarp();
+                if constexpr (FIRST) {
+#pragma unroll
+                    for (int i = 0; i < (NT + 127) / 128; ++i) {
+                        const int q = lane + 32 * i;
+                        if (q < 4 * n16)
+                            tma_gather4(st + Cfg::W_BYTES + q * 512, &p.tm_t, ks * 128, quad[i], full + slot, pol_t);
+                    }
+                } else {
+                    if (lane < n16)
+                        tma_load_2d(st + Cfg::W_BYTES + lane * 2048, &p.tm_t, ks * 128, w.row0 + 16 * lane, full + slot,
+                                    pol_t);
+                    if (lane == 0) {
+                        bulk_load(st + Cfg::SFW_OFF,
+                                  p.w_sf + (static_cast<size_t>(w.e * mw + w.m) * kc + ks) * 512, 512, full + slot, pol_w);
+                        bulk_load(st + Cfg::SFT_OFF,
+                                  p.act_sf + (static_cast<size_t>(w.tile) * kc + ks) * (Cfg::NTB * 512), Cfg::NTB * 512,
+                                  full + slot, pol_t);
+                    }
+                }
+                issued = gs + 1;
+            }
+        }
+    } else if (warp == 1 && lane == 0) {
+        int gs = 0, ul = 0, commits[2] = {0, 0};
+        for (int u = blockIdx.x; u < units; u += gridDim.x, ++ul) {
+            const Unit w = decode_unit(u, mw, p.E, NT, off, tile0);
+            const int buf = ul & 1;
+            if (ul >= 2 && !mbar_wait(acc_empty + buf, ((ul >> 1) - 1) & 1, &g_moe_error, kErrWaitAccum, p.wait_ns)) {
+                *abort_flag = 1;
+                break;
+            }
+            tc_fence_after();
+            const int n = (w.rows + 15) & ~15;
+            const uint32_t idesc = idesc_w4a8(n);
+            const uint32_t d = tmem + buf * NT;
+            bool ok = true;
+            for (int ks = 0; ks < kc; ++ks, ++gs) {
+                const int slot = gs % STAGES;
+                if (!mbar_wait(full + slot, (gs / STAGES) & 1, &g_moe_error, kErrWaitFull, p.wait_ns)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                uint8_t *st = smem + slot * Cfg::STAGE_BYTES;
+                // scale copies and MMAs of one thread run in order
+                const uint32_t tsfw = tmem_sf + slot * Cfg::SF_COLS, tsft = tsfw + 4;
+                tc_cp_scale_block(tsfw, sdesc_scale(smem_u32(st + Cfg::SFW_OFF)));
+                tc_cp_scale_block(tsft, sdesc_scale(smem_u32(st + Cfg::SFT_OFF)));
+                if (Cfg::NTB > 1 && n > 128) tc_cp_scale_block(tsft + 4, sdesc_scale(smem_u32(st + Cfg::SFT_OFF + 512)));
+                const uint64_t ad = sdesc_sw128(smem_u32(st)), bd = sdesc_sw128(smem_u32(st + Cfg::W_BYTES));
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_mxf8f6f4(d, ad + 2 * kk, bd + 2 * kk, idesc_with_sf_ids(idesc, kk, kk), tsfw, tsft,
+                                 (ks > 0 || kk > 0) ? 1u : 0u);
+                tc_commit(empty + slot);
+            }
+            tc_commit(accf + buf);
+            ++commits[buf];
+            if (!ok) {
+                *abort_flag = 1;
+                break;
+            }
+        }
+        // no MMA may be running when TMEM is released
+        for (int b = 0; b < 2; ++b)
+            if (commits[b] > 0) mbar_wait(accf + b, (commits[b] - 1) & 1, &g_moe_error, kErrWaitDrain);
+    } else if (FIRST && warp == 2) {
+        int gs = 0, done = 0;
+        bool ok = true;
+        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;   // one verdict for the warp
+            const Unit w = decode_unit(u, mw, p.E, NT, off, tile0);
+            // 64 channels are half of a 128-row scale block: 8 of each 16 bytes, of G and of U
+            const size_t blk = static_cast<size_t>(wrows >> 7) * w.e + (w.m >> 1);
+            const uint8_t *g_sf = p.w_sf + blk * kc * 512 + lane * 16 + (w.m & 1) * 8;
+            const uint8_t *u_sf = g_sf + static_cast<size_t>(p.I >> 7) * kc * 512;
+            const uint8_t *t_sf[NT / 32];
+#pragma unroll
+            for (int i = 0; i < NT / 32; ++i) {
+                const int t = __ldcg(p.src + w.row0 + min(lane + 32 * i, w.rows - 1));
+                t_sf[i] = p.x_sf + static_cast<size_t>(t >> 7) * kc * 512 + (t & 31) * 16 + ((t & 127) >> 5) * 4;
+            }
+            for (int ks = 0; ks < kc; ++ks, ++gs) {
+                const int slot = gs % STAGES;
+                if (gs >= STAGES)
+                    ok = mbar_wait_warp(empty + slot, ((gs / STAGES) - 1) & 1, &g_moe_error, kErrWaitEmpty, p.wait_ns);
+                if (!ok) {
+                    *abort_flag = 1;
+                    break;
+                }
+                uint8_t *st = smem + slot * Cfg::STAGE_BYTES;
+                cp_async<8>(st + Cfg::SFW_OFF + lane * 16, g_sf + ks * 512);
+                cp_async<8>(st + Cfg::SFW_OFF + lane * 16 + 8, u_sf + ks * 512);
+#pragma unroll
+                for (int i = 0; i < NT / 32; ++i)
+                    if (32 * i < w.rows)
+                        cp_async<4>(st + Cfg::SFT_OFF + (i >> 2) * 512 + lane * 16 + (i & 3) * 4, t_sf[i] + ks * 512);
+                cp_async_commit();
+                if (gs - done >= Cfg::LAG) {
+                    cp_async_wait<Cfg::LAG>();
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full + done % STAGES);
+                    ++done;
+                }
+            }
+        }
+        cp_async_wait<0>();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0)
+            for (; done < gs; ++done) mbar_arrive(full + done % STAGES);
+    } else if (warp >= 4) {
+        const int q = warp & 3, t = threadIdx.x - 128;
+        const int col = t >> 2, part = t & 3;      // this thread's token column and quarter of the staged rows
+        int ul = 0;
+        for (int u = blockIdx.x; u < units; u += gridDim.x, ++ul) {
+            const Unit w = decode_unit(u, mw, p.E, NT, off, tile0);
+            const int buf = ul & 1;
+            if (t == 0) {
+                const bool ok = mbar_wait(accf + buf, (ul >> 1) & 1, &g_moe_error, kErrWaitAccum, p.wait_ns);
+                if (!ok) *abort_flag = 1;
+                epi_go[buf] = ok && !*abort_flag;
+            }
+            epilogue_sync();
+            if (!epi_go[buf]) break;
+            tc_fence_after();
+            const uint32_t trow = tmem + buf * NT + (static_cast<uint32_t>(q * 32) << 16);
+            for (int c0 = 0; c0 < w.rows; c0 += 32) {
+                // 32 columns of the 128 rows through shared memory, so that a
+                // thread gets neighbouring rows (channels) of one column (token)
+                uint32_t v[32];
+                tmem_ld32(trow + c0, v);
+                tmem_ld_wait();
+                if (c0 + 32 >= w.rows) {
+                    tc_fence_before();
+                    mbar_arrive(acc_empty + buf);
+                }
+#pragma unroll
+                for (int j = 0; j < 32; ++j) epi[j * Cfg::EPI_LD + q * 32 + lane] = __uint_as_float(v[j]);
+                epilogue_sync();
+                const bool live = c0 + col < w.rows;
+                const size_t row = static_cast<size_t>(w.row0) + c0 + col;
+                if constexpr (FIRST) {
+                    // 16 channels a thread; two neighbours share a block of 32
+                    const float *g = epi + col * Cfg::EPI_LD + 16 * part;
+                    float a[16];
+                    uint32_t amax = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 gv = *reinterpret_cast<const float4 *>(g + 4 * i);
+                        const float4 uv = *reinterpret_cast<const float4 *>(g + 64 + 4 * i);
+                        a[4 * i] = __fdividef(gv.x, 1.0f + __expf(-gv.x)) * uv.x;
+                        a[4 * i + 1] = __fdividef(gv.y, 1.0f + __expf(-gv.y)) * uv.y;
+                        a[4 * i + 2] = __fdividef(gv.z, 1.0f + __expf(-gv.z)) * uv.z;
+                        a[4 * i + 3] = __fdividef(gv.w, 1.0f + __expf(-gv.w)) * uv.w;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) amax = max(amax, __float_as_uint(a[i]) & 0x7FFFFFFFu);
+                    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                    const uint32_t b = mxfp8_scale_byte(amax);
+                    const float inv = mxfp8_scale_inverse(b);
+                    const uint32_t b2 = __shfl_down_sync(0xffffffffu, b, 2);
+                    if (live) {
+                        uint4 c;
+                        c.x = e4m3x4_rn(a[0] * inv, a[1] * inv, a[2] * inv, a[3] * inv);
+                        c.y = e4m3x4_rn(a[4] * inv, a[5] * inv, a[6] * inv, a[7] * inv);
+                        c.z = e4m3x4_rn(a[8] * inv, a[9] * inv, a[10] * inv, a[11] * inv);
+                        c.w = e4m3x4_rn(a[12] * inv, a[13] * inv, a[14] * inv, a[15] * inv);
+                        *reinterpret_cast<uint4 *>(p.act + row * p.I + 64 * w.m + 16 * part) = c;
+                        if (part == 0) {
+                            const int r = c0 + col;
+                            uint8_t *sf = p.act_sf +
+                                          (static_cast<size_t>(w.tile) * (p.I >> 7) + (w.m >> 1)) * (Cfg::NTB * 512) +
+                                          (r >> 7) * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4 + (w.m & 1) * 2;
+                            *reinterpret_cast<uint16_t *>(sf) = static_cast<uint16_t>(b | (b2 << 8));
+                        }
+                    }
+                } else {
+                    const float *s = epi + col * Cfg::EPI_LD + 32 * part;
+                    if (live) {
+                        uint4 *o = reinterpret_cast<uint4 *>(p.y + row * p.H + 128 * w.m + 32 * part);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float4 x = *reinterpret_cast<const float4 *>(s + 8 * i);
+                            const float4 z = *reinterpret_cast<const float4 *>(s + 8 * i + 4);
+                            const __nv_bfloat162 h[4] = {__floats2bfloat162_rn(x.x, x.y), __floats2bfloat162_rn(x.z, x.w),
+                                                         __floats2bfloat162_rn(z.x, z.y), __floats2bfloat162_rn(z.z, z.w)};
+                            o[i] = *reinterpret_cast<const uint4 *>(h);
+                        }
+                    }
+                }
+                epilogue_sync();   // the staging buffer is reused
+            }
+        }
+    }
+    __syncwarp();
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0 && lane == 0) {
+        // copies still in flight (only after an abort) land before the block leaves
+        for (int i = max(0, issued - STAGES); i < issued; ++i)
+            mbar_wait(full + (i % STAGES), (i / STAGES) & 1, &g_moe_error, kErrWaitDrain);
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, Cfg::TMEM_COLS);
+    }
+}
+
+// ------------------------------------------------------------------ combine
+
+struct CombineParams {
+    const uint16_t *y;
+    const int *pos;
+    const float *weights;
+    uint16_t *out;
+    int64_t ldo;
+    int k, H;
+};
+
+// out[t] = sum_j w[t, j] * y[pos[t, j]]: eight channels a thread, one token a block row.
+__global__ void __launch_bounds__(256) moe_combine_kernel(const CombineParams p)
+{
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int64_t t = blockIdx.x;
+    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * 8;
+    if (c >= p.H) return;
+    float acc[8] = {};
+    for (int j = 0; j < p.k; ++j) {
+        const int r = __ldcg(p.pos + t * p.k + j);
+        if (r < 0) continue;
+        const float w = p.weights[t * p.k + j];
+        const uint4 v = __ldcg(reinterpret_cast<const uint4 *>(p.y + static_cast<size_t>(r) * p.H + c));
+        const uint32_t *pv = &v.x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            acc[2 * i] = fmaf(w, __uint_as_float(pv[i] << 16), acc[2 * i]);
+            acc[2 * i + 1] = fmaf(w, __uint_as_float(pv[i] & 0xFFFF0000u), acc[2 * i + 1]);
+        }
+    }
+    const __nv_bfloat162 h[4] = {__floats2bfloat162_rn(acc[0], acc[1]), __floats2bfloat162_rn(acc[2], acc[3]),
+                                 __floats2bfloat162_rn(acc[4], acc[5]), __floats2bfloat162_rn(acc[6], acc[7])};
+    *reinterpret_cast<uint4 *>(p.out + t * p.ldo + c) = *reinterpret_cast<const uint4 *>(h);
+}
+
+// ------------------------------------------------------------------- launch
+
+template <class Kern, class P>
+cudaError_t launch_pdl(Kern kern, dim3 grid, dim3 block, size_t smem, cudaStream_t stream, const P &params)
+{
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, params);
+}
+
+template <bool FIRST, int NT, int STAGES>
+cudaError_t launch_product(const ProductParams &p, int64_t max_units, cudaStream_t stream)
+{
+    using Cfg = ProductCfg<NT, STAGES>;
+    auto kern = moe_product_kernel<FIRST, NT, STAGES>;
+    static KernelOnce once;
+    int sms = 0;
+    const cudaError_t e = prepare_kernel(kern, Cfg::SMEM_BYTES, once, &sms);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(max_units, std::max(1, sms)));
+    return launch_pdl(kern, dim3(grid), dim3(256), Cfg::SMEM_BYTES, stream, p);
+}
+
+template <bool FIRST>
+cudaError_t launch_product_nt(int nt, const ProductParams &p, int64_t max_units, cudaStream_t stream)
+{
+    return nt == 32 ? launch_product<FIRST, 32, 9>(p, max_units, stream)
+                    : launch_product<FIRST, 224, 4>(p, max_units, stream);
+}
+
+inline size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+}  // namespace
+
+bool moe_layout(int64_t T, int k, int E, int64_t H, int64_t I, MoeLayout *out)
+{
+    const int64_t R = T * k;
+    // a tile of 32 tokens leaves room for nine stages of weights in flight, one of
+    // 224 halves the reads of the weights again and again for long batches
+    out->nt = R <= 32 * static_cast<int64_t>(E) ? 32 : 224;
+    out->max_tiles = static_cast<int>(R / out->nt + std::min<int64_t>(E, R));
+    out->chunks = static_cast<int>((R + kChunk - 1) / kChunk);
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += up256(bytes);
+        return here;
+    };
+    out->hist = take(out->chunks > 1 ? static_cast<size_t>(out->chunks) * E * 4 : 0);
+    out->off = take((E + 1) * 4);
+    out->tile0 = take((E + 1) * 4);
+    out->src = take(static_cast<size_t>(R) * 4);
+    out->pos = take(static_cast<size_t>(R) * 4);
+    out->act = take(static_cast<size_t>(R) * I);
+    out->act_sf = take(static_cast<size_t>(out->max_tiles) * (I / 128) * ((out->nt + 127) / 128) * 512);
+    out->y = take(static_cast<size_t>(R) * H * 2);
+    out->total = at;
+    return true;
+}
+
+cudaError_t launch_moe_experts(const MoeArgs &a, const MoeLayout &l, cudaStream_t stream)
+{
+    PlaceParams pp;
+    pp.ids = a.ids;
+    pp.hist = reinterpret_cast<int *>(a.ws + l.hist);
+    pp.off = reinterpret_cast<int *>(a.ws + l.off);
+    pp.tile0 = reinterpret_cast<int *>(a.ws + l.tile0);
+    pp.src = reinterpret_cast<int *>(a.ws + l.src);
+    pp.pos = reinterpret_cast<int *>(a.ws + l.pos);
+    pp.R = static_cast<int>(a.T * a.k);
+    pp.k = a.k;
+    pp.E = a.E;
+    pp.chunks = l.chunks;
+    pp.nt = l.nt;
+    cudaError_t e;
+    if (l.chunks > 1) {
+        e = launch_pdl(moe_count_kernel, dim3(l.chunks), dim3(kPlaceThreads), 0, stream, pp);
+        if (e != cudaSuccess) return e;
+    }
+    e = launch_pdl(moe_place_kernel, dim3(l.chunks), dim3(kPlaceThreads), 0, stream, pp);
+    if (e != cudaSuccess) return e;
+
+    ProductParams p;
+    memset(&p, 0, sizeof(p));
+    p.x_sf = a.x_sf;
+    p.act = a.ws + l.act;
+    p.act_sf = a.ws + l.act_sf;
+    p.y = reinterpret_cast<uint16_t *>(a.ws + l.y);
+    p.off = pp.off;
+    p.tile0 = pp.tile0;
+    p.src = pp.src;
+    p.E = a.E;
+    p.H = a.H;
+    p.I = a.I;
+    p.wait_ns = wait_limit_ns();
+    p.tm_w = a.tm_w13;
+    p.tm_t = a.tm_x;
+    p.w_sf = a.w13_sf;
+    e = launch_product_nt<true>(l.nt, p, static_cast<int64_t>(l.max_tiles) * (a.I / 64), stream);
+    if (e != cudaSuccess) return e;
+    p.tm_w = a.tm_w2;
+    p.tm_t = a.tm_act;
+    p.w_sf = a.w2_sf;
+    e = launch_product_nt<false>(l.nt, p, static_cast<int64_t>(l.max_tiles) * (a.H / 128), stream);
+    if (e != cudaSuccess) return e;
+
+    CombineParams c;
+    c.y = p.y;
+    c.pos = pp.pos;
+    c.weights = a.weights;
+    c.out = a.out;
+    c.ldo = a.ldo;
+    c.k = a.k;
+    c.H = a.H;
+    return launch_pdl(moe_combine_kernel, dim3(static_cast<unsigned>(a.T), (a.H / 8 + 255) / 256), dim3(256), 0, stream, c);
+}
+
+int read_and_clear_moe_error()
+{
+    int v = 0, zero = 0;
+    if (cudaMemcpyFromSymbol(&v, g_moe_error, sizeof(int)) != cudaSuccess) return -1;
+    cudaMemcpyToSymbol(g_moe_error, &zero, sizeof(int));
+    return v;
+}
+
+}  // namespace mxfp4

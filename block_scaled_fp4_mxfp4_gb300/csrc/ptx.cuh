@@ -215,6 +215,37 @@ __device__ __forceinline__ void tma_load_2d(void *smem_dst, const CUtensorMap *t
         : "memory");
 }
 
+// Loads four rows y.x .. y.w of a 2-D tensor whose map has a box one row high,
+// columns from x on, into four consecutive box rows of shared memory.
+__device__ __forceinline__ void tma_gather4(void *smem_dst, const CUtensorMap *tm, int32_t x, const int4 &y,
+                                            uint64_t *bar, uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2], %8;" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(smem_u32(bar)), "r"(x), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w),
+        "l"(policy)
+        : "memory");
+}
+
+// Asynchronous copy of BYTES (4 or 8) from global to shared memory by ordinary
+// (generic-proxy) writes, tracked by the thread's cp.async groups.
+template <int BYTES>
+__device__ __forceinline__ void cp_async(void *smem_dst, const void *gsrc)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(smem_dst)), "l"(gsrc), "n"(BYTES)
+                 : "memory");
+}
+
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// Waits until at most N of this thread's cp.async groups are in flight.
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // 2-D tiled store of box {x (innermost, elements), y} from shared memory;
 // parts of the box outside the tensor are not written. Completion is tracked
 // by the issuing thread's bulk async-groups (bulk_commit / bulk_wait_*).
@@ -341,6 +372,19 @@ __device__ __forceinline__ void mma_nvf4(uint32_t d_tmem, uint64_t adesc, uint64
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+}
+
+// D[tmem] (+)= A[smem] x B[smem]^T of 8-bit containers with per-32 E8M0 scales
+// (kind::mxf8f6f4): element types and N from the instruction descriptor.
+__device__ __forceinline__ void mma_mxf8f6f4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
             d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
         : "memory");
@@ -516,6 +560,18 @@ __host__ __device__ constexpr uint32_t idesc_block_scaled(int n, bool ue8m0, int
            | (1u << 10)                                 // B format E2M1
            | (static_cast<uint32_t>(n >> 3) << 17)      // N / 8
            | ((ue8m0 ? 1u : 0u) << 23)                  // scale type
+           | (static_cast<uint32_t>(m >> 4) << 24);     // M / 16
+}
+
+// Instruction descriptor of a kind::mxf8f6f4 MMA: A E2M1 (16 codes in the low 8
+// bytes of each 16, as the unpacking TMA load leaves them), B E4M3, both K-major,
+// E8M0 scales.
+__host__ __device__ constexpr uint32_t idesc_w4a8(int n, int m = 128)
+{
+    return (5u << 7)                                    // A format E2M1
+           | (0u << 10)                                 // B format E4M3
+           | (static_cast<uint32_t>(n >> 3) << 17)      // N / 8
+           | (1u << 23)                                 // E8M0 scales
            | (static_cast<uint32_t>(m >> 4) << 24);     // M / 16
 }
 

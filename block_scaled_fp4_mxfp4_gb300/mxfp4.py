@@ -1,4 +1,4 @@
-"""Python binding of libmxfp4 (the C ABI in include/mxfp4.h).
+"""Python binding of libmxfp4 (the C ABI in include/mxfp4.h and include/mxfp4_moe.h).
 
 Argument marshalling only: every function passes device pointers, sizes and the
 current CUDA stream to the library entry point of the same name and raises
@@ -15,6 +15,7 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libmxfp4.so")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "mxfp4.h")
+MOE_HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "mxfp4_moe.h")
 
 _i64 = ctypes.c_int64
 _p = ctypes.c_void_p
@@ -124,6 +125,16 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.mxfp4_group_gemm.argtypes = [ctypes.POINTER(MxProblem), ctypes.c_int, _p, _sz, _p]
     L.mxfp4_group_gemm_plan.restype = _st
     L.mxfp4_group_gemm_plan.argtypes = [ctypes.POINTER(MxProblem), ctypes.c_int, ctypes.POINTER(Plan)]
+    _i, _f = ctypes.c_int, ctypes.c_float
+    L.mxfp8_add_rmsnorm_quantize.restype = _st
+    L.mxfp8_add_rmsnorm_quantize.argtypes = [_p, _i64, _p, _i64, _p, _i, _f, _i64, _i64, _p, _i64, _p, _i64, _p, _i64,
+                                             _p, _p]
+    L.moe_route.restype = _st
+    L.moe_route.argtypes = [_p, _i, _i64, _i64, _i, _p, _i, _i, _i, _i, _i, _i, _f, _p, _p, _p]
+    L.mxfp4_moe_experts_workspace_bytes.restype = _sz
+    L.mxfp4_moe_experts_workspace_bytes.argtypes = [_i64, _i, _i, _i64, _i64]
+    L.mxfp4_moe_experts.restype = _st
+    L.mxfp4_moe_experts.argtypes = [_p, _i64, _p, _p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i, _i, _i64, _i64, _p, _sz, _p]
     return L
 
 
@@ -418,6 +429,138 @@ def nvfp4_group_quant_gemm(groups, problems=None, workspace=None, stream=None):
     _check(_lib.nvfp4_group_quant_gemm(problems, len(problems), workspace.data_ptr(), workspace.numel(),
                                        _stream_ptr(stream)), "nvfp4_group_quant_gemm")
     return [g["c"] for g in groups]
+
+
+# ---------------------------------------------------- mixture of experts --
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+MOE_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _vec(t, name, dtype, shape):
+    """A contiguous CUDA tensor of exactly this type and shape."""
+    _dev(t, name, dtype)
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {tuple(shape)} tensor")
+    return t
+
+
+def _rows(t, name, dtype, shape):
+    """A row-major CUDA matrix of this type and shape, with any row stride."""
+    _dev(t, name, dtype, 2)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _ld(t):
+    # the stride of a single row is no distance (torch may give any value)
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 15) // 16 * 16
+
+
+def mxfp8_add_rmsnorm_quantize(X, weight, eps: float = 1e-6, residual=None, H=None, Y=None, Aq=None, A_sf=None,
+                               want_y: bool = False, stream=None):
+    """h = X + residual, y = RMSNorm(h) * weight, and y in MXFP8 (see
+    include/mxfp4_moe.h): X [M, K] bf16 or fp16 -> (Aq [M, K] u8 E4M3, blocked
+    E8M0 scales, h or None without a residual, y or None unless want_y or Y is
+    given). H may be X or residual (in place)."""
+    if X.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"X must be bf16 or fp16, got {X.dtype}")
+    _dev(X, "X", X.dtype, 2)
+    M, K = X.shape
+    _vec(weight, "weight", X.dtype, (K,))
+    if residual is not None:
+        _rows(residual, "residual", X.dtype, (M, K))
+        H = torch.empty((M, K), dtype=X.dtype, device=X.device) if H is None else H
+    if H is not None:
+        _rows(H, "H", X.dtype, (M, K))
+    if want_y and Y is None:
+        Y = torch.empty((M, K), dtype=X.dtype, device=X.device)
+    if Y is not None:
+        _rows(Y, "Y", X.dtype, (M, K))
+    if Aq is None:
+        Aq = torch.empty((M, (K + 15) // 16 * 16), dtype=torch.uint8, device=X.device)[:, :K]
+    _rows(Aq, "Aq", torch.uint8, (M, K))
+    need = sf_bytes(M, K, 32)
+    if A_sf is None:
+        A_sf = torch.empty(need, dtype=torch.uint8, device=X.device)
+    _dev(A_sf, "A_sf", torch.uint8)
+    if A_sf.numel() < need or not A_sf.is_contiguous():
+        raise ValueError(f"A_sf must be contiguous with at least {need} bytes")
+    opt = lambda t: (t.data_ptr(), _ld(t)) if t is not None else (None, 0)  # noqa: E731
+    _check(_lib.mxfp8_add_rmsnorm_quantize(X.data_ptr(), _ld(X), *opt(residual), weight.data_ptr(), _DTYPES[X.dtype],
+                                           float(eps), M, K, *opt(H), *opt(Y), Aq.data_ptr(), _ld(Aq),
+                                           A_sf.data_ptr(), _stream_ptr(stream)),
+           "mxfp8_add_rmsnorm_quantize")
+    return Aq, A_sf, H, Y
+
+
+def moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, topk_groups: int = 1,
+              group_top: int = 2, renormalize: bool = True, scale: float = 1.0, ids=None, weights=None, stream=None):
+    """Routing of tokens to experts (see include/mxfp4_moe.h): logits [T, E] bf16 /
+    fp16 / fp32 -> (ids [T, k] int32, weights [T, k] fp32)."""
+    if logits.dtype not in _DTYPES:
+        raise ValueError(f"logits must be bf16, fp16 or fp32, got {logits.dtype}")
+    if score not in MOE_SCORES:
+        raise ValueError(f"score must be one of {sorted(MOE_SCORES)}, got {score!r}")
+    _dev(logits, "logits", logits.dtype, 2)
+    T, E = logits.shape
+    if bias is not None:
+        _vec(bias, "bias", torch.float32, (E,))
+    if ids is None:
+        ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=logits.device)
+    if weights is None:
+        weights = torch.empty((T, max(k, 0)), dtype=torch.float32, device=logits.device)
+    _vec(ids, "ids", torch.int32, (T, k))
+    _vec(weights, "weights", torch.float32, (T, k))
+    _check(_lib.moe_route(logits.data_ptr(), _DTYPES[logits.dtype], _ld(logits), T, E,
+                          bias.data_ptr() if bias is not None else None, MOE_SCORES[score], groups, topk_groups,
+                          group_top, k, int(bool(renormalize)), float(scale), ids.data_ptr(), weights.data_ptr(),
+                          _stream_ptr(stream)),
+           "moe_route")
+    return ids, weights
+
+
+def moe_experts_workspace_bytes(T: int, k: int, E: int, H: int, I: int) -> int:
+    return int(_lib.mxfp4_moe_experts_workspace_bytes(T, k, E, H, I))
+
+
+def moe_experts_workspace(T: int, k: int, E: int, H: int, I: int, device="cuda") -> torch.Tensor:
+    """A workspace for mxfp4_moe_experts with up to T tokens (no initialisation needed)."""
+    return torch.empty(max(1, moe_experts_workspace_bytes(T, k, E, H, I)), dtype=torch.uint8, device=device)
+
+
+def mxfp4_moe_experts(Xq, X_sf, ids, weights, W13q, W13_sf, W2q, W2_sf, out=None, workspace=None, stream=None):
+    """The experts' products of a mixture-of-experts layer (see
+    include/mxfp4_moe.h): MXFP8 activations Xq [T, H] with blocked scales X_sf,
+    ids / weights [T, k], MXFP4 weights W13q [E, 2I, H/2] and W2q [E, H, I/2] with
+    scales [E, sf_bytes] -> out [T, H] bf16."""
+    _dev(Xq, "Xq", torch.uint8, 2)
+    T, H = Xq.shape
+    _dev(W13q, "W13q", torch.uint8, 3)
+    E, I = W13q.shape[0], W13q.shape[1] // 2
+    _vec(W13q, "W13q", torch.uint8, (E, 2 * I, H // 2))
+    _vec(W2q, "W2q", torch.uint8, (E, H, I // 2))
+    for name, t, n in (("X_sf", X_sf, sf_bytes(T, H, 32)), ("W13_sf", W13_sf, E * sf_bytes(2 * I, H, 32)),
+                       ("W2_sf", W2_sf, E * sf_bytes(H, I, 32))):
+        _dev(t, name, torch.uint8)
+        if t.numel() < n or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous with at least {n} bytes")
+    k = ids.shape[-1]
+    _vec(ids, "ids", torch.int32, (T, k))
+    _vec(weights, "weights", torch.float32, (T, k))
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=Xq.device)
+    _rows(out, "out", torch.bfloat16, (T, H))
+    if workspace is None:
+        workspace = moe_experts_workspace(T, k, E, H, I, Xq.device)
+    _dev(workspace, "workspace", torch.uint8, 1)
+    _check(_lib.mxfp4_moe_experts(Xq.data_ptr(), _ld(Xq), X_sf.data_ptr(), ids.data_ptr(), weights.data_ptr(),
+                                  W13q.data_ptr(), W13_sf.data_ptr(), W2q.data_ptr(), W2_sf.data_ptr(), out.data_ptr(),
+                                  _ld(out), T, k, E, H, I, workspace.data_ptr(), workspace.numel(),
+                                  _stream_ptr(stream)),
+           "mxfp4_moe_experts")
+    return out
 
 
 def _plan_dict(p: Plan) -> dict:

@@ -398,8 +398,9 @@ MXFP4_API mxfp4_status_t mxfp4_group_gemm_plan(const mxfp4_problem_t *problems, 
  * leave the split-K counters of its workspace nonzero, so clear the
  * workspace before reusing it after a nonzero code. This call synchronizes
  * the current device. *code receives 0 when no kernel reported an error;
- * otherwise 1..15 (single-CTA GEMM), 16 + c (fused kernel) or 32 + c
- * (CTA-pair GEMM), c naming the wait that gave up. */
+ * otherwise 1..15 (single-CTA GEMM), 16 + c (fused kernel), 32 + c
+ * (CTA-pair GEMM) or 48 + c (experts' products of mxfp4_moe.h), c naming the
+ * wait that gave up. */
 MXFP4_API mxfp4_status_t mxfp4_get_device_error(int *code);
 
 /* K-splits of the split-K paths. The planner takes, in this order: a tuning
