@@ -102,6 +102,13 @@ bool encode_map_2d(CUtensorMap *out, CUtensorMapDataType dtype, const void *base
                     promo, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_packed_map(const void *base, int64_t inner, int64_t rows, int64_t stride, int box_rows, CUtensorMap *out)
+{
+    return encode_map_2d(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, static_cast<uint64_t>(inner),
+                         static_cast<uint64_t>(rows), static_cast<uint64_t>(stride), 128u,
+                         static_cast<uint32_t>(box_rows), CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
 }  // namespace mxfp4
 
 namespace {

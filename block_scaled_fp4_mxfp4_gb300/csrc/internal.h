@@ -66,6 +66,10 @@ cudaError_t prepare_kernel(Kern kern, uint32_t smem_bytes, KernelOnce &once, int
 // ------------------------------------------------------------------ api.cu
 // The current device's SM count in *sms; false if it is not a GB300.
 bool current_device_sms(int *sms);
+// Tensor map of a packed FP4 matrix [rows, inner bytes] (row stride `stride`
+// bytes), box {128 bytes, box_rows}, 128-byte swizzle, zero fill out of bounds.
+// Encoded anew on every call.
+bool encode_packed_map(const void *base, int64_t inner, int64_t rows, int64_t stride, int box_rows, CUtensorMap *out);
 // Encodes a 2-D tensor map (no caching): `inner` elements a row, `rows` rows
 // `stride` bytes apart, box {box_inner, box_rows}, zero fill out of bounds.
 bool encode_map_2d(CUtensorMap *out, CUtensorMapDataType dtype, const void *base, uint64_t inner, uint64_t rows,

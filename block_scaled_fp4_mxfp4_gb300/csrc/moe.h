@@ -50,6 +50,8 @@ struct MoeArgs {
     uint8_t *ws;
     CUtensorMap tm_x;       // Xq [T, H] u8, box {128, 1}: rows gathered by index
     CUtensorMap tm_w13;     // [E * 2I, H] 4-bit, box {128, 64}, unpacked to a byte each
+    CUtensorMap tm_pw13;    // packed weights [E * 2I, H / 2] u8, box 128 bytes x 64 rows, 128-byte swizzle
+    CUtensorMap tm_pw2;     // the same of [E * H, I / 2]
     CUtensorMap tm_act;     // activations [rows, I] u8, box {128, 16}
     CUtensorMap tm_w2;      // [E * H, I] 4-bit, box {128, 64}, unpacked
 };

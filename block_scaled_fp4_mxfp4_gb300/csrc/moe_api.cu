@@ -118,6 +118,8 @@ mxfp4_status_t mxfp4_moe_experts(const void *Xq, int64_t ldx, const void *X_sf, 
     if (!Xq || !X_sf || !ids || !weights || !W13q || !W13_sf || !W2q || !W2_sf || !out || !workspace)
         return MXFP4_ERR_INVALID_ARG;
     if (ldx < H || ldo < H) return MXFP4_ERR_INVALID_ARG;
+    // rows of tokens are addressed in units of 16 bytes held in 32 bits
+    if (ldx / 16 > (int64_t(1) << 32) / T || I / 16 > (int64_t(1) << 32) / (T * k)) return MXFP4_ERR_UNSUPPORTED_SHAPE;
     if (ldx % 16 || ldo % 8 || !aligned(Xq, 16) || !aligned(X_sf, 16) || !aligned(ids, 4) || !aligned(weights, 4) ||
         !aligned(W13q, 32) || !aligned(W2q, 32) || !aligned(W13_sf, 16) || !aligned(W2_sf, 16) || !aligned(out, 16) ||
         !aligned(workspace, 256))
@@ -151,6 +153,8 @@ mxfp4_status_t mxfp4_moe_experts(const void *Xq, int64_t ldx, const void *X_sf, 
         encode_map_2d(&a.tm_act, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.ws + l.act, static_cast<uint64_t>(I),
                       static_cast<uint64_t>(T * k), static_cast<uint64_t>(I), 128u, 16u, CU_TENSOR_MAP_SWIZZLE_128B,
                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B) &&
+        encode_packed_map(W13q, H / 2, 2 * I * E, H / 2, 64, &a.tm_pw13) &&
+        encode_packed_map(W2q, I / 2, H * E, I / 2, 64, &a.tm_pw2) &&
         unpacked_fp4_map(&a.tm_w13, W13q, H, 2 * I * E) && unpacked_fp4_map(&a.tm_w2, W2q, I, H * E);
     if (!maps) return MXFP4_ERR_CUDA;
     return cuda_status(launch_moe_experts(a, l, static_cast<cudaStream_t>(stream)));

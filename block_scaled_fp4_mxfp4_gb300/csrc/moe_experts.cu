@@ -171,6 +171,8 @@ struct ProductParams {
     CUtensorMap tm_w;       // weights, unpacked on load: box 128 elements x 64 rows
     CUtensorMap tm_t;       // tokens: product 1 gathers rows of Xq; product 2 loads 16-row boxes of act
     const uint8_t *w_sf;    // blocked weight scales, one buffer an expert
+    const uint8_t *x;       // product 1: Xq, rows ldx bytes apart
+    int64_t ldx;
     const uint8_t *x_sf;    // product 1: blocked scales of Xq
     uint8_t *act;           // [rows, I] E4M3 (product 1 writes, product 2 reads through tm_t)
     uint8_t *act_sf;        // [tiles][I / 128][NT / 128 rounded up][512]
@@ -431,12 +433,12 @@ __global__ void __launch_bounds__(256, 1) moe_product_kernel(const __grid_consta
                     break;
                 }
                 uint8_t *st = smem + slot * Cfg::STAGE_BYTES;
-                cp_async<8>(st + Cfg::SFW_OFF + lane * 16, g_sf + ks * 512);
-                cp_async<8>(st + Cfg::SFW_OFF + lane * 16 + 8, u_sf + ks * 512);
+                cp_async<8>(smem_u32(st) + Cfg::SFW_OFF + lane * 16, g_sf + ks * 512);
+                cp_async<8>(smem_u32(st) + Cfg::SFW_OFF + lane * 16 + 8, u_sf + ks * 512);
 #pragma unroll
                 for (int i = 0; i < NT / 32; ++i)
                     if (32 * i < w.rows)
-                        cp_async<4>(st + Cfg::SFT_OFF + (i >> 2) * 512 + lane * 16 + (i & 3) * 4, t_sf[i] + ks * 512);
+                        cp_async<4>(smem_u32(st) + Cfg::SFT_OFF + (i >> 2) * 512 + lane * 16 + (i & 3) * 4, t_sf[i] + ks * 512);
                 cp_async_commit();
                 if (gs - done >= Cfg::LAG) {
                     cp_async_wait<Cfg::LAG>();
@@ -551,6 +553,459 @@ __global__ void __launch_bounds__(256, 1) moe_product_kernel(const __grid_consta
     }
 }
 
+// --------------------------------------------------- products, few tokens
+//
+// Up to kSmallNT tokens a tile: what counts is the stream of weights from HBM. A
+// stage is 128 weight rows x 256 elements of K. Two rings of shared memory:
+//   packed   the weights as they lie in memory (16 KB), by TMA: the bytes in flight
+//   operand  the same, widened to the form the tensor core takes (16 codes and 8
+//            unused bytes in each 16; 32 KB), with the token rows and all scales
+// A stage costs every role some hundred clocks of waits, fences and issues, against
+// 740 clocks that its 16 KB take at the HBM's rate: so two groups widen, two
+// threads copy scales and two threads issue MMAs, on alternating stages (the two
+// issuers into accumulators of their own, which the epilogue adds).
+
+constexpr int kSmallNT = 32;
+constexpr int kSmallThreads = 672;
+
+struct SmallCfg {
+    static constexpr int PACKED = 4, OPER = 3;
+    static constexpr uint32_t PACKED_BYTES = 128 * 128;
+    static constexpr uint32_t WIDE_BYTES = 2 * 128 * 128;          // two halves of 128 elements
+    static constexpr uint32_t TOKEN_OFF = WIDE_BYTES;              // two halves of kSmallNT x 128 bytes
+    static constexpr uint32_t SFW_OFF = TOKEN_OFF + 2 * kSmallNT * 128;   // two 512-byte blocks
+    static constexpr uint32_t SFT_OFF = SFW_OFF + 1024;                   // two 512-byte blocks
+    static constexpr uint32_t OPER_BYTES = SFT_OFF + 1024;
+    static constexpr uint32_t OPER_AT = PACKED * PACKED_BYTES;
+    static constexpr uint32_t EPI_AT = OPER_AT + OPER * OPER_BYTES;
+    static constexpr int EPI_LD = 132;
+    static constexpr uint32_t TAB_AT = EPI_AT + 32 * EPI_LD * 4;
+    static constexpr uint32_t BAR_AT = TAB_AT + 2 * (kMaxExperts + 4) * 4;
+    static constexpr int BARS = 2 * PACKED + 3 * OPER + 6;
+    static constexpr uint32_t SMEM_BYTES = BAR_AT + BARS * 8 + 32 + 1024;
+    static constexpr uint32_t SF_COLS = 16;                        // two blocks of weights, two of tokens
+    static constexpr uint32_t ACC_COLS = 4 * kSmallNT;             // [buffer][issuer]
+    static constexpr uint32_t TMEM_COLS = 256;
+    static_assert(OPER_BYTES % 1024 == 0 && SMEM_BYTES <= 232448, "shared memory budget");
+    static_assert(ACC_COLS + OPER * SF_COLS <= TMEM_COLS, "TMEM budget");
+};
+
+// Slot (i mod N) of a ring of N and the parity of its i / N-th round.
+struct Ring {
+    int slot;
+    uint32_t parity;
+};
+template <int N>
+__device__ __forceinline__ Ring ring_at(int i)
+{
+    return Ring{i % N, static_cast<uint32_t>(i / N) & 1u};
+}
+
+// The 32 accumulator columns v of row (channel) q * 32 + lane of a tile of weight
+// rows, staged through shared memory so that a thread gets neighbouring channels
+// of one token, and stored: product 1 as MXFP8 of silu(g) * u, product 2 as
+// bf16. Called by the 128 epilogue threads; c0: first token of the columns.
+template <bool FIRST, int EPI_LD>
+__device__ __forceinline__ void store_columns(const uint32_t (&v)[32], float *epi, const Unit &w, int c0, int ntb,
+                                              const ProductParams &p)
+{
+    const int t = threadIdx.x & 127;
+    const int col = t >> 2, part = t & 3;      // this thread's token and quarter of the staged rows
+#pragma unroll
+    for (int j = 0; j < 32; ++j) epi[j * EPI_LD + t] = __uint_as_float(v[j]);
+    epilogue_sync();
+    const bool live = c0 + col < w.rows;
+    const size_t row = static_cast<size_t>(w.row0) + c0 + col;
+    if constexpr (FIRST) {
+        // 16 channels a thread; two neighbours share a block of 32
+        const float *g = epi + col * EPI_LD + 16 * part;
+        float a[16];
+        uint32_t amax = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 gv = *reinterpret_cast<const float4 *>(g + 4 * i);
+            const float4 uv = *reinterpret_cast<const float4 *>(g + 64 + 4 * i);
+            a[4 * i] = __fdividef(gv.x, 1.0f + __expf(-gv.x)) * uv.x;
+            a[4 * i + 1] = __fdividef(gv.y, 1.0f + __expf(-gv.y)) * uv.y;
+            a[4 * i + 2] = __fdividef(gv.z, 1.0f + __expf(-gv.z)) * uv.z;
+            a[4 * i + 3] = __fdividef(gv.w, 1.0f + __expf(-gv.w)) * uv.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) amax = max(amax, __float_as_uint(a[i]) & 0x7FFFFFFFu);
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        const uint32_t b = mxfp8_scale_byte(amax);
+        const float inv = mxfp8_scale_inverse(b);
+        const uint32_t b2 = __shfl_down_sync(0xffffffffu, b, 2);
+        if (live) {
+            uint4 c;
+            c.x = e4m3x4_rn(a[0] * inv, a[1] * inv, a[2] * inv, a[3] * inv);
+            c.y = e4m3x4_rn(a[4] * inv, a[5] * inv, a[6] * inv, a[7] * inv);
+            c.z = e4m3x4_rn(a[8] * inv, a[9] * inv, a[10] * inv, a[11] * inv);
+            c.w = e4m3x4_rn(a[12] * inv, a[13] * inv, a[14] * inv, a[15] * inv);
+            *reinterpret_cast<uint4 *>(p.act + row * p.I + 64 * w.m + 16 * part) = c;
+            if (part == 0) {
+                const int r = c0 + col;
+                uint8_t *sf = p.act_sf + (static_cast<size_t>(w.tile) * (p.I >> 7) + (w.m >> 1)) * (ntb * 512) +
+                              (r >> 7) * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4 + (w.m & 1) * 2;
+                *reinterpret_cast<uint16_t *>(sf) = static_cast<uint16_t>(b | (b2 << 8));
+            }
+        }
+    } else {
+        const float *s = epi + col * EPI_LD + 32 * part;
+        if (live) {
+            uint4 *o = reinterpret_cast<uint4 *>(p.y + row * p.H + 128 * w.m + 32 * part);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 x = *reinterpret_cast<const float4 *>(s + 8 * i);
+                const float4 z = *reinterpret_cast<const float4 *>(s + 8 * i + 4);
+                const __nv_bfloat162 h[4] = {__floats2bfloat162_rn(x.x, x.y), __floats2bfloat162_rn(x.z, x.w),
+                                             __floats2bfloat162_rn(z.x, z.y), __floats2bfloat162_rn(z.z, z.w)};
+                o[i] = *reinterpret_cast<const uint4 *>(h);
+            }
+        }
+    }
+    epilogue_sync();   // the staging buffer is reused
+}
+
+// FIRST: product 1 (tokens x [G; U], SwiGLU, MXFP8), else product 2. Warps:
+//   0-3    epilogue of a finished tile while the next one's mainloop runs
+//   4-7    copy token rows and all scales by cp.async
+//   8-15   widen packed weights: groups of four on alternating stages
+//   16,17  MMA issuers (lane 0), on alternating stages of a tile; 16 owns TMEM
+//   18     lane 0 loads packed weights by TMA
+//   19,20  lane 0 of each copies the scales of alternating stages to TMEM
+// Loading weights already widened was measured too: a TMA load that unpacks moves 16
+// bytes of shared memory a clock, 8-byte cp.async half of what HBM gives.
+template <bool FIRST>
+__global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(const __grid_constant__ ProductParams p)
+{
+    using Cfg = SmallCfg;
+    constexpr int PACKED = Cfg::PACKED, OPER = Cfg::OPER, NT = kSmallNT;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float *epi = reinterpret_cast<float *>(smem + Cfg::EPI_AT);
+    int *off = reinterpret_cast<int *>(smem + Cfg::TAB_AT);
+    int *tile0 = off + kMaxExperts + 4;
+    uint64_t *p_full = reinterpret_cast<uint64_t *>(smem + Cfg::BAR_AT);
+    uint64_t *p_empty = p_full + PACKED;
+    uint64_t *t_full = p_empty + PACKED;   // tokens and scales of a stage have landed
+    uint64_t *ready = t_full + OPER;       // weights widened, scales in TMEM
+    uint64_t *done = ready + OPER;         // the stage's MMAs have completed
+    uint64_t *accf = done + OPER;          // [2] accumulators complete
+    uint64_t *acc_empty = accf + 2;        // [2] accumulators drained
+    uint64_t *cp_done = acc_empty + 2;     // [2] the scale copies of warp 19 / 20 have completed
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(cp_done + 2);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    volatile int *epi_go = abort_flag + 1;   // [2]
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < PACKED; ++i) {
+            mbar_init(p_full + i, 1);
+            mbar_init(p_empty + i, 4);      // one arrival from each warp of a widening group
+        }
+        for (int i = 0; i < OPER; ++i) {
+            mbar_init(t_full + i, 128);     // one from each copying thread
+            mbar_init(ready + i, 5);        // a widening group's warps and the scale copies
+            mbar_init(done + i, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(accf + b, 2);         // both issuers
+            mbar_init(acc_empty + b, 128);
+            mbar_init(cp_done + b, 1);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&p.tm_w);
+    }
+    if (warp == 16) {
+        tmem_alloc(tmem_slot, Cfg::TMEM_COLS);
+        tmem_relinquish();
+    }
+    grid_dependency_wait();
+    grid_launch_dependents();
+    for (int e = threadIdx.x; e <= p.E; e += blockDim.x) {
+        off[e] = __ldcg(p.off + e);
+        tile0[e] = __ldcg(p.tile0 + e);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem_sf = tmem + Cfg::ACC_COLS;
+    const int K = FIRST ? p.H : p.I;
+    const int kc = K >> 7;                                  // blocks of 128 elements
+    const int stages = (kc + 1) >> 1;                       // the last one may be half
+    const int mw = FIRST ? p.I >> 6 : p.H >> 7;             // weight tiles of an expert
+    const int wrows = FIRST ? 2 * p.I : p.H;                // weight rows of an expert
+    const int units = tile0[p.E] * mw;
+
+    if (warp < 4) {
+        // ------------------------------------------------------------ epilogue
+        int ul = 0;
+        for (int u = blockIdx.x; u < units; u += gridDim.x, ++ul) {
+            const Unit w = decode_unit(u, mw, p.E, NT, off, tile0);
+            const int buf = ul & 1;
+            if (threadIdx.x == 0) {
+                const bool ok = mbar_wait(accf + buf, (ul >> 1) & 1, &g_moe_error, kErrWaitAccum, p.wait_ns);
+                if (!ok) *abort_flag = 1;
+                epi_go[buf] = ok && !*abort_flag;
+            }
+            epilogue_sync();
+            if (!epi_go[buf]) break;
+            tc_fence_after();
+            const uint32_t trow = tmem + buf * 2 * NT + (static_cast<uint32_t>(warp * 32) << 16);
+            uint32_t v[32];
+            tmem_ld32(trow, v);
+            tmem_ld_wait();
+            if (stages > 1) {
+                uint32_t v1[32];
+                tmem_ld32(trow + NT, v1);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(v1[j]));
+            }
+            tc_fence_before();
+            mbar_arrive(acc_empty + buf);
+            store_columns<FIRST, Cfg::EPI_LD>(v, epi, w, 0, 1, p);
+        }
+    } else if (warp < 8) {
+        // -------------------------------------------------- tokens and scales
+        // Thread t copies 16 bytes (column t % 8 of each half) of rows t / 8 and
+        // t / 8 + 16; in the 128-byte swizzle column c of row r is at c ^ (r % 8).
+        const int t = threadIdx.x - 128;
+        const int r0 = t >> 3, c = t & 7;
+        const uint32_t dst0 = Cfg::TOKEN_OFF + r0 * 128 + ((c ^ (r0 & 7)) << 4);
+        int gs = 0;
+        bool ok = true;
+        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            const Unit w = decode_unit(u, mw, p.E, NT, off, tile0);
+            const bool two = w.rows > 16;
+            // this thread's rows; past the tile's last row, that row again (its
+            // columns are not stored)
+            const uint8_t *tok[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = w.row0 + min(r0 + 16 * i, w.rows - 1);
+                tok[i] = (FIRST ? p.x + static_cast<size_t>(__ldcg(p.src + r)) * p.ldx
+                                : p.act + static_cast<size_t>(r) * p.I) + c * 16;
+            }
+            // scales: thread t < 64 those of the weights, of product 1 from the half of the
+            // 128-row blocks of G and of U that holds its 64 channels (8 of each 16
+            // bytes), 64 <= t < 96 a word a token
+            const uint8_t *sf = nullptr;
+            uint32_t sf_dst = 0;
+            int sf_step = 512;
+            if (t < 64) {
+                if constexpr (FIRST) {
+                    const size_t blk = static_cast<size_t>(wrows >> 7) * w.e + (w.m >> 1) + (t >= 32 ? p.I >> 7 : 0);
+                    sf = p.w_sf + blk * kc * 512 + lane * 16 + (w.m & 1) * 8;
+                    sf_dst = Cfg::SFW_OFF + lane * 16 + (t >= 32 ? 8 : 0);
+                } else {
+                    sf = p.w_sf + static_cast<size_t>(w.e * mw + w.m) * kc * 512 + (t & 31) * 16;
+                    sf_dst = Cfg::SFW_OFF + (t & 31) * 16;
+                }
+            } else if (t < 96) {
+                const int r = min(lane, w.rows - 1);
+                if constexpr (FIRST) {
+                    const int tk = __ldcg(p.src + w.row0 + r);
+                    sf = p.x_sf + static_cast<size_t>(tk >> 7) * kc * 512 + (tk & 31) * 16 + ((tk & 127) >> 5) * 4;
+                } else {
+                    sf = p.act_sf + static_cast<size_t>(w.tile) * kc * 512 + r * 16;
+                }
+                sf_dst = Cfg::SFT_OFF + lane * 16;
+            }
+            for (int ks = 0; ks < stages; ++ks, ++gs) {
+                const Ring r = ring_at<OPER>(gs);
+                if (gs >= OPER) ok = mbar_wait_warp(done + r.slot, r.parity ^ 1u, &g_moe_error, kErrWaitEmpty, p.wait_ns);
+                if (!ok) {
+                    *abort_flag = 1;
+                    break;
+                }
+                const uint32_t st = smem_u32(smem + Cfg::OPER_AT) + r.slot * Cfg::OPER_BYTES;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int kb = 2 * ks + h;
+                    if (kb < kc) {
+                        cp_async<16>(st + dst0 + h * (NT * 128), tok[0] + kb * 128);
+                        if (two) cp_async<16>(st + dst0 + h * (NT * 128) + 2048, tok[1] + kb * 128);
+                        if (t < 64) {
+                            if constexpr (FIRST)
+                                cp_async<8>(st + sf_dst + h * 512, sf + kb * sf_step);
+                            else if (t < 32)
+                                cp_async<16>(st + sf_dst + h * 512, sf + kb * sf_step);
+                        } else if (t < 96) {
+                            cp_async<4>(st + sf_dst + h * 512, sf + kb * sf_step);
+                        }
+                    }
+                }
+                cp_async_arrive(t_full + r.slot);
+            }
+        }
+        cp_async_wait_all();   // also after an abort: nothing of this thread is in flight when the block leaves
+    } else if (warp < 16) {
+        // -------------------------------------------------- widening of weights
+        // Lane l takes row l % 8 of a group of eight and 16-byte column l / 8 (+ 4): both
+        // swizzles then spread eight lanes over all banks.
+        const int group = (warp - 8) >> 2, w4 = (warp - 8) & 3;
+        const int row8 = lane & 7, j = lane >> 3;
+        int gs = 0;
+        bool ok = true;
+        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            for (int ks = 0; ks < stages; ++ks, ++gs) {
+                if ((gs & 1) != group) continue;
+                const Ring rp = ring_at<PACKED>(gs), ro = ring_at<OPER>(gs);
+                ok = mbar_wait_warp(p_full + rp.slot, rp.parity, &g_moe_error, kErrWaitFull, p.wait_ns);
+                if (ok && gs >= OPER)
+                    ok = mbar_wait_warp(done + ro.slot, ro.parity ^ 1u, &g_moe_error, kErrWaitEmpty, p.wait_ns);
+                if (!ok) {
+                    *abort_flag = 1;
+                    break;
+                }
+                const uint8_t *src = smem + rp.slot * Cfg::PACKED_BYTES + w4 * 4096 + row8 * 128;
+                uint8_t *dst = smem + Cfg::OPER_AT + ro.slot * Cfg::OPER_BYTES + w4 * 4096 + row8 * 128;
+                const int s0 = ((2 * j) ^ row8) << 4, s1 = ((2 * j + 1) ^ row8) << 4;
+                uint4 v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[i] = *reinterpret_cast<const uint4 *>(src + (i & 3) * 1024 + ((((i >> 2) * 4 + j) ^ row8) << 4));
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    uint8_t *d = dst + (i >> 2) * 16384 + (i & 3) * 1024;
+                    *reinterpret_cast<uint2 *>(d + s0) = make_uint2(v[i].x, v[i].y);
+                    *reinterpret_cast<uint2 *>(d + s1) = make_uint2(v[i].z, v[i].w);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(ready + ro.slot);
+                    mbar_arrive(p_empty + rp.slot);
+                }
+            }
+        }
+    } else if (warp < 18) {
+        if (lane == 0) {
+            // ------------------------------------------------------ MMA issuers
+            const int me = warp - 16;
+            int gs = 0, ul = 0, commits[2] = {0, 0};
+            for (int u = blockIdx.x; u < units; u += gridDim.x, ++ul) {
+                const Unit w = decode_unit(u, mw, p.E, NT, off, tile0);
+                const int buf = ul & 1;
+                if (ul >= 2 && !mbar_wait(acc_empty + buf, ((ul >> 1) - 1) & 1, &g_moe_error, kErrWaitAccum, p.wait_ns)) {
+                    *abort_flag = 1;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t idesc = idesc_w4a8((w.rows + 15) & ~15);
+                const uint32_t d = tmem + (buf * 2 + me) * NT;
+                bool ok = true;
+                for (int ks = me; ks < stages; ks += 2) {
+                    const Ring r = ring_at<OPER>(gs + ks);
+                    if (!mbar_wait(ready + r.slot, r.parity, &g_moe_error, kErrWaitOperand, p.wait_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t st = smem_u32(smem + Cfg::OPER_AT) + r.slot * Cfg::OPER_BYTES;
+                    const uint32_t tsf = tmem_sf + r.slot * Cfg::SF_COLS;
+                    const uint64_t ad = sdesc_sw128(st), bd = sdesc_sw128(st + Cfg::TOKEN_OFF);
+                    auto half = [&](int h, uint32_t accumulate) {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_mxf8f6f4(d, ad + h * 1024 + 2 * kk, bd + h * (NT * 8) + 2 * kk,
+                                         idesc_with_sf_ids(idesc, kk, kk), tsf + 4 * h, tsf + 8 + 4 * h,
+                                         kk > 0 ? 1u : accumulate);
+                    };
+                    half(0, ks > me ? 1u : 0u);
+                    if (2 * ks + 1 < kc) half(1, 1u);
+                    tc_commit(done + r.slot);
+                }
+                gs += stages;
+                tc_commit(accf + buf);
+                ++commits[buf];
+                if (!ok) {
+                    *abort_flag = 1;
+                    break;
+                }
+            }
+            // no MMA may be running when TMEM is released
+            for (int b = 0; b < 2; ++b)
+                if (commits[b] > 0) mbar_wait(accf + b, (commits[b] - 1) & 1, &g_moe_error, kErrWaitDrain);
+        }
+    } else if (warp == 18) {
+        if (lane == 0) {
+            // --------------------------------------------- packed weights by TMA
+            const uint64_t pol = policy_evict_first();
+            int gs = 0;
+            bool ok = true;
+            for (int u = blockIdx.x; u < units && ok && !*abort_flag; u += gridDim.x) {
+                const Unit w = decode_unit(u, mw, p.E, NT, off, tile0);
+                // the two halves of the tile: G and U of 64 channels, or 128 rows in a row
+                const int r0 = w.e * wrows + w.m * (FIRST ? 64 : 128);
+                const int r1 = r0 + (FIRST ? p.I : 64);
+                for (int ks = 0; ks < stages; ++ks) {
+                    const Ring r = ring_at<PACKED>(gs);
+                    if (gs >= PACKED &&
+                        !(ok = mbar_wait(p_empty + r.slot, r.parity ^ 1u, &g_moe_error, kErrWaitEmpty, p.wait_ns))) {
+                        *abort_flag = 1;
+                        break;
+                    }
+                    uint8_t *st = smem + r.slot * Cfg::PACKED_BYTES;
+                    mbar_arrive_expect_tx(p_full + r.slot, Cfg::PACKED_BYTES);
+                    tma_load_2d(st, &p.tm_w, ks * 128, r0, p_full + r.slot, pol);
+                    tma_load_2d(st + 8192, &p.tm_w, ks * 128, r1, p_full + r.slot, pol);
+                    ++gs;
+                }
+            }
+            // copies in flight land before the block leaves
+            for (int i = max(0, gs - PACKED); i < gs; ++i) {
+                const Ring r = ring_at<PACKED>(i);
+                mbar_wait(p_full + r.slot, r.parity, &g_moe_error, kErrWaitDrain);
+            }
+        }
+    } else if (lane == 0) {
+        // ------------------------------------------------------ scales to TMEM
+        // cp.async wrote the stage through the generic proxy; the fence here lets the
+        // scale copies, and the MMAs that wait for them, read it through the async
+        // proxy.
+        const int me = warp - 19;
+        int gs = 0;
+        bool ok = true;
+        for (int u = blockIdx.x; u < units && ok && !*abort_flag; u += gridDim.x)
+            for (int ks = 0; ks < stages; ++ks, ++gs) {
+                if ((gs & 1) != me) continue;
+                const Ring r = ring_at<OPER>(gs);
+                ok = mbar_wait(t_full + r.slot, r.parity, &g_moe_error, kErrWaitFull, p.wait_ns);
+                if (!ok) {
+                    *abort_flag = 1;
+                    break;
+                }
+                fence_proxy_async_smem();
+                tc_fence_after();
+                const uint32_t st = smem_u32(smem + Cfg::OPER_AT) + r.slot * Cfg::OPER_BYTES;
+                const uint32_t tsf = tmem_sf + r.slot * Cfg::SF_COLS;
+                tc_cp_scale_block(tsf, sdesc_scale(st + Cfg::SFW_OFF));
+                tc_cp_scale_block(tsf + 8, sdesc_scale(st + Cfg::SFT_OFF));
+                if (2 * ks + 1 < kc) {
+                    tc_cp_scale_block(tsf + 4, sdesc_scale(st + Cfg::SFW_OFF + 512));
+                    tc_cp_scale_block(tsf + 12, sdesc_scale(st + Cfg::SFT_OFF + 512));
+                }
+                tc_commit(ready + r.slot);
+            }
+        // no copy may be running when TMEM is released
+        tc_commit(cp_done + me);
+        mbar_wait(cp_done + me, 0, &g_moe_error, kErrWaitDrain);
+    }
+    __syncwarp();
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 16) {
+        tc_fence_after();
+        tmem_dealloc(tmem, Cfg::TMEM_COLS);
+    }
+}
+
 // ------------------------------------------------------------------ combine
 
 struct CombineParams {
@@ -621,10 +1076,22 @@ cudaError_t launch_product(const ProductParams &p, int64_t max_units, cudaStream
 }
 
 template <bool FIRST>
+cudaError_t launch_product_small(const ProductParams &p, int64_t max_units, cudaStream_t stream)
+{
+    auto kern = moe_product_small_kernel<FIRST>;
+    static KernelOnce once;
+    int sms = 0;
+    const cudaError_t e = prepare_kernel(kern, SmallCfg::SMEM_BYTES, once, &sms);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(max_units, std::max(1, sms)));
+    return launch_pdl(kern, dim3(grid), dim3(kSmallThreads), SmallCfg::SMEM_BYTES, stream, p);
+}
+
+template <bool FIRST>
 cudaError_t launch_product_nt(int nt, const ProductParams &p, int64_t max_units, cudaStream_t stream)
 {
-    return nt == 32 ? launch_product<FIRST, 32, 9>(p, max_units, stream)
-                    : launch_product<FIRST, 224, 4>(p, max_units, stream);
+    return nt == kSmallNT ? launch_product_small<FIRST>(p, max_units, stream)
+                          : launch_product<FIRST, 224, 4>(p, max_units, stream);
 }
 
 inline size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -692,12 +1159,14 @@ cudaError_t launch_moe_experts(const MoeArgs &a, const MoeLayout &l, cudaStream_
     p.H = a.H;
     p.I = a.I;
     p.wait_ns = wait_limit_ns();
-    p.tm_w = a.tm_w13;
+    p.x = a.xq;
+    p.ldx = a.ldx;
+    p.tm_w = l.nt == kSmallNT ? a.tm_pw13 : a.tm_w13;
     p.tm_t = a.tm_x;
     p.w_sf = a.w13_sf;
     e = launch_product_nt<true>(l.nt, p, static_cast<int64_t>(l.max_tiles) * (a.I / 64), stream);
     if (e != cudaSuccess) return e;
-    p.tm_w = a.tm_w2;
+    p.tm_w = l.nt == kSmallNT ? a.tm_pw2 : a.tm_w2;
     p.tm_t = a.tm_act;
     p.w_sf = a.w2_sf;
     e = launch_product_nt<false>(l.nt, p, static_cast<int64_t>(l.max_tiles) * (a.H / 128), stream);

@@ -228,14 +228,28 @@ __device__ __forceinline__ void tma_gather4(void *smem_dst, const CUtensorMap *t
         : "memory");
 }
 
-// Asynchronous copy of BYTES (4 or 8) from global to shared memory by ordinary
-// (generic-proxy) writes, tracked by the thread's cp.async groups.
+// Asynchronous copy of BYTES (4, 8 or 16) from global to shared memory by
+// ordinary (generic-proxy) writes of this thread. Copies of 16 bytes bypass L1;
+// L2 fetches whole 128-byte lines.
 template <int BYTES>
-__device__ __forceinline__ void cp_async(void *smem_dst, const void *gsrc)
+__device__ __forceinline__ void cp_async(uint32_t smem_dst, const void *gsrc)
 {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(smem_dst)), "l"(gsrc), "n"(BYTES)
-                 : "memory");
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(smem_dst), "l"(gsrc) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global.L2::128B [%0], [%1], %2;" ::"r"(smem_dst), "l"(gsrc), "n"(BYTES)
+                     : "memory");
 }
+
+// Arrives on `bar` (one of the arrivals it was initialised for) once every
+// cp.async that this thread issued before has landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Waits until every cp.async of this thread has landed.
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
