@@ -32,7 +32,7 @@ struct MoeLayout {
     int nt;                 // tokens of a tile (columns of the accumulator)
     int max_tiles;          // most token tiles T * k choices can need
     int chunks;             // blocks of the placing kernel
-    size_t hist, off, tile0, src, pos, act, act_sf, y, total;
+    size_t hist, off, tile0, rec, src, pos, act, act_sf, y, total;
 };
 bool moe_layout(int64_t T, int k, int E, int64_t H, int64_t I, MoeLayout *out);
 

@@ -49,6 +49,7 @@ struct PlaceParams {
     int *hist;      // [chunks][E], more than one chunk only
     int *off;       // [E + 1] first sorted row of each expert
     int *tile0;     // [E + 1] first token tile of each expert
+    int4 *rec;      // [tiles] expert, first sorted row, rows of a token tile
     int *src;       // [R] token of a sorted row
     int *pos;       // [R] sorted row of a choice, -1: left out
     int R, k, E, chunks, nt;
@@ -78,7 +79,8 @@ __global__ void __launch_bounds__(kPlaceThreads) moe_place_kernel(const PlacePar
 {
     __shared__ int total[kMaxExperts];    // rows of an expert
     __shared__ int next[kMaxExperts];     // rows of it before this block's; then the next free row
-    __shared__ int off[kMaxExperts + 1];
+    __shared__ int off[kMaxExperts];
+    __shared__ int tile0[kMaxExperts];
     grid_dependency_wait();
     grid_launch_dependents();
     const int tid = threadIdx.x, begin = blockIdx.x * kChunk;
@@ -135,6 +137,7 @@ __global__ void __launch_bounds__(kPlaceThreads) moe_place_kernel(const PlacePar
             const int e = tid * per + i;
             if (e < p.E) {
                 off[e] = r0;
+                tile0[e] = t0;
                 if (blockIdx.x == 0) {
                     p.off[e] = r0;
                     p.tile0[e] = t0;
@@ -149,7 +152,12 @@ __global__ void __launch_bounds__(kPlaceThreads) moe_place_kernel(const PlacePar
         }
     }
     __syncthreads();
-    for (int e = tid; e < p.E; e += blockDim.x) next[e] += off[e];
+    for (int e = tid; e < p.E; e += blockDim.x) {
+        next[e] += off[e];
+        if (blockIdx.x == 0)
+            for (int i = 0; i * p.nt < total[e]; ++i)
+                p.rec[tile0[e] + i] = make_int4(e, off[e] + i * p.nt, min(p.nt, total[e] - i * p.nt), 0);
+    }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
@@ -178,6 +186,7 @@ struct ProductParams {
     uint8_t *act_sf;        // [tiles][I / 128][NT / 128 rounded up][512]
     uint16_t *y;            // product 2: [rows, H] bf16
     const int *off, *tile0, *src;
+    const int4 *rec;
     int E, H, I;
     uint64_t wait_ns;
 };
@@ -556,10 +565,12 @@ __global__ void __launch_bounds__(256, 1) moe_product_kernel(const __grid_consta
 // --------------------------------------------------- products, few tokens
 //
 // Up to kSmallNT tokens a tile: what counts is the stream of weights from HBM. A
-// stage is 128 weight rows x 256 elements of K. Two rings of shared memory:
-//   packed   the weights as they lie in memory (16 KB), by TMA: the bytes in flight
-//   operand  the same, widened to the form the tensor core takes (16 codes and 8
-//            unused bytes in each 16; 32 KB), with the token rows and all scales
+// stage is 128 weight rows x 256 elements of K. Three rings of shared memory:
+//   packed  the weights as they lie in memory (16 KB), by TMA: the bytes in flight
+//   wide    the same, widened to the form the tensor core takes (16 codes and 8
+//           unused bytes in each 16; 32 KB)
+//   token   token rows and all scales, gathered by cp.async: deep enough for their
+//           latency (with three stages, those took 1350 clocks each)
 // A stage costs every role some hundred clocks of waits, fences and issues, against
 // 740 clocks that its 16 KB take at the HBM's rate: so two groups widen, two
 // threads copy scales and two threads issue MMAs, on alternating stages (the two
@@ -568,26 +579,28 @@ __global__ void __launch_bounds__(256, 1) moe_product_kernel(const __grid_consta
 constexpr int kSmallNT = 32;
 constexpr int kSmallThreads = 672;
 
+constexpr int kEpiLd = 132;                       // floats of a staged column
+constexpr uint32_t kEpiBytes = 16 * kEpiLd * 4;
+
 struct SmallCfg {
-    static constexpr int PACKED = 4, OPER = 3;
+    static constexpr int PACKED = 4, WIDE = 3, TOKEN = 5;
     static constexpr uint32_t PACKED_BYTES = 128 * 128;
     static constexpr uint32_t WIDE_BYTES = 2 * 128 * 128;          // two halves of 128 elements
-    static constexpr uint32_t TOKEN_OFF = WIDE_BYTES;              // two halves of kSmallNT x 128 bytes
-    static constexpr uint32_t SFW_OFF = TOKEN_OFF + 2 * kSmallNT * 128;   // two 512-byte blocks
-    static constexpr uint32_t SFT_OFF = SFW_OFF + 1024;                   // two 512-byte blocks
-    static constexpr uint32_t OPER_BYTES = SFT_OFF + 1024;
-    static constexpr uint32_t OPER_AT = PACKED * PACKED_BYTES;
-    static constexpr uint32_t EPI_AT = OPER_AT + OPER * OPER_BYTES;
-    static constexpr int EPI_LD = 132;
-    static constexpr uint32_t TAB_AT = EPI_AT + 32 * EPI_LD * 4;
-    static constexpr uint32_t BAR_AT = TAB_AT + 2 * (kMaxExperts + 4) * 4;
-    static constexpr int BARS = 2 * PACKED + 3 * OPER + 6;
+    static constexpr uint32_t SFW_OFF = 2 * kSmallNT * 128;        // two halves of token rows, then two 512-byte blocks
+    static constexpr uint32_t SFT_OFF = SFW_OFF + 1024;            // two 512-byte blocks
+    static constexpr uint32_t TOKEN_BYTES = SFT_OFF + 1024;
+    static constexpr uint32_t WIDE_AT = PACKED * PACKED_BYTES;
+    static constexpr uint32_t TOKEN_AT = WIDE_AT + WIDE * WIDE_BYTES;
+    static constexpr uint32_t EPI_AT = TOKEN_AT + TOKEN * TOKEN_BYTES;
+    static constexpr uint32_t BAR_AT = EPI_AT + kEpiBytes;
+    static constexpr int BARS = 2 * PACKED + 3 * TOKEN + 6;
     static constexpr uint32_t SMEM_BYTES = BAR_AT + BARS * 8 + 32 + 1024;
-    static constexpr uint32_t SF_COLS = 16;                        // two blocks of weights, two of tokens
+    static constexpr uint32_t SF_COLS = 16;                        // two blocks of weights, two of tokens, 4 columns each
     static constexpr uint32_t ACC_COLS = 4 * kSmallNT;             // [buffer][issuer]
     static constexpr uint32_t TMEM_COLS = 256;
-    static_assert(OPER_BYTES % 1024 == 0 && SMEM_BYTES <= 232448, "shared memory budget");
-    static_assert(ACC_COLS + OPER * SF_COLS <= TMEM_COLS, "TMEM budget");
+    static_assert(TOKEN_BYTES % 1024 == 0 && SMEM_BYTES <= 232448, "shared memory budget");
+    static_assert(WIDE <= TOKEN, "the wide ring is freed by the token ring's barriers");
+    static_assert(ACC_COLS + TOKEN * SF_COLS <= TMEM_COLS, "TMEM budget");
 };
 
 // Slot (i mod N) of a ring of N and the parity of its i / N-th round.
@@ -601,61 +614,63 @@ __device__ __forceinline__ Ring ring_at(int i)
     return Ring{i % N, static_cast<uint32_t>(i / N) & 1u};
 }
 
-// The 32 accumulator columns v of row (channel) q * 32 + lane of a tile of weight
-// rows, staged through shared memory so that a thread gets neighbouring channels
-// of one token, and stored: product 1 as MXFP8 of silu(g) * u, product 2 as
-// bf16. Called by the 128 epilogue threads; c0: first token of the columns.
-template <bool FIRST, int EPI_LD>
+// The 32 accumulator columns v of one weight row a thread, staged 16 at a time
+// through shared memory so that a thread gets neighbouring rows (channels) of one
+// column (token), and stored: product 1 as MXFP8 of silu(g) * u, product 2 as bf16.
+// Called by the 128 epilogue threads; c0: first token of the columns, which has
+// at least one.
+template <bool FIRST>
 __device__ __forceinline__ void store_columns(const uint32_t (&v)[32], float *epi, const Unit &w, int c0, int ntb,
                                               const ProductParams &p)
 {
     const int t = threadIdx.x & 127;
-    const int col = t >> 2, part = t & 3;      // this thread's token and quarter of the staged rows
+    const int col = t >> 3, part = t & 7;      // this thread's column and eighth of the staged rows
 #pragma unroll
-    for (int j = 0; j < 32; ++j) epi[j * EPI_LD + t] = __uint_as_float(v[j]);
-    epilogue_sync();
-    const bool live = c0 + col < w.rows;
-    const size_t row = static_cast<size_t>(w.row0) + c0 + col;
-    if constexpr (FIRST) {
-        // 16 channels a thread; two neighbours share a block of 32
-        const float *g = epi + col * EPI_LD + 16 * part;
-        float a[16];
-        uint32_t amax = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+        if (c0 + 16 * pass >= w.rows) break;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float4 gv = *reinterpret_cast<const float4 *>(g + 4 * i);
-            const float4 uv = *reinterpret_cast<const float4 *>(g + 64 + 4 * i);
-            a[4 * i] = __fdividef(gv.x, 1.0f + __expf(-gv.x)) * uv.x;
-            a[4 * i + 1] = __fdividef(gv.y, 1.0f + __expf(-gv.y)) * uv.y;
-            a[4 * i + 2] = __fdividef(gv.z, 1.0f + __expf(-gv.z)) * uv.z;
-            a[4 * i + 3] = __fdividef(gv.w, 1.0f + __expf(-gv.w)) * uv.w;
-        }
+        for (int j = 0; j < 16; ++j) epi[j * kEpiLd + t] = __uint_as_float(v[16 * pass + j]);
+        epilogue_sync();
+        const int r = c0 + 16 * pass + col;    // row of the tile
+        const bool live = r < w.rows;
+        const size_t row = static_cast<size_t>(w.row0) + r;
+        if constexpr (FIRST) {
+            // 8 channels a thread; four neighbours share a block of 32
+            const float *g = epi + col * kEpiLd + 8 * part;
+            float a[8];
+            uint32_t amax = 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) amax = max(amax, __float_as_uint(a[i]) & 0x7FFFFFFFu);
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        const uint32_t b = mxfp8_scale_byte(amax);
-        const float inv = mxfp8_scale_inverse(b);
-        const uint32_t b2 = __shfl_down_sync(0xffffffffu, b, 2);
-        if (live) {
-            uint4 c;
-            c.x = e4m3x4_rn(a[0] * inv, a[1] * inv, a[2] * inv, a[3] * inv);
-            c.y = e4m3x4_rn(a[4] * inv, a[5] * inv, a[6] * inv, a[7] * inv);
-            c.z = e4m3x4_rn(a[8] * inv, a[9] * inv, a[10] * inv, a[11] * inv);
-            c.w = e4m3x4_rn(a[12] * inv, a[13] * inv, a[14] * inv, a[15] * inv);
-            *reinterpret_cast<uint4 *>(p.act + row * p.I + 64 * w.m + 16 * part) = c;
-            if (part == 0) {
-                const int r = c0 + col;
-                uint8_t *sf = p.act_sf + (static_cast<size_t>(w.tile) * (p.I >> 7) + (w.m >> 1)) * (ntb * 512) +
-                              (r >> 7) * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4 + (w.m & 1) * 2;
-                *reinterpret_cast<uint16_t *>(sf) = static_cast<uint16_t>(b | (b2 << 8));
+            for (int i = 0; i < 2; ++i) {
+                const float4 gv = *reinterpret_cast<const float4 *>(g + 4 * i);
+                const float4 uv = *reinterpret_cast<const float4 *>(g + 64 + 4 * i);
+                a[4 * i] = __fdividef(gv.x, 1.0f + __expf(-gv.x)) * uv.x;
+                a[4 * i + 1] = __fdividef(gv.y, 1.0f + __expf(-gv.y)) * uv.y;
+                a[4 * i + 2] = __fdividef(gv.z, 1.0f + __expf(-gv.z)) * uv.z;
+                a[4 * i + 3] = __fdividef(gv.w, 1.0f + __expf(-gv.w)) * uv.w;
             }
-        }
-    } else {
-        const float *s = epi + col * EPI_LD + 32 * part;
-        if (live) {
-            uint4 *o = reinterpret_cast<uint4 *>(p.y + row * p.H + 128 * w.m + 32 * part);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(a[i]) & 0x7FFFFFFFu);
+            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            const uint32_t b = mxfp8_scale_byte(amax);
+            const float inv = mxfp8_scale_inverse(b);
+            const uint32_t b2 = __shfl_down_sync(0xffffffffu, b, 4);
+            if (live) {
+                uint2 c;
+                c.x = e4m3x4_rn(a[0] * inv, a[1] * inv, a[2] * inv, a[3] * inv);
+                c.y = e4m3x4_rn(a[4] * inv, a[5] * inv, a[6] * inv, a[7] * inv);
+                *reinterpret_cast<uint2 *>(p.act + row * p.I + 64 * w.m + 8 * part) = c;
+                if (part == 0) {
+                    uint8_t *sf = p.act_sf + (static_cast<size_t>(w.tile) * (p.I >> 7) + (w.m >> 1)) * (ntb * 512) +
+                                  (r >> 7) * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4 + (w.m & 1) * 2;
+                    *reinterpret_cast<uint16_t *>(sf) = static_cast<uint16_t>(b | (b2 << 8));
+                }
+            }
+        } else if (live) {
+            const float *s = epi + col * kEpiLd + 16 * part;
+            uint4 *o = reinterpret_cast<uint4 *>(p.y + row * p.H + 128 * w.m + 16 * part);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
                 const float4 x = *reinterpret_cast<const float4 *>(s + 8 * i);
                 const float4 z = *reinterpret_cast<const float4 *>(s + 8 * i + 4);
                 const __nv_bfloat162 h[4] = {__floats2bfloat162_rn(x.x, x.y), __floats2bfloat162_rn(x.z, x.w),
@@ -663,9 +678,32 @@ __device__ __forceinline__ void store_columns(const uint32_t (&v)[32], float *ep
                 o[i] = *reinterpret_cast<const uint4 *>(h);
             }
         }
+        epilogue_sync();   // the staging buffer is reused
     }
-    epilogue_sync();   // the staging buffer is reused
 }
+
+// Walks the units of a block of the small kernel: unit u is token tile u % tiles and
+// weight tile u / tiles, so the blocks at work read different experts, and tiles of
+// one expert read the same weights at the same time. The record of the next unit
+// is on its way while the current one is worked on.
+struct UnitWalk {
+    const int4 *rec;
+    int tiles, units, u;
+    int4 cur;
+    __device__ __forceinline__ UnitWalk(const ProductParams &p, int tiles_, int mw)
+        : rec(p.rec), tiles(tiles_), units(tiles_ * mw), u(blockIdx.x)
+    {
+        if (u < units) cur = __ldcg(rec + u % tiles);
+    }
+    __device__ __forceinline__ bool more() const { return u < units; }
+    __device__ __forceinline__ Unit take()
+    {
+        const Unit w{cur.x, u / tiles, u % tiles, cur.y, cur.z};
+        u += gridDim.x;
+        if (u < units) cur = __ldcg(rec + u % tiles);
+        return w;
+    }
+};
 
 // FIRST: product 1 (tokens x [G; U], SwiGLU, MXFP8), else product 2. Warps:
 //   0-3    epilogue of a finished tile while the next one's mainloop runs
@@ -680,18 +718,16 @@ template <bool FIRST>
 __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(const __grid_constant__ ProductParams p)
 {
     using Cfg = SmallCfg;
-    constexpr int PACKED = Cfg::PACKED, OPER = Cfg::OPER, NT = kSmallNT;
+    constexpr int PACKED = Cfg::PACKED, WIDE = Cfg::WIDE, TOKEN = Cfg::TOKEN, NT = kSmallNT;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float *epi = reinterpret_cast<float *>(smem + Cfg::EPI_AT);
-    int *off = reinterpret_cast<int *>(smem + Cfg::TAB_AT);
-    int *tile0 = off + kMaxExperts + 4;
     uint64_t *p_full = reinterpret_cast<uint64_t *>(smem + Cfg::BAR_AT);
     uint64_t *p_empty = p_full + PACKED;
     uint64_t *t_full = p_empty + PACKED;   // tokens and scales of a stage have landed
-    uint64_t *ready = t_full + OPER;       // weights widened, scales in TMEM
-    uint64_t *done = ready + OPER;         // the stage's MMAs have completed
-    uint64_t *accf = done + OPER;          // [2] accumulators complete
+    uint64_t *ready = t_full + TOKEN;      // [TOKEN] weights widened, scales in TMEM
+    uint64_t *done = ready + TOKEN;        // [TOKEN] the stage's MMAs have completed: its token and wide slots are free
+    uint64_t *accf = done + TOKEN;         // [2] accumulators complete
     uint64_t *acc_empty = accf + 2;        // [2] accumulators drained
     uint64_t *cp_done = acc_empty + 2;     // [2] the scale copies of warp 19 / 20 have completed
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(cp_done + 2);
@@ -704,7 +740,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
             mbar_init(p_full + i, 1);
             mbar_init(p_empty + i, 4);      // one arrival from each warp of a widening group
         }
-        for (int i = 0; i < OPER; ++i) {
+        for (int i = 0; i < TOKEN; ++i) {
             mbar_init(t_full + i, 128);     // one from each copying thread
             mbar_init(ready + i, 5);        // a widening group's warps and the scale copies
             mbar_init(done + i, 1);
@@ -722,29 +758,26 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
         tmem_alloc(tmem_slot, Cfg::TMEM_COLS);
         tmem_relinquish();
     }
-    grid_dependency_wait();
-    grid_launch_dependents();
-    for (int e = threadIdx.x; e <= p.E; e += blockDim.x) {
-        off[e] = __ldcg(p.off + e);
-        tile0[e] = __ldcg(p.tile0 + e);
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const uint32_t tmem_sf = tmem + Cfg::ACC_COLS;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int tiles = __ldcg(p.tile0 + p.E);
     const int K = FIRST ? p.H : p.I;
     const int kc = K >> 7;                                  // blocks of 128 elements
     const int stages = (kc + 1) >> 1;                       // the last one may be half
     const int mw = FIRST ? p.I >> 6 : p.H >> 7;             // weight tiles of an expert
     const int wrows = FIRST ? 2 * p.I : p.H;                // weight rows of an expert
-    const int units = tile0[p.E] * mw;
+    UnitWalk walk(p, tiles, mw);
 
     if (warp < 4) {
         // ------------------------------------------------------------ epilogue
         int ul = 0;
-        for (int u = blockIdx.x; u < units; u += gridDim.x, ++ul) {
-            const Unit w = decode_unit(u, mw, p.E, NT, off, tile0);
+        for (; walk.more(); ++ul) {
+            const Unit w = walk.take();
             const int buf = ul & 1;
             if (threadIdx.x == 0) {
                 const bool ok = mbar_wait(accf + buf, (ul >> 1) & 1, &g_moe_error, kErrWaitAccum, p.wait_ns);
@@ -767,7 +800,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
             }
             tc_fence_before();
             mbar_arrive(acc_empty + buf);
-            store_columns<FIRST, Cfg::EPI_LD>(v, epi, w, 0, 1, p);
+            store_columns<FIRST>(v, epi, w, 0, 1, p);
         }
     } else if (warp < 8) {
         // -------------------------------------------------- tokens and scales
@@ -775,11 +808,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
         // t / 8 + 16; in the 128-byte swizzle column c of row r is at c ^ (r % 8).
         const int t = threadIdx.x - 128;
         const int r0 = t >> 3, c = t & 7;
-        const uint32_t dst0 = Cfg::TOKEN_OFF + r0 * 128 + ((c ^ (r0 & 7)) << 4);
+        const uint32_t dst0 = r0 * 128 + ((c ^ (r0 & 7)) << 4);
         int gs = 0;
         bool ok = true;
-        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-            const Unit w = decode_unit(u, mw, p.E, NT, off, tile0);
+        while (walk.more() && ok) {
+            const Unit w = walk.take();
             const bool two = w.rows > 16;
             // this thread's rows; past the tile's last row, that row again (its
             // columns are not stored)
@@ -795,7 +828,6 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
             // bytes), 64 <= t < 96 a word a token
             const uint8_t *sf = nullptr;
             uint32_t sf_dst = 0;
-            int sf_step = 512;
             if (t < 64) {
                 if constexpr (FIRST) {
                     const size_t blk = static_cast<size_t>(wrows >> 7) * w.e + (w.m >> 1) + (t >= 32 ? p.I >> 7 : 0);
@@ -816,13 +848,13 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
                 sf_dst = Cfg::SFT_OFF + lane * 16;
             }
             for (int ks = 0; ks < stages; ++ks, ++gs) {
-                const Ring r = ring_at<OPER>(gs);
-                if (gs >= OPER) ok = mbar_wait_warp(done + r.slot, r.parity ^ 1u, &g_moe_error, kErrWaitEmpty, p.wait_ns);
+                const Ring r = ring_at<TOKEN>(gs);
+                if (gs >= TOKEN) ok = mbar_wait_warp(done + r.slot, r.parity ^ 1u, &g_moe_error, kErrWaitEmpty, p.wait_ns);
                 if (!ok) {
                     *abort_flag = 1;
                     break;
                 }
-                const uint32_t st = smem_u32(smem + Cfg::OPER_AT) + r.slot * Cfg::OPER_BYTES;
+                const uint32_t st = smem_u32(smem + Cfg::TOKEN_AT) + r.slot * Cfg::TOKEN_BYTES;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int kb = 2 * ks + h;
@@ -831,11 +863,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
                         if (two) cp_async<16>(st + dst0 + h * (NT * 128) + 2048, tok[1] + kb * 128);
                         if (t < 64) {
                             if constexpr (FIRST)
-                                cp_async<8>(st + sf_dst + h * 512, sf + kb * sf_step);
+                                cp_async<8>(st + sf_dst + h * 512, sf + kb * 512);
                             else if (t < 32)
-                                cp_async<16>(st + sf_dst + h * 512, sf + kb * sf_step);
+                                cp_async<16>(st + sf_dst + h * 512, sf + kb * 512);
                         } else if (t < 96) {
-                            cp_async<4>(st + sf_dst + h * 512, sf + kb * sf_step);
+                            cp_async<4>(st + sf_dst + h * 512, sf + kb * 512);
                         }
                     }
                 }
@@ -849,26 +881,29 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
         // swizzles then spread eight lanes over all banks.
         const int group = (warp - 8) >> 2, w4 = (warp - 8) & 3;
         const int row8 = lane & 7, j = lane >> 3;
-        int gs = 0;
         bool ok = true;
-        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-            for (int ks = 0; ks < stages; ++ks, ++gs) {
-                if ((gs & 1) != group) continue;
-                const Ring rp = ring_at<PACKED>(gs), ro = ring_at<OPER>(gs);
+        const int total = (walk.units - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) /
+                          static_cast<int>(gridDim.x) * stages;
+        for (int gs = group; gs < total; gs += 2) {
+                const Ring rp = ring_at<PACKED>(gs);
                 ok = mbar_wait_warp(p_full + rp.slot, rp.parity, &g_moe_error, kErrWaitFull, p.wait_ns);
-                if (ok && gs >= OPER)
-                    ok = mbar_wait_warp(done + ro.slot, ro.parity ^ 1u, &g_moe_error, kErrWaitEmpty, p.wait_ns);
-                if (!ok) {
-                    *abort_flag = 1;
-                    break;
-                }
+                if (!ok) break;
                 const uint8_t *src = smem + rp.slot * Cfg::PACKED_BYTES + w4 * 4096 + row8 * 128;
-                uint8_t *dst = smem + Cfg::OPER_AT + ro.slot * Cfg::OPER_BYTES + w4 * 4096 + row8 * 128;
-                const int s0 = ((2 * j) ^ row8) << 4, s1 = ((2 * j + 1) ^ row8) << 4;
                 uint4 v[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     v[i] = *reinterpret_cast<const uint4 *>(src + (i & 3) * 1024 + ((((i >> 2) * 4 + j) ^ row8) << 4));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_empty + rp.slot);   // the next load may start before the wide slot is free
+                if (gs >= WIDE) {
+                    // this barrier cannot complete another round before the stage at
+                    // hand has been multiplied (WIDE <= TOKEN)
+                    const Ring rd = ring_at<TOKEN>(gs - WIDE);
+                    ok = mbar_wait_warp(done + rd.slot, rd.parity, &g_moe_error, kErrWaitEmpty, p.wait_ns);
+                    if (!ok) break;
+                }
+                uint8_t *dst = smem + Cfg::WIDE_AT + (gs % WIDE) * Cfg::WIDE_BYTES + w4 * 4096 + row8 * 128;
+                const int s0 = ((2 * j) ^ row8) << 4, s1 = ((2 * j + 1) ^ row8) << 4;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     uint8_t *d = dst + (i >> 2) * 16384 + (i & 3) * 1024;
@@ -877,19 +912,16 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(ready + ro.slot);
-                    mbar_arrive(p_empty + rp.slot);
-                }
-            }
+                if (lane == 0) mbar_arrive(ready + gs % TOKEN);
         }
+        if (!ok) *abort_flag = 1;
     } else if (warp < 18) {
         if (lane == 0) {
             // ------------------------------------------------------ MMA issuers
             const int me = warp - 16;
             int gs = 0, ul = 0, commits[2] = {0, 0};
-            for (int u = blockIdx.x; u < units; u += gridDim.x, ++ul) {
-                const Unit w = decode_unit(u, mw, p.E, NT, off, tile0);
+            for (; walk.more(); ++ul) {
+                const Unit w = walk.take();
                 const int buf = ul & 1;
                 if (ul >= 2 && !mbar_wait(acc_empty + buf, ((ul >> 1) - 1) & 1, &g_moe_error, kErrWaitAccum, p.wait_ns)) {
                     *abort_flag = 1;
@@ -900,15 +932,15 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
                 const uint32_t d = tmem + (buf * 2 + me) * NT;
                 bool ok = true;
                 for (int ks = me; ks < stages; ks += 2) {
-                    const Ring r = ring_at<OPER>(gs + ks);
+                    const Ring r = ring_at<TOKEN>(gs + ks);
                     if (!mbar_wait(ready + r.slot, r.parity, &g_moe_error, kErrWaitOperand, p.wait_ns)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t st = smem_u32(smem + Cfg::OPER_AT) + r.slot * Cfg::OPER_BYTES;
                     const uint32_t tsf = tmem_sf + r.slot * Cfg::SF_COLS;
-                    const uint64_t ad = sdesc_sw128(st), bd = sdesc_sw128(st + Cfg::TOKEN_OFF);
+                    const uint64_t ad = sdesc_sw128(smem_u32(smem + Cfg::WIDE_AT) + ((gs + ks) % WIDE) * Cfg::WIDE_BYTES);
+                    const uint64_t bd = sdesc_sw128(smem_u32(smem + Cfg::TOKEN_AT) + r.slot * Cfg::TOKEN_BYTES);
                     auto half = [&](int h, uint32_t accumulate) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
@@ -938,8 +970,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
             const uint64_t pol = policy_evict_first();
             int gs = 0;
             bool ok = true;
-            for (int u = blockIdx.x; u < units && ok && !*abort_flag; u += gridDim.x) {
-                const Unit w = decode_unit(u, mw, p.E, NT, off, tile0);
+            while (walk.more() && ok && !*abort_flag) {
+                const Unit w = walk.take();
                 // the two halves of the tile: G and U of 64 channels, or 128 rows in a row
                 const int r0 = w.e * wrows + w.m * (FIRST ? 64 : 128);
                 const int r1 = r0 + (FIRST ? p.I : 64);
@@ -955,6 +987,14 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
                     tma_load_2d(st, &p.tm_w, ks * 128, r0, p_full + r.slot, pol);
                     tma_load_2d(st + 8192, &p.tm_w, ks * 128, r1, p_full + r.slot, pol);
                     ++gs;
+                    if (ks == min(PACKED, stages) - 1 && walk.more()) {
+                        // the weight scales of the next unit go to L2 ahead of their copies (of
+                        // product 1 two runs of blocks, which two units share)
+                        const size_t blk = static_cast<size_t>(wrows >> 7) * walk.cur.x +
+                                           (walk.u / walk.tiles) / (FIRST ? 2 : 1);
+                        prefetch_l2_bulk(p.w_sf + blk * kc * 512, kc * 512);
+                        if (FIRST) prefetch_l2_bulk(p.w_sf + (blk + (p.I >> 7)) * kc * 512, kc * 512);
+                    }
                 }
             }
             // copies in flight land before the block leaves
@@ -971,10 +1011,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
         const int me = warp - 19;
         int gs = 0;
         bool ok = true;
-        for (int u = blockIdx.x; u < units && ok && !*abort_flag; u += gridDim.x)
+        while (walk.more() && ok && !*abort_flag) {
+            walk.take();
             for (int ks = 0; ks < stages; ++ks, ++gs) {
                 if ((gs & 1) != me) continue;
-                const Ring r = ring_at<OPER>(gs);
+                const Ring r = ring_at<TOKEN>(gs);
                 ok = mbar_wait(t_full + r.slot, r.parity, &g_moe_error, kErrWaitFull, p.wait_ns);
                 if (!ok) {
                     *abort_flag = 1;
@@ -982,7 +1023,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
                 }
                 fence_proxy_async_smem();
                 tc_fence_after();
-                const uint32_t st = smem_u32(smem + Cfg::OPER_AT) + r.slot * Cfg::OPER_BYTES;
+                const uint32_t st = smem_u32(smem + Cfg::TOKEN_AT) + r.slot * Cfg::TOKEN_BYTES;
                 const uint32_t tsf = tmem_sf + r.slot * Cfg::SF_COLS;
                 tc_cp_scale_block(tsf, sdesc_scale(st + Cfg::SFW_OFF));
                 tc_cp_scale_block(tsf + 8, sdesc_scale(st + Cfg::SFT_OFF));
@@ -992,6 +1033,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
                 }
                 tc_commit(ready + r.slot);
             }
+        }
         // no copy may be running when TMEM is released
         tc_commit(cp_done + me);
         mbar_wait(cp_done + me, 0, &g_moe_error, kErrWaitDrain);
@@ -1115,6 +1157,7 @@ bool moe_layout(int64_t T, int k, int E, int64_t H, int64_t I, MoeLayout *out)
     out->hist = take(out->chunks > 1 ? static_cast<size_t>(out->chunks) * E * 4 : 0);
     out->off = take((E + 1) * 4);
     out->tile0 = take((E + 1) * 4);
+    out->rec = take(static_cast<size_t>(out->max_tiles) * 16);
     out->src = take(static_cast<size_t>(R) * 4);
     out->pos = take(static_cast<size_t>(R) * 4);
     out->act = take(static_cast<size_t>(R) * I);
@@ -1131,6 +1174,7 @@ cudaError_t launch_moe_experts(const MoeArgs &a, const MoeLayout &l, cudaStream_
     pp.hist = reinterpret_cast<int *>(a.ws + l.hist);
     pp.off = reinterpret_cast<int *>(a.ws + l.off);
     pp.tile0 = reinterpret_cast<int *>(a.ws + l.tile0);
+    pp.rec = reinterpret_cast<int4 *>(a.ws + l.rec);
     pp.src = reinterpret_cast<int *>(a.ws + l.src);
     pp.pos = reinterpret_cast<int *>(a.ws + l.pos);
     pp.R = static_cast<int>(a.T * a.k);
@@ -1155,6 +1199,7 @@ cudaError_t launch_moe_experts(const MoeArgs &a, const MoeLayout &l, cudaStream_
     p.off = pp.off;
     p.tile0 = pp.tile0;
     p.src = pp.src;
+    p.rec = pp.rec;
     p.E = a.E;
     p.H = a.H;
     p.I = a.I;
