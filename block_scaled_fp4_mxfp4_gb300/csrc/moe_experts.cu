@@ -813,9 +813,9 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
         bool ok = true;
         while (walk.more() && ok) {
             const Unit w = walk.take();
-            const bool two = w.rows > 16;
-            // this thread's rows; past the tile's last row, that row again (its
+            // this thread's rows; what lies past the tile's last row is left as it is (its
             // columns are not stored)
+            const bool one = r0 < w.rows, two = r0 + 16 < w.rows;
             const uint8_t *tok[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -837,8 +837,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
                     sf = p.w_sf + static_cast<size_t>(w.e * mw + w.m) * kc * 512 + (t & 31) * 16;
                     sf_dst = Cfg::SFW_OFF + (t & 31) * 16;
                 }
-            } else if (t < 96) {
-                const int r = min(lane, w.rows - 1);
+            } else if (t < 96 && lane < w.rows) {
+                const int r = lane;
                 if constexpr (FIRST) {
                     const int tk = __ldcg(p.src + w.row0 + r);
                     sf = p.x_sf + static_cast<size_t>(tk >> 7) * kc * 512 + (tk & 31) * 16 + ((tk & 127) >> 5) * 4;
@@ -859,14 +859,14 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
                 for (int h = 0; h < 2; ++h) {
                     const int kb = 2 * ks + h;
                     if (kb < kc) {
-                        cp_async<16>(st + dst0 + h * (NT * 128), tok[0] + kb * 128);
+                        if (one) cp_async<16>(st + dst0 + h * (NT * 128), tok[0] + kb * 128);
                         if (two) cp_async<16>(st + dst0 + h * (NT * 128) + 2048, tok[1] + kb * 128);
                         if (t < 64) {
                             if constexpr (FIRST)
                                 cp_async<8>(st + sf_dst + h * 512, sf + kb * 512);
                             else if (t < 32)
                                 cp_async<16>(st + sf_dst + h * 512, sf + kb * 512);
-                        } else if (t < 96) {
+                        } else if (t < 96 && lane < w.rows) {
                             cp_async<4>(st + sf_dst + h * 512, sf + kb * 512);
                         }
                     }
