@@ -432,30 +432,48 @@ def nvfp4_group_quant_gemm(groups, problems=None, workspace=None, stream=None):
 
 
 # ---------------------------------------------------- mixture of experts --
+# Decoding calls these once a layer with kernels of a few microseconds, so what
+# runs per call is kept short: one check a tensor, sizes in Python, the raw
+# handle of the current stream.
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 MOE_SCORES = {"softmax": 0, "sigmoid": 1}
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _stream_of(stream, t):
+    return _raw_stream(t.get_device()) if stream is None else stream.cuda_stream
+
+
+def _refuse(t, name, dtype, shape, what):
+    got = f"{tuple(t.shape)} {t.dtype} with strides {t.stride()} on {t.device}"
+    raise ValueError(f"{name} must be a {what} {tuple(shape)} CUDA tensor of {dtype}, got {got}")
 
 
 def _vec(t, name, dtype, shape):
-    """A contiguous CUDA tensor of exactly this type and shape."""
-    _dev(t, name, dtype)
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {tuple(shape)} tensor")
-    return t
+    """Address of a contiguous CUDA tensor of exactly this type and shape."""
+    if not (t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()):
+        _refuse(t, name, dtype, shape, "contiguous")
+    return t.data_ptr()
 
 
 def _rows(t, name, dtype, shape):
-    """A row-major CUDA matrix of this type and shape, with any row stride."""
-    _dev(t, name, dtype, 2)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t
+    """Address and row stride of a row-major CUDA matrix of this type and shape, with
+    any row stride (that of a single row is no distance: torch may give any value)."""
+    if not (t.dtype is dtype and t.shape == shape and t.is_cuda and t.stride(1) == 1):
+        _refuse(t, name, dtype, shape, "row-major")
+    return t.data_ptr(), (t.stride(0) if shape[0] > 1 else (shape[1] + 15) // 16 * 16)
 
 
-def _ld(t):
-    # the stride of a single row is no distance (torch may give any value)
-    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 15) // 16 * 16
+def _scales(t, name, need):
+    """Address of a contiguous byte buffer of at least `need` bytes."""
+    if not (t.dtype is torch.uint8 and t.numel() >= need and t.is_cuda and t.is_contiguous()):
+        _refuse(t, name, torch.uint8, (f"at least {need}",), "contiguous")
+    return t.data_ptr()
+
+
+def _sf_bytes32(rows: int, k: int) -> int:
+    return (rows + 127) // 128 * ((k + 127) // 128) * 512
 
 
 def mxfp8_add_rmsnorm_quantize(X, weight, eps: float = 1e-6, residual=None, H=None, Y=None, Aq=None, A_sf=None,
@@ -464,33 +482,34 @@ def mxfp8_add_rmsnorm_quantize(X, weight, eps: float = 1e-6, residual=None, H=No
     include/mxfp4_moe.h): X [M, K] bf16 or fp16 -> (Aq [M, K] u8 E4M3, blocked
     E8M0 scales, h or None without a residual, y or None unless want_y or Y is
     given). H may be X or residual (in place)."""
-    if X.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError(f"X must be bf16 or fp16, got {X.dtype}")
-    _dev(X, "X", X.dtype, 2)
-    M, K = X.shape
-    _vec(weight, "weight", X.dtype, (K,))
-    if residual is not None:
-        _rows(residual, "residual", X.dtype, (M, K))
-        H = torch.empty((M, K), dtype=X.dtype, device=X.device) if H is None else H
-    if H is not None:
-        _rows(H, "H", X.dtype, (M, K))
+    dtype, shape = X.dtype, X.shape
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise ValueError(f"X must be bf16 or fp16, got {dtype}")
+    if len(shape) != 2:
+        raise ValueError(f"X must have 2 dims, got {tuple(shape)}")
+    M, K = shape
+    device = X.device
+    x, ldx = _rows(X, "X", dtype, shape)
+    w = _vec(weight, "weight", dtype, (K,))
+    res, ldr = _rows(residual, "residual", dtype, shape) if residual is not None else (None, 0)
+    if residual is not None and H is None:
+        H = torch.empty(shape, dtype=dtype, device=device)
+    h, ldh = _rows(H, "H", dtype, shape) if H is not None else (None, 0)
     if want_y and Y is None:
-        Y = torch.empty((M, K), dtype=X.dtype, device=X.device)
-    if Y is not None:
-        _rows(Y, "Y", X.dtype, (M, K))
+        Y = torch.empty(shape, dtype=dtype, device=device)
+    y, ldy = _rows(Y, "Y", dtype, shape) if Y is not None else (None, 0)
     if Aq is None:
-        Aq = torch.empty((M, (K + 15) // 16 * 16), dtype=torch.uint8, device=X.device)[:, :K]
-    _rows(Aq, "Aq", torch.uint8, (M, K))
-    need = sf_bytes(M, K, 32)
+        # rows a multiple of 16 bytes apart, as the products want them
+        Aq = torch.empty((M, (K + 15) // 16 * 16), dtype=torch.uint8, device=device)
+        if K % 16:
+            Aq = Aq[:, :K]
+    q, ldq = _rows(Aq, "Aq", torch.uint8, shape)
+    need = _sf_bytes32(M, K)
     if A_sf is None:
-        A_sf = torch.empty(need, dtype=torch.uint8, device=X.device)
-    _dev(A_sf, "A_sf", torch.uint8)
-    if A_sf.numel() < need or not A_sf.is_contiguous():
-        raise ValueError(f"A_sf must be contiguous with at least {need} bytes")
-    opt = lambda t: (t.data_ptr(), _ld(t)) if t is not None else (None, 0)  # noqa: E731
-    _check(_lib.mxfp8_add_rmsnorm_quantize(X.data_ptr(), _ld(X), *opt(residual), weight.data_ptr(), _DTYPES[X.dtype],
-                                           float(eps), M, K, *opt(H), *opt(Y), Aq.data_ptr(), _ld(Aq),
-                                           A_sf.data_ptr(), _stream_ptr(stream)),
+        A_sf = torch.empty(need, dtype=torch.uint8, device=device)
+    sf = _scales(A_sf, "A_sf", need)
+    _check(_lib.mxfp8_add_rmsnorm_quantize(x, ldx, res, ldr, w, _DTYPES[dtype], eps, M, K, h, ldh, y, ldy, q, ldq, sf,
+                                           _stream_of(stream, X)),
            "mxfp8_add_rmsnorm_quantize")
     return Aq, A_sf, H, Y
 
@@ -499,24 +518,25 @@ def moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1
               group_top: int = 2, renormalize: bool = True, scale: float = 1.0, ids=None, weights=None, stream=None):
     """Routing of tokens to experts (see include/mxfp4_moe.h): logits [T, E] bf16 /
     fp16 / fp32 -> (ids [T, k] int32, weights [T, k] fp32)."""
-    if logits.dtype not in _DTYPES:
-        raise ValueError(f"logits must be bf16, fp16 or fp32, got {logits.dtype}")
+    dtype, shape = logits.dtype, logits.shape
+    if dtype not in _DTYPES:
+        raise ValueError(f"logits must be bf16, fp16 or fp32, got {dtype}")
+    if len(shape) != 2:
+        raise ValueError(f"logits must have 2 dims, got {tuple(shape)}")
     if score not in MOE_SCORES:
         raise ValueError(f"score must be one of {sorted(MOE_SCORES)}, got {score!r}")
-    _dev(logits, "logits", logits.dtype, 2)
-    T, E = logits.shape
-    if bias is not None:
-        _vec(bias, "bias", torch.float32, (E,))
+    T, E = shape
+    z, ldl = _rows(logits, "logits", dtype, shape)
+    out = (T, max(k, 0))
     if ids is None:
-        ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=logits.device)
+        ids = torch.empty(out, dtype=torch.int32, device=logits.device)
     if weights is None:
-        weights = torch.empty((T, max(k, 0)), dtype=torch.float32, device=logits.device)
-    _vec(ids, "ids", torch.int32, (T, k))
-    _vec(weights, "weights", torch.float32, (T, k))
-    _check(_lib.moe_route(logits.data_ptr(), _DTYPES[logits.dtype], _ld(logits), T, E,
-                          bias.data_ptr() if bias is not None else None, MOE_SCORES[score], groups, topk_groups,
-                          group_top, k, int(bool(renormalize)), float(scale), ids.data_ptr(), weights.data_ptr(),
-                          _stream_ptr(stream)),
+        weights = torch.empty(out, dtype=torch.float32, device=logits.device)
+    _check(_lib.moe_route(z, _DTYPES[dtype], ldl, T, E,
+                          _vec(bias, "bias", torch.float32, (E,)) if bias is not None else None, MOE_SCORES[score],
+                          groups, topk_groups, group_top, k, 1 if renormalize else 0, scale,
+                          _vec(ids, "ids", torch.int32, out), _vec(weights, "weights", torch.float32, out),
+                          _stream_of(stream, logits)),
            "moe_route")
     return ids, weights
 
@@ -535,30 +555,25 @@ def mxfp4_moe_experts(Xq, X_sf, ids, weights, W13q, W13_sf, W2q, W2_sf, out=None
     include/mxfp4_moe.h): MXFP8 activations Xq [T, H] with blocked scales X_sf,
     ids / weights [T, k], MXFP4 weights W13q [E, 2I, H/2] and W2q [E, H, I/2] with
     scales [E, sf_bytes] -> out [T, H] bf16."""
-    _dev(Xq, "Xq", torch.uint8, 2)
+    u8 = torch.uint8
+    if Xq.dim() != 2 or W13q.dim() != 3 or ids.dim() != 2:
+        raise ValueError("Xq and ids must have 2 dims and W13q 3")
     T, H = Xq.shape
-    _dev(W13q, "W13q", torch.uint8, 3)
-    E, I = W13q.shape[0], W13q.shape[1] // 2
-    _vec(W13q, "W13q", torch.uint8, (E, 2 * I, H // 2))
-    _vec(W2q, "W2q", torch.uint8, (E, H, I // 2))
-    for name, t, n in (("X_sf", X_sf, sf_bytes(T, H, 32)), ("W13_sf", W13_sf, E * sf_bytes(2 * I, H, 32)),
-                       ("W2_sf", W2_sf, E * sf_bytes(H, I, 32))):
-        _dev(t, name, torch.uint8)
-        if t.numel() < n or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous with at least {n} bytes")
-    k = ids.shape[-1]
-    _vec(ids, "ids", torch.int32, (T, k))
-    _vec(weights, "weights", torch.float32, (T, k))
+    E, two_i, _ = W13q.shape
+    I, k = two_i // 2, ids.shape[1]
+    x, ldx = _rows(Xq, "Xq", u8, (T, H))
     if out is None:
         out = torch.empty((T, H), dtype=torch.bfloat16, device=Xq.device)
-    _rows(out, "out", torch.bfloat16, (T, H))
+    o, ldo = _rows(out, "out", torch.bfloat16, (T, H))
     if workspace is None:
         workspace = moe_experts_workspace(T, k, E, H, I, Xq.device)
-    _dev(workspace, "workspace", torch.uint8, 1)
-    _check(_lib.mxfp4_moe_experts(Xq.data_ptr(), _ld(Xq), X_sf.data_ptr(), ids.data_ptr(), weights.data_ptr(),
-                                  W13q.data_ptr(), W13_sf.data_ptr(), W2q.data_ptr(), W2_sf.data_ptr(), out.data_ptr(),
-                                  _ld(out), T, k, E, H, I, workspace.data_ptr(), workspace.numel(),
-                                  _stream_ptr(stream)),
+    _check(_lib.mxfp4_moe_experts(x, ldx, _scales(X_sf, "X_sf", _sf_bytes32(T, H)), _vec(ids, "ids", torch.int32, (T, k)),
+                                  _vec(weights, "weights", torch.float32, (T, k)),
+                                  _vec(W13q, "W13q", u8, (E, 2 * I, H // 2)),
+                                  _scales(W13_sf, "W13_sf", E * _sf_bytes32(2 * I, H)),
+                                  _vec(W2q, "W2q", u8, (E, H, I // 2)),
+                                  _scales(W2_sf, "W2_sf", E * _sf_bytes32(H, I)), o, ldo, T, k, E, H, I,
+                                  _scales(workspace, "workspace", 0), workspace.numel(), _stream_of(stream, Xq)),
            "mxfp4_moe_experts")
     return out
 
