@@ -5,13 +5,21 @@
 // the quotients. h is rounded to the element type before it is squared: the
 // norm is that of the values the next layer reads.
 //
-// Bound: HBM (2 or 4 bytes read, 1 to 5 written an element; ~6 operations). So
+// Bound: HBM (2 or 4 bytes read, 1 to 5 written an element; ~12 operations). So
 // each row is read once: a block keeps its row in registers between the sum of
 // squares and the quantization, eight elements (one 16-byte vector) a lane, and
 // four neighbouring lanes hold one block of 32.
+//
+// Exactness: an E4M3 rounding turns an fp32 error of 2^-23 into a step of 2^-3 where
+// a value lies next to a midpoint, about one element in a million. So the sum of
+// squares is carried in two floats (vectors of eight, then error-free additions), r
+// too, and a value within the fp32 error (3 units) of a midpoint, or a block's
+// maximum within it of the border between two scales, is decided again in 64
+// bits. The rule costs three integer instructions an element.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cmath>
 #include <cstring>
 
 #include "internal.h"
@@ -31,8 +39,48 @@ struct NormParams {
     int64_t ldx, ldr, ldh, ldy, ldq;
     int64_t M;
     int K;
-    float eps;
+    float keps_hi, keps_lo;     // K * eps
+    float rootk_hi, rootk_lo;   // sqrt(K)
 };
+
+// An unevaluated sum of two floats.
+struct Two {
+    float hi, lo;
+};
+
+__device__ __forceinline__ Two two_add(const Two &a, const Two &b)
+{
+    const float s = __fadd_rn(a.hi, b.hi), z = __fsub_rn(s, a.hi);
+    const float e = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, z)), __fsub_rn(b.hi, z));
+    return Two{s, __fadd_rn(e, __fadd_rn(a.lo, b.lo))};
+}
+
+// sqrt(K / m) of m = ss + K * eps: rsqrt and one Newton step on its exact residual.
+__device__ __forceinline__ Two reciprocal_rms(const Two &ss, const NormParams &p)
+{
+    const Two m = two_add(ss, Two{p.keps_hi, p.keps_lo});
+    const float q = rsqrtf(m.hi);
+    // out of this range the residual leaves fp32 (an infinite or vanishing sum)
+    if (!(m.hi > 1e-30f && m.hi < 1e30f)) return Two{m.hi == 0.0f ? 0.0f : q * p.rootk_hi, 0.0f};
+    const float s = q * q, se = fmaf(q, q, -s);
+    const float t = fmaf(-m.hi, s, 1.0f) - fmaf(m.hi, se, m.lo * s);
+    const float hi = q * p.rootk_hi;
+    const float lo = fmaf(q, p.rootk_hi, -hi) + fmaf(q, p.rootk_lo, 0.5f * t * hi);
+    const float r = hi + lo;
+    return Two{r, lo - (r - hi)};
+}
+
+// 16 bytes that this kernel reads once. Not through the read-only path: the sum may
+// be written over them.
+__device__ __forceinline__ uint4 ld_row(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
 
 template <bool F16>
 __device__ __forceinline__ float2 unpack2(uint32_t v)
@@ -84,9 +132,17 @@ __device__ __forceinline__ float sumsq8(const uint4 &a)
 // Normalizes, stores and quantizes the vector of eight values of row `row` at
 // column 8 * vec; `live`: vec lies within the row (all lanes of the warp call).
 template <bool F16>
-__device__ __forceinline__ void finish8(const NormParams &p, int64_t row, int vec, bool live, const uint4 &hv, float r)
+__device__ __forceinline__ void finish8(const NormParams &p, int64_t row, int vec, bool live, const uint4 &hv, const Two &r)
 {
     float y[8];
+    // element i from 64-bit arithmetic
+    auto exact = [&](int i) {
+        const uint32_t *ph = &hv.x;
+        const uint32_t wv = __ldg(reinterpret_cast<const uint32_t *>(p.w) + 4 * vec + (i >> 1));
+        const float2 a = unpack2<F16>(ph[i >> 1]), b = unpack2<F16>(wv);
+        return static_cast<double>(i & 1 ? a.y : a.x) * (static_cast<double>(r.hi) + static_cast<double>(r.lo)) *
+               static_cast<double>(i & 1 ? b.y : b.x);
+    };
     uint32_t amax = 0;
     if (live) {
         const uint4 wv = __ldg(reinterpret_cast<const uint4 *>(p.w) + vec);
@@ -94,8 +150,8 @@ __device__ __forceinline__ void finish8(const NormParams &p, int64_t row, int ve
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 a = unpack2<F16>(ph[i]), b = unpack2<F16>(pw[i]);
-            y[2 * i] = __fmul_rn(a.x * r, b.x);
-            y[2 * i + 1] = __fmul_rn(a.y * r, b.y);
+            y[2 * i] = __fmul_rn(__fmul_rn(a.x, r.hi), b.x);
+            y[2 * i + 1] = __fmul_rn(__fmul_rn(a.y, r.hi), b.y);
         }
         if (p.y) {
             uint4 o;
@@ -109,9 +165,35 @@ __device__ __forceinline__ void finish8(const NormParams &p, int64_t row, int ve
     }
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    const uint32_t b = live ? mxfp8_scale_byte(amax) : 0x7Fu;
+    uint32_t b = live ? mxfp8_scale_byte(amax) : 0x7Fu;
+    // a maximum within 3 units of 1.75 * 2^n takes its scale from its exact value
+    const bool border = live && (amax & 0x7FFFFFu) - 0x5FFFFDu <= 6u && amax < 0x7F800000u;
+    if (__any_sync(0xffffffffu, border)) {
+        double top = 0.0;
+        if (border)
+            for (int i = 0; i < 8; ++i) top = fmax(top, fabs(exact(i)));
+        top = fmax(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmax(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        if (border && amax >= 0x04800000u)
+            b = (amax >> 23) - 8 + (top > static_cast<double>(__uint_as_float((amax & 0x7F800000u) | 0x600000u)) ? 1u : 0u);
+    }
     if (live) {
         const float inv = mxfp8_scale_inverse(b);
+        // E4M3 keeps three bits of the mantissa: its midpoints have 0x80000 in the other 20
+        bool near = false;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) near |= (__float_as_uint(y[i]) & 0xFFFFFu) - 0x7FFFDu <= 6u;
+        if (near) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t u = __float_as_uint(y[i]);
+                if ((u & 0xFFFFFu) - 0x7FFFDu <= 6u) {
+                    const uint32_t mid = (u & 0x7FF00000u) | 0x80000u;
+                    const double d = fabs(exact(i)), md = static_cast<double>(__uint_as_float(mid));
+                    y[i] = __uint_as_float((u & 0x80000000u) | (d > md ? mid + 1 : d < md ? mid - 1 : mid));
+                }
+            }
+        }
         uint2 c;
         c.x = e4m3x4_rn(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
         c.y = e4m3x4_rn(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv);
@@ -126,37 +208,40 @@ __device__ __forceinline__ void finish8(const NormParams &p, int64_t row, int ve
 }
 
 // Sum of v over the block, the same in every thread.
-__device__ __forceinline__ float block_sum(float v, float *buf)
+__device__ __forceinline__ Two block_sum(Two v, Two *buf)
 {
+    auto warp_sum = [](Two x) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    const int nw = blockDim.x >> 5;
+        for (int o = 16; o; o >>= 1)
+            x = two_add(x, Two{__shfl_xor_sync(0xffffffffu, x.hi, o), __shfl_xor_sync(0xffffffffu, x.lo, o)});
+        return x;
+    };
+    v = warp_sum(v);
+    const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
     if (nw == 1) return v;
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+    if (lane == 0) buf[threadIdx.x >> 5] = v;
     __syncthreads();
-    float t = static_cast<int>(threadIdx.x & 31) < nw ? buf[threadIdx.x & 31] : 0.0f;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    return t;
+    return warp_sum(lane < nw ? buf[lane] : Two{0.0f, 0.0f});
 }
 
 // One row a block; VPT vectors a thread stay in registers (VPT = 0: rows of any
 // length, read a second time for the quantization).
-template <bool F16, int VPT>
-__global__ void __launch_bounds__(1024) add_rmsnorm_mxfp8_kernel(const NormParams p)
+template <bool F16, int VPT, int MAX_THREADS>
+__global__ void __launch_bounds__(MAX_THREADS) add_rmsnorm_mxfp8_kernel(const NormParams p)
 {
-    __shared__ float buf[32];
+    __shared__ Two buf[32];
     grid_dependency_wait();
     grid_launch_dependents();
     const int64_t row = blockIdx.x;
     const int nvec = p.K >> 3, nt = blockDim.x;
     const int64_t xo = row * p.ldx, ro = row * p.ldr, ho = row * p.ldh;
     auto load_h = [&](int v) {
-        uint4 a = *reinterpret_cast<const uint4 *>(p.x + xo + 8 * v);
-        if (p.res) a = add8<F16>(a, *reinterpret_cast<const uint4 *>(p.res + ro + 8 * v));
+        uint4 a = ld_row(p.x + xo + 8 * v);
+        if (p.res) a = add8<F16>(a, ld_row(p.res + ro + 8 * v));
         return a;
     };
-    float ss = 0.0f;
+    auto add_vec = [](Two s, float v) { return two_add(s, Two{v, 0.0f}); };
+    Two ss{0.0f, 0.0f};
     if constexpr (VPT > 0) {
         uint4 hv[VPT];
 #pragma unroll
@@ -168,21 +253,19 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_mxfp8_kernel(const NormParam
         for (int i = 0; i < VPT; ++i) {
             const int v = threadIdx.x + i * nt;
             if (v < nvec) {
-                ss += sumsq8<F16>(hv[i]);
+                ss = add_vec(ss, sumsq8<F16>(hv[i]));
                 if (p.h) *reinterpret_cast<uint4 *>(p.h + ho + 8 * v) = hv[i];
             }
         }
-        const float m = block_sum(ss, buf) / static_cast<float>(p.K) + p.eps;
-        const float r = m == 0.0f ? 0.0f : rsqrtf(m);
+        const Two r = reciprocal_rms(block_sum(ss, buf), p);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = threadIdx.x + i * nt;
-            if (v - static_cast<int>(threadIdx.x & 31) < (nvec + 15) / 16 * 16) finish8<F16>(p, row, v, v < nvec, hv[i], r);
+            if (v - static_cast<int>(threadIdx.x & 31) < nvec) finish8<F16>(p, row, v, v < nvec, hv[i], r);
         }
     } else {
-        for (int v = threadIdx.x; v < nvec; v += nt) ss += sumsq8<F16>(load_h(v));
-        const float m = block_sum(ss, buf) / static_cast<float>(p.K) + p.eps;
-        const float r = m == 0.0f ? 0.0f : rsqrtf(m);
+        for (int v = threadIdx.x; v < nvec; v += nt) ss = add_vec(ss, sumsq8<F16>(load_h(v)));
+        const Two r = reciprocal_rms(block_sum(ss, buf), p);
         for (int v0 = threadIdx.x & ~31; v0 < nvec; v0 += nt) {
             const int v = v0 + (threadIdx.x & 31);
             uint4 hv = make_uint4(0, 0, 0, 0);
@@ -193,24 +276,25 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_mxfp8_kernel(const NormParam
             finish8<F16>(p, row, v, v < nvec, hv, r);
         }
     }
-    // pad rows of the last 128-row block of scales, shared out over the blocks
-    const int64_t rows_pad = (p.M + 127) / 128 * 128;
+    // pad rows of the last 128-row block of scales, shared out over all threads
     const int kc = (p.K + 127) / 128;
-    for (int64_t pr = p.M + blockIdx.x; pr < rows_pad; pr += gridDim.x)
-        for (int c = threadIdx.x; c < kc; c += nt)
-            *reinterpret_cast<uint32_t *>(p.sf + ((pr >> 7) * kc + c) * 512 + (pr & 31) * 16 + ((pr & 127) >> 5) * 4) =
-                0x7F7F7F7Fu;
+    const int64_t pad_words = ((p.M + 127) / 128 * 128 - p.M) * kc;
+    for (int64_t i = row * nt + threadIdx.x; i < pad_words; i += static_cast<int64_t>(gridDim.x) * nt) {
+        const int64_t pr = p.M + i / kc;
+        *reinterpret_cast<uint32_t *>(p.sf + ((pr >> 7) * kc + i % kc) * 512 + (pr & 31) * 16 + ((pr & 127) >> 5) * 4) =
+            0x7F7F7F7Fu;
+    }
 }
 
 template <bool F16>
-cudaError_t launch_norm(const NormParams &p, cudaStream_t stream)
+cudaError_t launch_norm(const NormParams &p, int num_sms, cudaStream_t stream)
 {
-    const int nvec = p.K / 8;
-    int threads = (nvec + 31) / 32 * 32, vpt = 1;
-    while (threads > 256 && vpt < 4) {
-        vpt *= 2;
-        threads = ((nvec + vpt - 1) / vpt + 31) / 32 * 32;
-    }
+    // Many rows: blocks of up to 256 threads, several on an SM, whose phases (load,
+    // sum, store) overlap. Few rows: a row's latency counts, so a vector a thread.
+    const int nvec = p.K / 8, most = p.M <= 2 * num_sms ? 1024 : 256;
+    int vpt = 1;
+    while ((nvec + vpt - 1) / vpt > most && vpt < 4) vpt *= 2;
+    int threads = ((nvec + vpt - 1) / vpt + 31) / 32 * 32;
     if (threads > 1024) {
         vpt = 0;
         threads = 1024;
@@ -225,19 +309,22 @@ cudaError_t launch_norm(const NormParams &p, cudaStream_t stream)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    switch (vpt) {
-    case 1: return cudaLaunchKernelEx(&cfg, add_rmsnorm_mxfp8_kernel<F16, 1>, p);
-    case 2: return cudaLaunchKernelEx(&cfg, add_rmsnorm_mxfp8_kernel<F16, 2>, p);
-    case 4: return cudaLaunchKernelEx(&cfg, add_rmsnorm_mxfp8_kernel<F16, 4>, p);
-    default: return cudaLaunchKernelEx(&cfg, add_rmsnorm_mxfp8_kernel<F16, 0>, p);
+    if (vpt == 0) return cudaLaunchKernelEx(&cfg, add_rmsnorm_mxfp8_kernel<F16, 0, 1024>, p);
+    if (threads <= 256) {
+        if (vpt == 1) return cudaLaunchKernelEx(&cfg, add_rmsnorm_mxfp8_kernel<F16, 1, 256>, p);
+        if (vpt == 2) return cudaLaunchKernelEx(&cfg, add_rmsnorm_mxfp8_kernel<F16, 2, 256>, p);
+        return cudaLaunchKernelEx(&cfg, add_rmsnorm_mxfp8_kernel<F16, 4, 256>, p);
     }
+    if (vpt == 1) return cudaLaunchKernelEx(&cfg, add_rmsnorm_mxfp8_kernel<F16, 1, 1024>, p);
+    if (vpt == 2) return cudaLaunchKernelEx(&cfg, add_rmsnorm_mxfp8_kernel<F16, 2, 1024>, p);
+    return cudaLaunchKernelEx(&cfg, add_rmsnorm_mxfp8_kernel<F16, 4, 1024>, p);
 }
 
 }  // namespace
 
 cudaError_t launch_add_rmsnorm_mxfp8(const void *X, int64_t ldx, const void *res, int64_t ldr, const void *w, bool f16,
                                      float eps, int64_t M, int64_t K, void *H, int64_t ldh, void *Y, int64_t ldy,
-                                     void *Aq, int64_t ldq, void *sf, cudaStream_t stream)
+                                     void *Aq, int64_t ldq, void *sf, int num_sms, cudaStream_t stream)
 {
     NormParams p;
     p.x = static_cast<const uint16_t *>(X);
@@ -254,8 +341,13 @@ cudaError_t launch_add_rmsnorm_mxfp8(const void *X, int64_t ldx, const void *res
     p.ldq = ldq;
     p.M = M;
     p.K = static_cast<int>(K);
-    p.eps = eps;
-    return f16 ? launch_norm<true>(p, stream) : launch_norm<false>(p, stream);
+    // constants of the row's reciprocal, each as the sum of two floats
+    const double keps = static_cast<double>(eps) * static_cast<double>(K), rootk = std::sqrt(static_cast<double>(K));
+    p.keps_hi = static_cast<float>(keps);
+    p.keps_lo = std::isinf(p.keps_hi) ? 0.0f : static_cast<float>(keps - p.keps_hi);
+    p.rootk_hi = static_cast<float>(rootk);
+    p.rootk_lo = static_cast<float>(rootk - p.rootk_hi);
+    return f16 ? launch_norm<true>(p, num_sms, stream) : launch_norm<false>(p, num_sms, stream);
 }
 
 }  // namespace mxfp4

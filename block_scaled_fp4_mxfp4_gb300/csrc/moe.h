@@ -11,7 +11,7 @@ namespace mxfp4 {
 // ---------------------------------------------------- add_rmsnorm_quant.cu
 cudaError_t launch_add_rmsnorm_mxfp8(const void *X, int64_t ldx, const void *res, int64_t ldr, const void *w, bool f16,
                                      float eps, int64_t M, int64_t K, void *H, int64_t ldh, void *Y, int64_t ldy,
-                                     void *Aq, int64_t ldq, void *sf, cudaStream_t stream);
+                                     void *Aq, int64_t ldq, void *sf, int num_sms, cudaStream_t stream);
 
 // ------------------------------------------------------------ moe_route.cu
 struct RouteParams {

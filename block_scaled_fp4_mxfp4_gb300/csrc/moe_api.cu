@@ -62,7 +62,7 @@ mxfp4_status_t mxfp8_add_rmsnorm_quantize(const void *X, int64_t ldx, const void
     int sms = 0;
     if (!current_device_sms(&sms)) return MXFP4_ERR_NO_DEVICE;
     return cuda_status(launch_add_rmsnorm_mxfp8(X, ldx, residual, ldr, weight, dtype == MXFP4_DTYPE_FP16, eps, M, K, H,
-                                                ldh, Y, ldy, Aq, ldq, A_sf, static_cast<cudaStream_t>(stream)));
+                                                ldh, Y, ldy, Aq, ldq, A_sf, sms, static_cast<cudaStream_t>(stream)));
 }
 
 mxfp4_status_t moe_route(const void *logits, int dtype, int64_t ldl, int64_t T, int E, const float *bias, int score,
