@@ -160,8 +160,10 @@ __device__ __forceinline__ void finish8(const NormParams &p, int64_t row, int ve
             for (int i = 0; i < 4; ++i) po[i] = round2<F16>(y[2 * i], y[2 * i + 1]);
             *reinterpret_cast<uint4 *>(p.y + row * p.ldy + 8 * vec) = o;
         }
+        float m = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+        for (int i = 0; i < 8; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(y[i])));
+        amax = __float_as_uint(m);
     }
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
@@ -221,13 +223,18 @@ __device__ __forceinline__ Two block_sum(Two v, Two *buf)
     if (nw == 1) return v;
     if (lane == 0) buf[threadIdx.x >> 5] = v;
     __syncthreads();
-    return warp_sum(lane < nw ? buf[lane] : Two{0.0f, 0.0f});
+    // up to 8 warps: three rounds; more: all five
+    v = buf[nw <= 8 ? lane & 7 : lane];
+    if ((nw <= 8 ? lane & 7 : lane) >= nw) v = Two{0.0f, 0.0f};
+    for (int o = nw <= 8 ? 4 : 16; o; o >>= 1)
+        v = two_add(v, Two{__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
+    return v;
 }
 
 // One row a block; VPT vectors a thread stay in registers (VPT = 0: rows of any
 // length, read a second time for the quantization).
 template <bool F16, int VPT, int MAX_THREADS>
-__global__ void __launch_bounds__(MAX_THREADS) add_rmsnorm_mxfp8_kernel(const NormParams p)
+__global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 6 : 1) add_rmsnorm_mxfp8_kernel(const NormParams p)
 {
     __shared__ Two buf[32];
     grid_dependency_wait();
