@@ -32,8 +32,9 @@ struct MoeLayout {
     int nt;                 // tokens of a tile (columns of the accumulator)
     int max_tiles;          // most token tiles T * k choices can need
     int chunks;             // blocks of the placing kernel
-    size_t hist, off, tile0, rec, src, pos, act, act_sf, y, total;
+    size_t hist, off, tile0, rec, src, pos, act, act_sf, y, xs, xs_sf, total;
 };
+constexpr int kMoeLargeTile = 224;   // nt of the layouts that need sorted token rows
 bool moe_layout(int64_t T, int k, int E, int64_t H, int64_t I, MoeLayout *out);
 
 struct MoeArgs {
@@ -48,12 +49,11 @@ struct MoeArgs {
     int64_t T;
     int k, E, H, I;
     uint8_t *ws;
-    CUtensorMap tm_x;       // Xq [T, H] u8, box {128, 1}: rows gathered by index
-    CUtensorMap tm_w13;     // [E * 2I, H] 4-bit, box {128, 64}, unpacked to a byte each
-    CUtensorMap tm_pw13;    // packed weights [E * 2I, H / 2] u8, box 128 bytes x 64 rows, 128-byte swizzle
-    CUtensorMap tm_pw2;     // the same of [E * H, I / 2]
-    CUtensorMap tm_act;     // activations [rows, I] u8, box {128, 16}
-    CUtensorMap tm_w2;      // [E * H, I] 4-bit, box {128, 64}, unpacked
+    CUtensorMap tm_w13;     // packed weights [E * 2I, H / 2] u8, box 128 bytes x 64 rows
+    CUtensorMap tm_w2;      // the same of [E * H, I / 2]
+    // large tiles only: sorted token rows [R, H] and activations [R, I] (u8, box 128 bytes x half
+    // a token tile), and their scales (blocks of 128 u32, box two blocks)
+    CUtensorMap tm_xs, tm_xs_sf, tm_act, tm_act_sf;
 };
 cudaError_t launch_moe_experts(const MoeArgs &a, const MoeLayout &l, cudaStream_t stream);
 int read_and_clear_moe_error();

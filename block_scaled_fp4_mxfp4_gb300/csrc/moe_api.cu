@@ -31,13 +31,19 @@ mxfp4_status_t check_moe_sizes(int64_t T, int k, int E, int64_t H, int64_t I)
     return MXFP4_OK;
 }
 
-// Tensor map of packed E2M1 [rows, K / 2 bytes] that unpacks on load: 128 codes
-// of 64 rows, 16 codes in the low half of each 16 bytes of shared memory.
-bool unpacked_fp4_map(CUtensorMap *out, const void *base, int64_t K, int64_t rows)
+// Tensor map of contiguous 8-bit rows [rows, K], box 128 bytes x half a large token tile.
+bool token_map(CUtensorMap *out, const void *base, int64_t K, int64_t rows)
 {
-    return encode_map_2d(out, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, base, static_cast<uint64_t>(K),
-                         static_cast<uint64_t>(rows), static_cast<uint64_t>(K / 2), 128u, 64u,
-                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+    return encode_map_2d(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, static_cast<uint64_t>(K), static_cast<uint64_t>(rows),
+                         static_cast<uint64_t>(K), 128u, kMoeLargeTile / 2, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
+// Tensor map of blocks of 512 scale bytes, box two blocks.
+bool block_map(CUtensorMap *out, const void *base, int64_t blocks)
+{
+    return encode_map_2d(out, CU_TENSOR_MAP_DATA_TYPE_UINT32, base, 128u, static_cast<uint64_t>(blocks), 512u, 128u, 2u,
+                         CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 }  // namespace
@@ -146,16 +152,12 @@ mxfp4_status_t mxfp4_moe_experts(const void *Xq, int64_t ldx, const void *X_sf, 
     a.H = static_cast<int>(H);
     a.I = static_cast<int>(I);
     a.ws = static_cast<uint8_t *>(workspace);
-    const bool maps =
-        encode_map_2d(&a.tm_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, Xq, static_cast<uint64_t>(H), static_cast<uint64_t>(T),
-                      static_cast<uint64_t>(ldx), 128u, 1u, CU_TENSOR_MAP_SWIZZLE_128B,
-                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B) &&
-        encode_map_2d(&a.tm_act, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.ws + l.act, static_cast<uint64_t>(I),
-                      static_cast<uint64_t>(T * k), static_cast<uint64_t>(I), 128u, 16u, CU_TENSOR_MAP_SWIZZLE_128B,
-                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B) &&
-        encode_packed_map(W13q, H / 2, 2 * I * E, H / 2, 64, &a.tm_pw13) &&
-        encode_packed_map(W2q, I / 2, H * E, I / 2, 64, &a.tm_pw2) &&
-        unpacked_fp4_map(&a.tm_w13, W13q, H, 2 * I * E) && unpacked_fp4_map(&a.tm_w2, W2q, I, H * E);
+    bool maps = encode_packed_map(W13q, H / 2, 2 * I * E, H / 2, 64, &a.tm_w13) &&
+                encode_packed_map(W2q, I / 2, H * E, I / 2, 64, &a.tm_w2);
+    if (l.nt == kMoeLargeTile)
+        maps = maps && token_map(&a.tm_xs, a.ws + l.xs, H, T * k) && token_map(&a.tm_act, a.ws + l.act, I, T * k) &&
+               block_map(&a.tm_xs_sf, a.ws + l.xs_sf, int64_t(l.max_tiles) * (H / 128) * 2) &&
+               block_map(&a.tm_act_sf, a.ws + l.act_sf, int64_t(l.max_tiles) * (I / 128) * 2);
     if (!maps) return MXFP4_ERR_CUDA;
     return cuda_status(launch_moe_experts(a, l, static_cast<cudaStream_t>(stream)));
 }

@@ -12,8 +12,8 @@
 //            choice i sits in row pos[i]; tile0[e] counts tiles of NT rows.
 //            More than kChunk choices take several blocks and a counting launch
 //            before it.
-//   product1 rows gathered by TMA from the unsorted activations; epilogue
-//            silu(g) * u, MXFP8, to the workspace in sorted order
+//   gather   long batches only: token rows and their scales in sorted order
+//   product1 epilogue silu(g) * u, MXFP8, to the workspace in sorted order
 //   product2 act x W2^T, bf16 rows to the workspace
 //   combine  out_t = sum_j w_tj row[pos[t, j]], in the order of j: no atomics, so
 //            the result does not depend on the order of the sorted rows
@@ -176,8 +176,9 @@ __global__ void __launch_bounds__(kPlaceThreads) moe_place_kernel(const PlacePar
 // ----------------------------------------------------------------- products
 
 struct ProductParams {
-    CUtensorMap tm_w;       // weights, unpacked on load: box 128 elements x 64 rows
-    CUtensorMap tm_t;       // tokens: product 1 gathers rows of Xq; product 2 loads 16-row boxes of act
+    CUtensorMap tm_w;       // packed weights [E * rows, K / 2] u8, box 128 bytes x 64 rows
+    CUtensorMap tm_t;       // large tiles: token rows [R, K] u8, box 128 bytes x kLargeNT / 2 rows
+    CUtensorMap tm_tsf;     // large tiles: their scales [tiles * K / 128 * 2] blocks of 128 u32, box two blocks
     const uint8_t *w_sf;    // blocked weight scales, one buffer an expert
     const uint8_t *x;       // product 1: Xq, rows ldx bytes apart
     int64_t ldx;
@@ -185,382 +186,18 @@ struct ProductParams {
     uint8_t *act;           // [rows, I] E4M3 (product 1 writes, product 2 reads through tm_t)
     uint8_t *act_sf;        // [tiles][I / 128][NT / 128 rounded up][512]
     uint16_t *y;            // product 2: [rows, H] bf16
-    const int *off, *tile0, *src;
+    const int *tile0, *src;
     const int4 *rec;
     int E, H, I;
     uint64_t wait_ns;
 };
 
-__host__ __device__ constexpr uint32_t tmem_pow2(uint32_t n)
-{
-    return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : n <= 256 ? 256 : 512;
-}
-
-template <int NT, int STAGES>
-struct ProductCfg {
-    static constexpr int NTB = (NT + 127) / 128;           // scale blocks of a token tile
-    static constexpr uint32_t W_BYTES = 128 * 128;         // 128 weight rows, a byte an element
-    static constexpr uint32_t T_BYTES = NT * 128;
-    static constexpr uint32_t SFW_OFF = W_BYTES + T_BYTES;
-    static constexpr uint32_t SFT_OFF = SFW_OFF + 512;
-    static constexpr uint32_t STAGE_BYTES = (SFT_OFF + NTB * 512 + 1023) / 1024 * 1024;
-    static constexpr int EPI_LD = 132;                     // floats of a staged column
-    static constexpr uint32_t EPI_BYTES = 32 * EPI_LD * 4;
-    static constexpr uint32_t TAB_BYTES = 2 * (kMaxExperts + 4) * 4;
-    static constexpr uint32_t BAR_BYTES = 512;
-    static constexpr uint32_t SMEM_BYTES = STAGES * STAGE_BYTES + EPI_BYTES + TAB_BYTES + BAR_BYTES + 1024;
-    static constexpr uint32_t SF_COLS = 4 + 4 * NTB;
-    static constexpr uint32_t TMEM_COLS = tmem_pow2(2 * NT + STAGES * SF_COLS);
-    static constexpr int LAG = STAGES / 2;                 // stages whose gathered scales are in flight
-    static_assert(NT % 32 == 0 && NT <= 256, "token tile");
-    static_assert(2 * NT + STAGES * SF_COLS <= 512, "TMEM budget");
-    static_assert(SMEM_BYTES <= 232448, "shared memory budget");
-    static_assert((2 * STAGES + 6) * 8 + 32 <= BAR_BYTES, "barrier area");
-};
-
-// One unit of work: 128 weight rows x one token tile of an expert.
+// One unit of work: a tile of weight rows (index m) x one token tile of an expert.
 struct Unit {
     int e, m, tile, row0, rows;
 };
 
-// Units of one expert are consecutive, its token tiles innermost: the blocks that
-// work on the same weights at the same time read them from L2.
-__device__ __forceinline__ Unit decode_unit(int u, int mw, int E, int nt, const int *off, const int *tile0)
-{
-    Unit w;
-    const int q = u / mw;
-    int lo = 0, hi = E - 1;   // the last expert with tile0[e] <= q; it has tiles, since tile0[e + 1] > q
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (tile0[mid] <= q)
-            lo = mid;
-        else
-            hi = mid - 1;
-    }
-    w.e = lo;
-    const int t0 = tile0[lo], nj = tile0[lo + 1] - t0;
-    const int local = u - t0 * mw;
-    w.m = local / nj;
-    const int j = local - w.m * nj;
-    w.tile = t0 + j;
-    w.row0 = off[lo] + j * nt;
-    w.rows = min(nt, off[lo + 1] - w.row0);
-    return w;
-}
-
 __device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-
-// FIRST: product 1 (tokens x [G; U], SwiGLU, MXFP8), else product 2. Warps:
-//   0    loads: weights by TMA (lane 0), token rows by TMA (all lanes), and in
-//        product 2 the scales
-//   1    TMEM owner; lane 0 copies scales to TMEM and issues the MMAs
-//   2    product 1: scales of weights and gathered tokens (4 and 8 byte copies)
-//   4-7  epilogue of a finished tile while the next one's mainloop runs (two
-//        accumulators)
-template <bool FIRST, int NT, int STAGES>
-__global__ void __launch_bounds__(256, 1) moe_product_kernel(const __grid_constant__ ProductParams p)
-{
-    using Cfg = ProductCfg<NT, STAGES>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float *epi = reinterpret_cast<float *>(smem + STAGES * Cfg::STAGE_BYTES);
-    int *off = reinterpret_cast<int *>(smem + STAGES * Cfg::STAGE_BYTES + Cfg::EPI_BYTES);
-    int *tile0 = off + kMaxExperts + 4;
-    uint64_t *full = reinterpret_cast<uint64_t *>(tile0 + kMaxExperts + 4);
-    uint64_t *empty = full + STAGES;
-    uint64_t *accf = empty + STAGES;      // [2] accumulator complete
-    uint64_t *acc_empty = accf + 2;       // [2] accumulator drained
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    volatile int *epi_go = abort_flag + 1;   // [2]
-
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) {
-            mbar_init(full + s, FIRST ? 2 : 1);
-            mbar_init(empty + s, 1);
-        }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(accf + b, 1);
-            mbar_init(acc_empty + b, 128);
-        }
-        *abort_flag = 0;
-        fence_mbar_init();
-        tma_prefetch_desc(&p.tm_w);
-        tma_prefetch_desc(&p.tm_t);
-    }
-    if (warp == 1) {
-        tmem_alloc(tmem_slot, Cfg::TMEM_COLS);
-        tmem_relinquish();
-    }
-    grid_dependency_wait();
-    grid_launch_dependents();
-    for (int e = threadIdx.x; e <= p.E; e += blockDim.x) {
-        off[e] = __ldcg(p.off + e);
-        tile0[e] = __ldcg(p.tile0 + e);
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    const uint32_t tmem_sf = tmem + 2 * NT;
-    const int K = FIRST ? p.H : p.I;
-    const int kc = K >> 7;                                  // stages of a tile
-    const int mw = FIRST ? p.I >> 6 : p.H >> 7;             // weight tiles of an expert
-    const int wrows = FIRST ? 2 * p.I : p.H;                // weight rows of an expert
-    const int units = tile0[p.E] * mw;
-    int issued = 0;
-
-    if (warp == 0) {
-        const uint64_t pol_w = policy_evict_first(), pol_t = policy_evict_last();
-        int gs = 0;
-        bool ok = true;
-        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;   // one verdict for the warp
-            const Unit w = decode_unit(u, mw, p.E, NT, off, tile0);
-            const int n16 = (w.rows + 15) >> 4;
-            // weight rows of the two halves of the tile
-            const int r0 = w.e * wrows + w.m * (FIRST ? 64 : 128);
-            const int r1 = r0 + (FIRST ? p.I : 64);
-            int4 quad[(NT + 127) / 128];
-            if constexpr (FIRST) {
-                // this lane's rows 4 q .. 4 q + 3, q = lane and lane + 32; past the
-                // tile's last row, that row again (its columns are not stored)
-#pragma unroll
-                for (int i = 0; i < (NT + 127) / 128; ++i) {
-                    const int r = 4 * (lane + 32 * i);
-                    const int *s = p.src + w.row0;
-                    quad[i] = make_int4(__ldcg(s + min(r, w.rows - 1)), __ldcg(s + min(r + 1, w.rows - 1)),
-                                        __ldcg(s + min(r + 2, w.rows - 1)), __ldcg(s + min(r + 3, w.rows - 1)));
-                }
-            }
-            // an unpacking load counts the packed bytes it reads, 64 a row
-            const uint32_t bytes = Cfg::W_BYTES / 2 + n16 * 2048u + (FIRST ? 0u : 512u + Cfg::NTB * 512u);
-            for (int ks = 0; ks < kc; ++ks, ++gs) {
-                const int slot = gs % STAGES;
-                if (gs >= STAGES)
-                    ok = mbar_wait_warp(empty + slot, ((gs / STAGES) - 1) & 1, &g_moe_error, kErrWaitEmpty, p.wait_ns);
-                if (!ok) {
-                    *abort_flag = 1;
-                    break;
-                }
-                uint8_t *st = smem + slot * Cfg::STAGE_BYTES;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(full + slot, bytes);
-                    tma_load_2d(st, &p.tm_w, ks * 128, r0, full + slot, pol_w);
-                    tma_load_2d(st + 8192, &p.tm_w, ks * 128, r1, full + slot, pol_w);
-                }
-                __syncwarp();
-                if constexpr (FIRST) {
-#pragma unroll
-                    for (int i = 0; i < (NT + 127) / 128; ++i) {
-                        const int q = lane + 32 * i;
-                        if (q < 4 * n16)
-                            tma_gather4(st + Cfg::W_BYTES + q * 512, &p.tm_t, ks * 128, quad[i], full + slot, pol_t);
-                    }
-                } else {
-                    if (lane < n16)
-                        tma_load_2d(st + Cfg::W_BYTES + lane * 2048, &p.tm_t, ks * 128, w.row0 + 16 * lane, full + slot,
-                                    pol_t);
-                    if (lane == 0) {
-                        bulk_load(st + Cfg::SFW_OFF,
-                                  p.w_sf + (static_cast<size_t>(w.e * mw + w.m) * kc + ks) * 512, 512, full + slot, pol_w);
-                        bulk_load(st + Cfg::SFT_OFF,
-                                  p.act_sf + (static_cast<size_t>(w.tile) * kc + ks) * (Cfg::NTB * 512), Cfg::NTB * 512,
-                                  full + slot, pol_t);
-                    }
-                }
-                issued = gs + 1;
-            }
-        }
-    } else if (warp == 1 && lane == 0) {
-        int gs = 0, ul = 0, commits[2] = {0, 0};
-        for (int u = blockIdx.x; u < units; u += gridDim.x, ++ul) {
-            const Unit w = decode_unit(u, mw, p.E, NT, off, tile0);
-            const int buf = ul & 1;
-            if (ul >= 2 && !mbar_wait(acc_empty + buf, ((ul >> 1) - 1) & 1, &g_moe_error, kErrWaitAccum, p.wait_ns)) {
-                *abort_flag = 1;
-                break;
-            }
-            tc_fence_after();
-            const int n = (w.rows + 15) & ~15;
-            const uint32_t idesc = idesc_w4a8(n);
-            const uint32_t d = tmem + buf * NT;
-            bool ok = true;
-            for (int ks = 0; ks < kc; ++ks, ++gs) {
-                const int slot = gs % STAGES;
-                if (!mbar_wait(full + slot, (gs / STAGES) & 1, &g_moe_error, kErrWaitFull, p.wait_ns)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                uint8_t *st = smem + slot * Cfg::STAGE_BYTES;
-                // scale copies and MMAs of one thread run in order
-                const uint32_t tsfw = tmem_sf + slot * Cfg::SF_COLS, tsft = tsfw + 4;
-                tc_cp_scale_block(tsfw, sdesc_scale(smem_u32(st + Cfg::SFW_OFF)));
-                tc_cp_scale_block(tsft, sdesc_scale(smem_u32(st + Cfg::SFT_OFF)));
-                if (Cfg::NTB > 1 && n > 128) tc_cp_scale_block(tsft + 4, sdesc_scale(smem_u32(st + Cfg::SFT_OFF + 512)));
-                const uint64_t ad = sdesc_sw128(smem_u32(st)), bd = sdesc_sw128(smem_u32(st + Cfg::W_BYTES));
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_mxf8f6f4(d, ad + 2 * kk, bd + 2 * kk, idesc_with_sf_ids(idesc, kk, kk), tsfw, tsft,
-                                 (ks > 0 || kk > 0) ? 1u : 0u);
-                tc_commit(empty + slot);
-            }
-            tc_commit(accf + buf);
-            ++commits[buf];
-            if (!ok) {
-                *abort_flag = 1;
-                break;
-            }
-        }
-        // no MMA may be running when TMEM is released
-        for (int b = 0; b < 2; ++b)
-            if (commits[b] > 0) mbar_wait(accf + b, (commits[b] - 1) & 1, &g_moe_error, kErrWaitDrain);
-    } else if (FIRST && warp == 2) {
-        int gs = 0, done = 0;
-        bool ok = true;
-        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;   // one verdict for the warp
-            const Unit w = decode_unit(u, mw, p.E, NT, off, tile0);
-            // 64 channels are half of a 128-row scale block: 8 of each 16 bytes, of G and of U
-            const size_t blk = static_cast<size_t>(wrows >> 7) * w.e + (w.m >> 1);
-            const uint8_t *g_sf = p.w_sf + blk * kc * 512 + lane * 16 + (w.m & 1) * 8;
-            const uint8_t *u_sf = g_sf + static_cast<size_t>(p.I >> 7) * kc * 512;
-            const uint8_t *t_sf[NT / 32];
-#pragma unroll
-            for (int i = 0; i < NT / 32; ++i) {
-                const int t = __ldcg(p.src + w.row0 + min(lane + 32 * i, w.rows - 1));
-                t_sf[i] = p.x_sf + static_cast<size_t>(t >> 7) * kc * 512 + (t & 31) * 16 + ((t & 127) >> 5) * 4;
-            }
-            for (int ks = 0; ks < kc; ++ks, ++gs) {
-                const int slot = gs % STAGES;
-                if (gs >= STAGES)
-                    ok = mbar_wait_warp(empty + slot, ((gs / STAGES) - 1) & 1, &g_moe_error, kErrWaitEmpty, p.wait_ns);
-                if (!ok) {
-                    *abort_flag = 1;
-                    break;
-                }
-                uint8_t *st = smem + slot * Cfg::STAGE_BYTES;
-                cp_async<8>(smem_u32(st) + Cfg::SFW_OFF + lane * 16, g_sf + ks * 512);
-                cp_async<8>(smem_u32(st) + Cfg::SFW_OFF + lane * 16 + 8, u_sf + ks * 512);
-#pragma unroll
-                for (int i = 0; i < NT / 32; ++i)
-                    if (32 * i < w.rows)
-                        cp_async<4>(smem_u32(st) + Cfg::SFT_OFF + (i >> 2) * 512 + lane * 16 + (i & 3) * 4, t_sf[i] + ks * 512);
-                cp_async_commit();
-                if (gs - done >= Cfg::LAG) {
-                    cp_async_wait<Cfg::LAG>();
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(full + done % STAGES);
-                    ++done;
-                }
-            }
-        }
-        cp_async_wait<0>();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0)
-            for (; done < gs; ++done) mbar_arrive(full + done % STAGES);
-    } else if (warp >= 4) {
-        const int q = warp & 3, t = threadIdx.x - 128;
-        const int col = t >> 2, part = t & 3;      // this thread's token column and quarter of the staged rows
-        int ul = 0;
-        for (int u = blockIdx.x; u < units; u += gridDim.x, ++ul) {
-            const Unit w = decode_unit(u, mw, p.E, NT, off, tile0);
-            const int buf = ul & 1;
-            if (t == 0) {
-                const bool ok = mbar_wait(accf + buf, (ul >> 1) & 1, &g_moe_error, kErrWaitAccum, p.wait_ns);
-                if (!ok) *abort_flag = 1;
-                epi_go[buf] = ok && !*abort_flag;
-            }
-            epilogue_sync();
-            if (!epi_go[buf]) break;
-            tc_fence_after();
-            const uint32_t trow = tmem + buf * NT + (static_cast<uint32_t>(q * 32) << 16);
-            for (int c0 = 0; c0 < w.rows; c0 += 32) {
-                // 32 columns of the 128 rows through shared memory, so that a
-                // thread gets neighbouring rows (channels) of one column (token)
-                uint32_t v[32];
-                tmem_ld32(trow + c0, v);
-                tmem_ld_wait();
-                if (c0 + 32 >= w.rows) {
-                    tc_fence_before();
-                    mbar_arrive(acc_empty + buf);
-                }
-#pragma unroll
-                for (int j = 0; j < 32; ++j) epi[j * Cfg::EPI_LD + q * 32 + lane] = __uint_as_float(v[j]);
-                epilogue_sync();
-                const bool live = c0 + col < w.rows;
-                const size_t row = static_cast<size_t>(w.row0) + c0 + col;
-                if constexpr (FIRST) {
-                    // 16 channels a thread; two neighbours share a block of 32
-                    const float *g = epi + col * Cfg::EPI_LD + 16 * part;
-                    float a[16];
-                    uint32_t amax = 0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 gv = *reinterpret_cast<const float4 *>(g + 4 * i);
-                        const float4 uv = *reinterpret_cast<const float4 *>(g + 64 + 4 * i);
-                        a[4 * i] = __fdividef(gv.x, 1.0f + __expf(-gv.x)) * uv.x;
-                        a[4 * i + 1] = __fdividef(gv.y, 1.0f + __expf(-gv.y)) * uv.y;
-                        a[4 * i + 2] = __fdividef(gv.z, 1.0f + __expf(-gv.z)) * uv.z;
-                        a[4 * i + 3] = __fdividef(gv.w, 1.0f + __expf(-gv.w)) * uv.w;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) amax = max(amax, __float_as_uint(a[i]) & 0x7FFFFFFFu);
-                    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                    const uint32_t b = mxfp8_scale_byte(amax);
-                    const float inv = mxfp8_scale_inverse(b);
-                    const uint32_t b2 = __shfl_down_sync(0xffffffffu, b, 2);
-                    if (live) {
-                        uint4 c;
-                        c.x = e4m3x4_rn(a[0] * inv, a[1] * inv, a[2] * inv, a[3] * inv);
-                        c.y = e4m3x4_rn(a[4] * inv, a[5] * inv, a[6] * inv, a[7] * inv);
-                        c.z = e4m3x4_rn(a[8] * inv, a[9] * inv, a[10] * inv, a[11] * inv);
-                        c.w = e4m3x4_rn(a[12] * inv, a[13] * inv, a[14] * inv, a[15] * inv);
-                        *reinterpret_cast<uint4 *>(p.act + row * p.I + 64 * w.m + 16 * part) = c;
-                        if (part == 0) {
-                            const int r = c0 + col;
-                            uint8_t *sf = p.act_sf +
-                                          (static_cast<size_t>(w.tile) * (p.I >> 7) + (w.m >> 1)) * (Cfg::NTB * 512) +
-                                          (r >> 7) * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4 + (w.m & 1) * 2;
-                            *reinterpret_cast<uint16_t *>(sf) = static_cast<uint16_t>(b | (b2 << 8));
-                        }
-                    }
-                } else {
-                    const float *s = epi + col * Cfg::EPI_LD + 32 * part;
-                    if (live) {
-                        uint4 *o = reinterpret_cast<uint4 *>(p.y + row * p.H + 128 * w.m + 32 * part);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float4 x = *reinterpret_cast<const float4 *>(s + 8 * i);
-                            const float4 z = *reinterpret_cast<const float4 *>(s + 8 * i + 4);
-                            const __nv_bfloat162 h[4] = {__floats2bfloat162_rn(x.x, x.y), __floats2bfloat162_rn(x.z, x.w),
-                                                         __floats2bfloat162_rn(z.x, z.y), __floats2bfloat162_rn(z.z, z.w)};
-                            o[i] = *reinterpret_cast<const uint4 *>(h);
-                        }
-                    }
-                }
-                epilogue_sync();   // the staging buffer is reused
-            }
-        }
-    }
-    __syncwarp();
-
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 0 && lane == 0) {
-        // copies still in flight (only after an abort) land before the block leaves
-        for (int i = max(0, issued - STAGES); i < issued; ++i)
-            mbar_wait(full + (i % STAGES), (i / STAGES) & 1, &g_moe_error, kErrWaitDrain);
-    }
-    if (warp == 1) {
-        tc_fence_after();
-        tmem_dealloc(tmem, Cfg::TMEM_COLS);
-    }
-}
 
 // --------------------------------------------------- products, few tokens
 //
@@ -682,25 +319,44 @@ __device__ __forceinline__ void store_columns(const uint32_t (&v)[32], float *ep
     }
 }
 
-// Walks the units of a block of the small kernel: unit u is token tile u % tiles and
-// weight tile u / tiles, so the blocks at work read different experts, and tiles of
-// one expert read the same weights at the same time. The record of the next unit
-// is on its way while the current one is worked on.
+// Walks the units first, first + step, ... of `tiles` token tiles x mw weight tiles:
+// GROUP token tiles (all of them if 0) for one weight tile after another. Tiles of
+// one expert are neighbours, so those at work on the same weights read them from
+// L2, and a group's tokens stay there too. The record of the next unit is on its
+// way while the current one is worked on.
+template <int GROUP>
 struct UnitWalk {
     const int4 *rec;
-    int tiles, units, u;
-    int4 cur;
-    __device__ __forceinline__ UnitWalk(const ProductParams &p, int tiles_, int mw)
-        : rec(p.rec), tiles(tiles_), units(tiles_ * mw), u(blockIdx.x)
+    int tiles, mw, units, u, step;
+    int next_tile, next_m;
+    int4 next;
+    __device__ __forceinline__ UnitWalk(const ProductParams &p, int tiles_, int mw_, int first, int step_)
+        : rec(p.rec), tiles(tiles_), mw(mw_), units(tiles_ * mw_), u(first), step(step_)
     {
-        if (u < units) cur = __ldcg(rec + u % tiles);
+        fetch();
+    }
+    __device__ __forceinline__ void fetch()
+    {
+        if (u >= units) return;
+        if constexpr (GROUP == 0) {
+            next_m = u / tiles;
+            next_tile = u - next_m * tiles;
+        } else {
+            const int g = u / (GROUP * mw), local = u - g * (GROUP * mw);
+            const int n = min(GROUP, tiles - g * GROUP);   // the last group may be smaller
+            next_m = local / n;
+            next_tile = g * GROUP + local - next_m * n;
+        }
+        next = __ldcg(rec + next_tile);
     }
     __device__ __forceinline__ bool more() const { return u < units; }
+    // units that are left for this walker
+    __device__ __forceinline__ int left() const { return u < units ? (units - u + step - 1) / step : 0; }
     __device__ __forceinline__ Unit take()
     {
-        const Unit w{cur.x, u / tiles, u % tiles, cur.y, cur.z};
-        u += gridDim.x;
-        if (u < units) cur = __ldcg(rec + u % tiles);
+        const Unit w{next.x, next_m, next_tile, next.y, next.z};
+        u += step;
+        fetch();
         return w;
     }
 };
@@ -771,7 +427,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
     const int stages = (kc + 1) >> 1;                       // the last one may be half
     const int mw = FIRST ? p.I >> 6 : p.H >> 7;             // weight tiles of an expert
     const int wrows = FIRST ? 2 * p.I : p.H;                // weight rows of an expert
-    UnitWalk walk(p, tiles, mw);
+    UnitWalk<0> walk(p, tiles, mw, blockIdx.x, gridDim.x);
 
     if (warp < 4) {
         // ------------------------------------------------------------ epilogue
@@ -882,8 +538,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
         const int group = (warp - 8) >> 2, w4 = (warp - 8) & 3;
         const int row8 = lane & 7, j = lane >> 3;
         bool ok = true;
-        const int total = (walk.units - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) /
-                          static_cast<int>(gridDim.x) * stages;
+        const int total = walk.left() * stages;
         for (int gs = group; gs < total; gs += 2) {
                 const Ring rp = ring_at<PACKED>(gs);
                 ok = mbar_wait_warp(p_full + rp.slot, rp.parity, &g_moe_error, kErrWaitFull, p.wait_ns);
@@ -990,8 +645,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
                     if (ks == min(PACKED, stages) - 1 && walk.more()) {
                         // the weight scales of the next unit go to L2 ahead of their copies (of
                         // product 1 two runs of blocks, which two units share)
-                        const size_t blk = static_cast<size_t>(wrows >> 7) * walk.cur.x +
-                                           (walk.u / walk.tiles) / (FIRST ? 2 : 1);
+                        const size_t blk = static_cast<size_t>(wrows >> 7) * walk.next.x + walk.next_m / (FIRST ? 2 : 1);
                         prefetch_l2_bulk(p.w_sf + blk * kc * 512, kc * 512);
                         if (FIRST) prefetch_l2_bulk(p.w_sf + (blk + (p.I >> 7)) * kc * 512, kc * 512);
                     }
@@ -1045,6 +699,384 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
     if (warp == 16) {
         tc_fence_after();
         tmem_dealloc(tmem, Cfg::TMEM_COLS);
+    }
+}
+
+// --------------------------------------------------- products, many tokens
+//
+// Tiles of 256 weight rows x up to kLargeNT tokens on CTA pairs (cta_group::2): each
+// CTA holds 128 of the weight rows and half of the tokens, so an SM takes in 16 KB of
+// widened weights and 14 KB of tokens for 448 clocks of MMA a stage of 128 elements.
+// What bounds a stage is shared memory (128 bytes a clock): packed weights in 64
+// clocks, read again 64, widened 128, tokens 112, read by the MMAs 128 + 112, together
+// 608. (A single CTA's tile of 128 x 224 needs 832.) Token rows come by TMA, which
+// wants them in sorted order: moe_gather_kernel copies them there. (Gathered by
+// cp.async instead, 28 KB a stage took 900 clocks.)
+
+constexpr int kLargeNT = kMoeLargeTile;
+constexpr int kLargeThreads = 544;
+
+struct LargeCfg {
+    static constexpr int PACKED = 3, OPER = 5;
+    static constexpr int HALF = kLargeNT / 2;                        // token rows of a CTA
+    static constexpr uint32_t PSF_OFF = 128 * 128;                   // packed stage: 256 elements of 128 rows, then scales
+    static constexpr uint32_t PACKED_BYTES = PSF_OFF + 2048;         // of G and of U, or of 128 rows: 2 x 2 blocks
+    static constexpr uint32_t WSF_OFF = 128 * 128;                   // widened stage: 128 elements, then their block of scales
+    static constexpr uint32_t WIDE_BYTES = WSF_OFF + 1024;
+    static constexpr uint32_t TSF_OFF = HALF * 128;                  // token stage: 128 elements, then two blocks of scales
+    static constexpr uint32_t TOKEN_BYTES = TSF_OFF + 1024;
+    static constexpr uint32_t WIDE_AT = PACKED * PACKED_BYTES;
+    static constexpr uint32_t TOKEN_AT = WIDE_AT + OPER * WIDE_BYTES;
+    static constexpr uint32_t EPI_AT = TOKEN_AT + OPER * TOKEN_BYTES;
+    static constexpr uint32_t BAR_AT = EPI_AT + kEpiBytes;
+    static constexpr int BARS = 2 * PACKED + 4 * OPER + 6;
+    static constexpr uint32_t SMEM_BYTES = BAR_AT + BARS * 8 + 32 + 1024;
+    static constexpr uint32_t SF_COLS = 12;                          // a block of weights, two of tokens
+    static constexpr uint32_t TMEM_COLS = 512;
+    static_assert(PACKED_BYTES % 1024 == 0 && WIDE_BYTES % 1024 == 0 && TOKEN_BYTES % 1024 == 0, "swizzle atoms");
+    static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+    static_assert(2 * kLargeNT + OPER * SF_COLS <= TMEM_COLS, "TMEM budget");
+    static_assert(HALF % 16 == 0, "halves of a tile are MMA operands");
+};
+
+// FIRST: product 1 (a pair's tile: 128 channels of G and of U, 64 of each in a CTA),
+// else product 2 (256 rows). Warps of each CTA:
+//   0-3    epilogue of the CTA's 128 weight rows
+//   4-11   widen packed weights: groups of four on alternating packed stages; they
+//          also see the stage's tokens land, and tell rank 0
+//   12     owns TMEM; lane 0 of rank 0 issues the MMAs
+//   13     lane 0 loads packed weights and their scales by TMA
+//   14     lane 0 loads tokens and their scales by TMA
+//   15,16  lane 0 of each, rank 0: copies the scales of alternating stages to both TMEMs
+template <bool FIRST>
+__global__ void __launch_bounds__(kLargeThreads, 1) moe_product_large_kernel(const __grid_constant__ ProductParams p)
+{
+    using Cfg = LargeCfg;
+    constexpr int PACKED = Cfg::PACKED, OPER = Cfg::OPER, NT = kLargeNT;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float *epi = reinterpret_cast<float *>(smem + Cfg::EPI_AT);
+    uint64_t *p_full = reinterpret_cast<uint64_t *>(smem + Cfg::BAR_AT);
+    uint64_t *p_empty = p_full + PACKED;
+    uint64_t *t_full = p_empty + PACKED;
+    uint64_t *ready = t_full + OPER;       // rank 0: both CTAs' operands of a stage are in shared memory
+    uint64_t *s_full = ready + OPER;       // rank 0: its scales are in both TMEMs
+    uint64_t *done = s_full + OPER;        // its MMAs have completed
+    uint64_t *accf = done + OPER;          // [2] accumulators complete
+    uint64_t *acc_empty = accf + 2;        // [2] rank 0: both CTAs have drained them
+    uint64_t *cp_done = acc_empty + 2;     // [2] rank 0: the scale copies of warp 15 / 16 have completed
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(cp_done + 2);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    volatile int *epi_go = abort_flag + 1;   // [2]
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(cluster_ctarank());
+    const bool leader = rank == 0;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < PACKED; ++i) {
+            mbar_init(p_full + i, 1);
+            mbar_init(p_empty + i, 4);      // one arrival from each warp of a widening group
+        }
+        for (int i = 0; i < OPER; ++i) {
+            mbar_init(t_full + i, 1);
+            mbar_init(ready + i, 8);        // a widening group of each CTA
+            mbar_init(s_full + i, 1);
+            mbar_init(done + i, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(accf + b, 1);
+            mbar_init(acc_empty + b, 8);    // one arrival from each epilogue warp of both CTAs
+            mbar_init(cp_done + b, 1);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&p.tm_w);
+        tma_prefetch_desc(&p.tm_t);
+        tma_prefetch_desc(&p.tm_tsf);
+    }
+    if (warp == 12) {
+        tmem_alloc_pair(tmem_slot, Cfg::TMEM_COLS);
+        tmem_relinquish_pair();
+    }
+    // both CTAs' barriers exist before any arrival from the other CTA
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem_sf = tmem + 2 * NT;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int tiles = __ldcg(p.tile0 + p.E);
+    const int K = FIRST ? p.H : p.I;
+    const int kc = K >> 7;                                  // stages of a tile
+    const int kp = (kc + 1) >> 1;                           // packed stages; the last one may be half
+    const int wrows = FIRST ? 2 * p.I : p.H;                // weight rows of an expert
+    const int mw = FIRST ? p.I >> 7 : (p.H + 255) >> 8;     // weight tiles of an expert
+    UnitWalk<8> walk(p, tiles, mw, blockIdx.x >> 1, gridDim.x >> 1);
+
+    if (warp < 4) {
+        // ------------------------------------------------------------ epilogue
+        const uint32_t acc_empty_r0 = mapa_shared(smem_u32(acc_empty), 0);
+        int ul = 0;
+        for (; walk.more(); ++ul) {
+            Unit w = walk.take();
+            const int buf = ul & 1;
+            if (threadIdx.x == 0) {
+                const bool ok = mbar_wait(accf + buf, (ul >> 1) & 1, &g_moe_error, kErrWaitAccum, p.wait_ns);
+                if (!ok) *abort_flag = 1;
+                epi_go[buf] = ok && !*abort_flag;
+            }
+            epilogue_sync();
+            if (!epi_go[buf]) break;
+            tc_fence_after();
+            // this CTA's half of the tile, in units of 64 channels or 128 rows
+            w.m = 2 * w.m + rank;
+            const bool live = FIRST || 128 * w.m < p.H;
+            const uint32_t trow = tmem + buf * NT + (static_cast<uint32_t>(warp * 32) << 16);
+            for (int c0 = 0; c0 < w.rows; c0 += 32) {
+                uint32_t v[32];
+                tmem_ld32(trow + c0, v);
+                tmem_ld_wait();
+                if (c0 + 32 >= w.rows) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty_r0 + buf * 8);
+                }
+                if (live) store_columns<FIRST>(v, epi, w, c0, 2, p);
+            }
+        }
+    } else if (warp < 12) {
+        // -------------------------------------------------- widening of weights
+        // Lane l takes row l % 8 of a group of eight and 16-byte column l / 8 of a half:
+        // both swizzles then spread eight lanes over all banks.
+        const int group = (warp - 4) >> 2, w4 = (warp - 4) & 3;
+        const int row8 = lane & 7, j = lane >> 3;
+        const uint32_t ready_r0 = mapa_shared(smem_u32(ready), 0);
+        const int s0 = ((2 * j) ^ row8) << 4, s1 = ((2 * j + 1) ^ row8) << 4;
+        const int n = walk.left();
+        int pk = 0;
+        bool ok = true;
+        for (int ul = 0; ul < n && ok; ++ul)
+            for (int kq = 0; kq < kp && ok; ++kq, ++pk) {
+                if ((pk & 1) != group) continue;
+                const Ring rp = ring_at<PACKED>(pk);
+                ok = mbar_wait_warp(p_full + rp.slot, rp.parity, &g_moe_error, kErrWaitFull, p.wait_ns);
+                if (!ok) break;
+                const uint8_t *src = smem + rp.slot * Cfg::PACKED_BYTES + w4 * 4096 + row8 * 128;
+                const uint8_t *psf = smem + rp.slot * Cfg::PACKED_BYTES + Cfg::PSF_OFF + lane * 16;
+                const int halves = min(2, kc - 2 * kq);
+                for (int h = 0; h < halves; ++h) {
+                    const int gs = ul * kc + 2 * kq + h;
+                    const Ring ro = ring_at<OPER>(gs);
+                    uint4 v[4], sf = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        v[i] = *reinterpret_cast<const uint4 *>(src + i * 1024 + (((h * 4 + j) ^ row8) << 4));
+                    if (w4 == 0) {
+                        if constexpr (FIRST) {
+                            // the half of the 128-row blocks of G and U that holds this CTA's channels
+                            const uint2 g = *reinterpret_cast<const uint2 *>(psf + h * 512 + rank * 8);
+                            const uint2 u = *reinterpret_cast<const uint2 *>(psf + 1024 + h * 512 + rank * 8);
+                            sf = make_uint4(g.x, g.y, u.x, u.y);
+                        } else {
+                            sf = *reinterpret_cast<const uint4 *>(psf + h * 512);
+                        }
+                    }
+                    if (h + 1 == halves) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(p_empty + rp.slot);
+                    }
+                    if (gs >= OPER)
+                        ok = mbar_wait_warp(done + ro.slot, ro.parity ^ 1u, &g_moe_error, kErrWaitEmpty, p.wait_ns);
+                    if (!ok) break;
+                    uint8_t *wide = smem + Cfg::WIDE_AT + ro.slot * Cfg::WIDE_BYTES;
+                    uint8_t *dst = wide + w4 * 4096 + row8 * 128;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        *reinterpret_cast<uint2 *>(dst + i * 1024 + s0) = make_uint2(v[i].x, v[i].y);
+                        *reinterpret_cast<uint2 *>(dst + i * 1024 + s1) = make_uint2(v[i].z, v[i].w);
+                    }
+                    if (w4 == 0) *reinterpret_cast<uint4 *>(wide + Cfg::WSF_OFF + lane * 16) = sf;
+                    ok = mbar_wait_warp(t_full + ro.slot, ro.parity, &g_moe_error, kErrWaitFull, p.wait_ns);
+                    if (!ok) break;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(ready_r0 + ro.slot * 8);
+                }
+            }
+        if (!ok) *abort_flag = 1;
+    } else if (warp == 12) {
+        if (leader && lane == 0) {
+            // ------------------------------------------------------- MMA issuer
+            int gs = 0, ul = 0, commits[2] = {0, 0};
+            for (; walk.more(); ++ul) {
+                const Unit w = walk.take();
+                const int buf = ul & 1;
+                if (ul >= 2 && !mbar_wait(acc_empty + buf, ((ul >> 1) - 1) & 1, &g_moe_error, kErrWaitAccum, p.wait_ns)) {
+                    *abort_flag = 1;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t idesc = idesc_w4a8((w.rows + 31) & ~31, 256);
+                const uint32_t d = tmem + buf * NT;
+                bool ok = true;
+                for (int ks = 0; ks < kc; ++ks, ++gs) {
+                    const Ring r = ring_at<OPER>(gs);
+                    // s_full stands for the operands too
+                    if (!mbar_wait(s_full + r.slot, r.parity, &g_moe_error, kErrWaitOperand, p.wait_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t ad = sdesc_sw128(smem_u32(smem + Cfg::WIDE_AT) + r.slot * Cfg::WIDE_BYTES);
+                    const uint64_t bd = sdesc_sw128(smem_u32(smem + Cfg::TOKEN_AT) + r.slot * Cfg::TOKEN_BYTES);
+                    const uint32_t tsf = tmem_sf + r.slot * Cfg::SF_COLS;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_mxf8f6f4_pair(d, ad + 2 * kk, bd + 2 * kk, idesc_with_sf_ids(idesc, kk, kk), tsf, tsf + 4,
+                                          (ks > 0 || kk > 0) ? 1u : 0u);
+                    tc_commit_pair_mc(done + r.slot, 0x3);
+                }
+                tc_commit_pair_mc(accf + buf, 0x3);
+                ++commits[buf];
+                if (!ok) {
+                    *abort_flag = 1;
+                    break;
+                }
+            }
+            // no MMA may be running when the pair frees TMEM
+            for (int b = 0; b < 2; ++b)
+                if (commits[b] > 0) mbar_wait(accf + b, (commits[b] - 1) & 1, &g_moe_error, kErrWaitDrain);
+        }
+    } else if (warp == 13) {
+        if (lane == 0) {
+            // --------------------------------------------- packed weights by TMA
+            const uint64_t pol = policy_evict_last();
+            int pk = 0;
+            bool ok = true;
+            while (walk.more() && ok && !*abort_flag) {
+                const Unit w = walk.take();
+                // the two halves of this CTA's rows: G and U of 64 channels, or 128 rows in a
+                // row (past the expert's last they are not stored)
+                const int r0 = w.e * wrows + (FIRST ? w.m * 128 + rank * 64 : w.m * 256 + rank * 128);
+                const int r1 = r0 + (FIRST ? p.I : 64);
+                const size_t blk = static_cast<size_t>(wrows >> 7) * w.e +
+                                   (FIRST ? w.m : min(2 * w.m + rank, (p.H >> 7) - 1));
+                const uint8_t *sf0 = p.w_sf + blk * kc * 512;
+                const uint8_t *sf1 = sf0 + static_cast<size_t>(p.I >> 7) * kc * 512;
+                for (int kq = 0; kq < kp; ++kq, ++pk) {
+                    const Ring r = ring_at<PACKED>(pk);
+                    if (pk >= PACKED &&
+                        !(ok = mbar_wait(p_empty + r.slot, r.parity ^ 1u, &g_moe_error, kErrWaitEmpty, p.wait_ns))) {
+                        *abort_flag = 1;
+                        break;
+                    }
+                    uint8_t *st = smem + r.slot * Cfg::PACKED_BYTES;
+                    const uint32_t nsf = min(2, kc - 2 * kq) * 512;
+                    mbar_arrive_expect_tx(p_full + r.slot, Cfg::PSF_OFF + (FIRST ? 2 : 1) * nsf);
+                    tma_load_2d(st, &p.tm_w, kq * 128, r0, p_full + r.slot, pol);
+                    tma_load_2d(st + 8192, &p.tm_w, kq * 128, r1, p_full + r.slot, pol);
+                    bulk_load(st + Cfg::PSF_OFF, sf0 + kq * 1024, nsf, p_full + r.slot, pol);
+                    if (FIRST) bulk_load(st + Cfg::PSF_OFF + 1024, sf1 + kq * 1024, nsf, p_full + r.slot, pol);
+                }
+            }
+            // copies in flight land before the block leaves
+            for (int i = max(0, pk - PACKED); i < pk; ++i) {
+                const Ring r = ring_at<PACKED>(i);
+                mbar_wait(p_full + r.slot, r.parity, &g_moe_error, kErrWaitDrain);
+            }
+        }
+    } else if (warp == 14) {
+        if (lane == 0) {
+            // ----------------------------------------------------- tokens by TMA
+            const uint64_t pol = policy_evict_last();
+            int gs = 0;
+            bool ok = true;
+            while (walk.more() && ok && !*abort_flag) {
+                const Unit w = walk.take();
+                // rank 0 holds the first half of the MMA's columns, rank 1 the second
+                const int row = w.row0 + rank * (((w.rows + 31) & ~31) >> 1);
+                for (int ks = 0; ks < kc; ++ks, ++gs) {
+                    const Ring r = ring_at<OPER>(gs);
+                    if (gs >= OPER &&
+                        !(ok = mbar_wait(done + r.slot, r.parity ^ 1u, &g_moe_error, kErrWaitEmpty, p.wait_ns))) {
+                        *abort_flag = 1;
+                        break;
+                    }
+                    uint8_t *st = smem + Cfg::TOKEN_AT + r.slot * Cfg::TOKEN_BYTES;
+                    mbar_arrive_expect_tx(t_full + r.slot, Cfg::HALF * 128 + 1024);
+                    tma_load_2d(st, &p.tm_t, ks * 128, row, t_full + r.slot, pol);
+                    tma_load_2d(st + Cfg::TSF_OFF, &p.tm_tsf, 0, (w.tile * kc + ks) * 2, t_full + r.slot, pol);
+                }
+            }
+            for (int i = max(0, gs - OPER); i < gs; ++i) {
+                const Ring r = ring_at<OPER>(i);
+                mbar_wait(t_full + r.slot, r.parity, &g_moe_error, kErrWaitDrain);
+            }
+        }
+    } else if (leader && lane == 0) {
+        // ------------------------------------------------------ scales to TMEM
+        const int me = warp - 15, total = walk.left() * kc;
+        bool ok = true;
+        for (int gs = me; gs < total && !*abort_flag; gs += 2) {
+            const Ring r = ring_at<OPER>(gs);
+            ok = mbar_wait<true>(ready + r.slot, r.parity, &g_moe_error, kErrWaitFull, p.wait_ns);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t ws = smem_u32(smem + Cfg::WIDE_AT) + r.slot * Cfg::WIDE_BYTES + Cfg::WSF_OFF;
+            const uint32_t ts = smem_u32(smem + Cfg::TOKEN_AT) + r.slot * Cfg::TOKEN_BYTES + Cfg::TSF_OFF;
+            const uint32_t tsf = tmem_sf + r.slot * Cfg::SF_COLS;
+            tc_cp_scale_block_pair(tsf, sdesc_scale(ws));
+            tc_cp_scale_block_pair(tsf + 4, sdesc_scale(ts));
+            tc_cp_scale_block_pair(tsf + 8, sdesc_scale(ts + 512));
+            tc_commit_pair(s_full + r.slot);
+        }
+        if (!ok) *abort_flag = 1;
+        // no copy may be running when the pair frees TMEM
+        tc_commit_pair(cp_done + me);
+        mbar_wait(cp_done + me, 0, &g_moe_error, kErrWaitDrain);
+    }
+    __syncwarp();
+
+    // neither CTA leaves while the other may still arrive on its barriers or use
+    // its shared memory and TMEM
+    tc_fence_before();
+    cluster_sync();
+    if (warp == 12) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, Cfg::TMEM_COLS);
+    }
+}
+
+// Token rows and their scales in sorted order, for the large tiles' TMA: block row
+// blockIdx.x is a token tile, its rows shared out over warps and blockIdx.y.
+struct GatherParams {
+    const uint8_t *x, *x_sf;
+    int64_t ldx;
+    const int *tile0, *src;
+    const int4 *rec;
+    uint8_t *xs;        // [R, H]
+    uint8_t *xs_sf;     // [tiles][H / 128][2][512]
+    int E, H;
+};
+
+__global__ void __launch_bounds__(256) moe_gather_kernel(const GatherParams p)
+{
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int tile = blockIdx.x;
+    if (tile >= __ldcg(p.tile0 + p.E)) return;
+    const int4 rec = __ldcg(p.rec + tile);
+    const int lane = threadIdx.x & 31, kc = p.H >> 7;
+    for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < rec.z; r += gridDim.y * 8) {
+        const int t = __ldcg(p.src + rec.y + r);
+        const uint4 *from = reinterpret_cast<const uint4 *>(p.x + static_cast<size_t>(t) * p.ldx);
+        uint4 *to = reinterpret_cast<uint4 *>(p.xs + static_cast<size_t>(rec.y + r) * p.H);
+        for (int i = lane; i < p.H / 16; i += 32) to[i] = from[i];
+        const uint8_t *sf = p.x_sf + static_cast<size_t>(t >> 7) * kc * 512 + (t & 31) * 16 + ((t & 127) >> 5) * 4;
+        uint8_t *sfo = p.xs_sf + static_cast<size_t>(tile) * kc * 1024 + (r >> 7) * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4;
+        for (int c = lane; c < kc; c += 32)
+            *reinterpret_cast<uint32_t *>(sfo + c * 1024) = *reinterpret_cast<const uint32_t *>(sf + c * 512);
     }
 }
 
@@ -1104,19 +1136,6 @@ cudaError_t launch_pdl(Kern kern, dim3 grid, dim3 block, size_t smem, cudaStream
     return cudaLaunchKernelEx(&cfg, kern, params);
 }
 
-template <bool FIRST, int NT, int STAGES>
-cudaError_t launch_product(const ProductParams &p, int64_t max_units, cudaStream_t stream)
-{
-    using Cfg = ProductCfg<NT, STAGES>;
-    auto kern = moe_product_kernel<FIRST, NT, STAGES>;
-    static KernelOnce once;
-    int sms = 0;
-    const cudaError_t e = prepare_kernel(kern, Cfg::SMEM_BYTES, once, &sms);
-    if (e != cudaSuccess) return e;
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(max_units, std::max(1, sms)));
-    return launch_pdl(kern, dim3(grid), dim3(256), Cfg::SMEM_BYTES, stream, p);
-}
-
 template <bool FIRST>
 cudaError_t launch_product_small(const ProductParams &p, int64_t max_units, cudaStream_t stream)
 {
@@ -1130,10 +1149,30 @@ cudaError_t launch_product_small(const ProductParams &p, int64_t max_units, cuda
 }
 
 template <bool FIRST>
-cudaError_t launch_product_nt(int nt, const ProductParams &p, int64_t max_units, cudaStream_t stream)
+cudaError_t launch_product_large(const ProductParams &p, int64_t max_units, cudaStream_t stream)
 {
-    return nt == kSmallNT ? launch_product_small<FIRST>(p, max_units, stream)
-                          : launch_product<FIRST, 224, 4>(p, max_units, stream);
+    auto kern = moe_product_large_kernel<FIRST>;
+    static KernelOnce once;
+    int sms = 0;
+    const cudaError_t e = prepare_kernel(kern, LargeCfg::SMEM_BYTES, once, &sms);
+    if (e != cudaSuccess) return e;
+    const unsigned pairs = static_cast<unsigned>(std::min<int64_t>(max_units, std::max(1, sms / 2)));
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(2 * pairs, 1, 1);
+    cfg.blockDim = dim3(kLargeThreads, 1, 1);
+    cfg.dynamicSmemBytes = LargeCfg::SMEM_BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 inline size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -1145,7 +1184,7 @@ bool moe_layout(int64_t T, int k, int E, int64_t H, int64_t I, MoeLayout *out)
     const int64_t R = T * k;
     // a tile of 32 tokens leaves room for nine stages of weights in flight, one of
     // 224 halves the reads of the weights again and again for long batches
-    out->nt = R <= 32 * static_cast<int64_t>(E) ? 32 : 224;
+    out->nt = R <= 32 * static_cast<int64_t>(E) ? kSmallNT : kLargeNT;
     out->max_tiles = static_cast<int>(R / out->nt + std::min<int64_t>(E, R));
     out->chunks = static_cast<int>((R + kChunk - 1) / kChunk);
     size_t at = 0;
@@ -1163,6 +1202,8 @@ bool moe_layout(int64_t T, int k, int E, int64_t H, int64_t I, MoeLayout *out)
     out->act = take(static_cast<size_t>(R) * I);
     out->act_sf = take(static_cast<size_t>(out->max_tiles) * (I / 128) * ((out->nt + 127) / 128) * 512);
     out->y = take(static_cast<size_t>(R) * H * 2);
+    out->xs = take(out->nt == kLargeNT ? static_cast<size_t>(R) * H : 0);
+    out->xs_sf = take(out->nt == kLargeNT ? static_cast<size_t>(out->max_tiles) * (H / 128) * 1024 : 0);
     out->total = at;
     return true;
 }
@@ -1190,13 +1231,31 @@ cudaError_t launch_moe_experts(const MoeArgs &a, const MoeLayout &l, cudaStream_
     e = launch_pdl(moe_place_kernel, dim3(l.chunks), dim3(kPlaceThreads), 0, stream, pp);
     if (e != cudaSuccess) return e;
 
+    const bool large = l.nt == kLargeNT;
+    if (large) {
+        GatherParams g;
+        g.x = a.xq;
+        g.x_sf = a.x_sf;
+        g.ldx = a.ldx;
+        g.tile0 = pp.tile0;
+        g.src = pp.src;
+        g.rec = pp.rec;
+        g.xs = a.ws + l.xs;
+        g.xs_sf = a.ws + l.xs_sf;
+        g.E = a.E;
+        g.H = a.H;
+        e = launch_pdl(moe_gather_kernel, dim3(l.max_tiles, 4), dim3(256), 0, stream, g);
+        if (e != cudaSuccess) return e;
+    }
+
     ProductParams p;
     memset(&p, 0, sizeof(p));
+    p.x = a.xq;
+    p.ldx = a.ldx;
     p.x_sf = a.x_sf;
     p.act = a.ws + l.act;
     p.act_sf = a.ws + l.act_sf;
     p.y = reinterpret_cast<uint16_t *>(a.ws + l.y);
-    p.off = pp.off;
     p.tile0 = pp.tile0;
     p.src = pp.src;
     p.rec = pp.rec;
@@ -1204,17 +1263,25 @@ cudaError_t launch_moe_experts(const MoeArgs &a, const MoeLayout &l, cudaStream_
     p.H = a.H;
     p.I = a.I;
     p.wait_ns = wait_limit_ns();
-    p.x = a.xq;
-    p.ldx = a.ldx;
-    p.tm_w = l.nt == kSmallNT ? a.tm_pw13 : a.tm_w13;
-    p.tm_t = a.tm_x;
+    p.tm_w = a.tm_w13;
     p.w_sf = a.w13_sf;
-    e = launch_product_nt<true>(l.nt, p, static_cast<int64_t>(l.max_tiles) * (a.I / 64), stream);
+    if (large) {
+        p.tm_t = a.tm_xs;
+        p.tm_tsf = a.tm_xs_sf;
+        e = launch_product_large<true>(p, static_cast<int64_t>(l.max_tiles) * (a.I / 128), stream);
+    } else {
+        e = launch_product_small<true>(p, static_cast<int64_t>(l.max_tiles) * (a.I / 64), stream);
+    }
     if (e != cudaSuccess) return e;
-    p.tm_w = l.nt == kSmallNT ? a.tm_pw2 : a.tm_w2;
-    p.tm_t = a.tm_act;
+    p.tm_w = a.tm_w2;
     p.w_sf = a.w2_sf;
-    e = launch_product_nt<false>(l.nt, p, static_cast<int64_t>(l.max_tiles) * (a.H / 128), stream);
+    if (large) {
+        p.tm_t = a.tm_act;
+        p.tm_tsf = a.tm_act_sf;
+        e = launch_product_large<false>(p, static_cast<int64_t>(l.max_tiles) * ((a.H + 255) / 256), stream);
+    } else {
+        e = launch_product_small<false>(p, static_cast<int64_t>(l.max_tiles) * (a.H / 128), stream);
+    }
     if (e != cudaSuccess) return e;
 
     CombineParams c;
