@@ -901,7 +901,10 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_product_large_kernel(con
                     if (!ok) break;
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(ready_r0 + ro.slot * 8);
+                    if (lane == 0) {
+                        fence_release_own_smem_cluster();
+                        mbar_arrive_cluster_relaxed(ready_r0 + ro.slot * 8);
+                    }
                 }
             }
         if (!ok) *abort_flag = 1;

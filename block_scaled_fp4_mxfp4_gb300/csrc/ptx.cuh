@@ -188,6 +188,15 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_add
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// Release at cluster scope of this thread's earlier writes (and those ordered
+// before them) to its CTA's own shared memory only. With a relaxed arrive after
+// it, it publishes them as mbar_arrive_cluster does; that one also waits for the
+// thread's global accesses, over a thousand clocks in a kernel that streams.
+__device__ __forceinline__ void fence_release_own_smem_cluster()
+{
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+}
+
 // --------------------------------------------------------------------- TMA
 
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap *tm)
