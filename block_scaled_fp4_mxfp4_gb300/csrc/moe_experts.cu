@@ -769,7 +769,7 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_product_large_kernel(con
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     volatile int *epi_go = abort_flag + 1;   // [2]
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_ctarank());
     const bool leader = rank == 0;
     if (threadIdx.x == 0) {
@@ -812,6 +812,10 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_product_large_kernel(con
     const int kp = (kc + 1) >> 1;                           // packed stages; the last one may be half
     const int wrows = FIRST ? 2 * p.I : p.H;                // weight rows of an expert
     const int mw = FIRST ? p.I >> 7 : (p.H + 255) >> 8;     // weight tiles of an expert
+    // uniform across the warp, for the MMA issuer
+    const uint32_t tmem_u = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t wide_desc = sdesc_sw128(smem_u32(smem + Cfg::WIDE_AT));
+    const uint64_t token_desc = sdesc_sw128(smem_u32(smem + Cfg::TOKEN_AT));
     UnitWalk<8> walk(p, tiles, mw, blockIdx.x >> 1, gridDim.x >> 1);
 
     if (warp < 4) {
@@ -909,47 +913,47 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_product_large_kernel(con
             }
         if (!ok) *abort_flag = 1;
     } else if (warp == 12) {
-        if (leader && lane == 0) {
+        if (leader) {
             // ------------------------------------------------------- MMA issuer
+            // The whole warp walks the stages and one elected lane issues, so that
+            // descriptors stay in uniform registers.
             int gs = 0, ul = 0, commits[2] = {0, 0};
-            for (; walk.more(); ++ul) {
+            bool ok = true;
+            for (; walk.more() && ok; ++ul) {
                 const Unit w = walk.take();
                 const int buf = ul & 1;
-                if (ul >= 2 && !mbar_wait(acc_empty + buf, ((ul >> 1) - 1) & 1, &g_moe_error, kErrWaitAccum, p.wait_ns)) {
-                    *abort_flag = 1;
-                    break;
-                }
+                if (ul >= 2)
+                    ok = mbar_wait_warp(acc_empty + buf, ((ul >> 1) - 1) & 1, &g_moe_error, kErrWaitAccum, p.wait_ns);
+                if (!ok) break;
                 tc_fence_after();
-                const uint32_t idesc = idesc_w4a8((w.rows + 31) & ~31, 256);
-                const uint32_t d = tmem + buf * NT;
-                bool ok = true;
+                const uint32_t idesc = __shfl_sync(0xffffffffu, idesc_w4a8((w.rows + 31) & ~31, 256), 0);
+                const uint32_t d = tmem_u + buf * NT;
                 for (int ks = 0; ks < kc; ++ks, ++gs) {
                     const Ring r = ring_at<OPER>(gs);
                     // s_full stands for the operands too
-                    if (!mbar_wait(s_full + r.slot, r.parity, &g_moe_error, kErrWaitOperand, p.wait_ns)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = mbar_wait_warp(s_full + r.slot, r.parity, &g_moe_error, kErrWaitOperand, p.wait_ns);
+                    if (!ok) break;
                     tc_fence_after();
-                    const uint64_t ad = sdesc_sw128(smem_u32(smem + Cfg::WIDE_AT) + r.slot * Cfg::WIDE_BYTES);
-                    const uint64_t bd = sdesc_sw128(smem_u32(smem + Cfg::TOKEN_AT) + r.slot * Cfg::TOKEN_BYTES);
-                    const uint32_t tsf = tmem_sf + r.slot * Cfg::SF_COLS;
+                    const uint64_t ad = wide_desc + static_cast<uint64_t>(r.slot * (Cfg::WIDE_BYTES >> 4));
+                    const uint64_t bd = token_desc + static_cast<uint64_t>(r.slot * (Cfg::TOKEN_BYTES >> 4));
+                    const uint32_t tsf = tmem_u + 2 * NT + r.slot * Cfg::SF_COLS;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_mxf8f6f4_pair(d, ad + 2 * kk, bd + 2 * kk, idesc_with_sf_ids(idesc, kk, kk), tsf, tsf + 4,
-                                          (ks > 0 || kk > 0) ? 1u : 0u);
-                    tc_commit_pair_mc(done + r.slot, 0x3);
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_mxf8f6f4_pair(d, ad + 2 * kk, bd + 2 * kk, idesc_with_sf_ids(idesc, kk, kk), tsf, tsf + 4,
+                                              (ks > 0 || kk > 0) ? 1u : 0u);
+                        tc_commit_pair_mc(done + r.slot, 0x3);
+                    }
+                    __syncwarp();
                 }
-                tc_commit_pair_mc(accf + buf, 0x3);
+                if (elect_one()) tc_commit_pair_mc(accf + buf, 0x3);
+                __syncwarp();
                 ++commits[buf];
-                if (!ok) {
-                    *abort_flag = 1;
-                    break;
-                }
             }
+            if (!ok) *abort_flag = 1;
             // no MMA may be running when the pair frees TMEM
             for (int b = 0; b < 2; ++b)
-                if (commits[b] > 0) mbar_wait(accf + b, (commits[b] - 1) & 1, &g_moe_error, kErrWaitDrain);
+                if (commits[b] > 0) mbar_wait_warp(accf + b, (commits[b] - 1) & 1, &g_moe_error, kErrWaitDrain);
         }
     } else if (warp == 13) {
         if (lane == 0) {
