@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     volatile int *epi_go = abort_flag + 1;   // [2]
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < PACKED; ++i) {
             mbar_init(p_full + i, 1);
@@ -427,6 +427,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
     const int stages = (kc + 1) >> 1;                       // the last one may be half
     const int mw = FIRST ? p.I >> 6 : p.H >> 7;             // weight tiles of an expert
     const int wrows = FIRST ? 2 * p.I : p.H;                // weight rows of an expert
+    // uniform across the warp, for the MMA issuers
+    const uint32_t tmem_u = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t wide_desc = sdesc_sw128(smem_u32(smem + Cfg::WIDE_AT));
+    const uint64_t token_desc = sdesc_sw128(smem_u32(smem + Cfg::TOKEN_AT));
     UnitWalk<0> walk(p, tiles, mw, blockIdx.x, gridDim.x);
 
     if (warp < 4) {
@@ -571,31 +575,30 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
         }
         if (!ok) *abort_flag = 1;
     } else if (warp < 18) {
-        if (lane == 0) {
-            // ------------------------------------------------------ MMA issuers
-            const int me = warp - 16;
-            int gs = 0, ul = 0, commits[2] = {0, 0};
-            for (; walk.more(); ++ul) {
-                const Unit w = walk.take();
-                const int buf = ul & 1;
-                if (ul >= 2 && !mbar_wait(acc_empty + buf, ((ul >> 1) - 1) & 1, &g_moe_error, kErrWaitAccum, p.wait_ns)) {
-                    *abort_flag = 1;
-                    break;
-                }
+        // ---------------------------------------------------------- MMA issuers
+        // Whole warps walk the stages and one elected lane issues, so that descriptors
+        // stay in uniform registers.
+        const int me = warp - 16;
+        int gs = 0, ul = 0, commits[2] = {0, 0};
+        bool ok = true;
+        for (; walk.more() && ok; ++ul) {
+            const Unit w = walk.take();
+            const int buf = ul & 1;
+            if (ul >= 2)
+                ok = mbar_wait_warp(acc_empty + buf, ((ul >> 1) - 1) & 1, &g_moe_error, kErrWaitAccum, p.wait_ns);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t idesc = __shfl_sync(0xffffffffu, idesc_w4a8((w.rows + 15) & ~15), 0);
+            const uint32_t d = tmem_u + (buf * 2 + me) * NT;
+            for (int ks = me; ks < stages; ks += 2) {
+                const Ring r = ring_at<TOKEN>(gs + ks);
+                ok = mbar_wait_warp(ready + r.slot, r.parity, &g_moe_error, kErrWaitOperand, p.wait_ns);
+                if (!ok) break;
                 tc_fence_after();
-                const uint32_t idesc = idesc_w4a8((w.rows + 15) & ~15);
-                const uint32_t d = tmem + (buf * 2 + me) * NT;
-                bool ok = true;
-                for (int ks = me; ks < stages; ks += 2) {
-                    const Ring r = ring_at<TOKEN>(gs + ks);
-                    if (!mbar_wait(ready + r.slot, r.parity, &g_moe_error, kErrWaitOperand, p.wait_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t tsf = tmem_sf + r.slot * Cfg::SF_COLS;
-                    const uint64_t ad = sdesc_sw128(smem_u32(smem + Cfg::WIDE_AT) + ((gs + ks) % WIDE) * Cfg::WIDE_BYTES);
-                    const uint64_t bd = sdesc_sw128(smem_u32(smem + Cfg::TOKEN_AT) + r.slot * Cfg::TOKEN_BYTES);
+                const uint32_t tsf = tmem_u + Cfg::ACC_COLS + r.slot * Cfg::SF_COLS;
+                const uint64_t ad = wide_desc + static_cast<uint64_t>((gs + ks) % WIDE * (Cfg::WIDE_BYTES >> 4));
+                const uint64_t bd = token_desc + static_cast<uint64_t>(r.slot * (Cfg::TOKEN_BYTES >> 4));
+                if (elect_one()) {
                     auto half = [&](int h, uint32_t accumulate) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
@@ -607,18 +610,17 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
                     if (2 * ks + 1 < kc) half(1, 1u);
                     tc_commit(done + r.slot);
                 }
-                gs += stages;
-                tc_commit(accf + buf);
-                ++commits[buf];
-                if (!ok) {
-                    *abort_flag = 1;
-                    break;
-                }
+                __syncwarp();
             }
-            // no MMA may be running when TMEM is released
-            for (int b = 0; b < 2; ++b)
-                if (commits[b] > 0) mbar_wait(accf + b, (commits[b] - 1) & 1, &g_moe_error, kErrWaitDrain);
+            gs += stages;
+            if (elect_one()) tc_commit(accf + buf);
+            __syncwarp();
+            ++commits[buf];
         }
+        if (!ok) *abort_flag = 1;
+        // no MMA may be running when TMEM is released
+        for (int b = 0; b < 2; ++b)
+            if (commits[b] > 0) mbar_wait_warp(accf + b, (commits[b] - 1) & 1, &g_moe_error, kErrWaitDrain);
     } else if (warp == 18) {
         if (lane == 0) {
             // --------------------------------------------- packed weights by TMA
