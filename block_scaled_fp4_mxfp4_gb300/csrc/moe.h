@@ -23,6 +23,8 @@ struct RouteParams {
     int E, k, groups, topk_groups, group_top;
     int sigmoid, renorm;
     float scale;
+    int group_lanes;        // set at launch: lanes a group fills, 0 where groups are no runs of lanes
+    int vec;                // set at launch: rows allow 16-byte vectors
 };
 cudaError_t launch_moe_route(const RouteParams &p, int dtype, int num_sms, cudaStream_t stream);
 

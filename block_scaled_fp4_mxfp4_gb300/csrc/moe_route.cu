@@ -1,9 +1,11 @@
 // Routing of tokens to experts (moe_route): scores, groups, top k, weights.
 //
-// One warp a token; lane l holds experts l, l + 32, ... in registers. What a
+// One warp a token; lane l holds the V experts from V l on in registers. What a
 // token costs is not its E logits (a few hundred bytes) but the selection: k
-// rounds of a warp-wide maximum over order-preserving integer keys
-// (redux.sync), each giving the lowest index among equals.
+// rounds of a warp-wide maximum (redux.sync) over order-preserving integer keys, of
+// which the lowest lane that has it, and there the first expert, is the one of
+// lowest index. A group of experts is a run of lanes where its size allows (a
+// power of two of them); its score then takes a few shuffles, all groups at once.
 //
 // Exactness. With a bias or groups the choice compares sums s + bias that fp32
 // holds to about 2^-22 only, and two experts of a large batch come closer than
@@ -12,8 +14,9 @@
 // sum 1 + e or the division 1 each, c itself 1, so 2^-21 for the sigmoid; the
 // softmax adds 1 for x - max and up to V + 7 for the sum of the row, so 2^-19.
 // Rows with a closer decision (under one in a hundred) are decided again from
-// 64-bit scores. Without bias and groups the logits themselves are compared,
-// which is exact.
+// 64-bit scores: of the candidates that fp32 leaves, or of all experts where the
+// choice of groups is open. Without bias and groups the logits themselves are
+// compared, which is exact.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -90,35 +93,42 @@ __device__ __forceinline__ void warp_best64(double &v, int &i)
 }
 
 // A row decided in 64 bits: the ids of its k experts in lane order (lane j < k
-// holds the j-th; -1 where nothing is left). `c` is the warp's [E] doubles of
-// shared memory.
-__device__ __noinline__ int route_row64(const RouteParams &p, int dtype, int64_t t, double *c)
+// holds the j-th; -1 where nothing is left). `c` is the warp's shared memory, [E]
+// doubles and two a group. chosen: groups are decided, and c holds fp32 values of
+// which those below `least` are out of the question.
+__device__ __noinline__ int route_row64(const RouteParams &p, int dtype, int64_t t, double *c, bool chosen, double least)
 {
     const int lane = threadIdx.x & 31;
     const double kNegInf = -__longlong_as_double(0x7FF0000000000000ll);
     double m = kNegInf;
-    for (int e = lane; e < p.E; e += 32) {
-        const double z = load_logit(p.logits, t * p.ldl + e, dtype);
-        c[e] = z;
-        m = z > m || z != z ? z : m;
-    }
     double s = 0.0;
     if (!p.sigmoid) {
+        for (int e = lane; e < p.E; e += 32) {
+            const double z = load_logit(p.logits, t * p.ldl + e, dtype);
+            m = z > m || z != z ? z : m;
+        }
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
             const double om = __shfl_xor_sync(kAll, m, o);
             m = om > m || om != om ? om : m;
         }
-        for (int e = lane; e < p.E; e += 32) s += c[e] == kNegInf ? 0.0 : exp(c[e] - m);
+        for (int e = lane; e < p.E; e += 32) {
+            const double z = load_logit(p.logits, t * p.ldl + e, dtype);
+            s += z == kNegInf ? 0.0 : exp(z - m);
+        }
         s = warp_sum(s);
     }
     for (int e = lane; e < p.E; e += 32) {
-        const double z = c[e];
+        if (chosen && c[e] < least) {
+            c[e] = kNegInf;
+            continue;
+        }
+        const double z = load_logit(p.logits, t * p.ldl + e, dtype);
         const double score = p.sigmoid ? 1.0 / (1.0 + exp(-z)) : exp(z - m) / s;
         c[e] = z == kNegInf ? kNegInf : p.bias ? score + static_cast<double>(p.bias[e]) : score;
     }
     __syncwarp();
-    if (p.groups > 1) {
+    if (p.groups > 1 && !chosen) {
         const int n = p.E / p.groups;
         for (int g = lane; g < p.groups; g += 32) {
             double b1 = kNegInf, b2 = kNegInf;
@@ -176,9 +186,49 @@ __device__ __noinline__ int route_row64(const RouteParams &p, int dtype, int64_t
     return mine;
 }
 
+__device__ __forceinline__ float value_of(uint32_t k)   // inverse of key32
+{
+    return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
+
+// The V logits from element i on (E of them in the row from column e): by 16-byte
+// vectors where `vec` says that rows allow them.
+template <int V, int DTYPE>
+__device__ __forceinline__ void load_row(const RouteParams &p, int64_t t, int e, float (&z)[V])
+{
+    constexpr int W = DTYPE == 2 ? 4 : 8;   // elements of a vector
+    const float kNegInf = -__int_as_float(0x7F800000);
+    const int64_t at = t * p.ldl + e;
+    if (V % W == 0 && p.vec && e + V <= p.E) {
+#pragma unroll
+        for (int i = 0; i < V / W; ++i) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if constexpr (V % W == 0)
+                v = *(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.logits) + at * (16 / W)) + i);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (DTYPE == 2) {
+                    z[W * i + j] = __uint_as_float(w[j]);
+                } else if constexpr (DTYPE == 0) {
+                    z[W * i + 2 * j] = __uint_as_float(w[j] << 16);
+                    z[W * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+                } else {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
+                    z[W * i + 2 * j] = f.x;
+                    z[W * i + 2 * j + 1] = f.y;
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[i] = e + i < p.E ? load_logit(p.logits, at + i, DTYPE) : kNegInf;
+    }
+}
+
 // V: experts a lane, E <= 32 V.
-template <int V>
-__global__ void __launch_bounds__(128) moe_route_kernel(const RouteParams p, int dtype)
+template <int V, int DTYPE>
+__global__ void __launch_bounds__(128) moe_route_kernel(const RouteParams p)
 {
     extern __shared__ double smem_route[];
     grid_dependency_wait();
@@ -186,153 +236,186 @@ __global__ void __launch_bounds__(128) moe_route_kernel(const RouteParams p, int
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarps = blockDim.x >> 5;
     double *c64 = smem_route + static_cast<size_t>(warp) * (p.E + 2 * p.groups);
     const float kNegInf = -__int_as_float(0x7F800000);
+    const int e0 = lane * V, n = p.E / p.groups;
+    float bias[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) bias[i] = p.bias && e0 + i < p.E ? p.bias[e0 + i] : 0.0f;
     for (int64_t t = static_cast<int64_t>(blockIdx.x) * nwarps + warp; t < p.T;
          t += static_cast<int64_t>(gridDim.x) * nwarps) {
         float z[V];
         uint32_t key[V];
-        float zmax = kNegInf;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = lane + 32 * i;
-            z[i] = e < p.E ? load_logit(p.logits, t * p.ldl + e, dtype) : kNegInf;
-            zmax = z[i] != z[i] || z[i] > zmax ? z[i] : zmax;
-        }
-        float sum = 1.0f;
+        load_row<V, DTYPE>(p, t, e0, z);
+        float zmax = 0.0f, sum = 1.0f;
         if (!p.sigmoid) {
-            bool nan = zmax != zmax;
+            zmax = kNegInf;
+            bool nan = false;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                nan |= z[i] != z[i];
+                zmax = fmaxf(zmax, z[i]);
+            }
             zmax = warp_max(zmax);
-            nan = __any_sync(kAll, nan);
             sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < V; ++i) sum += z[i] == kNegInf ? 0.0f : expf(z[i] - zmax);
             sum = warp_sum(sum);
-            if (nan) sum = zmax = __int_as_float(0x7FC00000);
+            if (__any_sync(kAll, nan)) sum = zmax = __int_as_float(0x7FC00000);
         }
         auto score = [&](float x) {
             if (x == kNegInf) return 0.0f;
             return p.sigmoid ? 1.0f / (1.0f + expf(-x)) : expf(x - zmax) / sum;
         };
         const bool by_logit = !p.bias && p.groups == 1 && (p.sigmoid || sum == sum);
-        bool open = false;    // a decision closer than fp32 can tell
+        bool open = false;         // a decision closer than fp32 can tell
+        bool open_groups = false;  // such a one between groups, or a value without order
         float tol = 0.0f;
         if (by_logit) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) key[i] = lane + 32 * i < p.E ? key32(z[i]) : 0u;
+            for (int i = 0; i < V; ++i) key[i] = e0 + i < p.E ? key32(z[i]) : 0u;
         } else {
+            bool odd = false;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const int e = lane + 32 * i;
-                key[i] = 0u;
-                if (e < p.E) {
-                    const float s = score(z[i]);
-                    const float c = z[i] == kNegInf ? kNegInf : p.bias ? s + p.bias[e] : s;
-                    if (c != kNegInf) tol = fmaxf(tol, fmaxf(s, fabsf(c)));
-                    open |= c != c;
-                    key[i] = key32(c);
-                }
+                const float s = score(z[i]);
+                const float c = z[i] == kNegInf ? kNegInf : s + bias[i];
+                odd |= !(c < 1e30f);
+                if (c > kNegInf) tol = fmaxf(tol, fmaxf(s, fabsf(c)));
+                key[i] = e0 + i < p.E ? key32(c) : 0u;
             }
-            tol = warp_max(tol) * (p.sigmoid ? 0x1p-21f : 0x1p-19f);
-            open = __any_sync(kAll, open) || !(tol < 1e30f);
+            // tol >= 0, so its bits order as it does
+            tol = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(tol))) * (p.sigmoid ? 0x1p-21f : 0x1p-19f);
+            open_groups = __any_sync(kAll, odd) || !(tol < 1e20f);
         }
-        auto value_of = [&](uint32_t k) {   // inverse of key32
-            return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
-        };
-        if (p.groups > 1 && !open) {
-            const int n = p.E / p.groups;
-            // scores of the groups, lane g (and g + 32, ...) holding group g's;
-            // at most 512 groups of one expert each
-            uint32_t best[V];
-#pragma unroll
-            for (int i = 0; i < V; ++i) best[i] = 0u;
-            for (int g = 0; g < p.groups; ++g) {
+        if (p.groups > 1 && !open_groups) {
+            // A group's two best keys, in every lane of the group (`run` lanes of it, from
+            // a multiple of run on), or group g's in lane g, g + 32, ...
+            uint32_t kept = 0u;       // groups of this lane that stay: bit 0, or bit i for group lane + 32 i
+            const int run = p.group_lanes;
+            if (run > 0) {
                 uint32_t k1 = 0u, k2 = 0u;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    const int e = lane + 32 * i;
-                    if (e >= g * n && e < (g + 1) * n) {
-                        if (key[i] > k1) {
-                            k2 = k1;
-                            k1 = key[i];
-                        } else if (key[i] > k2) {
-                            k2 = key[i];
+                    k2 = max(k2, min(k1, key[i]));
+                    k1 = max(k1, key[i]);
+                }
+                for (int o = 1; o < run; o <<= 1) {
+                    const uint32_t a1 = __shfl_xor_sync(kAll, k1, o), a2 = __shfl_xor_sync(kAll, k2, o);
+                    k2 = max(max(k2, a2), min(k1, a1));
+                    k1 = max(k1, a1);
+                }
+                const float gs = value_of(k1) + (p.group_top == 2 && n > 1 ? value_of(k2) : 0.0f);
+                const bool real = e0 < p.E;
+                const uint32_t mine = real ? key32(gs) : 0u;
+                int rank = 0;         // groups before this one
+                for (int g = 0; g < p.groups; ++g) {
+                    const uint32_t other = __shfl_sync(kAll, mine, g * run);
+                    rank += other > mine || (other == mine && g * run < (lane & ~(run - 1)));
+                }
+                kept = real && rank < p.topk_groups;
+                // the worst that stays against the best that goes; sums of two carry twice the error
+                const uint32_t low = __reduce_min_sync(kAll, kept ? mine : 0xFFFFFFFFu);
+                const uint32_t high = __reduce_max_sync(kAll, real && !kept ? mine : 0u);
+                if (high > kKeyNegInf && !(value_of(low) - value_of(high) > 4.0f * tol)) open_groups = true;
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (!kept && e0 + i < p.E) key[i] = kKeyNegInf;
+            } else {
+                // groups that are no runs of lanes: one lane a group, through shared memory
+                float *cs = reinterpret_cast<float *>(c64);
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (e0 + i < p.E) cs[e0 + i] = value_of(key[i]);
+                __syncwarp();
+                constexpr int GV = V;      // groups a lane: at most as many as experts
+                uint32_t best[GV];
+#pragma unroll
+                for (int i = 0; i < GV; ++i) {
+                    const int g = lane + 32 * i;
+                    best[i] = 0u;
+                    if (g < p.groups) {
+                        float b1 = kNegInf, b2 = kNegInf;
+                        for (int j = 0; j < n; ++j) {
+                            const float c = cs[g * n + j];
+                            b2 = fmaxf(b2, fminf(b1, c));
+                            b1 = fmaxf(b1, c);
                         }
+                        best[i] = key32(p.group_top == 2 && n > 1 ? b1 + b2 : b1);
                     }
                 }
-                const uint32_t m1 = __reduce_max_sync(kAll, k1);
-                float gs = value_of(m1);
-                if (p.group_top == 2 && n > 1) {
-                    const unsigned has = __ballot_sync(kAll, k1 == m1);
-                    const uint32_t second = lane == __ffs(has) - 1 ? k2 : k1;
-                    gs += value_of(__reduce_max_sync(kAll, second));
-                }
+                __syncwarp();
+                uint32_t low = 0u;
+                for (int r = 0; r <= p.topk_groups && r < p.groups; ++r) {
+                    uint32_t b = 0u;
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (lane + 32 * i == g) best[i] = key32(gs);
-            }
-            // the topk_groups best; a group that is not among them loses its experts
-            float last = 0.0f;
-            bool any_last = false;
-            uint32_t keep_bits = 0u;   // bit i: this lane's group lane + 32 i is kept
-            for (int r = 0; r <= p.topk_groups && r < p.groups; ++r) {
-                uint32_t b = 0u;
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (!(keep_bits >> i & 1)) b = max(b, best[i]);
-                const uint32_t m = __reduce_max_sync(kAll, b);
-                if (r == p.topk_groups) {
-                    // against the best group left out; sums of two carry twice the error
-                    if (any_last && !(last - value_of(m) > 4.0f * tol) && value_of(m) != kNegInf) open = true;
-                    break;
-                }
-                int mine = 1 << 20;
-#pragma unroll
-                for (int i = V - 1; i >= 0; --i)
-                    if (!(keep_bits >> i & 1) && best[i] == m && lane + 32 * i < p.groups) mine = lane + 32 * i;
-                const int g = __reduce_min_sync(kAll, mine);
-                if ((g & 31) == lane) keep_bits |= 1u << (g >> 5);
-                last = value_of(m);
-                any_last = true;
-            }
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int e = lane + 32 * i;
-                const int g = e < p.E ? e / n : 0;
-                const uint32_t bits = __shfl_sync(kAll, keep_bits, g & 31);
-                if (e < p.E && !(bits >> (g >> 5) & 1)) key[i] = kKeyNegInf;
-            }
-        }
-        int id = -1;          // lane j < k: the j-th choice
-        if (!open) {
-            float prev = 0.0f;
-            for (int j = 0; j <= p.k; ++j) {
-                uint32_t b = 0u;
-#pragma unroll
-                for (int i = 0; i < V; ++i) b = max(b, key[i]);
-                const uint32_t m = __reduce_max_sync(kAll, b);
-                if (m <= kKeyNegInf) break;    // nothing is left
-                if (!by_logit) {
-                    const float v = value_of(m);
-                    if (j > 0 && !(prev - v > 2.0f * tol)) {
-                        open = true;
+                    for (int i = 0; i < GV; ++i)
+                        if (!(kept >> i & 1)) b = max(b, best[i]);
+                    const uint32_t m = __reduce_max_sync(kAll, b);
+                    if (r == p.topk_groups) {
+                        if (m > kKeyNegInf && !(value_of(low) - value_of(m) > 4.0f * tol)) open_groups = true;
                         break;
                     }
-                    prev = v;
+                    int first = 1 << 20;
+#pragma unroll
+                    for (int i = GV - 1; i >= 0; --i)
+                        if (!(kept >> i & 1) && best[i] == m && lane + 32 * i < p.groups) first = lane + 32 * i;
+                    const int g = __reduce_min_sync(kAll, first);
+                    if ((g & 31) == lane) kept |= 1u << (g >> 5);
+                    low = m;
                 }
-                if (j == p.k) break;
-                int mine = 1 << 20;
 #pragma unroll
-                for (int i = V - 1; i >= 0; --i)
-                    if (key[i] == m) mine = lane + 32 * i;
-                const int e = __reduce_min_sync(kAll, mine);
-                if (lane == j) id = e;
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (lane + 32 * i == e) key[i] = 0u;
+                for (int i = 0; i < V; ++i) {
+                    const int g = e0 + i < p.E ? (e0 + i) / n : 0;
+                    const uint32_t bits = __shfl_sync(kAll, kept, g & 31);
+                    if (e0 + i < p.E && !(bits >> (g >> 5) & 1)) key[i] = kKeyNegInf;
+                }
             }
         }
-        if (open) id = route_row64(p, dtype, t, c64);
+        int id = -1;               // lane j < k: the j-th choice
+        float least = kNegInf;     // value of the last choice
+        if (!open_groups) {
+            uint32_t taken = 0u;   // bit i: this lane's expert i is chosen
+            uint32_t mine = 0u;    // this lane's best key that is left
+#pragma unroll
+            for (int i = 0; i < V; ++i) mine = max(mine, key[i]);
+            uint32_t prev = 0xFFFFFFFFu;
+            for (int j = 0; j <= p.k; ++j) {
+                const uint32_t m = __reduce_max_sync(kAll, mine);
+                if (m <= kKeyNegInf) break;    // nothing is left
+                if (!by_logit) {
+                    if (j > 0 && !(value_of(prev) - value_of(m) > 2.0f * tol)) open = true;
+                    prev = m;
+                }
+                if (j == p.k) break;
+                least = value_of(m);
+                const int winner = __ffs(__ballot_sync(kAll, mine == m)) - 1;
+                int at = 0;
+                if (lane == winner) {
+                    mine = 0u;
+#pragma unroll
+                    for (int i = V - 1; i >= 0; --i)
+                        if (key[i] == m && !(taken >> i & 1)) at = i;
+                    taken |= 1u << at;
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        if (!(taken >> i & 1)) mine = max(mine, key[i]);
+                }
+                const int e = __shfl_sync(kAll, e0 + at, winner);
+                if (lane == j) id = e;
+            }
+        }
+        if (open || open_groups) {
+            if (!open_groups) {
+                // fp32 leaves what lies within the error of the last choice
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (e0 + i < p.E) c64[e0 + i] = key[i] <= kKeyNegInf ? kNegInf : value_of(key[i]);
+                __syncwarp();
+            }
+            id = route_row64(p, DTYPE, t, c64, !open_groups, static_cast<double>(least) - 2.0 * tol);
+            __syncwarp();
+        }
         float w = 0.0f;
-        if (id >= 0) w = score(load_logit(p.logits, t * p.ldl + id, dtype));
+        if (id >= 0) w = score(load_logit(p.logits, t * p.ldl + id, DTYPE));
         if (p.renorm) {
             // the sum in the order of the choices
             float total = 0.0f;
@@ -346,10 +429,14 @@ __global__ void __launch_bounds__(128) moe_route_kernel(const RouteParams p, int
     }
 }
 
-template <int V>
-cudaError_t launch_v(const RouteParams &p, int dtype, int num_sms, cudaStream_t stream)
+template <int V, int DTYPE>
+cudaError_t launch_v(RouteParams p, int num_sms, cudaStream_t stream)
 {
     constexpr int kWarps = 4;
+    const int n = p.E / p.groups, lanes = n / V;
+    p.group_lanes = n % V == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
+    const int size = DTYPE == 2 ? 4 : 2;
+    p.vec = (reinterpret_cast<uintptr_t>(p.logits) & 15u) == 0 && p.ldl * size % 16 == 0;
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
     const int64_t blocks = (p.T + kWarps - 1) / kWarps;
@@ -364,18 +451,25 @@ cudaError_t launch_v(const RouteParams &p, int dtype, int num_sms, cudaStream_t 
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     // 4 warps x (512 + 2 * 512) doubles is 48 KB, the limit without opting in
-    return cudaLaunchKernelEx(&cfg, moe_route_kernel<V>, p, dtype);
+    return cudaLaunchKernelEx(&cfg, moe_route_kernel<V, DTYPE>, p);
+}
+
+template <int DTYPE>
+cudaError_t launch_dtype(const RouteParams &p, int num_sms, cudaStream_t stream)
+{
+    if (p.E <= 32) return launch_v<1, DTYPE>(p, num_sms, stream);
+    if (p.E <= 64) return launch_v<2, DTYPE>(p, num_sms, stream);
+    if (p.E <= 128) return launch_v<4, DTYPE>(p, num_sms, stream);
+    if (p.E <= 256) return launch_v<8, DTYPE>(p, num_sms, stream);
+    return launch_v<16, DTYPE>(p, num_sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_moe_route(const RouteParams &p, int dtype, int num_sms, cudaStream_t stream)
 {
-    if (p.E <= 32) return launch_v<1>(p, dtype, num_sms, stream);
-    if (p.E <= 64) return launch_v<2>(p, dtype, num_sms, stream);
-    if (p.E <= 128) return launch_v<4>(p, dtype, num_sms, stream);
-    if (p.E <= 256) return launch_v<8>(p, dtype, num_sms, stream);
-    return launch_v<16>(p, dtype, num_sms, stream);
+    return dtype == 0 ? launch_dtype<0>(p, num_sms, stream)
+                      : dtype == 1 ? launch_dtype<1>(p, num_sms, stream) : launch_dtype<2>(p, num_sms, stream);
 }
 
 }  // namespace mxfp4
