@@ -13,10 +13,12 @@
 // bounds the error of both sides. In units of 2^-24 of max(s, |c|): expf 2, the
 // sum 1 + e or the division 1 each, c itself 1, so 2^-21 for the sigmoid; the
 // softmax adds 1 for x - max and up to V + 7 for the sum of the row, so 2^-19.
-// Rows with a closer decision (under one in a hundred) are decided again from
-// 64-bit scores: of the candidates that fp32 leaves, or of all experts where the
-// choice of groups is open. Without bias and groups the logits themselves are
-// compared, which is exact.
+// Rows with a closer decision (one in a few hundred) are decided again from 64-bit
+// scores of the few experts that fp32 leaves in question: those about the border
+// between two groups, or about the last choice. FP64 instructions are slow here (a
+// warp's takes 16 clocks or more): scoring whole rows in 64 bits took half of the
+// kernel's time, though it was for so few. Without bias and groups the logits
+// themselves are compared, which is exact.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -93,10 +95,10 @@ __device__ __forceinline__ void warp_best64(double &v, int &i)
 }
 
 // A row decided in 64 bits: the ids of its k experts in lane order (lane j < k
-// holds the j-th; -1 where nothing is left). `c` is the warp's shared memory, [E]
-// doubles and two a group. chosen: groups are decided, and c holds fp32 values of
-// which those below `least` are out of the question.
-__device__ __noinline__ int route_row64(const RouteParams &p, int dtype, int64_t t, double *c, bool chosen, double least)
+// holds the j-th; -1 where nothing is left), for rows with values that have no order
+// (NaN, infinities) or groups that are no runs of lanes. `c` is the warp's shared
+// memory, [E] doubles and two a group.
+__device__ __noinline__ int route_row64(const RouteParams &p, int dtype, int64_t t, double *c)
 {
     const int lane = threadIdx.x & 31;
     const double kNegInf = -__longlong_as_double(0x7FF0000000000000ll);
@@ -119,16 +121,12 @@ __device__ __noinline__ int route_row64(const RouteParams &p, int dtype, int64_t
         s = warp_sum(s);
     }
     for (int e = lane; e < p.E; e += 32) {
-        if (chosen && c[e] < least) {
-            c[e] = kNegInf;
-            continue;
-        }
         const double z = load_logit(p.logits, t * p.ldl + e, dtype);
         const double score = p.sigmoid ? 1.0 / (1.0 + exp(-z)) : exp(z - m) / s;
         c[e] = z == kNegInf ? kNegInf : p.bias ? score + static_cast<double>(p.bias[e]) : score;
     }
     __syncwarp();
-    if (p.groups > 1 && !chosen) {
+    if (p.groups > 1) {
         const int n = p.E / p.groups;
         for (int g = lane; g < p.groups; g += 32) {
             double b1 = kNegInf, b2 = kNegInf;
@@ -184,6 +182,53 @@ __device__ __noinline__ int route_row64(const RouteParams &p, int dtype, int64_t
         __syncwarp();
     }
     return mine;
+}
+
+// The terms of a row's scores in 64 bits.
+struct Row64 {
+    double m, sum;    // softmax: maximum and sum of exponentials
+};
+
+template <int V>
+__device__ __noinline__ Row64 softmax_terms64(const float (&z)[V])
+{
+    const float kNegInf = -__int_as_float(0x7F800000);
+    float m = kNegInf;
+#pragma unroll
+    for (int i = 0; i < V; ++i) m = fmaxf(m, z[i]);
+    Row64 r;
+    r.m = static_cast<double>(warp_max(m));
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (z[i] != kNegInf) s += exp(static_cast<double>(z[i]) - r.m);
+    r.sum = warp_sum(s);
+    return r;
+}
+
+// Score + bias of expert e in 64 bits, as a monotone integer key (finite values).
+__device__ __noinline__ unsigned long long exact_key64(const RouteParams &p, int dtype, int64_t t, int e, Row64 r)
+{
+    const double z = load_logit(p.logits, t * p.ldl + e, dtype);
+    double c = p.sigmoid ? 1.0 / (1.0 + exp(-z)) : exp(z - r.m) / r.sum;
+    if (p.bias) c += static_cast<double>(p.bias[e]);
+    if (c == 0.0) c = 0.0;
+    const unsigned long long b = __double_as_longlong(c);
+    return (b >> 63) ? ~b : (b | 0x8000000000000000ull);
+}
+__device__ __forceinline__ double value64(unsigned long long k)
+{
+    return __longlong_as_double((k >> 63) ? (k & 0x7FFFFFFFFFFFFFFFull) : ~k);
+}
+
+// The largest key of the warp, and the lowest lane that has it.
+__device__ __forceinline__ unsigned long long warp_max64(unsigned long long k, int &lane_of)
+{
+    const uint32_t hi = __reduce_max_sync(kAll, static_cast<uint32_t>(k >> 32));
+    const bool in = static_cast<uint32_t>(k >> 32) == hi;
+    const uint32_t lo = __reduce_max_sync(kAll, in ? static_cast<uint32_t>(k) : 0u);
+    lane_of = __ffs(__ballot_sync(kAll, in && static_cast<uint32_t>(k) == lo)) - 1;
+    return (static_cast<unsigned long long>(hi) << 32) | lo;
 }
 
 __device__ __forceinline__ float value_of(uint32_t k)   // inverse of key32
@@ -267,8 +312,10 @@ __global__ void __launch_bounds__(128) moe_route_kernel(const RouteParams p)
         };
         const bool by_logit = !p.bias && p.groups == 1 && (p.sigmoid || sum == sum);
         bool open = false;         // a decision closer than fp32 can tell
-        bool open_groups = false;  // such a one between groups, or a value without order
+        bool open_groups = false;  // such a one between groups that are no runs of lanes, or a value without order
         float tol = 0.0f;
+        Row64 row64{0.0, 1.0};
+        bool have64 = false;
         if (by_logit) {
 #pragma unroll
             for (int i = 0; i < V; ++i) key[i] = e0 + i < p.E ? key32(z[i]) : 0u;
@@ -315,7 +362,42 @@ __global__ void __launch_bounds__(128) moe_route_kernel(const RouteParams p)
                 // the worst that stays against the best that goes; sums of two carry twice the error
                 const uint32_t low = __reduce_min_sync(kAll, kept ? mine : 0xFFFFFFFFu);
                 const uint32_t high = __reduce_max_sync(kAll, real && !kept ? mine : 0u);
-                if (high > kKeyNegInf && !(value_of(low) - value_of(high) > 4.0f * tol)) open_groups = true;
+                if (high > kKeyNegInf && !(value_of(low) - value_of(high) > 4.0f * tol)) {
+                    // In question: the groups that stay by less than the error over the best that
+                    // goes, and those that go by less under the worst that stays. Their exact
+                    // scores come from the experts that may be among their best.
+                    if (!p.sigmoid && !have64) {
+                        row64 = softmax_terms64<V>(z);
+                        have64 = true;
+                    }
+                    const bool asked = real && mine > kKeyNegInf &&
+                                       (kept ? gs <= value_of(high) + 4.0f * tol : gs >= value_of(low) - 4.0f * tol);
+                    const float from = value_of(p.group_top == 2 && n > 1 ? k2 : k1) - 2.0f * tol;
+                    unsigned long long d1 = 0, d2 = 0;
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        if (asked && e0 + i < p.E && key[i] > kKeyNegInf && value_of(key[i]) >= from) {
+                            const unsigned long long x = exact_key64(p, DTYPE, t, e0 + i, row64);
+                            d2 = max(d2, min(d1, x));
+                            d1 = max(d1, x);
+                        }
+                    for (int o = 1; o < run; o <<= 1) {
+                        const unsigned long long a1 = __shfl_xor_sync(kAll, d1, o), a2 = __shfl_xor_sync(kAll, d2, o);
+                        d2 = max(max(d2, a2), min(d1, a1));
+                        d1 = max(d1, a1);
+                    }
+                    // a group with one expert left has -inf beside it, and with that is not asked
+                    double exact = asked ? value64(d1) : 0.0;
+                    if (asked && p.group_top == 2 && n > 1) exact += value64(d2);
+                    const int places = p.topk_groups - __popc(__ballot_sync(kAll, kept && !asked)) / run;
+                    int before = 0;
+                    for (int g = 0; g < p.groups; ++g) {
+                        const double other = __shfl_sync(kAll, exact, g * run);
+                        const bool is = __shfl_sync(kAll, asked, g * run);
+                        before += is && (other > exact || (other == exact && g * run < (lane & ~(run - 1))));
+                    }
+                    if (asked) kept = before < places;
+                }
 #pragma unroll
                 for (int i = 0; i < V; ++i)
                     if (!kept && e0 + i < p.E) key[i] = kKeyNegInf;
@@ -403,15 +485,38 @@ __global__ void __launch_bounds__(128) moe_route_kernel(const RouteParams p)
                 if (lane == j) id = e;
             }
         }
-        if (open || open_groups) {
-            if (!open_groups) {
-                // fp32 leaves what lies within the error of the last choice
+        if (open && !open_groups) {
+            // the candidates: what lies within the error of the last choice, or above
+            if (!p.sigmoid && !have64) row64 = softmax_terms64<V>(z);
+            unsigned long long *k64 = reinterpret_cast<unsigned long long *>(c64) + e0;   // this lane's own
+            uint32_t left = 0u;
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (e0 + i < p.E) c64[e0 + i] = key[i] <= kKeyNegInf ? kNegInf : value_of(key[i]);
-                __syncwarp();
+            for (int i = 0; i < V; ++i)
+                if (e0 + i < p.E && key[i] > kKeyNegInf && value_of(key[i]) >= least - 2.0f * tol) left |= 1u << i;
+            for (uint32_t todo = left; todo; todo &= todo - 1) {
+                const int i = __ffs(todo) - 1;
+                k64[i] = exact_key64(p, DTYPE, t, e0 + i, row64);
             }
-            id = route_row64(p, DTYPE, t, c64, !open_groups, static_cast<double>(least) - 2.0 * tol);
+            __syncwarp();
+            id = -1;
+            for (int j = 0; j < p.k; ++j) {
+                unsigned long long best = 0;
+                int at = 0;
+                for (uint32_t todo = left; todo; todo &= todo - 1) {
+                    const int i = __ffs(todo) - 1;
+                    if (k64[i] > best) {
+                        best = k64[i];
+                        at = i;
+                    }
+                }
+                int winner;
+                if (warp_max64(best, winner) == 0) break;     // nothing is left
+                if (lane == winner) left &= ~(1u << at);
+                const int e = __shfl_sync(kAll, e0 + at, winner);
+                if (lane == j) id = e;
+            }
+        } else if (open_groups) {
+            id = route_row64(p, DTYPE, t, c64);
             __syncwarp();
         }
         float w = 0.0f;
