@@ -251,16 +251,33 @@ __device__ __forceinline__ Ring ring_at(int i)
     return Ring{i % N, static_cast<uint32_t>(i / N) & 1u};
 }
 
-// The 32 accumulator columns v of one weight row a thread, staged 16 at a time
-// through shared memory so that a thread gets neighbouring rows (channels) of one
-// column (token), and stored: product 1 as MXFP8 of silu(g) * u, product 2 as bf16.
-// Called by the 128 epilogue threads; c0: first token of the columns, which has
-// at least one.
+// Stores the 32 accumulator columns (tokens) v of one weight row (channel) a thread:
+// product 2 as bf16 from registers; product 1 as MXFP8 of silu(g) * u, staged 16
+// columns at a time through shared memory so that a thread gets neighbouring
+// channels of one token. Called by the 128 epilogue threads; c0: first column,
+// below w.rows.
 template <bool FIRST>
 __device__ __forceinline__ void store_columns(const uint32_t (&v)[32], float *epi, const Unit &w, int c0, int ntb,
                                               const ProductParams &p)
 {
     const int t = threadIdx.x & 127;
+    if constexpr (!FIRST) {
+        // neighbouring lanes hold neighbouring channels: an even lane takes the pair of
+        // an even column, its neighbour that of the next, so a warp stores 64 bytes
+        // of each of two tokens at a time
+        const int odd = t & 1;
+        __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(p.y) + (static_cast<size_t>(w.row0) + c0) * p.H + 128 * w.m +
+                           (t & ~1);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const float mine = __uint_as_float(odd ? v[2 * j + 1] : v[2 * j]);
+            const float other = __uint_as_float(__shfl_xor_sync(0xffffffffu, odd ? v[2 * j] : v[2 * j + 1], 1));
+            if (c0 + 2 * j + odd < w.rows)
+                *reinterpret_cast<__nv_bfloat162 *>(o + static_cast<size_t>(2 * j + odd) * p.H) =
+                    odd ? __floats2bfloat162_rn(other, mine) : __floats2bfloat162_rn(mine, other);
+        }
+        return;
+    }
     const int col = t >> 3, part = t & 7;      // this thread's column and eighth of the staged rows
 #pragma unroll
     for (int pass = 0; pass < 2; ++pass) {
@@ -302,17 +319,6 @@ __device__ __forceinline__ void store_columns(const uint32_t (&v)[32], float *ep
                                   (r >> 7) * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4 + (w.m & 1) * 2;
                     *reinterpret_cast<uint16_t *>(sf) = static_cast<uint16_t>(b | (b2 << 8));
                 }
-            }
-        } else if (live) {
-            const float *s = epi + col * kEpiLd + 16 * part;
-            uint4 *o = reinterpret_cast<uint4 *>(p.y + row * p.H + 128 * w.m + 16 * part);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float4 x = *reinterpret_cast<const float4 *>(s + 8 * i);
-                const float4 z = *reinterpret_cast<const float4 *>(s + 8 * i + 4);
-                const __nv_bfloat162 h[4] = {__floats2bfloat162_rn(x.x, x.y), __floats2bfloat162_rn(x.z, x.w),
-                                             __floats2bfloat162_rn(z.x, z.y), __floats2bfloat162_rn(z.z, z.w)};
-                o[i] = *reinterpret_cast<const uint4 *>(h);
             }
         }
         epilogue_sync();   // the staging buffer is reused
@@ -653,10 +659,15 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
                     }
                 }
             }
-            // copies in flight land before the block leaves
+            // copies in flight land before the block leaves, and so do the arrivals of its
+            // last MMAs, which nobody else waits for
             for (int i = max(0, gs - PACKED); i < gs; ++i) {
                 const Ring r = ring_at<PACKED>(i);
                 mbar_wait(p_full + r.slot, r.parity, &g_moe_error, kErrWaitDrain);
+            }
+            for (int i = max(0, gs - TOKEN); i < gs && !*abort_flag; ++i) {
+                const Ring r = ring_at<TOKEN>(i);
+                if (!mbar_wait(done + r.slot, r.parity, &g_moe_error, kErrWaitDrain)) break;
             }
         }
     } else if (lane == 0) {
@@ -716,7 +727,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
 // cp.async instead, 28 KB a stage took 900 clocks.)
 
 constexpr int kLargeNT = kMoeLargeTile;
-constexpr int kLargeThreads = 544;
+constexpr int kLargeGroups = 3;                    // widening groups of four warps
+constexpr int kLargeThreads = 32 * (9 + 4 * kLargeGroups);
 
 struct LargeCfg {
     static constexpr int PACKED = 3, OPER = 5;
@@ -744,17 +756,19 @@ struct LargeCfg {
 // FIRST: product 1 (a pair's tile: 128 channels of G and of U, 64 of each in a CTA),
 // else product 2 (256 rows). Warps of each CTA:
 //   0-3    epilogue of the CTA's 128 weight rows
-//   4-11   widen packed weights: groups of four on alternating packed stages; they
-//          also see the stage's tokens land, and tell rank 0
-//   12     owns TMEM; lane 0 of rank 0 issues the MMAs
-//   13     lane 0 loads packed weights and their scales by TMA
-//   14     lane 0 loads tokens and their scales by TMA
-//   15,16  lane 0 of each, rank 0: copies the scales of alternating stages to both TMEMs
+//   4-15   widen packed weights: three groups of four take the packed stages in turn
+//          (a group's two stages take it about 2700 clocks of waits, copies and
+//          fences); they also see the tokens land, and tell rank 0
+//   16     owns TMEM; rank 0: issues the MMAs
+//   17     lane 0 loads packed weights and their scales by TMA
+//   18     lane 0 loads tokens and their scales by TMA
+//   19,20  lane 0 of each, rank 0: copies the scales of alternating stages to both TMEMs
 template <bool FIRST>
 __global__ void __launch_bounds__(kLargeThreads, 1) moe_product_large_kernel(const __grid_constant__ ProductParams p)
 {
     using Cfg = LargeCfg;
     constexpr int PACKED = Cfg::PACKED, OPER = Cfg::OPER, NT = kLargeNT;
+    constexpr int kMmaWarp = 4 + 4 * kLargeGroups;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float *epi = reinterpret_cast<float *>(smem + Cfg::EPI_AT);
@@ -766,7 +780,7 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_product_large_kernel(con
     uint64_t *done = s_full + OPER;        // its MMAs have completed
     uint64_t *accf = done + OPER;          // [2] accumulators complete
     uint64_t *acc_empty = accf + 2;        // [2] rank 0: both CTAs have drained them
-    uint64_t *cp_done = acc_empty + 2;     // [2] rank 0: the scale copies of warp 15 / 16 have completed
+    uint64_t *cp_done = acc_empty + 2;     // [2] rank 0: the scale copies of the last two warps have completed
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(cp_done + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     volatile int *epi_go = abort_flag + 1;   // [2]
@@ -796,7 +810,7 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_product_large_kernel(con
         tma_prefetch_desc(&p.tm_t);
         tma_prefetch_desc(&p.tm_tsf);
     }
-    if (warp == 12) {
+    if (warp == kMmaWarp) {
         tmem_alloc_pair(tmem_slot, Cfg::TMEM_COLS);
         tmem_relinquish_pair();
     }
@@ -851,7 +865,7 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_product_large_kernel(con
                 if (live) store_columns<FIRST>(v, epi, w, c0, 2, p);
             }
         }
-    } else if (warp < 12) {
+    } else if (warp < kMmaWarp) {
         // -------------------------------------------------- widening of weights
         // Lane l takes row l % 8 of a group of eight and 16-byte column l / 8 of a half:
         // both swizzles then spread eight lanes over all banks.
@@ -864,7 +878,7 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_product_large_kernel(con
         bool ok = true;
         for (int ul = 0; ul < n && ok; ++ul)
             for (int kq = 0; kq < kp && ok; ++kq, ++pk) {
-                if ((pk & 1) != group) continue;
+                if (pk % kLargeGroups != group) continue;
                 const Ring rp = ring_at<PACKED>(pk);
                 ok = mbar_wait_warp(p_full + rp.slot, rp.parity, &g_moe_error, kErrWaitFull, p.wait_ns);
                 if (!ok) break;
@@ -914,7 +928,7 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_product_large_kernel(con
                 }
             }
         if (!ok) *abort_flag = 1;
-    } else if (warp == 12) {
+    } else if (warp == kMmaWarp) {
         if (leader) {
             // ------------------------------------------------------- MMA issuer
             // The whole warp walks the stages and one elected lane issues, so that
@@ -957,7 +971,7 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_product_large_kernel(con
             for (int b = 0; b < 2; ++b)
                 if (commits[b] > 0) mbar_wait_warp(accf + b, (commits[b] - 1) & 1, &g_moe_error, kErrWaitDrain);
         }
-    } else if (warp == 13) {
+    } else if (warp == kMmaWarp + 1) {
         if (lane == 0) {
             // --------------------------------------------- packed weights by TMA
             const uint64_t pol = policy_evict_last();
@@ -995,7 +1009,7 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_product_large_kernel(con
                 mbar_wait(p_full + r.slot, r.parity, &g_moe_error, kErrWaitDrain);
             }
         }
-    } else if (warp == 14) {
+    } else if (warp == kMmaWarp + 2) {
         if (lane == 0) {
             // ----------------------------------------------------- tokens by TMA
             const uint64_t pol = policy_evict_last();
@@ -1018,14 +1032,20 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_product_large_kernel(con
                     tma_load_2d(st + Cfg::TSF_OFF, &p.tm_tsf, 0, (w.tile * kc + ks) * 2, t_full + r.slot, pol);
                 }
             }
+            // copies in flight land before the block leaves, and so do the arrivals of the
+            // last MMAs, which come from rank 0 and nobody else waits for
             for (int i = max(0, gs - OPER); i < gs; ++i) {
                 const Ring r = ring_at<OPER>(i);
                 mbar_wait(t_full + r.slot, r.parity, &g_moe_error, kErrWaitDrain);
             }
+            for (int i = max(0, gs - OPER); i < gs && !*abort_flag; ++i) {
+                const Ring r = ring_at<OPER>(i);
+                if (!mbar_wait(done + r.slot, r.parity, &g_moe_error, kErrWaitDrain)) break;
+            }
         }
     } else if (leader && lane == 0) {
         // ------------------------------------------------------ scales to TMEM
-        const int me = warp - 15, total = walk.left() * kc;
+        const int me = warp - kMmaWarp - 3, total = walk.left() * kc;
         bool ok = true;
         for (int gs = me; gs < total && !*abort_flag; gs += 2) {
             const Ring r = ring_at<OPER>(gs);
@@ -1051,7 +1071,7 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_product_large_kernel(con
     // its shared memory and TMEM
     tc_fence_before();
     cluster_sync();
-    if (warp == 12) {
+    if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_dealloc_pair(tmem, Cfg::TMEM_COLS);
     }
