@@ -492,22 +492,33 @@ def mxfp8_add_rmsnorm_quantize(X, weight, eps: float = 1e-6, residual=None, H=No
     x, ldx = _rows(X, "X", dtype, shape)
     w = _vec(weight, "weight", dtype, (K,))
     res, ldr = _rows(residual, "residual", dtype, shape) if residual is not None else (None, 0)
-    if residual is not None and H is None:
+    # outputs made here need no check
+    if H is not None:
+        h, ldh = _rows(H, "H", dtype, shape)
+    elif residual is not None:
         H = torch.empty(shape, dtype=dtype, device=device)
-    h, ldh = _rows(H, "H", dtype, shape) if H is not None else (None, 0)
-    if want_y and Y is None:
+        h, ldh = H.data_ptr(), K
+    else:
+        h, ldh = None, 0
+    if Y is not None:
+        y, ldy = _rows(Y, "Y", dtype, shape)
+    elif want_y:
         Y = torch.empty(shape, dtype=dtype, device=device)
-    y, ldy = _rows(Y, "Y", dtype, shape) if Y is not None else (None, 0)
-    if Aq is None:
-        # rows a multiple of 16 bytes apart, as the products want them
-        Aq = torch.empty((M, (K + 15) // 16 * 16), dtype=torch.uint8, device=device)
-        if K % 16:
-            Aq = Aq[:, :K]
-    q, ldq = _rows(Aq, "Aq", torch.uint8, shape)
+        y, ldy = Y.data_ptr(), K
+    else:
+        y, ldy = None, 0
+    if Aq is not None:
+        q, ldq = _rows(Aq, "Aq", torch.uint8, shape)
+    else:
+        # K is a multiple of 32, so rows lie a multiple of 16 bytes apart, as the products want them
+        Aq = torch.empty(shape, dtype=torch.uint8, device=device)
+        q, ldq = Aq.data_ptr(), K
     need = _sf_bytes32(M, K)
-    if A_sf is None:
+    if A_sf is not None:
+        sf = _scales(A_sf, "A_sf", need)
+    else:
         A_sf = torch.empty(need, dtype=torch.uint8, device=device)
-    sf = _scales(A_sf, "A_sf", need)
+        sf = A_sf.data_ptr()
     _check(_lib.mxfp8_add_rmsnorm_quantize(x, ldx, res, ldr, w, _DTYPES[dtype], eps, M, K, h, ldh, y, ldy, q, ldq, sf,
                                            _stream_of(stream, X)),
            "mxfp8_add_rmsnorm_quantize")
@@ -528,14 +539,19 @@ def moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1
     T, E = shape
     z, ldl = _rows(logits, "logits", dtype, shape)
     out = (T, max(k, 0))
-    if ids is None:
+    if ids is not None:
+        pi = _vec(ids, "ids", torch.int32, out)
+    else:
         ids = torch.empty(out, dtype=torch.int32, device=logits.device)
-    if weights is None:
+        pi = ids.data_ptr()
+    if weights is not None:
+        pw = _vec(weights, "weights", torch.float32, out)
+    else:
         weights = torch.empty(out, dtype=torch.float32, device=logits.device)
+        pw = weights.data_ptr()
     _check(_lib.moe_route(z, _DTYPES[dtype], ldl, T, E,
                           _vec(bias, "bias", torch.float32, (E,)) if bias is not None else None, MOE_SCORES[score],
-                          groups, topk_groups, group_top, k, 1 if renormalize else 0, scale,
-                          _vec(ids, "ids", torch.int32, out), _vec(weights, "weights", torch.float32, out),
+                          groups, topk_groups, group_top, k, 1 if renormalize else 0, scale, pi, pw,
                           _stream_of(stream, logits)),
            "moe_route")
     return ids, weights
@@ -562,9 +578,11 @@ def mxfp4_moe_experts(Xq, X_sf, ids, weights, W13q, W13_sf, W2q, W2_sf, out=None
     E, two_i, _ = W13q.shape
     I, k = two_i // 2, ids.shape[1]
     x, ldx = _rows(Xq, "Xq", u8, (T, H))
-    if out is None:
+    if out is not None:
+        o, ldo = _rows(out, "out", torch.bfloat16, (T, H))
+    else:
         out = torch.empty((T, H), dtype=torch.bfloat16, device=Xq.device)
-    o, ldo = _rows(out, "out", torch.bfloat16, (T, H))
+        o, ldo = out.data_ptr(), H
     if workspace is None:
         workspace = moe_experts_workspace(T, k, E, H, I, Xq.device)
     _check(_lib.mxfp4_moe_experts(x, ldx, _scales(X_sf, "X_sf", _sf_bytes32(T, H)), _vec(ids, "ids", torch.int32, (T, k)),
