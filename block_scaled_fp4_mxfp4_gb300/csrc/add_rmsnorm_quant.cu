@@ -283,13 +283,14 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 6 : 1) add_r
             finish8<F16>(p, row, v, v < nvec, hv, r);
         }
     }
-    // pad rows of the last 128-row block of scales, shared out over all threads
-    const int kc = (p.K + 127) / 128;
-    const int64_t pad_words = ((p.M + 127) / 128 * 128 - p.M) * kc;
-    for (int64_t i = row * nt + threadIdx.x; i < pad_words; i += static_cast<int64_t>(gridDim.x) * nt) {
-        const int64_t pr = p.M + i / kc;
-        *reinterpret_cast<uint32_t *>(p.sf + ((pr >> 7) * kc + i % kc) * 512 + (pr & 31) * 16 + ((pr & 127) >> 5) * 4) =
-            0x7F7F7F7Fu;
+    // pad rows of the last 128-row block of scales, shared out over all threads in the
+    // order of memory: word w of a 512-byte block is row w / 4 + 32 (w % 4)
+    const int last = static_cast<int>(p.M & 127), words = (p.K + 127) / 128 * 128;
+    if (last == 0) return;
+    uint32_t *sf = reinterpret_cast<uint32_t *>(p.sf + (p.M >> 7) * (static_cast<int64_t>(words) * 4));
+    for (int64_t i = row * nt + threadIdx.x; i < words; i += static_cast<int64_t>(gridDim.x) * nt) {
+        const int w = static_cast<int>(i) & 127;
+        if ((w >> 2) + 32 * (w & 3) >= last) sf[i] = 0x7F7F7F7Fu;
     }
 }
 

@@ -236,6 +236,7 @@ struct SmallCfg {
     static constexpr uint32_t ACC_COLS = 4 * kSmallNT;             // [buffer][issuer]
     static constexpr uint32_t TMEM_COLS = 256;
     static_assert(TOKEN_BYTES % 1024 == 0 && SMEM_BYTES <= 232448, "shared memory budget");
+    static_assert(PACKED % 2 == 0 && WIDE == 3 && TOKEN == 5, "what the waits' parities rest on");
     static_assert(WIDE <= TOKEN, "the wide ring is freed by the token ring's barriers");
     static_assert(ACC_COLS + TOKEN * SF_COLS <= TMEM_COLS, "TMEM budget");
 };
@@ -374,6 +375,14 @@ struct UnitWalk {
 //   16,17  MMA issuers (lane 0), on alternating stages of a tile; 16 owns TMEM
 //   18     lane 0 loads packed weights by TMA
 //   19,20  lane 0 of each copies the scales of alternating stages to TMEM
+//
+// A wait on a ring's barrier names the round by its parity alone, so it is right only
+// if the barrier can be neither a round further nor a round behind. What makes it so
+// here: a packed slot belongs to one group (PACKED is even); tokens are copied in
+// order; a stage is widened only after the MMAs of the stage WIDE = 3 before it, and
+// its group and its scale thread have served stage i - 2 before: so who has seen stage
+// i - 2 ready knows that i - 5, whose slot it shares, was multiplied. A third group
+// breaks this: a stage could then be two ahead of a slow one, and the waits fail.
 // Loading weights already widened was measured too: a TMA load that unpacks moves 16
 // bytes of shared memory a clock, 8-byte cp.async half of what HBM gives.
 template <bool FIRST>
@@ -728,7 +737,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
 
 constexpr int kLargeNT = kMoeLargeTile;
 constexpr int kLargeGroups = 3;                    // widening groups of four warps
-constexpr int kLargeThreads = 32 * (9 + 4 * kLargeGroups);
+constexpr int kLargeThreads = 32 * (8 + 4 * kLargeGroups);
 
 struct LargeCfg {
     static constexpr int PACKED = 3, OPER = 5;
@@ -743,13 +752,14 @@ struct LargeCfg {
     static constexpr uint32_t TOKEN_AT = WIDE_AT + OPER * WIDE_BYTES;
     static constexpr uint32_t EPI_AT = TOKEN_AT + OPER * TOKEN_BYTES;
     static constexpr uint32_t BAR_AT = EPI_AT + kEpiBytes;
-    static constexpr int BARS = 2 * PACKED + 4 * OPER + 6;
+    static constexpr int BARS = 2 * PACKED + 4 * OPER + 5;
     static constexpr uint32_t SMEM_BYTES = BAR_AT + BARS * 8 + 32 + 1024;
     static constexpr uint32_t SF_COLS = 12;                          // a block of weights, two of tokens
     static constexpr uint32_t TMEM_COLS = 512;
     static_assert(PACKED_BYTES % 1024 == 0 && WIDE_BYTES % 1024 == 0 && TOKEN_BYTES % 1024 == 0, "swizzle atoms");
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
     static_assert(2 * kLargeNT + OPER * SF_COLS <= TMEM_COLS, "TMEM budget");
+    static_assert(PACKED == kLargeGroups, "a packed slot belongs to one group");
     static_assert(HALF % 16 == 0, "halves of a tile are MMA operands");
 };
 
@@ -762,7 +772,15 @@ struct LargeCfg {
 //   16     owns TMEM; rank 0: issues the MMAs
 //   17     lane 0 loads packed weights and their scales by TMA
 //   18     lane 0 loads tokens and their scales by TMA
-//   19,20  lane 0 of each, rank 0: copies the scales of alternating stages to both TMEMs
+//   19     rank 0: copies the scales to both TMEMs, stage by stage
+//
+// A wait on a ring's barrier names the round by its parity alone, so it is right only
+// if the barrier can be neither a round further nor a round behind. Not behind:
+// a packed slot belongs to one group (PACKED = groups); a group that waits for `done`
+// of stage i - OPER has seen that of i - 2 OPER or a later one, and MMAs complete in
+// order; one warp waits for `ready`, of every stage in order (two that took turns
+// could find a stage's slot still in the round before: groups finish out of order).
+// Not further: a stage's next round needs its MMAs, and so all who wait for it.
 template <bool FIRST>
 __global__ void __launch_bounds__(kLargeThreads, 1) moe_product_large_kernel(const __grid_constant__ ProductParams p)
 {
@@ -780,8 +798,8 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_product_large_kernel(con
     uint64_t *done = s_full + OPER;        // its MMAs have completed
     uint64_t *accf = done + OPER;          // [2] accumulators complete
     uint64_t *acc_empty = accf + 2;        // [2] rank 0: both CTAs have drained them
-    uint64_t *cp_done = acc_empty + 2;     // [2] rank 0: the scale copies of the last two warps have completed
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(cp_done + 2);
+    uint64_t *cp_done = acc_empty + 2;     // rank 0: the scale copies have completed
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(cp_done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     volatile int *epi_go = abort_flag + 1;   // [2]
 
@@ -802,8 +820,8 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_product_large_kernel(con
         for (int b = 0; b < 2; ++b) {
             mbar_init(accf + b, 1);
             mbar_init(acc_empty + b, 8);    // one arrival from each epilogue warp of both CTAs
-            mbar_init(cp_done + b, 1);
         }
+        mbar_init(cp_done, 1);
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&p.tm_w);
@@ -819,7 +837,6 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_product_large_kernel(con
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const uint32_t tmem_sf = tmem + 2 * NT;
     grid_dependency_wait();
     grid_launch_dependents();
     const int tiles = __ldcg(p.tile0 + p.E);
@@ -828,7 +845,7 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_product_large_kernel(con
     const int kp = (kc + 1) >> 1;                           // packed stages; the last one may be half
     const int wrows = FIRST ? 2 * p.I : p.H;                // weight rows of an expert
     const int mw = FIRST ? p.I >> 7 : (p.H + 255) >> 8;     // weight tiles of an expert
-    // uniform across the warp, for the MMA issuer
+    // uniform across the warp, for the issuers of MMAs and scale copies
     const uint32_t tmem_u = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t wide_desc = sdesc_sw128(smem_u32(smem + Cfg::WIDE_AT));
     const uint64_t token_desc = sdesc_sw128(smem_u32(smem + Cfg::TOKEN_AT));
@@ -1043,27 +1060,33 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_product_large_kernel(con
                 if (!mbar_wait(done + r.slot, r.parity, &g_moe_error, kErrWaitDrain)) break;
             }
         }
-    } else if (leader && lane == 0) {
+    } else if (leader) {
         // ------------------------------------------------------ scales to TMEM
-        const int me = warp - kMmaWarp - 3, total = walk.left() * kc;
+        const int total = walk.left() * kc;
+        const uint64_t w_desc = sdesc_scale(smem_u32(smem + Cfg::WIDE_AT + Cfg::WSF_OFF));
+        const uint64_t t_desc = sdesc_scale(smem_u32(smem + Cfg::TOKEN_AT + Cfg::TSF_OFF));
         bool ok = true;
-        for (int gs = me; gs < total && !*abort_flag; gs += 2) {
+        for (int gs = 0; gs < total; ++gs) {
             const Ring r = ring_at<OPER>(gs);
-            ok = mbar_wait<true>(ready + r.slot, r.parity, &g_moe_error, kErrWaitFull, p.wait_ns);
+            ok = mbar_wait_warp<true>(ready + r.slot, r.parity, &g_moe_error, kErrWaitFull, p.wait_ns);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t ws = smem_u32(smem + Cfg::WIDE_AT) + r.slot * Cfg::WIDE_BYTES + Cfg::WSF_OFF;
-            const uint32_t ts = smem_u32(smem + Cfg::TOKEN_AT) + r.slot * Cfg::TOKEN_BYTES + Cfg::TSF_OFF;
-            const uint32_t tsf = tmem_sf + r.slot * Cfg::SF_COLS;
-            tc_cp_scale_block_pair(tsf, sdesc_scale(ws));
-            tc_cp_scale_block_pair(tsf + 4, sdesc_scale(ts));
-            tc_cp_scale_block_pair(tsf + 8, sdesc_scale(ts + 512));
-            tc_commit_pair(s_full + r.slot);
+            const uint64_t wd = w_desc + static_cast<uint64_t>(r.slot * (Cfg::WIDE_BYTES >> 4));
+            const uint64_t td = t_desc + static_cast<uint64_t>(r.slot * (Cfg::TOKEN_BYTES >> 4));
+            const uint32_t tsf = tmem_u + 2 * NT + r.slot * Cfg::SF_COLS;
+            if (elect_one()) {
+                tc_cp_scale_block_pair(tsf, wd);
+                tc_cp_scale_block_pair(tsf + 4, td);
+                tc_cp_scale_block_pair(tsf + 8, td + 32);
+                tc_commit_pair(s_full + r.slot);
+            }
+            __syncwarp();
         }
         if (!ok) *abort_flag = 1;
         // no copy may be running when the pair frees TMEM
-        tc_commit_pair(cp_done + me);
-        mbar_wait(cp_done + me, 0, &g_moe_error, kErrWaitDrain);
+        if (elect_one()) tc_commit_pair(cp_done);
+        __syncwarp();
+        mbar_wait_warp(cp_done, 0, &g_moe_error, kErrWaitDrain);
     }
     __syncwarp();
 
