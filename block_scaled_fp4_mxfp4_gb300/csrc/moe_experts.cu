@@ -550,6 +550,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
             }
         }
         cp_async_wait_all();   // also after an abort: nothing of this thread is in flight when the block leaves
+        // nor are the arrivals of the last MMAs, which nobody else waits for
+        for (int i = max(0, gs - TOKEN); i < gs && ok; ++i) {
+            const Ring r = ring_at<TOKEN>(i);
+            ok = mbar_wait_warp(done + r.slot, r.parity, &g_moe_error, kErrWaitDrain);
+        }
     } else if (warp < 16) {
         // -------------------------------------------------- widening of weights
         // Lane l takes row l % 8 of a group of eight and 16-byte column l / 8 (+ 4): both
@@ -668,15 +673,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
                     }
                 }
             }
-            // copies in flight land before the block leaves, and so do the arrivals of its
-            // last MMAs, which nobody else waits for
+            // copies in flight land before the block leaves
             for (int i = max(0, gs - PACKED); i < gs; ++i) {
                 const Ring r = ring_at<PACKED>(i);
                 mbar_wait(p_full + r.slot, r.parity, &g_moe_error, kErrWaitDrain);
-            }
-            for (int i = max(0, gs - TOKEN); i < gs && !*abort_flag; ++i) {
-                const Ring r = ring_at<TOKEN>(i);
-                if (!mbar_wait(done + r.slot, r.parity, &g_moe_error, kErrWaitDrain)) break;
             }
         }
     } else if (lane == 0) {

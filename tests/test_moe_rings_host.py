@@ -76,8 +76,6 @@ def small(rng, units, stages, groups=2, packed=4, wide=3, token=5):
                 yield from wait(p_empty[g % packed], g // packed - 1)
             yield
             flying.append(p_full[g % packed])
-        for g in range(max(0, total - token), total):
-            yield from wait(done[g % token], g // token)
 
     def tokens():
         for g in range(total):
@@ -85,6 +83,8 @@ def small(rng, units, stages, groups=2, packed=4, wide=3, token=5):
                 yield from wait(done[g % token], g // token - 1)
             yield
             t_full[g % token].arrive()
+        for g in range(max(0, total - token), total):
+            yield from wait(done[g % token], g // token)
 
     def widen(group):
         for g in range(group, total, groups):
