@@ -230,7 +230,7 @@ struct SmallCfg {
     static constexpr uint32_t TOKEN_AT = WIDE_AT + WIDE * WIDE_BYTES;
     static constexpr uint32_t EPI_AT = TOKEN_AT + TOKEN * TOKEN_BYTES;
     static constexpr uint32_t BAR_AT = EPI_AT + kEpiBytes;
-    static constexpr int BARS = 2 * PACKED + 3 * TOKEN + 6;
+    static constexpr int BARS = 2 * PACKED + 3 * TOKEN + 8;
     static constexpr uint32_t SMEM_BYTES = BAR_AT + BARS * 8 + 32 + 1024;
     static constexpr uint32_t SF_COLS = 16;                        // two blocks of weights, two of tokens, 4 columns each
     static constexpr uint32_t ACC_COLS = 4 * kSmallNT;             // [buffer][issuer]
@@ -401,7 +401,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
     uint64_t *accf = done + TOKEN;         // [2] accumulators complete
     uint64_t *acc_empty = accf + 2;        // [2] accumulators drained
     uint64_t *cp_done = acc_empty + 2;     // [2] the scale copies of warp 19 / 20 have completed
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(cp_done + 2);
+    uint64_t *mma_done = cp_done + 2;      // [2] the MMAs of each issuer have completed
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     volatile int *epi_go = abort_flag + 1;   // [2]
 
@@ -420,6 +421,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
             mbar_init(accf + b, 2);         // both issuers
             mbar_init(acc_empty + b, 128);
             mbar_init(cp_done + b, 1);
+            mbar_init(mma_done + b, 1);
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -434,7 +436,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const uint32_t tmem_sf = tmem + Cfg::ACC_COLS;
-    grid_dependency_wait();
+    // Product 2 starts while product 1 drains, and loads weights meanwhile: product 1
+    // let it start only after everything before it had completed, so the tables of the
+    // placing kernel and the weights are there; only the activations are not. (Asking L2
+    // for more of the weights than the ring holds was measured slower.)
+    if (FIRST) grid_dependency_wait();
     grid_launch_dependents();
     const int tiles = __ldcg(p.tile0 + p.E);
     const int K = FIRST ? p.H : p.I;
@@ -484,6 +490,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
         const int t = threadIdx.x - 128;
         const int r0 = t >> 3, c = t & 7;
         const uint32_t dst0 = r0 * 128 + ((c ^ (r0 & 7)) << 4);
+        if (!FIRST) grid_dependency_wait();
         int gs = 0;
         bool ok = true;
         while (walk.more() && ok) {
@@ -599,7 +606,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
         // Whole warps walk the stages and one elected lane issues, so that descriptors
         // stay in uniform registers.
         const int me = warp - 16;
-        int gs = 0, ul = 0, commits[2] = {0, 0};
+        int gs = 0, ul = 0;
         bool ok = true;
         for (; walk.more() && ok; ++ul) {
             const Unit w = walk.take();
@@ -635,12 +642,12 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
             gs += stages;
             if (elect_one()) tc_commit(accf + buf);
             __syncwarp();
-            ++commits[buf];
         }
         if (!ok) *abort_flag = 1;
         // no MMA may be running when TMEM is released
-        for (int b = 0; b < 2; ++b)
-            if (commits[b] > 0) mbar_wait_warp(accf + b, (commits[b] - 1) & 1, &g_moe_error, kErrWaitDrain);
+        if (elect_one()) tc_commit(mma_done + me);
+        __syncwarp();
+        mbar_wait_warp(mma_done + me, 0, &g_moe_error, kErrWaitDrain);
     } else if (warp == 18) {
         if (lane == 0) {
             // --------------------------------------------- packed weights by TMA
@@ -752,7 +759,7 @@ struct LargeCfg {
     static constexpr uint32_t TOKEN_AT = WIDE_AT + OPER * WIDE_BYTES;
     static constexpr uint32_t EPI_AT = TOKEN_AT + OPER * TOKEN_BYTES;
     static constexpr uint32_t BAR_AT = EPI_AT + kEpiBytes;
-    static constexpr int BARS = 2 * PACKED + 4 * OPER + 5;
+    static constexpr int BARS = 2 * PACKED + 4 * OPER + 6;
     static constexpr uint32_t SMEM_BYTES = BAR_AT + BARS * 8 + 32 + 1024;
     static constexpr uint32_t SF_COLS = 12;                          // a block of weights, two of tokens
     static constexpr uint32_t TMEM_COLS = 512;
@@ -799,7 +806,8 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_product_large_kernel(con
     uint64_t *accf = done + OPER;          // [2] accumulators complete
     uint64_t *acc_empty = accf + 2;        // [2] rank 0: both CTAs have drained them
     uint64_t *cp_done = acc_empty + 2;     // rank 0: the scale copies have completed
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(cp_done + 1);
+    uint64_t *mma_done = cp_done + 1;      // all MMAs have completed
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     volatile int *epi_go = abort_flag + 1;   // [2]
 
@@ -822,6 +830,7 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_product_large_kernel(con
             mbar_init(acc_empty + b, 8);    // one arrival from each epilogue warp of both CTAs
         }
         mbar_init(cp_done, 1);
+        mbar_init(mma_done, 1);
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&p.tm_w);
@@ -837,7 +846,11 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_product_large_kernel(con
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    grid_dependency_wait();
+    // Product 2 starts while product 1 drains, and loads weights meanwhile: product 1
+    // let it start only after everything before it had completed, so the tables of the
+    // placing kernel and the weights are there; only the activations are not. (Asking L2
+    // for more of the weights than the ring holds was measured slower.)
+    if (FIRST) grid_dependency_wait();
     grid_launch_dependents();
     const int tiles = __ldcg(p.tile0 + p.E);
     const int K = FIRST ? p.H : p.I;
@@ -950,7 +963,7 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_product_large_kernel(con
             // ------------------------------------------------------- MMA issuer
             // The whole warp walks the stages and one elected lane issues, so that
             // descriptors stay in uniform registers.
-            int gs = 0, ul = 0, commits[2] = {0, 0};
+            int gs = 0, ul = 0;
             bool ok = true;
             for (; walk.more() && ok; ++ul) {
                 const Unit w = walk.take();
@@ -981,13 +994,13 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_product_large_kernel(con
                 }
                 if (elect_one()) tc_commit_pair_mc(accf + buf, 0x3);
                 __syncwarp();
-                ++commits[buf];
             }
             if (!ok) *abort_flag = 1;
-            // no MMA may be running when the pair frees TMEM
-            for (int b = 0; b < 2; ++b)
-                if (commits[b] > 0) mbar_wait_warp(accf + b, (commits[b] - 1) & 1, &g_moe_error, kErrWaitDrain);
+            if (elect_one()) tc_commit_pair_mc(mma_done, 0x3);
+            __syncwarp();
         }
+        // no MMA may be running when the pair frees TMEM, nor an arrival of one be on its way
+        mbar_wait_warp(mma_done, 0, &g_moe_error, kErrWaitDrain);
     } else if (warp == kMmaWarp + 1) {
         if (lane == 0) {
             // --------------------------------------------- packed weights by TMA
@@ -1029,6 +1042,7 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_product_large_kernel(con
     } else if (warp == kMmaWarp + 2) {
         if (lane == 0) {
             // ----------------------------------------------------- tokens by TMA
+            if (!FIRST) grid_dependency_wait();
             const uint64_t pol = policy_evict_last();
             int gs = 0;
             bool ok = true;

@@ -18,8 +18,10 @@
  * byte 0xFF (NaN), so that whatever is computed from it is NaN.
  *
  * Overlap of consecutive calls: every launch uses programmatic dependent
- * launch and reads and writes nothing before its wait for the preceding grid,
- * so all inputs, weights too, are read in stream order.
+ * launch, but none reads or writes anything before the kernels that were in the
+ * stream before the call have completed (the later launches of one call may
+ * read weights while an earlier one of it runs), so all inputs, weights too, are
+ * read in stream order.
  */
 #ifndef MXFP4_MOE_GB300_H
 #define MXFP4_MOE_GB300_H
