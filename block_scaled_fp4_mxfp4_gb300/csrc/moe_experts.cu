@@ -1138,7 +1138,15 @@ __global__ void __launch_bounds__(256) moe_gather_kernel(const GatherParams p)
         const int t = __ldcg(p.src + rec.y + r);
         const uint4 *from = reinterpret_cast<const uint4 *>(p.x + static_cast<size_t>(t) * p.ldx);
         uint4 *to = reinterpret_cast<uint4 *>(p.xs + static_cast<size_t>(rec.y + r) * p.H);
-        for (int i = lane; i < p.H / 16; i += 32) to[i] = from[i];
+        for (int i = lane; i < p.H / 16; i += 4 * 32) {
+            uint4 v[4];       // loads ahead of the stores that depend on them
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (i + 32 * j < p.H / 16) v[j] = __ldg(from + i + 32 * j);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (i + 32 * j < p.H / 16) to[i + 32 * j] = v[j];
+        }
         const uint8_t *sf = p.x_sf + static_cast<size_t>(t >> 7) * kc * 512 + (t & 31) * 16 + ((t & 127) >> 5) * 4;
         uint8_t *sfo = p.xs_sf + static_cast<size_t>(tile) * kc * 1024 + (r >> 7) * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4;
         for (int c = lane; c < kc; c += 32)
@@ -1310,7 +1318,7 @@ cudaError_t launch_moe_experts(const MoeArgs &a, const MoeLayout &l, cudaStream_
         g.xs_sf = a.ws + l.xs_sf;
         g.E = a.E;
         g.H = a.H;
-        e = launch_pdl(moe_gather_kernel, dim3(l.max_tiles, 4), dim3(256), 0, stream, g);
+        e = launch_pdl(moe_gather_kernel, dim3(l.max_tiles, 14), dim3(256), 0, stream, g);
         if (e != cudaSuccess) return e;
     }
 
