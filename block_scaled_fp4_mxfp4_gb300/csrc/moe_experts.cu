@@ -435,7 +435,6 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const uint32_t tmem_sf = tmem + Cfg::ACC_COLS;
     // Product 2 starts while product 1 drains, and loads weights meanwhile: product 1
     // let it start only after everything before it had completed, so the tables of the
     // placing kernel and the weights are there; only the activations are not. (Asking L2
@@ -448,7 +447,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
     const int stages = (kc + 1) >> 1;                       // the last one may be half
     const int mw = FIRST ? p.I >> 6 : p.H >> 7;             // weight tiles of an expert
     const int wrows = FIRST ? 2 * p.I : p.H;                // weight rows of an expert
-    // uniform across the warp, for the MMA issuers
+    // uniform across the warp, for the issuers of MMAs and scale copies
     const uint32_t tmem_u = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t wide_desc = sdesc_sw128(smem_u32(smem + Cfg::WIDE_AT));
     const uint64_t token_desc = sdesc_sw128(smem_u32(smem + Cfg::TOKEN_AT));
@@ -686,40 +685,40 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
                 mbar_wait(p_full + r.slot, r.parity, &g_moe_error, kErrWaitDrain);
             }
         }
-    } else if (lane == 0) {
+    } else {
         // ------------------------------------------------------ scales to TMEM
         // cp.async wrote the stage through the generic proxy; the fence here lets the
         // scale copies, and the MMAs that wait for them, read it through the async
         // proxy.
-        const int me = warp - 19;
-        int gs = 0;
+        const int me = warp - 19, total = walk.left() * stages;
+        const uint64_t sf_desc = sdesc_scale(smem_u32(smem + Cfg::TOKEN_AT + Cfg::SFW_OFF));
+        int ks = 0;                    // stage of the tile: the last one may be half
         bool ok = true;
-        while (walk.more() && ok && !*abort_flag) {
-            walk.take();
-            for (int ks = 0; ks < stages; ++ks, ++gs) {
-                if ((gs & 1) != me) continue;
-                const Ring r = ring_at<TOKEN>(gs);
-                ok = mbar_wait(t_full + r.slot, r.parity, &g_moe_error, kErrWaitFull, p.wait_ns);
-                if (!ok) {
-                    *abort_flag = 1;
-                    break;
-                }
-                fence_proxy_async_smem();
-                tc_fence_after();
-                const uint32_t st = smem_u32(smem + Cfg::TOKEN_AT) + r.slot * Cfg::TOKEN_BYTES;
-                const uint32_t tsf = tmem_sf + r.slot * Cfg::SF_COLS;
-                tc_cp_scale_block(tsf, sdesc_scale(st + Cfg::SFW_OFF));
-                tc_cp_scale_block(tsf + 8, sdesc_scale(st + Cfg::SFT_OFF));
+        for (int gs = 0; gs < total; ++gs, ks = ks + 1 == stages ? 0 : ks + 1) {
+            if ((gs & 1) != me) continue;
+            const Ring r = ring_at<TOKEN>(gs);
+            ok = mbar_wait_warp(t_full + r.slot, r.parity, &g_moe_error, kErrWaitFull, p.wait_ns);
+            if (!ok) break;
+            fence_proxy_async_smem();
+            tc_fence_after();
+            const uint64_t sd = sf_desc + static_cast<uint64_t>(r.slot * (Cfg::TOKEN_BYTES >> 4));
+            const uint32_t tsf = tmem_u + Cfg::ACC_COLS + r.slot * Cfg::SF_COLS;
+            if (elect_one()) {
+                tc_cp_scale_block(tsf, sd);
+                tc_cp_scale_block(tsf + 8, sd + 64);
                 if (2 * ks + 1 < kc) {
-                    tc_cp_scale_block(tsf + 4, sdesc_scale(st + Cfg::SFW_OFF + 512));
-                    tc_cp_scale_block(tsf + 12, sdesc_scale(st + Cfg::SFT_OFF + 512));
+                    tc_cp_scale_block(tsf + 4, sd + 32);
+                    tc_cp_scale_block(tsf + 12, sd + 96);
                 }
                 tc_commit(ready + r.slot);
             }
+            __syncwarp();
         }
+        if (!ok) *abort_flag = 1;
         // no copy may be running when TMEM is released
-        tc_commit(cp_done + me);
-        mbar_wait(cp_done + me, 0, &g_moe_error, kErrWaitDrain);
+        if (elect_one()) tc_commit(cp_done + me);
+        __syncwarp();
+        mbar_wait_warp(cp_done + me, 0, &g_moe_error, kErrWaitDrain);
     }
     __syncwarp();
 
