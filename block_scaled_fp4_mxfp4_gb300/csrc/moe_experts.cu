@@ -578,8 +578,6 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     v[i] = *reinterpret_cast<const uint4 *>(src + (i & 3) * 1024 + ((((i >> 2) * 4 + j) ^ row8) << 4));
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_empty + rp.slot);   // the next load may start before the wide slot is free
                 if (gs >= WIDE) {
                     // this barrier cannot complete another round before the stage at
                     // hand has been multiplied (WIDE <= TOKEN)
@@ -597,7 +595,13 @@ __global__ void __launch_bounds__(kSmallThreads, 1) moe_product_small_kernel(con
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(ready + gs % TOKEN);
+                if (lane == 0) {
+                    mbar_arrive(ready + gs % TOKEN);
+                    // Only now: the stores needed the values. Released right after the loads,
+                    // the slot was refilled before some had been executed (the compiler
+                    // sinks them to the stores).
+                    mbar_arrive(p_empty + rp.slot);
+                }
         }
         if (!ok) *abort_flag = 1;
     } else if (warp < 18) {
@@ -931,10 +935,6 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_product_large_kernel(con
                             sf = *reinterpret_cast<const uint4 *>(psf + h * 512);
                         }
                     }
-                    if (h + 1 == halves) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(p_empty + rp.slot);
-                    }
                     if (gs >= OPER)
                         ok = mbar_wait_warp(done + ro.slot, ro.parity ^ 1u, &g_moe_error, kErrWaitEmpty, p.wait_ns);
                     if (!ok) break;
@@ -946,6 +946,11 @@ __global__ void __launch_bounds__(kLargeThreads, 1) moe_product_large_kernel(con
                         *reinterpret_cast<uint2 *>(dst + i * 1024 + s1) = make_uint2(v[i].z, v[i].w);
                     }
                     if (w4 == 0) *reinterpret_cast<uint4 *>(wide + Cfg::WSF_OFF + lane * 16) = sf;
+                    if (h + 1 == halves) {
+                        // only now, when the stores have had the values (see the small tiles)
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(p_empty + rp.slot);
+                    }
                     ok = mbar_wait_warp(t_full + ro.slot, ro.parity, &g_moe_error, kErrWaitFull, p.wait_ns);
                     if (!ok) break;
                     fence_proxy_async_smem();

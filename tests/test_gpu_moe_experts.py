@@ -27,12 +27,18 @@ class Layer:
     def run(self, **kw):
         return mx.mxfp4_moe_experts(self.xq, self.xs, self.ids, self.w, self.w13, self.s13, self.w2, self.s2, **kw)
 
-    def check(self, out, rows=None):
+    def check(self, out, rows=None, long=False):
         torch.cuda.synchronize()
         assert mx.get_device_error() == 0
         ref, bound = moe_ref.experts(self.x, self.ids, self.w, self.v13, self.v2)
-        # the bound (a worst case over all roundings) is itself small beside the results
-        assert float(bound.norm()) <= 0.1 * float(ref.norm()) + 1e-20
+        if long:
+            # over long sums the worst case over all roundings says little: beside it, the norm of the error. A product
+            # row is off by half a step of bf16, 2^-8, and a sum of k of them with signs by chance has a norm of their
+            # absolute values over sqrt(k); the result is rounded once more: 2^-8 (1 + sqrt(k)) <= 2^-6 for k <= 9.
+            assert float((out.double() - ref).norm()) <= 2.0 ** -6 * float(ref.norm())
+        else:
+            # the bound (a worst case over all roundings) is itself small beside the results
+            assert float(bound.norm()) <= 0.1 * float(ref.norm()) + 1e-20
         err = (out.double() - ref).abs()
         rows = slice(None) if rows is None else rows
         worst = float((err / bound)[rows].max())
@@ -61,6 +67,20 @@ class Layer:
 def test_experts_match_their_definition(T, k, E, H, I):
     s = Layer(T, k, E, H, I, seed=T + 10 * k + E)
     s.check(s.run())
+
+
+@pytest.mark.parametrize("T,k,E,H,I", [(1, 8, 8, 7168, 512), (16, 8, 64, 2048, 768), (200, 6, 64, 1024, 1024),
+                                       (600, 4, 8, 4096, 1024), (900, 2, 5, 1280, 1408)])
+def test_many_stages_and_units_give_the_same_bits_every_time(T, k, E, H, I):
+    """Long pipelines over many units, run again and again: whatever is read before it has landed, or overwritten before
+    it was read, changes bits from run to run."""
+    s = Layer(T, k, E, H, I, seed=20)
+    ws = mx.moe_experts_workspace(T, k, E, H, I)
+    first = s.run(workspace=ws).clone()
+    s.check(first, long=True)
+    differ = sum(not torch.equal(s.run(workspace=ws), first) for _ in range(40))
+    torch.cuda.synchronize()
+    assert differ == 0 and mx.get_device_error() == 0
 
 
 def test_choices_left_out():

@@ -89,12 +89,12 @@ def small(rng, units, stages, groups=2, packed=4, wide=3, token=5):
     def widen(group):
         for g in range(group, total, groups):
             yield from wait(p_full[g % packed], g // packed)
-            yield
-            p_empty[g % packed].arrive()
             if g >= wide:
                 yield from wait(done[(g - wide) % token], (g - wide) // token)
             yield
             ready[g % token].arrive()
+            yield
+            p_empty[g % packed].arrive()
 
     def scales(me):
         for g in range(me, total, 2):
@@ -158,11 +158,11 @@ def large(rng, units, kc, groups=3, packed=3, oper=5, scale_threads=1):
                     halves = min(2, kc - 2 * q)
                     for h in range(halves):
                         g = u * kc + 2 * q + h
+                        if g >= oper:
+                            yield from wait(c["done"][g % oper], g // oper - 1)
                         yield
                         if h + 1 == halves:
                             c["p_empty"][pk % packed].arrive()
-                        if g >= oper:
-                            yield from wait(c["done"][g % oper], g // oper - 1)
                         yield from wait(c["t_full"][g % oper], g // oper)
                         yield
                         ready[g % oper].arrive()
