@@ -8,7 +8,8 @@
 // Bound: HBM (2 or 4 bytes read, 1 to 5 written an element; ~12 operations). So
 // each row is read once: a block keeps its row in registers between the sum of
 // squares and the quantization, eight elements (one 16-byte vector) a lane, and
-// four neighbouring lanes hold one block of 32.
+// four neighbouring lanes hold one block of 32. Measured: 4096 x 7168 bf16 with
+// residual, h and y (265 MB) 54 us, 4.9 TB/s; one row 4.3 us.
 //
 // Exactness: an E4M3 rounding turns an fp32 error of 2^-23 into a step of 2^-3 where
 // a value lies next to a midpoint, about one element in a million. So the sum of

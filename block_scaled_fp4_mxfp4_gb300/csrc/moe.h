@@ -34,7 +34,7 @@ struct MoeLayout {
     int nt;                 // tokens of a tile (columns of the accumulator)
     int max_tiles;          // most token tiles T * k choices can need
     int chunks;             // blocks of the placing kernel
-    size_t hist, off, tile0, rec, src, pos, act, act_sf, y, xs, xs_sf, total;
+    size_t hist, tiles, rec, src, pos, act, act_sf, y, xs, xs_sf, total;
 };
 constexpr int kMoeLargeTile = 224;   // nt of the layouts that need sorted token rows
 bool moe_layout(int64_t T, int k, int E, int64_t H, int64_t I, MoeLayout *out);

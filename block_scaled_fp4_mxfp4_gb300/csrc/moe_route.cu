@@ -19,6 +19,10 @@
 // warp's takes 16 clocks or more): scoring whole rows in 64 bits took half of the
 // kernel's time, though it was for so few. Without bias and groups the logits
 // themselves are compared, which is exact.
+//
+// Measured: 16384 x 256 fp32, sigmoid, bias, 4 of 8 groups, 8 experts: 38 us (the
+// logits alone are 2.5 us of HBM time; 29 us without any 64-bit decision); one token
+// 3.9 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
