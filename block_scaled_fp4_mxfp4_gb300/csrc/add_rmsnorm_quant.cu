@@ -13,10 +13,12 @@
 //
 // Exactness: an E4M3 rounding turns an fp32 error of 2^-23 into a step of 2^-3 where
 // a value lies next to a midpoint, about one element in a million. So the sum of
-// squares is carried in two floats (vectors of eight, then error-free additions), r
-// too, and a value within the fp32 error (3 units) of a midpoint, or a block's
-// maximum within it of the border between two scales, is decided again in 64
-// bits. The rule costs three integer instructions an element.
+// squares is carried in two floats (vectors of eight in fp32, then error-free
+// additions), r too, and a value within the fp32 error (3 units) of a midpoint, or a
+// block's maximum within it of the border between two scales, is decided again in 64
+// bits. The rule costs three integer instructions an element. What is left is r's own
+// error of about 2^-28: a value closer than that to a midpoint may still go to
+// either side.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -1,28 +1,34 @@
 // Routing of tokens to experts (moe_route): scores, groups, top k, weights.
 //
 // One warp a token; lane l holds the V experts from V l on in registers. What a
-// token costs is not its E logits (a few hundred bytes) but the selection: k
-// rounds of a warp-wide maximum (redux.sync) over order-preserving integer keys, of
-// which the lowest lane that has it, and there the first expert, is the one of
-// lowest index. A group of experts is a run of lanes where its size allows (a
-// power of two of them); its score then takes a few shuffles, all groups at once.
+// token costs is not its E logits (a few hundred bytes) but the instructions of the
+// selection: k rounds of a warp-wide maximum (redux.sync) over order-preserving
+// integer keys, of which the lowest lane that has it, and there the first expert, is
+// the one of lowest index. A lane enters a round with its best key and keeps its
+// second, so most rounds look at no other key of the lane; which expert a chosen key
+// belongs to, and how close two choices came, is worked out for all k at once after
+// the rounds (a lane a choice). A group of experts is a run of lanes where its size
+// allows (a power of two of them); its score then takes a few shuffles, all groups
+// at once.
 //
 // Exactness. With a bias or groups the choice compares sums s + bias that fp32
 // holds to about 2^-22 only, and two experts of a large batch come closer than
 // that. Every fp32 decision is therefore checked against a margin `tol` that
 // bounds the error of both sides. In units of 2^-24 of max(s, |c|): expf 2, the
-// sum 1 + e or the division 1 each, c itself 1, so 2^-21 for the sigmoid; the
+// sum 1 + e 1, its reciprocal 2 (rcp.approx), c itself 1, so 2^-21 for the sigmoid; the
 // softmax adds 1 for x - max and up to V + 7 for the sum of the row, so 2^-19.
 // Rows with a closer decision (one in a few hundred) are decided again from 64-bit
 // scores of the few experts that fp32 leaves in question: those about the border
 // between two groups, or about the last choice. FP64 instructions are slow here (a
 // warp's takes 16 clocks or more): scoring whole rows in 64 bits took half of the
 // kernel's time, though it was for so few. Without bias and groups the logits
-// themselves are compared, which is exact.
+// themselves are compared, which is exact. The weights are computed with IEEE
+// divisions from the chosen logits.
 //
-// Measured: 16384 x 256 fp32, sigmoid, bias, 4 of 8 groups, 8 experts: 38 us (the
-// logits alone are 2.5 us of HBM time; 29 us without any 64-bit decision); one token
-// 3.9 us.
+// Measured: 16384 x 256 fp32, sigmoid, bias, 4 of 8 groups, 8 experts: 24 us (1200
+// instructions a token, issued in 70 % of the cycles; the logits alone are 2.5 us of
+// HBM time; 21 us without any 64-bit decision; 39 us when each round searched
+// its lane's keys). 3001 x 60: 6.9 us. One token: 3.5 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -188,37 +194,39 @@ __device__ __noinline__ int route_row64(const RouteParams &p, int dtype, int64_t
     return mine;
 }
 
-// The terms of a row's scores in 64 bits.
-struct Row64 {
-    double m, sum;    // softmax: maximum and sum of exponentials
-};
-
+// The 64-bit exponentials exp(z - max) of a softmax row, to `c` [E] (each lane its own V
+// from e0 on), and their sum.
 template <int V>
-__device__ __noinline__ Row64 softmax_terms64(const float (&z)[V])
+__device__ __noinline__ double softmax_terms64(const RouteParams &p, int dtype, int64_t t, int e0, double *c)
 {
     const float kNegInf = -__int_as_float(0x7F800000);
     float m = kNegInf;
-#pragma unroll
-    for (int i = 0; i < V; ++i) m = fmaxf(m, z[i]);
-    Row64 r;
-    r.m = static_cast<double>(warp_max(m));
+    for (int e = e0; e < e0 + V && e < p.E; ++e) m = fmaxf(m, load_logit(p.logits, t * p.ldl + e, dtype));
+    m = warp_max(m);
     double s = 0.0;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-        if (z[i] != kNegInf) s += exp(static_cast<double>(z[i]) - r.m);
-    r.sum = warp_sum(s);
-    return r;
+    for (int e = e0; e < e0 + V && e < p.E; ++e) {
+        const float z = load_logit(p.logits, t * p.ldl + e, dtype);
+        const double x = z == kNegInf ? 0.0 : exp(static_cast<double>(z) - m);
+        c[e] = x;
+        s += x;
+    }
+    return warp_sum(s);
 }
 
 // Score + bias of expert e in 64 bits, as a monotone integer key (finite values).
-__device__ __noinline__ unsigned long long exact_key64(const RouteParams &p, int dtype, int64_t t, int e, Row64 r)
+// `terms`, `sum`: of a softmax row, from softmax_terms64.
+__device__ __noinline__ unsigned long long exact_key64(const RouteParams &p, int dtype, int64_t t, int e, double sum,
+                                                       const double *terms)
 {
-    const double z = load_logit(p.logits, t * p.ldl + e, dtype);
-    double c = p.sigmoid ? 1.0 / (1.0 + exp(-z)) : exp(z - r.m) / r.sum;
+    double c;
+    if (p.sigmoid)
+        c = 1.0 / (1.0 + exp(-static_cast<double>(load_logit(p.logits, t * p.ldl + e, dtype))));
+    else
+        c = terms[e] / sum;
     if (p.bias) c += static_cast<double>(p.bias[e]);
     if (c == 0.0) c = 0.0;
-    const unsigned long long b = __double_as_longlong(c);
-    return (b >> 63) ? ~b : (b | 0x8000000000000000ull);
+    const unsigned long long u = __double_as_longlong(c);
+    return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
 }
 __device__ __forceinline__ double value64(unsigned long long k)
 {
@@ -235,9 +243,44 @@ __device__ __forceinline__ unsigned long long warp_max64(unsigned long long k, i
     return (static_cast<unsigned long long>(hi) << 32) | lo;
 }
 
+// 1 / x to one unit in the last place; results below 2^-126 become 0.
+__device__ __forceinline__ float reciprocal_approx(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// key32 of what is neither NaN nor -0
+__device__ __forceinline__ uint32_t key32_plain(float v)
+{
+    const uint32_t b = __float_as_uint(v);
+    return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+}
+
 __device__ __forceinline__ float value_of(uint32_t k)   // inverse of key32
 {
     return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
+
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// The two largest keys of a lane.
+template <int V>
+__device__ __forceinline__ void best_two(const uint32_t (&key)[V], uint32_t &k1, uint32_t &k2)
+{
+    k1 = key[0];
+    k2 = 0u;
+#pragma unroll
+    for (int i = 1; i < V; ++i) {
+        k2 = max(k2, min(k1, key[i]));
+        k1 = max(k1, key[i]);
+    }
 }
 
 // The V logits from element i on (E of them in the row from column e): by 16-byte
@@ -276,8 +319,9 @@ __device__ __forceinline__ void load_row(const RouteParams &p, int64_t t, int e,
 }
 
 // V: experts a lane, E <= 32 V.
+// Eight blocks an SM hold 64 registers a thread: 25.0 us against 26.6 us of five (16384 x 256).
 template <int V, int DTYPE>
-__global__ void __launch_bounds__(128) moe_route_kernel(const RouteParams p)
+__global__ void __launch_bounds__(128, V <= 8 ? 8 : 5) moe_route_kernel(const RouteParams p)
 {
     extern __shared__ double smem_route[];
     grid_dependency_wait();
@@ -318,37 +362,42 @@ __global__ void __launch_bounds__(128) moe_route_kernel(const RouteParams p)
         bool open = false;         // a decision closer than fp32 can tell
         bool open_groups = false;  // such a one between groups that are no runs of lanes, or a value without order
         float tol = 0.0f;
-        Row64 row64{0.0, 1.0};
+        double sum64 = 1.0;
         bool have64 = false;
         if (by_logit) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) key[i] = e0 + i < p.E ? key32(z[i]) : 0u;
+            for (int i = 0; i < V; ++i) key[i] = key32(z[i]);
         } else {
-            bool odd = false;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float s = score(z[i]);
+            auto set = [&](int i, float s) {
                 const float c = z[i] == kNegInf ? kNegInf : s + bias[i];
-                odd |= !(c < 1e30f);
-                if (c > kNegInf) tol = fmaxf(tol, fmaxf(s, fabsf(c)));
-                key[i] = e0 + i < p.E ? key32(c) : 0u;
+                const float size = max_nan(s, fabsf(c));
+                tol = max_nan(tol, c == kNegInf ? 0.0f : size);
+                key[i] = key32_plain(c);   // a NaN shows in tol; s + bias is no -0
+            };
+            if (p.sigmoid) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) set(i, reciprocal_approx(1.0f + expf(-z[i])));
+            } else {
+                const float rsum = 1.0f / sum;
+#pragma unroll
+                for (int i = 0; i < V; ++i) set(i, expf(z[i] - zmax) * rsum);
             }
-            // tol >= 0, so its bits order as it does
-            tol = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(tol))) * (p.sigmoid ? 0x1p-21f : 0x1p-19f);
-            open_groups = __any_sync(kAll, odd) || !(tol < 1e20f);
+            // tol >= 0 or the largest NaN, so its bits order as it does; 2^-125 stands for scores that became 0
+            tol = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(tol))) * (p.sigmoid ? 0x1p-21f : 0x1p-19f) +
+                  0x1p-125f;
+            open_groups = !(tol < 1e20f);
         }
+        // this lane's two best keys that are left; a second of 0 stands for "not known"
+        uint32_t mine = 0u, next = 0u;
+        bool in = true;        // this lane's experts may be chosen
+        best_two<V>(key, mine, next);
         if (p.groups > 1 && !open_groups) {
             // A group's two best keys, in every lane of the group (`run` lanes of it, from
             // a multiple of run on), or group g's in lane g, g + 32, ...
             uint32_t kept = 0u;       // groups of this lane that stay: bit 0, or bit i for group lane + 32 i
             const int run = p.group_lanes;
             if (run > 0) {
-                uint32_t k1 = 0u, k2 = 0u;
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    k2 = max(k2, min(k1, key[i]));
-                    k1 = max(k1, key[i]);
-                }
+                uint32_t k1 = mine, k2 = next;
                 for (int o = 1; o < run; o <<= 1) {
                     const uint32_t a1 = __shfl_xor_sync(kAll, k1, o), a2 = __shfl_xor_sync(kAll, k2, o);
                     k2 = max(max(k2, a2), min(k1, a1));
@@ -356,35 +405,43 @@ __global__ void __launch_bounds__(128) moe_route_kernel(const RouteParams p)
                 }
                 const float gs = value_of(k1) + (p.group_top == 2 && n > 1 ? value_of(k2) : 0.0f);
                 const bool real = e0 < p.E;
-                const uint32_t mine = real ? key32(gs) : 0u;
-                int rank = 0;         // groups before this one
-                for (int g = 0; g < p.groups; ++g) {
-                    const uint32_t other = __shfl_sync(kAll, mine, g * run);
-                    rank += other > mine || (other == mine && g * run < (lane & ~(run - 1)));
+                const uint32_t group = real ? key32(gs) : 0u;
+                // groups before this one: each lane of a group compares it with every run-th
+                // group, and the lanes add up
+                const int sub = lane & (run - 1), base = lane - sub;
+                int rank = 0;
+                for (int g0 = 0; g0 < p.groups; g0 += run) {
+                    const int from = (g0 + sub) * run;
+                    const uint32_t other = __shfl_sync(kAll, group, from & 31);
+                    rank += g0 + sub < p.groups && (other > group || (other == group && from < base));
                 }
+                for (int o = 1; o < run; o <<= 1) rank += __shfl_xor_sync(kAll, rank, o);
                 kept = real && rank < p.topk_groups;
                 // the worst that stays against the best that goes; sums of two carry twice the error
-                const uint32_t low = __reduce_min_sync(kAll, kept ? mine : 0xFFFFFFFFu);
-                const uint32_t high = __reduce_max_sync(kAll, real && !kept ? mine : 0u);
+                const uint32_t low = __reduce_min_sync(kAll, kept ? group : 0xFFFFFFFFu);
+                const uint32_t high = __reduce_max_sync(kAll, real && !kept ? group : 0u);
                 if (high > kKeyNegInf && !(value_of(low) - value_of(high) > 4.0f * tol)) {
                     // In question: the groups that stay by less than the error over the best that
                     // goes, and those that go by less under the worst that stays. Their exact
                     // scores come from the experts that may be among their best.
                     if (!p.sigmoid && !have64) {
-                        row64 = softmax_terms64<V>(z);
+                        sum64 = softmax_terms64<V>(p, DTYPE, t, e0, c64);
                         have64 = true;
                     }
-                    const bool asked = real && mine > kKeyNegInf &&
+                    const bool asked = real && group > kKeyNegInf &&
                                        (kept ? gs <= value_of(high) + 4.0f * tol : gs >= value_of(low) - 4.0f * tol);
                     const float from = value_of(p.group_top == 2 && n > 1 ? k2 : k1) - 2.0f * tol;
                     unsigned long long d1 = 0, d2 = 0;
+                    uint32_t todo = 0u;
 #pragma unroll
                     for (int i = 0; i < V; ++i)
-                        if (asked && e0 + i < p.E && key[i] > kKeyNegInf && value_of(key[i]) >= from) {
-                            const unsigned long long x = exact_key64(p, DTYPE, t, e0 + i, row64);
-                            d2 = max(d2, min(d1, x));
-                            d1 = max(d1, x);
-                        }
+                        if (asked && key[i] > kKeyNegInf && value_of(key[i]) >= from) todo |= 1u << i;
+                    for (; todo; todo &= todo - 1) {
+                        const unsigned long long x = exact_key64(p, DTYPE, t, e0 + __ffs(todo) - 1, sum64, c64);
+                        d2 = max(d2, min(d1, x));
+                        d1 = max(d1, x);
+                    }
+                    __syncwarp();
                     for (int o = 1; o < run; o <<= 1) {
                         const unsigned long long a1 = __shfl_xor_sync(kAll, d1, o), a2 = __shfl_xor_sync(kAll, d2, o);
                         d2 = max(max(d2, a2), min(d1, a1));
@@ -398,13 +455,12 @@ __global__ void __launch_bounds__(128) moe_route_kernel(const RouteParams p)
                     for (int g = 0; g < p.groups; ++g) {
                         const double other = __shfl_sync(kAll, exact, g * run);
                         const bool is = __shfl_sync(kAll, asked, g * run);
-                        before += is && (other > exact || (other == exact && g * run < (lane & ~(run - 1))));
+                        before += is && (other > exact || (other == exact && g * run < base));
                     }
                     if (asked) kept = before < places;
                 }
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (!kept && e0 + i < p.E) key[i] = kKeyNegInf;
+                in = kept;
+                if (!in) mine = next = 0u;
             } else {
                 // groups that are no runs of lanes: one lane a group, through shared memory
                 float *cs = reinterpret_cast<float *>(c64);
@@ -454,52 +510,69 @@ __global__ void __launch_bounds__(128) moe_route_kernel(const RouteParams p)
                     const uint32_t bits = __shfl_sync(kAll, kept, g & 31);
                     if (e0 + i < p.E && !(bits >> (g >> 5) & 1)) key[i] = kKeyNegInf;
                 }
+                best_two<V>(key, mine, next);
             }
         }
         int id = -1;               // lane j < k: the j-th choice
         float least = kNegInf;     // value of the last choice
         if (!open_groups) {
-            uint32_t taken = 0u;   // bit i: this lane's expert i is chosen
-            uint32_t mine = 0u;    // this lane's best key that is left
-#pragma unroll
-            for (int i = 0; i < V; ++i) mine = max(mine, key[i]);
-            uint32_t prev = 0xFFFFFFFFu;
-            for (int j = 0; j <= p.k; ++j) {
+            // lane j notes the j-th choice: its key, its lane, and how many of that lane's
+            // equal keys went before (equal keys of one lane go one after another)
+            uint32_t chosen = 0u, prev = 0u;
+            int from = 0, dup = 0, prev_lane = -1, nth = 0, j = 0;
+            for (; j < p.k; ++j) {
                 const uint32_t m = __reduce_max_sync(kAll, mine);
                 if (m <= kKeyNegInf) break;    // nothing is left
-                if (!by_logit) {
-                    if (j > 0 && !(value_of(prev) - value_of(m) > 2.0f * tol)) open = true;
-                    prev = m;
-                }
-                if (j == p.k) break;
-                least = value_of(m);
                 const int winner = __ffs(__ballot_sync(kAll, mine == m)) - 1;
-                int at = 0;
-                if (lane == winner) {
-                    mine = 0u;
-#pragma unroll
-                    for (int i = V - 1; i >= 0; --i)
-                        if (key[i] == m && !(taken >> i & 1)) at = i;
-                    taken |= 1u << at;
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        if (!(taken >> i & 1)) mine = max(mine, key[i]);
+                dup = m == prev && winner == prev_lane ? dup + 1 : 0;
+                prev = m;
+                prev_lane = winner;
+                if (lane == j) {
+                    chosen = m;
+                    from = winner;
+                    nth = dup;
                 }
-                const int e = __shfl_sync(kAll, e0 + at, winner);
-                if (lane == j) id = e;
+                if (lane == winner) {
+                    mine = next;
+                    next = 0u;
+                    if (mine == 0u) {
+                        int equal = 0;
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            equal += key[i] == m;
+                            if (key[i] < m) mine = max(mine, key[i]);
+                        }
+                        if (equal > dup + 1) mine = m;
+                    }
+                }
+                __syncwarp();
             }
+            if (j > 0) least = value_of(prev);
+            if (!by_logit) {
+                // each choice against the one after it, the last against the best that is left
+                uint32_t after = __shfl_down_sync(kAll, chosen, 1);
+                const uint32_t rest = j == p.k ? __reduce_max_sync(kAll, mine) : 0u;
+                if (lane == j - 1) after = rest;
+                open = __any_sync(kAll, lane < j && after > kKeyNegInf &&
+                                            !(value_of(chosen) - value_of(after) > 2.0f * tol));
+            }
+            int at = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (__shfl_sync(kAll, key[i], from) == chosen && nth-- == 0) at = i;
+            if (lane < j) id = from * V + at;
         }
         if (open && !open_groups) {
             // the candidates: what lies within the error of the last choice, or above
-            if (!p.sigmoid && !have64) row64 = softmax_terms64<V>(z);
+            if (!p.sigmoid && !have64) sum64 = softmax_terms64<V>(p, DTYPE, t, e0, c64);
             unsigned long long *k64 = reinterpret_cast<unsigned long long *>(c64) + e0;   // this lane's own
             uint32_t left = 0u;
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                if (e0 + i < p.E && key[i] > kKeyNegInf && value_of(key[i]) >= least - 2.0f * tol) left |= 1u << i;
+                if (in && key[i] > kKeyNegInf && value_of(key[i]) >= least - 2.0f * tol) left |= 1u << i;
             for (uint32_t todo = left; todo; todo &= todo - 1) {
                 const int i = __ffs(todo) - 1;
-                k64[i] = exact_key64(p, DTYPE, t, e0 + i, row64);
+                k64[i] = exact_key64(p, DTYPE, t, e0 + i, sum64, c64);
             }
             __syncwarp();
             id = -1;
@@ -526,9 +599,9 @@ __global__ void __launch_bounds__(128) moe_route_kernel(const RouteParams p)
         float w = 0.0f;
         if (id >= 0) w = score(load_logit(p.logits, t * p.ldl + id, DTYPE));
         if (p.renorm) {
-            // the sum in the order of the choices
-            float total = 0.0f;
-            for (int j = 0; j < p.k; ++j) total += __shfl_sync(kAll, w, j);
+            // in pairs: every lane that writes has the same sum
+            float total = w;
+            for (int o = 1; o < p.k; o <<= 1) total += __shfl_xor_sync(kAll, total, o);
             w = w / (total + 1e-20f);
         }
         if (lane < p.k) {

@@ -63,6 +63,30 @@ def test_route_equal_scores_take_the_lower_index():
     assert mx.moe_route(z, 3)[0][0].tolist() == [0, 1, 2]
 
 
+@pytest.mark.parametrize("E", [24, 64, 128, 256, 512])
+def test_route_many_equal_keys_of_neighbours(E):
+    """Three values only, so runs of experts tie within and across the lanes of a warp."""
+    z = logits(12, E, seed=E).round().clamp(-1, 1)
+    z[0] = 1.0
+    z[1, : E // 2] = -math.inf
+    for score in ("softmax", "sigmoid"):
+        for k in (1, 9, 20):
+            check(z, k, score)
+            check(z, k, score, torch.ones(E, device="cuda"))
+            check(z, min(k, 2 * (E // 8)), score, None, 8, 2, 2)
+
+
+def test_route_scores_below_the_normal_range():
+    """Sigmoids of logits below -87 are subnormal or zero in fp32."""
+    z = -86.5 - logits(20, 64, seed=3, spread=1.0).abs() * 2
+    z[10:] -= 30
+    for bias in (None, torch.zeros(64, device="cuda")):
+        for args in ((), (8, 3, 2), (16, 2, 1)):
+            ids, _ = mx.moe_route(z, 6, "sigmoid", bias, *args, renormalize=False)
+            ri, _ = moe_ref.route(z, 6, "sigmoid", bias, *((args or (1, 1, 2))), False, 1.0)
+            assert torch.equal(ids.cpu(), ri)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_route_scores_closer_than_fp32(score):
     """Sums s + bias that fp32 cannot order: neighbours a few 2^-28 apart."""
