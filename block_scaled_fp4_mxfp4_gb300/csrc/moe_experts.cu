@@ -185,7 +185,7 @@ struct ProductParams {
     uint16_t *y;            // product 2: [rows, H] bf16
     const int *tiles, *src;
     const int4 *rec;
-    int E, H, I;
+    int H, I;
     uint64_t wait_ns;
 };
 
@@ -1333,7 +1333,6 @@ cudaError_t launch_moe_experts(const MoeArgs &a, const MoeLayout &l, cudaStream_
     p.tiles = pp.tiles;
     p.src = pp.src;
     p.rec = pp.rec;
-    p.E = a.E;
     p.H = a.H;
     p.I = a.I;
     p.wait_ns = wait_limit_ns();
