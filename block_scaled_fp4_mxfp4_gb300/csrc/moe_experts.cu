@@ -14,9 +14,12 @@
 //            before it.
 //   gather   long batches only: token rows and their scales in sorted order
 //   product1 epilogue silu(g) * u, MXFP8, to the workspace in sorted order
-//   product2 act x W2^T, bf16 rows to the workspace
+//   product2 act x W2^T, fp32 rows to the workspace
 //   combine  out_t = sum_j w_tj row[pos[t, j]], in the order of j: no atomics, so
-//            the result does not depend on the order of the sorted rows
+//            the result does not depend on the order of the sorted rows. The rows are
+//            the accumulators as they are, so the sum is rounded once, to bf16; rows
+//            of half the size would make the error of the result 1.4 times that
+//            of this rounding, and more where experts cancel
 //
 // Both products swap the operands: the 128 rows of the MMA are weight rows, its
 // columns are tokens. Weights, which dominate the traffic of a small batch, fill
@@ -182,7 +185,7 @@ struct ProductParams {
     const uint8_t *x_sf;    // product 1: blocked scales of Xq
     uint8_t *act;           // [rows, I] E4M3 (product 1 writes, product 2 reads through tm_t)
     uint8_t *act_sf;        // [tiles][I / 128][NT / 128 rounded up][512]
-    uint16_t *y;            // product 2: [rows, H] bf16
+    float *y;               // product 2: [rows, H]
     const int *tiles, *src;
     const int4 *rec;
     int H, I;
@@ -250,7 +253,7 @@ __device__ __forceinline__ Ring ring_at(int i)
 }
 
 // Stores the 32 accumulator columns (tokens) v of one weight row (channel) a thread:
-// product 2 as bf16 from registers; product 1 as MXFP8 of silu(g) * u, staged 16
+// product 2 as it is, from registers; product 1 as MXFP8 of silu(g) * u, staged 16
 // columns at a time through shared memory so that a thread gets neighbouring
 // channels of one token. Called by the 128 epilogue threads; c0: first column,
 // below w.rows.
@@ -260,20 +263,11 @@ __device__ __forceinline__ void store_columns(const uint32_t (&v)[32], float *ep
 {
     const int t = threadIdx.x & 127;
     if constexpr (!FIRST) {
-        // neighbouring lanes hold neighbouring channels: an even lane takes the pair of
-        // an even column, its neighbour that of the next, so a warp stores 64 bytes
-        // of each of two tokens at a time
-        const int odd = t & 1;
-        __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16 *>(p.y) + (static_cast<size_t>(w.row0) + c0) * p.H + 128 * w.m +
-                           (t & ~1);
+        // neighbouring lanes hold neighbouring channels: a warp stores 128 bytes of a token
+        float *o = p.y + (static_cast<size_t>(w.row0) + c0) * p.H + 128 * w.m + t;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const float mine = __uint_as_float(odd ? v[2 * j + 1] : v[2 * j]);
-            const float other = __uint_as_float(__shfl_xor_sync(0xffffffffu, odd ? v[2 * j] : v[2 * j + 1], 1));
-            if (c0 + 2 * j + odd < w.rows)
-                *reinterpret_cast<__nv_bfloat162 *>(o + static_cast<size_t>(2 * j + odd) * p.H) =
-                    odd ? __floats2bfloat162_rn(other, mine) : __floats2bfloat162_rn(mine, other);
-        }
+        for (int j = 0; j < 32; ++j)
+            if (c0 + j < w.rows) o[static_cast<size_t>(j) * p.H] = __uint_as_float(v[j]);
         return;
     }
     const int col = t >> 3, part = t & 7;      // this thread's column and eighth of the staged rows
@@ -1158,7 +1152,7 @@ __global__ void __launch_bounds__(256) moe_gather_kernel(const GatherParams p)
 // ------------------------------------------------------------------ combine
 
 struct CombineParams {
-    const uint16_t *y;
+    const float *y;
     const int *pos;
     const float *weights;
     uint16_t *out;
@@ -1166,30 +1160,27 @@ struct CombineParams {
     int k, H;
 };
 
-// out[t] = sum_j w[t, j] * y[pos[t, j]]: eight channels a thread, one token a block row.
+// out[t] = sum_j w[t, j] * y[pos[t, j]]: four channels a thread, one token a block row.
 __global__ void __launch_bounds__(256) moe_combine_kernel(const CombineParams p)
 {
     grid_dependency_wait();
     grid_launch_dependents();
     const int64_t t = blockIdx.x;
-    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * 8;
+    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * 4;
     if (c >= p.H) return;
-    float acc[8] = {};
+    float acc[4] = {};
     for (int j = 0; j < p.k; ++j) {
         const int r = __ldcg(p.pos + t * p.k + j);
         if (r < 0) continue;
         const float w = p.weights[t * p.k + j];
-        const uint4 v = __ldcg(reinterpret_cast<const uint4 *>(p.y + static_cast<size_t>(r) * p.H + c));
-        const uint32_t *pv = &v.x;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            acc[2 * i] = fmaf(w, __uint_as_float(pv[i] << 16), acc[2 * i]);
-            acc[2 * i + 1] = fmaf(w, __uint_as_float(pv[i] & 0xFFFF0000u), acc[2 * i + 1]);
-        }
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.y + static_cast<size_t>(r) * p.H + c));
+        acc[0] = fmaf(w, v.x, acc[0]);
+        acc[1] = fmaf(w, v.y, acc[1]);
+        acc[2] = fmaf(w, v.z, acc[2]);
+        acc[3] = fmaf(w, v.w, acc[3]);
     }
-    const __nv_bfloat162 h[4] = {__floats2bfloat162_rn(acc[0], acc[1]), __floats2bfloat162_rn(acc[2], acc[3]),
-                                 __floats2bfloat162_rn(acc[4], acc[5]), __floats2bfloat162_rn(acc[6], acc[7])};
-    *reinterpret_cast<uint4 *>(p.out + t * p.ldo + c) = *reinterpret_cast<const uint4 *>(h);
+    const __nv_bfloat162 h[2] = {__floats2bfloat162_rn(acc[0], acc[1]), __floats2bfloat162_rn(acc[2], acc[3])};
+    *reinterpret_cast<uint2 *>(p.out + t * p.ldo + c) = *reinterpret_cast<const uint2 *>(h);
 }
 
 // ------------------------------------------------------------------- launch
@@ -1277,7 +1268,7 @@ bool moe_layout(int64_t T, int k, int E, int64_t H, int64_t I, MoeLayout *out)
     out->pos = take(static_cast<size_t>(R) * 4);
     out->act = take(static_cast<size_t>(R) * I);
     out->act_sf = take(static_cast<size_t>(out->max_tiles) * (I / 128) * ((out->nt + 127) / 128) * 512);
-    out->y = take(static_cast<size_t>(R) * H * 2);
+    out->y = take(static_cast<size_t>(R) * H * 4);
     out->xs = take(out->nt == kLargeNT ? static_cast<size_t>(R) * H : 0);
     out->xs_sf = take(out->nt == kLargeNT ? static_cast<size_t>(out->max_tiles) * (H / 128) * 1024 : 0);
     out->total = at;
@@ -1329,7 +1320,7 @@ cudaError_t launch_moe_experts(const MoeArgs &a, const MoeLayout &l, cudaStream_
     p.x_sf = a.x_sf;
     p.act = a.ws + l.act;
     p.act_sf = a.ws + l.act_sf;
-    p.y = reinterpret_cast<uint16_t *>(a.ws + l.y);
+    p.y = reinterpret_cast<float *>(a.ws + l.y);
     p.tiles = pp.tiles;
     p.src = pp.src;
     p.rec = pp.rec;
@@ -1365,7 +1356,7 @@ cudaError_t launch_moe_experts(const MoeArgs &a, const MoeLayout &l, cudaStream_
     c.ldo = a.ldo;
     c.k = a.k;
     c.H = a.H;
-    return launch_pdl(moe_combine_kernel, dim3(static_cast<unsigned>(a.T), (a.H / 8 + 255) / 256), dim3(256), 0, stream, c);
+    return launch_pdl(moe_combine_kernel, dim3(static_cast<unsigned>(a.T), (a.H / 4 + 255) / 256), dim3(256), 0, stream, c);
 }
 
 int read_and_clear_moe_error()

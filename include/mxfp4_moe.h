@@ -90,7 +90,7 @@ MXFP4_API mxfp4_status_t moe_route(const void *logits, int dtype, int64_t ldl, i
 MXFP4_API size_t mxfp4_moe_experts_workspace_bytes(int64_t T, int k, int E, int64_t H, int64_t I);
 
 /* The experts' products of a mixture-of-experts layer: for every token t
- *   out[t] = bf16_rne( sum_j weights[t, j] * bf16_rne( act_j . W2[e]^T ) ),  e = ids[t, j],
+ *   out[t] = bf16_rne( sum_j weights[t, j] * ( act_j . W2[e]^T ) ),  e = ids[t, j],
  *   act_j  = MXFP8( silu(x_t . G[e]^T) * (x_t . U[e]^T) ),   silu(g) = g / (1 + exp(-g)),
  * summed in the order of j in fp32; all products accumulate in fp32 on the
  * tensor cores (tcgen05.mma kind::mxf8f6f4). A choice whose id is outside
