@@ -5,7 +5,14 @@ current CUDA stream to the library entry point of the same name and raises
 ``Mxfp4Error`` on a non-OK status. All arithmetic runs in the library's CUDA
 kernels; there is no fallback. If the library has not been built, importing
 this module raises immediately.
+
+``stream`` (default: the current one) is where a call's kernels run. Work that
+made its inputs, and work that reads its outputs, is put in order with it by the
+caller, as for any torch work on a side stream. What the caller leaves to the call
+to allocate (outputs, workspace) comes from that stream's memory, so nothing on
+another stream is given it while the kernels run.
 """
+import contextlib
 import ctypes
 import os
 import re
@@ -163,6 +170,24 @@ def _stream_ptr(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _scratch(make, n: int, device, stream):
+    """A byte buffer for the kernels of one call, from the memory of the stream they run on: the call may drop it as soon
+    as they are enqueued."""
+    with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+        return make(n, dtype=torch.uint8, device=device)
+
+
+def _output(shape, dtype, device, stream):
+    """An output of a call, likewise; it is meant for the caller's stream too, which may still read it when it is dropped
+    there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _dev(t: torch.Tensor, name: str, dtype=None, ndim=None):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -190,6 +215,11 @@ def new_workspace(M: int, N: int, K: int, device="cuda") -> torch.Tensor:
     return torch.zeros(max(1, workspace_bytes(M, N, K)), dtype=torch.uint8, device=device)
 
 
+def _gemm_workspace(M, N, K, device, stream):
+    # zero-filled on the stream that uses it
+    return _scratch(torch.zeros, max(1, workspace_bytes(M, N, K)), device, stream)
+
+
 # --------------------------------------------------------- quantization --
 
 def _quant(fn, vec, A, Aq, A_sf, stream, where):
@@ -198,9 +228,9 @@ def _quant(fn, vec, A, Aq, A_sf, stream, where):
     if Aq is None:
         # row stride rounded up to 16 bytes so Aq can feed the TMA-based GEMMs
         ld = (K // 2 + 15) // 16 * 16
-        Aq = torch.empty((M, ld), dtype=torch.uint8, device=A.device)[:, :K // 2]
+        Aq = _output((M, ld), torch.uint8, A.device, stream)[:, :K // 2]
     if A_sf is None:
-        A_sf = torch.empty(max(1, sf_bytes(M, K, vec)), dtype=torch.uint8, device=A.device)
+        A_sf = _output(max(1, sf_bytes(M, K, vec)), torch.uint8, A.device, stream)
     _dev(Aq, "Aq", torch.uint8, 2)
     _dev(A_sf, "A_sf", torch.uint8)
     _check(fn(A.data_ptr(), M, K, A.stride(0), Aq.data_ptr(), Aq.stride(0), A_sf.data_ptr(),
@@ -230,9 +260,9 @@ def mxfp4_rmsnorm_quantize(X, weight, eps: float = 1e-6, Aq=None, A_sf=None, str
         raise ValueError("weight must be a contiguous [K] bf16 tensor")
     if Aq is None:
         ld = (K // 2 + 15) // 16 * 16
-        Aq = torch.empty((M, ld), dtype=torch.uint8, device=X.device)[:, :K // 2]
+        Aq = _output((M, ld), torch.uint8, X.device, stream)[:, :K // 2]
     if A_sf is None:
-        A_sf = torch.empty(max(1, sf_bytes(M, K, 32)), dtype=torch.uint8, device=X.device)
+        A_sf = _output(max(1, sf_bytes(M, K, 32)), torch.uint8, X.device, stream)
     _dev(Aq, "Aq", torch.uint8, 2)
     _dev(A_sf, "A_sf", torch.uint8)
     if not stats:
@@ -240,8 +270,8 @@ def mxfp4_rmsnorm_quantize(X, weight, eps: float = 1e-6, Aq=None, A_sf=None, str
                                            Aq.data_ptr(), Aq.stride(0), A_sf.data_ptr(), _stream_ptr(stream)),
                "mxfp4_rmsnorm_quantize")
         return Aq, A_sf
-    rstd = torch.empty(M, dtype=torch.float32, device=X.device)
-    sumsq = torch.empty(M, dtype=torch.float64, device=X.device)
+    rstd = _output(M, torch.float32, X.device, stream)
+    sumsq = _output(M, torch.float64, X.device, stream)
     _check(_lib.mxfp4_rmsnorm_quantize_ex(X.data_ptr(), M, K, X.stride(0), weight.data_ptr(), float(eps),
                                           Aq.data_ptr(), Aq.stride(0), A_sf.data_ptr(), rstd.data_ptr(),
                                           sumsq.data_ptr(), _stream_ptr(stream)),
@@ -257,9 +287,9 @@ def mxfp4_gemm_a4w4(Aq, A_sf, Bq, B_sf, K: int, C=None, workspace=None, stream=N
     _dev(Bq, "Bq", torch.uint8, 2)
     M, N = Aq.shape[0], Bq.shape[0]
     if C is None:
-        C = torch.empty((M, N), dtype=torch.bfloat16, device=Aq.device)
+        C = _output((M, N), torch.bfloat16, Aq.device, stream)
     if workspace is None:
-        workspace = new_workspace(M, N, K, Aq.device)
+        workspace = _gemm_workspace(M, N, K, Aq.device, stream)
     _dev(C, "C", torch.bfloat16, 2)
     _check(_lib.mxfp4_gemm_a4w4(Aq.data_ptr(), Aq.stride(0), A_sf.data_ptr(), Bq.data_ptr(),
                                 Bq.stride(0), B_sf.data_ptr(), C.data_ptr(), C.stride(0), M, N, K,
@@ -277,14 +307,14 @@ def mxfp4_gemm_a4w4_ex(Aq, A_sf, Bq, B_sf, K: int, C=None, alpha: float = 1.0, b
     if C is None:
         if beta != 0.0:
             raise ValueError("beta != 0 needs the input C")
-        C = torch.empty((M, N), dtype=torch.bfloat16, device=Aq.device)
+        C = _output((M, N), torch.bfloat16, Aq.device, stream)
     _dev(C, "C", torch.bfloat16, 2)
     if bias is not None:
         _dev(bias, "bias", torch.bfloat16, 1)
         if bias.numel() != N:
             raise ValueError(f"bias must have N = {N} elements")
     if workspace is None:
-        workspace = new_workspace(M, N, K, Aq.device)
+        workspace = _gemm_workspace(M, N, K, Aq.device, stream)
     _check(_lib.mxfp4_gemm_a4w4_ex(Aq.data_ptr(), Aq.stride(0), A_sf.data_ptr(), Bq.data_ptr(), Bq.stride(0),
                                    B_sf.data_ptr(), C.data_ptr(), C.stride(0), M, N, K, float(alpha), float(beta),
                                    bias.data_ptr() if bias is not None else None, workspace.data_ptr(),
@@ -314,9 +344,9 @@ def mxfp4_quant_gemm_fused(A, Bq, B_sf, C=None, workspace=None, stream=None):
     M, K = A.shape
     N = Bq.shape[0]
     if C is None:
-        C = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+        C = _output((M, N), torch.bfloat16, A.device, stream)
     if workspace is None:
-        workspace = new_workspace(M, N, K, A.device)
+        workspace = _gemm_workspace(M, N, K, A.device, stream)
     _dev(C, "C", torch.bfloat16, 2)
     _check(_lib.mxfp4_quant_gemm_fused(A.data_ptr(), A.stride(0), Bq.data_ptr(), Bq.stride(0),
                                        B_sf.data_ptr(), C.data_ptr(), C.stride(0), M, N, K,
@@ -332,7 +362,7 @@ def nvfp4_quant_gemm_fused(A, Bq, B_sf, C=None, stream=None):
     M, K = A.shape
     N = Bq.shape[0]
     if C is None:
-        C = torch.empty((M, N), dtype=torch.float16, device=A.device)
+        C = _output((M, N), torch.float16, A.device, stream)
     _dev(C, "C", torch.float16, 2)
     _check(_lib.nvfp4_quant_gemm_fused(A.data_ptr(), A.stride(0), Bq.data_ptr(), Bq.stride(0), B_sf.data_ptr(),
                                        C.data_ptr(), C.stride(0), M, N, K, _stream_ptr(stream)),
@@ -360,11 +390,11 @@ def make_mx_problems(groups):
     return make_nv_problems(groups, MxProblem)
 
 
-def group_workspace(num_groups: int, device="cuda", nvfp4: bool = True):
-    """Workspace for a grouped GEMM of num_groups problems (None when none is
-    needed: up to 16 problems travel in kernel parameters)."""
+def group_workspace(num_groups: int, device="cuda", nvfp4: bool = True, stream=None):
+    """Workspace for a grouped GEMM of num_groups problems, on `stream` (None when
+    none is needed: up to 16 problems travel in kernel parameters)."""
     n = int((_lib.nvfp4_group_workspace_bytes if nvfp4 else _lib.mxfp4_group_workspace_bytes)(num_groups))
-    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+    return _scratch(torch.empty, n, device, stream) if n else None
 
 
 def _ws_args(workspace):
@@ -376,7 +406,7 @@ def mxfp4_group_gemm(groups, problems=None, workspace=None, stream=None):
     if problems is None:
         problems = make_mx_problems(groups)
     if workspace is None and len(problems) > NVFP4_MAX_GROUPS:
-        workspace = group_workspace(len(problems), groups[0]["c"].device, nvfp4=False)
+        workspace = group_workspace(len(problems), groups[0]["c"].device, nvfp4=False, stream=stream)
     _check(_lib.mxfp4_group_gemm(problems, len(problems), *_ws_args(workspace), _stream_ptr(stream)),
            "mxfp4_group_gemm")
     return [g["c"] for g in groups]
@@ -394,7 +424,7 @@ def nvfp4_group_gemm(groups, problems=None, workspace=None, stream=None):
     if problems is None:
         problems = make_nv_problems(groups)
     if workspace is None and len(problems) > NVFP4_MAX_GROUPS:
-        workspace = group_workspace(len(problems), groups[0]["c"].device)
+        workspace = group_workspace(len(problems), groups[0]["c"].device, stream=stream)
     _check(_lib.nvfp4_group_gemm(problems, len(problems), *_ws_args(workspace), _stream_ptr(stream)),
            "nvfp4_group_gemm")
     return [g["c"] for g in groups]
@@ -425,7 +455,7 @@ def nvfp4_group_quant_gemm(groups, problems=None, workspace=None, stream=None):
         problems = make_nv_act_problems(groups)
     if workspace is None:
         n = nvfp4_group_quant_gemm_workspace_bytes(problems)
-        workspace = torch.empty(max(1, n), dtype=torch.uint8, device=groups[0]["a"].device)
+        workspace = _scratch(torch.empty, max(1, n), groups[0]["a"].device, stream)
     _check(_lib.nvfp4_group_quant_gemm(problems, len(problems), workspace.data_ptr(), workspace.numel(),
                                        _stream_ptr(stream)), "nvfp4_group_quant_gemm")
     return [g["c"] for g in groups]
@@ -496,14 +526,14 @@ def mxfp8_add_rmsnorm_quantize(X, weight, eps: float = 1e-6, residual=None, H=No
     if H is not None:
         h, ldh = _rows(H, "H", dtype, shape)
     elif residual is not None:
-        H = torch.empty(shape, dtype=dtype, device=device)
+        H = _output(shape, dtype, device, stream)
         h, ldh = H.data_ptr(), K
     else:
         h, ldh = None, 0
     if Y is not None:
         y, ldy = _rows(Y, "Y", dtype, shape)
     elif want_y:
-        Y = torch.empty(shape, dtype=dtype, device=device)
+        Y = _output(shape, dtype, device, stream)
         y, ldy = Y.data_ptr(), K
     else:
         y, ldy = None, 0
@@ -511,13 +541,13 @@ def mxfp8_add_rmsnorm_quantize(X, weight, eps: float = 1e-6, residual=None, H=No
         q, ldq = _rows(Aq, "Aq", torch.uint8, shape)
     else:
         # K is a multiple of 32, so rows lie a multiple of 16 bytes apart, as the products want them
-        Aq = torch.empty(shape, dtype=torch.uint8, device=device)
+        Aq = _output(shape, torch.uint8, device, stream)
         q, ldq = Aq.data_ptr(), K
     need = _sf_bytes32(M, K)
     if A_sf is not None:
         sf = _scales(A_sf, "A_sf", need)
     else:
-        A_sf = torch.empty(need, dtype=torch.uint8, device=device)
+        A_sf = _output(need, torch.uint8, device, stream)
         sf = A_sf.data_ptr()
     _check(_lib.mxfp8_add_rmsnorm_quantize(x, ldx, res, ldr, w, _DTYPES[dtype], eps, M, K, h, ldh, y, ldy, q, ldq, sf,
                                            _stream_of(stream, X)),
@@ -542,12 +572,12 @@ def moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1
     if ids is not None:
         pi = _vec(ids, "ids", torch.int32, out)
     else:
-        ids = torch.empty(out, dtype=torch.int32, device=logits.device)
+        ids = _output(out, torch.int32, logits.device, stream)
         pi = ids.data_ptr()
     if weights is not None:
         pw = _vec(weights, "weights", torch.float32, out)
     else:
-        weights = torch.empty(out, dtype=torch.float32, device=logits.device)
+        weights = _output(out, torch.float32, logits.device, stream)
         pw = weights.data_ptr()
     _check(_lib.moe_route(z, _DTYPES[dtype], ldl, T, E,
                           _vec(bias, "bias", torch.float32, (E,)) if bias is not None else None, MOE_SCORES[score],
@@ -581,10 +611,10 @@ def mxfp4_moe_experts(Xq, X_sf, ids, weights, W13q, W13_sf, W2q, W2_sf, out=None
     if out is not None:
         o, ldo = _rows(out, "out", torch.bfloat16, (T, H))
     else:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=Xq.device)
+        out = _output((T, H), torch.bfloat16, Xq.device, stream)
         o, ldo = out.data_ptr(), H
     if workspace is None:
-        workspace = moe_experts_workspace(T, k, E, H, I, Xq.device)
+        workspace = _scratch(torch.empty, max(1, moe_experts_workspace_bytes(T, k, E, H, I)), Xq.device, stream)
     _check(_lib.mxfp4_moe_experts(x, ldx, _scales(X_sf, "X_sf", _sf_bytes32(T, H)), _vec(ids, "ids", torch.int32, (T, k)),
                                   _vec(weights, "weights", torch.float32, (T, k)),
                                   _vec(W13q, "W13q", u8, (E, 2 * I, H // 2)),
