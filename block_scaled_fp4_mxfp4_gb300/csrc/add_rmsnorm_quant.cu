@@ -16,9 +16,11 @@
 // squares is carried in two floats (vectors of eight in fp32, then error-free
 // additions), r too, and a value within the fp32 error (3 units) of a midpoint, or a
 // block's maximum within it of the border between two scales, is decided again in 64
-// bits. The rule costs three integer instructions an element. What is left is r's own
-// error of about 2^-28: a value closer than that to a midpoint may still go to
-// either side.
+// bits; what those find within 2^-40 of either counts as on it. The rule costs four
+// instructions an element (lanes that hold a subnormal code, whose midpoints are
+// others, look a second time: 4096 x 7168 53 us with and without; with the 64-bit part
+// entered for every such lane, 59.5 us). What is left is r's own error of about
+// 2^-28: a value closer than that to a midpoint may still go to either side.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -132,6 +134,10 @@ __device__ __forceinline__ float sumsq8(const uint4 &a)
     return s;
 }
 
+// What 64 bits find closer than this (relative) to a midpoint or a border is on it:
+// beyond the error of r, and a tie to the definition where its r has few bits.
+constexpr double kTie = 0x1p-40;
+
 // Normalizes, stores and quantizes the vector of eight values of row `row` at
 // column 8 * vec; `live`: vec lies within the row (all lanes of the warp call).
 template <bool F16>
@@ -179,29 +185,40 @@ __device__ __forceinline__ void finish8(const NormParams &p, int64_t row, int ve
             for (int i = 0; i < 8; ++i) top = fmax(top, fabs(exact(i)));
         top = fmax(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmax(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        if (border && amax >= 0x04800000u)
-            b = (amax >> 23) - 8 + (top > static_cast<double>(__uint_as_float((amax & 0x7F800000u) | 0x600000u)) ? 1u : 0u);
+        const double at = static_cast<double>(__uint_as_float((amax & 0x7F800000u) | 0x600000u));
+        if (border && amax >= 0x04800000u) b = (amax >> 23) - 8 + (top > at * (1.0 + kTie) ? 1u : 0u);
     }
     if (live) {
         const float inv = mxfp8_scale_inverse(b);
-        // E4M3 keeps three bits of the mantissa: its midpoints have 0x80000 in the other 20
-        bool near = false;
+        // E4M3 keeps three bits of the mantissa: its midpoints have 0x80000 in the other 20.
+        // Below 2^-6 it keeps steps of 2^-9: there those bits are looked at in |v| + 2^-6.
+        auto is_near = [](float v) { return (__float_as_uint(v) & 0xFFFFFu) - 0x7FFFDu <= 6u; };
+        bool near = false, small = false;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) near |= (__float_as_uint(y[i]) & 0xFFFFFu) - 0x7FFFDu <= 6u;
+        for (int i = 0; i < 8; ++i) {
+            y[i] *= inv;
+            near |= is_near(y[i]);
+            small |= fabsf(y[i]) < 0x1p-6f;
+        }
+        if (small) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) near |= fabsf(y[i]) < 0x1p-6f && is_near(fabsf(y[i]) + 0x1p-6f);
+        }
         if (near) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const uint32_t u = __float_as_uint(y[i]);
-                if ((u & 0xFFFFFu) - 0x7FFFDu <= 6u) {
-                    const uint32_t mid = (u & 0x7FF00000u) | 0x80000u;
-                    const double d = fabs(exact(i)), md = static_cast<double>(__uint_as_float(mid));
-                    y[i] = __uint_as_float((u & 0x80000000u) | (d > md ? mid + 1 : d < md ? mid - 1 : mid));
+                const float v = fabsf(y[i]), up = v < 0x1p-6f ? 0x1p-6f : 0.0f;
+                if (is_near(v + up)) {
+                    const float mid = __uint_as_float((__float_as_uint(v + up) & 0x7FF00000u) | 0x80000u) - up;
+                    const double d = fabs(exact(i)) * static_cast<double>(inv), md = static_cast<double>(mid);
+                    const int to = d > md * (1.0 + kTie) ? 1 : d < md * (1.0 - kTie) ? -1 : 0;
+                    y[i] = copysignf(__int_as_float(__float_as_int(mid) + to), y[i]);
                 }
             }
         }
         uint2 c;
-        c.x = e4m3x4_rn(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
-        c.y = e4m3x4_rn(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv);
+        c.x = e4m3x4_rn(y[0], y[1], y[2], y[3]);
+        c.y = e4m3x4_rn(y[4], y[5], y[6], y[7]);
         *reinterpret_cast<uint2 *>(p.q + row * p.ldq + 8 * vec) = c;
     }
     // the four scale bytes of 128 columns are one word of the blocked layout

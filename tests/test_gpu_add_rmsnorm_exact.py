@@ -1,0 +1,86 @@
+"""The codes and scales of mxfp8_add_rmsnorm_quantize are those of its definition in 64 bits, where fp32 arithmetic
+would take the neighbour: no tolerance but for values that lie within 2^-40 of a rounding midpoint, or maxima that close
+to the border between two scales."""
+import pytest
+import torch
+
+import moe_ref
+
+pytestmark = pytest.mark.gpu
+
+mx = pytest.importorskip("block_scaled_fp4_mxfp4_gb300.mxfp4")
+
+TYPES = [torch.bfloat16, torch.float16]
+
+
+def definition(x, res, w, eps):
+    """(y / scale, exponents, codes as multiples of the scale), float64."""
+    h, y = moe_ref.add_rmsnorm(x, res, w, eps)
+    q, e = moe_ref.mxfp8(y)
+    s = torch.exp2(e.double()).repeat_interleave(32, 1)
+    return y / s, e, q / s
+
+
+def check(x, res, w, eps):
+    M, K = x.shape
+    Aq, sf, _, _ = mx.mxfp8_add_rmsnorm_quantize(x, w, eps, residual=res)
+    v, e, q = definition(x, res, w, eps)
+    bytes_ = sf[moe_ref.blocked_index(M, K // 32, x.device)]
+    assert torch.equal(bytes_.int(), e.int() + 127)
+    got = moe_ref.e4m3_values(Aq)
+    wrong = got != q
+    step = moe_ref.e4m3_step(v)
+    on = ((v.abs() / step - torch.floor(v.abs() / step) - 0.5) * step).abs() <= 2.0 ** -40 * v.abs()
+    assert not bool((wrong & ~on).any()), (int((wrong & ~on).sum()), v[wrong][:4], got[wrong][:4], q[wrong][:4])
+    return v, e
+
+
+def near_one(dtype, side):
+    """A row of ones, but for one element, and an eps, for which r is 1 to fp32 and lies on `side` of it."""
+    if side == 0:
+        return torch.ones(7168, device="cuda", dtype=dtype), 0.0
+    if side < 0:                                        # 1 - 2^-26
+        return torch.ones(7168, device="cuda", dtype=dtype), 2.0 ** -25
+    x = torch.ones(65536 if dtype == torch.bfloat16 else 8192, device="cuda", dtype=dtype)
+    x[70] -= 2.0 ** (-8 if dtype == torch.bfloat16 else -11)          # 1 + 2^-24
+    return x, 0.0
+
+
+def r_of(x, eps):
+    return float(1 / torch.sqrt(x.double().square().mean() + eps))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("side", [-1, 0, 1])
+@pytest.mark.parametrize("subnormal", [False, True])
+def test_values_on_either_side_of_a_midpoint(dtype, side, subnormal):
+    """y = r w with w a midpoint of E4M3 and r = 1 to fp32."""
+    x, eps = near_one(dtype, side)
+    K = x.numel()
+    r = r_of(x, eps)
+    assert (r > 1) - (r < 1) == side and torch.tensor(r, dtype=torch.float64).float() == 1.0
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    n = torch.randint(0, 8, (K,), device="cuda", generator=gen)
+    if subnormal:
+        w = (n + 0.5) * 2.0 ** -9
+    else:
+        w = (1 + (n + 0.5) / 8) * torch.exp2(torch.randint(-6, 8, (K,), device="cuda", generator=gen).float())
+    w = w * (1 - 2 * torch.randint(0, 2, (K,), device="cuda", generator=gen))
+    w[::32] = 256.0                                     # of every block the maximum: its scale is 1
+    v, e = check(torch.stack([x, -x, x]), None, w.to(dtype), eps)
+    assert not e.any()
+    if side == 0:
+        assert torch.equal(v[0], w.to(dtype).double())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("side", [-1, 0, 1])
+def test_maxima_on_either_side_of_the_border_between_scales(dtype, side):
+    x, eps = near_one(dtype, side)
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    w = torch.rand(x.numel(), device="cuda", generator=gen) * 100
+    w[5::32] = 448.0
+    _, e = check(torch.stack([x, x]), None, w.to(dtype), eps)
+    keep = torch.ones_like(e, dtype=torch.bool)
+    keep[:, 70 // 32] = False
+    assert bool((e == (1 if side > 0 else 0))[keep].all())
