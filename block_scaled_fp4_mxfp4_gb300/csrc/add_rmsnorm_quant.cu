@@ -13,14 +13,16 @@
 //
 // Exactness: an E4M3 rounding turns an fp32 error of 2^-23 into a step of 2^-3 where
 // a value lies next to a midpoint, about one element in a million. So the sum of
-// squares is carried in two floats (vectors of eight in fp32, then error-free
-// additions), r too, and a value within the fp32 error (3 units) of a midpoint, or a
-// block's maximum within it of the border between two scales, is decided again in 64
-// bits; what those find within 2^-40 of either counts as on it. The rule costs four
-// instructions an element (lanes that hold a subnormal code, whose midpoints are
-// others, look a second time: 4096 x 7168 53 us with and without; with the 64-bit part
-// entered for every such lane, 59.5 us). What is left is r's own error of about
-// 2^-28: a value closer than that to a midpoint may still go to either side.
+// squares is carried in two floats, by error-free additions from the first square on
+// (a row is often dominated by a few channels: with the eight squares of a vector
+// summed in fp32, its r was off by up to 2^-24; 4096 x 7168 53.4 us so, 54.4 us now),
+// and r is two floats good to 2^-42: the low parts add up in fp32, 2^-48 of the sum an
+// addition, about forty in a row. A value within the fp32 error (3 units) of a
+// midpoint, or a block's maximum within it of the border between two scales, is
+// decided again in 64 bits; what those find within 2^-40 of either counts as on it.
+// The rule costs four instructions an element. Lanes that hold a subnormal code, whose
+// midpoints are others, look a second time (no difference at 4096 x 7168; with the
+// 64-bit part entered for every such lane, 59.5 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -53,6 +55,7 @@ struct Two {
     float hi, lo;
 };
 
+// Knuth's TwoSum of the high parts; the low ones are added in fp32.
 __device__ __forceinline__ Two two_add(const Two &a, const Two &b)
 {
     const float s = __fadd_rn(a.hi, b.hi), z = __fsub_rn(s, a.hi);
@@ -120,18 +123,63 @@ __device__ __forceinline__ uint4 add8(const uint4 &a, const uint4 &b)
     return o;
 }
 
+// Two such sums side by side: the lanes of 64-bit registers of packed fp32
+// arithmetic, half the instructions of two.
+struct TwoPair {
+    uint64_t hi, lo;
+};
+
+__device__ __forceinline__ uint64_t pack(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack(uint64_t v)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t sub_pair(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t square_pair(uint64_t a)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %1;" : "=l"(r) : "l"(a));
+    return r;
+}
+
+// Adds the squares of eight values to s. The square of a bf16 or fp16 value is exact
+// in fp32 (16 or 22 bits), and so is each addition to hi with its error to lo.
 template <bool F16>
-__device__ __forceinline__ float sumsq8(const uint4 &a)
+__device__ __forceinline__ void add_squares8(TwoPair &s, const uint4 &a)
 {
     const uint32_t *p = &a.x;
-    float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 u = unpack2<F16>(p[i]);
-        s = fmaf(u.x, u.x, s);
-        s = fmaf(u.y, u.y, s);
+        const uint64_t q = square_pair(pack(u.x, u.y));
+        const uint64_t t = add_pair(s.hi, q), z = sub_pair(t, s.hi);
+        s.lo = add_pair(s.lo, add_pair(sub_pair(s.hi, sub_pair(t, z)), sub_pair(q, z)));
+        s.hi = t;
     }
-    return s;
+}
+
+__device__ __forceinline__ Two total(const TwoPair &s)
+{
+    const float2 hi = unpack(s.hi), lo = unpack(s.lo);
+    return two_add(Two{hi.x, lo.x}, Two{hi.y, lo.y});
 }
 
 // What 64 bits find closer than this (relative) to a midpoint or a border is on it:
@@ -267,8 +315,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 6 : 1) add_r
         if (p.res) a = add8<F16>(a, ld_row(p.res + ro + 8 * v));
         return a;
     };
-    auto add_vec = [](Two s, float v) { return two_add(s, Two{v, 0.0f}); };
-    Two ss{0.0f, 0.0f};
+    TwoPair ss{0, 0};
     if constexpr (VPT > 0) {
         uint4 hv[VPT];
 #pragma unroll
@@ -280,19 +327,19 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 6 : 1) add_r
         for (int i = 0; i < VPT; ++i) {
             const int v = threadIdx.x + i * nt;
             if (v < nvec) {
-                ss = add_vec(ss, sumsq8<F16>(hv[i]));
+                add_squares8<F16>(ss, hv[i]);
                 if (p.h) *reinterpret_cast<uint4 *>(p.h + ho + 8 * v) = hv[i];
             }
         }
-        const Two r = reciprocal_rms(block_sum(ss, buf), p);
+        const Two r = reciprocal_rms(block_sum(total(ss), buf), p);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = threadIdx.x + i * nt;
             if (v - static_cast<int>(threadIdx.x & 31) < nvec) finish8<F16>(p, row, v, v < nvec, hv[i], r);
         }
     } else {
-        for (int v = threadIdx.x; v < nvec; v += nt) ss = add_vec(ss, sumsq8<F16>(load_h(v)));
-        const Two r = reciprocal_rms(block_sum(ss, buf), p);
+        for (int v = threadIdx.x; v < nvec; v += nt) add_squares8<F16>(ss, load_h(v));
+        const Two r = reciprocal_rms(block_sum(total(ss), buf), p);
         for (int v0 = threadIdx.x & ~31; v0 < nvec; v0 += nt) {
             const int v = v0 + (threadIdx.x & 31);
             uint4 hv = make_uint4(0, 0, 0, 0);

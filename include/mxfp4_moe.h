@@ -39,9 +39,11 @@ extern "C" {
 
 /* Residual sum, RMSNorm and MXFP8 quantization of rows X [M, K] (bf16 or fp16):
  *   h   = X + residual, in fp32, rounded to the element type (residual NULL: h = X)
- *   r   = 1 / sqrt(mean_k(h_k^2) + eps), sums in fp32 (r = 0 where that mean + eps is 0)
- *   y_k = (h_k * r) * weight_k, in fp32
- *   Aq, A_sf = MXFP8 of y (see above); pad cells of A_sf are written with 0x7F.
+ *   r   = 1 / sqrt(mean_k(h_k^2) + eps), good to 2^-42 (squares are taken in fp32, so
+ *         those below 2^-149 count as 0; r = 0 where that mean + eps is 0)
+ *   y_k = h_k * r * weight_k (Y: in fp32, then rounded)
+ *   Aq, A_sf = MXFP8 of y (see above), the codes and scales of 64-bit arithmetic;
+ *         pad cells of A_sf are written with 0x7F.
  *   X, residual, weight, H, Y : element type `dtype` (MXFP4_DTYPE_BF16 / _FP16).
  *   weight : [K], 16-byte aligned.
  *   H   : out, [M, K], h (NULL: not stored). May be X or residual itself (same
