@@ -46,6 +46,7 @@ struct NormParams {
     int64_t ldx, ldr, ldh, ldy, ldq;
     int64_t M;
     int K;
+    float eps;
     float keps_hi, keps_lo;     // K * eps
     float rootk_hi, rootk_lo;   // sqrt(K)
 };
@@ -63,13 +64,12 @@ __device__ __forceinline__ Two two_add(const Two &a, const Two &b)
     return Two{s, __fadd_rn(e, __fadd_rn(a.lo, b.lo))};
 }
 
-// sqrt(K / m) of m = ss + K * eps: rsqrt and one Newton step on its exact residual.
-__device__ __forceinline__ Two reciprocal_rms(const Two &ss, const NormParams &p)
+// sqrt(K / m), m < kHuge: rsqrt and one Newton step on its exact residual.
+__device__ __forceinline__ Two reciprocal_rms(const Two &m, const NormParams &p)
 {
-    const Two m = two_add(ss, Two{p.keps_hi, p.keps_lo});
     const float q = rsqrtf(m.hi);
-    // out of this range the residual leaves fp32 (an infinite or vanishing sum)
-    if (!(m.hi > 1e-30f && m.hi < 1e30f)) return Two{m.hi == 0.0f ? 0.0f : q * p.rootk_hi, 0.0f};
+    // below this the residual leaves fp32 (a vanishing sum)
+    if (!(m.hi > 1e-30f)) return Two{m.hi == 0.0f ? 0.0f : q * p.rootk_hi, 0.0f};
     const float s = q * q, se = fmaf(q, q, -s);
     const float t = fmaf(-m.hi, s, 1.0f) - fmaf(m.hi, se, m.lo * s);
     const float hi = q * p.rootk_hi;
@@ -77,6 +77,10 @@ __device__ __forceinline__ Two reciprocal_rms(const Two &ss, const NormParams &p
     const float r = hi + lo;
     return Two{r, lo - (r - hi)};
 }
+
+// Sums from here on, whose squares, reciprocal or its residual may leave fp32 (bf16
+// values above 10^13, or a huge eps), take the way of finish_huge_row.
+constexpr float kHuge = 1e30f;
 
 // 16 bytes that this kernel reads once. Not through the read-only path: the sum may
 // be written over them.
@@ -188,16 +192,18 @@ constexpr double kTie = 0x1p-40;
 
 // Normalizes, stores and quantizes the vector of eight values of row `row` at
 // column 8 * vec; `live`: vec lies within the row (all lanes of the warp call).
-template <bool F16>
+// HUGE_ROW: r is 2^64 of the reciprocal, for values taken as 2^-64 of theirs.
+template <bool F16, bool HUGE_ROW = false>
 __device__ __forceinline__ void finish8(const NormParams &p, int64_t row, int vec, bool live, const uint4 &hv, const Two &r)
 {
+    constexpr float kPre = HUGE_ROW ? 0x1p-64f : 1.0f;
     float y[8];
     // element i from 64-bit arithmetic
     auto exact = [&](int i) {
         const uint32_t *ph = &hv.x;
         const uint32_t wv = __ldg(reinterpret_cast<const uint32_t *>(p.w) + 4 * vec + (i >> 1));
         const float2 a = unpack2<F16>(ph[i >> 1]), b = unpack2<F16>(wv);
-        return static_cast<double>(i & 1 ? a.y : a.x) * (static_cast<double>(r.hi) + static_cast<double>(r.lo)) *
+        return static_cast<double>((i & 1 ? a.y : a.x) * kPre) * (static_cast<double>(r.hi) + static_cast<double>(r.lo)) *
                static_cast<double>(i & 1 ? b.y : b.x);
     };
     uint32_t amax = 0;
@@ -207,8 +213,8 @@ __device__ __forceinline__ void finish8(const NormParams &p, int64_t row, int ve
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 a = unpack2<F16>(ph[i]), b = unpack2<F16>(pw[i]);
-            y[2 * i] = __fmul_rn(__fmul_rn(a.x, r.hi), b.x);
-            y[2 * i + 1] = __fmul_rn(__fmul_rn(a.y, r.hi), b.y);
+            y[2 * i] = __fmul_rn(__fmul_rn(a.x * kPre, r.hi), b.x);
+            y[2 * i + 1] = __fmul_rn(__fmul_rn(a.y * kPre, r.hi), b.y);
         }
         if (p.y) {
             uint4 o;
@@ -299,29 +305,73 @@ __device__ __forceinline__ Two block_sum(Two v, Two *buf)
     return v;
 }
 
+// h of vector v of a row, from X and the residual.
+template <bool F16>
+__device__ __forceinline__ uint4 load_h(const NormParams &p, int64_t row, int v)
+{
+    uint4 a = ld_row(p.x + row * p.ldx + 8 * v);
+    if (p.res) a = add8<F16>(a, ld_row(p.res + row * p.ldr + 8 * v));
+    return a;
+}
+
+// The rest of a row whose sum of squares is kHuge or more, with that sum taken again in
+// 64 bits. `stored`: h is in H already (each thread's own vectors). An infinite value
+// makes r = 0, so it becomes NaN and the finite ones 0. Seldom, so kept out of line.
+template <bool F16>
+__device__ __noinline__ void finish_huge_row(const NormParams &p, int64_t row, bool stored, double *buf)
+{
+    const int nvec = p.K >> 3, nt = blockDim.x, nw = nt >> 5, lane = threadIdx.x & 31;
+    auto load = [&](int v) { return stored ? ld_row(p.h + row * p.ldh + 8 * v) : load_h<F16>(p, row, v); };
+    double ss = 0.0;
+    for (int v = threadIdx.x; v < nvec; v += nt) {
+        const uint4 hv = load(v);
+        const uint32_t *w = &hv.x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 u = unpack2<F16>(w[i]);
+            ss += static_cast<double>(u.x) * u.x + static_cast<double>(u.y) * u.y;
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (lane == 0) buf[threadIdx.x >> 5] = ss;
+    __syncthreads();
+    ss = 0.0;
+    for (int i = 0; i < nw; ++i) ss += buf[i];
+    const double r64 = 0x1p64 * sqrt(p.K / (ss + static_cast<double>(p.eps) * p.K));
+    const float hi = static_cast<float>(r64);
+    const Two r{hi, static_cast<float>(r64 - hi)};
+    for (int v0 = threadIdx.x & ~31; v0 < nvec; v0 += nt) {
+        const int v = v0 + lane;
+        uint4 hv = make_uint4(0, 0, 0, 0);
+        if (v < nvec) {
+            hv = load(v);
+            if (p.h && !stored) *reinterpret_cast<uint4 *>(p.h + row * p.ldh + 8 * v) = hv;
+        }
+        finish8<F16, true>(p, row, v, v < nvec, hv, r);
+    }
+}
+
 // One row a block; VPT vectors a thread stay in registers (VPT = 0: rows of any
 // length, read a second time for the quantization).
 template <bool F16, int VPT, int MAX_THREADS>
-__global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 6 : 1) add_rmsnorm_mxfp8_kernel(const NormParams p)
+__global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 6 : 1) add_rmsnorm_mxfp8_kernel(const __grid_constant__ NormParams p)
 {
     __shared__ Two buf[32];
+    __shared__ double buf64[32];
     grid_dependency_wait();
     grid_launch_dependents();
     const int64_t row = blockIdx.x;
     const int nvec = p.K >> 3, nt = blockDim.x;
-    const int64_t xo = row * p.ldx, ro = row * p.ldr, ho = row * p.ldh;
-    auto load_h = [&](int v) {
-        uint4 a = ld_row(p.x + xo + 8 * v);
-        if (p.res) a = add8<F16>(a, ld_row(p.res + ro + 8 * v));
-        return a;
-    };
+    const int64_t ho = row * p.ldh;
     TwoPair ss{0, 0};
+    const Two keps{p.keps_hi, p.keps_lo};
     if constexpr (VPT > 0) {
         uint4 hv[VPT];
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = threadIdx.x + i * nt;
-            if (v < nvec) hv[i] = load_h(v);
+            if (v < nvec) hv[i] = load_h<F16>(p, row, v);
         }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
@@ -331,23 +381,33 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 6 : 1) add_r
                 if (p.h) *reinterpret_cast<uint4 *>(p.h + ho + 8 * v) = hv[i];
             }
         }
-        const Two r = reciprocal_rms(block_sum(total(ss), buf), p);
+        const Two m = two_add(block_sum(total(ss), buf), keps);
+        if (m.hi >= kHuge) {
+            finish_huge_row<F16>(p, row, p.h != nullptr, buf64);
+        } else {
+            const Two r = reciprocal_rms(m, p);
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int v = threadIdx.x + i * nt;
-            if (v - static_cast<int>(threadIdx.x & 31) < nvec) finish8<F16>(p, row, v, v < nvec, hv[i], r);
+            for (int i = 0; i < VPT; ++i) {
+                const int v = threadIdx.x + i * nt;
+                if (v - static_cast<int>(threadIdx.x & 31) < nvec) finish8<F16>(p, row, v, v < nvec, hv[i], r);
+            }
         }
     } else {
-        for (int v = threadIdx.x; v < nvec; v += nt) add_squares8<F16>(ss, load_h(v));
-        const Two r = reciprocal_rms(block_sum(total(ss), buf), p);
-        for (int v0 = threadIdx.x & ~31; v0 < nvec; v0 += nt) {
-            const int v = v0 + (threadIdx.x & 31);
-            uint4 hv = make_uint4(0, 0, 0, 0);
-            if (v < nvec) {
-                hv = load_h(v);
-                if (p.h) *reinterpret_cast<uint4 *>(p.h + ho + 8 * v) = hv;
+        for (int v = threadIdx.x; v < nvec; v += nt) add_squares8<F16>(ss, load_h<F16>(p, row, v));
+        const Two m = two_add(block_sum(total(ss), buf), keps);
+        if (m.hi >= kHuge) {
+            finish_huge_row<F16>(p, row, false, buf64);
+        } else {
+            const Two r = reciprocal_rms(m, p);
+            for (int v0 = threadIdx.x & ~31; v0 < nvec; v0 += nt) {
+                const int v = v0 + (threadIdx.x & 31);
+                uint4 hv = make_uint4(0, 0, 0, 0);
+                if (v < nvec) {
+                    hv = load_h<F16>(p, row, v);
+                    if (p.h) *reinterpret_cast<uint4 *>(p.h + ho + 8 * v) = hv;
+                }
+                finish8<F16>(p, row, v, v < nvec, hv, r);
             }
-            finish8<F16>(p, row, v, v < nvec, hv, r);
         }
     }
     // pad rows of the last 128-row block of scales, shared out over all threads in the
@@ -416,6 +476,7 @@ cudaError_t launch_add_rmsnorm_mxfp8(const void *X, int64_t ldx, const void *res
     p.ldq = ldq;
     p.M = M;
     p.K = static_cast<int>(K);
+    p.eps = eps;
     // constants of the row's reciprocal, each as the sum of two floats
     const double keps = static_cast<double>(eps) * static_cast<double>(K), rootk = std::sqrt(static_cast<double>(K));
     p.keps_hi = static_cast<float>(keps);

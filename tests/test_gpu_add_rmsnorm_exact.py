@@ -127,3 +127,36 @@ def test_codes_and_scales_are_those_of_64_bits(M, K, amp, dtype):
     of a row's squares, or where a block has an outlier and its other values are subnormal codes."""
     x, res, w = rows(M, K, dtype, M + K, amp, res=amp is some_channels)
     check(x, res, w, 1e-6)
+
+
+@pytest.mark.parametrize("M,K", [(5, 256), (7, 7168), (400, 2112), (400, 7168), (6, 33024)])
+@pytest.mark.parametrize("res", [False, True])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_rows_whose_squares_leave_fp32(M, K, res, in_place):
+    """bf16 holds values whose squares, or the sum of them, are beyond fp32: rows of 2^45 to 2^120, among ordinary ones,
+    and ordinary rows with one such value."""
+    x, r, w = rows(M, K, torch.bfloat16, M * K, some_channels, res)
+    up = torch.exp2(torch.tensor([0.0, 45, 50, 62, 64, 100, 118], device="cuda"))[torch.arange(M, device="cuda") % 7]
+    x = (x.float() * up[:, None]).to(torch.bfloat16)
+    x[::5, 11] = 2.0 ** 127
+    if res:
+        r = (r.float() * up[:, None]).to(torch.bfloat16)
+    h, y = moe_ref.add_rmsnorm(x, r, w, 1e-6)
+    assert bool(torch.isfinite(h).all()) and bool((h.float().square().sum(-1) == torch.inf).any())
+    check(x, r, w, 1e-6)
+    given = x.clone()
+    Aq, sf, H, Y = mx.mxfp8_add_rmsnorm_quantize(given, w, 1e-6, residual=r, H=given if in_place else None, want_y=True)
+    plain = mx.mxfp8_add_rmsnorm_quantize(x, w, 1e-6, residual=r)
+    assert torch.equal(Aq, plain[0]) and torch.equal(sf, plain[1])
+    if H is not None:
+        assert torch.equal(H, h)
+    # y: three fp32 roundings, then half a step of bf16 (2^-134: of its smallest values)
+    assert bool(((Y.double() - y).abs() <= (2.0 ** -8 + 2.0 ** -21) * y.abs() + 2.0 ** -134).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("eps", [1e25, 1e34, 3e38])
+def test_an_eps_beyond_the_squares(dtype, eps):
+    x, _, w = rows(9, 7168, dtype, 3, plain)
+    eps = float(torch.tensor(eps))
+    check(x, None, w, eps)
