@@ -124,8 +124,6 @@ mxfp4_status_t mxfp4_moe_experts(const void *Xq, int64_t ldx, const void *X_sf, 
     if (!Xq || !X_sf || !ids || !weights || !W13q || !W13_sf || !W2q || !W2_sf || !out || !workspace)
         return MXFP4_ERR_INVALID_ARG;
     if (ldx < H || ldo < H) return MXFP4_ERR_INVALID_ARG;
-    // rows of tokens are addressed in units of 16 bytes held in 32 bits
-    if (ldx / 16 > (int64_t(1) << 32) / T || I / 16 > (int64_t(1) << 32) / (T * k)) return MXFP4_ERR_UNSUPPORTED_SHAPE;
     if (ldx % 16 || ldo % 8 || !aligned(Xq, 16) || !aligned(X_sf, 16) || !aligned(ids, 4) || !aligned(weights, 4) ||
         !aligned(W13q, 32) || !aligned(W2q, 32) || !aligned(W13_sf, 16) || !aligned(W2_sf, 16) || !aligned(out, 16) ||
         !aligned(workspace, 256))

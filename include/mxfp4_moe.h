@@ -105,8 +105,9 @@ MXFP4_API size_t mxfp4_moe_experts_workspace_bytes(int64_t T, int k, int E, int6
  *   W13_sf   : E blocked E8M0 buffers of mxfp4_sf_bytes(2I, H, 32) bytes, one after another.
  *   W2q      : packed E2M1 [E, H, I/2], contiguous;  W2_sf : E buffers of mxfp4_sf_bytes(H, I, 32).
  *   out      : bf16 [T, H], row stride ldo elements.
- * T >= 0; H and I positive multiples of 128; 1 <= k <= MOE_MAX_TOPK;
- * 1 <= E <= MOE_MAX_EXPERTS; T * k < 2^30. Xq 16-byte aligned with ldx a multiple of 16;
+ * T >= 0; H and I positive multiples of 128 up to 2^20; 1 <= k <= MOE_MAX_TOPK;
+ * 1 <= E <= MOE_MAX_EXPERTS; T * k < 2^30; 2 I E, H E, (T k / 32 + E) (I / 64) and
+ * (T k / 32 + E) (H / 128) < 2^31 (the workspace query refuses the same sizes). Xq 16-byte aligned with ldx a multiple of 16;
  * W13q and W2q 32-byte aligned; scales 16; out 16 with ldo a multiple of 8;
  * workspace 256. The workspace needs no initialisation and keeps nothing from
  * one call for the next; calls that share one must not overlap. */
