@@ -5,8 +5,9 @@
     out     = sum over a token's k experts of weight * W2 (silu(G y) * (U y))
 
 Three calls of the library (norm with its 8-bit output, routing, experts'
-products) around one small dense product for the router's logits. The next
-layer's norm adds ``out`` to ``h``.
+products) around one small dense product for the router's logits (torch's, in
+bf16, so the logits are rounded to bf16). The next layer's norm adds ``out`` to
+``h``.
 
     python -m block_scaled_fp4_mxfp4_gb300.moe_layer [--tokens 1 16 256 4096]
 
@@ -29,11 +30,12 @@ class MoeLayer:
     """
 
     def __init__(self, gate, up, down, router, norm, k, max_tokens, bias=None, score="softmax", groups=1,
-                 topk_groups=1, renormalize=True, scale=1.0, eps=1e-6):
+                 topk_groups=1, renormalize=True, scale=1.0, eps=1e-6, group_top=2):
         E, I, H = gate.shape
         self.E, self.I, self.H, self.k = E, I, H, k
         self.router, self.norm, self.bias, self.eps = router, norm, bias, eps
-        self.how = dict(score=score, groups=groups, topk_groups=topk_groups, renormalize=renormalize, scale=scale)
+        self.how = dict(score=score, groups=groups, topk_groups=topk_groups, group_top=group_top, renormalize=renormalize,
+                        scale=scale)
         dev = gate.device
         self.w13 = torch.empty((E, 2 * I, H // 2), dtype=torch.uint8, device=dev)
         self.s13 = torch.empty((E, mx.sf_bytes(2 * I, H, 32)), dtype=torch.uint8, device=dev)
