@@ -210,7 +210,7 @@ __device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;
 //           latency (with three stages, those took 1350 clocks each)
 // A stage costs every role some hundred clocks of waits, fences and issues, against
 // 740 clocks that its 16 KB take at the HBM's rate: so two groups widen, two
-// threads copy scales and two threads issue MMAs, on alternating stages (the two
+// warps copy scales and two warps issue MMAs, on alternating stages (the two
 // issuers into accumulators of their own, which the epilogue adds).
 
 constexpr int kSmallNT = 32;
@@ -281,7 +281,11 @@ __device__ __forceinline__ void store_columns(const uint32_t (&v)[32], float *ep
         const bool live = r < w.rows;
         const size_t row = static_cast<size_t>(w.row0) + r;
         if constexpr (FIRST) {
-            // 8 channels a thread; four neighbours share a block of 32
+            // 8 channels a thread; four neighbours share a block of 32. silu by __expf and
+            // __fdividef: off by up to (5 + 1.2 |g|) 2^-23 of itself, and 0 below -87.3 where
+            // its size is under 2^-118; E4M3 keeps 2^-4, so this moves a code only next to a
+            // midpoint, as the products' own fp32 sums do. expf and an IEEE division were
+            // measured: 16 tokens 55 -> 64 us, 1111 ragged 105 -> 122, the others 1 to 4 %.
             const float *g = epi + col * kEpiLd + 8 * part;
             float a[8];
             uint32_t amax = 0;
@@ -363,9 +367,9 @@ struct UnitWalk {
 //   0-3    epilogue of a finished tile while the next one's mainloop runs
 //   4-7    copy token rows and all scales by cp.async
 //   8-15   widen packed weights: groups of four on alternating stages
-//   16,17  MMA issuers (lane 0), on alternating stages of a tile; 16 owns TMEM
+//   16,17  MMA issuers (an elected lane), on alternating stages of a tile; 16 owns TMEM
 //   18     lane 0 loads packed weights by TMA
-//   19,20  lane 0 of each copies the scales of alternating stages to TMEM
+//   19,20  copy the scales of alternating stages to TMEM (an elected lane)
 //
 // A wait on a ring's barrier names the round by its parity alone, so it is right only
 // if the barrier can be neither a round further nor a round behind. What makes it so
@@ -770,10 +774,10 @@ struct LargeCfg {
 //   4-15   widen packed weights: three groups of four take the packed stages in turn
 //          (a group's two stages take it about 2700 clocks of waits, copies and
 //          fences); they also see the tokens land, and tell rank 0
-//   16     owns TMEM; rank 0: issues the MMAs
+//   16     owns TMEM; rank 0: issues the MMAs (an elected lane)
 //   17     lane 0 loads packed weights and their scales by TMA
 //   18     lane 0 loads tokens and their scales by TMA
-//   19     rank 0: copies the scales to both TMEMs, stage by stage
+//   19     rank 0: copies the scales to both TMEMs, stage by stage (an elected lane)
 //
 // A wait on a ring's barrier names the round by its parity alone, so it is right only
 // if the barrier can be neither a round further nor a round behind. Not behind:

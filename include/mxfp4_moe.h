@@ -77,6 +77,8 @@ MXFP4_API mxfp4_status_t mxfp8_add_rmsnorm_quantize(const void *X, int64_t ldx, 
  * again in 64 bits for rows in which that bound leaves it open. Without a bias
  * and without groups the experts are ranked by their logits, which rank them as
  * their scores do, but also where scores saturate. A NaN score ranks first.
+ * The weights are computed in fp32 from the chosen logits: good to 2^-17 of
+ * themselves at worst, 2^-24 on average; a score below 2^-126 may count as 0.
  * An expert whose logit is -inf is not chosen: a slot for which no expert is
  * left gets id -1 and weight 0 (a row of -inf: all of them).
  *   logits : [T, E] of type dtype (bf16, fp16, fp32), row stride ldl elements, aligned to its type.
@@ -96,7 +98,8 @@ MXFP4_API size_t mxfp4_moe_experts_workspace_bytes(int64_t T, int k, int E, int6
  *   out[t] = bf16_rne( sum_j weights[t, j] * ( act_j . W2[e]^T ) ),  e = ids[t, j],
  *   act_j  = MXFP8( silu(x_t . G[e]^T) * (x_t . U[e]^T) ),   silu(g) = g / (1 + exp(-g)),
  * summed in the order of j in fp32; all products accumulate in fp32 on the
- * tensor cores (tcgen05.mma kind::mxf8f6f4). A choice whose id is outside
+ * tensor cores (tcgen05.mma kind::mxf8f6f4); silu is good to (5 + 1.2 |g|) 2^-23
+ * of its value, and 0 for g < -87.3. A choice whose id is outside
  * [0, E) is left out (experts of other devices, slots without one); a token
  * with no choice left gets zeros.
  *   Xq, X_sf : MXFP8 activations [T, H], row stride ldx bytes.
