@@ -37,7 +37,7 @@ struct MoeLayout {
     size_t hist, tiles, rec, src, pos, act, act_sf, y, xs, xs_sf, total;
 };
 constexpr int kMoeLargeTile = 224;   // nt of the layouts that need sorted token rows
-bool moe_layout(int64_t T, int k, int E, int64_t H, int64_t I, MoeLayout *out);
+MoeLayout moe_layout(int64_t T, int k, int E, int64_t H, int64_t I);
 
 struct MoeArgs {
     const uint8_t *xq;

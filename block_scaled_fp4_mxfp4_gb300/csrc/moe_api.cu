@@ -109,8 +109,7 @@ mxfp4_status_t moe_route(const void *logits, int dtype, int64_t ldl, int64_t T, 
 size_t mxfp4_moe_experts_workspace_bytes(int64_t T, int k, int E, int64_t H, int64_t I)
 {
     if (check_moe_sizes(T, k, E, H, I) != MXFP4_OK || T == 0) return 0;
-    MoeLayout l;
-    return moe_layout(T, k, E, H, I, &l) ? l.total : 0;
+    return moe_layout(T, k, E, H, I).total;
 }
 
 mxfp4_status_t mxfp4_moe_experts(const void *Xq, int64_t ldx, const void *X_sf, const int32_t *ids, const float *weights,
@@ -128,8 +127,7 @@ mxfp4_status_t mxfp4_moe_experts(const void *Xq, int64_t ldx, const void *X_sf, 
         !aligned(W13q, 32) || !aligned(W2q, 32) || !aligned(W13_sf, 16) || !aligned(W2_sf, 16) || !aligned(out, 16) ||
         !aligned(workspace, 256))
         return MXFP4_ERR_MISALIGNED;
-    MoeLayout l;
-    if (!moe_layout(T, k, E, H, I, &l)) return MXFP4_ERR_UNSUPPORTED_SHAPE;
+    const MoeLayout l = moe_layout(T, k, E, H, I);
     if (ws_bytes < l.total) return MXFP4_ERR_WORKSPACE_TOO_SMALL;
     int sms = 0;
     if (!current_device_sms(&sms)) return MXFP4_ERR_NO_DEVICE;

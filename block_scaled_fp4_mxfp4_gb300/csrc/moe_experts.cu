@@ -56,7 +56,7 @@ struct PlaceParams {
     const int32_t *ids;
     int *hist;      // [chunks][E], more than one chunk only
     int *tiles;     // token tiles of all experts
-    int4 *rec;      // [tiles] expert, first sorted row, rows of a token tile
+    int4 *rec;      // [tiles] expert, first sorted row, rows of a token tile (a 16-byte load; the fourth word is 0)
     int *src;       // [R] token of a sorted row
     int *pos;       // [R] sorted row of a choice, -1: left out
     int R, k, E, chunks, nt;
@@ -280,41 +280,39 @@ __device__ __forceinline__ void store_columns(const uint32_t (&v)[32], float *ep
         const int r = c0 + 16 * pass + col;    // row of the tile
         const bool live = r < w.rows;
         const size_t row = static_cast<size_t>(w.row0) + r;
-        if constexpr (FIRST) {
-            // 8 channels a thread; four neighbours share a block of 32. silu by __expf and
-            // __fdividef: off by up to (5 + 1.2 |g|) 2^-23 of itself, and 0 below -87.3 where
-            // its size is under 2^-118; E4M3 keeps 2^-4, so this moves a code only next to a
-            // midpoint, as the products' own fp32 sums do. expf and an IEEE division were
-            // measured: 16 tokens 55 -> 64 us, 1111 ragged 105 -> 122, the others 1 to 4 %.
-            const float *g = epi + col * kEpiLd + 8 * part;
-            float a[8];
-            uint32_t amax = 0;
+        // 8 channels a thread; four neighbours share a block of 32. silu by __expf and
+        // __fdividef: off by up to (5 + 1.2 |g|) 2^-23 of itself, and 0 below -87.3 where
+        // its size is under 2^-118; E4M3 keeps 2^-4, so this moves a code only next to a
+        // midpoint, as the products' own fp32 sums do. expf and an IEEE division were
+        // measured: 16 tokens 55 -> 64 us, 1111 ragged 105 -> 122, the others 1 to 4 %.
+        const float *g = epi + col * kEpiLd + 8 * part;
+        float a[8];
+        uint32_t amax = 0;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float4 gv = *reinterpret_cast<const float4 *>(g + 4 * i);
-                const float4 uv = *reinterpret_cast<const float4 *>(g + 64 + 4 * i);
-                a[4 * i] = __fdividef(gv.x, 1.0f + __expf(-gv.x)) * uv.x;
-                a[4 * i + 1] = __fdividef(gv.y, 1.0f + __expf(-gv.y)) * uv.y;
-                a[4 * i + 2] = __fdividef(gv.z, 1.0f + __expf(-gv.z)) * uv.z;
-                a[4 * i + 3] = __fdividef(gv.w, 1.0f + __expf(-gv.w)) * uv.w;
-            }
+        for (int i = 0; i < 2; ++i) {
+            const float4 gv = *reinterpret_cast<const float4 *>(g + 4 * i);
+            const float4 uv = *reinterpret_cast<const float4 *>(g + 64 + 4 * i);
+            a[4 * i] = __fdividef(gv.x, 1.0f + __expf(-gv.x)) * uv.x;
+            a[4 * i + 1] = __fdividef(gv.y, 1.0f + __expf(-gv.y)) * uv.y;
+            a[4 * i + 2] = __fdividef(gv.z, 1.0f + __expf(-gv.z)) * uv.z;
+            a[4 * i + 3] = __fdividef(gv.w, 1.0f + __expf(-gv.w)) * uv.w;
+        }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(a[i]) & 0x7FFFFFFFu);
-            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            const uint32_t b = mxfp8_scale_byte(amax);
-            const float inv = mxfp8_scale_inverse(b);
-            const uint32_t b2 = __shfl_down_sync(0xffffffffu, b, 4);
-            if (live) {
-                uint2 c;
-                c.x = e4m3x4_rn(a[0] * inv, a[1] * inv, a[2] * inv, a[3] * inv);
-                c.y = e4m3x4_rn(a[4] * inv, a[5] * inv, a[6] * inv, a[7] * inv);
-                *reinterpret_cast<uint2 *>(p.act + row * p.I + 64 * w.m + 8 * part) = c;
-                if (part == 0) {
-                    uint8_t *sf = p.act_sf + (static_cast<size_t>(w.tile) * (p.I >> 7) + (w.m >> 1)) * (ntb * 512) +
-                                  (r >> 7) * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4 + (w.m & 1) * 2;
-                    *reinterpret_cast<uint16_t *>(sf) = static_cast<uint16_t>(b | (b2 << 8));
-                }
+        for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(a[i]) & 0x7FFFFFFFu);
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        const uint32_t b = mxfp8_scale_byte(amax);
+        const float inv = mxfp8_scale_inverse(b);
+        const uint32_t b2 = __shfl_down_sync(0xffffffffu, b, 4);
+        if (live) {
+            uint2 c;
+            c.x = e4m3x4_rn(a[0] * inv, a[1] * inv, a[2] * inv, a[3] * inv);
+            c.y = e4m3x4_rn(a[4] * inv, a[5] * inv, a[6] * inv, a[7] * inv);
+            *reinterpret_cast<uint2 *>(p.act + row * p.I + 64 * w.m + 8 * part) = c;
+            if (part == 0) {
+                uint8_t *sf = p.act_sf + (static_cast<size_t>(w.tile) * (p.I >> 7) + (w.m >> 1)) * (ntb * 512) +
+                              (r >> 7) * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4 + (w.m & 1) * 2;
+                *reinterpret_cast<uint16_t *>(sf) = static_cast<uint16_t>(b | (b2 << 8));
             }
         }
         epilogue_sync();   // the staging buffer is reused
@@ -1249,34 +1247,35 @@ inline size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace
 
-bool moe_layout(int64_t T, int k, int E, int64_t H, int64_t I, MoeLayout *out)
+MoeLayout moe_layout(int64_t T, int k, int E, int64_t H, int64_t I)
 {
+    MoeLayout out;
     const int64_t R = T * k;
     // Small tiles stream the weights of an expert once for 32 rows, large ones once for
     // 224 but with less of them in flight. Measured both ways: 256 tokens x 6 over 64
     // experts (24 rows an expert) 122 us small, 139 us large; 1111 x 5 over 40, a third
     // left out (93 rows) 166 us small, 109 us large.
-    out->nt = R <= 32 * static_cast<int64_t>(E) ? kSmallNT : kLargeNT;
-    out->max_tiles = static_cast<int>(R / out->nt + std::min<int64_t>(E, R));
-    out->chunks = static_cast<int>((R + kChunk - 1) / kChunk);
+    out.nt = R <= 32 * static_cast<int64_t>(E) ? kSmallNT : kLargeNT;
+    out.max_tiles = static_cast<int>(R / out.nt + std::min<int64_t>(E, R));
+    out.chunks = static_cast<int>((R + kChunk - 1) / kChunk);
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t here = at;
         at += up256(bytes);
         return here;
     };
-    out->hist = take(out->chunks > 1 ? static_cast<size_t>(out->chunks) * E * 4 : 0);
-    out->tiles = take(4);
-    out->rec = take(static_cast<size_t>(out->max_tiles) * 16);
-    out->src = take(static_cast<size_t>(R) * 4);
-    out->pos = take(static_cast<size_t>(R) * 4);
-    out->act = take(static_cast<size_t>(R) * I);
-    out->act_sf = take(static_cast<size_t>(out->max_tiles) * (I / 128) * ((out->nt + 127) / 128) * 512);
-    out->y = take(static_cast<size_t>(R) * H * 4);
-    out->xs = take(out->nt == kLargeNT ? static_cast<size_t>(R) * H : 0);
-    out->xs_sf = take(out->nt == kLargeNT ? static_cast<size_t>(out->max_tiles) * (H / 128) * 1024 : 0);
-    out->total = at;
-    return true;
+    out.hist = take(out.chunks > 1 ? static_cast<size_t>(out.chunks) * E * 4 : 0);
+    out.tiles = take(4);
+    out.rec = take(static_cast<size_t>(out.max_tiles) * 16);
+    out.src = take(static_cast<size_t>(R) * 4);
+    out.pos = take(static_cast<size_t>(R) * 4);
+    out.act = take(static_cast<size_t>(R) * I);
+    out.act_sf = take(static_cast<size_t>(out.max_tiles) * (I / 128) * ((out.nt + 127) / 128) * 512);
+    out.y = take(static_cast<size_t>(R) * H * 4);
+    out.xs = take(out.nt == kLargeNT ? static_cast<size_t>(R) * H : 0);
+    out.xs_sf = take(out.nt == kLargeNT ? static_cast<size_t>(out.max_tiles) * (H / 128) * 1024 : 0);
+    out.total = at;
+    return out;
 }
 
 cudaError_t launch_moe_experts(const MoeArgs &a, const MoeLayout &l, cudaStream_t stream)
