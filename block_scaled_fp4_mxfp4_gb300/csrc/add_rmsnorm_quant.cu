@@ -5,11 +5,13 @@
 // the quotients. h is rounded to the element type before it is squared: the
 // norm is that of the values the next layer reads.
 //
-// Bound: HBM (2 or 4 bytes read, 1 to 5 written an element; ~12 operations). So
-// each row is read once: a block keeps its row in registers between the sum of
-// squares and the quantization, eight elements (one 16-byte vector) a lane, and
-// four neighbouring lanes hold one block of 32. Measured: 4096 x 7168 bf16 with
-// residual, h and y (265 MB) 54 us, 4.9 TB/s; one row 4.3 us.
+// Bound: instructions and their latency (45 an element, with the exactness below, in
+// 68 % of the cycles), not far above HBM (2 or 4 bytes read, 1 to 5 written an
+// element). Each row is read once: a block keeps its row in registers between the sum
+// of squares and the quantization, eight elements (one 16-byte vector) a lane, and
+// four neighbouring lanes hold one block of 32. The variant of four vectors a lane has
+// 40 registers, so that six blocks fit an SM, and spills a few. Measured: 4096 x 7168 bf16 with
+// residual, h and y (265 MB) 54 us, 4.9 TB/s; one row 4.2 us.
 //
 // Exactness: an E4M3 rounding turns an fp32 error of 2^-23 into a step of 2^-3 where
 // a value lies next to a midpoint, about one element in a million. So the sum of

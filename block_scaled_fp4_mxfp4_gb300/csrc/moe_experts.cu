@@ -30,7 +30,8 @@
 // Bound: few rows an expert, the weights' bytes from HBM; many, the tensor core and
 // the shared memory that feeds it. Measured whole (hidden size 7168, intermediate
 // 2048, 32 experts, 8 choices): 1 token 53 us (187 MB, 28 us at the copy bandwidth),
-// 4096 tokens 1.23 ms (2.9 TFLOP; product 1 at 3.0 PFLOP/s).
+// 4096 tokens 1.32 ms called one after another, 1.28 ms in a graph (2.9 TFLOP; product 1
+// at 3.1 PFLOP/s).
 #include <algorithm>
 #include <cstring>
 
@@ -1254,7 +1255,8 @@ MoeLayout moe_layout(int64_t T, int k, int E, int64_t H, int64_t I)
     // Small tiles stream the weights of an expert once for 32 rows, large ones once for
     // 224 but with less of them in flight. Measured both ways: 256 tokens x 6 over 64
     // experts (24 rows an expert) 122 us small, 139 us large; 1111 x 5 over 40, a third
-    // left out (93 rows) 166 us small, 109 us large.
+    // left out (93 rows) 166 us small, 109 us large; the border lies between and was not
+    // measured. Choices that are left out count as rows, since only the GPU knows them.
     out.nt = R <= 32 * static_cast<int64_t>(E) ? kSmallNT : kLargeNT;
     out.max_tiles = static_cast<int>(R / out.nt + std::min<int64_t>(E, R));
     out.chunks = static_cast<int>((R + kChunk - 1) / kChunk);

@@ -26,10 +26,10 @@
 // divisions, from the chosen logits: they only scale rows that go into an fp32 sum
 // (off from 64 bits by 6e-8 of their size, where one rounding costs 3e-8).
 //
-// Measured: 16384 x 256 fp32, sigmoid, bias, 4 of 8 groups, 8 experts: 24 us (1200
-// instructions a token, issued in 70 % of the cycles; the logits alone are 2.5 us of
+// Measured: 16384 x 256 fp32, sigmoid, bias, 4 of 8 groups, 8 experts: 24 us (1130
+// instructions a token, issued in 73 % of the cycles; the logits alone are 2.5 us of
 // HBM time; 21 us without any 64-bit decision; 39 us when each round searched
-// its lane's keys). 3001 x 60: 6.9 us. One token: 3.5 us.
+// its lane's keys). 3001 x 60: 6.5 us. One token: 3.2 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
