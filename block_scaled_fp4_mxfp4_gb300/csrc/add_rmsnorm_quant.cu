@@ -66,12 +66,12 @@ __device__ __forceinline__ Two two_add(const Two &a, const Two &b)
     return Two{s, __fadd_rn(e, __fadd_rn(a.lo, b.lo))};
 }
 
-// sqrt(K / m), m < kHuge: rsqrt and one Newton step on its exact residual.
+// sqrt(K / m) of an ordinary sum, or 0 or NaN: rsqrt and one Newton step on its exact
+// residual.
 __device__ __forceinline__ Two reciprocal_rms(const Two &m, const NormParams &p)
 {
+    if (!(m.hi > 0.0f)) return Two{m.hi, 0.0f};
     const float q = rsqrtf(m.hi);
-    // below this the residual leaves fp32 (a vanishing sum)
-    if (!(m.hi > 1e-30f)) return Two{m.hi == 0.0f ? 0.0f : q * p.rootk_hi, 0.0f};
     const float s = q * q, se = fmaf(q, q, -s);
     const float t = fmaf(-m.hi, s, 1.0f) - fmaf(m.hi, se, m.lo * s);
     const float hi = q * p.rootk_hi;
@@ -80,9 +80,9 @@ __device__ __forceinline__ Two reciprocal_rms(const Two &m, const NormParams &p)
     return Two{r, lo - (r - hi)};
 }
 
-// Sums from here on, whose squares, reciprocal or its residual may leave fp32 (bf16
-// values above 10^13, or a huge eps), take the way of finish_huge_row.
-constexpr float kHuge = 1e30f;
+// Sums whose squares, reciprocal or its residual may leave fp32 (bf16 values above 10^13
+// or below 10^-15, or an eps as far out) take the way of finish_far_row.
+__device__ __forceinline__ bool is_far(const Two &m) { return m.hi >= 1e30f || (m.hi > 0.0f && m.hi <= 1e-30f); }
 
 // 16 bytes that this kernel reads once. Not through the read-only path: the sum may
 // be written over them.
@@ -316,11 +316,11 @@ __device__ __forceinline__ uint4 load_h(const NormParams &p, int64_t row, int v)
     return a;
 }
 
-// The rest of a row whose sum of squares is kHuge or more, with that sum taken again in
-// 64 bits. `stored`: h is in H already (each thread's own vectors). An infinite value
-// makes r = 0, so it becomes NaN and the finite ones 0. Seldom, so kept out of line.
+// The rest of a row whose sum of squares is_far, with that sum taken again in 64 bits.
+// `stored`: h is in H already (each thread's own vectors). An infinite value makes
+// r = 0, so it becomes NaN and the finite ones 0. Seldom, so kept out of line.
 template <bool F16>
-__device__ __noinline__ void finish_huge_row(const NormParams &p, int64_t row, bool stored, double *buf)
+__device__ __noinline__ void finish_far_row(const NormParams &p, int64_t row, bool stored, double *buf)
 {
     const int nvec = p.K >> 3, nt = blockDim.x, nw = nt >> 5, lane = threadIdx.x & 31;
     auto load = [&](int v) { return stored ? ld_row(p.h + row * p.ldh + 8 * v) : load_h<F16>(p, row, v); };
@@ -340,7 +340,9 @@ __device__ __noinline__ void finish_huge_row(const NormParams &p, int64_t row, b
     __syncthreads();
     ss = 0.0;
     for (int i = 0; i < nw; ++i) ss += buf[i];
-    const double r64 = 0x1p64 * sqrt(p.K / (ss + static_cast<double>(p.eps) * p.K));
+    const double m = ss + static_cast<double>(p.eps) * p.K;
+    const bool huge = m > 1.0;      // the same in all threads
+    const double r64 = (huge ? 0x1p64 : 1.0) * sqrt(p.K / m);
     const float hi = static_cast<float>(r64);
     const Two r{hi, static_cast<float>(r64 - hi)};
     for (int v0 = threadIdx.x & ~31; v0 < nvec; v0 += nt) {
@@ -350,7 +352,10 @@ __device__ __noinline__ void finish_huge_row(const NormParams &p, int64_t row, b
             hv = load(v);
             if (p.h && !stored) *reinterpret_cast<uint4 *>(p.h + row * p.ldh + 8 * v) = hv;
         }
-        finish8<F16, true>(p, row, v, v < nvec, hv, r);
+        if (huge)
+            finish8<F16, true>(p, row, v, v < nvec, hv, r);
+        else
+            finish8<F16>(p, row, v, v < nvec, hv, r);
     }
 }
 
@@ -384,8 +389,8 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 6 : 1) add_r
             }
         }
         const Two m = two_add(block_sum(total(ss), buf), keps);
-        if (m.hi >= kHuge) {
-            finish_huge_row<F16>(p, row, p.h != nullptr, buf64);
+        if (is_far(m)) {
+            finish_far_row<F16>(p, row, p.h != nullptr, buf64);
         } else {
             const Two r = reciprocal_rms(m, p);
 #pragma unroll
@@ -397,8 +402,8 @@ __global__ void __launch_bounds__(MAX_THREADS, MAX_THREADS == 256 ? 6 : 1) add_r
     } else {
         for (int v = threadIdx.x; v < nvec; v += nt) add_squares8<F16>(ss, load_h<F16>(p, row, v));
         const Two m = two_add(block_sum(total(ss), buf), keps);
-        if (m.hi >= kHuge) {
-            finish_huge_row<F16>(p, row, false, buf64);
+        if (is_far(m)) {
+            finish_far_row<F16>(p, row, false, buf64);
         } else {
             const Two r = reciprocal_rms(m, p);
             for (int v0 = threadIdx.x & ~31; v0 < nvec; v0 += nt) {

@@ -39,9 +39,9 @@ extern "C" {
 
 /* Residual sum, RMSNorm and MXFP8 quantization of rows X [M, K] (bf16 or fp16):
  *   h   = X + residual, in fp32, rounded to the element type (residual NULL: h = X)
- *   r   = 1 / sqrt(mean_k(h_k^2) + eps), good to 2^-42, for rows of any finite size (squares
- *         below 2^-149 count as 0; r = 0 where that mean + eps is 0; an infinite h gives
- *         NaN in its place and zeros in the rest of its row)
+ *   r   = 1 / sqrt(mean_k(h_k^2) + eps), good to 2^-42, for rows of any finite size; r = 0
+ *         where every h_k^2 is below fp32 (2^-149) and K eps too; an infinite h gives NaN in
+ *         its place and zeros in the rest of its row
  *   y_k = h_k * r * weight_k (Y: in fp32, then rounded)
  *   Aq, A_sf = MXFP8 of y (see above), the codes and scales of 64-bit arithmetic;
  *         pad cells of A_sf are written with 0x7F.

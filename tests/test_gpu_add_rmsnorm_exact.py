@@ -160,3 +160,22 @@ def test_an_eps_beyond_the_squares(dtype, eps):
     x, _, w = rows(9, 7168, dtype, 3, plain)
     eps = float(torch.tensor(eps))
     check(x, None, w, eps)
+
+
+@pytest.mark.parametrize("M,K", [(6, 256), (9, 7168), (400, 2112), (400, 7168), (6, 33024)])
+@pytest.mark.parametrize("eps", [0.0, 1e-38])
+def test_rows_whose_squares_nearly_vanish(M, K, eps):
+    """Sums of squares far below one, among them subnormal ones and such that lose most of their squares in fp32."""
+    x, _, w = rows(M, K, torch.bfloat16, M * K, some_channels)
+    down = torch.exp2(torch.tensor([0.0, -45, -55, -60, -66, -70], device="cuda"))[torch.arange(M, device="cuda") % 6]
+    x = (x.float() * down[:, None]).to(torch.bfloat16)
+    x[::6, 3] = 2.0 ** -70                                     # an ordinary row with such a value
+    assert bool((x.float().square().sum(-1) > 0).all())
+    check(x, None, w, eps)
+    H = torch.zeros_like(x)
+    q, sf, _, Y = mx.mxfp8_add_rmsnorm_quantize(x, w, eps, residual=torch.zeros_like(x), H=H, want_y=True)
+    assert torch.equal(H, x)
+    plain = mx.mxfp8_add_rmsnorm_quantize(x, w, eps)
+    assert torch.equal(q, plain[0]) and torch.equal(sf, plain[1])
+    _, y = moe_ref.add_rmsnorm(x, None, w, eps)
+    assert bool(((Y.double() - y).abs() <= (2.0 ** -8 + 2.0 ** -21) * y.abs() + 2.0 ** -134).all())
