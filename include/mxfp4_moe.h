@@ -43,8 +43,8 @@ extern "C" {
  *         where every h_k^2 is below fp32 (2^-149) and K eps too; an infinite h gives NaN in
  *         its place and zeros in the rest of its row
  *   y_k = h_k * r * weight_k (Y: in fp32, then rounded)
- *   Aq, A_sf = MXFP8 of y (see above), the codes and scales of 64-bit arithmetic;
- *         pad cells of A_sf are written with 0x7F.
+ *   Aq, A_sf = MXFP8 of y (see above), the codes and scales of 64-bit arithmetic (values
+ *         of y below 2^-126: of fp32); pad cells of A_sf are written with 0x7F.
  *   X, residual, weight, H, Y : element type `dtype` (MXFP4_DTYPE_BF16 / _FP16).
  *   weight : [K], 16-byte aligned.
  *   H   : out, [M, K], h (NULL: not stored). May be X or residual itself (same
