@@ -1,4 +1,5 @@
-"""Python binding of libmxfp4 (the C ABI in include/mxfp4.h and include/mxfp4_moe.h).
+"""Python binding of libmxfp4 (the C ABI in include/mxfp4.h, include/mxfp4_moe.h and
+include/mxfp4_layer.h).
 
 Argument marshalling only: every function passes device pointers, sizes and the
 current CUDA stream to the library entry point of the same name and raises
@@ -23,6 +24,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libmxfp4.so")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "mxfp4.h")
 MOE_HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "mxfp4_moe.h")
+LAYER_HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "mxfp4_layer.h")
 
 _i64 = ctypes.c_int64
 _p = ctypes.c_void_p
@@ -142,6 +144,13 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.mxfp4_moe_experts_workspace_bytes.argtypes = [_i64, _i, _i, _i64, _i64]
     L.mxfp4_moe_experts.restype = _st
     L.mxfp4_moe_experts.argtypes = [_p, _i64, _p, _p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i, _i, _i64, _i64, _p, _sz, _p]
+    L.lora_workspace_bytes.restype = _sz
+    L.lora_workspace_bytes.argtypes = [_i64, _i64, _i, _i]
+    L.lora_add.restype = _st
+    L.lora_add.argtypes = [_p, _i64, _p, _p, _p, _p, _p, _p, _i64, _i, _p, _i64, _i64, _i64, _i64, _i, _i, _p, _sz, _p]
+    L.qk_norm_rope.restype = _st
+    L.qk_norm_rope.argtypes = [_p, _i64, _i64, _p, _i64, _i64, _p, _p, _p, _p, _i, _i, _f, _i64, _i, _i, _i, _i, _i, _i64,
+                               _p, _i64, _i64, _p, _i64, _i64, _p]
     return L
 
 
@@ -624,6 +633,114 @@ def mxfp4_moe_experts(Xq, X_sf, ids, weights, W13q, W13_sf, W2q, W2_sf, out=None
                                   _scales(workspace, "workspace", 0), workspace.numel(), _stream_of(stream, Xq)),
            "mxfp4_moe_experts")
     return out
+
+
+# ------------------------------------------------ around the attention --
+
+def _same_device(t, *others):
+    """All of a call's tensors lie on the device of `t`, and that is the current one: the library launches there."""
+    i = t.get_device()
+    for o in others:
+        if o is not None and o.get_device() != i:
+            raise ValueError(f"tensors on different devices: {t.device} and {o.device}")
+    if i != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def lora_workspace_bytes(T: int, K: int, R: int, L: int) -> int:
+    return int(_lib.lora_workspace_bytes(T, K, R, L))
+
+
+def lora_workspace(T: int, K: int, R: int, L: int, device="cuda") -> torch.Tensor:
+    """A workspace for lora_add with up to T tokens, width K, rank R and L adapters (no initialisation needed)."""
+    return torch.empty(max(1, lora_workspace_bytes(T, K, R, L)), dtype=torch.uint8, device=device)
+
+
+def lora_add(base, X, A, B, ids, scales=None, ranks=None, C=None, workspace=None, stream=None):
+    """C = base + scales[a] * (X A[a]^T) B[a]^T with a = ids[t] for each token (see
+    include/mxfp4_layer.h): base [T, N] bf16 or fp16, what a shared projection of bf16
+    X [T, K] gave; adapters A [L, R, K] and B [L, N, R] bf16; ids [T] int32, outside
+    [0, L) for a token without an adapter; scales [L] fp32, ranks [L] int32. C may be
+    base (in place)."""
+    bf16 = torch.bfloat16
+    if base.dim() != 2 or X.dim() != 2 or A.dim() != 3:
+        raise ValueError("base and X must have 2 dims and A 3")
+    dtype = base.dtype
+    if dtype is not bf16 and dtype is not torch.float16:
+        raise ValueError(f"base must be bf16 or fp16, got {dtype}")
+    T, N = base.shape
+    K = X.shape[1]
+    L, R, _ = A.shape
+    x, ldx = _rows(X, "X", bf16, (T, K))
+    b, ldb = _rows(base, "base", dtype, (T, N))
+    if C is None:
+        C = _output((T, N), dtype, base.device, stream)
+        c, ldc = C.data_ptr(), N
+    else:
+        c, ldc = _rows(C, "C", dtype, (T, N))
+    if workspace is None:
+        workspace = _scratch(torch.empty, max(1, lora_workspace_bytes(T, K, R, L)), base.device, stream)
+    pa, pb = _vec(A, "A", bf16, (L, R, K)), _vec(B, "B", bf16, (L, N, R))
+    pi = _vec(ids, "ids", torch.int32, (T,))
+    ps = _vec(scales, "scales", torch.float32, (L,)) if scales is not None else None
+    pr = _vec(ranks, "ranks", torch.int32, (L,)) if ranks is not None else None
+    ws = _scales(workspace, "workspace", 0)
+    _same_device(base, X, A, B, ids, scales, ranks, C, workspace)
+    _check(_lib.lora_add(x, ldx, pa, pb, pi, ps, pr, b, ldb, _DTYPES[dtype], c, ldc, T, K, N, R, L, ws, workspace.numel(),
+                         _stream_of(stream, base)), "lora_add")
+    return C
+
+
+def _heads(t, name, dtype, T, D):
+    """Address, heads and strides (between tokens, between heads) of a CUDA tensor [T, H, D] of this type."""
+    if not (t.dtype is dtype and t.dim() == 3 and t.shape[0] == T and t.shape[2] == D and t.is_cuda and t.stride(2) == 1):
+        _refuse(t, name, dtype, (T, "H", D), "row-major")
+    H = t.shape[1]
+    # strides of dimensions of size one are no distances: torch may give any value
+    return t.data_ptr(), H, t.stride(0) if T > 1 else 0, t.stride(1) if H > 1 else 0
+
+
+def qk_norm_rope(q, k, table=None, positions=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """Norm of each head of q [T, Hq, D] and k [T, Hk, D] (bf16 or fp16) and their
+    rotation by `positions` [T] (int32 or int64) in one pass (see
+    include/mxfp4_layer.h) -> (q_out, k_out). `table` fp32 [P, rot] holds the cosines
+    and sines of every position (None: no rotation), q_weight and k_weight [D] the
+    norms' weights (None: no norm). Views of a joint projection need no copy; an
+    output may be its own input."""
+    if q.dim() != 3:
+        raise ValueError(f"q must have 3 dims, got {tuple(q.shape)}")
+    dtype = q.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise ValueError(f"q must be bf16 or fp16, got {dtype}")
+    T, _, D = q.shape
+    pq, Hq, q_st, q_sh = _heads(q, "q", dtype, T, D)
+    pk, Hk, k_st, k_sh = _heads(k, "k", dtype, T, D)
+    if q_out is None:
+        q_out = _output((T, Hq, D), dtype, q.device, stream)
+    if k_out is None:
+        k_out = _output((T, Hk, D), dtype, q.device, stream)
+    po, ho, qo_st, qo_sh = _heads(q_out, "q_out", dtype, T, D)
+    pp, hp, ko_st, ko_sh = _heads(k_out, "k_out", dtype, T, D)
+    if ho != Hq or hp != Hk:
+        raise ValueError(f"outputs have {ho} and {hp} heads, inputs {Hq} and {Hk}")
+    pt, pos, P, rot, pos64 = None, None, 0, 0, 0
+    if table is not None:
+        if table.dim() != 2:
+            raise ValueError(f"table must have 2 dims, got {tuple(table.shape)}")
+        if positions is None or positions.dtype not in (torch.int32, torch.int64):
+            raise ValueError("positions must be given with a table, in int32 or int64")
+        P, rot = table.shape
+        pt = _vec(table, "table", torch.float32, (P, rot))
+        pos = _vec(positions, "positions", positions.dtype, (T,))
+        pos64 = 1 if positions.dtype is torch.int64 else 0
+    wq = _vec(q_weight, "q_weight", dtype, (D,)) if q_weight is not None else None
+    wk = _vec(k_weight, "k_weight", dtype, (D,)) if k_weight is not None else None
+    _same_device(q, k, table, positions if table is not None else None, q_weight, k_weight, q_out, k_out)
+    _check(_lib.qk_norm_rope(pq, q_st, q_sh, pk, k_st, k_sh, wq, wk, pt, pos, pos64, _DTYPES[dtype], eps, T, Hq, Hk, D,
+                             rot, 1 if interleaved else 0, P, po, qo_st, qo_sh, pp, ko_st, ko_sh, _stream_of(stream, q)),
+           "qk_norm_rope")
+    return q_out, k_out
 
 
 def _plan_dict(p: Plan) -> dict:

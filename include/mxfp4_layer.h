@@ -1,0 +1,80 @@
+/*
+ * mxfp4_layer.h -- the calls of libmxfp4 (GB300, sm_103a) around a decoder
+ * layer's attention when many requests are served at once: low-rank adapters
+ * beside a shared projection, and the norm and rotation of queries and keys.
+ *
+ * The conventions of mxfp4_moe.h hold for every call here (device pointers,
+ * caller-owned memory, no allocation and no synchronization, work enqueued on
+ * `stream`, arguments checked on the host before anything is enqueued, zero
+ * tokens enqueue nothing and give MXFP4_OK, and every input is read in stream
+ * order). Element types are the MXFP4_DTYPE_ constants of that header.
+ */
+#ifndef MXFP4_LAYER_GB300_H
+#define MXFP4_LAYER_GB300_H
+
+#include "mxfp4_moe.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define LORA_MAX_ADAPTERS 4096
+#define LORA_MAX_RANK 256
+
+/* Workspace bytes of lora_add for T tokens of width K and L adapters of rank up
+ * to R (0 for sizes that it refuses). It grows with each of the four: one made
+ * for the largest serves smaller ones too. */
+MXFP4_API size_t lora_workspace_bytes(int64_t T, int64_t K, int R, int L);
+
+/* Low-rank adapters of many requests beside a projection they share: for every
+ * token t whose adapter is a = ids[t],
+ *   C[t, n] = round( base[t, n] + scales[a] * sum_{r < ranks[a]} u[r] * B[a, n, r] ),
+ *   u[r]    = sum_k X[t, k] * A[a, r, k],
+ * both sums in fp32 and one rounding, to C's type; between the products u is
+ * held to 2^-17 of itself (as two bf16). A token whose id is outside [0, L) has
+ * no adapter: its row of C is that of base. Elements of A and B at or beyond an
+ * adapter's rank are not used, whatever they hold.
+ *   X      : bf16 [T, K], row stride ldx.     base, C : [T, N] of type dtype (bf16 or fp16),
+ *            row strides ldb and ldc; C may be base itself (same pointer and stride).
+ *   A      : bf16 [L, R, K], contiguous.      B : bf16 [L, N, R], contiguous.
+ *   ids    : int32 [T], in any order.         scales : fp32 [L] or NULL (1).
+ *   ranks  : int32 [L] or NULL (all R); taken as 0 below 0 and as R above R.
+ * T >= 0; 1 <= L <= LORA_MAX_ADAPTERS; R a multiple of 8 up to LORA_MAX_RANK; K and N
+ * positive multiples of 8; T, K and N below 2^31. Strides in elements, multiples of 8;
+ * X, base, C, A, B 16-byte aligned; ids, scales, ranks 4; workspace 256. The
+ * workspace needs no initialisation and keeps nothing from one call for the next;
+ * calls that share one must not overlap. */
+MXFP4_API mxfp4_status_t lora_add(const void *X, int64_t ldx, const void *A, const void *B, const int32_t *ids,
+                                  const float *scales, const int32_t *ranks, const void *base, int64_t ldb, int dtype,
+                                  void *C, int64_t ldc, int64_t T, int64_t K, int64_t N, int R, int L, void *workspace,
+                                  size_t ws_bytes, void *stream);
+
+/* Norm and rotation of queries and keys, one pass: for every token t and head x of
+ * q [T, Hq, D] and k [T, Hk, D],
+ *   y   = x / sqrt(mean(x^2) + eps) * weight     (weight NULL: y = x)
+ *   out = y with the pairs (y_i, y_j) of its first `rot` elements turned by the token's angle i:
+ *         (y_i cos - y_j sin, y_j cos + y_i sin),  j = i + rot / 2, or with `interleaved`
+ *         the pair i is (2i, 2i + 1),
+ * in fp32 with one rounding. Rows of any finite size are normalized; where mean + eps is 0 the
+ * result is 0; an infinite x gives NaN in its place and its pair's, and zeros in the rest of its head.
+ *   table     : fp32 [P, rot], row p: the rot / 2 cosines, then the rot / 2 sines of position p.
+ *   positions : int32 [T] (pos64 0) or int64 [T] (pos64 1). A position outside [0, P) gives
+ *               NaN in all of its token's outputs.
+ *   q, k, q_out, k_out : type dtype (bf16 or fp16), rows of D; strides in elements between
+ *               tokens (st) and heads (sh), any multiples of 8, so that views of a joint
+ *               projection need no copy. An output may be its own input (same pointer and strides).
+ *   q_weight, k_weight : type dtype [D], or NULL.
+ * T, Hq, Hk >= 0 (zero heads: that tensor is not touched); D a positive multiple of 8 up to 256;
+ * 0 <= rot <= D, a multiple of 16, with `interleaved` of 8 (rot 0: no table and no positions);
+ * T * (Hq + Hk) < 2^31; eps finite and >= 0. Tensors, weights and table 16-byte aligned. */
+MXFP4_API mxfp4_status_t qk_norm_rope(const void *q, int64_t q_st, int64_t q_sh, const void *k, int64_t k_st,
+                                      int64_t k_sh, const void *q_weight, const void *k_weight, const float *table,
+                                      const void *positions, int pos64, int dtype, float eps, int64_t T, int Hq, int Hk,
+                                      int D, int rot, int interleaved, int64_t P, void *q_out, int64_t qo_st,
+                                      int64_t qo_sh, void *k_out, int64_t ko_st, int64_t ko_sh, void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* MXFP4_LAYER_GB300_H */
