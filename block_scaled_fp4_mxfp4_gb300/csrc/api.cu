@@ -870,8 +870,9 @@ mxfp4_status_t mxfp4_get_device_error(int *code)
     const int f = read_and_clear_fused_error();
     const int pg = read_and_clear_gemm_pair_error();
     const int me = read_and_clear_moe_error();
-    if (g < 0 || f < 0 || pg < 0 || me < 0) return MXFP4_ERR_CUDA;
-    *code = g != 0 ? g : (f != 0 ? 16 + f : (pg != 0 ? 32 + pg : (me != 0 ? 48 + me : 0)));
+    const int mf = read_and_clear_moe_few_error();
+    if (g < 0 || f < 0 || pg < 0 || me < 0 || mf < 0) return MXFP4_ERR_CUDA;
+    *code = g != 0 ? g : (f != 0 ? 16 + f : (pg != 0 ? 32 + pg : (me != 0 ? 48 + me : (mf != 0 ? 64 + mf : 0))));
     return MXFP4_OK;
 }
 

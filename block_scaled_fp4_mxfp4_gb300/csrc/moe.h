@@ -60,4 +60,27 @@ struct MoeArgs {
 cudaError_t launch_moe_experts(const MoeArgs &a, const MoeLayout &l, cudaStream_t stream);
 int read_and_clear_moe_error();
 
+// -------------------------------------------------------------- moe_few.cu
+// The whole layer for up to kMoeFewTokens tokens: one MMA of 8 columns, or two.
+constexpr int kMoeFewTokens = 16;
+struct MoeFewLayout {
+    size_t counters, h, part, part_ss, xh, sx, ids, weights, act, act_sx, y, total;
+};
+MoeFewLayout moe_few_layout(int64_t T, int k, int E, int64_t H, int64_t I);
+
+struct MoeFewArgs {
+    const uint16_t *x, *res, *w, *router;
+    uint16_t *h_out, *out;
+    int64_t ldx, ldr, ldh, ldo;
+    const uint8_t *w13_sf, *w2_sf;
+    RouteParams route;      // logits, ldl and T unused; ids and weights may be null
+    int T, H, I;
+    float eps;
+    uint8_t *ws;
+    CUtensorMap tm_w13;     // packed weights [E * 2I, H / 2] u8, box 128 bytes x 32 rows
+    CUtensorMap tm_w2;      // the same of [E * H, I / 2], box 64 rows
+};
+cudaError_t launch_moe_few(const MoeFewArgs &a, const MoeFewLayout &l, cudaStream_t stream);
+int read_and_clear_moe_few_error();
+
 }  // namespace mxfp4

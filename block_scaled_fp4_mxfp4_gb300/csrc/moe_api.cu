@@ -1,11 +1,12 @@
-// extern "C" entry points of include/mxfp4_moe.h: argument validation, tensor
-// maps and workspace layout. Nothing here allocates device memory or
+// extern "C" entry points of include/mxfp4_moe.h, and mxfp4_moe_layer of
+// include/mxfp4_layer.h: argument validation, tensor maps and workspace layout. Nothing here allocates device memory or
 // synchronizes.
 #include <cmath>
 #include <cstring>
 
 #include "internal.h"
 #include "moe.h"
+#include "mxfp4_layer.h"
 #include "mxfp4_moe.h"
 
 using namespace mxfp4;
@@ -156,6 +157,76 @@ mxfp4_status_t mxfp4_moe_experts(const void *Xq, int64_t ldx, const void *X_sf, 
                block_map(&a.tm_act_sf, a.ws + l.act_sf, int64_t(l.max_tiles) * (I / 128) * 2);
     if (!maps) return MXFP4_ERR_CUDA;
     return cuda_status(launch_moe_experts(a, l, static_cast<cudaStream_t>(stream)));
+}
+
+size_t mxfp4_moe_layer_workspace_bytes(int64_t T, int k, int E, int64_t H, int64_t I)
+{
+    if (check_moe_sizes(T, k, E, H, I) != MXFP4_OK || T == 0 || T > MOE_LAYER_MAX_TOKENS) return 0;
+    return moe_few_layout(T, k, E, H, I).total;
+}
+
+mxfp4_status_t mxfp4_moe_layer(const void *X, int64_t ldx, const void *residual, int64_t ldr, const void *weight,
+                               float eps, const void *router, const float *bias, int score, int groups, int topk_groups,
+                               int group_top, int k, int renormalize, float scale, const void *W13q, const void *W13_sf,
+                               const void *W2q, const void *W2_sf, void *H, int64_t ldh, void *out, int64_t ldo,
+                               int32_t *ids, float *out_weights, int64_t T, int E, int64_t Hd, int64_t I, void *workspace,
+                               size_t ws_bytes, void *stream)
+{
+    static_assert(kMoeFewTokens == MOE_LAYER_MAX_TOKENS, "one limit");
+    if (!(eps >= 0.0f) || std::isinf(eps) || !std::isfinite(scale)) return MXFP4_ERR_INVALID_ARG;
+    if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) return MXFP4_ERR_INVALID_ARG;
+    if (groups < 1 || topk_groups < 1 || topk_groups > groups || (group_top != 1 && group_top != 2))
+        return MXFP4_ERR_INVALID_ARG;
+    const mxfp4_status_t st = check_moe_sizes(T, k, E, Hd, I);
+    if (st != MXFP4_OK) return st;
+    if (T > MOE_LAYER_MAX_TOKENS || E % groups != 0 || k > topk_groups * (E / groups)) return MXFP4_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0) return MXFP4_OK;
+    if (!X || !weight || !router || !W13q || !W13_sf || !W2q || !W2_sf || !out || !workspace) return MXFP4_ERR_INVALID_ARG;
+    if (ldx < Hd || ldo < Hd || (residual && ldr < Hd) || (H && ldh < Hd)) return MXFP4_ERR_INVALID_ARG;
+    if (H && (H == out || (H == X && ldh != ldx) || (H == residual && ldh != ldr))) return MXFP4_ERR_INVALID_ARG;
+    if (ldx % 8 || ldo % 8 || (residual && ldr % 8) || (H && ldh % 8) || !aligned(X, 16) || !aligned(residual, 16) ||
+        !aligned(H, 16) || !aligned(out, 16) || !aligned(weight, 16) || !aligned(router, 16) || !aligned(bias, 4) ||
+        !aligned(W13q, 32) || !aligned(W2q, 32) || !aligned(W13_sf, 16) || !aligned(W2_sf, 16) || !aligned(ids, 4) ||
+        !aligned(out_weights, 4) || !aligned(workspace, 256))
+        return MXFP4_ERR_MISALIGNED;
+    const MoeFewLayout l = moe_few_layout(T, k, E, Hd, I);
+    if (ws_bytes < l.total) return MXFP4_ERR_WORKSPACE_TOO_SMALL;
+    int sms = 0;
+    if (!current_device_sms(&sms)) return MXFP4_ERR_NO_DEVICE;
+    MoeFewArgs a;
+    memset(&a, 0, sizeof(a));
+    a.x = static_cast<const uint16_t *>(X);
+    a.res = static_cast<const uint16_t *>(residual);
+    a.w = static_cast<const uint16_t *>(weight);
+    a.router = static_cast<const uint16_t *>(router);
+    a.h_out = static_cast<uint16_t *>(H);
+    a.out = static_cast<uint16_t *>(out);
+    a.ldx = ldx;
+    a.ldr = ldr;
+    a.ldh = ldh;
+    a.ldo = ldo;
+    a.w13_sf = static_cast<const uint8_t *>(W13_sf);
+    a.w2_sf = static_cast<const uint8_t *>(W2_sf);
+    a.route.bias = bias;
+    a.route.ids = ids;
+    a.route.weights = out_weights;
+    a.route.E = E;
+    a.route.k = k;
+    a.route.groups = groups;
+    a.route.topk_groups = topk_groups;
+    a.route.group_top = group_top;
+    a.route.sigmoid = score == MOE_SCORE_SIGMOID;
+    a.route.renorm = renormalize != 0;
+    a.route.scale = scale;
+    a.T = static_cast<int>(T);
+    a.H = static_cast<int>(Hd);
+    a.I = static_cast<int>(I);
+    a.eps = eps;
+    a.ws = static_cast<uint8_t *>(workspace);
+    if (!encode_packed_map(W13q, Hd / 2, 2 * I * E, Hd / 2, 32, &a.tm_w13) ||
+        !encode_packed_map(W2q, I / 2, Hd * E, I / 2, 64, &a.tm_w2))
+        return MXFP4_ERR_CUDA;
+    return cuda_status(launch_moe_few(a, l, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

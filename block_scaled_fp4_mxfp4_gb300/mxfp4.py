@@ -151,6 +151,11 @@ def _load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.qk_norm_rope.restype = _st
     L.qk_norm_rope.argtypes = [_p, _i64, _i64, _p, _i64, _i64, _p, _p, _p, _p, _i, _i, _f, _i64, _i, _i, _i, _i, _i, _i64,
                                _p, _i64, _i64, _p, _i64, _i64, _p]
+    L.mxfp4_moe_layer_workspace_bytes.restype = _sz
+    L.mxfp4_moe_layer_workspace_bytes.argtypes = [_i64, _i, _i, _i64, _i64]
+    L.mxfp4_moe_layer.restype = _st
+    L.mxfp4_moe_layer.argtypes = [_p, _i64, _p, _i64, _p, _f, _p, _p, _i, _i, _i, _i, _i, _i, _f, _p, _p, _p, _p, _p, _i64,
+                                  _p, _i64, _p, _p, _i64, _i, _i64, _i64, _p, _sz, _p]
     return L
 
 
@@ -741,6 +746,74 @@ def qk_norm_rope(q, k, table=None, positions=None, q_weight=None, k_weight=None,
                              rot, 1 if interleaved else 0, P, po, qo_st, qo_sh, pp, ko_st, ko_sh, _stream_of(stream, q)),
            "qk_norm_rope")
     return q_out, k_out
+
+
+MOE_LAYER_MAX_TOKENS = 16
+
+
+def moe_layer_workspace_bytes(T: int, k: int, E: int, H: int, I: int) -> int:
+    return int(_lib.mxfp4_moe_layer_workspace_bytes(T, k, E, H, I))
+
+
+def moe_layer_workspace(T: int, k: int, E: int, H: int, I: int, device="cuda") -> torch.Tensor:
+    """A workspace for mxfp4_moe_layer with up to T tokens (no initialisation needed)."""
+    return torch.empty(max(1, moe_layer_workspace_bytes(T, k, E, H, I)), dtype=torch.uint8, device=device)
+
+
+def mxfp4_moe_layer(X, weight, router, W13q, W13_sf, W2q, W2_sf, k: int, eps: float = 1e-6, residual=None, bias=None,
+                    score: str = "softmax", groups: int = 1, topk_groups: int = 1, group_top: int = 2,
+                    renormalize: bool = True, scale: float = 1.0, H=None, out=None, ids=None, weights=None,
+                    workspace=None, stream=None):
+    """The feed-forward half of a mixture-of-experts layer for up to
+    MOE_LAYER_MAX_TOKENS tokens in one call (see include/mxfp4_layer.h): X [T, Hd]
+    bf16, the norm's weight [Hd], the router's matrix [E, Hd] bf16, and the experts'
+    MXFP4 weights as mxfp4_moe_experts takes them -> (out, h, ids, weights); h is X
+    itself without a residual, unless H is given. H may be X or residual (in place)."""
+    bf16, u8 = torch.bfloat16, torch.uint8
+    if X.dim() != 2 or W13q.dim() != 3:
+        raise ValueError("X must have 2 dims and W13q 3")
+    if score not in MOE_SCORES:
+        raise ValueError(f"score must be one of {sorted(MOE_SCORES)}, got {score!r}")
+    T, Hd = X.shape
+    E, two_i, _ = W13q.shape
+    I = two_i // 2
+    x, ldx = _rows(X, "X", bf16, (T, Hd))
+    res, ldr = _rows(residual, "residual", bf16, (T, Hd)) if residual is not None else (None, 0)
+    if H is not None:
+        h, ldh = _rows(H, "H", bf16, (T, Hd))
+    elif residual is not None:
+        H = _output((T, Hd), bf16, X.device, stream)
+        h, ldh = H.data_ptr(), Hd
+    else:
+        H, h, ldh = X, None, 0
+    if out is not None:
+        o, ldo = _rows(out, "out", bf16, (T, Hd))
+    else:
+        out = _output((T, Hd), bf16, X.device, stream)
+        o, ldo = out.data_ptr(), Hd
+    if ids is not None:
+        pi = _vec(ids, "ids", torch.int32, (T, k))
+    else:
+        ids = _output((T, max(k, 0)), torch.int32, X.device, stream)
+        pi = ids.data_ptr()
+    if weights is not None:
+        pw = _vec(weights, "weights", torch.float32, (T, k))
+    else:
+        weights = _output((T, max(k, 0)), torch.float32, X.device, stream)
+        pw = weights.data_ptr()
+    if workspace is None:
+        workspace = _scratch(torch.empty, max(1, moe_layer_workspace_bytes(T, k, E, Hd, I)), X.device, stream)
+    b = _vec(bias, "bias", torch.float32, (E,)) if bias is not None else None
+    _same_device(X, weight, router, W13q, W13_sf, W2q, W2_sf, residual, bias, H, out, ids, weights, workspace)
+    _check(_lib.mxfp4_moe_layer(x, ldx, res, ldr, _vec(weight, "weight", bf16, (Hd,)), eps,
+                                _vec(router, "router", bf16, (E, Hd)), b, MOE_SCORES[score], groups, topk_groups,
+                                group_top, k, 1 if renormalize else 0, scale, _vec(W13q, "W13q", u8, (E, 2 * I, Hd // 2)),
+                                _scales(W13_sf, "W13_sf", E * _sf_bytes32(2 * I, Hd)),
+                                _vec(W2q, "W2q", u8, (E, Hd, I // 2)), _scales(W2_sf, "W2_sf", E * _sf_bytes32(Hd, I)),
+                                h, ldh, o, ldo, pi, pw, T, E, Hd, I, _scales(workspace, "workspace", 0),
+                                workspace.numel(), _stream_of(stream, X)),
+           "mxfp4_moe_layer")
+    return out, H, ids, weights
 
 
 def _plan_dict(p: Plan) -> dict:

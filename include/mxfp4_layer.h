@@ -1,7 +1,8 @@
 /*
  * mxfp4_layer.h -- the calls of libmxfp4 (GB300, sm_103a) around a decoder
  * layer's attention when many requests are served at once: low-rank adapters
- * beside a shared projection, and the norm and rotation of queries and keys.
+ * beside a shared projection, the norm and rotation of queries and keys, and the
+ * whole mixture-of-experts half of a layer for a few tokens.
  *
  * The conventions of mxfp4_moe.h hold for every call here (device pointers,
  * caller-owned memory, no allocation and no synchronization, work enqueued on
@@ -72,6 +73,45 @@ MXFP4_API mxfp4_status_t qk_norm_rope(const void *q, int64_t q_st, int64_t q_sh,
                                       const void *positions, int pos64, int dtype, float eps, int64_t T, int Hq, int Hk,
                                       int D, int rot, int interleaved, int64_t P, void *q_out, int64_t qo_st,
                                       int64_t qo_sh, void *k_out, int64_t ko_st, int64_t ko_sh, void *stream);
+
+#define MOE_LAYER_MAX_TOKENS 16
+
+/* Workspace bytes of mxfp4_moe_layer (0 for sizes that it refuses). It grows with
+ * T: one made for the largest T serves smaller ones too. */
+MXFP4_API size_t mxfp4_moe_layer_workspace_bytes(int64_t T, int k, int E, int64_t H, int64_t I);
+
+/* The feed-forward half of a mixture-of-experts layer for up to MOE_LAYER_MAX_TOKENS
+ * tokens, in three launches (for more tokens: mxfp8_add_rmsnorm_quantize, the router's
+ * product, moe_route and mxfp4_moe_experts):
+ *   h       = X + residual, in fp32, rounded to bf16 (residual NULL: h = X)
+ *   y       = h / sqrt(mean(h^2) + eps) * weight, in fp32 (0 where mean + eps is 0)
+ *   logits  = y . router^T, of y unrounded, good to 2^-22 of the sum of their terms' sizes
+ *   ids, weights = moe_route of those logits (see there for score .. scale), but decided by
+ *             scores in fp32: where two differ by less than 2^-20 either may come first
+ *   out[t]  = bf16_rne( sum_j weights[t, j] * ( act_j . W2[e]^T ) ),  e = ids[t, j],
+ *   act_j   = MXFP8( silu(q . G[e]^T) * (q . U[e]^T) ),  q = MXFP8(y),
+ * with sums, silu and the order of the weighted sum as in mxfp4_moe_experts; the codes of y
+ * and act are those of fp32 arithmetic. A block of weights with the scale byte 0 counts as
+ * zeros, one with 0xFF gives infinities or NaN. Magnitudes of h, and of h * weight: 0 or 2^-60 to 2^60;
+ * infinities and NaN stay in their tokens.
+ *   X, residual, H : bf16 [T, Hd], row strides ldx, ldr, ldh. H (out, NULL: not stored)
+ *                    may be X or residual itself (same pointer and stride).
+ *   weight : bf16 [Hd].    router : bf16 [E, Hd], contiguous.    bias : fp32 [E] or NULL.
+ *   W13q, W13_sf, W2q, W2_sf : as in mxfp4_moe_experts, Hd and I its H and I.
+ *   out    : bf16 [T, Hd], row stride ldo; may be X or residual where H is not.
+ *   ids, out_weights : out, int32 and fp32 [T, k], or NULL.
+ * 0 <= T <= MOE_LAYER_MAX_TOKENS; the other sizes as in moe_route and mxfp4_moe_experts.
+ * Strides in elements, multiples of 8; X, residual, H, out, weight, router and scales 16-byte
+ * aligned; W13q and W2q 32; workspace 256. eps finite and >= 0. The workspace needs
+ * no initialisation and keeps nothing from one call for the next; calls that
+ * share one must not overlap. */
+MXFP4_API mxfp4_status_t mxfp4_moe_layer(const void *X, int64_t ldx, const void *residual, int64_t ldr,
+                                         const void *weight, float eps, const void *router, const float *bias, int score,
+                                         int groups, int topk_groups, int group_top, int k, int renormalize, float scale,
+                                         const void *W13q, const void *W13_sf, const void *W2q, const void *W2_sf,
+                                         void *H, int64_t ldh, void *out, int64_t ldo, int32_t *ids, float *out_weights,
+                                         int64_t T, int E, int64_t Hd, int64_t I, void *workspace, size_t ws_bytes,
+                                         void *stream);
 
 #ifdef __cplusplus
 }

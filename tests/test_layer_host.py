@@ -107,3 +107,46 @@ def test_reference_adapters_are_a_low_rank_update_of_the_weight():
     assert torch.allclose(c[1], 0.5 * (b[0] @ a[0]).double() @ x[1].double(), atol=1e-5)
     assert torch.allclose(c[3], 2.0 * (b[1, :, :1] @ a[1, :1]).double() @ x[3].double(), atol=1e-5)
     assert not c[2].any() and not c[4].any() and bool((bound >= 0).all())
+
+
+def layer(**kw):
+    a = dict(x=256, ldx=256, res=512, ldr=256, w=16, eps=1e-6, router=16, bias=16, score=0, groups=1, topk_groups=1,
+             group_top=2, k=2, renorm=1, scale=1.0, w13=32, s13=16, w2=32, s2=16, h=1024, ldh=256, out=2048, ldo=256, ids=16,
+             ow=16, T=4, E=8, H=256, I=128, ws=256, wsb=1 << 40)
+    a.update(kw)
+    return L.mxfp4_moe_layer(a["x"], a["ldx"], a["res"], a["ldr"], a["w"], a["eps"], a["router"], a["bias"], a["score"],
+                             a["groups"], a["topk_groups"], a["group_top"], a["k"], a["renorm"], a["scale"], a["w13"],
+                             a["s13"], a["w2"], a["s2"], a["h"], a["ldh"], a["out"], a["ldo"], a["ids"], a["ow"], a["T"],
+                             a["E"], a["H"], a["I"], a["ws"], a["wsb"], None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(T=0), OK), (dict(T=-1), INVALID), (dict(T=17), SHAPE), (dict(k=0), INVALID), (dict(k=9), SHAPE), (dict(E=0), INVALID),
+    (dict(E=513), SHAPE), (dict(H=192), SHAPE), (dict(I=64), SHAPE), (dict(H=0), INVALID), (dict(I=0), INVALID),
+    (dict(score=2), INVALID), (dict(groups=0), INVALID), (dict(groups=3), SHAPE), (dict(groups=2, topk_groups=3), INVALID),
+    (dict(groups=8, topk_groups=1), SHAPE), (dict(group_top=3), INVALID), (dict(scale=float("nan")), INVALID),
+    (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID), (dict(eps=float("inf")), INVALID), (dict(x=None), INVALID),
+    (dict(w=None), INVALID), (dict(router=None), INVALID), (dict(w13=None), INVALID), (dict(s13=None), INVALID),
+    (dict(w2=None), INVALID), (dict(s2=None), INVALID), (dict(out=None), INVALID), (dict(ws=None), INVALID),
+    (dict(ldx=128), INVALID), (dict(ldr=128), INVALID), (dict(ldh=128), INVALID), (dict(ldo=128), INVALID),
+    (dict(h=2048), INVALID), (dict(h=256, ldh=264), INVALID), (dict(h=512, ldh=264), INVALID), (dict(ldx=260), MISALIGNED),
+    (dict(ldr=260), MISALIGNED), (dict(ldh=260), MISALIGNED), (dict(ldo=260), MISALIGNED), (dict(x=264), MISALIGNED),
+    (dict(res=520), MISALIGNED), (dict(h=1032), MISALIGNED), (dict(out=2056), MISALIGNED), (dict(w=24), MISALIGNED),
+    (dict(router=24), MISALIGNED), (dict(bias=18), MISALIGNED), (dict(w13=48), MISALIGNED), (dict(w2=48), MISALIGNED),
+    (dict(s13=24), MISALIGNED), (dict(s2=24), MISALIGNED), (dict(ids=18), MISALIGNED), (dict(ow=18), MISALIGNED),
+    (dict(ws=128), MISALIGNED), (dict(wsb=0), WORKSPACE),
+])
+def test_moe_layer_refusals(kw, want):
+    assert layer(**kw) == want
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-GPU answer")
+def test_valid_moe_layer_calls_without_gpu_report_no_device():
+    assert layer() == layer(res=None, bias=None, h=None, ids=None, ow=None) == layer(h=256) == layer(out=256) == NO_DEVICE
+
+
+def test_moe_layer_workspace_grows_with_tokens():
+    f = mx.moe_layer_workspace_bytes
+    sizes = [f(T, 8, 64, 2048, 768) for T in range(1, 17)]
+    assert sizes == sorted(sizes) and sizes[0] > 0
+    assert f(0, 8, 64, 2048, 768) == 0 and f(17, 8, 64, 2048, 768) == 0 and f(4, 8, 64, 2000, 768) == 0
