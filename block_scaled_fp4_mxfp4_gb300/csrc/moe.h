@@ -61,10 +61,10 @@ cudaError_t launch_moe_experts(const MoeArgs &a, const MoeLayout &l, cudaStream_
 int read_and_clear_moe_error();
 
 // -------------------------------------------------------------- moe_few.cu
-// The whole layer for up to kMoeFewTokens tokens: one MMA of 8 columns, or two.
+// The whole layer for up to kMoeFewTokens tokens: eight columns of an MMA each.
 constexpr int kMoeFewTokens = 16;
 struct MoeFewLayout {
-    size_t counters, h, part, part_ss, xh, sx, ids, weights, act, act_sx, y, total;
+    size_t counters, h, part, part_ss, xd, xsf, ids, weights, ad, asf, y, total;
 };
 MoeFewLayout moe_few_layout(int64_t T, int k, int E, int64_t H, int64_t I);
 
@@ -77,8 +77,8 @@ struct MoeFewArgs {
     int T, H, I;
     float eps;
     uint8_t *ws;
-    CUtensorMap tm_w13;     // packed weights [E * 2I, H / 2] u8, box 128 bytes x 32 rows
-    CUtensorMap tm_w2;      // the same of [E * H, I / 2], box 64 rows
+    CUtensorMap tm_w13;     // packed weights [E * 2I, H / 2] u8, box 128 bytes x 64 rows
+    CUtensorMap tm_w2;      // the same of [E * H, I / 2]
 };
 cudaError_t launch_moe_few(const MoeFewArgs &a, const MoeFewLayout &l, cudaStream_t stream);
 int read_and_clear_moe_few_error();

@@ -10,28 +10,24 @@
 //            products over them, for all tokens
 //   tokens   a block a token: adds those sums in 64 bits, y in MXFP8, routing
 //   experts  both products and the sum. Weights are what there is to read, so the
-//            kernel is a stream of them: a ring of shared memory that one thread fills by TMA,
-//            and warps that widen packed codes in registers (one conversion gives
-//            two fp16) and multiply with mma.sync, 16 weight rows x 8 tokens x 16. An
-//            E4M3 or E2M1 value is exact in fp16 and so is each product in fp32; the
-//            sums of one block of 32 take the two scales in fp32, whatever their size.
+//            kernel is a stream of them into a ring of shared memory, by TMA, as they
+//            lie in memory, and tcgen05.mma kind::mxf4 of them with the activations'
+//            digits (below). (mxfp4_moe_experts multiplies with kind::mxf8f6f4, which
+//            takes E2M1 in 8-bit containers: widening them in shared memory holds a decoding
+//            batch at half of HBM's rate. Widening in registers for mma.sync was measured
+//            too: 90 instructions for 512 weights, 114 us where the stream takes 28.)
 //
-// Why not tcgen05, which mxfp4_moe_experts uses for the same products: its weights have
-// to lie in shared memory in 8-bit containers, and writing them there (690 wavefronts
-// a stage of 16 KB) holds a decoding batch at half of HBM's rate. Here a packed word is read
-// from shared memory once, and the tensor work is small: 8 columns.
-//
-// Units of work: 32 channels of an expert in product 1 (its rows of G and U: one block of
-// the activations' MXFP8, quantized where it is made), 64 channels in product 2. Blocks
-// claim them from one counter, product 1 first, so that a unit that waits for
-// activations only waits for units that somebody already works on: no assumption on
-// which blocks run at the same time. While it waits, its weights fill the ring.
+// Units of work: 64 channels of an expert in product 1 (their rows of G and of U), 128 in
+// product 2. Blocks claim them from one counter, product 1 first, so that a unit that
+// waits for activations only waits for units that somebody already works on: no
+// assumption on which blocks run at the same time. While it waits, its weights fill the ring.
 //
 // Bound: HBM, the weights of the experts that some token chose.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <cstddef>
 #include <cstring>
 
 #include "internal.h"
@@ -48,6 +44,61 @@ namespace {
 constexpr int kMaxTokens = kMoeFewTokens;
 constexpr int kMaxExperts = 512;
 constexpr int kMaxChoices = kMaxTokens * 32;
+
+// ------------------------------------------------------------------ digits
+//
+// The products run in kind::mxf4, whose operands are both E2M1: weights as they lie in
+// memory. An MXFP8 activation goes in as six E2M1 columns: the magnitude of an E4M3
+// value is a whole number n < 2^18 of 2^-9, and n = sum_i d_i 8^i with d_i in -3 .. 4 for
+// i < 5; what is left for i = 5 is 0 .. 7, and 5 and 7 become 6 with d_4 less or more by 8
+// (n has four significant bits: d_4 is then a multiple of 4 from 0 to 4). All of 0, 1, 2, 3, 4, 6, 8
+// are twice an E2M1 value, so digit i enters with the scale 2^(e - 8 + 3 i), e the
+// exponent of the activation's own scale, and the six columns' sums add up to the product
+// of the activation itself: every term is exact.
+
+// E8M0 byte of digit i where the activations' byte is b (255: NaN).
+__device__ __forceinline__ uint32_t digit_scale(uint32_t b, int i)
+{
+    return b == 255 ? 255 : max(static_cast<int>(b) - 8 + 3 * i, 0);
+}
+
+// Eight E2M1 codes a digit of y (four bits each, the first lowest), y of a block whose
+// MXFP8 scale byte is b. Digits whose scale lies below 2^-127 are left out.
+__device__ __forceinline__ void digits_of(const float (&y)[8], uint32_t b, uint32_t (&out)[6])
+{
+    const float inv = mxfp8_scale_inverse(b);
+    uint32_t codes[2];
+    codes[0] = e4m3x4_rn(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+    codes[1] = e4m3x4_rn(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv);
+#pragma unroll
+    for (int i = 0; i < 6; ++i) out[i] = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t c = (codes[j >> 2] >> (8 * (j & 3))) & 0xFFu, ex = (c >> 3) & 15u, m = c & 7u;
+        int n = static_cast<int>(ex ? (8 + m) << (ex - 1) : m);
+        int d[6];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) {
+            d[i] = ((n + 3) & 7) - 3;
+            n = (n - d[i]) >> 3;
+        }
+        d[5] = n;
+        if (n == 5 || n == 7) {
+            d[5] = 6;
+            d[4] += n == 5 ? -8 : 8;
+        }
+        const uint32_t sign = c >> 7;
+#pragma unroll
+        for (int i = 0; i < 6; ++i) {
+            const uint32_t a = static_cast<uint32_t>(abs(d[i]));
+            const uint32_t code = (a <= 4 ? a : (a >> 1) + 2) | ((sign ^ (d[i] < 0 ? 1u : 0u)) << 3);
+            out[i] |= code << (4 * j);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        if (b + 3 * i < 8) out[i] = 0;
+}
 
 // ------------------------------------------------------------------ router
 
@@ -161,8 +212,8 @@ struct TokenParams {
     const uint16_t *h, *w;
     const float *part, *part_ss;
     const float *bias;                  // [E] or null
-    uint16_t *xh;                       // [T, H] the E4M3 values of y as fp16
-    float *sx;                          // [T, H / 32] their scales
+    uint8_t *xd;                        // [T][6][H / 2] digits of y
+    uint32_t *xsf;                      // [T][H / 128][8] their scales, four blocks of 32 a word, six words used
     int *ids;                           // [T, k], of the workspace
     float *weights;
     int *ids_out;                       // the caller's, or null
@@ -170,12 +221,6 @@ struct TokenParams {
     int T, H, E, k, slices, groups, topk_groups, group_top, sigmoid, renorm;
     float eps, scale;
 };
-
-// 2^(b - 127) of a scale byte, NaN for 255.
-__device__ __forceinline__ float scale_value(uint32_t b)
-{
-    return __uint_as_float(b == 255 ? 0x7FC00000u : (b == 0 ? 0x00400000u : b << 23));
-}
 
 // A key that orders as the values do, NaN above all; 0 stands for "none".
 __device__ __forceinline__ uint32_t order_key(float v)
@@ -367,60 +412,72 @@ __global__ void __launch_bounds__(kTokenThreads) moe_few_token_kernel(const Toke
         amax = max(amax, __shfl_xor_sync(quad, amax, 1));
         amax = max(amax, __shfl_xor_sync(quad, amax, 2));
         const uint32_t b = mxfp8_scale_byte(amax);
-        const float inv = mxfp8_scale_inverse(b);
-        uint32_t o[4];
+        uint32_t dg[6];
+        digits_of(y, b, dg);
+        uint8_t *o = p.xd + static_cast<size_t>(t) * 6 * (p.H >> 1) + 4 * v;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            o[i] = f16x2_of_e4m3(y[2 * i] * inv, y[2 * i + 1] * inv);
-        *reinterpret_cast<uint4 *>(p.xh + static_cast<int64_t>(t) * p.H + 8 * v) = make_uint4(o[0], o[1], o[2], o[3]);
-        if ((v & 3) == 0) p.sx[static_cast<int64_t>(t) * (p.H >> 5) + (v >> 2)] = scale_value(b);
+        for (int d = 0; d < 6; ++d) *reinterpret_cast<uint32_t *>(o + static_cast<size_t>(d) * (p.H >> 1)) = dg[d];
+        if ((v & 3) == 0) {
+            uint8_t *f = reinterpret_cast<uint8_t *>(p.xsf + (static_cast<size_t>(t) * (p.H >> 7) + (v >> 4)) * 8) + ((v >> 2) & 3);
+#pragma unroll
+            for (int d = 0; d < 6; ++d) f[4 * d] = static_cast<uint8_t>(digit_scale(b, d));
+        }
     }
 }
 
 // ----------------------------------------------------------------- experts
 
-constexpr int kConsumers = 256;                  // eight warps: four groups of 16 rows x two halves of a stage's K
-constexpr int kExpertThreads = kConsumers + 32;
-constexpr int kStages = 8;
-constexpr uint32_t kStageWeights = 64 * 128;     // 64 rows x 256 elements
-constexpr uint32_t kStageBytes = kStageWeights + 2048;   // and up to four blocks of scales
+constexpr int kExpertThreads = 320;
+constexpr int kMaxStages = 12;
+constexpr int kEpiLd = 132;                              // floats of a staged token
+constexpr uint32_t kStageWeights = 128 * 128;            // 128 rows x 256 elements
+constexpr uint32_t kStageScales = 1024;                  // two blocks of 512 bytes: of the weights, then of the tokens
+constexpr uint32_t kTokenBytes = 1024;                   // of a token in a stage: eight rows (six used) x 256 elements
+constexpr uint32_t kAccColumns = 8 * kMaxTokens;
+constexpr uint32_t kSfColumns = 16;                      // of a stage: two blocks of weights, two of tokens
+constexpr uint32_t kTmemColumns = 512;
+static_assert(2 * kAccColumns + kMaxStages * kSfColumns <= kTmemColumns, "TMEM budget");
 
 struct ExpertsParams {
-    CUtensorMap tm_w13;                 // packed weights [E * 2I, H / 2] u8, box 128 bytes x 32 rows
-    CUtensorMap tm_w2;                  // the same of [E * H, I / 2], box 64 rows
+    CUtensorMap tm_w13;                 // packed weights [E * 2I, H / 2] u8, box 128 bytes x 64 rows
+    CUtensorMap tm_w2;                  // the same of [E * H, I / 2]
     const uint8_t *w13_sf, *w2_sf;
-    const uint16_t *xh;
-    const float *sx;
+    const uint8_t *xd;                  // [T][6][H / 2] digits of the tokens
+    const uint32_t *xsf;                // [T][H / 128][8] their scales
     const int *ids;
     const float *weights;
-    uint16_t *act;                      // [T * k, I] fp16 of E4M3 values
-    float *act_sx;                      // [T * k, I / 32]
+    uint8_t *ad;                        // [T * k][6][I / 2] of the activations
+    uint32_t *asf;                      // [T * k][I / 128][8]
     float *y;                           // [T * k, H]
     uint16_t *out;
     int64_t ldo;
     int *queue;                         // units claimed
     int *made;                          // units of product 1 that are complete
-    int *arrived;                       // [H / 64] experts whose product 2 of these channels is complete
+    int *arrived;                       // [H / 128] experts whose product 2 of these channels is complete
     int T, k, E, H, I;
+    int stages, room;                   // stages of the ring, tokens that one has room for
     uint64_t wait_ns;
 };
 
 struct ExpertsShared {
-    uint64_t full[kStages], empty[kStages];
-    int header[kStages];                // unit of a stage, -1: there are no more
-    int abort[2];
-    int last;
-    int active;
+    float epi[kMaxTokens][kEpiLd];
+    uint64_t w_full[kMaxStages];        // weights have landed
+    uint64_t t_full[kMaxStages];        // tokens and scales have landed
+    uint64_t empty[kMaxStages];         // the stage's MMAs have completed
+    uint64_t unit_full[4], unit_empty[4];
+    uint64_t acc_full[2], acc_empty[2];
+    uint64_t mma_done;
+    uint32_t tmem;
+    int unit[4];                        // units in the order they were claimed, -1: there are no more
+    int abort, active, last, go[2];
     uint16_t expert[kMaxChoices];       // the experts that some token chose
-    uint8_t rows[kMaxExperts];          // choices of an expert
-    uint16_t slot[kMaxExperts * kMaxTokens];   // t * k + j of them
-    float red[2][4][8][32];             // sums of the second half of K: [unit parity][rows][value][lane]
-    float act[kMaxTokens][33];
+    uint16_t first[kMaxChoices];        // the first of an expert's entries in slot, in that order
+    uint16_t slot[kMaxChoices];         // choices t * k + j by expert
+    alignas(16) uint8_t rows[kMaxExperts];   // choices of an expert, counted four in a word
 };
-constexpr uint32_t kExpertsSmem = kStages * kStageBytes + sizeof(ExpertsShared) + 1024;
+static_assert(offsetof(ExpertsShared, rows) % 4 == 0 && offsetof(ExpertsShared, w_full) % 8 == 0, "aligned as it is used");
 
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-__device__ __forceinline__ void first_half_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 __device__ __forceinline__ int load_acquire(const int *p)
 {
@@ -429,176 +486,262 @@ __device__ __forceinline__ int load_acquire(const int *p)
     return v;
 }
 
-// fp16 pairs of the eight E2M1 codes of a word.
-__device__ __forceinline__ void widen(uint32_t w, uint32_t (&h)[4])
-{
-    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-        "mov.b32 {a, b, c, d}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-        : "r"(w));
-}
-
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1)
-{
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Activations of this lane for 128 elements of K: of the token of its MMA column, and
-// the scales of the two tokens whose sums it holds.
-struct Tokens {
-    uint4 x[4];
-    float4 s[2];
+// A position in the ring of stages.
+struct Place {
+    int slot;
+    uint32_t parity;
+    __device__ __forceinline__ void step(int n)
+    {
+        if (++slot == n) {
+            slot = 0;
+            parity ^= 1u;
+        }
+    }
 };
 
-__global__ void __launch_bounds__(kExpertThreads, 2) moe_few_experts_kernel(const __grid_constant__ ExpertsParams p)
+// Unit u: weight tile c of the active expert a, product 1 if u < n1.
+struct Unit {
+    bool first;
+    int a, c;
+};
+__device__ __forceinline__ Unit unit_at(int u, int n1, int active, int tiles1)
+{
+    Unit w;
+    w.first = u < n1;
+    if (w.first) {
+        w.a = u / tiles1;
+        w.c = u - w.a * tiles1;
+    } else {
+        w.c = (u - n1) / active;
+        w.a = u - n1 - w.c * active;
+    }
+    return w;
+}
+
+// Warps:
+//   0-3  epilogue of a finished tile while the next one's products run
+//   4-7  copy tokens' digits and all scales into the ring by cp.async
+//   8    lane 0 claims units and loads their weights by TMA
+//   9    issues scale copies and MMAs (an elected lane); owns TMEM
+// Waits name a round of a barrier by its parity. Nobody can be a round behind: the next
+// round of a stage needs the TMA thread and every copying thread, the next of a unit's
+// entry or of an accumulator everyone who waits for this one.
+__global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(const __grid_constant__ ExpertsParams p)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    ExpertsShared &sh = *reinterpret_cast<ExpertsShared *>(smem + kStages * kStageBytes);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int S = p.stages;
+    const uint32_t stage_bytes = kStageWeights + 2 * kStageScales + p.room * kTokenBytes;
+    ExpertsShared &sh = *reinterpret_cast<ExpertsShared *>(smem + S * stage_bytes);
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(&sh.full[i], 1);
-            mbar_init(&sh.empty[i], kConsumers / 32);
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&sh.w_full[i], 1);
+            mbar_init(&sh.t_full[i], 128);
+            mbar_init(&sh.empty[i], 1);
         }
-        sh.abort[0] = sh.abort[1] = 0;
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&sh.unit_full[i], 1);
+            mbar_init(&sh.unit_empty[i], 6);     // four copying warps, the issuer, the epilogue
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.acc_full[i], 1);
+            mbar_init(&sh.acc_empty[i], 128);
+        }
+        mbar_init(&sh.mma_done, 1);
+        sh.abort = 0;
         fence_mbar_init();
         tma_prefetch_desc(&p.tm_w13);
         tma_prefetch_desc(&p.tm_w2);
     }
     for (int i = tid; i < kMaxExperts / 4; i += kExpertThreads) reinterpret_cast<uint32_t *>(sh.rows)[i] = 0;
+    if (warp == 9) {
+        tmem_alloc(&sh.tmem, kTmemColumns);
+        tmem_relinquish();
+    }
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
     grid_dependency_wait();
-    // which experts have which choices: their order in a list does not matter, columns of
-    // an MMA do not mix
-    for (int i = tid; i < p.T * p.k; i += kExpertThreads) {
-        const int e = __ldcg(p.ids + i);
+    // Choices by expert. The order of an expert's choices does not matter: columns of an
+    // MMA do not mix.
+    uint32_t mine[2] = {0, 0};               // (expert + 1, place among its choices) of this thread's choices
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int c = tid + i * kExpertThreads;
+        const int e = c < p.T * p.k ? __ldcg(p.ids + c) : -1;
         if (e >= 0) {
             const uint32_t was = atomicAdd(reinterpret_cast<uint32_t *>(sh.rows) + (e >> 2), 1u << (8 * (e & 3)));
-            sh.slot[e * kMaxTokens + ((was >> (8 * (e & 3))) & 0xFF)] = static_cast<uint16_t>(i);
+            mine[i] = (static_cast<uint32_t>(e + 1) << 8) | ((was >> (8 * (e & 3))) & 0xFF);
         }
     }
     __syncthreads();
+    uint16_t *start_of = reinterpret_cast<uint16_t *>(&sh.epi[0][0]);      // [E], before the epilogue needs it
     if (warp == 0) {
-        int n = 0;
+        int n = 0, before = 0;
         for (int e0 = 0; e0 < p.E; e0 += 32) {
-            const bool has = e0 + lane < p.E && sh.rows[e0 + lane] > 0;
-            const unsigned m = __ballot_sync(0xffffffffu, has);
-            if (has) sh.expert[n + __popc(m & ((1u << lane) - 1))] = static_cast<uint16_t>(e0 + lane);
+            const int r = e0 + lane < p.E ? sh.rows[e0 + lane] : 0;
+            int sum = r;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += x;
+            }
+            const unsigned m = __ballot_sync(0xffffffffu, r > 0);
+            if (r > 0) {
+                const int at = n + __popc(m & ((1u << lane) - 1));
+                sh.expert[at] = static_cast<uint16_t>(e0 + lane);
+                sh.first[at] = start_of[e0 + lane] = static_cast<uint16_t>(before + sum - r);
+            }
             n += __popc(m);
+            before += __shfl_sync(0xffffffffu, sum, 31);
         }
         if (lane == 0) sh.active = n;
     }
     __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (mine[i]) sh.slot[start_of[(mine[i] >> 8) - 1] + (mine[i] & 0xFF)] = static_cast<uint16_t>(tid + i * kExpertThreads);
+    __syncthreads();
     const int active = sh.active;
-    const int n1 = active * (p.I >> 5), n2 = active * (p.H >> 6);
+    const int tiles1 = p.I >> 6, n1 = active * tiles1, n2 = active * (p.H >> 7);
 
-    if (warp == kConsumers / 32) {
+    if (warp == 8) {
         if (lane == 0) {
             // ---------------------------------------------- weights, by TMA
             const uint64_t pol = policy_evict_first();
-            int gs = 0;
+            Place at{0, 0};
+            int issued = 0;
             bool ok = true;
-            auto slot_free = [&]() {
-                return gs < kStages || mbar_wait(&sh.empty[gs % kStages], ((gs / kStages) & 1) ^ 1u, &g_moe_few_error,
-                                                 kErrWaitEmpty, p.wait_ns);
+            // the weight scales of a unit go to L2 ahead of their copies
+            auto ask_scales = [&](int u) {
+                if (u >= n1 + n2) return;
+                const Unit w = unit_at(u, n1, active, tiles1);
+                const int e = sh.expert[w.a];
+                if (w.first) {
+                    const uint32_t run = (p.H >> 7) * 512;
+                    const size_t blk = static_cast<size_t>(2 * p.I >> 7) * e + (w.c >> 1);
+                    prefetch_l2_bulk(p.w13_sf + blk * run, run);
+                    prefetch_l2_bulk(p.w13_sf + (blk + (p.I >> 7)) * run, run);
+                } else {
+                    const uint32_t run = (p.I >> 7) * 512;
+                    prefetch_l2_bulk(p.w2_sf + (static_cast<size_t>(p.H >> 7) * e + w.c) * run, run);
+                }
             };
             int u = atomicAdd(p.queue, 1);
-            while (u < n1 + n2) {
+            for (int i = 0;; ++i) {
+                const bool more = u < n1 + n2;
+                if (!(ok = mbar_wait(&sh.unit_empty[i & 3], ((i >> 2) & 1) ^ 1u, &g_moe_few_error, kErrWaitEmpty, p.wait_ns)))
+                    break;
+                sh.unit[i & 3] = more ? u : -1;
+                mbar_arrive(&sh.unit_full[i & 3]);
+                if (!more) break;
                 const int next = atomicAdd(p.queue, 1);    // on its way while this unit loads
-                const bool first = u < n1;
-                const int K = first ? p.H : p.I, kc = K >> 7, stages = (kc + 1) >> 1;
-                const int tiles = p.I >> 5;
-                int e, r0;
-                const uint8_t *sf0, *sf1 = nullptr;
-                if (first) {
-                    // 32 channels: their rows of G and of U
-                    const int a = u / tiles, c = u - a * tiles;
-                    e = sh.expert[a];
-                    r0 = e * 2 * p.I + 32 * c;
-                    sf0 = p.w13_sf + (static_cast<size_t>(e) * (2 * p.I >> 7) + (c >> 2)) * kc * 512;
-                    sf1 = sf0 + static_cast<size_t>(p.I >> 7) * kc * 512;
-                } else {
-                    const int c = (u - n1) / active;
-                    e = sh.expert[u - n1 - c * active];
-                    r0 = e * p.H + 64 * c;
-                    sf0 = p.w2_sf + (static_cast<size_t>(e) * (p.H >> 7) + (c >> 1)) * kc * 512;
-                }
-                for (int ks = 0; ks < stages; ++ks, ++gs) {
-                    if (!(ok = slot_free())) break;
-                    const int s = gs % kStages;
-                    uint8_t *st = smem + s * kStageBytes;
-                    const uint32_t sf_bytes = 512u * min(2, kc - 2 * ks);
-                    sh.header[s] = u;
-                    mbar_arrive_expect_tx(&sh.full[s], kStageWeights + sf_bytes * (first ? 2 : 1));
-                    if (first) {
-                        tma_load_2d(st, &p.tm_w13, ks * 128, r0, &sh.full[s], pol);
-                        tma_load_2d(st + 4096, &p.tm_w13, ks * 128, r0 + p.I, &sh.full[s], pol);
-                        bulk_load(st + kStageWeights + 1024, sf1 + ks * 1024, sf_bytes, &sh.full[s], pol);
-                    } else {
-                        tma_load_2d(st, &p.tm_w2, ks * 128, r0, &sh.full[s], pol);
-                    }
-                    bulk_load(st + kStageWeights, sf0 + ks * 1024, sf_bytes, &sh.full[s], pol);
+                const Unit w = unit_at(u, n1, active, tiles1);
+                const int e = sh.expert[w.a];
+                const int stages = ((w.first ? p.H : p.I) + 255) >> 8;
+                // 64 rows of G and the same of U, or 128 rows
+                const int r0 = w.first ? e * 2 * p.I + 64 * w.c : e * p.H + 128 * w.c;
+                const int r1 = r0 + (w.first ? p.I : 64);
+                const CUtensorMap *tm = w.first ? &p.tm_w13 : &p.tm_w2;
+                for (int ks = 0; ks < stages; ++ks) {
+                    if (!(ok = mbar_wait(&sh.empty[at.slot], at.parity ^ 1u, &g_moe_few_error, kErrWaitEmpty, p.wait_ns))) break;
+                    uint8_t *st = smem + at.slot * stage_bytes;
+                    mbar_arrive_expect_tx(&sh.w_full[at.slot], kStageWeights);
+                    tma_load_2d(st, tm, ks * 128, r0, &sh.w_full[at.slot], pol);
+                    tma_load_2d(st + 8192, tm, ks * 128, r1, &sh.w_full[at.slot], pol);
+                    ++issued;
+                    at.step(S);
+                    if (ks == 0) ask_scales(next);
                 }
                 if (!ok) break;
                 u = next;
             }
-            grid_launch_dependents();
-            if (ok && (ok = slot_free())) {
-                sh.header[gs % kStages] = -1;
-                mbar_arrive(&sh.full[gs % kStages]);
-                ++gs;
-            }
+            if (!ok) *reinterpret_cast<volatile int *>(&sh.abort) = 1;
             // copies in flight land before the block leaves
-            for (int i = max(0, gs - kStages); i < gs; ++i)
-                mbar_wait(&sh.full[i % kStages], (i / kStages) & 1, &g_moe_few_error, kErrWaitDrain);
-        }
-        return;
-    }
-
-    // ------------------------------------------------------------- products
-    const int m = warp & 3, kh = warp >> 2, g = lane >> 2, q = lane & 3;
-    int gs = 0;
-    for (int it = 0;; ++it) {
-        // Every consumer warp passes consumers_sync once a turn, whatever it met, and
-        // they all leave after the same one: abort[it & 1] is written before it and read
-        // after it, and not written again before the next.
-        bool ok = mbar_wait_warp(&sh.full[gs % kStages], (gs / kStages) & 1, &g_moe_few_error, kErrWaitFull, p.wait_ns);
-        const int u = ok ? *reinterpret_cast<volatile int *>(&sh.header[gs % kStages]) : -1;
-        const bool first = u < n1;
-        int a = 0, c = 0, rows = 0;
-        float acc[2][4];
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[nt][i] = 0.0f;
-        const uint16_t *slots = sh.slot;
-        if (u >= 0) {
-            const int tiles = p.I >> 5;
-            if (first) {
-                a = u / tiles;
-                c = u - a * tiles;
-            } else {
-                c = (u - n1) / active;
-                a = u - n1 - c * active;
+            Place back{0, 0};
+            for (int i = 0; i < issued; ++i) {
+                if (i >= issued - S) mbar_wait(&sh.w_full[back.slot], back.parity, &g_moe_few_error, kErrWaitDrain);
+                back.step(S);
             }
-            const int e = sh.expert[a];
-            rows = sh.rows[e];
-            slots = sh.slot + e * kMaxTokens;
-            const int K = first ? p.H : p.I, kc = K >> 7, stages = (kc + 1) >> 1;
-            if (!first) {
-                // all activations have to be there
+        }
+    } else if (warp == 9) {
+        // ------------------------------------------------ scales and products
+        Place at{0, 0};
+        bool ok = true;
+        for (int i = 0; ok; ++i) {
+            ok = mbar_wait_warp(&sh.unit_full[i & 3], (i >> 2) & 1, &g_moe_few_error, kErrWaitFull, p.wait_ns);
+            if (!ok) break;
+            const int u = *reinterpret_cast<volatile int *>(&sh.unit[i & 3]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.unit_empty[i & 3]);
+            if (u < 0) break;
+            const Unit w = unit_at(u, n1, active, tiles1);
+            const int kc = (w.first ? p.H : p.I) >> 7, stages = (kc + 1) >> 1, buf = i & 1;
+            const int rows = sh.rows[sh.expert[w.a]];
+            ok = mbar_wait_warp(&sh.acc_empty[buf], ((i >> 1) & 1) ^ 1u, &g_moe_few_error, kErrWaitAccum, p.wait_ns);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t idesc = __shfl_sync(0xffffffffu, idesc_block_scaled((8 * rows + 15) & ~15, true), 0);
+            const uint32_t d = tmem + buf * kAccColumns;
+            for (int ks = 0; ks < stages; ++ks) {
+                ok = mbar_wait_warp(&sh.w_full[at.slot], at.parity, &g_moe_few_error, kErrWaitFull, p.wait_ns) &&
+                     mbar_wait_warp(&sh.t_full[at.slot], at.parity, &g_moe_few_error, kErrWaitOperand, p.wait_ns);
+                if (!ok) break;
+                // cp.async wrote through the generic proxy; scale copies and MMAs read through the async one
+                fence_proxy_async_smem();
+                tc_fence_after();
+                const uint32_t st = smem_u32(smem) + at.slot * stage_bytes;
+                const uint64_t ad = sdesc_sw128(st), bd = sdesc_sw128(st + kStageWeights + 2 * kStageScales);
+                const uint64_t sd = sdesc_scale(st + kStageWeights);
+                const uint32_t tsf = tmem + 2 * kAccColumns + at.slot * kSfColumns;
+                if (elect_one()) {
+                    auto half = [&](int h, uint32_t accumulate) {
+                        tc_cp_scale_block(tsf + 4 * h, sd + 32 * h);
+                        tc_cp_scale_block(tsf + 8 + 4 * h, sd + 64 + 32 * h);
+                        mma_mxf4(d, ad + 4 * h, bd + 4 * h, idesc_with_sf_ids(idesc, 0, 0), tsf + 4 * h, tsf + 8 + 4 * h,
+                                 accumulate);
+                        mma_mxf4(d, ad + 4 * h + 2, bd + 4 * h + 2, idesc_with_sf_ids(idesc, 2, 2), tsf + 4 * h,
+                                 tsf + 8 + 4 * h, 1u);
+                    };
+                    half(0, ks > 0 ? 1u : 0u);
+                    if (2 * ks + 1 < kc) half(1, 1u);
+                    tc_commit(&sh.empty[at.slot]);
+                }
+                __syncwarp();
+                at.step(S);
+            }
+            if (!ok) break;
+            if (elect_one()) tc_commit(&sh.acc_full[buf]);
+            __syncwarp();
+        }
+        if (!ok) *reinterpret_cast<volatile int *>(&sh.abort) = 1;
+        // no MMA may be running when TMEM is released
+        if (elect_one()) tc_commit(&sh.mma_done);
+        __syncwarp();
+        mbar_wait_warp(&sh.mma_done, 0, &g_moe_few_error, kErrWaitDrain);
+    } else if (warp >= 4) {
+        // -------------------------------------------------- tokens and scales
+        const int t = tid - 128;
+        Place at{0, 0};
+        int count = 0;
+        bool ok = true, ready = false;
+        for (int i = 0; ok; ++i) {
+            ok = mbar_wait_warp(&sh.unit_full[i & 3], (i >> 2) & 1, &g_moe_few_error, kErrWaitFull, p.wait_ns);
+            if (!ok) break;
+            const int u = *reinterpret_cast<volatile int *>(&sh.unit[i & 3]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.unit_empty[i & 3]);
+            if (u < 0) break;
+            const Unit w = unit_at(u, n1, active, tiles1);
+            const int e = sh.expert[w.a], rows = sh.rows[e];
+            const uint16_t *slots = sh.slot + sh.first[w.a];
+            const int K = w.first ? p.H : p.I, kc = K >> 7, stages = (kc + 1) >> 1;
+            if (!w.first && !ready) {
+                // the activations have to be there, of all units
                 int v = 1;
-                if (lane == 0 && load_acquire(p.made) < n1) {
+                if (lane == 0) {
                     const uint64_t t0 = global_timer_ns();
                     while (load_acquire(p.made) < n1) {
                         if (global_timer_ns() - t0 > p.wait_ns) {
@@ -606,151 +749,202 @@ __global__ void __launch_bounds__(kExpertThreads, 2) moe_few_experts_kernel(cons
                             v = 0;
                             break;
                         }
-                        __nanosleep(64);
                     }
                 }
                 ok = __shfl_sync(0xffffffffu, v, 0) != 0;
                 __syncwarp();
+                if (!ok) break;
+                ready = true;
             }
-            const uint16_t *xsrc = first ? p.xh : p.act;
-            const float *ssrc = first ? p.sx : p.act_sx;
-            // row of a choice among the activations: its token in product 1
-            auto row_of = [&](int i) { return static_cast<int64_t>(first ? slots[i] / p.k : slots[i]); };
-            const uint16_t *xr[2];
-            const float *sr[2][2];
+            // a row of digits is K / 2 bytes, six of them a token; pieces of 16 bytes, column c of row n at c ^ (n % 8)
+            const uint8_t *digits = w.first ? p.xd : p.ad;
+            const uint32_t *scales = w.first ? p.xsf : p.asf;
+            const uint8_t *src[6];
+            uint32_t dst[6];
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-                xr[nt] = 8 * nt + g < rows ? xsrc + row_of(8 * nt + g) * K + kh * 128 + 8 * q : nullptr;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int col = 8 * nt + 2 * q + i;
-                    sr[nt][i] = col < rows ? ssrc + row_of(col) * (K >> 5) + kh * 4 : nullptr;
+            for (int j = 0; j < 6; ++j) {
+                const int piece = t + 128 * j, r = piece / 48, dc = piece - 48 * r, c = dc & 7, dg = dc >> 3;
+                src[j] = nullptr;
+                dst[j] = 0;
+                if (r < rows) {
+                    const int row = w.first ? slots[r] / p.k : slots[r];
+                    src[j] = digits + static_cast<size_t>(row * 6 + dg) * (K >> 1) + 16 * c;
+                    dst[j] = kStageWeights + 2 * kStageScales + (8 * r + dg) * 128 + ((c ^ dg) << 4);
                 }
             }
-            // where this lane's rows and their scales lie in a stage
-            const uint32_t w0 = (first ? 8 * m + g : 16 * m + g) * 128, w1 = w0 + (first ? 4096 : 1024);
-            uint32_t f0, f1;
-            if (first) {
-                f0 = kStageWeights + (8 * m + g) * 16 + (c & 3) * 4;
-                f1 = f0 + 1024;
-            } else {
-                f0 = kStageWeights + ((m & 1) * 16 + g) * 16 + ((c & 1) * 2 + (m >> 1)) * 4;
-                f1 = f0 + 128;
-            }
-            const bool wide = rows > 8;
-            for (int ks = 0; ks < stages && ok; ++ks, ++gs) {
-                const bool mine = 2 * ks + kh < kc;            // the last stage may have one half only
-                Tokens tk[2];
+            const bool tail_col = (t & 7) < 4;               // columns of a stage's first half (piece 128 j + t: column t % 8)
+            const uint32_t *ssrc[2];
+            uint32_t sdst[2];
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
-                    if (nt && !wide) break;
-#pragma unroll
-                    for (int b = 0; b < 4; ++b)
-                        tk[nt].x[b] = xr[nt] && mine ? *reinterpret_cast<const uint4 *>(xr[nt] + ks * 256 + 32 * b)
-                                                     : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        tk[nt].s[i] = sr[nt][i] && mine ? *reinterpret_cast<const float4 *>(sr[nt][i] + ks * 8)
-                                                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int j = 0; j < 2; ++j) {
+                const int piece = t + 128 * j, r = piece >> 4, h = piece & 1, dg = (piece >> 1) & 7, n = 8 * r + dg;
+                ssrc[j] = nullptr;
+                sdst[j] = kStageWeights + kStageScales + h * 512 + (n & 31) * 16 + (n >> 5) * 4;
+                if (r < rows && dg < 6) {
+                    const int row = w.first ? slots[r] / p.k : slots[r];
+                    ssrc[j] = scales + (static_cast<size_t>(row) * kc + h) * 8 + dg;
                 }
-                const int s = gs % kStages;
-                if (ks && !(ok = mbar_wait_warp(&sh.full[s], (gs / kStages) & 1, &g_moe_few_error, kErrWaitFull, p.wait_ns)))
-                    break;
-                const uint8_t *st = smem + s * kStageBytes;
-                if (mine) {
-                    const uint32_t sf0 = *reinterpret_cast<const uint32_t *>(st + f0 + kh * 512);
-                    const uint32_t sf1 = *reinterpret_cast<const uint32_t *>(st + f1 + kh * 512);
+            }
+            const bool second = (t & 1) != 0;                // scale words of a stage's second half
+            // scales of the weights: of product 1 from the halves of the 128-row blocks of G and of U
+            // that hold its 64 channels (8 of each 16 bytes)
+            const uint8_t *wsf = nullptr;
+            uint32_t wdst = kStageWeights;
+            if (w.first && t < 64) {
+                const size_t blk = static_cast<size_t>(2 * p.I >> 7) * e + (w.c >> 1) + (t >= 32 ? p.I >> 7 : 0);
+                wsf = p.w13_sf + blk * kc * 512 + lane * 16 + (w.c & 1) * 8;
+                wdst += lane * 16 + (t >= 32 ? 8 : 0);
+            } else if (!w.first && t < 32) {
+                wsf = p.w2_sf + (static_cast<size_t>(p.H >> 7) * e + w.c) * kc * 512 + lane * 16;
+                wdst += lane * 16;
+            }
+            for (int ks = 0; ks < stages; ++ks) {
+                ok = mbar_wait_warp(&sh.empty[at.slot], at.parity ^ 1u, &g_moe_few_error, kErrWaitEmpty, p.wait_ns);
+                if (!ok) break;
+                const uint32_t st = smem_u32(smem) + at.slot * stage_bytes;
+                const bool whole = 2 * ks + 1 < kc;
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        const uint32_t at = ((4 * kh + b) ^ g) * 16 + 4 * q;
-                        uint32_t h0[4], h1[4];
-                        widen(*reinterpret_cast<const uint32_t *>(st + w0 + at), h0);
-                        widen(*reinterpret_cast<const uint32_t *>(st + w1 + at), h1);
-                        const float s0 = __uint_as_float(((sf0 >> (8 * b)) & 0xFFu) << 23);
-                        const float s1 = __uint_as_float(((sf1 >> (8 * b)) & 0xFFu) << 23);
+                for (int j = 0; j < 6; ++j)
+                    if (src[j] && (whole || tail_col)) cp_async<16>(st + dst[j], src[j] + ks * 128);
 #pragma unroll
-                        for (int nt = 0; nt < 2; ++nt) {
-                            if (nt && !wide) break;
-                            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                            mma_f16(d, h0[0], h1[0], h0[1], h1[1], tk[nt].x[b].x, tk[nt].x[b].y);
-                            mma_f16(d, h0[2], h1[2], h0[3], h1[3], tk[nt].x[b].z, tk[nt].x[b].w);
-                            const float x0 = (&tk[nt].s[0].x)[b], x1 = (&tk[nt].s[1].x)[b];
-                            acc[nt][0] = fmaf(d[0] * x0, s0, acc[nt][0]);
-                            acc[nt][1] = fmaf(d[1] * x1, s0, acc[nt][1]);
-                            acc[nt][2] = fmaf(d[2] * x0, s1, acc[nt][2]);
-                            acc[nt][3] = fmaf(d[3] * x1, s1, acc[nt][3]);
+                for (int j = 0; j < 2; ++j)
+                    if (ssrc[j] && (whole || !second)) cp_async<4>(st + sdst[j], ssrc[j] + ks * 16);
+                if (wsf) {
+                    if (w.first) {
+                        cp_async<8>(st + wdst, wsf + ks * 1024);
+                        if (whole) cp_async<8>(st + wdst + 512, wsf + ks * 1024 + 512);
+                    } else {
+                        cp_async<16>(st + wdst, wsf + ks * 1024);
+                        if (whole) cp_async<16>(st + wdst + 512, wsf + ks * 1024 + 512);
+                    }
+                }
+                cp_async_arrive(&sh.t_full[at.slot]);
+                ++count;
+                at.step(S);
+            }
+        }
+        if (!ok) *reinterpret_cast<volatile int *>(&sh.abort) = 1;
+        cp_async_wait_all();   // also after an abort: nothing of this thread is in flight when the block leaves
+        // nor are the arrivals of the last MMAs, which nobody else waits for
+        Place back{0, 0};
+        for (int i = 0; i < count && ok; ++i) {
+            if (i >= count - S) ok = mbar_wait_warp(&sh.empty[back.slot], back.parity, &g_moe_few_error, kErrWaitDrain);
+            back.step(S);
+        }
+    } else {
+        // ------------------------------------------------------------ epilogue
+        for (int i = 0;; ++i) {
+            const int buf = i & 1;
+            if (tid == 0) {
+                bool ok = mbar_wait(&sh.unit_full[i & 3], (i >> 2) & 1, &g_moe_few_error, kErrWaitFull, p.wait_ns);
+                int u = -1;
+                if (ok) {
+                    u = *reinterpret_cast<volatile int *>(&sh.unit[i & 3]);
+                    mbar_arrive(&sh.unit_empty[i & 3]);
+                    if (u >= 0) ok = mbar_wait(&sh.acc_full[buf], (i >> 1) & 1, &g_moe_few_error, kErrWaitAccum, p.wait_ns);
+                }
+                if (!ok) *reinterpret_cast<volatile int *>(&sh.abort) = 1;
+                sh.go[buf] = ok && !*reinterpret_cast<volatile int *>(&sh.abort) ? u : -1;
+            }
+            epilogue_sync();
+            const int u = sh.go[buf];
+            if (u < 0) break;
+            tc_fence_after();
+            const Unit w = unit_at(u, n1, active, tiles1);
+            const int rows = sh.rows[sh.expert[w.a]];
+            const uint16_t *slots = sh.slot + sh.first[w.a];
+            const uint32_t trow = tmem + buf * kAccColumns + (static_cast<uint32_t>(warp * 32) << 16);
+            for (int r0 = 0; r0 < rows; r0 += 4) {
+                uint32_t v[32];
+                tmem_ld32(trow + 8 * r0, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    // the digits' sums, smallest first
+                    float s = __uint_as_float(v[8 * r]);
+#pragma unroll
+                    for (int d = 1; d < 6; ++d) s += __uint_as_float(v[8 * r + d]);
+                    if (r0 + r < rows) {
+                        if (w.first)
+                            sh.epi[r0 + r][tid] = s;
+                        else
+                            p.y[static_cast<size_t>(slots[r0 + r]) * p.H + 128 * w.c + tid] = s;
+                    }
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(&sh.acc_empty[buf]);
+            epilogue_sync();
+            if (w.first) {
+                // a thread has 8 channels of a token; four neighbours share a block of 32
+                const int r = tid >> 3, part = tid & 7;
+                if ((r & ~3) < rows) {
+                    float a[8];
+                    uint32_t amax = 0;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        // silu as in moe_experts.cu: off by up to (5 + 1.2 |g|) 2^-23 of itself, 0 below -87.3
+                        const float g = sh.epi[r][8 * part + j];
+                        a[j] = __fdividef(g, 1.0f + __expf(-g)) * sh.epi[r][64 + 8 * part + j];
+                        amax = max(amax, __float_as_uint(a[j]) & 0x7FFFFFFFu);
+                    }
+                    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                    const uint32_t b = mxfp8_scale_byte(amax);
+                    const uint32_t b2 = __shfl_down_sync(0xffffffffu, b, 4);
+                    if (r < rows) {
+                        uint32_t dg[6];
+                        digits_of(a, b, dg);
+                        uint8_t *o = p.ad + static_cast<size_t>(slots[r]) * 6 * (p.I >> 1) + 32 * w.c + 4 * part;
+#pragma unroll
+                        for (int d = 0; d < 6; ++d) *reinterpret_cast<uint32_t *>(o + static_cast<size_t>(d) * (p.I >> 1)) = dg[d];
+                        if (part == 0) {
+                            uint8_t *f = reinterpret_cast<uint8_t *>(p.asf + (static_cast<size_t>(slots[r]) * (p.I >> 7) + (w.c >> 1)) * 8) +
+                                         2 * (w.c & 1);
+#pragma unroll
+                            for (int d = 0; d < 6; ++d)
+                                *reinterpret_cast<uint16_t *>(f + 4 * d) =
+                                    static_cast<uint16_t>(digit_scale(b, d) | (digit_scale(b2, d) << 8));
                         }
                     }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.empty[s]);
-            }
-            if (kh == 1) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) sh.red[it & 1][m][i][lane] = acc[i >> 2][i & 3];
-            }
-        }
-        if (!ok) *reinterpret_cast<volatile int *>(&sh.abort[it & 1]) = 1;
-        consumers_sync();
-        if (*reinterpret_cast<volatile int *>(&sh.abort[it & 1]) || u < 0) break;
-        if (kh == 1) continue;
-        // ------------------------------------------ epilogue, by the first half
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i >> 2][i & 3] += sh.red[it & 1][m][i][lane];
-        if (first) {
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int col = 8 * nt + 2 * q + i;
-                    // silu as in moe_experts.cu: off by up to (5 + 1.2 |g|) 2^-23 of itself, 0 below -87.3
-                    const float gv = acc[nt][i];
-                    if (col < rows) sh.act[col][8 * m + g] = __fdividef(gv, 1.0f + __expf(-gv)) * acc[nt][2 + i];
+                epilogue_sync();
+                if (tid == 0) {
+                    __threadfence();
+                    atomicAdd(p.made, 1);
                 }
-            first_half_sync();
-            for (int r = m; r < rows; r += 4) {
-                const float v = sh.act[r][lane];
-                const uint32_t b = mxfp8_scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7FFFFFFFu));
-                const int64_t row = slots[r];
-                p.act[row * p.I + 32 * c + lane] =
-                    static_cast<uint16_t>(f16x2_of_e4m3(v * mxfp8_scale_inverse(b), 0.0f) & 0xFFFFu);
-                if (lane == 0) p.act_sx[row * (p.I >> 5) + c] = scale_value(b);
-            }
-            first_half_sync();
-            if (tid == 0) {
-                __threadfence();
-                atomicAdd(p.made, 1);
-            }
-        } else {
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int col = 8 * nt + 2 * q + (i & 1);
-                    if (col < rows)
-                        p.y[static_cast<int64_t>(slots[col]) * p.H + 64 * c + 16 * m + g + 8 * (i >> 1)] = acc[nt][i];
+            } else {
+                if (tid == 0) {
+                    __threadfence();
+                    sh.last = atomicAdd(p.arrived + w.c, 1) == active - 1;
+                    __threadfence();
                 }
-            first_half_sync();
-            if (tid == 0) {
-                __threadfence();
-                sh.last = atomicAdd(p.arrived + c, 1) == active - 1;
-                __threadfence();
-            }
-            first_half_sync();
-            if (sh.last) {
-                // all experts' rows of these channels are there: the weighted sum, in the order of a token's choices
-                for (int i = tid; i < p.T * 64; i += 128) {
-                    const int t = i >> 6, ch = 64 * c + (i & 63);
-                    float s = 0.0f;
-                    for (int j = 0; j < p.k; ++j)
-                        if (p.ids[t * p.k + j] >= 0)
-                            s = fmaf(p.weights[t * p.k + j], __ldcg(p.y + static_cast<int64_t>(t * p.k + j) * p.H + ch), s);
-                    p.out[t * p.ldo + ch] = __bfloat16_as_ushort(__float2bfloat16_rn(s));
+                epilogue_sync();
+                if (sh.last) {
+                    // all experts' rows of these channels are there: the weighted sum, in the order of a token's choices
+                    const int ch = 128 * w.c + tid;
+                    for (int t = 0; t < p.T; ++t) {
+                        float s = 0.0f;
+                        for (int j = 0; j < p.k; ++j)
+                            if (p.ids[t * p.k + j] >= 0)
+                                s = fmaf(p.weights[t * p.k + j], __ldcg(p.y + static_cast<size_t>(t * p.k + j) * p.H + ch), s);
+                        p.out[t * p.ldo + ch] = __bfloat16_as_ushort(__float2bfloat16_rn(s));
+                    }
                 }
             }
         }
     }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    grid_launch_dependents();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemColumns);
+    }
 }
+
+constexpr uint32_t kExpertsSmem = 232448;
 
 template <typename Kern, typename P>
 cudaError_t launch_pdl(Kern kern, unsigned grid, unsigned block, size_t smem, cudaStream_t stream, const P &params)
@@ -780,16 +974,16 @@ MoeFewLayout moe_few_layout(int64_t T, int k, int E, int64_t H, int64_t I)
         return was;
     };
     const size_t slices = H / kSlice, R = static_cast<size_t>(T) * k;
-    l.counters = take(sizeof(int) * (64 + H / 64));
+    l.counters = take(sizeof(int) * (64 + H / 128));
     l.h = take(2 * T * H);
     l.part = take(4 * slices * T * E);
     l.part_ss = take(4 * slices * T);
-    l.xh = take(2 * T * H);
-    l.sx = take(4 * T * (H / 32));
+    l.xd = take(3 * T * H);
+    l.xsf = take(32 * T * (H / 128));
     l.ids = take(4 * R);
     l.weights = take(4 * R);
-    l.act = take(2 * R * I);
-    l.act_sx = take(4 * R * (I / 32));
+    l.ad = take(3 * R * I);
+    l.asf = take(32 * R * (I / 128));
     l.y = take(4 * R * H);
     l.total = at;
     return l;
@@ -815,7 +1009,7 @@ cudaError_t launch_moe_few(const MoeFewArgs &a, const MoeFewLayout &l, cudaStrea
     r.part = reinterpret_cast<float *>(a.ws + l.part);
     r.part_ss = reinterpret_cast<float *>(a.ws + l.part_ss);
     r.counters = reinterpret_cast<int *>(a.ws + l.counters);
-    r.num_counters = 64 + a.H / 64;
+    r.num_counters = 64 + a.H / 128;
     r.T = a.T;
     r.H = a.H;
     r.E = a.route.E;
@@ -829,8 +1023,8 @@ cudaError_t launch_moe_few(const MoeFewArgs &a, const MoeFewLayout &l, cudaStrea
     t.part = r.part;
     t.part_ss = r.part_ss;
     t.bias = a.route.bias;
-    t.xh = reinterpret_cast<uint16_t *>(a.ws + l.xh);
-    t.sx = reinterpret_cast<float *>(a.ws + l.sx);
+    t.xd = a.ws + l.xd;
+    t.xsf = reinterpret_cast<uint32_t *>(a.ws + l.xsf);
     t.ids = reinterpret_cast<int *>(a.ws + l.ids);
     t.weights = reinterpret_cast<float *>(a.ws + l.weights);
     t.ids_out = a.route.ids;
@@ -856,12 +1050,12 @@ cudaError_t launch_moe_few(const MoeFewArgs &a, const MoeFewLayout &l, cudaStrea
     p.tm_w2 = a.tm_w2;
     p.w13_sf = a.w13_sf;
     p.w2_sf = a.w2_sf;
-    p.xh = t.xh;
-    p.sx = t.sx;
+    p.xd = t.xd;
+    p.xsf = t.xsf;
     p.ids = t.ids;
     p.weights = t.weights;
-    p.act = reinterpret_cast<uint16_t *>(a.ws + l.act);
-    p.act_sx = reinterpret_cast<float *>(a.ws + l.act_sx);
+    p.ad = a.ws + l.ad;
+    p.asf = reinterpret_cast<uint32_t *>(a.ws + l.asf);
     p.y = reinterpret_cast<float *>(a.ws + l.y);
     p.out = a.out;
     p.ldo = a.ldo;
@@ -874,10 +1068,14 @@ cudaError_t launch_moe_few(const MoeFewArgs &a, const MoeFewLayout &l, cudaStrea
     p.H = a.H;
     p.I = a.I;
     p.wait_ns = wait_limit_ns();
+    // a stage has room for every token, and for the 16 columns of the smallest MMA
+    p.room = (a.T + 1) & ~1;
+    const uint32_t stage = kStageWeights + 2 * kStageScales + p.room * kTokenBytes;
+    p.stages = std::min<int>(kMaxStages, (kExpertsSmem - 1024 - sizeof(ExpertsShared)) / stage);
     // no more blocks than there can be units
     const int64_t experts = std::min<int64_t>(p.E, int64_t(p.T) * p.k);
-    const int64_t units = experts * (p.I / 32 + p.H / 64);
-    return launch_pdl(moe_few_experts_kernel, static_cast<unsigned>(std::min<int64_t>(2 * sms, units)), kExpertThreads,
+    const int64_t units = experts * (p.I / 64 + p.H / 128);
+    return launch_pdl(moe_few_experts_kernel, static_cast<unsigned>(std::min<int64_t>(sms, units)), kExpertThreads,
                       kExpertsSmem, stream, p);
 }
 

@@ -39,16 +39,4 @@ __device__ __forceinline__ uint32_t e4m3x4_rn(float x0, float x1, float x2, floa
     return r;
 }
 
-// fp16 pair of the E4M3 values of x0 (low half) and x1 (ties to even; exact in fp16).
-__device__ __forceinline__ uint32_t f16x2_of_e4m3(float x0, float x1)
-{
-    uint32_t r;
-    asm("{\n\t.reg .b16 c;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f32 c, %2, %1;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, c;\n\t}"
-        : "=r"(r)
-        : "f"(x0), "f"(x1));
-    return r;
-}
-
 }  // namespace mxfp4
