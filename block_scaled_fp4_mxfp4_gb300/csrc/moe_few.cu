@@ -108,8 +108,7 @@ constexpr int kSub = 20;                // floats from one 16 channels to the ne
 
 struct RouterParams {
     const uint16_t *x, *res, *w, *router;
-    uint16_t *h_out;                    // the caller's, or null
-    int64_t ldx, ldr, ldh;
+    int64_t ldx, ldr;
     uint16_t *h;                        // [T, H]
     float *part;                        // [slices][T][E]
     float *part_ss;                     // [slices][T]
@@ -129,7 +128,8 @@ __global__ void __launch_bounds__(kRouterThreads) moe_few_router_kernel(const Ro
     const int tid = threadIdx.x, k0 = blockIdx.x * kSlice;
     grid_dependency_wait();
     grid_launch_dependents();
-    for (int i = blockIdx.x * kRouterThreads + tid; i < p.num_counters; i += gridDim.x * kRouterThreads) p.counters[i] = 0;
+    if (blockIdx.y == 0)
+        for (int i = blockIdx.x * kRouterThreads + tid; i < p.num_counters; i += gridDim.x * kRouterThreads) p.counters[i] = 0;
     // eight neighbouring threads have the 64 channels of a token; whole warps go on for the shuffles
     const int t = tid >> 3, v = tid & 7, c = k0 + 8 * v;
     if ((t & ~3) < p.T) {
@@ -148,8 +148,7 @@ __global__ void __launch_bounds__(kRouterThreads) moe_few_router_kernel(const Ro
                 }
             }
             const uint4 h4 = make_uint4(hv[0], hv[1], hv[2], hv[3]);
-            *reinterpret_cast<uint4 *>(p.h + static_cast<int64_t>(t) * p.H + c) = h4;
-            if (p.h_out) *reinterpret_cast<uint4 *>(p.h_out + t * p.ldh + c) = h4;
+            if (blockIdx.y == 0) *reinterpret_cast<uint4 *>(p.h + static_cast<int64_t>(t) * p.H + c) = h4;
             const uint4 wv = *reinterpret_cast<const uint4 *>(p.w + c);
             const uint32_t w[4] = {wv.x, wv.y, wv.z, wv.w};
             float *o = &hw[t][(v >> 1) * kSub + (v & 1) * 8];
@@ -164,13 +163,13 @@ __global__ void __launch_bounds__(kRouterThreads) moe_few_router_kernel(const Ro
         ss += __shfl_xor_sync(0xffffffffu, ss, 1);
         ss += __shfl_xor_sync(0xffffffffu, ss, 2);
         ss += __shfl_xor_sync(0xffffffffu, ss, 4);
-        if (t < p.T && v == 0) p.part_ss[blockIdx.x * p.T + t] = ss;
+        if (t < p.T && v == 0 && blockIdx.y == 0) p.part_ss[blockIdx.x * p.T + t] = ss;
     }
     __syncthreads();
-    // four neighbouring lanes take 16 channels each of one expert
+    // four neighbouring lanes take 16 channels each of one expert, a block 64 experts
     const int sub = tid & 3;
-    for (int e0 = (tid >> 5) * 8; e0 < p.E; e0 += kRouterThreads / 4) {
-        const int e = e0 + ((tid & 31) >> 2);
+    const int e = blockIdx.y * (kRouterThreads / 4) + (tid >> 2);
+    if ((e & ~7) < p.E) {
         float wr[16];
         if (e < p.E) {
             const uint4 *src = reinterpret_cast<const uint4 *>(p.router + static_cast<int64_t>(e) * p.H + k0 + 16 * sub);
@@ -214,12 +213,15 @@ struct TokenParams {
     const float *bias;                  // [E] or null
     uint8_t *xd;                        // [T][6][H / 2] digits of y
     uint32_t *xsf;                      // [T][H / 128][8] their scales, four blocks of 32 a word, six words used
+    uint16_t *h_out;                    // the caller's, or null
+    int64_t ldh;
     int *ids;                           // [T, k], of the workspace
     float *weights;
     int *ids_out;                       // the caller's, or null
     float *weights_out;
     int T, H, E, k, slices, groups, topk_groups, group_top, sigmoid, renorm;
     float eps, scale;
+    double inv_h;
 };
 
 // A key that orders as the values do, NaN above all; 0 stands for "none".
@@ -274,8 +276,11 @@ __global__ void __launch_bounds__(kTokenThreads) moe_few_token_kernel(const Toke
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         if (lane == 0) {
-            const double m = ss / p.H + static_cast<double>(p.eps);
-            r_shared = m == 0.0 ? 0.0 : 1.0 / sqrt(m);
+            // a root of fp32 and one step of Newton's method in 64 bits: 2^-44, and a quarter of
+            // the time of a division and a root there
+            const double m = ss * p.inv_h + static_cast<double>(p.eps);
+            const double r0 = rsqrtf(static_cast<float>(m));
+            r_shared = m == 0.0 ? 0.0 : (isinf(m) ? 0.0 : r0 * (1.5 - 0.5 * m * r0 * r0));
         }
     }
     // logits: `parts` threads an expert over interleaved slices, added in a fixed order
@@ -398,6 +403,8 @@ __global__ void __launch_bounds__(kTokenThreads) moe_few_token_kernel(const Toke
     for (int v = tid; v < p.H / 8; v += kTokenThreads) {     // H / 8 is a multiple of 16: whole groups of four
         const uint4 hv = *reinterpret_cast<const uint4 *>(p.h + static_cast<int64_t>(t) * p.H + 8 * v);
         const uint4 wv = *reinterpret_cast<const uint4 *>(p.w + 8 * v);
+        // only now: H may be X or residual, which the launch before read
+        if (p.h_out) *reinterpret_cast<uint4 *>(p.h_out + t * p.ldh + 8 * v) = hv;
         const uint32_t ha[4] = {hv.x, hv.y, hv.z, hv.w}, wa[4] = {wv.x, wv.y, wv.z, wv.w};
         float y[8];
         uint32_t amax = 0;
@@ -427,7 +434,7 @@ __global__ void __launch_bounds__(kTokenThreads) moe_few_token_kernel(const Toke
 
 // ----------------------------------------------------------------- experts
 
-constexpr int kExpertThreads = 320;
+constexpr int kExpertThreads = 448;
 constexpr int kMaxStages = 12;
 constexpr int kEpiLd = 132;                              // floats of a staged token
 constexpr uint32_t kStageWeights = 128 * 128;            // 128 rows x 256 elements
@@ -453,7 +460,7 @@ struct ExpertsParams {
     int64_t ldo;
     int *queue;                         // units claimed
     int *made;                          // units of product 1 that are complete
-    int *arrived;                       // [H / 128] experts whose product 2 of these channels is complete
+    int *arrived;                       // [H / 32] experts whose product 2 of these channels is complete
     int T, k, E, H, I;
     int stages, room;                   // stages of the ring, tokens that one has room for
     uint64_t wait_ns;
@@ -466,13 +473,17 @@ struct ExpertsShared {
     uint64_t empty[kMaxStages];         // the stage's MMAs have completed
     uint64_t unit_full[4], unit_empty[4];
     uint64_t acc_full[2], acc_empty[2];
+    uint64_t fin_full[4], fin_empty[4]; // a unit's results are written / accounted for
     uint64_t mma_done;
     uint32_t tmem;
     int unit[4];                        // units in the order they were claimed, -1: there are no more
-    int abort, active, last, go[2];
+    int abort, active, last[4], go[2];
+    float weight[kMaxChoices];          // of the choices
     uint16_t expert[kMaxChoices];       // the experts that some token chose
     uint16_t first[kMaxChoices];        // the first of an expert's entries in slot, in that order
     uint16_t slot[kMaxChoices];         // choices t * k + j by expert
+    uint8_t token[kMaxChoices];         // their tokens
+    uint8_t kept[kMaxChoices];          // whether choice t * k + j has an expert
     alignas(16) uint8_t rows[kMaxExperts];   // choices of an expert, counted four in a word
 };
 static_assert(offsetof(ExpertsShared, rows) % 4 == 0 && offsetof(ExpertsShared, w_full) % 8 == 0, "aligned as it is used");
@@ -523,6 +534,7 @@ __device__ __forceinline__ Unit unit_at(int u, int n1, int active, int tiles1)
 //   4-7  copy tokens' digits and all scales into the ring by cp.async
 //   8    lane 0 claims units and loads their weights by TMA
 //   9    issues scale copies and MMAs (an elected lane); owns TMEM
+//   10-13 publish a unit's results and, after the last expert of a tile, sum its rows
 // Waits name a round of a barrier by its parity. Nobody can be a round behind: the next
 // round of a stage needs the TMA thread and every copying thread, the next of a unit's
 // entry or of an accumulator everyone who waits for this one.
@@ -542,7 +554,9 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&sh.unit_full[i], 1);
-            mbar_init(&sh.unit_empty[i], 6);     // four copying warps, the issuer, the epilogue
+            mbar_init(&sh.unit_empty[i], 10);    // four copying warps, the issuer, the epilogue, four finishing warps
+            mbar_init(&sh.fin_full[i], 128);
+            mbar_init(&sh.fin_empty[i], 4);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.acc_full[i], 1);
@@ -571,6 +585,10 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
     for (int i = 0; i < 2; ++i) {
         const int c = tid + i * kExpertThreads;
         const int e = c < p.T * p.k ? __ldcg(p.ids + c) : -1;
+        if (c < p.T * p.k) {
+            sh.kept[c] = e >= 0;
+            sh.weight[c] = __ldcg(p.weights + c);
+        }
         if (e >= 0) {
             const uint32_t was = atomicAdd(reinterpret_cast<uint32_t *>(sh.rows) + (e >> 2), 1u << (8 * (e & 3)));
             mine[i] = (static_cast<uint32_t>(e + 1) << 8) | ((was >> (8 * (e & 3))) & 0xFF);
@@ -602,7 +620,11 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-        if (mine[i]) sh.slot[start_of[(mine[i] >> 8) - 1] + (mine[i] & 0xFF)] = static_cast<uint16_t>(tid + i * kExpertThreads);
+        if (mine[i]) {
+            const int at = start_of[(mine[i] >> 8) - 1] + (mine[i] & 0xFF), c = tid + i * kExpertThreads;
+            sh.slot[at] = static_cast<uint16_t>(c);
+            sh.token[at] = static_cast<uint8_t>(c / p.k);
+        }
     __syncthreads();
     const int active = sh.active;
     const int tiles1 = p.I >> 6, n1 = active * tiles1, n2 = active * (p.H >> 7);
@@ -721,7 +743,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
         if (elect_one()) tc_commit(&sh.mma_done);
         __syncwarp();
         mbar_wait_warp(&sh.mma_done, 0, &g_moe_few_error, kErrWaitDrain);
-    } else if (warp >= 4) {
+    } else if (warp >= 4 && warp < 8) {
         // -------------------------------------------------- tokens and scales
         const int t = tid - 128;
         Place at{0, 0};
@@ -736,7 +758,9 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
             if (u < 0) break;
             const Unit w = unit_at(u, n1, active, tiles1);
             const int e = sh.expert[w.a], rows = sh.rows[e];
-            const uint16_t *slots = sh.slot + sh.first[w.a];
+            const int first = sh.first[w.a];
+            // row of an expert's choice among the tokens or the activations
+            auto row_of = [&](int r) { return static_cast<size_t>(w.first ? sh.token[first + r] : sh.slot[first + r]); };
             const int K = w.first ? p.H : p.I, kc = K >> 7, stages = (kc + 1) >> 1;
             if (!w.first && !ready) {
                 // the activations have to be there, of all units
@@ -767,8 +791,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
                 src[j] = nullptr;
                 dst[j] = 0;
                 if (r < rows) {
-                    const int row = w.first ? slots[r] / p.k : slots[r];
-                    src[j] = digits + static_cast<size_t>(row * 6 + dg) * (K >> 1) + 16 * c;
+                    src[j] = digits + (row_of(r) * 6 + dg) * (K >> 1) + 16 * c;
                     dst[j] = kStageWeights + 2 * kStageScales + (8 * r + dg) * 128 + ((c ^ dg) << 4);
                 }
             }
@@ -781,8 +804,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
                 ssrc[j] = nullptr;
                 sdst[j] = kStageWeights + kStageScales + h * 512 + (n & 31) * 16 + (n >> 5) * 4;
                 if (r < rows && dg < 6) {
-                    const int row = w.first ? slots[r] / p.k : slots[r];
-                    ssrc[j] = scales + (static_cast<size_t>(row) * kc + h) * 8 + dg;
+                    ssrc[j] = scales + (row_of(r) * kc + h) * 8 + dg;
                 }
             }
             const bool second = (t & 1) != 0;                // scale words of a stage's second half
@@ -831,6 +853,56 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
             if (i >= count - S) ok = mbar_wait_warp(&sh.empty[back.slot], back.parity, &g_moe_few_error, kErrWaitDrain);
             back.step(S);
         }
+    } else if (warp >= 10) {
+        // ------------------------------- results are published, and summed by the last
+        // Off the epilogue's path: a fence for the whole GPU and an atomic take it over a
+        // microsecond.
+        const int t0 = tid - 320;
+        for (int i = 0;; ++i) {
+            bool ok = mbar_wait_warp(&sh.unit_full[i & 3], (i >> 2) & 1, &g_moe_few_error, kErrWaitFull, p.wait_ns);
+            const int u = ok ? *reinterpret_cast<volatile int *>(&sh.unit[i & 3]) : -1;
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(&sh.unit_empty[i & 3]);
+            if (u >= 0)
+                ok = mbar_wait_warp(&sh.fin_full[i & 3], (i >> 2) & 1, &g_moe_few_error, kErrWaitAccum, p.wait_ns);
+            if (!ok) *reinterpret_cast<volatile int *>(&sh.abort) = 1;
+            if (!ok || u < 0) break;
+            const Unit w = unit_at(u, n1, active, tiles1);
+            if (lane == 0) {
+                // a quarter of the unit's channels each: the warps need not meet
+                __threadfence();
+                if (w.first) {
+                    if (warp == 10) atomicAdd(p.made, 1);
+                } else {
+                    sh.last[warp - 10] = atomicAdd(p.arrived + 4 * w.c + warp - 10, 1) == active - 1;
+                    __threadfence();
+                }
+                mbar_arrive(&sh.fin_empty[i & 3]);
+            }
+            __syncwarp();
+            if (!w.first && sh.last[warp - 10]) {
+                // all experts' rows of these channels are there: the weighted sum, in the order of a token's choices
+                const int ch = 128 * w.c + t0;
+                for (int t = 0; t < p.T; ++t) {
+                    float s = 0.0f;
+                    for (int j0 = 0; j0 < p.k; j0 += 8) {
+                        float y[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int c = t * p.k + j0 + j;
+                            y[j] = j0 + j < p.k && sh.kept[c] ? __ldcg(p.y + static_cast<size_t>(c) * p.H + ch) : 0.0f;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int c = t * p.k + j0 + j;
+                            if (j0 + j < p.k && sh.kept[c]) s = fmaf(sh.weight[c], y[j], s);
+                        }
+                    }
+                    p.out[t * p.ldo + ch] = __bfloat16_as_ushort(__float2bfloat16_rn(s));
+                }
+            }
+            __syncwarp();
+        }
     } else {
         // ------------------------------------------------------------ epilogue
         for (int i = 0;; ++i) {
@@ -844,6 +916,9 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
                     if (u >= 0) ok = mbar_wait(&sh.acc_full[buf], (i >> 1) & 1, &g_moe_few_error, kErrWaitAccum, p.wait_ns);
                 }
                 if (!ok) *reinterpret_cast<volatile int *>(&sh.abort) = 1;
+                // and the finishing warps are done with the unit four before
+                if (ok && u >= 0)
+                    ok = mbar_wait(&sh.fin_empty[i & 3], ((i >> 2) & 1) ^ 1u, &g_moe_few_error, kErrWaitEmpty, p.wait_ns);
                 sh.go[buf] = ok && !*reinterpret_cast<volatile int *>(&sh.abort) ? u : -1;
             }
             epilogue_sync();
@@ -874,8 +949,8 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
             }
             tc_fence_before();
             mbar_arrive(&sh.acc_empty[buf]);
-            epilogue_sync();
             if (w.first) {
+                epilogue_sync();
                 // a thread has 8 channels of a token; four neighbours share a block of 32
                 const int r = tid >> 3, part = tid & 7;
                 if ((r & ~3) < rows) {
@@ -908,30 +983,9 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
                         }
                     }
                 }
-                epilogue_sync();
-                if (tid == 0) {
-                    __threadfence();
-                    atomicAdd(p.made, 1);
-                }
-            } else {
-                if (tid == 0) {
-                    __threadfence();
-                    sh.last = atomicAdd(p.arrived + w.c, 1) == active - 1;
-                    __threadfence();
-                }
-                epilogue_sync();
-                if (sh.last) {
-                    // all experts' rows of these channels are there: the weighted sum, in the order of a token's choices
-                    const int ch = 128 * w.c + tid;
-                    for (int t = 0; t < p.T; ++t) {
-                        float s = 0.0f;
-                        for (int j = 0; j < p.k; ++j)
-                            if (p.ids[t * p.k + j] >= 0)
-                                s = fmaf(p.weights[t * p.k + j], __ldcg(p.y + static_cast<size_t>(t * p.k + j) * p.H + ch), s);
-                        p.out[t * p.ldo + ch] = __bfloat16_as_ushort(__float2bfloat16_rn(s));
-                    }
-                }
+                epilogue_sync();     // the staging buffer is reused
             }
+            mbar_arrive(&sh.fin_full[i & 3]);
         }
     }
     __syncwarp();
@@ -947,10 +1001,10 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
 constexpr uint32_t kExpertsSmem = 232448;
 
 template <typename Kern, typename P>
-cudaError_t launch_pdl(Kern kern, unsigned grid, unsigned block, size_t smem, cudaStream_t stream, const P &params)
+cudaError_t launch_pdl(Kern kern, dim3 grid, unsigned block, size_t smem, cudaStream_t stream, const P &params)
 {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -974,7 +1028,7 @@ MoeFewLayout moe_few_layout(int64_t T, int k, int E, int64_t H, int64_t I)
         return was;
     };
     const size_t slices = H / kSlice, R = static_cast<size_t>(T) * k;
-    l.counters = take(sizeof(int) * (64 + H / 128));
+    l.counters = take(sizeof(int) * (64 + H / 32));
     l.h = take(2 * T * H);
     l.part = take(4 * slices * T * E);
     l.part_ss = take(4 * slices * T);
@@ -1001,19 +1055,17 @@ cudaError_t launch_moe_few(const MoeFewArgs &a, const MoeFewLayout &l, cudaStrea
     r.res = a.res;
     r.w = a.w;
     r.router = a.router;
-    r.h_out = a.h_out;
     r.ldx = a.ldx;
     r.ldr = a.ldr;
-    r.ldh = a.ldh;
     r.h = reinterpret_cast<uint16_t *>(a.ws + l.h);
     r.part = reinterpret_cast<float *>(a.ws + l.part);
     r.part_ss = reinterpret_cast<float *>(a.ws + l.part_ss);
     r.counters = reinterpret_cast<int *>(a.ws + l.counters);
-    r.num_counters = 64 + a.H / 128;
+    r.num_counters = 64 + a.H / 32;
     r.T = a.T;
     r.H = a.H;
     r.E = a.route.E;
-    e = launch_pdl(moe_few_router_kernel, a.H / kSlice, kRouterThreads, 0, stream, r);
+    e = launch_pdl(moe_few_router_kernel, dim3(a.H / kSlice, (a.route.E + 63) / 64), kRouterThreads, 0, stream, r);
     if (e != cudaSuccess) return e;
 
     TokenParams t;
@@ -1025,6 +1077,8 @@ cudaError_t launch_moe_few(const MoeFewArgs &a, const MoeFewLayout &l, cudaStrea
     t.bias = a.route.bias;
     t.xd = a.ws + l.xd;
     t.xsf = reinterpret_cast<uint32_t *>(a.ws + l.xsf);
+    t.h_out = a.h_out;
+    t.ldh = a.ldh;
     t.ids = reinterpret_cast<int *>(a.ws + l.ids);
     t.weights = reinterpret_cast<float *>(a.ws + l.weights);
     t.ids_out = a.route.ids;
@@ -1040,6 +1094,7 @@ cudaError_t launch_moe_few(const MoeFewArgs &a, const MoeFewLayout &l, cudaStrea
     t.sigmoid = a.route.sigmoid;
     t.renorm = a.route.renorm;
     t.eps = a.eps;
+    t.inv_h = 1.0 / a.H;
     t.scale = a.route.scale;
     e = launch_pdl(moe_few_token_kernel, a.T, kTokenThreads, 0, stream, t);
     if (e != cudaSuccess) return e;
