@@ -62,9 +62,45 @@ __device__ __forceinline__ uint32_t digit_scale(uint32_t b, int i)
     return b == 255 ? 255 : max(static_cast<int>(b) - 8 + 3 * i, 0);
 }
 
+// The six digits of the magnitudes of all E4M3 codes, four bits each as E2M1, d_0 lowest.
+struct DigitTable {
+    uint32_t of[128];
+};
+constexpr DigitTable digit_table()
+{
+    DigitTable t{};
+    for (int c = 0; c < 128; ++c) {
+        const int ex = c >> 3, m = c & 7;
+        int n = c == 127 ? 0 : (ex ? (8 + m) << (ex - 1) : m);      // 127: NaN, its scale says so
+        int d[6] = {};
+        for (int i = 0; i < 5; ++i) {
+            d[i] = ((n + 3) & 7) - 3;
+            n = (n - d[i]) / 8;
+        }
+        d[5] = n;
+        if (n == 5 || n == 7) {
+            d[5] = 6;
+            d[4] += n == 5 ? -8 : 8;
+        }
+        for (int i = 0; i < 6; ++i) {
+            const int a = d[i] < 0 ? -d[i] : d[i];
+            t.of[c] |= static_cast<uint32_t>((a <= 4 ? a : a / 2 + 2) | (d[i] < 0 ? 8 : 0)) << (4 * i);
+        }
+    }
+    return t;
+}
+__constant__ DigitTable kDigits = digit_table();
+
+// A copy of it in shared memory, where lanes may look up different codes at once; of
+// the block's first 128 threads.
+__device__ __forceinline__ void copy_digits(uint32_t (&table)[128])
+{
+    if (threadIdx.x < 128) table[threadIdx.x] = kDigits.of[threadIdx.x];
+}
+
 // Eight E2M1 codes a digit of y (four bits each, the first lowest), y of a block whose
 // MXFP8 scale byte is b. Digits whose scale lies below 2^-127 are left out.
-__device__ __forceinline__ void digits_of(const float (&y)[8], uint32_t b, uint32_t (&out)[6])
+__device__ __forceinline__ void digits_of(const uint32_t (&table)[128], const float (&y)[8], uint32_t b, uint32_t (&out)[6])
 {
     const float inv = mxfp8_scale_inverse(b);
     uint32_t codes[2];
@@ -74,26 +110,10 @@ __device__ __forceinline__ void digits_of(const float (&y)[8], uint32_t b, uint3
     for (int i = 0; i < 6; ++i) out[i] = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const uint32_t c = (codes[j >> 2] >> (8 * (j & 3))) & 0xFFu, ex = (c >> 3) & 15u, m = c & 7u;
-        int n = static_cast<int>(ex ? (8 + m) << (ex - 1) : m);
-        int d[6];
+        const uint32_t c = (codes[j >> 2] >> (8 * (j & 3))) & 0xFFu;
+        const uint32_t d = table[c & 0x7Fu] ^ (c & 0x80u ? 0x888888u : 0u);
 #pragma unroll
-        for (int i = 0; i < 5; ++i) {
-            d[i] = ((n + 3) & 7) - 3;
-            n = (n - d[i]) >> 3;
-        }
-        d[5] = n;
-        if (n == 5 || n == 7) {
-            d[5] = 6;
-            d[4] += n == 5 ? -8 : 8;
-        }
-        const uint32_t sign = c >> 7;
-#pragma unroll
-        for (int i = 0; i < 6; ++i) {
-            const uint32_t a = static_cast<uint32_t>(abs(d[i]));
-            const uint32_t code = (a <= 4 ? a : (a >> 1) + 2) | ((sign ^ (d[i] < 0 ? 1u : 0u)) << 3);
-            out[i] |= code << (4 * j);
-        }
+        for (int i = 0; i < 6; ++i) out[i] |= ((d >> (4 * i)) & 0xFu) << (4 * j);
     }
 #pragma unroll
     for (int i = 0; i < 3; ++i)
@@ -130,6 +150,25 @@ __global__ void __launch_bounds__(kRouterThreads) moe_few_router_kernel(const Ro
     grid_launch_dependents();
     if (blockIdx.y == 0)
         for (int i = blockIdx.x * kRouterThreads + tid; i < p.num_counters; i += gridDim.x * kRouterThreads) p.counters[i] = 0;
+    // four neighbouring lanes take 16 channels each of one expert, a block 64 experts
+    const int sub = tid & 3;
+    const int e = blockIdx.y * (kRouterThreads / 4) + (tid >> 2);
+    float wr[16];
+    {
+        uint4 a = make_uint4(0, 0, 0, 0), b = a;
+        if (e < p.E) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(p.router + static_cast<int64_t>(e) * p.H + k0 + 16 * sub);
+            a = __ldg(src);
+            b = __ldg(src + 1);
+        }
+        const uint32_t r[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 f = bf16x2(r[i]);
+            wr[2 * i] = f.x;
+            wr[2 * i + 1] = f.y;
+        }
+    }
     // eight neighbouring threads have the 64 channels of a token; whole warps go on for the shuffles
     const int t = tid >> 3, v = tid & 7, c = k0 + 8 * v;
     if ((t & ~3) < p.T) {
@@ -166,25 +205,7 @@ __global__ void __launch_bounds__(kRouterThreads) moe_few_router_kernel(const Ro
         if (t < p.T && v == 0 && blockIdx.y == 0) p.part_ss[blockIdx.x * p.T + t] = ss;
     }
     __syncthreads();
-    // four neighbouring lanes take 16 channels each of one expert, a block 64 experts
-    const int sub = tid & 3;
-    const int e = blockIdx.y * (kRouterThreads / 4) + (tid >> 2);
     if ((e & ~7) < p.E) {
-        float wr[16];
-        if (e < p.E) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(p.router + static_cast<int64_t>(e) * p.H + k0 + 16 * sub);
-            const uint4 a = __ldg(src), b = __ldg(src + 1);
-            const uint32_t r[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float2 f = bf16x2(r[i]);
-                wr[2 * i] = f.x;
-                wr[2 * i + 1] = f.y;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) wr[i] = 0.0f;
-        }
         for (int tk = 0; tk < p.T; ++tk) {
             const float4 *q = reinterpret_cast<const float4 *>(&hw[tk][sub * kSub]);
             float s = 0.0f;
@@ -258,6 +279,7 @@ __device__ __forceinline__ int take_best(uint32_t (&key)[kMaxExperts / 32], int 
     return static_cast<int>(e);
 }
 
+// Grid: tokens x parts of their channels; the first part of a token routes it too.
 __global__ void __launch_bounds__(kTokenThreads) moe_few_token_kernel(const TokenParams p)
 {
     __shared__ double sums[kTokenThreads];
@@ -265,14 +287,27 @@ __global__ void __launch_bounds__(kTokenThreads) moe_few_token_kernel(const Toke
     __shared__ double r_shared;
     __shared__ float red[kTokenThreads / 32];
     __shared__ uint32_t group_kept[kMaxExperts / 32];
+    __shared__ uint32_t table[128];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, t = blockIdx.x;
+    const int v = blockIdx.y * kTokenThreads + tid;          // this thread's eight channels
+    const bool in = v < p.H / 8;                             // H / 8 is a multiple of 16: whole groups of four
+    copy_digits(table);
+    // the launch before let this one start when all of its inputs were there
+    const uint4 wv = in ? *reinterpret_cast<const uint4 *>(p.w + 8 * v) : make_uint4(0, 0, 0, 0);
     grid_dependency_wait();
     grid_launch_dependents();
+    const uint4 hv = in ? *reinterpret_cast<const uint4 *>(p.h + static_cast<int64_t>(t) * p.H + 8 * v) : make_uint4(0, 0, 0, 0);
 
     // r, by one warp
     if (warp == 0) {
         double ss = 0.0;
-        for (int s = lane; s < p.slices; s += 32) ss += static_cast<double>(p.part_ss[s * p.T + t]);
+        for (int s0 = 0; s0 < p.slices; s0 += 128) {
+            float f[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = s0 + 32 * i + lane < p.slices ? p.part_ss[(s0 + 32 * i + lane) * p.T + t] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ss += static_cast<double>(f[i]);
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         if (lane == 0) {
@@ -284,15 +319,57 @@ __global__ void __launch_bounds__(kTokenThreads) moe_few_token_kernel(const Toke
         }
     }
     // logits: `parts` threads an expert over interleaved slices, added in a fixed order
-    const int parts = kTokenThreads / p.E;           // E <= 512
-    const int e = tid % p.E, part = tid / p.E;
     double z = 0.0;
-    if (part < parts)
-        for (int s = part; s < p.slices; s += parts)
-            z += static_cast<double>(p.part[(static_cast<int64_t>(s) * p.T + t) * p.E + e]);
-    sums[tid] = z;
+    const int parts = kTokenThreads / p.E;           // E <= 512
+    if (blockIdx.y == 0) {
+        const int e = tid % p.E, part = tid / p.E;
+        if (part < parts) {
+            const float *src = p.part + static_cast<int64_t>(t) * p.E + e;
+            const int64_t step = static_cast<int64_t>(p.T) * p.E;
+            for (int s0 = part; s0 < p.slices; s0 += 8 * parts) {
+                float f[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = s0 + i * parts < p.slices ? src[(s0 + i * parts) * step] : 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) z += static_cast<double>(f[i]);
+            }
+        }
+        sums[tid] = z;
+    }
     __syncthreads();
     const double r = r_shared;
+    {
+        // y in MXFP8, four lanes a block of 32
+        const float rf = static_cast<float>(r);
+        // only now: H may be X or residual, which the launch before read
+        if (in && p.h_out) *reinterpret_cast<uint4 *>(p.h_out + t * p.ldh + 8 * v) = hv;
+        const uint32_t ha[4] = {hv.x, hv.y, hv.z, hv.w}, wa[4] = {wv.x, wv.y, wv.z, wv.w};
+        float y[8];
+        uint32_t amax = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 a = bf16x2(ha[i]), b = bf16x2(wa[i]);
+            y[2 * i] = a.x * b.x * rf;
+            y[2 * i + 1] = a.y * b.y * rf;
+            amax = max(amax, max(__float_as_uint(y[2 * i]) & 0x7FFFFFFFu, __float_as_uint(y[2 * i + 1]) & 0x7FFFFFFFu));
+        }
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        if (in) {
+            const uint32_t b = mxfp8_scale_byte(amax);
+            uint32_t dg[6];
+            digits_of(table, y, b, dg);
+            uint8_t *o = p.xd + static_cast<size_t>(t) * 6 * (p.H >> 1) + 4 * v;
+#pragma unroll
+            for (int d = 0; d < 6; ++d) *reinterpret_cast<uint32_t *>(o + static_cast<size_t>(d) * (p.H >> 1)) = dg[d];
+            if ((v & 3) == 0) {
+                uint8_t *f = reinterpret_cast<uint8_t *>(p.xsf + (static_cast<size_t>(t) * (p.H >> 7) + (v >> 4)) * 8) + ((v >> 2) & 3);
+#pragma unroll
+                for (int d = 0; d < 6; ++d) f[4 * d] = static_cast<uint8_t>(digit_scale(b, d));
+            }
+        }
+    }
+    if (blockIdx.y > 0) return;
     float zf = -INFINITY;
     if (tid < p.E) {
         for (int i = 1; i < parts; ++i) z += sums[i * p.E + tid];
@@ -398,43 +475,12 @@ __global__ void __launch_bounds__(kTokenThreads) moe_few_token_kernel(const Toke
             if (p.weights_out) p.weights_out[t * p.k + lane] = w;
         }
     }
-    // y in MXFP8, four lanes a block of 32
-    const float rf = static_cast<float>(r);
-    for (int v = tid; v < p.H / 8; v += kTokenThreads) {     // H / 8 is a multiple of 16: whole groups of four
-        const uint4 hv = *reinterpret_cast<const uint4 *>(p.h + static_cast<int64_t>(t) * p.H + 8 * v);
-        const uint4 wv = *reinterpret_cast<const uint4 *>(p.w + 8 * v);
-        // only now: H may be X or residual, which the launch before read
-        if (p.h_out) *reinterpret_cast<uint4 *>(p.h_out + t * p.ldh + 8 * v) = hv;
-        const uint32_t ha[4] = {hv.x, hv.y, hv.z, hv.w}, wa[4] = {wv.x, wv.y, wv.z, wv.w};
-        float y[8];
-        uint32_t amax = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 a = bf16x2(ha[i]), b = bf16x2(wa[i]);
-            y[2 * i] = a.x * b.x * rf;
-            y[2 * i + 1] = a.y * b.y * rf;
-            amax = max(amax, max(__float_as_uint(y[2 * i]) & 0x7FFFFFFFu, __float_as_uint(y[2 * i + 1]) & 0x7FFFFFFFu));
-        }
-        const unsigned quad = 0xFu << (lane & ~3);
-        amax = max(amax, __shfl_xor_sync(quad, amax, 1));
-        amax = max(amax, __shfl_xor_sync(quad, amax, 2));
-        const uint32_t b = mxfp8_scale_byte(amax);
-        uint32_t dg[6];
-        digits_of(y, b, dg);
-        uint8_t *o = p.xd + static_cast<size_t>(t) * 6 * (p.H >> 1) + 4 * v;
-#pragma unroll
-        for (int d = 0; d < 6; ++d) *reinterpret_cast<uint32_t *>(o + static_cast<size_t>(d) * (p.H >> 1)) = dg[d];
-        if ((v & 3) == 0) {
-            uint8_t *f = reinterpret_cast<uint8_t *>(p.xsf + (static_cast<size_t>(t) * (p.H >> 7) + (v >> 4)) * 8) + ((v >> 2) & 3);
-#pragma unroll
-            for (int d = 0; d < 6; ++d) f[4 * d] = static_cast<uint8_t>(digit_scale(b, d));
-        }
-    }
 }
 
 // ----------------------------------------------------------------- experts
 
 constexpr int kExpertThreads = 448;
+constexpr int kMadeAt = 32, kArrivedAt = kMadeAt + kMaxExperts;     // counters behind the queue's
 constexpr int kMaxStages = 12;
 constexpr int kEpiLd = 132;                              // floats of a staged token
 constexpr uint32_t kStageWeights = 128 * 128;            // 128 rows x 256 elements
@@ -459,7 +505,7 @@ struct ExpertsParams {
     uint16_t *out;
     int64_t ldo;
     int *queue;                         // units claimed
-    int *made;                          // units of product 1 that are complete
+    int *made;                          // [active] units of an expert's product 1 that are complete
     int *arrived;                       // [H / 32] experts whose product 2 of these channels is complete
     int T, k, E, H, I;
     int stages, room;                   // stages of the ring, tokens that one has room for
@@ -479,6 +525,7 @@ struct ExpertsShared {
     int unit[4];                        // units in the order they were claimed, -1: there are no more
     int abort, active, last[4], go[2];
     float weight[kMaxChoices];          // of the choices
+    uint32_t digits[128];
     uint16_t expert[kMaxChoices];       // the experts that some token chose
     uint16_t first[kMaxChoices];        // the first of an expert's entries in slot, in that order
     uint16_t slot[kMaxChoices];         // choices t * k + j by expert
@@ -510,22 +557,19 @@ struct Place {
     }
 };
 
-// Unit u: weight tile c of the active expert a, product 1 if u < n1.
+// Unit u: weight tile c of the active expert a, product 1 if u < n1. Experts one after
+// another in both products: the first experts' activations are there when product 2 begins.
 struct Unit {
     bool first;
     int a, c;
 };
-__device__ __forceinline__ Unit unit_at(int u, int n1, int active, int tiles1)
+__device__ __forceinline__ Unit unit_at(int u, int n1, int tiles1, int tiles2)
 {
     Unit w;
     w.first = u < n1;
-    if (w.first) {
-        w.a = u / tiles1;
-        w.c = u - w.a * tiles1;
-    } else {
-        w.c = (u - n1) / active;
-        w.a = u - n1 - w.c * active;
-    }
+    const int i = w.first ? u : u - n1, tiles = w.first ? tiles1 : tiles2;
+    w.a = i / tiles;
+    w.c = i - w.a * tiles;
     return w;
 }
 
@@ -568,6 +612,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
         tma_prefetch_desc(&p.tm_w13);
         tma_prefetch_desc(&p.tm_w2);
     }
+    copy_digits(sh.digits);
     for (int i = tid; i < kMaxExperts / 4; i += kExpertThreads) reinterpret_cast<uint32_t *>(sh.rows)[i] = 0;
     if (warp == 9) {
         tmem_alloc(&sh.tmem, kTmemColumns);
@@ -627,7 +672,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
         }
     __syncthreads();
     const int active = sh.active;
-    const int tiles1 = p.I >> 6, n1 = active * tiles1, n2 = active * (p.H >> 7);
+    const int tiles1 = p.I >> 6, tiles2 = p.H >> 7, n1 = active * tiles1, n2 = active * tiles2;
 
     if (warp == 8) {
         if (lane == 0) {
@@ -639,7 +684,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
             // the weight scales of a unit go to L2 ahead of their copies
             auto ask_scales = [&](int u) {
                 if (u >= n1 + n2) return;
-                const Unit w = unit_at(u, n1, active, tiles1);
+                const Unit w = unit_at(u, n1, tiles1, tiles2);
                 const int e = sh.expert[w.a];
                 if (w.first) {
                     const uint32_t run = (p.H >> 7) * 512;
@@ -652,6 +697,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
                 }
             };
             int u = atomicAdd(p.queue, 1);
+            ask_scales(u);
             for (int i = 0;; ++i) {
                 const bool more = u < n1 + n2;
                 if (!(ok = mbar_wait(&sh.unit_empty[i & 3], ((i >> 2) & 1) ^ 1u, &g_moe_few_error, kErrWaitEmpty, p.wait_ns)))
@@ -660,7 +706,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
                 mbar_arrive(&sh.unit_full[i & 3]);
                 if (!more) break;
                 const int next = atomicAdd(p.queue, 1);    // on its way while this unit loads
-                const Unit w = unit_at(u, n1, active, tiles1);
+                const Unit w = unit_at(u, n1, tiles1, tiles2);
                 const int e = sh.expert[w.a];
                 const int stages = ((w.first ? p.H : p.I) + 255) >> 8;
                 // 64 rows of G and the same of U, or 128 rows
@@ -699,7 +745,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.unit_empty[i & 3]);
             if (u < 0) break;
-            const Unit w = unit_at(u, n1, active, tiles1);
+            const Unit w = unit_at(u, n1, tiles1, tiles2);
             const int kc = (w.first ? p.H : p.I) >> 7, stages = (kc + 1) >> 1, buf = i & 1;
             const int rows = sh.rows[sh.expert[w.a]];
             ok = mbar_wait_warp(&sh.acc_empty[buf], ((i >> 1) & 1) ^ 1u, &g_moe_few_error, kErrWaitAccum, p.wait_ns);
@@ -748,7 +794,8 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
         const int t = tid - 128;
         Place at{0, 0};
         int count = 0;
-        bool ok = true, ready = false;
+        int ready = -1;                  // active experts up to this one have all their activations
+        bool ok = true;
         for (int i = 0; ok; ++i) {
             ok = mbar_wait_warp(&sh.unit_full[i & 3], (i >> 2) & 1, &g_moe_few_error, kErrWaitFull, p.wait_ns);
             if (!ok) break;
@@ -756,18 +803,18 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.unit_empty[i & 3]);
             if (u < 0) break;
-            const Unit w = unit_at(u, n1, active, tiles1);
+            const Unit w = unit_at(u, n1, tiles1, tiles2);
             const int e = sh.expert[w.a], rows = sh.rows[e];
             const int first = sh.first[w.a];
             // row of an expert's choice among the tokens or the activations
             auto row_of = [&](int r) { return static_cast<size_t>(w.first ? sh.token[first + r] : sh.slot[first + r]); };
             const int K = w.first ? p.H : p.I, kc = K >> 7, stages = (kc + 1) >> 1;
-            if (!w.first && !ready) {
-                // the activations have to be there, of all units
+            if (!w.first && w.a > ready) {
+                // this expert's activations have to be there
                 int v = 1;
                 if (lane == 0) {
                     const uint64_t t0 = global_timer_ns();
-                    while (load_acquire(p.made) < n1) {
+                    while (load_acquire(p.made + w.a) < tiles1) {
                         if (global_timer_ns() - t0 > p.wait_ns) {
                             atomicCAS(&g_moe_few_error, 0, kErrWaitOperand);
                             v = 0;
@@ -778,7 +825,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
                 ok = __shfl_sync(0xffffffffu, v, 0) != 0;
                 __syncwarp();
                 if (!ok) break;
-                ready = true;
+                ready = w.a;
             }
             // a row of digits is K / 2 bytes, six of them a token; pieces of 16 bytes, column c of row n at c ^ (n % 8)
             const uint8_t *digits = w.first ? p.xd : p.ad;
@@ -857,7 +904,6 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
         // ------------------------------- results are published, and summed by the last
         // Off the epilogue's path: a fence for the whole GPU and an atomic take it over a
         // microsecond.
-        const int t0 = tid - 320;
         for (int i = 0;; ++i) {
             bool ok = mbar_wait_warp(&sh.unit_full[i & 3], (i >> 2) & 1, &g_moe_few_error, kErrWaitFull, p.wait_ns);
             const int u = ok ? *reinterpret_cast<volatile int *>(&sh.unit[i & 3]) : -1;
@@ -867,12 +913,12 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
                 ok = mbar_wait_warp(&sh.fin_full[i & 3], (i >> 2) & 1, &g_moe_few_error, kErrWaitAccum, p.wait_ns);
             if (!ok) *reinterpret_cast<volatile int *>(&sh.abort) = 1;
             if (!ok || u < 0) break;
-            const Unit w = unit_at(u, n1, active, tiles1);
+            const Unit w = unit_at(u, n1, tiles1, tiles2);
             if (lane == 0) {
                 // a quarter of the unit's channels each: the warps need not meet
                 __threadfence();
                 if (w.first) {
-                    if (warp == 10) atomicAdd(p.made, 1);
+                    if (warp == 10) atomicAdd(p.made + w.a, 1);
                 } else {
                     sh.last[warp - 10] = atomicAdd(p.arrived + 4 * w.c + warp - 10, 1) == active - 1;
                     __threadfence();
@@ -882,23 +928,31 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
             __syncwarp();
             if (!w.first && sh.last[warp - 10]) {
                 // all experts' rows of these channels are there: the weighted sum, in the order of a token's choices
-                const int ch = 128 * w.c + t0;
-                for (int t = 0; t < p.T; ++t) {
-                    float s = 0.0f;
+                const int ch = 128 * w.c + tid - 320;
+                for (int t0 = 0; t0 < p.T; t0 += 4) {
+                    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                     for (int j0 = 0; j0 < p.k; j0 += 8) {
-                        float y[8];
+                        // 32 loads on their way
+                        float y[4][8];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const int c = t * p.k + j0 + j;
-                            y[j] = j0 + j < p.k && sh.kept[c] ? __ldcg(p.y + static_cast<size_t>(c) * p.H + ch) : 0.0f;
-                        }
+                        for (int t = 0; t < 4; ++t)
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const int c = t * p.k + j0 + j;
-                            if (j0 + j < p.k && sh.kept[c]) s = fmaf(sh.weight[c], y[j], s);
-                        }
+                            for (int j = 0; j < 8; ++j) {
+                                const int c = (t0 + t) * p.k + j0 + j;
+                                const bool has = t0 + t < p.T && j0 + j < p.k && sh.kept[c];
+                                y[t][j] = has ? __ldcg(p.y + static_cast<size_t>(c) * p.H + ch) : 0.0f;
+                            }
+#pragma unroll
+                        for (int t = 0; t < 4; ++t)
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const int c = (t0 + t) * p.k + j0 + j;
+                                if (t0 + t < p.T && j0 + j < p.k && sh.kept[c]) s[t] = fmaf(sh.weight[c], y[t][j], s[t]);
+                            }
                     }
-                    p.out[t * p.ldo + ch] = __bfloat16_as_ushort(__float2bfloat16_rn(s));
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        if (t0 + t < p.T) p.out[(t0 + t) * p.ldo + ch] = __bfloat16_as_ushort(__float2bfloat16_rn(s[t]));
                 }
             }
             __syncwarp();
@@ -925,7 +979,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
             const int u = sh.go[buf];
             if (u < 0) break;
             tc_fence_after();
-            const Unit w = unit_at(u, n1, active, tiles1);
+            const Unit w = unit_at(u, n1, tiles1, tiles2);
             const int rows = sh.rows[sh.expert[w.a]];
             const uint16_t *slots = sh.slot + sh.first[w.a];
             const uint32_t trow = tmem + buf * kAccColumns + (static_cast<uint32_t>(warp * 32) << 16);
@@ -969,7 +1023,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
                     const uint32_t b2 = __shfl_down_sync(0xffffffffu, b, 4);
                     if (r < rows) {
                         uint32_t dg[6];
-                        digits_of(a, b, dg);
+                        digits_of(sh.digits, a, b, dg);
                         uint8_t *o = p.ad + static_cast<size_t>(slots[r]) * 6 * (p.I >> 1) + 32 * w.c + 4 * part;
 #pragma unroll
                         for (int d = 0; d < 6; ++d) *reinterpret_cast<uint32_t *>(o + static_cast<size_t>(d) * (p.I >> 1)) = dg[d];
@@ -1028,7 +1082,7 @@ MoeFewLayout moe_few_layout(int64_t T, int k, int E, int64_t H, int64_t I)
         return was;
     };
     const size_t slices = H / kSlice, R = static_cast<size_t>(T) * k;
-    l.counters = take(sizeof(int) * (64 + H / 32));
+    l.counters = take(sizeof(int) * (kArrivedAt + H / 32));
     l.h = take(2 * T * H);
     l.part = take(4 * slices * T * E);
     l.part_ss = take(4 * slices * T);
@@ -1061,7 +1115,7 @@ cudaError_t launch_moe_few(const MoeFewArgs &a, const MoeFewLayout &l, cudaStrea
     r.part = reinterpret_cast<float *>(a.ws + l.part);
     r.part_ss = reinterpret_cast<float *>(a.ws + l.part_ss);
     r.counters = reinterpret_cast<int *>(a.ws + l.counters);
-    r.num_counters = 64 + a.H / 32;
+    r.num_counters = kArrivedAt + a.H / 32;
     r.T = a.T;
     r.H = a.H;
     r.E = a.route.E;
@@ -1096,7 +1150,7 @@ cudaError_t launch_moe_few(const MoeFewArgs &a, const MoeFewLayout &l, cudaStrea
     t.eps = a.eps;
     t.inv_h = 1.0 / a.H;
     t.scale = a.route.scale;
-    e = launch_pdl(moe_few_token_kernel, a.T, kTokenThreads, 0, stream, t);
+    e = launch_pdl(moe_few_token_kernel, dim3(a.T, (a.H / 8 + kTokenThreads - 1) / kTokenThreads), kTokenThreads, 0, stream, t);
     if (e != cudaSuccess) return e;
 
     ExpertsParams p;
@@ -1115,8 +1169,8 @@ cudaError_t launch_moe_few(const MoeFewArgs &a, const MoeFewLayout &l, cudaStrea
     p.out = a.out;
     p.ldo = a.ldo;
     p.queue = r.counters;
-    p.made = r.counters + 32;
-    p.arrived = r.counters + 64;
+    p.made = r.counters + kMadeAt;
+    p.arrived = r.counters + kArrivedAt;
     p.T = a.T;
     p.k = a.route.k;
     p.E = a.route.E;
