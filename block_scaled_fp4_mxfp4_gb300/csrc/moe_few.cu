@@ -5,11 +5,11 @@
 // logits z_e = r sum_k h_k w_k Wr[e, k], the k best experts and their weights, then
 //   act = MXFP8(silu(G_e q) * (U_e q)),  q = MXFP8(y),  out_t = sum_j w_tj (W2_e act).
 //
-// Three launches, each one starting while the last drains:
+// Four launches, each one starting while the last drains:
 //   router   blocks take 64 channels each: h, sums of squares and of the router's
 //            products over them, for all tokens
 //   tokens   a block a token: adds those sums in 64 bits, y in MXFP8, routing
-//   experts  both products and the sum. Weights are what there is to read, so the
+//   experts  both products. Weights are what there is to read, so the
 //            kernel is a stream of them into a ring of shared memory, by TMA, as they
 //            lie in memory, and tcgen05.mma kind::mxf4 of them with the activations'
 //            digits (below). (mxfp4_moe_experts multiplies with kind::mxf8f6f4, which
@@ -17,8 +17,11 @@
 //            batch at half of HBM's rate. Widening in registers for mma.sync was measured
 //            too: 90 instructions for 512 weights, 114 us where the stream takes 28.)
 //
+//   sum      the weighted sum of a token's rows, in the order of its choices
+//
 // Units of work: 64 channels of an expert in product 1 (their rows of G and of U), 128 in
-// product 2. Blocks claim them from one counter, product 1 first, so that a unit that
+// product 2, each for up to four of its tokens: more than four take another unit, whose
+// weights come from L2. Blocks claim them from one counter, product 1 first, so that a unit that
 // waits for activations only waits for units that somebody already works on: no
 // assumption on which blocks run at the same time. While it waits, its weights fill the ring.
 //
@@ -98,8 +101,19 @@ __device__ __forceinline__ void copy_digits(uint32_t (&table)[128])
     if (threadIdx.x < 128) table[threadIdx.x] = kDigits.of[threadIdx.x];
 }
 
+// The six digits of an E4M3 code in a block whose scale byte is b, four bits each. Those
+// whose scale lies below 2^-127 are left out.
+__device__ __forceinline__ uint32_t digits_of(const uint32_t (&table)[128], uint32_t c, uint32_t b)
+{
+    uint32_t d = table[c & 0x7Fu] ^ (c & 0x80u ? 0x888888u : 0u);
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        if (b + 3 * i < 8) d &= ~(0xFu << (4 * i));
+    return d;
+}
+
 // Eight E2M1 codes a digit of y (four bits each, the first lowest), y of a block whose
-// MXFP8 scale byte is b. Digits whose scale lies below 2^-127 are left out.
+// MXFP8 scale byte is b.
 __device__ __forceinline__ void digits_of(const uint32_t (&table)[128], const float (&y)[8], uint32_t b, uint32_t (&out)[6])
 {
     const float inv = mxfp8_scale_inverse(b);
@@ -111,13 +125,10 @@ __device__ __forceinline__ void digits_of(const uint32_t (&table)[128], const fl
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const uint32_t c = (codes[j >> 2] >> (8 * (j & 3))) & 0xFFu;
-        const uint32_t d = table[c & 0x7Fu] ^ (c & 0x80u ? 0x888888u : 0u);
+        const uint32_t d = digits_of(table, c, b);
 #pragma unroll
         for (int i = 0; i < 6; ++i) out[i] |= ((d >> (4 * i)) & 0xFu) << (4 * j);
     }
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-        if (b + 3 * i < 8) out[i] = 0;
 }
 
 // ------------------------------------------------------------------ router
@@ -479,17 +490,18 @@ __global__ void __launch_bounds__(kTokenThreads) moe_few_token_kernel(const Toke
 
 // ----------------------------------------------------------------- experts
 
-constexpr int kExpertThreads = 448;
-constexpr int kMadeAt = 32, kArrivedAt = kMadeAt + kMaxExperts;     // counters behind the queue's
-constexpr int kMaxStages = 12;
-constexpr int kEpiLd = 132;                              // floats of a staged token
+constexpr int kExpertThreads = 320;
+constexpr int kRoom = 4;                                 // tokens of a unit at most
+constexpr int kMaxEntries = kMaxChoices;
+constexpr int kMaxStages = 5;
+constexpr int kMadeAt = 32;                              // counters of the entries behind the queue's
 constexpr uint32_t kStageWeights = 128 * 128;            // 128 rows x 256 elements
 constexpr uint32_t kStageScales = 1024;                  // two blocks of 512 bytes: of the weights, then of the tokens
 constexpr uint32_t kTokenBytes = 1024;                   // of a token in a stage: eight rows (six used) x 256 elements
-constexpr uint32_t kAccColumns = 8 * kMaxTokens;
+constexpr uint32_t kAccColumns = 8 * kRoom;
 constexpr uint32_t kSfColumns = 16;                      // of a stage: two blocks of weights, two of tokens
-constexpr uint32_t kTmemColumns = 512;
-static_assert(2 * kAccColumns + kMaxStages * kSfColumns <= kTmemColumns, "TMEM budget");
+constexpr uint32_t kTmemColumns = 256;
+static_assert(2 * kAccColumns + kMaxStages * kSfColumns <= kTmemColumns, "TMEM budget: half of it, two blocks an SM");
 
 struct ExpertsParams {
     CUtensorMap tm_w13;                 // packed weights [E * 2I, H / 2] u8, box 128 bytes x 64 rows
@@ -498,39 +510,40 @@ struct ExpertsParams {
     const uint8_t *xd;                  // [T][6][H / 2] digits of the tokens
     const uint32_t *xsf;                // [T][H / 128][8] their scales
     const int *ids;
-    const float *weights;
     uint8_t *ad;                        // [T * k][6][I / 2] of the activations
     uint32_t *asf;                      // [T * k][I / 128][8]
     float *y;                           // [T * k, H]
-    uint16_t *out;
-    int64_t ldo;
     int *queue;                         // units claimed
-    int *made;                          // [active] units of an expert's product 1 that are complete
-    int *arrived;                       // [H / 32] experts whose product 2 of these channels is complete
+    int *made;                          // [entries] warps that are done with a unit of an entry's product 1
     int T, k, E, H, I;
     int stages, room;                   // stages of the ring, tokens that one has room for
     uint64_t wait_ns;
 };
 
+// A unit of work: weight tile c of expert e for up to four of its choices.
+struct Unit {
+    int first;                          // product 1; -1: there are no more units
+    int e, c;
+    int entry, slots, rows;             // in the list of entries; its first choice in `slot`, and how many
+};
+
 struct ExpertsShared {
-    float epi[kMaxTokens][kEpiLd];
+    float epi[kRoom][128];
     uint64_t w_full[kMaxStages];        // weights have landed
     uint64_t t_full[kMaxStages];        // tokens and scales have landed
     uint64_t empty[kMaxStages];         // the stage's MMAs have completed
     uint64_t unit_full[4], unit_empty[4];
     uint64_t acc_full[2], acc_empty[2];
-    uint64_t fin_full[4], fin_empty[4]; // a unit's results are written / accounted for
     uint64_t mma_done;
     uint32_t tmem;
-    int unit[4];                        // units in the order they were claimed, -1: there are no more
-    int abort, active, last[4], go[2];
-    float weight[kMaxChoices];          // of the choices
+    int abort, entries, go[2];
+    Unit unit[4];                       // in the order they were claimed
     uint32_t digits[128];
-    uint16_t expert[kMaxChoices];       // the experts that some token chose
-    uint16_t first[kMaxChoices];        // the first of an expert's entries in slot, in that order
+    uint16_t entry_expert[kMaxEntries], entry_slots[kMaxEntries];
     uint16_t slot[kMaxChoices];         // choices t * k + j by expert
-    uint8_t token[kMaxChoices];         // their tokens
-    uint8_t kept[kMaxChoices];          // whether choice t * k + j has an expert
+    uint16_t start[kMaxExperts];        // the first of an expert's choices there
+    uint8_t entry_rows[kMaxEntries];
+    uint8_t token[kMaxChoices];         // tokens of the choices in slot
     alignas(16) uint8_t rows[kMaxExperts];   // choices of an expert, counted four in a word
 };
 static_assert(offsetof(ExpertsShared, rows) % 4 == 0 && offsetof(ExpertsShared, w_full) % 8 == 0, "aligned as it is used");
@@ -557,32 +570,17 @@ struct Place {
     }
 };
 
-// Unit u: weight tile c of the active expert a, product 1 if u < n1. Experts one after
-// another in both products: the first experts' activations are there when product 2 begins.
-struct Unit {
-    bool first;
-    int a, c;
-};
-__device__ __forceinline__ Unit unit_at(int u, int n1, int tiles1, int tiles2)
-{
-    Unit w;
-    w.first = u < n1;
-    const int i = w.first ? u : u - n1, tiles = w.first ? tiles1 : tiles2;
-    w.a = i / tiles;
-    w.c = i - w.a * tiles;
-    return w;
-}
-
 // Warps:
 //   0-3  epilogue of a finished tile while the next one's products run
 //   4-7  copy tokens' digits and all scales into the ring by cp.async
 //   8    lane 0 claims units and loads their weights by TMA
 //   9    issues scale copies and MMAs (an elected lane); owns TMEM
-//   10-13 publish a unit's results and, after the last expert of a tile, sum its rows
+// Two blocks share an SM: what a unit costs beside its bytes (a microsecond or two of
+// latencies at its start and end) passes while the other block's weights stream.
 // Waits name a round of a barrier by its parity. Nobody can be a round behind: the next
 // round of a stage needs the TMA thread and every copying thread, the next of a unit's
 // entry or of an accumulator everyone who waits for this one.
-__global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(const __grid_constant__ ExpertsParams p)
+__global__ void __launch_bounds__(kExpertThreads, 2) moe_few_experts_kernel(const __grid_constant__ ExpertsParams p)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -598,9 +596,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&sh.unit_full[i], 1);
-            mbar_init(&sh.unit_empty[i], 10);    // four copying warps, the issuer, the epilogue, four finishing warps
-            mbar_init(&sh.fin_full[i], 128);
-            mbar_init(&sh.fin_empty[i], 4);
+            mbar_init(&sh.unit_empty[i], 6);     // four copying warps, the issuer, the epilogue
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.acc_full[i], 1);
@@ -623,6 +619,8 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
     grid_dependency_wait();
+    int claimed = 0;
+    if (tid == 256) claimed = atomicAdd(p.queue, 1);     // on its way while the lists are made
     // Choices by expert. The order of an expert's choices does not matter: columns of an
     // MMA do not mix.
     uint32_t mine[2] = {0, 0};               // (expert + 1, place among its choices) of this thread's choices
@@ -630,49 +628,46 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
     for (int i = 0; i < 2; ++i) {
         const int c = tid + i * kExpertThreads;
         const int e = c < p.T * p.k ? __ldcg(p.ids + c) : -1;
-        if (c < p.T * p.k) {
-            sh.kept[c] = e >= 0;
-            sh.weight[c] = __ldcg(p.weights + c);
-        }
         if (e >= 0) {
             const uint32_t was = atomicAdd(reinterpret_cast<uint32_t *>(sh.rows) + (e >> 2), 1u << (8 * (e & 3)));
             mine[i] = (static_cast<uint32_t>(e + 1) << 8) | ((was >> (8 * (e & 3))) & 0xFF);
         }
     }
     __syncthreads();
-    uint16_t *start_of = reinterpret_cast<uint16_t *>(&sh.epi[0][0]);      // [E], before the epilogue needs it
     if (warp == 0) {
-        int n = 0, before = 0;
+        int entries = 0, choices = 0;
         for (int e0 = 0; e0 < p.E; e0 += 32) {
-            const int r = e0 + lane < p.E ? sh.rows[e0 + lane] : 0;
-            int sum = r;
+            const int r = e0 + lane < p.E ? sh.rows[e0 + lane] : 0, n = (r + kRoom - 1) / kRoom;
+            int sums = (n << 16) | r;        // entries and choices up to this expert
+            const int own = sums;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, sum, o);
-                if (lane >= o) sum += x;
+                const int x = __shfl_up_sync(0xffffffffu, sums, o);
+                if (lane >= o) sums += x;
             }
-            const unsigned m = __ballot_sync(0xffffffffu, r > 0);
-            if (r > 0) {
-                const int at = n + __popc(m & ((1u << lane) - 1));
-                sh.expert[at] = static_cast<uint16_t>(e0 + lane);
-                sh.first[at] = start_of[e0 + lane] = static_cast<uint16_t>(before + sum - r);
+            const int all = __shfl_sync(0xffffffffu, sums, 31), before = sums - own;
+            const int at = entries + (before >> 16), c0 = choices + (before & 0xFFFF);
+            if (r > 0) sh.start[e0 + lane] = static_cast<uint16_t>(c0);
+            for (int i = 0; i < n; ++i) {
+                sh.entry_expert[at + i] = static_cast<uint16_t>(e0 + lane);
+                sh.entry_slots[at + i] = static_cast<uint16_t>(c0 + kRoom * i);
+                sh.entry_rows[at + i] = static_cast<uint8_t>(min(kRoom, r - kRoom * i));
             }
-            n += __popc(m);
-            before += __shfl_sync(0xffffffffu, sum, 31);
+            entries += all >> 16;
+            choices += all & 0xFFFF;
         }
-        if (lane == 0) sh.active = n;
+        if (lane == 0) sh.entries = entries;
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 2; ++i)
         if (mine[i]) {
-            const int at = start_of[(mine[i] >> 8) - 1] + (mine[i] & 0xFF), c = tid + i * kExpertThreads;
+            const int at = sh.start[(mine[i] >> 8) - 1] + (mine[i] & 0xFF), c = tid + i * kExpertThreads;
             sh.slot[at] = static_cast<uint16_t>(c);
             sh.token[at] = static_cast<uint8_t>(c / p.k);
         }
     __syncthreads();
-    const int active = sh.active;
-    const int tiles1 = p.I >> 6, tiles2 = p.H >> 7, n1 = active * tiles1, n2 = active * tiles2;
+    const int tiles1 = p.I >> 6, tiles2 = p.H >> 7, n1 = sh.entries * tiles1, n2 = sh.entries * tiles2;
 
     if (warp == 8) {
         if (lane == 0) {
@@ -681,36 +676,45 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
             Place at{0, 0};
             int issued = 0;
             bool ok = true;
+            // Unit u: product 1 first, entry by entry in both products, so that the first experts'
+            // activations are there when product 2 begins.
+            auto unit_at = [&](int u) {
+                Unit w;
+                w.first = u < n1 + n2 ? u < n1 : -1;
+                if (w.first < 0) return w;
+                const int i = w.first ? u : u - n1, tiles = w.first ? tiles1 : tiles2;
+                w.entry = i / tiles;
+                w.c = i - w.entry * tiles;
+                w.e = sh.entry_expert[w.entry];
+                w.slots = sh.entry_slots[w.entry];
+                w.rows = sh.entry_rows[w.entry];
+                return w;
+            };
             // the weight scales of a unit go to L2 ahead of their copies
-            auto ask_scales = [&](int u) {
-                if (u >= n1 + n2) return;
-                const Unit w = unit_at(u, n1, tiles1, tiles2);
-                const int e = sh.expert[w.a];
+            auto ask_scales = [&](const Unit &w) {
+                if (w.first < 0) return;
                 if (w.first) {
                     const uint32_t run = (p.H >> 7) * 512;
-                    const size_t blk = static_cast<size_t>(2 * p.I >> 7) * e + (w.c >> 1);
+                    const size_t blk = static_cast<size_t>(2 * p.I >> 7) * w.e + (w.c >> 1);
                     prefetch_l2_bulk(p.w13_sf + blk * run, run);
                     prefetch_l2_bulk(p.w13_sf + (blk + (p.I >> 7)) * run, run);
                 } else {
                     const uint32_t run = (p.I >> 7) * 512;
-                    prefetch_l2_bulk(p.w2_sf + (static_cast<size_t>(p.H >> 7) * e + w.c) * run, run);
+                    prefetch_l2_bulk(p.w2_sf + (static_cast<size_t>(p.H >> 7) * w.e + w.c) * run, run);
                 }
             };
-            int u = atomicAdd(p.queue, 1);
-            ask_scales(u);
+            Unit w = unit_at(claimed);
+            ask_scales(w);
             for (int i = 0;; ++i) {
-                const bool more = u < n1 + n2;
                 if (!(ok = mbar_wait(&sh.unit_empty[i & 3], ((i >> 2) & 1) ^ 1u, &g_moe_few_error, kErrWaitEmpty, p.wait_ns)))
                     break;
-                sh.unit[i & 3] = more ? u : -1;
+                sh.unit[i & 3] = w;
                 mbar_arrive(&sh.unit_full[i & 3]);
-                if (!more) break;
+                if (w.first < 0) break;
                 const int next = atomicAdd(p.queue, 1);    // on its way while this unit loads
-                const Unit w = unit_at(u, n1, tiles1, tiles2);
-                const int e = sh.expert[w.a];
                 const int stages = ((w.first ? p.H : p.I) + 255) >> 8;
                 // 64 rows of G and the same of U, or 128 rows
-                const int r0 = w.first ? e * 2 * p.I + 64 * w.c : e * p.H + 128 * w.c;
+                const int r0 = w.first ? w.e * 2 * p.I + 64 * w.c : w.e * p.H + 128 * w.c;
                 const int r1 = r0 + (w.first ? p.I : 64);
                 const CUtensorMap *tm = w.first ? &p.tm_w13 : &p.tm_w2;
                 for (int ks = 0; ks < stages; ++ks) {
@@ -721,10 +725,10 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
                     tma_load_2d(st + 8192, tm, ks * 128, r1, &sh.w_full[at.slot], pol);
                     ++issued;
                     at.step(S);
-                    if (ks == 0) ask_scales(next);
                 }
                 if (!ok) break;
-                u = next;
+                w = unit_at(next);
+                ask_scales(w);
             }
             if (!ok) *reinterpret_cast<volatile int *>(&sh.abort) = 1;
             // copies in flight land before the block leaves
@@ -741,17 +745,15 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
         for (int i = 0; ok; ++i) {
             ok = mbar_wait_warp(&sh.unit_full[i & 3], (i >> 2) & 1, &g_moe_few_error, kErrWaitFull, p.wait_ns);
             if (!ok) break;
-            const int u = *reinterpret_cast<volatile int *>(&sh.unit[i & 3]);
+            const Unit w = sh.unit[i & 3];
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.unit_empty[i & 3]);
-            if (u < 0) break;
-            const Unit w = unit_at(u, n1, tiles1, tiles2);
+            if (w.first < 0) break;
             const int kc = (w.first ? p.H : p.I) >> 7, stages = (kc + 1) >> 1, buf = i & 1;
-            const int rows = sh.rows[sh.expert[w.a]];
             ok = mbar_wait_warp(&sh.acc_empty[buf], ((i >> 1) & 1) ^ 1u, &g_moe_few_error, kErrWaitAccum, p.wait_ns);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t idesc = __shfl_sync(0xffffffffu, idesc_block_scaled((8 * rows + 15) & ~15, true), 0);
+            const uint32_t idesc = __shfl_sync(0xffffffffu, idesc_block_scaled((8 * w.rows + 15) & ~15, true), 0);
             const uint32_t d = tmem + buf * kAccColumns;
             for (int ks = 0; ks < stages; ++ks) {
                 ok = mbar_wait_warp(&sh.w_full[at.slot], at.parity, &g_moe_few_error, kErrWaitFull, p.wait_ns) &&
@@ -789,32 +791,57 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
         if (elect_one()) tc_commit(&sh.mma_done);
         __syncwarp();
         mbar_wait_warp(&sh.mma_done, 0, &g_moe_few_error, kErrWaitDrain);
-    } else if (warp >= 4 && warp < 8) {
+    } else if (warp >= 4) {
         // -------------------------------------------------- tokens and scales
         const int t = tid - 128;
         Place at{0, 0};
         int count = 0;
-        int ready = -1;                  // active experts up to this one have all their activations
+        int ready = -1;                  // entries up to this one have all their activations
         bool ok = true;
         for (int i = 0; ok; ++i) {
             ok = mbar_wait_warp(&sh.unit_full[i & 3], (i >> 2) & 1, &g_moe_few_error, kErrWaitFull, p.wait_ns);
             if (!ok) break;
-            const int u = *reinterpret_cast<volatile int *>(&sh.unit[i & 3]);
+            const Unit w = sh.unit[i & 3];
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.unit_empty[i & 3]);
-            if (u < 0) break;
-            const Unit w = unit_at(u, n1, tiles1, tiles2);
-            const int e = sh.expert[w.a], rows = sh.rows[e];
-            const int first = sh.first[w.a];
-            // row of an expert's choice among the tokens or the activations
-            auto row_of = [&](int r) { return static_cast<size_t>(w.first ? sh.token[first + r] : sh.slot[first + r]); };
+            if (w.first < 0) break;
+            // row of a choice among the tokens or the activations
+            auto row_of = [&](int r) { return static_cast<size_t>(w.first ? sh.token[w.slots + r] : sh.slot[w.slots + r]); };
             const int K = w.first ? p.H : p.I, kc = K >> 7, stages = (kc + 1) >> 1;
-            if (!w.first && w.a > ready) {
-                // this expert's activations have to be there
+            // a row of digits is K / 2 bytes, six of them a token; pieces of 16 bytes, column c of row n at c ^ (n % 8)
+            const uint8_t *digits = w.first ? p.xd : p.ad;
+            const uint32_t *scales = w.first ? p.xsf : p.asf;
+            const uint8_t *src[2] = {nullptr, nullptr};
+            uint32_t dst[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int piece = t + 128 * j, r = piece / 48, dc = piece - 48 * r, c = dc & 7, dg = dc >> 3;
+                dst[j] = kStageWeights + 2 * kStageScales + (8 * r + dg) * 128 + ((c ^ dg) << 4);
+                if (r < w.rows) src[j] = digits + (row_of(r) * 6 + dg) * (K >> 1) + 16 * c;
+            }
+            const bool tail_col = (t & 7) < 4;               // columns of a stage's first half (piece 128 j + t: column t % 8)
+            // scale words: thread t < 64 that of half t % 2, digit t / 2 % 8, token t / 16
+            const int sr = t >> 4, sdg = (t >> 1) & 7, sh2 = t & 1;
+            const uint32_t sdst = kStageWeights + kStageScales + sh2 * 512 + (8 * sr + sdg) * 16;
+            const uint32_t *ssrc = sr < w.rows && sdg < 6 ? scales + (row_of(sr) * kc + sh2) * 8 + sdg : nullptr;
+            // scales of the weights: of product 1 from the halves of the 128-row blocks of G and of U
+            // that hold its 64 channels (8 of each 16 bytes)
+            const uint8_t *wsf = nullptr;
+            uint32_t wdst = kStageWeights;
+            if (w.first && t >= 64) {
+                const size_t blk = static_cast<size_t>(2 * p.I >> 7) * w.e + (w.c >> 1) + (t >= 96 ? p.I >> 7 : 0);
+                wsf = p.w13_sf + blk * kc * 512 + lane * 16 + (w.c & 1) * 8;
+                wdst += lane * 16 + (t >= 96 ? 8 : 0);
+            } else if (!w.first && t >= 64 && t < 96) {
+                wsf = p.w2_sf + (static_cast<size_t>(p.H >> 7) * w.e + w.c) * kc * 512 + lane * 16;
+                wdst += lane * 16;
+            }
+            if (!w.first && w.entry > ready) {
+                // this entry's activations have to be there
                 int v = 1;
                 if (lane == 0) {
                     const uint64_t t0 = global_timer_ns();
-                    while (load_acquire(p.made + w.a) < tiles1) {
+                    while (load_acquire(p.made + w.entry) < 4 * tiles1) {
                         if (global_timer_ns() - t0 > p.wait_ns) {
                             atomicCAS(&g_moe_few_error, 0, kErrWaitOperand);
                             v = 0;
@@ -825,47 +852,7 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
                 ok = __shfl_sync(0xffffffffu, v, 0) != 0;
                 __syncwarp();
                 if (!ok) break;
-                ready = w.a;
-            }
-            // a row of digits is K / 2 bytes, six of them a token; pieces of 16 bytes, column c of row n at c ^ (n % 8)
-            const uint8_t *digits = w.first ? p.xd : p.ad;
-            const uint32_t *scales = w.first ? p.xsf : p.asf;
-            const uint8_t *src[6];
-            uint32_t dst[6];
-#pragma unroll
-            for (int j = 0; j < 6; ++j) {
-                const int piece = t + 128 * j, r = piece / 48, dc = piece - 48 * r, c = dc & 7, dg = dc >> 3;
-                src[j] = nullptr;
-                dst[j] = 0;
-                if (r < rows) {
-                    src[j] = digits + (row_of(r) * 6 + dg) * (K >> 1) + 16 * c;
-                    dst[j] = kStageWeights + 2 * kStageScales + (8 * r + dg) * 128 + ((c ^ dg) << 4);
-                }
-            }
-            const bool tail_col = (t & 7) < 4;               // columns of a stage's first half (piece 128 j + t: column t % 8)
-            const uint32_t *ssrc[2];
-            uint32_t sdst[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int piece = t + 128 * j, r = piece >> 4, h = piece & 1, dg = (piece >> 1) & 7, n = 8 * r + dg;
-                ssrc[j] = nullptr;
-                sdst[j] = kStageWeights + kStageScales + h * 512 + (n & 31) * 16 + (n >> 5) * 4;
-                if (r < rows && dg < 6) {
-                    ssrc[j] = scales + (row_of(r) * kc + h) * 8 + dg;
-                }
-            }
-            const bool second = (t & 1) != 0;                // scale words of a stage's second half
-            // scales of the weights: of product 1 from the halves of the 128-row blocks of G and of U
-            // that hold its 64 channels (8 of each 16 bytes)
-            const uint8_t *wsf = nullptr;
-            uint32_t wdst = kStageWeights;
-            if (w.first && t < 64) {
-                const size_t blk = static_cast<size_t>(2 * p.I >> 7) * e + (w.c >> 1) + (t >= 32 ? p.I >> 7 : 0);
-                wsf = p.w13_sf + blk * kc * 512 + lane * 16 + (w.c & 1) * 8;
-                wdst += lane * 16 + (t >= 32 ? 8 : 0);
-            } else if (!w.first && t < 32) {
-                wsf = p.w2_sf + (static_cast<size_t>(p.H >> 7) * e + w.c) * kc * 512 + lane * 16;
-                wdst += lane * 16;
+                ready = w.entry;
             }
             for (int ks = 0; ks < stages; ++ks) {
                 ok = mbar_wait_warp(&sh.empty[at.slot], at.parity ^ 1u, &g_moe_few_error, kErrWaitEmpty, p.wait_ns);
@@ -873,11 +860,9 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
                 const uint32_t st = smem_u32(smem) + at.slot * stage_bytes;
                 const bool whole = 2 * ks + 1 < kc;
 #pragma unroll
-                for (int j = 0; j < 6; ++j)
-                    if (src[j] && (whole || tail_col)) cp_async<16>(st + dst[j], src[j] + ks * 128);
-#pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    if (ssrc[j] && (whole || !second)) cp_async<4>(st + sdst[j], ssrc[j] + ks * 16);
+                    if (src[j] && (whole || tail_col)) cp_async<16>(st + dst[j], src[j] + ks * 128);
+                if (ssrc && (whole || !sh2)) cp_async<4>(st + sdst, ssrc + ks * 16);
                 if (wsf) {
                     if (w.first) {
                         cp_async<8>(st + wdst, wsf + ks * 1024);
@@ -900,146 +885,77 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
             if (i >= count - S) ok = mbar_wait_warp(&sh.empty[back.slot], back.parity, &g_moe_few_error, kErrWaitDrain);
             back.step(S);
         }
-    } else if (warp >= 10) {
-        // ------------------------------- results are published, and summed by the last
-        // Off the epilogue's path: a fence for the whole GPU and an atomic take it over a
-        // microsecond.
-        for (int i = 0;; ++i) {
-            bool ok = mbar_wait_warp(&sh.unit_full[i & 3], (i >> 2) & 1, &g_moe_few_error, kErrWaitFull, p.wait_ns);
-            const int u = ok ? *reinterpret_cast<volatile int *>(&sh.unit[i & 3]) : -1;
-            __syncwarp();
-            if (ok && lane == 0) mbar_arrive(&sh.unit_empty[i & 3]);
-            if (u >= 0)
-                ok = mbar_wait_warp(&sh.fin_full[i & 3], (i >> 2) & 1, &g_moe_few_error, kErrWaitAccum, p.wait_ns);
-            if (!ok) *reinterpret_cast<volatile int *>(&sh.abort) = 1;
-            if (!ok || u < 0) break;
-            const Unit w = unit_at(u, n1, tiles1, tiles2);
-            if (lane == 0) {
-                // a quarter of the unit's channels each: the warps need not meet
-                __threadfence();
-                if (w.first) {
-                    if (warp == 10) atomicAdd(p.made + w.a, 1);
-                } else {
-                    sh.last[warp - 10] = atomicAdd(p.arrived + 4 * w.c + warp - 10, 1) == active - 1;
-                    __threadfence();
-                }
-                mbar_arrive(&sh.fin_empty[i & 3]);
-            }
-            __syncwarp();
-            if (!w.first && sh.last[warp - 10]) {
-                // all experts' rows of these channels are there: the weighted sum, in the order of a token's choices
-                const int ch = 128 * w.c + tid - 320;
-                for (int t0 = 0; t0 < p.T; t0 += 4) {
-                    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    for (int j0 = 0; j0 < p.k; j0 += 8) {
-                        // 32 loads on their way
-                        float y[4][8];
-#pragma unroll
-                        for (int t = 0; t < 4; ++t)
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const int c = (t0 + t) * p.k + j0 + j;
-                                const bool has = t0 + t < p.T && j0 + j < p.k && sh.kept[c];
-                                y[t][j] = has ? __ldcg(p.y + static_cast<size_t>(c) * p.H + ch) : 0.0f;
-                            }
-#pragma unroll
-                        for (int t = 0; t < 4; ++t)
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const int c = (t0 + t) * p.k + j0 + j;
-                                if (t0 + t < p.T && j0 + j < p.k && sh.kept[c]) s[t] = fmaf(sh.weight[c], y[t][j], s[t]);
-                            }
-                    }
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        if (t0 + t < p.T) p.out[(t0 + t) * p.ldo + ch] = __bfloat16_as_ushort(__float2bfloat16_rn(s[t]));
-                }
-            }
-            __syncwarp();
-        }
     } else {
         // ------------------------------------------------------------ epilogue
         for (int i = 0;; ++i) {
             const int buf = i & 1;
+            // one thread waits for all, so that all four warps leave after the same unit
             if (tid == 0) {
                 bool ok = mbar_wait(&sh.unit_full[i & 3], (i >> 2) & 1, &g_moe_few_error, kErrWaitFull, p.wait_ns);
-                int u = -1;
-                if (ok) {
-                    u = *reinterpret_cast<volatile int *>(&sh.unit[i & 3]);
-                    mbar_arrive(&sh.unit_empty[i & 3]);
-                    if (u >= 0) ok = mbar_wait(&sh.acc_full[buf], (i >> 1) & 1, &g_moe_few_error, kErrWaitAccum, p.wait_ns);
-                }
+                const bool more = ok && sh.unit[i & 3].first >= 0;
+                if (more) ok = mbar_wait(&sh.acc_full[buf], (i >> 1) & 1, &g_moe_few_error, kErrWaitAccum, p.wait_ns);
                 if (!ok) *reinterpret_cast<volatile int *>(&sh.abort) = 1;
-                // and the finishing warps are done with the unit four before
-                if (ok && u >= 0)
-                    ok = mbar_wait(&sh.fin_empty[i & 3], ((i >> 2) & 1) ^ 1u, &g_moe_few_error, kErrWaitEmpty, p.wait_ns);
-                sh.go[buf] = ok && !*reinterpret_cast<volatile int *>(&sh.abort) ? u : -1;
+                sh.go[buf] = more && ok && !*reinterpret_cast<volatile int *>(&sh.abort);
             }
             epilogue_sync();
-            const int u = sh.go[buf];
-            if (u < 0) break;
+            if (!sh.go[buf]) break;
             tc_fence_after();
-            const Unit w = unit_at(u, n1, tiles1, tiles2);
-            const int rows = sh.rows[sh.expert[w.a]];
-            const uint16_t *slots = sh.slot + sh.first[w.a];
-            const uint32_t trow = tmem + buf * kAccColumns + (static_cast<uint32_t>(warp * 32) << 16);
-            for (int r0 = 0; r0 < rows; r0 += 4) {
-                uint32_t v[32];
-                tmem_ld32(trow + 8 * r0, v);
-                tmem_ld_wait();
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    // the digits' sums, smallest first
-                    float s = __uint_as_float(v[8 * r]);
-#pragma unroll
-                    for (int d = 1; d < 6; ++d) s += __uint_as_float(v[8 * r + d]);
-                    if (r0 + r < rows) {
-                        if (w.first)
-                            sh.epi[r0 + r][tid] = s;
-                        else
-                            p.y[static_cast<size_t>(slots[r0 + r]) * p.H + 128 * w.c + tid] = s;
-                    }
-                }
-            }
+            const Unit w = sh.unit[i & 3];
+            uint32_t v[32];
+            tmem_ld32(tmem + buf * kAccColumns + (static_cast<uint32_t>(warp * 32) << 16), v);
+            tmem_ld_wait();
             tc_fence_before();
             mbar_arrive(&sh.acc_empty[buf]);
-            if (w.first) {
-                epilogue_sync();
-                // a thread has 8 channels of a token; four neighbours share a block of 32
-                const int r = tid >> 3, part = tid & 7;
-                if ((r & ~3) < rows) {
-                    float a[8];
-                    uint32_t amax = 0;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        // silu as in moe_experts.cu: off by up to (5 + 1.2 |g|) 2^-23 of itself, 0 below -87.3
-                        const float g = sh.epi[r][8 * part + j];
-                        a[j] = __fdividef(g, 1.0f + __expf(-g)) * sh.epi[r][64 + 8 * part + j];
-                        amax = max(amax, __float_as_uint(a[j]) & 0x7FFFFFFFu);
-                    }
-                    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                    const uint32_t b = mxfp8_scale_byte(amax);
-                    const uint32_t b2 = __shfl_down_sync(0xffffffffu, b, 4);
-                    if (r < rows) {
-                        uint32_t dg[6];
-                        digits_of(sh.digits, a, b, dg);
-                        uint8_t *o = p.ad + static_cast<size_t>(slots[r]) * 6 * (p.I >> 1) + 32 * w.c + 4 * part;
+            for (int r = 0; r < kRoom; ++r) {
+                if (r >= w.rows) break;
+                // the digits' sums, smallest first
+                float s = __uint_as_float(v[8 * r]);
 #pragma unroll
-                        for (int d = 0; d < 6; ++d) *reinterpret_cast<uint32_t *>(o + static_cast<size_t>(d) * (p.I >> 1)) = dg[d];
-                        if (part == 0) {
-                            uint8_t *f = reinterpret_cast<uint8_t *>(p.asf + (static_cast<size_t>(slots[r]) * (p.I >> 7) + (w.c >> 1)) * 8) +
-                                         2 * (w.c & 1);
-#pragma unroll
-                            for (int d = 0; d < 6; ++d)
-                                *reinterpret_cast<uint16_t *>(f + 4 * d) =
-                                    static_cast<uint16_t>(digit_scale(b, d) | (digit_scale(b2, d) << 8));
-                        }
-                    }
-                }
-                epilogue_sync();     // the staging buffer is reused
+                for (int d = 1; d < 6; ++d) s += __uint_as_float(v[8 * r + d]);
+                if (w.first)
+                    sh.epi[r][tid] = s;
+                else
+                    p.y[static_cast<size_t>(sh.slot[w.slots + r]) * p.H + 128 * w.c + tid] = s;
             }
-            mbar_arrive(&sh.fin_full[i & 3]);
+            epilogue_sync();
+            if (tid == 0) mbar_arrive(&sh.unit_empty[i & 3]);
+            if (!w.first) continue;
+            // a warp has a token, a lane two of its 64 channels; half a warp is a block of 32
+            const int r = warp;
+            if (r < w.rows) {
+                float a[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    // silu as in moe_experts.cu: off by up to (5 + 1.2 |g|) 2^-23 of itself, 0 below -87.3
+                    const float g = sh.epi[r][2 * lane + j];
+                    a[j] = __fdividef(g, 1.0f + __expf(-g)) * sh.epi[r][64 + 2 * lane + j];
+                }
+                uint32_t amax = max(__float_as_uint(a[0]) & 0x7FFFFFFFu, __float_as_uint(a[1]) & 0x7FFFFFFFu);
+#pragma unroll
+                for (int o = 1; o < 16; o <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                const uint32_t b = mxfp8_scale_byte(amax), b2 = __shfl_down_sync(0xffffffffu, b, 16);
+                const float inv = mxfp8_scale_inverse(b);
+                const uint32_t codes = e4m3x4_rn(a[0] * inv, a[1] * inv, 0.0f, 0.0f);
+                const uint32_t d0 = digits_of(sh.digits, codes & 0xFFu, b), d1 = digits_of(sh.digits, (codes >> 8) & 0xFFu, b);
+                const size_t row = sh.slot[w.slots + r];
+                uint8_t *o = p.ad + row * 6 * (p.I >> 1) + 32 * w.c + lane;
+#pragma unroll
+                for (int d = 0; d < 6; ++d)
+                    o[static_cast<size_t>(d) * (p.I >> 1)] =
+                        static_cast<uint8_t>(((d0 >> (4 * d)) & 0xFu) | (((d1 >> (4 * d)) & 0xFu) << 4));
+                if (lane < 6) {
+                    uint8_t *f = reinterpret_cast<uint8_t *>(p.asf + (row * (p.I >> 7) + (w.c >> 1)) * 8) + 2 * (w.c & 1);
+                    // b is the first block's for these lanes, b2 the second's
+                    *reinterpret_cast<uint16_t *>(f + 4 * lane) =
+                        static_cast<uint16_t>(digit_scale(b, lane) | (digit_scale(b2, lane) << 8));
+                }
+            }
+            __syncwarp();
+            if (lane == 0) {
+                __threadfence();
+                atomicAdd(p.made + w.entry, 1);
+            }
         }
     }
     __syncwarp();
@@ -1052,7 +968,57 @@ __global__ void __launch_bounds__(kExpertThreads, 1) moe_few_experts_kernel(cons
     }
 }
 
-constexpr uint32_t kExpertsSmem = 232448;
+// --------------------------------------------------------------------- sum
+
+struct SumParams {
+    const float *y;                     // [T * k, H]
+    const int *ids;
+    const float *weights;
+    uint16_t *out;
+    int64_t ldo;
+    int T, k, H;
+};
+
+// out_t = sum_j w_tj y[t, j], in the order of j. Grid: blocks of 512 channels x tokens, four
+// channels a thread.
+__global__ void __launch_bounds__(128) moe_few_sum_kernel(const SumParams p)
+{
+    __shared__ float weight[32];
+    __shared__ int id[32];
+    const int t = blockIdx.y, ch = (blockIdx.x * 128 + threadIdx.x) * 4;
+    // what the launches before the last one wrote is there already
+    if (threadIdx.x < p.k) {
+        id[threadIdx.x] = __ldcg(p.ids + t * p.k + threadIdx.x);
+        weight[threadIdx.x] = __ldcg(p.weights + t * p.k + threadIdx.x);
+    }
+    __syncthreads();
+    grid_dependency_wait();
+    grid_launch_dependents();
+    if (ch >= p.H) return;
+    const float *y = p.y + static_cast<size_t>(t) * p.k * p.H + ch;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int j0 = 0; j0 < p.k; j0 += 8) {
+        float4 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = j0 + j < p.k && id[j0 + j] >= 0 ? __ldcg(reinterpret_cast<const float4 *>(y + static_cast<size_t>(j0 + j) * p.H))
+                                                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (j0 + j >= p.k || id[j0 + j] < 0) continue;
+            const float w = weight[j0 + j];
+            s.x = fmaf(w, v[j].x, s.x);
+            s.y = fmaf(w, v[j].y, s.y);
+            s.z = fmaf(w, v[j].z, s.z);
+            s.w = fmaf(w, v[j].w, s.w);
+        }
+    }
+    const __nv_bfloat162 a = __floats2bfloat162_rn(s.x, s.y), b = __floats2bfloat162_rn(s.z, s.w);
+    *reinterpret_cast<uint2 *>(p.out + t * p.ldo + ch) =
+        make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+}
+
+constexpr uint32_t kExpertsSmem = 115712;   // half of an SM's, less what a block takes beside
 
 template <typename Kern, typename P>
 cudaError_t launch_pdl(Kern kern, dim3 grid, unsigned block, size_t smem, cudaStream_t stream, const P &params)
@@ -1082,7 +1048,7 @@ MoeFewLayout moe_few_layout(int64_t T, int k, int E, int64_t H, int64_t I)
         return was;
     };
     const size_t slices = H / kSlice, R = static_cast<size_t>(T) * k;
-    l.counters = take(sizeof(int) * (kArrivedAt + H / 32));
+    l.counters = take(sizeof(int) * (kMadeAt + kMaxEntries));
     l.h = take(2 * T * H);
     l.part = take(4 * slices * T * E);
     l.part_ss = take(4 * slices * T);
@@ -1115,7 +1081,7 @@ cudaError_t launch_moe_few(const MoeFewArgs &a, const MoeFewLayout &l, cudaStrea
     r.part = reinterpret_cast<float *>(a.ws + l.part);
     r.part_ss = reinterpret_cast<float *>(a.ws + l.part_ss);
     r.counters = reinterpret_cast<int *>(a.ws + l.counters);
-    r.num_counters = kArrivedAt + a.H / 32;
+    r.num_counters = kMadeAt + kMaxEntries;
     r.T = a.T;
     r.H = a.H;
     r.E = a.route.E;
@@ -1162,30 +1128,39 @@ cudaError_t launch_moe_few(const MoeFewArgs &a, const MoeFewLayout &l, cudaStrea
     p.xd = t.xd;
     p.xsf = t.xsf;
     p.ids = t.ids;
-    p.weights = t.weights;
     p.ad = a.ws + l.ad;
     p.asf = reinterpret_cast<uint32_t *>(a.ws + l.asf);
     p.y = reinterpret_cast<float *>(a.ws + l.y);
-    p.out = a.out;
-    p.ldo = a.ldo;
     p.queue = r.counters;
     p.made = r.counters + kMadeAt;
-    p.arrived = r.counters + kArrivedAt;
     p.T = a.T;
     p.k = a.route.k;
     p.E = a.route.E;
     p.H = a.H;
     p.I = a.I;
     p.wait_ns = wait_limit_ns();
-    // a stage has room for every token, and for the 16 columns of the smallest MMA
-    p.room = (a.T + 1) & ~1;
+    // a stage has room for the tokens of a unit, and for the 16 columns of the smallest MMA
+    p.room = p.T <= 2 ? 2 : kRoom;
     const uint32_t stage = kStageWeights + 2 * kStageScales + p.room * kTokenBytes;
     p.stages = std::min<int>(kMaxStages, (kExpertsSmem - 1024 - sizeof(ExpertsShared)) / stage);
     // no more blocks than there can be units
-    const int64_t experts = std::min<int64_t>(p.E, int64_t(p.T) * p.k);
-    const int64_t units = experts * (p.I / 64 + p.H / 128);
-    return launch_pdl(moe_few_experts_kernel, static_cast<unsigned>(std::min<int64_t>(sms, units)), kExpertThreads,
-                      kExpertsSmem, stream, p);
+    const int64_t entries = std::min<int64_t>(p.E + p.T * p.k / kRoom, int64_t(p.T) * p.k);
+    const int64_t units = entries * (p.I / 64 + p.H / 128);
+    e = launch_pdl(moe_few_experts_kernel, static_cast<unsigned>(std::min<int64_t>(2 * sms, units)), kExpertThreads,
+                   kExpertsSmem, stream, p);
+    if (e != cudaSuccess) return e;
+
+    SumParams c;
+    memset(&c, 0, sizeof(c));
+    c.y = p.y;
+    c.ids = t.ids;
+    c.weights = t.weights;
+    c.out = a.out;
+    c.ldo = a.ldo;
+    c.T = a.T;
+    c.k = a.route.k;
+    c.H = a.H;
+    return launch_pdl(moe_few_sum_kernel, dim3((a.H + 511) / 512, a.T), 128, 0, stream, c);
 }
 
 int read_and_clear_moe_few_error()

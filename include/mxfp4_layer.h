@@ -81,7 +81,7 @@ MXFP4_API mxfp4_status_t qk_norm_rope(const void *q, int64_t q_st, int64_t q_sh,
 MXFP4_API size_t mxfp4_moe_layer_workspace_bytes(int64_t T, int k, int E, int64_t H, int64_t I);
 
 /* The feed-forward half of a mixture-of-experts layer for up to MOE_LAYER_MAX_TOKENS
- * tokens, in three launches (for more tokens: mxfp8_add_rmsnorm_quantize, the router's
+ * tokens, in four launches (for more tokens: mxfp8_add_rmsnorm_quantize, the router's
  * product, moe_route and mxfp4_moe_experts):
  *   h       = X + residual, in fp32, rounded to bf16 (residual NULL: h = X)
  *   y       = h / sqrt(mean(h^2) + eps) * weight, in fp32 (0 where mean + eps is 0)
