@@ -30,6 +30,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstddef>
 #include <cstring>
 
@@ -252,8 +253,7 @@ struct TokenParams {
     int *ids_out;                       // the caller's, or null
     float *weights_out;
     int T, H, E, k, slices, groups, topk_groups, group_top, sigmoid, renorm;
-    float eps, scale;
-    double inv_h;
+    float heps, root_h, scale;          // H eps, sqrt(H)
 };
 
 // A key that orders as the values do, NaN above all; 0 stands for "none".
@@ -263,41 +263,33 @@ __device__ __forceinline__ uint32_t order_key(float v)
     if (isnan(v)) return 0xFFFFFFFFu;
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
-constexpr uint32_t kKeyNone = 0x007FFFFFu;      // of -infinity: nothing below it is chosen
+constexpr uint32_t kKeyNone = 0x007FFFFFu;      // of -infinity: neither it nor what lies below is chosen
 
-// Position of the largest of `n` <= 512 keys, the first of equals; all lanes of one warp,
-// lane l holding keys l, l + 32, ...; takes it out (0). -1 if none is above `floor`.
-__device__ __forceinline__ int take_best(uint32_t (&key)[kMaxExperts / 32], int n, uint32_t floor)
+__device__ __forceinline__ float key_value(uint32_t key)
 {
-    const int lane = threadIdx.x & 31;
-    uint32_t best = 0;
-    int at = 0;
-#pragma unroll
-    for (int i = 0; i < kMaxExperts / 32; ++i) {
-        if (32 * i >= n) break;
-        if (key[i] > best) {
-            best = key[i];
-            at = i;
-        }
-    }
-    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-    if (top <= floor) return -1;
-    const uint32_t mine = best == top ? static_cast<uint32_t>(32 * at + lane) : 0xFFFFFFFFu;
-    const uint32_t e = __reduce_min_sync(0xffffffffu, mine);
-#pragma unroll
-    for (int i = 0; i < kMaxExperts / 32; ++i)
-        if (static_cast<uint32_t>(32 * i + lane) == e) key[i] = 0;
-    return static_cast<int>(e);
+    return __uint_as_float(key == 0xFFFFFFFFu ? 0x7FC00000u : (key & 0x80000000u ? key & 0x7FFFFFFFu : ~key));
+}
+
+// An unevaluated sum of two floats, and what is added to it: by error-free additions of
+// the high parts, the low ones in fp32.
+struct Two {
+    float hi, lo;
+};
+__device__ __forceinline__ void add(Two &a, float hi, float lo)
+{
+    const float s = a.hi + hi, b = s - a.hi;
+    a.lo += ((a.hi - (s - b)) + (hi - b)) + lo;
+    a.hi = s;
 }
 
 // Grid: tokens x parts of their channels; the first part of a token routes it too.
 __global__ void __launch_bounds__(kTokenThreads) moe_few_token_kernel(const TokenParams p)
 {
-    __shared__ double sums[kTokenThreads];
-    __shared__ float choice[kMaxExperts], score[kMaxExperts], group_score[kMaxExperts];
-    __shared__ double r_shared;
-    __shared__ float red[kTokenThreads / 32];
-    __shared__ uint32_t group_kept[kMaxExperts / 32];
+    __shared__ float2 sums[kTokenThreads];
+    __shared__ float logit[kMaxExperts], chosen_score[32];
+    __shared__ uint32_t keys[kMaxExperts], group_key[kMaxExperts];
+    __shared__ int rank[kMaxExperts], chosen[32];
+    __shared__ float r_shared;
     __shared__ uint32_t table[128];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, t = blockIdx.x;
     const int v = blockIdx.y * kTokenThreads + tid;          // this thread's eight channels
@@ -311,28 +303,29 @@ __global__ void __launch_bounds__(kTokenThreads) moe_few_token_kernel(const Toke
 
     // r, by one warp
     if (warp == 0) {
-        double ss = 0.0;
+        Two ss{0.0f, 0.0f};
         for (int s0 = 0; s0 < p.slices; s0 += 128) {
             float f[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) f[i] = s0 + 32 * i + lane < p.slices ? p.part_ss[(s0 + 32 * i + lane) * p.T + t] : 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) ss += static_cast<double>(f[i]);
+            for (int i = 0; i < 4; ++i) add(ss, f[i], 0.0f);
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        for (int o = 16; o > 0; o >>= 1) add(ss, __shfl_xor_sync(0xffffffffu, ss.hi, o), __shfl_xor_sync(0xffffffffu, ss.lo, o));
         if (lane == 0) {
-            // a root of fp32 and one step of Newton's method in 64 bits: 2^-44, and a quarter of
-            // the time of a division and a root there
-            const double m = ss * p.inv_h + static_cast<double>(p.eps);
-            const double r0 = rsqrtf(static_cast<float>(m));
-            r_shared = m == 0.0 ? 0.0 : (isinf(m) ? 0.0 : r0 * (1.5 - 0.5 * m * r0 * r0));
+            // a root of fp32 and one step of Newton's method: m r^2 - 1 to 2^-40
+            add(ss, p.heps, 0.0f);
+            const float r0 = rsqrtf(ss.hi);
+            const float q = r0 * r0, qe = fmaf(r0, r0, -q);
+            const float e = fmaf(ss.hi, q, -1.0f) + (fmaf(ss.hi, qe, ss.lo * q));
+            r_shared = ss.hi == 0.0f || isinf(ss.hi) ? 0.0f : fmaf(r0 * p.root_h, -0.5f * e, r0 * p.root_h);
         }
     }
     // logits: `parts` threads an expert over interleaved slices, added in a fixed order
-    double z = 0.0;
     const int parts = kTokenThreads / p.E;           // E <= 512
     if (blockIdx.y == 0) {
+        Two z{0.0f, 0.0f};
         const int e = tid % p.E, part = tid / p.E;
         if (part < parts) {
             const float *src = p.part + static_cast<int64_t>(t) * p.E + e;
@@ -342,16 +335,15 @@ __global__ void __launch_bounds__(kTokenThreads) moe_few_token_kernel(const Toke
 #pragma unroll
                 for (int i = 0; i < 8; ++i) f[i] = s0 + i * parts < p.slices ? src[(s0 + i * parts) * step] : 0.0f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) z += static_cast<double>(f[i]);
+                for (int i = 0; i < 8; ++i) add(z, f[i], 0.0f);
             }
         }
-        sums[tid] = z;
+        sums[tid] = make_float2(z.hi, z.lo);
     }
     __syncthreads();
-    const double r = r_shared;
+    const float rf = r_shared;
     {
         // y in MXFP8, four lanes a block of 32
-        const float rf = static_cast<float>(r);
         // only now: H may be X or residual, which the launch before read
         if (in && p.h_out) *reinterpret_cast<uint4 *>(p.h_out + t * p.ldh + 8 * v) = hv;
         const uint32_t ha[4] = {hv.x, hv.y, hv.z, hv.w}, wa[4] = {wv.x, wv.y, wv.z, wv.w};
@@ -381,102 +373,101 @@ __global__ void __launch_bounds__(kTokenThreads) moe_few_token_kernel(const Toke
         }
     }
     if (blockIdx.y > 0) return;
-    float zf = -INFINITY;
     if (tid < p.E) {
-        for (int i = 1; i < parts; ++i) z += sums[i * p.E + tid];
-        zf = static_cast<float>(z * r);
+        Two z{sums[tid].x, sums[tid].y};
+        for (int i = 1; i < parts; ++i) add(z, sums[i * p.E + tid].x, sums[i * p.E + tid].y);
+        logit[tid] = (z.hi + z.lo) * rf;
     }
-    // scores
-    float s = 0.0f;
-    if (p.sigmoid) {
-        s = 1.0f / (1.0f + expf(-zf));
-    } else {
-        float m = zf;
-        bool nan = isnan(zf);
+    __syncthreads();
+    // scores: every warp finds the largest logit and the sum by itself
+    float largest = -INFINITY, sum = 0.0f;
+    if (!p.sigmoid) {
+        bool nan = false;
+        for (int e = lane; e < p.E; e += 32) {
+            largest = fmaxf(largest, logit[e]);
+            nan |= isnan(logit[e]);
+        }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (lane == 0) red[warp] = m;
-        nan = __syncthreads_or(nan);
-        m = red[0];
-#pragma unroll
-        for (int i = 1; i < kTokenThreads / 32; ++i) m = fmaxf(m, red[i]);
-        __syncthreads();
-        const float ex = tid < p.E && zf > -INFINITY ? expf(zf - m) : 0.0f;
-        float sum = ex;
+        for (int o = 16; o > 0; o >>= 1) largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, o));
+        for (int e = lane; e < p.E; e += 32) sum += logit[e] > -INFINITY ? expf(logit[e] - largest) : 0.0f;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0) red[warp] = sum;
-        __syncthreads();
-        sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kTokenThreads / 32; ++i) sum += red[i];
-        s = nan ? __int_as_float(0x7FC00000) : (sum > 0.0f ? ex / sum : 0.0f);
+        if (__any_sync(0xffffffffu, nan)) sum = __int_as_float(0x7FC00000);
     }
+    float s = 0.0f;
+    uint32_t key = 0;                        // of this thread's expert; 0 where there is none
     if (tid < p.E) {
-        score[tid] = s;
+        const float z = logit[tid];
+        if (p.sigmoid)
+            s = 1.0f / (1.0f + expf(-z));
+        else if (isnan(sum))
+            s = sum;
+        else
+            s = sum > 0.0f && z > -INFINITY ? expf(z - largest) / sum : 0.0f;
         // without a bias and groups the logits rank the experts as the scores do, also where those saturate
-        float c = p.bias || p.groups > 1 ? s + (p.bias ? p.bias[tid] : 0.0f) : (isnan(s) ? s : zf);
-        if (zf == -INFINITY) c = -INFINITY;
-        choice[tid] = c;
+        float c = p.bias || p.groups > 1 ? s + (p.bias ? p.bias[tid] : 0.0f) : (isnan(s) ? s : z);
+        if (z == -INFINITY) c = -INFINITY;
+        key = order_key(c);
+        keys[tid] = key;
+        rank[tid] = 0;
     }
     __syncthreads();
     const int n = p.E / p.groups;
     if (p.groups > 1) {
+        // a group's score: the sum of its best, or two best
         for (int g = warp; g < p.groups; g += kTokenThreads / 32) {
-            // the two best keys of the group
             uint32_t k1 = 0, k2 = 0;
             for (int i = lane; i < n; i += 32) {
-                const uint32_t key = order_key(choice[g * n + i]);
-                if (key > k1) {
+                const uint32_t k = keys[g * n + i];
+                if (k > k1) {
                     k2 = k1;
-                    k1 = key;
-                } else if (key > k2) {
-                    k2 = key;
+                    k1 = k;
+                } else if (k > k2) {
+                    k2 = k;
                 }
             }
             const uint32_t top = __reduce_max_sync(0xffffffffu, k1);
             const unsigned who = __ballot_sync(0xffffffffu, k1 == top);
             if (lane == __ffs(who) - 1) k1 = k2;
             const uint32_t second = __reduce_max_sync(0xffffffffu, k1);
-            auto value = [](uint32_t key) {
-                return __uint_as_float(key == 0xFFFFFFFFu ? 0x7FC00000u : (key & 0x80000000u ? key & 0x7FFFFFFFu : ~key));
-            };
-            if (lane == 0) group_score[g] = value(top) + (p.group_top == 2 && n > 1 ? value(second) : 0.0f);
+            if (lane == 0) group_key[g] = order_key(key_value(top) + (p.group_top == 2 && n > 1 ? key_value(second) : 0.0f));
+        }
+        __syncthreads();
+        if (tid < p.E) {
+            const int own = tid / n;
+            int before = 0;
+            for (int g = 0; g < p.groups; ++g) before += group_key[g] > group_key[own] || (group_key[g] == group_key[own] && g < own);
+            if (before >= p.topk_groups) keys[tid] = key = 0;
         }
         __syncthreads();
     }
+    // An expert's place is the number of those before it: larger keys, and equal ones with a
+    // lower index. `parts` threads count for one expert.
+    {
+        const int e = tid % p.E, part = tid / p.E;
+        if (part < parts) {
+            const uint32_t own = keys[e];
+            const int per = (p.E + parts - 1) / parts, end = min(p.E, (part + 1) * per);
+            int before = 0;
+            for (int i = part * per; i < end; ++i) before += keys[i] > own || (keys[i] == own && i < e);
+            if (before) atomicAdd(&rank[e], before);
+        }
+    }
+    if (tid < 32) chosen[tid] = -1;
+    __syncthreads();
+    if (tid < p.E && key > kKeyNone && rank[tid] < p.k) {
+        chosen[rank[tid]] = tid;
+        chosen_score[rank[tid]] = s;
+    }
+    __syncthreads();
     if (warp == 0) {
-        uint32_t key[kMaxExperts / 32];
-        if (p.groups > 1) {
-#pragma unroll
-            for (int i = 0; i < kMaxExperts / 32; ++i) {
-                key[i] = 32 * i + lane < p.groups ? order_key(group_score[32 * i + lane]) : 0;
-                if (lane == 0) group_kept[i] = 0;
-            }
-            __syncwarp();
-            for (int i = 0; i < p.topk_groups; ++i) {
-                const int g = take_best(key, p.groups, 0);
-                if (g >= 0 && lane == 0) group_kept[g >> 5] |= 1u << (g & 31);
-            }
-            __syncwarp();
-        }
-#pragma unroll
-        for (int i = 0; i < kMaxExperts / 32; ++i) {
-            const int x = 32 * i + lane;
-            key[i] = 0;
-            if (x < p.E && (p.groups == 1 || (group_kept[(x / n) >> 5] >> ((x / n) & 31) & 1))) key[i] = order_key(choice[x]);
-        }
-        int id = -1;
-        for (int i = 0; i < p.k; ++i) {
-            const int x = take_best(key, p.E, kKeyNone);
-            if (lane == i) id = x;
-        }
-        float w = id >= 0 ? score[id] : 0.0f;
+        const int id = lane < p.k ? chosen[lane] : -1;
+        float w = id >= 0 ? chosen_score[lane] : 0.0f;
         if (p.renorm) {
-            float sum = w;
+            float all = w;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            w = w / (sum + 1e-20f);
+            for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+            w = w / (all + 1e-20f);
         }
         w *= p.scale;
         if (lane < p.k) {
@@ -619,6 +610,7 @@ __global__ void __launch_bounds__(kExpertThreads, 2) moe_few_experts_kernel(cons
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
     grid_dependency_wait();
+    grid_launch_dependents();        // the sum's blocks have room beside this kernel's, and wait
     int claimed = 0;
     if (tid == 256) claimed = atomicAdd(p.queue, 1);     // on its way while the lists are made
     // Choices by expert. The order of an expert's choices does not matter: columns of an
@@ -732,11 +724,8 @@ __global__ void __launch_bounds__(kExpertThreads, 2) moe_few_experts_kernel(cons
             }
             if (!ok) *reinterpret_cast<volatile int *>(&sh.abort) = 1;
             // copies in flight land before the block leaves
-            Place back{0, 0};
-            for (int i = 0; i < issued; ++i) {
-                if (i >= issued - S) mbar_wait(&sh.w_full[back.slot], back.parity, &g_moe_few_error, kErrWaitDrain);
-                back.step(S);
-            }
+            for (int i = max(0, issued - S); i < issued; ++i)
+                mbar_wait(&sh.w_full[i % S], (i / S) & 1, &g_moe_few_error, kErrWaitDrain);
         }
     } else if (warp == 9) {
         // ------------------------------------------------ scales and products
@@ -880,11 +869,8 @@ __global__ void __launch_bounds__(kExpertThreads, 2) moe_few_experts_kernel(cons
         if (!ok) *reinterpret_cast<volatile int *>(&sh.abort) = 1;
         cp_async_wait_all();   // also after an abort: nothing of this thread is in flight when the block leaves
         // nor are the arrivals of the last MMAs, which nobody else waits for
-        Place back{0, 0};
-        for (int i = 0; i < count && ok; ++i) {
-            if (i >= count - S) ok = mbar_wait_warp(&sh.empty[back.slot], back.parity, &g_moe_few_error, kErrWaitDrain);
-            back.step(S);
-        }
+        for (int i = max(0, count - S); i < count && ok; ++i)
+            ok = mbar_wait_warp(&sh.empty[i % S], (i / S) & 1, &g_moe_few_error, kErrWaitDrain);
     } else {
         // ------------------------------------------------------------ epilogue
         for (int i = 0;; ++i) {
@@ -961,7 +947,6 @@ __global__ void __launch_bounds__(kExpertThreads, 2) moe_few_experts_kernel(cons
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    grid_launch_dependents();
     if (warp == 9) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemColumns);
@@ -1018,7 +1003,7 @@ __global__ void __launch_bounds__(128) moe_few_sum_kernel(const SumParams p)
         make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
 }
 
-constexpr uint32_t kExpertsSmem = 115712;   // half of an SM's, less what a block takes beside
+constexpr uint32_t kExpertsSmem = 113664;   // two blocks an SM, and room for some of the sum's
 
 template <typename Kern, typename P>
 cudaError_t launch_pdl(Kern kern, dim3 grid, unsigned block, size_t smem, cudaStream_t stream, const P &params)
@@ -1113,8 +1098,8 @@ cudaError_t launch_moe_few(const MoeFewArgs &a, const MoeFewLayout &l, cudaStrea
     t.group_top = a.route.group_top;
     t.sigmoid = a.route.sigmoid;
     t.renorm = a.route.renorm;
-    t.eps = a.eps;
-    t.inv_h = 1.0 / a.H;
+    t.heps = static_cast<float>(static_cast<double>(a.H) * a.eps);
+    t.root_h = static_cast<float>(std::sqrt(static_cast<double>(a.H)));
     t.scale = a.route.scale;
     e = launch_pdl(moe_few_token_kernel, dim3(a.T, (a.H / 8 + kTokenThreads - 1) / kTokenThreads), kTokenThreads, 0, stream, t);
     if (e != cudaSuccess) return e;
