@@ -77,8 +77,8 @@ struct MoeFewArgs {
     int T, H, I;
     float eps;
     uint8_t *ws;
-    CUtensorMap tm_w13;     // packed weights [E * 2I, H / 2] u8, box 128 bytes x 64 rows
-    CUtensorMap tm_w2;      // the same of [E * H, I / 2]
+    CUtensorMap tm_w13;     // packed weights [E * 2I, H / 2] u8, box 128 bytes x 32 rows
+    CUtensorMap tm_w2;      // the same of [E * H, I / 2], box 64 rows
 };
 cudaError_t launch_moe_few(const MoeFewArgs &a, const MoeFewLayout &l, cudaStream_t stream);
 int read_and_clear_moe_few_error();

@@ -223,7 +223,7 @@ mxfp4_status_t mxfp4_moe_layer(const void *X, int64_t ldx, const void *residual,
     a.I = static_cast<int>(I);
     a.eps = eps;
     a.ws = static_cast<uint8_t *>(workspace);
-    if (!encode_packed_map(W13q, Hd / 2, 2 * I * E, Hd / 2, 64, &a.tm_w13) ||
+    if (!encode_packed_map(W13q, Hd / 2, 2 * I * E, Hd / 2, 32, &a.tm_w13) ||
         !encode_packed_map(W2q, I / 2, Hd * E, I / 2, 64, &a.tm_w2))
         return MXFP4_ERR_CUDA;
     return cuda_status(launch_moe_few(a, l, static_cast<cudaStream_t>(stream)));

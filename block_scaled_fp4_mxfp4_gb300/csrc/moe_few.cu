@@ -19,8 +19,8 @@
 //
 //   sum      the weighted sum of a token's rows, in the order of its choices
 //
-// Units of work: 64 channels of an expert in product 1 (their rows of G and of U), 128 in
-// product 2, each for up to four of its tokens: more than four take another unit, whose
+// Units of work: 32 channels of an expert in product 1 (their rows of G and of U: a block of
+// the activations' MXFP8), 128 in product 2, each for up to four of its tokens: more than four take another unit, whose
 // weights come from L2. Blocks claim them from one counter, product 1 first, so that a unit that
 // waits for activations only waits for units that somebody already works on: no
 // assumption on which blocks run at the same time. While it waits, its weights fill the ring.
@@ -484,19 +484,23 @@ __global__ void __launch_bounds__(kTokenThreads) moe_few_token_kernel(const Toke
 constexpr int kExpertThreads = 320;
 constexpr int kRoom = 4;                                 // tokens of a unit at most
 constexpr int kMaxEntries = kMaxChoices;
-constexpr int kMaxStages = 5;
+constexpr int kMaxStages = 4;
 constexpr int kMadeAt = 32;                              // counters of the entries behind the queue's
-constexpr uint32_t kStageWeights = 128 * 128;            // 128 rows x 256 elements
-constexpr uint32_t kStageScales = 1024;                  // two blocks of 512 bytes: of the weights, then of the tokens
-constexpr uint32_t kTokenBytes = 1024;                   // of a token in a stage: eight rows (six used) x 256 elements
+// A stage holds 16 KB of weights: in product 1 64 rows x 512 elements, as two tiles of 256
+// elements one after another, in product 2 one tile of 128 rows x 256. (An MMA takes 128
+// rows: of a tile of 64 the other 64 are whatever follows it, and so are their sums.)
+constexpr uint32_t kStageWeights = 128 * 128;
+constexpr uint32_t kStageScales = 2048;                  // four blocks of 512 bytes: of the weights, then of the tokens
+constexpr uint32_t kTokenTile = 1024;                    // of a token: eight rows (six used) x 256 elements
+constexpr uint32_t kTokenBytes = 2 * kTokenTile;
 constexpr uint32_t kAccColumns = 8 * kRoom;
-constexpr uint32_t kSfColumns = 16;                      // of a stage: two blocks of weights, two of tokens
+constexpr uint32_t kSfColumns = 32;                      // of a stage: four blocks of weights, four of tokens
 constexpr uint32_t kTmemColumns = 256;
 static_assert(2 * kAccColumns + kMaxStages * kSfColumns <= kTmemColumns, "TMEM budget: half of it, two blocks an SM");
 
 struct ExpertsParams {
-    CUtensorMap tm_w13;                 // packed weights [E * 2I, H / 2] u8, box 128 bytes x 64 rows
-    CUtensorMap tm_w2;                  // the same of [E * H, I / 2]
+    CUtensorMap tm_w13;                 // packed weights [E * 2I, H / 2] u8, box 128 bytes x 32 rows
+    CUtensorMap tm_w2;                  // the same of [E * H, I / 2], box 64 rows
     const uint8_t *w13_sf, *w2_sf;
     const uint8_t *xd;                  // [T][6][H / 2] digits of the tokens
     const uint32_t *xsf;                // [T][H / 128][8] their scales
@@ -505,7 +509,7 @@ struct ExpertsParams {
     uint32_t *asf;                      // [T * k][I / 128][8]
     float *y;                           // [T * k, H]
     int *queue;                         // units claimed
-    int *made;                          // [entries] warps that are done with a unit of an entry's product 1
+    int *made;                          // [entries] rows of units of an entry's product 1 that are complete
     int T, k, E, H, I;
     int stages, room;                   // stages of the ring, tokens that one has room for
     uint64_t wait_ns;
@@ -519,7 +523,7 @@ struct Unit {
 };
 
 struct ExpertsShared {
-    float epi[kRoom][128];
+    float epi[kRoom][64];               // G, then U of 32 channels
     uint64_t w_full[kMaxStages];        // weights have landed
     uint64_t t_full[kMaxStages];        // tokens and scales have landed
     uint64_t empty[kMaxStages];         // the stage's MMAs have completed
@@ -535,9 +539,9 @@ struct ExpertsShared {
     uint16_t start[kMaxExperts];        // the first of an expert's choices there
     uint8_t entry_rows[kMaxEntries];
     uint8_t token[kMaxChoices];         // tokens of the choices in slot
-    alignas(16) uint8_t rows[kMaxExperts];   // choices of an expert, counted four in a word
+    alignas(16) uint32_t tokens[kMaxExperts];   // a bit for each token that chose the expert
 };
-static_assert(offsetof(ExpertsShared, rows) % 4 == 0 && offsetof(ExpertsShared, w_full) % 8 == 0, "aligned as it is used");
+static_assert(offsetof(ExpertsShared, w_full) % 8 == 0 && kMaxTokens <= 32, "aligned and sized as it is used");
 
 __device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
@@ -600,7 +604,7 @@ __global__ void __launch_bounds__(kExpertThreads, 2) moe_few_experts_kernel(cons
         tma_prefetch_desc(&p.tm_w2);
     }
     copy_digits(sh.digits);
-    for (int i = tid; i < kMaxExperts / 4; i += kExpertThreads) reinterpret_cast<uint32_t *>(sh.rows)[i] = 0;
+    for (int i = tid; i < kMaxExperts; i += kExpertThreads) sh.tokens[i] = 0;
     if (warp == 9) {
         tmem_alloc(&sh.tmem, kTmemColumns);
         tmem_relinquish();
@@ -613,23 +617,20 @@ __global__ void __launch_bounds__(kExpertThreads, 2) moe_few_experts_kernel(cons
     grid_launch_dependents();        // the sum's blocks have room beside this kernel's, and wait
     int claimed = 0;
     if (tid == 256) claimed = atomicAdd(p.queue, 1);     // on its way while the lists are made
-    // Choices by expert. The order of an expert's choices does not matter: columns of an
-    // MMA do not mix.
-    uint32_t mine[2] = {0, 0};               // (expert + 1, place among its choices) of this thread's choices
+    // Choices by expert, and an expert's by token. Every block makes the same list, whatever
+    // the order its threads come in: an entry has to be the same tokens for all of them.
+    int expert[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int c = tid + i * kExpertThreads;
-        const int e = c < p.T * p.k ? __ldcg(p.ids + c) : -1;
-        if (e >= 0) {
-            const uint32_t was = atomicAdd(reinterpret_cast<uint32_t *>(sh.rows) + (e >> 2), 1u << (8 * (e & 3)));
-            mine[i] = (static_cast<uint32_t>(e + 1) << 8) | ((was >> (8 * (e & 3))) & 0xFF);
-        }
+        expert[i] = c < p.T * p.k ? __ldcg(p.ids + c) : -1;
+        if (expert[i] >= 0) atomicOr(&sh.tokens[expert[i]], 1u << (c / p.k));
     }
     __syncthreads();
     if (warp == 0) {
         int entries = 0, choices = 0;
         for (int e0 = 0; e0 < p.E; e0 += 32) {
-            const int r = e0 + lane < p.E ? sh.rows[e0 + lane] : 0, n = (r + kRoom - 1) / kRoom;
+            const int r = e0 + lane < p.E ? __popc(sh.tokens[e0 + lane]) : 0, n = (r + kRoom - 1) / kRoom;
             int sums = (n << 16) | r;        // entries and choices up to this expert
             const int own = sums;
 #pragma unroll
@@ -653,13 +654,14 @@ __global__ void __launch_bounds__(kExpertThreads, 2) moe_few_experts_kernel(cons
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-        if (mine[i]) {
-            const int at = sh.start[(mine[i] >> 8) - 1] + (mine[i] & 0xFF), c = tid + i * kExpertThreads;
+        if (expert[i] >= 0) {
+            const int c = tid + i * kExpertThreads, t = c / p.k;
+            const int at = sh.start[expert[i]] + __popc(sh.tokens[expert[i]] & ((1u << t) - 1));
             sh.slot[at] = static_cast<uint16_t>(c);
-            sh.token[at] = static_cast<uint8_t>(c / p.k);
+            sh.token[at] = static_cast<uint8_t>(t);
         }
     __syncthreads();
-    const int tiles1 = p.I >> 6, tiles2 = p.H >> 7, n1 = sh.entries * tiles1, n2 = sh.entries * tiles2;
+    const int tiles1 = p.I >> 5, tiles2 = p.H >> 7, n1 = sh.entries * tiles1, n2 = sh.entries * tiles2;
 
     if (warp == 8) {
         if (lane == 0) {
@@ -687,7 +689,7 @@ __global__ void __launch_bounds__(kExpertThreads, 2) moe_few_experts_kernel(cons
                 if (w.first < 0) return;
                 if (w.first) {
                     const uint32_t run = (p.H >> 7) * 512;
-                    const size_t blk = static_cast<size_t>(2 * p.I >> 7) * w.e + (w.c >> 1);
+                    const size_t blk = static_cast<size_t>(2 * p.I >> 7) * w.e + (w.c >> 2);
                     prefetch_l2_bulk(p.w13_sf + blk * run, run);
                     prefetch_l2_bulk(p.w13_sf + (blk + (p.I >> 7)) * run, run);
                 } else {
@@ -704,17 +706,27 @@ __global__ void __launch_bounds__(kExpertThreads, 2) moe_few_experts_kernel(cons
                 mbar_arrive(&sh.unit_full[i & 3]);
                 if (w.first < 0) break;
                 const int next = atomicAdd(p.queue, 1);    // on its way while this unit loads
-                const int stages = ((w.first ? p.H : p.I) + 255) >> 8;
-                // 64 rows of G and the same of U, or 128 rows
-                const int r0 = w.first ? w.e * 2 * p.I + 64 * w.c : w.e * p.H + 128 * w.c;
-                const int r1 = r0 + (w.first ? p.I : 64);
-                const CUtensorMap *tm = w.first ? &p.tm_w13 : &p.tm_w2;
+                const int kc = (w.first ? p.H : p.I) >> 7, stages = w.first ? (kc + 3) >> 2 : (kc + 1) >> 1;
+                // 32 rows of G and the same of U, or 128 rows
+                const int r0 = w.first ? w.e * 2 * p.I + 32 * w.c : w.e * p.H + 128 * w.c;
                 for (int ks = 0; ks < stages; ++ks) {
                     if (!(ok = mbar_wait(&sh.empty[at.slot], at.parity ^ 1u, &g_moe_few_error, kErrWaitEmpty, p.wait_ns))) break;
                     uint8_t *st = smem + at.slot * stage_bytes;
-                    mbar_arrive_expect_tx(&sh.w_full[at.slot], kStageWeights);
-                    tma_load_2d(st, tm, ks * 128, r0, &sh.w_full[at.slot], pol);
-                    tma_load_2d(st + 8192, tm, ks * 128, r1, &sh.w_full[at.slot], pol);
+                    uint64_t *full = &sh.w_full[at.slot];
+                    if (w.first) {
+                        const bool two = 4 * ks + 2 < kc;
+                        mbar_arrive_expect_tx(full, two ? kStageWeights : kStageWeights / 2);
+                        tma_load_2d(st, &p.tm_w13, ks * 256, r0, full, pol);
+                        tma_load_2d(st + 4096, &p.tm_w13, ks * 256, r0 + p.I, full, pol);
+                        if (two) {
+                            tma_load_2d(st + 8192, &p.tm_w13, ks * 256 + 128, r0, full, pol);
+                            tma_load_2d(st + 12288, &p.tm_w13, ks * 256 + 128, r0 + p.I, full, pol);
+                        }
+                    } else {
+                        mbar_arrive_expect_tx(full, kStageWeights);
+                        tma_load_2d(st, &p.tm_w2, ks * 128, r0, full, pol);
+                        tma_load_2d(st + 8192, &p.tm_w2, ks * 128, r0 + 64, full, pol);
+                    }
                     ++issued;
                     at.step(S);
                 }
@@ -738,7 +750,7 @@ __global__ void __launch_bounds__(kExpertThreads, 2) moe_few_experts_kernel(cons
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.unit_empty[i & 3]);
             if (w.first < 0) break;
-            const int kc = (w.first ? p.H : p.I) >> 7, stages = (kc + 1) >> 1, buf = i & 1;
+            const int kc = (w.first ? p.H : p.I) >> 7, stages = w.first ? (kc + 3) >> 2 : (kc + 1) >> 1, buf = i & 1;
             ok = mbar_wait_warp(&sh.acc_empty[buf], ((i >> 1) & 1) ^ 1u, &g_moe_few_error, kErrWaitAccum, p.wait_ns);
             if (!ok) break;
             tc_fence_after();
@@ -756,16 +768,21 @@ __global__ void __launch_bounds__(kExpertThreads, 2) moe_few_experts_kernel(cons
                 const uint64_t sd = sdesc_scale(st + kStageWeights);
                 const uint32_t tsf = tmem + 2 * kAccColumns + at.slot * kSfColumns;
                 if (elect_one()) {
-                    auto half = [&](int h, uint32_t accumulate) {
-                        tc_cp_scale_block(tsf + 4 * h, sd + 32 * h);
-                        tc_cp_scale_block(tsf + 8 + 4 * h, sd + 64 + 32 * h);
-                        mma_mxf4(d, ad + 4 * h, bd + 4 * h, idesc_with_sf_ids(idesc, 0, 0), tsf + 4 * h, tsf + 8 + 4 * h,
-                                 accumulate);
-                        mma_mxf4(d, ad + 4 * h + 2, bd + 4 * h + 2, idesc_with_sf_ids(idesc, 2, 2), tsf + 4 * h,
-                                 tsf + 8 + 4 * h, 1u);
+                    // block b of 128 elements: two MMAs of 64
+                    auto block = [&](int b, uint32_t accumulate) {
+                        const uint64_t a = ad + (b >> 1) * 512 + (b & 1) * 4;
+                        const uint64_t x = bd + (b >> 1) * (p.room * (kTokenTile >> 4)) + (b & 1) * 4;
+                        const uint32_t sa = tsf + 4 * b, sx = tsf + 16 + 4 * b;
+                        tc_cp_scale_block(sa, sd + 32 * b);
+                        tc_cp_scale_block(sx, sd + 128 + 32 * b);
+                        mma_mxf4(d, a, x, idesc_with_sf_ids(idesc, 0, 0), sa, sx, accumulate);
+                        mma_mxf4(d, a + 2, x + 2, idesc_with_sf_ids(idesc, 2, 2), sa, sx, 1u);
                     };
-                    half(0, ks > 0 ? 1u : 0u);
-                    if (2 * ks + 1 < kc) half(1, 1u);
+                    const int left = w.first ? kc - 4 * ks : min(2, kc - 2 * ks);
+                    block(0, ks > 0 ? 1u : 0u);
+                    if (left > 1) block(1, 1u);
+                    if (left > 2) block(2, 1u);
+                    if (left > 3) block(3, 1u);
                     tc_commit(&sh.empty[at.slot]);
                 }
                 __syncwarp();
@@ -796,7 +813,7 @@ __global__ void __launch_bounds__(kExpertThreads, 2) moe_few_experts_kernel(cons
             if (w.first < 0) break;
             // row of a choice among the tokens or the activations
             auto row_of = [&](int r) { return static_cast<size_t>(w.first ? sh.token[w.slots + r] : sh.slot[w.slots + r]); };
-            const int K = w.first ? p.H : p.I, kc = K >> 7, stages = (kc + 1) >> 1;
+            const int K = w.first ? p.H : p.I, kc = K >> 7, stages = w.first ? (kc + 3) >> 2 : (kc + 1) >> 1;
             // a row of digits is K / 2 bytes, six of them a token; pieces of 16 bytes, column c of row n at c ^ (n % 8)
             const uint8_t *digits = w.first ? p.xd : p.ad;
             const uint32_t *scales = w.first ? p.xsf : p.asf;
@@ -808,29 +825,28 @@ __global__ void __launch_bounds__(kExpertThreads, 2) moe_few_experts_kernel(cons
                 dst[j] = kStageWeights + 2 * kStageScales + (8 * r + dg) * 128 + ((c ^ dg) << 4);
                 if (r < w.rows) src[j] = digits + (row_of(r) * 6 + dg) * (K >> 1) + 16 * c;
             }
-            const bool tail_col = (t & 7) < 4;               // columns of a stage's first half (piece 128 j + t: column t % 8)
-            // scale words: thread t < 64 that of half t % 2, digit t / 2 % 8, token t / 16
-            const int sr = t >> 4, sdg = (t >> 1) & 7, sh2 = t & 1;
-            const uint32_t sdst = kStageWeights + kStageScales + sh2 * 512 + (8 * sr + sdg) * 16;
-            const uint32_t *ssrc = sr < w.rows && sdg < 6 ? scales + (row_of(sr) * kc + sh2) * 8 + sdg : nullptr;
-            // scales of the weights: of product 1 from the halves of the 128-row blocks of G and of U
-            // that hold its 64 channels (8 of each 16 bytes)
+            const bool low = (t & 7) < 4;                    // columns of a tile's first 128 elements (piece 128 j + t: column t % 8)
+            // scale words: thread t < 64 those of blocks t % 2 (and that + 2), digit t / 2 % 8, token t / 16
+            const int sr = t >> 4, sdg = (t >> 1) & 7, sblk = t & 1;
+            const uint32_t sdst = kStageWeights + kStageScales + sblk * 512 + (8 * sr + sdg) * 16;
+            const uint32_t *ssrc = sr < w.rows && sdg < 6 ? scales + (row_of(sr) * kc + sblk) * 8 + sdg : nullptr;
+            // scales of the weights, lane l line l of a block: in product 1 the word of each line that
+            // is of the 32 rows of G (threads 64 to 95) and of U, in product 2 the whole line
             const uint8_t *wsf = nullptr;
-            uint32_t wdst = kStageWeights;
+            uint32_t wdst = kStageWeights + lane * 16;
             if (w.first && t >= 64) {
-                const size_t blk = static_cast<size_t>(2 * p.I >> 7) * w.e + (w.c >> 1) + (t >= 96 ? p.I >> 7 : 0);
-                wsf = p.w13_sf + blk * kc * 512 + lane * 16 + (w.c & 1) * 8;
-                wdst += lane * 16 + (t >= 96 ? 8 : 0);
+                const size_t blk = static_cast<size_t>(2 * p.I >> 7) * w.e + (w.c >> 2) + (t >= 96 ? p.I >> 7 : 0);
+                wsf = p.w13_sf + blk * kc * 512 + lane * 16 + (w.c & 3) * 4;
+                wdst += t >= 96 ? 4 : 0;
             } else if (!w.first && t >= 64 && t < 96) {
                 wsf = p.w2_sf + (static_cast<size_t>(p.H >> 7) * w.e + w.c) * kc * 512 + lane * 16;
-                wdst += lane * 16;
             }
             if (!w.first && w.entry > ready) {
                 // this entry's activations have to be there
                 int v = 1;
                 if (lane == 0) {
                     const uint64_t t0 = global_timer_ns();
-                    while (load_acquire(p.made + w.entry) < 4 * tiles1) {
+                    while (load_acquire(p.made + w.entry) < w.rows * tiles1) {
                         if (global_timer_ns() - t0 > p.wait_ns) {
                             atomicCAS(&g_moe_few_error, 0, kErrWaitOperand);
                             v = 0;
@@ -847,16 +863,27 @@ __global__ void __launch_bounds__(kExpertThreads, 2) moe_few_experts_kernel(cons
                 ok = mbar_wait_warp(&sh.empty[at.slot], at.parity ^ 1u, &g_moe_few_error, kErrWaitEmpty, p.wait_ns);
                 if (!ok) break;
                 const uint32_t st = smem_u32(smem) + at.slot * stage_bytes;
-                const bool whole = 2 * ks + 1 < kc;
+                if (w.first) {
+                    const int left = kc - 4 * ks;            // blocks of 128 elements
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    if (src[j] && (whole || tail_col)) cp_async<16>(st + dst[j], src[j] + ks * 128);
-                if (ssrc && (whole || !sh2)) cp_async<4>(st + sdst, ssrc + ks * 16);
-                if (wsf) {
-                    if (w.first) {
-                        cp_async<8>(st + wdst, wsf + ks * 1024);
-                        if (whole) cp_async<8>(st + wdst + 512, wsf + ks * 1024 + 512);
-                    } else {
+                    for (int j = 0; j < 2; ++j) {
+                        if (src[j] && (left > 1 || low)) cp_async<16>(st + dst[j], src[j] + ks * 256);
+                        if (src[j] && (left > 3 || (left > 2 && low)))
+                            cp_async<16>(st + dst[j] + p.room * kTokenTile, src[j] + ks * 256 + 128);
+                    }
+                    if (ssrc && sblk < left) cp_async<4>(st + sdst, ssrc + ks * 32);
+                    if (ssrc && sblk + 2 < left) cp_async<4>(st + sdst + 1024, ssrc + ks * 32 + 16);
+                    if (wsf)
+#pragma unroll
+                        for (int b = 0; b < 4; ++b)
+                            if (b < left) cp_async<4>(st + wdst + b * 512, wsf + ks * 2048 + b * 512);
+                } else {
+                    const bool whole = 2 * ks + 1 < kc;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        if (src[j] && (whole || low)) cp_async<16>(st + dst[j], src[j] + ks * 128);
+                    if (ssrc && (whole || sblk == 0)) cp_async<4>(st + sdst, ssrc + ks * 16);
+                    if (wsf) {
                         cp_async<16>(st + wdst, wsf + ks * 1024);
                         if (whole) cp_async<16>(st + wdst + 512, wsf + ks * 1024 + 512);
                     }
@@ -899,48 +926,39 @@ __global__ void __launch_bounds__(kExpertThreads, 2) moe_few_experts_kernel(cons
                 float s = __uint_as_float(v[8 * r]);
 #pragma unroll
                 for (int d = 1; d < 6; ++d) s += __uint_as_float(v[8 * r + d]);
-                if (w.first)
+                if (w.first && tid < 64)
                     sh.epi[r][tid] = s;
-                else
+                else if (!w.first)
                     p.y[static_cast<size_t>(sh.slot[w.slots + r]) * p.H + 128 * w.c + tid] = s;
             }
             epilogue_sync();
             if (tid == 0) mbar_arrive(&sh.unit_empty[i & 3]);
             if (!w.first) continue;
-            // a warp has a token, a lane two of its 64 channels; half a warp is a block of 32
+            // a warp has a token, a lane one of its 32 channels: a block of MXFP8
             const int r = warp;
             if (r < w.rows) {
-                float a[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    // silu as in moe_experts.cu: off by up to (5 + 1.2 |g|) 2^-23 of itself, 0 below -87.3
-                    const float g = sh.epi[r][2 * lane + j];
-                    a[j] = __fdividef(g, 1.0f + __expf(-g)) * sh.epi[r][64 + 2 * lane + j];
-                }
-                uint32_t amax = max(__float_as_uint(a[0]) & 0x7FFFFFFFu, __float_as_uint(a[1]) & 0x7FFFFFFFu);
-#pragma unroll
-                for (int o = 1; o < 16; o <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                const uint32_t b = mxfp8_scale_byte(amax), b2 = __shfl_down_sync(0xffffffffu, b, 16);
-                const float inv = mxfp8_scale_inverse(b);
-                const uint32_t codes = e4m3x4_rn(a[0] * inv, a[1] * inv, 0.0f, 0.0f);
-                const uint32_t d0 = digits_of(sh.digits, codes & 0xFFu, b), d1 = digits_of(sh.digits, (codes >> 8) & 0xFFu, b);
+                // silu as in moe_experts.cu: off by up to (5 + 1.2 |g|) 2^-23 of itself, 0 below -87.3
+                const float g = sh.epi[r][lane], a = __fdividef(g, 1.0f + __expf(-g)) * sh.epi[r][32 + lane];
+                const uint32_t b = mxfp8_scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(a) & 0x7FFFFFFFu));
+                const uint32_t code = e4m3x4_rn(a * mxfp8_scale_inverse(b), 0.0f, 0.0f, 0.0f) & 0xFFu;
+                const uint32_t d0 = digits_of(sh.digits, code, b), d1 = __shfl_down_sync(0xffffffffu, d0, 1);
                 const size_t row = sh.slot[w.slots + r];
-                uint8_t *o = p.ad + row * 6 * (p.I >> 1) + 32 * w.c + lane;
+                if (!(lane & 1)) {
+                    uint8_t *o = p.ad + row * 6 * (p.I >> 1) + 16 * w.c + (lane >> 1);
 #pragma unroll
-                for (int d = 0; d < 6; ++d)
-                    o[static_cast<size_t>(d) * (p.I >> 1)] =
-                        static_cast<uint8_t>(((d0 >> (4 * d)) & 0xFu) | (((d1 >> (4 * d)) & 0xFu) << 4));
-                if (lane < 6) {
-                    uint8_t *f = reinterpret_cast<uint8_t *>(p.asf + (row * (p.I >> 7) + (w.c >> 1)) * 8) + 2 * (w.c & 1);
-                    // b is the first block's for these lanes, b2 the second's
-                    *reinterpret_cast<uint16_t *>(f + 4 * lane) =
-                        static_cast<uint16_t>(digit_scale(b, lane) | (digit_scale(b2, lane) << 8));
+                    for (int d = 0; d < 6; ++d)
+                        o[static_cast<size_t>(d) * (p.I >> 1)] =
+                            static_cast<uint8_t>(((d0 >> (4 * d)) & 0xFu) | (((d1 >> (4 * d)) & 0xFu) << 4));
                 }
-            }
-            __syncwarp();
-            if (lane == 0) {
-                __threadfence();
-                atomicAdd(p.made + w.entry, 1);
+                if (lane < 6)
+                    reinterpret_cast<uint8_t *>(p.asf + (row * (p.I >> 7) + (w.c >> 2)) * 8)[4 * lane + (w.c & 3)] =
+                        static_cast<uint8_t>(digit_scale(b, lane));
+                __syncwarp();
+                if (lane == 0) {
+                    // what the warp wrote is there before the count says so
+                    asm volatile("fence.acq_rel.gpu;" ::: "memory");
+                    asm volatile("red.relaxed.gpu.global.add.s32 [%0], 1;" ::"l"(p.made + w.entry) : "memory");
+                }
             }
         }
     }
@@ -1130,7 +1148,7 @@ cudaError_t launch_moe_few(const MoeFewArgs &a, const MoeFewLayout &l, cudaStrea
     p.stages = std::min<int>(kMaxStages, (kExpertsSmem - 1024 - sizeof(ExpertsShared)) / stage);
     // no more blocks than there can be units
     const int64_t entries = std::min<int64_t>(p.E + p.T * p.k / kRoom, int64_t(p.T) * p.k);
-    const int64_t units = entries * (p.I / 64 + p.H / 128);
+    const int64_t units = entries * (p.I / 32 + p.H / 128);
     e = launch_pdl(moe_few_experts_kernel, static_cast<unsigned>(std::min<int64_t>(2 * sms, units)), kExpertThreads,
                    kExpertsSmem, stream, p);
     if (e != cudaSuccess) return e;

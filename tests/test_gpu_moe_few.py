@@ -215,3 +215,16 @@ def test_zero_tokens_and_refusals_of_the_binding():
         call(dict(s, x=torch.zeros((17, 256), device="cuda").bfloat16()), 2, residual=False)
     with pytest.raises(mx.Mxfp4Error):
         call(s, 2, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_experts_whose_tokens_take_several_units(seed):
+    """More than four tokens of an expert are several units of work: all blocks agree on which tokens are whose, call after
+    call, and a token's result is that of its call alone."""
+    s = make(11, 24, 256, 128, seed=seed)
+    how = dict(groups=2, topk_groups=1, bias=s["bias"], scale=0.5)
+    alone = [call(dict(s, x=s["x"][t:t + 1], res=s["res"][t:t + 1]), 3, **how) for t in range(11)]
+    assert int(torch.bincount(torch.cat([a[2] for a in alone]).flatten().long()).max()) > 4
+    for _ in range(40):
+        got = call(s, 3, **how)
+        assert all(torch.equal(g, torch.cat(parts)) for g, parts in zip(got, zip(*alone)))
