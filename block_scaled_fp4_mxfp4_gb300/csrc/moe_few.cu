@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(kTokenThreads) moe_few_token_kernel(const Toke
 
 // ----------------------------------------------------------------- experts
 
-constexpr int kExpertThreads = 320;
+constexpr int kExpertThreads = 352;
 constexpr int kRoom = 4;                                 // tokens of a unit at most
 constexpr int kMaxEntries = kMaxChoices;
 constexpr int kMaxStages = 4;
@@ -529,6 +529,7 @@ struct ExpertsShared {
     uint64_t empty[kMaxStages];         // the stage's MMAs have completed
     uint64_t unit_full[4], unit_empty[4];
     uint64_t acc_full[2], acc_empty[2];
+    uint64_t written[4];                // a unit's results are written
     uint64_t mma_done;
     uint32_t tmem;
     int abort, entries, go[2];
@@ -570,6 +571,8 @@ struct Place {
 //   4-7  copy tokens' digits and all scales into the ring by cp.async
 //   8    lane 0 claims units and loads their weights by TMA
 //   9    issues scale copies and MMAs (an elected lane); owns TMEM
+//   10   publishes the activations that the epilogue wrote: a fence for the whole GPU takes
+//        two microseconds here, in which the epilogue goes on
 // Two blocks share an SM: what a unit costs beside its bytes (a microsecond or two of
 // latencies at its start and end) passes while the other block's weights stream.
 // Waits name a round of a barrier by its parity. Nobody can be a round behind: the next
@@ -591,7 +594,8 @@ __global__ void __launch_bounds__(kExpertThreads, 2) moe_few_experts_kernel(cons
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&sh.unit_full[i], 1);
-            mbar_init(&sh.unit_empty[i], 6);     // four copying warps, the issuer, the epilogue
+            mbar_init(&sh.unit_empty[i], 7);     // four copying warps, the issuer, the epilogue, the publisher
+            mbar_init(&sh.written[i], 4);        // the epilogue's warps
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.acc_full[i], 1);
@@ -628,28 +632,31 @@ __global__ void __launch_bounds__(kExpertThreads, 2) moe_few_experts_kernel(cons
     }
     __syncthreads();
     if (warp == 0) {
-        int entries = 0, choices = 0;
-        for (int e0 = 0; e0 < p.E; e0 += 32) {
-            const int r = e0 + lane < p.E ? __popc(sh.tokens[e0 + lane]) : 0, n = (r + kRoom - 1) / kRoom;
-            int sums = (n << 16) | r;        // entries and choices up to this expert
-            const int own = sums;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, sums, o);
-                if (lane >= o) sums += x;
-            }
-            const int all = __shfl_sync(0xffffffffu, sums, 31), before = sums - own;
-            const int at = entries + (before >> 16), c0 = choices + (before & 0xFFFF);
-            if (r > 0) sh.start[e0 + lane] = static_cast<uint16_t>(c0);
-            for (int i = 0; i < n; ++i) {
-                sh.entry_expert[at + i] = static_cast<uint16_t>(e0 + lane);
-                sh.entry_slots[at + i] = static_cast<uint16_t>(c0 + kRoom * i);
-                sh.entry_rows[at + i] = static_cast<uint8_t>(min(kRoom, r - kRoom * i));
-            }
-            entries += all >> 16;
-            choices += all & 0xFFFF;
+        // a lane takes neighbouring experts
+        const int per = (p.E + 31) >> 5, e0 = lane * per, e1 = min(p.E, e0 + per);
+        int own = 0;                         // entries << 16 | choices
+        for (int e = e0; e < e1; ++e) {
+            const int r = __popc(sh.tokens[e]);
+            own += ((r + kRoom - 1) / kRoom) << 16 | r;
         }
-        if (lane == 0) sh.entries = entries;
+        int sums = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, sums, o);
+            if (lane >= o) sums += x;
+        }
+        if (lane == 31) sh.entries = sums >> 16;
+        int at = (sums - own) >> 16, c0 = (sums - own) & 0xFFFF;
+        for (int e = e0; e < e1; ++e) {
+            const int r = __popc(sh.tokens[e]);
+            sh.start[e] = static_cast<uint16_t>(c0);
+            for (int i = 0; i < r; i += kRoom) {
+                sh.entry_expert[at] = static_cast<uint16_t>(e);
+                sh.entry_slots[at] = static_cast<uint16_t>(c0 + i);
+                sh.entry_rows[at++] = static_cast<uint8_t>(min(kRoom, r - i));
+            }
+            c0 += r;
+        }
     }
     __syncthreads();
 #pragma unroll
@@ -797,6 +804,20 @@ __global__ void __launch_bounds__(kExpertThreads, 2) moe_few_experts_kernel(cons
         if (elect_one()) tc_commit(&sh.mma_done);
         __syncwarp();
         mbar_wait_warp(&sh.mma_done, 0, &g_moe_few_error, kErrWaitDrain);
+    } else if (warp == 10) {
+        if (lane == 0) {
+            // ----------------------------------------------------- publishing
+            // It gives up its entry of the ring of units last, so the epilogue is at most four units ahead.
+            for (int i = 0;; ++i) {
+                if (!mbar_wait(&sh.unit_full[i & 3], (i >> 2) & 1, &g_moe_few_error, kErrWaitFull, p.wait_ns)) break;
+                const Unit w = sh.unit[i & 3];
+                if (w.first < 0 || !mbar_wait(&sh.written[i & 3], (i >> 2) & 1, &g_moe_few_error, kErrWaitAccum, p.wait_ns)) break;
+                if (w.first)
+                    // what the epilogue's warps wrote is there before the count says so
+                    asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p.made + w.entry), "r"(w.rows) : "memory");
+                mbar_arrive(&sh.unit_empty[i & 3]);
+            }
+        }
     } else if (warp >= 4) {
         // -------------------------------------------------- tokens and scales
         const int t = tid - 128;
@@ -933,7 +954,10 @@ __global__ void __launch_bounds__(kExpertThreads, 2) moe_few_experts_kernel(cons
             }
             epilogue_sync();
             if (tid == 0) mbar_arrive(&sh.unit_empty[i & 3]);
-            if (!w.first) continue;
+            if (!w.first) {
+                if (lane == 0) mbar_arrive(&sh.written[i & 3]);
+                continue;
+            }
             // a warp has a token, a lane one of its 32 channels: a block of MXFP8
             const int r = warp;
             if (r < w.rows) {
@@ -953,13 +977,9 @@ __global__ void __launch_bounds__(kExpertThreads, 2) moe_few_experts_kernel(cons
                 if (lane < 6)
                     reinterpret_cast<uint8_t *>(p.asf + (row * (p.I >> 7) + (w.c >> 2)) * 8)[4 * lane + (w.c & 3)] =
                         static_cast<uint8_t>(digit_scale(b, lane));
-                __syncwarp();
-                if (lane == 0) {
-                    // what the warp wrote is there before the count says so
-                    asm volatile("fence.acq_rel.gpu;" ::: "memory");
-                    asm volatile("red.relaxed.gpu.global.add.s32 [%0], 1;" ::"l"(p.made + w.entry) : "memory");
-                }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.written[i & 3]);
         }
     }
     __syncwarp();
