@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "internal.h"
+#include "layer.h"
 #include "moe.h"
 #include "mxfp4.h"
 
@@ -871,8 +872,12 @@ mxfp4_status_t mxfp4_get_device_error(int *code)
     const int pg = read_and_clear_gemm_pair_error();
     const int me = read_and_clear_moe_error();
     const int mf = read_and_clear_moe_few_error();
-    if (g < 0 || f < 0 || pg < 0 || me < 0 || mf < 0) return MXFP4_ERR_CUDA;
-    *code = g != 0 ? g : (f != 0 ? 16 + f : (pg != 0 ? 32 + pg : (me != 0 ? 48 + me : (mf != 0 ? 64 + mf : 0))));
+    const int lo = read_and_clear_lora_error();
+    if (g < 0 || f < 0 || pg < 0 || me < 0 || mf < 0 || lo < 0) return MXFP4_ERR_CUDA;
+    const int codes[6] = {g, f, pg, me, mf, lo};
+    *code = 0;
+    for (int i = 5; i >= 0; --i)
+        if (codes[i] != 0) *code = 16 * i + codes[i];
     return MXFP4_OK;
 }
 

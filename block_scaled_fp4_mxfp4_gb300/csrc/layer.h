@@ -21,7 +21,7 @@ struct QkParams {
     int heads[2];
     int D, rot, pos64;
     float eps;
-    int units[2];               // set at launch: units of heads a token has
+    int units, unit_heads;      // set at launch: units that a token's heads make, and heads of one
 };
 cudaError_t launch_qk_norm_rope(const QkParams &p, bool f16, bool interleaved, int num_sms, cudaStream_t stream);
 
@@ -40,14 +40,14 @@ struct LoraParams {
     float *u;                   // [splits][T][R] partial sums of the first product
     int *order;                 // [T] tokens by adapter            (long batches only)
     int4 *tiles;                // adapter, first of order, tokens  (long batches only)
-    int *num_tiles;
-    int splits;
+    int splits, max_tiles;
 };
 struct LoraLayout {
     int splits, max_tiles;
-    size_t u, order, tiles, count, total;
+    size_t u, order, tiles, total;
 };
 LoraLayout lora_layout(int64_t T, int64_t K, int R, int L);
 cudaError_t launch_lora(LoraParams p, const LoraLayout &l, bool f16, cudaStream_t stream);
+int read_and_clear_lora_error();
 
 }  // namespace mxfp4

@@ -76,7 +76,6 @@ mxfp4_status_t lora_add(const void *X, int64_t ldx, const void *A, const void *B
     p.u = reinterpret_cast<float *>(ws + l.u);
     p.order = reinterpret_cast<int *>(ws + l.order);
     p.tiles = reinterpret_cast<int4 *>(ws + l.tiles);
-    p.num_tiles = reinterpret_cast<int *>(ws + l.count);
     return cuda_status(launch_lora(p, l, dtype == MXFP4_DTYPE_FP16, static_cast<cudaStream_t>(stream)));
 }
 

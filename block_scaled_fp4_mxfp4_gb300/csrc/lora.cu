@@ -2,26 +2,26 @@
 //
 // Mathematics, for token t of adapter a: u = x_t A_a^T (R numbers), then
 // C_t = base_t + s_a u B_a^T. Two launches, and one before them for long batches:
-//   sort    tokens by adapter, in tiles of up to 64 tokens of one adapter. Up to
+//   sort    tokens by adapter, in tiles of up to 128 tokens of one adapter. Up to
 //           kInline tokens every block works the tiles out for itself, from the ids
 //           in shared memory.
-//   shrink  u. The 16 rows of an MMA are rows of A_a, its columns are tokens, so that a
-//           tile of one token wastes columns only. K is split over blocks, and inside
-//           a block over its warps: a warp holds all of the tile's u (up to 64 ranks x
-//           64 tokens) in registers and reads each x and each a of its part of K
-//           once, from global memory straight into the MMA's registers (which order
-//           of K the operands take is free as long as it is the same for both: a lane
-//           holds 8 neighbouring k, one 16-byte vector). Sums of a block go to
-//           the workspace, those of the splits are added in order by the next launch.
-//   expand  u B_a^T + base. Rows of the MMA are tokens, columns are channels, chosen so
-//           that a lane ends with 8 neighbouring channels of a token: one 16-byte
-//           load of base and one store. u, summed in fp32, enters as two bf16 (high
-//           and low part, 2^-17 together): twice the MMAs of a product that is not
-//           bound by them, where one bf16 would cost 2^-9 of the update.
+//   shrink  u, K split over blocks: sums go to the workspace, and those of the splits are added
+//           in order by the next launch. Up to kInline tokens a block's warps split its
+//           part of K once more; a warp holds all of the tile's u in registers
+//           (mma.sync: 16 ranks x 8 tokens, so that a tile of one token wastes columns only)
+//           and reads each x and each a once, from global memory straight into the
+//           MMA's registers (which order of K the operands take is free as long as it
+//           is the same for both: a lane holds 8 neighbouring k, one 16-byte vector).
+//           Longer batches: tcgen05.mma kind::f16 with the ranks as the 128 rows and up
+//           to 128 tokens as columns, a_a by TMA, token rows gathered by cp.async, which
+//           take a ring of shared memory at the rate of HBM.
+//   expand  u B_a^T + base, for up to 64 tokens a block. Rows of the MMA are tokens, columns
+//           are channels, chosen so that a lane ends with 8 neighbouring channels of a
+//           token: one 16-byte load of base and one store. u, summed in fp32, enters as two
+//           bf16 (high and low part, 2^-17 together): twice the MMAs of a product that is
+//           not bound by them, where one bf16 would cost 2^-9 of the update.
 //
 // Bound: few tokens, latency of two dependent launches; many, HBM (x once, base and C).
-// mma.sync and not tcgen05: tiles are as small as one token, and a tile of 128 rows of
-// the latter would be filled by padding; the products take R operations a byte.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -33,13 +33,16 @@
 
 namespace mxfp4 {
 
+__device__ int g_lora_error;
+
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kTile = 64;          // tokens of a tile
+constexpr int kTile = 128;         // tokens of a tile
+constexpr int kHalf = 64;          // tokens of a block of the second product
 constexpr int kInline = 64;        // tokens up to which blocks work out the tiles themselves
-constexpr int kRanks = 64;         // ranks of one block of the first product
+constexpr int kRanks = 64;         // ranks of one block of the first product, up to kInline tokens
 constexpr int kMaxRank = 256;
 constexpr int kSortThreads = 1024;
 
@@ -52,117 +55,128 @@ struct Tile {
 __device__ __forceinline__ int adapter_of(int id, int L) { return id >= 0 && id < L ? id : L; }
 
 // Tokens by adapter, and the tiles of it. One block: counts in shared memory, prefix
-// sums, ranks. In which order a tile's tokens stand does not matter to their results.
+// sums, ranks. In which order a tile's tokens stand does not matter to their results. A
+// thread keeps its first kSortKeep ids in registers.
+constexpr int kSortKeep = 8;
 __global__ void __launch_bounds__(kSortThreads) lora_sort_kernel(const LoraParams p)
 {
     extern __shared__ int bins[];            // [L + 1]: tokens, then the next free place
-    __shared__ int scan[2][32];
-    const int tid = threadIdx.x, groups = p.L + 1;
+    __shared__ int2 scan[kSortThreads / 32]; // tokens and tiles of the groups before a warp's
+    __shared__ int2 all;
+    const int tid = threadIdx.x, lane = tid & 31, groups = p.L + 1;
     for (int i = tid; i < groups; i += kSortThreads) bins[i] = 0;
     __syncthreads();
     grid_dependency_wait();
     grid_launch_dependents();
-    // neighbours often share an adapter: one atomic for all of a warp's lanes that do
-    for (int64_t base = 0; base < p.T; base += kSortThreads) {
-        const int64_t i = base + tid;
-        const int g = i < p.T ? adapter_of(p.ids[i], p.L) : -1;
-        const unsigned same = __match_any_sync(0xffffffffu, g);
-        if (g >= 0 && (tid & 31) == __ffs(same) - 1) atomicAdd(&bins[g], __popc(same));
+    int kept[kSortKeep];
+#pragma unroll
+    for (int i = 0; i < kSortKeep; ++i) {
+        const int at = i * kSortThreads + tid;
+        kept[i] = at < p.T ? p.ids[at] : 0;
     }
+    // neighbours often share an adapter: one atomic for all of a warp's lanes that do
+    auto count = [&](int64_t at, int id) {
+        const int g = at < p.T ? adapter_of(id, p.L) : -1;
+        const unsigned same = __match_any_sync(0xffffffffu, g);
+        if (g >= 0 && lane == __ffs(same) - 1) atomicAdd(&bins[g], __popc(same));
+    };
+#pragma unroll
+    for (int i = 0; i < kSortKeep; ++i)
+        if (i * kSortThreads < p.T) count(i * kSortThreads + tid, kept[i]);
+    for (int64_t base = kSortKeep * kSortThreads; base < p.T; base += kSortThreads)
+        count(base + tid, base + tid < p.T ? p.ids[base + tid] : 0);
     __syncthreads();
-    int places = 0, tiles = 0;               // of the groups before this round's
+    int2 before = make_int2(0, 0);           // tokens and tiles of the groups before this round's
     for (int g0 = 0; g0 < groups; g0 += kSortThreads) {
         const int g = g0 + tid;
         const int n = g < groups ? bins[g] : 0;
-        const bool skip = g == p.L && !p.copy;
-        const int nt = skip ? 0 : (n + kTile - 1) / kTile;
+        const int nt = g == p.L && !p.copy ? 0 : (n + kTile - 1) / kTile;
         int a = n, b = nt;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
-            if ((tid & 31) >= o) {
+            if (lane >= o) {
                 a += x;
                 b += y;
             }
         }
-        if ((tid & 31) == 31) {
-            scan[0][tid >> 5] = a;
-            scan[1][tid >> 5] = b;
+        if (lane == 31) scan[tid >> 5] = make_int2(a, b);
+        __syncthreads();
+        if (tid < 32) {
+            const int2 own = scan[lane];
+            int2 sum = own;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, sum.x, o), y = __shfl_up_sync(0xffffffffu, sum.y, o);
+                if (lane >= o) {
+                    sum.x += x;
+                    sum.y += y;
+                }
+            }
+            scan[lane] = make_int2(sum.x - own.x, sum.y - own.y);
+            if (lane == 31) all = sum;
         }
         __syncthreads();
-        int before_a = places, before_b = tiles;
-        for (int w = 0; w < kSortThreads / 32; ++w) {
-            if (w < (tid >> 5)) {
-                before_a += scan[0][w];
-                before_b += scan[1][w];
-            }
-            places += scan[0][w];
-            tiles += scan[1][w];
-        }
         if (g < groups) {
-            const int first = before_a + a - n, tile = before_b + b - nt;
+            const int first = before.x + scan[tid >> 5].x + a - n, tile = before.y + scan[tid >> 5].y + b - nt;
             bins[g] = first;
             for (int i = 0; i < nt; ++i)
                 p.tiles[tile + i] = make_int4(g, first + i * kTile, min(kTile, n - i * kTile), 0);
         }
+        before.x += all.x;
+        before.y += all.y;
         __syncthreads();
     }
-    if (tid == 0) *p.num_tiles = tiles;
-    for (int64_t base = 0; base < p.T; base += kSortThreads) {
-        const int64_t i = base + tid;
-        const int g = i < p.T ? adapter_of(p.ids[i], p.L) : -1;
+    // the others of the grid's tiles are empty
+    for (int i = before.y + tid; i < p.max_tiles; i += kSortThreads) p.tiles[i] = make_int4(p.L, 0, 0, 0);
+    auto place = [&](int64_t at, int id) {
+        const int g = at < p.T ? adapter_of(id, p.L) : -1;
         const unsigned same = __match_any_sync(0xffffffffu, g);
-        const int leader = __ffs(same) - 1, lane = tid & 31;
-        int at = 0;
-        if (g >= 0 && lane == leader) at = atomicAdd(&bins[g], __popc(same));
-        at = __shfl_sync(0xffffffffu, at, leader);
-        if (g >= 0) p.order[at + __popc(same & ((1u << lane) - 1))] = static_cast<int>(i);
-    }
+        const int leader = __ffs(same) - 1;
+        int first = 0;
+        if (g >= 0 && lane == leader) first = atomicAdd(&bins[g], __popc(same));
+        first = __shfl_sync(0xffffffffu, first, leader);
+        if (g >= 0) p.order[first + __popc(same & ((1u << lane) - 1))] = static_cast<int>(at);
+    };
+#pragma unroll
+    for (int i = 0; i < kSortKeep; ++i)
+        if (i * kSortThreads < p.T) place(i * kSortThreads + tid, kept[i]);
+    for (int64_t base = kSortKeep * kSortThreads; base < p.T; base += kSortThreads)
+        place(base + tid, base + tid < p.T ? p.ids[base + tid] : 0);
 }
 
-// Tile `index` of the batch and its tokens in `tok` (shared memory). False if there is
-// no such tile. Called by a whole block; inline tiles are worked out from the ids: a
-// token is first of a tile if no token before it has its adapter, and tiles stand
-// in the order of their first tokens.
-template <bool INLINE>
+// Tile `index` of a batch of up to kInline tokens, and its tokens in `tok` (shared memory).
+// False if there is no such tile. Called by a whole block. A token is first of a tile if
+// no token before it has its adapter, and tiles stand in the order of their first tokens.
 __device__ __forceinline__ bool find_tile(const LoraParams &p, int index, Tile &tile, int *tok, int *ids, int *found)
 {
     const int tid = threadIdx.x;
-    if constexpr (INLINE) {
-        if (tid < kInline) ids[tid] = tid < p.T ? adapter_of(p.ids[tid], p.L) : -1;
-        if (tid == 0) found[0] = -1;
-        __syncthreads();
-        if (tid < 32) {
-            int tiles = 0;
-            for (int base = 0; base < p.T; base += 32) {
-                const int i = base + tid, g = i < p.T ? ids[i] : -1;
-                bool first = g >= 0 && !(g == p.L && !p.copy);
-                for (int k = 0; k < i && first; ++k) first = ids[k] != g;
-                const unsigned m = __ballot_sync(0xffffffffu, first);
-                if (first && tiles + __popc(m & ((1u << tid) - 1)) == index) found[0] = g;
-                tiles += __popc(m);
-            }
+    if (tid < kInline) ids[tid] = tid < p.T ? adapter_of(p.ids[tid], p.L) : -1;
+    if (tid == 0) found[0] = -1;
+    __syncthreads();
+    if (tid < 32) {
+        int tiles = 0;
+        for (int base = 0; base < p.T; base += 32) {
+            const int i = base + tid, g = i < p.T ? ids[i] : -1;
+            bool first = g >= 0 && !(g == p.L && !p.copy);
+            for (int k = 0; k < i && first; ++k) first = ids[k] != g;
+            const unsigned m = __ballot_sync(0xffffffffu, first);
+            if (first && tiles + __popc(m & ((1u << tid) - 1)) == index) found[0] = g;
+            tiles += __popc(m);
         }
-        __syncthreads();
-        const int g = found[0];
-        if (g < 0) return false;
-        const bool in = tid < kInline && ids[tid] == g;
-        int at = 0;
-        if (in) {
-            for (int k = 0; k < tid; ++k) at += ids[k] == g;
-            tok[at] = tid;
-        }
-        const int n = __syncthreads_count(in);
-        tile = Tile{g, 0, n};
-        return true;
-    } else {
-        if (index >= *p.num_tiles) return false;
-        const int4 r = p.tiles[index];
-        tile = Tile{r.x, r.y, r.z};
-        if (tid < r.z) tok[tid] = p.order[r.y + tid];
-        __syncthreads();
-        return true;
     }
+    __syncthreads();
+    const int g = found[0];
+    if (g < 0) return false;
+    const bool in = tid < kInline && ids[tid] == g;
+    if (in) {
+        int at = 0;
+        for (int k = 0; k < tid; ++k) at += ids[k] == g;
+        tok[at] = tid;
+    }
+    const int n = __syncthreads_count(in);
+    tile = Tile{g, 0, n};
+    return true;
 }
 
 __device__ __forceinline__ int rank_of(const LoraParams &p, int a)
@@ -253,7 +267,7 @@ __device__ __forceinline__ void shrink_steps(const LoraParams &p, const uint16_t
 // Shared memory of the warps' sums, for the most tokens a tile of a batch can have.
 constexpr size_t shrink_smem(int T)
 {
-    return sizeof(float) * kWarps * (T <= 8 ? 8 : (T <= 16 ? 16 : (T <= 32 ? 32 : kTile))) * (kRanks + 1);
+    return sizeof(float) * kWarps * (T <= 8 ? 8 : (T <= 16 ? 16 : (T <= 32 ? 32 : kInline))) * (kRanks + 1);
 }
 
 template <int MT>
@@ -270,16 +284,15 @@ __device__ __forceinline__ void shrink_tile(const LoraParams &p, const uint16_t 
         shrink_steps<MT, 8>(p, a, rows, tok, count, kb, ke, red);
 }
 
-// Grid: tiles x splits of K x blocks of 64 ranks.
-template <bool INLINE>
-__global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const LoraParams p)
+// Up to kInline tokens. Grid: tiles x splits of K x blocks of 64 ranks.
+__global__ void __launch_bounds__(kThreads) lora_shrink_few_kernel(const LoraParams p)
 {
     extern __shared__ float red[];
-    __shared__ int tok[kTile], ids[kInline], found[1];
+    __shared__ int tok[kInline], ids[kInline], found[1];
     grid_dependency_wait();
     grid_launch_dependents();
     Tile tile;
-    if (!find_tile<INLINE>(p, blockIdx.x, tile, tok, ids, found) || tile.adapter == p.L) return;
+    if (!find_tile(p, blockIdx.x, tile, tok, ids, found) || tile.adapter == p.L) return;
     // the adapter's ranks of this block; those it lacks are zeros
     const int rows = rank_of(p, tile.adapter) - blockIdx.z * kRanks;
     if (rows <= 0) return;                       // nobody reads sums beyond the rank
@@ -293,6 +306,182 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const LoraParams 
         shrink_tile<2>(p, a, rows, tok, tile.count, kb, ke, red);
     else
         shrink_tile<4>(p, a, rows, tok, tile.count, kb, ke, red);
+}
+
+// More than kInline tokens, on the tensor core. Grid: tiles x splits of K x blocks of 128
+// ranks. A stage is 64 elements of K: the adapter's rows (as many as it has, up to 128; the
+// MMA takes 128, and what its further rows read is whatever follows) and 128 token rows,
+// both in the 128-byte swizzle. Warps:
+//   0-3  gather token rows by cp.async; then store the sums, a rank a lane
+//   4    lane 0 loads the adapter's rows by TMA
+//   5    issues the MMAs (an elected lane); owns TMEM
+constexpr int kLongThreads = 192;
+constexpr int kLongStages = 8;
+constexpr uint32_t kLongTokens = kTile * 128;
+constexpr uint32_t kLongSmem = 112 * 1024;       // two blocks an SM
+
+struct LongParams {
+    CUtensorMap tm_a;                // A as [L * R, K] bf16, box 64 elements x `rows`
+    LoraParams l;
+    int rows, stages;                // rows of a box; stages of the ring
+    uint64_t wait_ns;
+};
+
+struct LongShared {
+    uint64_t a_full[kLongStages], x_full[kLongStages], empty[kLongStages];
+    uint64_t done;
+    uint32_t tmem;
+    int tok[kTile];
+};
+
+// kind::f16: bf16 operands, both K-major, sums in fp32.
+__host__ __device__ constexpr uint32_t idesc_bf16(int n, int m)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_tc_bf16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// 16 bytes from global to shared memory, of which the first `bytes` are copied and the others zeros.
+__device__ __forceinline__ void cp_async_or_zero(uint32_t smem_dst, const void *gsrc, uint32_t bytes)
+{
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(smem_dst), "l"(gsrc), "r"(bytes) : "memory");
+}
+
+__global__ void __launch_bounds__(kLongThreads, 2) lora_shrink_long_kernel(const __grid_constant__ LongParams lp)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const LoraParams &p = lp.l;
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int S = lp.stages;
+    const uint32_t a_bytes = lp.rows * 128u, stage_bytes = a_bytes + kLongTokens;
+    LongShared &sh = *reinterpret_cast<LongShared *>(smem + S * stage_bytes);
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&sh.a_full[i], 1);
+            mbar_init(&sh.x_full[i], 128);
+            mbar_init(&sh.empty[i], 1);
+        }
+        mbar_init(&sh.done, 1);
+        fence_mbar_init();
+        tma_prefetch_desc(&lp.tm_a);
+    }
+    grid_dependency_wait();
+    grid_launch_dependents();
+    // whole blocks leave here, before TMEM is theirs
+    const int4 rec = __ldcg(p.tiles + blockIdx.x);
+    const int adapter = rec.x, count = rec.z, rank0 = blockIdx.z * kTile;
+    if (adapter == p.L || rank_of(p, adapter) <= rank0) return;       // nobody reads sums beyond the rank
+    const int per = (p.K + 64 * p.splits - 1) / (64 * p.splits) * 64;
+    const int kb = static_cast<int>(min(static_cast<int64_t>(blockIdx.y) * per, static_cast<int64_t>(p.K)));
+    const int ke = static_cast<int>(min(static_cast<int64_t>(kb) + per, static_cast<int64_t>(p.K)));
+    const int steps = (ke - kb + 63) / 64;
+    if (warp == 5) {
+        tmem_alloc(&sh.tmem, kTile);
+        tmem_relinquish();
+    }
+    if (tid < count) sh.tok[tid] = __ldcg(p.order + rec.y + tid);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
+    const int n = (count + 15) & ~15;
+
+    if (warp == 4) {
+        if (lane == 0) {
+            const uint64_t pol = policy_evict_last();        // other tiles of the adapter read the same rows
+            bool ok = true;
+            int i = 0;
+            for (; i < steps; ++i) {
+                const int s = i % S;
+                ok = mbar_wait(&sh.empty[s], ((i / S) & 1) ^ 1u, &g_lora_error, kErrWaitEmpty, lp.wait_ns);
+                if (!ok) break;
+                mbar_arrive_expect_tx(&sh.a_full[s], a_bytes);
+                tma_load_2d(smem + s * stage_bytes, &lp.tm_a, kb + 64 * i, adapter * p.R + rank0, &sh.a_full[s], pol);
+            }
+            // copies in flight land before the block leaves
+            for (int j = max(0, i - S); j < i; ++j)
+                mbar_wait(&sh.a_full[j % S], (j / S) & 1, &g_lora_error, kErrWaitDrain);
+        }
+    } else if (warp == 5) {
+        const uint32_t idesc = idesc_bf16(n, 128);
+        bool ok = true;
+        for (int i = 0; i < steps; ++i) {
+            const int s = i % S;
+            ok = mbar_wait_warp(&sh.a_full[s], (i / S) & 1, &g_lora_error, kErrWaitFull, lp.wait_ns) &&
+                 mbar_wait_warp(&sh.x_full[s], (i / S) & 1, &g_lora_error, kErrWaitOperand, lp.wait_ns);
+            if (!ok) break;
+            fence_proxy_async_smem();        // cp.async wrote through the generic proxy
+            tc_fence_after();
+            const uint64_t ad = sdesc_sw128(smem_u32(smem + s * stage_bytes));
+            const uint64_t bd = sdesc_sw128(smem_u32(smem + s * stage_bytes + a_bytes));
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mma_tc_bf16(tmem, ad + 2 * k, bd + 2 * k, idesc, i > 0 || k > 0 ? 1u : 0u);
+                tc_commit(&sh.empty[s]);
+            }
+            __syncwarp();
+        }
+        // the sums are complete, or nothing of this thread runs any more; phase 0 of `done`, whichever
+        if (elect_one()) tc_commit(&sh.done);
+        __syncwarp();
+    } else {
+        // column tid % 8 of rows tid / 8 + 16 j
+        const int c = tid & 7, r0 = tid >> 3;
+        const uint16_t *src[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            src[j] = r0 + 16 * j < count ? p.x + static_cast<int64_t>(sh.tok[r0 + 16 * j]) * p.ldx : nullptr;
+        const uint32_t dst = smem_u32(smem) + a_bytes + r0 * 128 + ((c ^ (r0 & 7)) << 4);
+        bool ok = true;
+        int i = 0;
+        for (; i < steps; ++i) {
+            const int s = i % S;
+            ok = mbar_wait_warp(&sh.empty[s], ((i / S) & 1) ^ 1u, &g_lora_error, kErrWaitEmpty, lp.wait_ns);
+            if (!ok) break;
+            const int k = kb + 64 * i + 8 * c;
+            const bool in = k < p.K;             // beyond the end both operands are zeros
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (src[j]) cp_async_or_zero(dst + s * stage_bytes + j * 2048, src[j] + (in ? k : 0), in ? 16u : 0u);
+            cp_async_arrive(&sh.x_full[s]);
+        }
+        cp_async_wait_all();
+        // nobody else waits for the arrivals of the last MMAs
+        for (int j = max(0, i - S); j < i && ok; ++j)
+            ok = mbar_wait_warp(&sh.empty[j % S], (j / S) & 1, &g_lora_error, kErrWaitDrain);
+        const bool done = mbar_wait_warp(&sh.done, 0, &g_lora_error, kErrWaitAccum);
+        tc_fence_after();
+        const int r = 32 * warp + lane;
+        if (ok && done && rank0 + 32 * warp < p.R) {
+            for (int c0 = 0; c0 < count; c0 += 32) {
+                uint32_t v[32];
+                tmem_ld32(tmem + c0 + (static_cast<uint32_t>(warp * 32) << 16), v);
+                tmem_ld_wait();
+                if (rank0 + r < p.R) {
+                    float *u = p.u + static_cast<int64_t>(blockIdx.y) * p.T * p.R + rank0 + r;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (c0 + j < count) u[static_cast<int64_t>(sh.tok[c0 + j]) * p.R] = steps ? __uint_as_float(v[j]) : 0.0f;
+                }
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 5) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTile);
+    }
 }
 
 // ----------------------------------------------------------------- expand
@@ -329,30 +518,34 @@ __device__ __forceinline__ uint4 keep_first(uint4 v, int n)
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// Columns 32c .. 32c + 31 of C for the 16 tokens 16m ...: channel of column `col` of the
+// Columns 32c .. 32c + 31 of C for the tokens 16m .. 16 (m + MG) - 1: channel of column `col` of the
 // n-tile j is 32c + 8 (col / 2) + 2j + (col & 1), so lane (g, q) ends with channels 8q .. 8q + 7 of
-// tokens g and g + 8.
-template <bool F16>
+// tokens g and g + 8 of each 16.
+template <bool F16, int MG>
 __device__ __forceinline__ void expand_block(const LoraParams &p, const uint16_t *b, int rank, const uint32_t *hi,
                                              const uint32_t *lo, int ldu, const int *tok, int count, int m, int c)
 {
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    float d[4][4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) d[j][i] = 0.0f;
+    float d[MG][4][4];
     const int n = 32 * c + 8 * q;            // this lane's channels of C
     const bool in = n < p.N;
-    int64_t row[2];
-    uint4 base[2];
+    int64_t row[MG][2];
+    uint4 base[MG][2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int t = 16 * m + 8 * h + g;
-        row[h] = t < count ? tok[t] : -1;
-        base[h] = make_uint4(0, 0, 0, 0);
-        if (in && row[h] >= 0) base[h] = *reinterpret_cast<const uint4 *>(p.base + row[h] * p.ldb + n);
-    }
+    for (int i = 0; i < MG; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int t = 16 * (m + i) + 8 * h + g;
+            row[i][h] = in && t < count ? tok[t] : -1;
+            base[i][h] = make_uint4(0, 0, 0, 0);
+            if (row[i][h] >= 0) base[i][h] = *reinterpret_cast<const uint4 *>(p.base + row[i][h] * p.ldb + n);
+        }
+#pragma unroll
+    for (int i = 0; i < MG; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d[i][j][e] = 0.0f;
     for (int k0 = 0; k0 < rank; k0 += 32) {
         const int k = k0 + 8 * q;
         uint4 w[4];
@@ -360,72 +553,125 @@ __device__ __forceinline__ void expand_block(const LoraParams &p, const uint16_t
         for (int j = 0; j < 4; ++j) {
             const int ch = 32 * c + 8 * (g >> 1) + 2 * j + (g & 1);
             w[j] = make_uint4(0, 0, 0, 0);
-            if (k < rank && ch < p.N)
-                w[j] = keep_first(__ldg(reinterpret_cast<const uint4 *>(b + static_cast<int64_t>(ch) * p.R + k)), rank - k);
+            if (k < rank && ch < p.N) w[j] = __ldg(reinterpret_cast<const uint4 *>(b + static_cast<int64_t>(ch) * p.R + k));
         }
-        // two words of hi / lo hold four k of a token
+        if (k0 + 32 > rank)
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int at = (16 * m + g) * ldu + (k >> 1) + 2 * s;
-            const uint2 h0 = *reinterpret_cast<const uint2 *>(hi + at), h1 = *reinterpret_cast<const uint2 *>(hi + at + 8 * ldu);
-            const uint2 l0 = *reinterpret_cast<const uint2 *>(lo + at), l1 = *reinterpret_cast<const uint2 *>(lo + at + 8 * ldu);
+            for (int j = 0; j < 4; ++j) w[j] = keep_first(w[j], rank - k);
+#pragma unroll
+        for (int i = 0; i < MG; ++i)
+            // two words of hi / lo hold four k of a token
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int at = (16 * (m + i) + g) * ldu + (k >> 1) + 2 * s;
+                const uint2 h0 = *reinterpret_cast<const uint2 *>(hi + at), h1 = *reinterpret_cast<const uint2 *>(hi + at + 8 * ldu);
+                const uint2 l0 = *reinterpret_cast<const uint2 *>(lo + at), l1 = *reinterpret_cast<const uint2 *>(lo + at + 8 * ldu);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t b0 = s ? w[j].z : w[j].x, b1 = s ? w[j].w : w[j].y;
+                    mma_bf16(d[i][j], l0.x, l1.x, l0.y, l1.y, b0, b1);
+                    mma_bf16(d[i][j], h0.x, h1.x, h0.y, h1.y, b0, b1);
+                }
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < MG; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (row[i][h] < 0) continue;
+            const uint32_t v[4] = {base[i][h].x, base[i][h].y, base[i][h].z, base[i][h].w};
+            uint32_t o[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const uint32_t b0 = s ? w[j].z : w[j].x, b1 = s ? w[j].w : w[j].y;
-                mma_bf16(d[j], l0.x, l1.x, l0.y, l1.y, b0, b1);
-                mma_bf16(d[j], h0.x, h1.x, h0.y, h1.y, b0, b1);
+                const float2 f = unpack2<F16>(v[j]);
+                o[j] = pack2<F16>(f.x + d[i][j][2 * h], f.y + d[i][j][2 * h + 1]);
             }
+            *reinterpret_cast<uint4 *>(p.c + row[i][h] * p.ldc + n) = make_uint4(o[0], o[1], o[2], o[3]);
         }
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        if (!in || row[h] < 0) continue;
-        const uint32_t v[4] = {base[h].x, base[h].y, base[h].z, base[h].w};
-        uint32_t o[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 f = unpack2<F16>(v[j]);
-            o[j] = pack2<F16>(f.x + d[j][2 * h], f.y + d[j][2 * h + 1]);
-        }
-        *reinterpret_cast<uint4 *>(p.c + row[h] * p.ldc + n) = make_uint4(o[0], o[1], o[2], o[3]);
-    }
 }
 
-// Grid: tiles x blocks of channels. Shared memory: the tile's u as high and low bf16,
-// [64 tokens][ranks rounded up to 32, and 8 more against conflicts].
+__device__ __forceinline__ void prefetch_l2(const void *p)
+{
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
+// Grid: halves of tiles (up to kInline tokens: tiles) x blocks of channels. Shared memory: u as
+// high and low bf16, [64 tokens][ranks rounded up to 32, and 8 more against conflicts].
 template <bool INLINE, bool F16>
 __global__ void __launch_bounds__(kThreads) lora_expand_kernel(const LoraParams p)
 {
     extern __shared__ uint32_t ushared[];
-    __shared__ int tok[kTile], ids[kInline], found[1];
-    grid_dependency_wait();
-    grid_launch_dependents();
+    __shared__ int tok[kHalf], ids[kInline], found[1];
+    const int chunks = (p.N + 31) / 32, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     Tile tile;
-    if (!find_tile<INLINE>(p, blockIdx.x, tile, tok, ids, found)) return;
-    const int chunks = (p.N + 31) / 32;
+    // The launch before let this one start when everything before it had completed: all but u
+    // is there.
+    if constexpr (INLINE) {
+        if (!find_tile(p, blockIdx.x, tile, tok, ids, found)) {
+            grid_dependency_wait();
+            return;
+        }
+    } else {
+        const int4 r = p.tiles[blockIdx.x >> 1];
+        const int skip = (blockIdx.x & 1) * kHalf;
+        if (r.z <= skip) {
+            grid_dependency_wait();
+            return;
+        }
+        tile = Tile{r.x, r.y + skip, min(kHalf, r.z - skip)};
+        if (threadIdx.x < tile.count) tok[threadIdx.x] = p.order[tile.first + threadIdx.x];
+        __syncthreads();
+    }
     if (tile.adapter == p.L) {
         // no adapter: a copy of base, as it is
-        const int vectors = p.N / 8, total = gridDim.y * kThreads;
-        for (int t = 0; t < tile.count; ++t) {
-            const uint4 *s = reinterpret_cast<const uint4 *>(p.base + tok[t] * p.ldb);
-            uint4 *o = reinterpret_cast<uint4 *>(p.c + tok[t] * p.ldc);
-            for (int64_t i = blockIdx.y * kThreads + threadIdx.x; i < vectors; i += total) o[i] = s[i];
-        }
+        grid_dependency_wait();
+        grid_launch_dependents();
+        const uint32_t vectors = p.N / 8, total = gridDim.y * kThreads;
+        for (uint32_t i = blockIdx.y * kThreads + threadIdx.x; i < vectors; i += total)
+            for (int t0 = 0; t0 < tile.count; t0 += 8) {
+                uint4 v[8];
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+                    if (t0 + t < tile.count) v[t] = reinterpret_cast<const uint4 *>(p.base + tok[t0 + t] * p.ldb)[i];
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+                    if (t0 + t < tile.count) reinterpret_cast<uint4 *>(p.c + tok[t0 + t] * p.ldc)[i] = v[t];
+            }
         return;
     }
     const int rank = rank_of(p, tile.adapter);
-    const int rows = (tile.count + 15) / 16 * 16, cols = (rank + 31) / 32 * 32, ldu = ((p.R + 31) / 32 * 32 + 8) / 2;
-    uint32_t *hi = ushared, *lo = ushared + kTile * ldu;
+    const uint16_t *b = p.b + static_cast<int64_t>(tile.adapter) * p.N * p.R;
+    const int mt = (tile.count + 15) / 16, rows = mt * 16, cols = (rank + 31) / 32 * 32;
+    const int ldu = ((p.R + 31) / 32 * 32 + 8) / 2;
+    const int c0 = blockIdx.y * kWarps + warp, step = gridDim.y * kWarps;
+    // this warp's first channels go to L2 while u is made
+    if (c0 < chunks) {
+        const int ch = 32 * c0 + lane;
+        if (ch < p.N)
+            for (int k = 0; k < rank; k += 64) prefetch_l2(b + static_cast<int64_t>(ch) * p.R + k);
+        for (int t = lane; t < tile.count; t += 32) prefetch_l2(p.base + tok[t] * p.ldb + 32 * c0);
+    }
     const float scale = p.scales ? p.scales[tile.adapter] : 1.0f;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    uint32_t *hi = ushared, *lo = ushared + kHalf * ldu;
     for (int i = threadIdx.x; i < rows * (cols / 2); i += kThreads) {
         const int t = i / (cols / 2), r = 2 * (i - t * (cols / 2));
         float2 v = make_float2(0.0f, 0.0f);
         if (t < tile.count && r < rank) {
             const float *u = p.u + static_cast<int64_t>(tok[t]) * p.R + r;
-            for (int s = 0; s < p.splits; ++s) {
-                const float2 part = __ldcg(reinterpret_cast<const float2 *>(u + static_cast<int64_t>(s) * p.T * p.R));
-                v.x += part.x;
-                v.y += part.y;
+            for (int s0 = 0; s0 < p.splits; s0 += 8) {
+                float2 part[8];
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    part[s] = s0 + s < p.splits
+                                  ? __ldcg(reinterpret_cast<const float2 *>(u + static_cast<int64_t>(s0 + s) * p.T * p.R))
+                                  : make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+                    v.x += part[s].x;
+                    v.y += part[s].y;
+                }
             }
             v.x *= scale;
             v.y = r + 1 < rank ? v.y * scale : 0.0f;
@@ -439,14 +685,17 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(const LoraParams 
         lo[t * ldu + r / 2] = *reinterpret_cast<const uint32_t *>(&l);
     }
     __syncthreads();
-    const uint16_t *b = p.b + static_cast<int64_t>(tile.adapter) * p.N * p.R;
-    const int mt = rows / 16, step = gridDim.y * kWarps;
-    for (int64_t i = blockIdx.y * kWarps + (threadIdx.x >> 5); i < static_cast<int64_t>(chunks) * mt; i += step)
-        expand_block<F16>(p, b, rank, hi, lo, ldu, tok, tile.count, static_cast<int>(i % mt), static_cast<int>(i / mt));
+    for (int c = c0; c < chunks; c += step)
+        for (int m = 0; m < mt; m += 2) {
+            if (m + 1 < mt)
+                expand_block<F16, 2>(p, b, rank, hi, lo, ldu, tok, tile.count, m, c);
+            else
+                expand_block<F16, 1>(p, b, rank, hi, lo, ldu, tok, tile.count, m, c);
+        }
 }
 
-template <typename Kern>
-cudaError_t launch(Kern kern, dim3 grid, int threads, size_t smem, cudaStream_t stream, const LoraParams &p)
+template <typename Kern, typename P>
+cudaError_t launch(Kern kern, dim3 grid, int threads, size_t smem, cudaStream_t stream, const P &p)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -462,55 +711,84 @@ cudaError_t launch(Kern kern, dim3 grid, int threads, size_t smem, cudaStream_t 
 }
 
 template <bool INLINE, bool F16>
-cudaError_t launch_products(const LoraParams &p, const LoraLayout &l, cudaStream_t stream)
+cudaError_t launch_expand(const LoraParams &p, const LoraLayout &l, cudaStream_t stream)
 {
-    static KernelOnce shrink_once, expand_once;
-    cudaError_t e = prepare_kernel(lora_shrink_kernel<INLINE>, shrink_smem(kTile), shrink_once, nullptr);
-    if (e != cudaSuccess) return e;
-    const size_t expand_smem = sizeof(uint32_t) * 2 * kTile * (((p.R + 31) / 32 * 32 + 8) / 2);
-    constexpr size_t most = sizeof(uint32_t) * 2 * kTile * ((kMaxRank + 8) / 2);
+    static KernelOnce once;
+    constexpr size_t most = sizeof(uint32_t) * 2 * kHalf * ((kMaxRank + 8) / 2);
     int sms = 0;
-    e = prepare_kernel(lora_expand_kernel<INLINE, F16>, most, expand_once, &sms);
+    const cudaError_t e = prepare_kernel(lora_expand_kernel<INLINE, F16>, most, once, &sms);
     if (e != cudaSuccess) return e;
-    e = launch(lora_shrink_kernel<INLINE>, dim3(l.max_tiles, l.splits, (p.R + kRanks - 1) / kRanks), kThreads,
-               shrink_smem(p.T), stream, p);
-    if (e != cudaSuccess) return e;
-    // blocks of channels: as many as give every SM two blocks, no more than one step a warp
-    const int items = (p.N + 31) / 32 * ((std::min(p.T, kTile) + 15) / 16);
-    const int blocks = std::max(1, std::min((items + kWarps - 1) / kWarps, (2 * sms + l.max_tiles - 1) / l.max_tiles));
-    return launch(lora_expand_kernel<INLINE, F16>, dim3(l.max_tiles, blocks), kThreads, expand_smem, stream, p);
+    const size_t smem = sizeof(uint32_t) * 2 * kHalf * (((p.R + 31) / 32 * 32 + 8) / 2);
+    // blocks of channels: as many as give every SM two blocks, no more than one chunk a warp. How
+    // many halves of tiles there are the GPU alone knows: an adapter leaves one half empty on average
+    const int tiles = INLINE ? l.max_tiles : 2 * l.max_tiles, chunks = (p.N + 31) / 32;
+    const int full = INLINE ? tiles : std::min<int>(tiles, p.T / kHalf + (p.L + 1) / 2 + 1);
+    const int blocks = std::max(1, std::min((chunks + kWarps - 1) / kWarps, 2 * sms / full));
+    return launch(lora_expand_kernel<INLINE, F16>, dim3(tiles, blocks), kThreads, smem, stream, p);
 }
 
 }  // namespace
 
+// A tile is 128 tokens, but a block of a batch that works its tiles out itself has all of an adapter's.
 LoraLayout lora_layout(int64_t T, int64_t K, int R, int L)
 {
     LoraLayout l;
-    const int64_t full = (T + kTile - 1) / kTile;
-    // splits of K: two blocks an SM if all tokens shared one adapter, each with 512
-    // elements at least (one step of every warp)
-    l.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({304 / full, 32, (K + 511) / 512})));
     // every group of tokens wastes less than one tile
     l.max_tiles = static_cast<int>(std::min<int64_t>(T, T / kTile + L + 1));
+    // splits of K: two blocks an SM, each with 512 elements at least (one step of every warp, or
+    // eight stages)
+    const int64_t tiles = T <= kInline ? (T + kInline - 1) / kInline : l.max_tiles;
+    l.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({304 / tiles, 32, (K + 511) / 512})));
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
-    // splits * T is at most 32 T, and at most 304 / (T / 64) * T or T: a bound that grows with T
+    // splits * T is at most 32 T, and at most 304 / (T / 128) * T or T: a bound that grows with T
     const int64_t most = std::min<int64_t>(32 * T, std::max<int64_t>(304 * kTile, T));
     l.u = 0;
     l.order = l.u + up(sizeof(float) * static_cast<size_t>(most) * R);
     l.tiles = l.order + up(sizeof(int) * static_cast<size_t>(T));
-    l.count = l.tiles + up(sizeof(int4) * static_cast<size_t>(l.max_tiles));
-    l.total = l.count + 256;
+    l.total = l.tiles + up(sizeof(int4) * static_cast<size_t>(l.max_tiles));
     return l;
 }
 
 cudaError_t launch_lora(LoraParams p, const LoraLayout &l, bool f16, cudaStream_t stream)
 {
     p.splits = l.splits;
-    if (p.T <= kInline)
-        return f16 ? launch_products<true, true>(p, l, stream) : launch_products<true, false>(p, l, stream);
-    cudaError_t e = launch(lora_sort_kernel, dim3(1), kSortThreads, sizeof(int) * (p.L + 1), stream, p);
+    p.max_tiles = l.max_tiles;
+    cudaError_t e;
+    if (p.T <= kInline) {
+        static KernelOnce once;
+        e = prepare_kernel(lora_shrink_few_kernel, shrink_smem(kInline), once, nullptr);
+        if (e != cudaSuccess) return e;
+        e = launch(lora_shrink_few_kernel, dim3(l.max_tiles, l.splits, (p.R + kRanks - 1) / kRanks), kThreads,
+                   shrink_smem(p.T), stream, p);
+        if (e != cudaSuccess) return e;
+        return f16 ? launch_expand<true, true>(p, l, stream) : launch_expand<true, false>(p, l, stream);
+    }
+    e = launch(lora_sort_kernel, dim3(1), kSortThreads, sizeof(int) * (p.L + 1), stream, p);
     if (e != cudaSuccess) return e;
-    return f16 ? launch_products<false, true>(p, l, stream) : launch_products<false, false>(p, l, stream);
+    static KernelOnce once;
+    e = prepare_kernel(lora_shrink_long_kernel, kLongSmem, once, nullptr);
+    if (e != cudaSuccess) return e;
+    LongParams lp;
+    lp.l = p;
+    lp.rows = std::min(p.R, kTile);
+    lp.stages = std::min<int>(kLongStages, (kLongSmem - 1024 - sizeof(LongShared)) / (lp.rows * 128 + kLongTokens));
+    lp.wait_ns = wait_limit_ns();
+    if (!encode_map_2d(&lp.tm_a, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.a, p.K, static_cast<uint64_t>(p.L) * p.R,
+                       static_cast<uint64_t>(p.K) * 2, 64u, lp.rows, CU_TENSOR_MAP_SWIZZLE_128B,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
+        return cudaErrorInvalidValue;
+    e = launch(lora_shrink_long_kernel, dim3(l.max_tiles, l.splits, (p.R + kTile - 1) / kTile), kLongThreads, kLongSmem,
+               stream, lp);
+    if (e != cudaSuccess) return e;
+    return f16 ? launch_expand<false, true>(p, l, stream) : launch_expand<false, false>(p, l, stream);
+}
+
+int read_and_clear_lora_error()
+{
+    int v = 0, zero = 0;
+    if (cudaMemcpyFromSymbol(&v, g_lora_error, sizeof(int)) != cudaSuccess) return -1;
+    cudaMemcpyToSymbol(g_lora_error, &zero, sizeof(int));
+    return v;
 }
 
 }  // namespace mxfp4

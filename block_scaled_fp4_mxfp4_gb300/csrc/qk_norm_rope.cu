@@ -6,13 +6,15 @@
 //   out_i = r (x_i a_i + x_j b_i),  a_i = w_i cos, b_i = -+ w_j sin,
 // (a = w, b = 0 where nothing turns), and a, b are the same for all heads of a token.
 //
-// Bound: HBM (2 bytes read, 2 written an element). A head is one 16-byte vector for
-// each of LPH lanes, read once and kept in registers between the sum of squares and
-// the rotation; the partner's vector in the layout of halves comes by shuffles of
-// packed registers. A group of LPH lanes takes U heads of one token, all loads
-// ahead, and forms a, b once for them.
+// Bound: HBM (2 bytes read, 2 written an element). A lane has two 16-byte vectors of a
+// head: in the layout of halves the two whose elements turn with each other, so that
+// nothing but the sum of squares crosses lanes. A group of LPH lanes has a head, a warp
+// the heads of one token, which share a and b; U of a group's heads are on their way at a
+// time. Arithmetic in pairs of floats (mul and fma of f32x2: one issue for two).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <algorithm>
 
 #include "internal.h"
 #include "layer.h"
@@ -58,6 +60,62 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8])
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
+// Two floats in a register pair, and operations on both at once.
+struct Pair {
+    uint64_t v;
+};
+__device__ __forceinline__ Pair pair(float x, float y)
+{
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(x), "f"(y));
+    return p;
+}
+__device__ __forceinline__ float2 floats(Pair p)
+{
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p.v));
+    return f;
+}
+__device__ __forceinline__ Pair mul(Pair a, Pair b)
+{
+    Pair d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+    return d;
+}
+__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c)
+{
+    Pair d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return d;
+}
+
+// A vector of eight as four pairs.
+struct Vec {
+    Pair p[4];
+};
+template <bool F16>
+__device__ __forceinline__ Vec unpack(const uint4 &v)
+{
+    float f[8];
+    unpack8<F16>(v, f);
+    Vec o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o.p[i] = pair(f[2 * i], f[2 * i + 1]);
+    return o;
+}
+template <bool F16>
+__device__ __forceinline__ uint4 pack(const Vec &v)
+{
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 t = floats(v.p[i]);
+        f[2 * i] = t.x;
+        f[2 * i + 1] = t.y;
+    }
+    return pack8<F16>(f);
+}
+
 template <int LPH>
 __device__ __forceinline__ float group_sum(float v)
 {
@@ -66,166 +124,200 @@ __device__ __forceinline__ float group_sum(float v)
     return v;
 }
 
-// r for a head whose squares leave fp32, or whose sum is so small that it lost bits
-// and eps does not hide it: the values are brought to about 1 by a power of two
-// first (exact), and x and its partner are left scaled by it.
+// r for heads whose squares leave fp32, or whose sum is so small that it lost bits and
+// eps does not hide it (`odd`): the values are brought to about 1 by a power of two
+// first (exact), and are left scaled by it.
 template <int LPH>
-__device__ __noinline__ float rescaled_r(float (&x)[8], float (&xp)[8], bool odd, float eps, int D)
+__device__ __noinline__ float rescaled_r(Vec &x0, Vec &x1, bool odd, float eps, int D)
 {
     float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
+    for (int i = 0; i < 4; ++i) {
+        const float2 a = floats(x0.p[i]), b = floats(x1.p[i]);
+        top = fmaxf(fmaxf(top, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(b.x), fabsf(b.y)));
+    }
 #pragma unroll
     for (int o = LPH / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     float s = 1.0f;
     if (odd && top > 0.0f && !isinf(top)) s = exp2f(static_cast<float>(max(-126, min(126, -ilogbf(top)))));
+    const Pair s2 = pair(s, s);
     float ss = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        x[i] *= s;
-        xp[i] *= s;
-        ss = fmaf(x[i], x[i], ss);
+    for (int i = 0; i < 4; ++i) {
+        x0.p[i] = mul(x0.p[i], s2);
+        x1.p[i] = mul(x1.p[i], s2);
+        const float2 a = floats(x0.p[i]), b = floats(x1.p[i]);
+        ss = fmaf(a.x, a.x, fmaf(a.y, a.y, fmaf(b.x, b.x, fmaf(b.y, b.y, ss))));
     }
     ss = group_sum<LPH>(ss);
     const double m = static_cast<double>(ss) / D + static_cast<double>(eps) * s * s;
     return m == 0.0 ? 0.0f : static_cast<float>(1.0 / sqrt(m));
 }
 
+// Heads h0 .. h1 - 1 of one token's queries or keys (which: 0, 1).
 template <bool F16, bool INTER, int LPH, int U>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const QkParams p)
+__device__ __forceinline__ void heads_of(const QkParams &p, int which, int64_t t, int64_t pos, int h0, int h1, int j, int hv,
+                                         int v0, int v1, bool in0, bool in1)
 {
-    const int j = threadIdx.x & (LPH - 1);              // this lane's vector of a head
-    const int per_token = p.units[0] + p.units[1];
-    const int64_t total = p.T * per_token;
-    int64_t unit = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / LPH;
-    const bool live = unit < total;
-    if (!live) unit = total - 1;                        // a whole warp stays for the shuffles
-    const int64_t t = unit / per_token;
-    int c = static_cast<int>(unit - t * per_token);
-    const int is_k = c >= p.units[0];
-    if (is_k) c -= p.units[0];
-    const int h0 = c * U, heads = min(U, p.heads[is_k] - h0);
-    const bool mine = live && 8 * j < p.D;
-    const int half = p.rot >> 1;
-
-    grid_dependency_wait();
-    grid_launch_dependents();
-    const uint16_t *src = p.x[is_k] + t * p.st[is_k] + h0 * p.sh[is_k] + 8 * j;
-    uint4 raw[U];
+    constexpr int G = 32 / LPH;                         // heads a warp has side by side
+    const int group = (threadIdx.x & 31) / LPH;
+    // what an element is multiplied with (a), and what its partner is (b)
+    Vec a0, a1, b0, b1;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        raw[u] = make_uint4(0, 0, 0, 0);
-        if (mine && u < heads) raw[u] = *reinterpret_cast<const uint4 *>(src + u * p.sh[is_k]);
+    for (int i = 0; i < 4; ++i) {
+        a0.p[i] = a1.p[i] = pair(1.0f, 1.0f);
+        b0.p[i] = b1.p[i] = pair(0.0f, 0.0f);
     }
-
-    // partner lane of the layout of halves; lanes beyond the rotated part keep their own
-    const int hv = p.rot >> 4;                          // vectors of a half
-    const bool turned = 8 * j < p.rot;
-    const int group = (threadIdx.x & 31) & ~(LPH - 1);
-    const int partner = INTER || !turned ? j : (j < hv ? j + hv : j - hv);
-
-    float a[8], b[8];
     float bad = 0.0f;                                   // NaN for a position outside the table
-    {
-        const uint16_t *w = p.w[is_k];
-        float own[8], other[8];
+    if (p.rot) {
+        const float *row = p.table + pos * p.rot, *sines = row + (p.rot >> 1);
+        auto turn_pairs = [&](int v, Vec &a, Vec &b) {
+            const float4 cs = *reinterpret_cast<const float4 *>(row + 4 * v), sn = *reinterpret_cast<const float4 *>(sines + 4 * v);
+            a.p[0] = pair(cs.x, cs.x);
+            a.p[1] = pair(cs.y, cs.y);
+            a.p[2] = pair(cs.z, cs.z);
+            a.p[3] = pair(cs.w, cs.w);
+            b.p[0] = pair(-sn.x, sn.x);
+            b.p[1] = pair(-sn.y, sn.y);
+            b.p[2] = pair(-sn.z, sn.z);
+            b.p[3] = pair(-sn.w, sn.w);
+        };
+        if (pos < 0 || pos >= p.P) {
+            bad = __int_as_float(0x7FC00000);
+        } else if constexpr (INTER) {
+            if (in0 && 8 * v0 < p.rot) turn_pairs(v0, a0, b0);
+            if (in1 && 8 * v1 < p.rot) turn_pairs(v1, a1, b1);
+        } else if (j < hv) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) own[i] = other[i] = 1.0f;
-        if (w && mine) {
-            unpack8<F16>(*reinterpret_cast<const uint4 *>(w + 8 * j), own);
-            if constexpr (!INTER) unpack8<F16>(*reinterpret_cast<const uint4 *>(w + 8 * partner), other);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            a[i] = own[i];
-            b[i] = 0.0f;
-        }
-        if (p.rot) {
-            const int64_t pos = p.pos64 ? static_cast<const int64_t *>(p.positions)[t]
-                                        : static_cast<const int32_t *>(p.positions)[t];
-            const bool inside = pos >= 0 && pos < p.P;
-            if (!inside) bad = __int_as_float(0x7FC00000);
-            if (turned && inside) {
-                const float *row = p.table + pos * p.rot;
-                if constexpr (INTER) {
-                    const float4 cs = *reinterpret_cast<const float4 *>(row + 4 * j);
-                    const float4 sn = *reinterpret_cast<const float4 *>(row + half + 4 * j);
-                    const float cv[4] = {cs.x, cs.y, cs.z, cs.w}, sv[4] = {sn.x, sn.y, sn.z, sn.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        a[2 * i] = own[2 * i] * cv[i];
-                        b[2 * i] = -own[2 * i + 1] * sv[i];
-                        a[2 * i + 1] = own[2 * i + 1] * cv[i];
-                        b[2 * i + 1] = own[2 * i] * sv[i];
-                    }
-                } else {
-                    const int at = 8 * (j < hv ? j : j - hv);
-                    const float sign = j < hv ? -1.0f : 1.0f;
-#pragma unroll
-                    for (int i = 0; i < 8; i += 4) {
-                        const float4 cs = *reinterpret_cast<const float4 *>(row + at + i);
-                        const float4 sn = *reinterpret_cast<const float4 *>(row + half + at + i);
-                        const float cv[4] = {cs.x, cs.y, cs.z, cs.w}, sv[4] = {sn.x, sn.y, sn.z, sn.w};
-#pragma unroll
-                        for (int l = 0; l < 4; ++l) {
-                            a[i + l] = own[i + l] * cv[l];
-                            b[i + l] = sign * other[i + l] * sv[l];
-                        }
-                    }
-                }
+            for (int i = 0; i < 2; ++i) {
+                const float4 cs = *reinterpret_cast<const float4 *>(row + 8 * j + 4 * i);
+                const float4 sn = *reinterpret_cast<const float4 *>(sines + 8 * j + 4 * i);
+                a0.p[2 * i] = a1.p[2 * i] = pair(cs.x, cs.y);
+                a0.p[2 * i + 1] = a1.p[2 * i + 1] = pair(cs.z, cs.w);
+                b0.p[2 * i] = pair(-sn.x, -sn.y);
+                b0.p[2 * i + 1] = pair(-sn.z, -sn.w);
+                b1.p[2 * i] = pair(sn.x, sn.y);
+                b1.p[2 * i + 1] = pair(sn.z, sn.w);
             }
         }
     }
-
-    uint16_t *dst = p.out[is_k] + t * p.ost[is_k] + h0 * p.osh[is_k] + 8 * j;
-    const bool norm = p.w[is_k] != nullptr;
-    const float inv_d = 1.0f / static_cast<float>(p.D);
+    const uint16_t *w = p.w[which];
+    if (w) {
+        const Vec w0 = unpack<F16>(in0 ? *reinterpret_cast<const uint4 *>(w + 8 * v0) : make_uint4(0, 0, 0, 0));
+        const Vec w1 = unpack<F16>(in1 ? *reinterpret_cast<const uint4 *>(w + 8 * v1) : make_uint4(0, 0, 0, 0));
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        float x[8], xp[8];
-        unpack8<F16>(raw[u], x);
-        if constexpr (INTER) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) xp[i] = x[i ^ 1];
-        } else {
-            uint4 q;
-            q.x = __shfl_sync(0xffffffffu, raw[u].x, group + partner);
-            q.y = __shfl_sync(0xffffffffu, raw[u].y, group + partner);
-            q.z = __shfl_sync(0xffffffffu, raw[u].z, group + partner);
-            q.w = __shfl_sync(0xffffffffu, raw[u].w, group + partner);
-            unpack8<F16>(q, xp);
+        for (int i = 0; i < 4; ++i) {
+            a0.p[i] = mul(a0.p[i], w0.p[i]);
+            a1.p[i] = mul(a1.p[i], w1.p[i]);
+            if constexpr (INTER) {
+                const float2 f0 = floats(w0.p[i]), f1 = floats(w1.p[i]);
+                b0.p[i] = mul(b0.p[i], pair(f0.y, f0.x));
+                b1.p[i] = mul(b1.p[i], pair(f1.y, f1.x));
+            } else {
+                b0.p[i] = mul(b0.p[i], w1.p[i]);
+                b1.p[i] = mul(b1.p[i], w0.p[i]);
+            }
         }
-        float ss = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-        ss = group_sum<LPH>(ss);
-        float r = 1.0f;
-        // 1e36: the sum has not overflowed; 1e-24: squares below 2^-126 are less than 2^-24 of it
-        const bool odd = norm && u < heads && (!(ss < 1e36f) || (ss < 1e-24f && p.eps < 1e-20f));
-        if (norm) r = rsqrtf(fmaf(ss, inv_d, p.eps));
-        if (__any_sync(0xffffffffu, odd)) {
-            const float rr = rescaled_r<LPH>(x, xp, odd, p.eps, p.D);
-            if (odd) r = rr;
-        }
-        r += bad;
-        float o[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = r * fmaf(xp[i], b[i], x[i] * a[i]);
-        if (mine && u < heads) *reinterpret_cast<uint4 *>(dst + u * p.osh[is_k]) = pack8<F16>(o);
     }
+    const float inv_d = 1.0f / static_cast<float>(p.D);
+    const int64_t in_step = G * p.sh[which], out_step = G * p.osh[which];
+    const uint16_t *src = p.x[which] + t * p.st[which] + (h0 + group) * p.sh[which];
+    uint16_t *dst = p.out[which] + t * p.ost[which] + (h0 + group) * p.osh[which];
+    for (int h = h0; h < h1; h += G * U) {
+        uint4 raw[U][2];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            raw[u][0] = raw[u][1] = make_uint4(0, 0, 0, 0);
+            if (h + G * u + group < h1) {
+                if (in0) raw[u][0] = *reinterpret_cast<const uint4 *>(src + u * in_step + 8 * v0);
+                if (in1) raw[u][1] = *reinterpret_cast<const uint4 *>(src + u * in_step + 8 * v1);
+            }
+        }
+        src += U * in_step;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool live = h + G * u + group < h1;
+            Vec x0 = unpack<F16>(raw[u][0]), x1 = unpack<F16>(raw[u][1]);
+            float r = 1.0f;
+            if (w) {
+                Pair q = mul(x0.p[0], x0.p[0]);
+#pragma unroll
+                for (int i = 1; i < 4; ++i) q = fma(x0.p[i], x0.p[i], q);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q = fma(x1.p[i], x1.p[i], q);
+                const float2 f = floats(q);
+                const float ss = group_sum<LPH>(f.x + f.y);
+                r = rsqrtf(fmaf(ss, inv_d, p.eps));
+                // 1e36: the sum has not overflowed; 1e-24: squares below 2^-126 are less than 2^-24 of it
+                const bool odd = live && (!(ss < 1e36f) || (ss < 1e-24f && p.eps < 1e-20f));
+                if (__any_sync(0xffffffffu, odd)) {
+                    const float rr = rescaled_r<LPH>(x0, x1, odd, p.eps, p.D);
+                    if (odd) r = rr;
+                }
+            }
+            r += bad;
+            const Pair r2 = pair(r, r);
+            Vec o0, o1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                Pair y0 = x1.p[i], y1 = x0.p[i];
+                if constexpr (INTER) {
+                    const float2 f0 = floats(x0.p[i]), f1 = floats(x1.p[i]);
+                    y0 = pair(f0.y, f0.x);
+                    y1 = pair(f1.y, f1.x);
+                }
+                o0.p[i] = mul(fma(y0, b0.p[i], mul(x0.p[i], a0.p[i])), r2);
+                o1.p[i] = mul(fma(y1, b1.p[i], mul(x1.p[i], a1.p[i])), r2);
+            }
+            if (live) {
+                if (in0) *reinterpret_cast<uint4 *>(dst + u * out_step + 8 * v0) = pack<F16>(o0);
+                if (in1) *reinterpret_cast<uint4 *>(dst + u * out_step + 8 * v1) = pack<F16>(o1);
+            }
+        }
+        dst += U * out_step;
+    }
+}
+
+template <bool F16, bool INTER, int LPH, int U>
+__global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kernel(const QkParams p)
+{
+    const int j = threadIdx.x & (LPH - 1);
+    const uint32_t item = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const uint32_t t = item / p.units, unit = item - t * p.units;
+    if (t >= p.T) return;                               // whole warps
+    // heads of this warp, queries before keys
+    const int h0 = unit * p.unit_heads, h1 = min(p.heads[0] + p.heads[1], h0 + p.unit_heads);
+
+    // Vectors of this lane. Halves: those that turn with each other, and two of the rest for
+    // the lanes behind; pairs: any two.
+    const int nv = p.D >> 3, hv = INTER ? 0 : p.rot >> 4, half_rest = (nv - 2 * hv + 1) >> 1;
+    const bool in0 = j < hv + half_rest;
+    const int v0 = j < hv ? j : j + hv, v1 = v0 + (j < hv ? hv : half_rest);
+    const bool in1 = in0 && v1 < nv;
+
+    grid_dependency_wait();
+    grid_launch_dependents();
+    int64_t pos = 0;
+    if (p.rot) pos = p.pos64 ? static_cast<const int64_t *>(p.positions)[t] : static_cast<const int32_t *>(p.positions)[t];
+    const int hq = p.heads[0];
+    if (h0 < hq) heads_of<F16, INTER, LPH, U>(p, 0, t, pos, h0, min(h1, hq), j, hv, v0, v1, in0, in1);
+    if (h1 > hq) heads_of<F16, INTER, LPH, U>(p, 1, t, pos, max(h0, hq) - hq, h1 - hq, j, hv, v0, v1, in0, in1);
 }
 
 template <bool F16, bool INTER, int LPH>
 cudaError_t launch_lph(QkParams p, int num_sms, cudaStream_t stream)
 {
-    // four heads a lane group as soon as that still gives every SM a full set of threads
-    const int64_t vectors = p.T * (p.heads[0] + p.heads[1]) * LPH;
-    const bool many = vectors >= int64_t(4) * num_sms * 1024;
-    const int U = many ? 4 : 1;
-    for (int i = 0; i < 2; ++i) p.units[i] = (p.heads[i] + U - 1) / U;
-    const int64_t threads = p.T * (p.units[0] + p.units[1]) * LPH;
+    // A warp takes as many of a token's heads, two of a lane group at a time, as still leave
+    // six rounds of 24 warps an SM; below that one head a lane group.
+    constexpr int G = 32 / LPH;
+    const int heads = p.heads[0] + p.heads[1], all = (heads + G - 1) / G;
+    const int64_t each = p.T * all / (int64_t(num_sms) * 24 * 6);
+    const bool many = each >= 2;
+    p.unit_heads = G * static_cast<int>(many ? std::min<int64_t>(all, each) : 1);
+    p.units = (heads + p.unit_heads - 1) / p.unit_heads;
+    const int64_t items = p.T * p.units;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((threads + kThreads - 1) / kThreads));
+    cfg.gridDim = dim3(static_cast<unsigned>((items + kThreads / 32 - 1) / (kThreads / 32)));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -233,16 +325,16 @@ cudaError_t launch_lph(QkParams p, int num_sms, cudaStream_t stream)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (many) return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<F16, INTER, LPH, 4>, p);
+    if (many) return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<F16, INTER, LPH, 2>, p);
     return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<F16, INTER, LPH, 1>, p);
 }
 
 template <bool F16, bool INTER>
 cudaError_t launch_type(const QkParams &p, int num_sms, cudaStream_t stream)
 {
-    if (p.D <= 64) return launch_lph<F16, INTER, 8>(p, num_sms, stream);
-    if (p.D <= 128) return launch_lph<F16, INTER, 16>(p, num_sms, stream);
-    return launch_lph<F16, INTER, 32>(p, num_sms, stream);
+    if (p.D <= 64) return launch_lph<F16, INTER, 4>(p, num_sms, stream);
+    if (p.D <= 128) return launch_lph<F16, INTER, 8>(p, num_sms, stream);
+    return launch_lph<F16, INTER, 16>(p, num_sms, stream);
 }
 
 }  // namespace

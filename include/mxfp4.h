@@ -399,8 +399,8 @@ MXFP4_API mxfp4_status_t mxfp4_group_gemm_plan(const mxfp4_problem_t *problems, 
  * workspace before reusing it after a nonzero code. This call synchronizes
  * the current device. *code receives 0 when no kernel reported an error;
  * otherwise 1..15 (single-CTA GEMM), 16 + c (fused kernel), 32 + c
- * (CTA-pair GEMM), 48 + c (experts' products of mxfp4_moe.h) or 64 + c
- * (mxfp4_moe_layer), c naming the wait that gave up. */
+ * (CTA-pair GEMM), 48 + c (experts' products of mxfp4_moe.h), 64 + c
+ * (mxfp4_moe_layer) or 80 + c (lora_add), c naming the wait that gave up. */
 MXFP4_API mxfp4_status_t mxfp4_get_device_error(int *code);
 
 /* K-splits of the split-K paths. The planner takes, in this order: a tuning

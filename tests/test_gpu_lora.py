@@ -177,3 +177,37 @@ def test_refusals_of_the_binding():
         mx.lora_add(base, x, a, b, ids, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     with pytest.raises(mx.Mxfp4Error):
         mx.lora_add(base, x[:, :60], a[:, :, :60].contiguous(), b, ids)
+
+
+@pytest.mark.parametrize("T", [16, 130])
+@pytest.mark.parametrize("K", [8, 56, 72, 16392])
+def test_lengths_of_the_sum_that_leave_splits_short_or_empty(T, K):
+    args = case(T, K, 48, 24, 2, none=0.0)
+    base, x, a, b, ids, scales, ranks = args
+    check(mx.lora_add(base, x, a, b, ids, scales, ranks), layer_ref.lora(*args))
+
+
+@pytest.mark.parametrize("T", [64, 65, 127, 128, 129, 193, 257])
+@pytest.mark.parametrize("R", [8, 120, 128, 136, 256])
+def test_one_adapter_for_all_tokens(T, R):
+    args = case(T, 200, 72, R, 1, none=0.0)
+    base, x, a, b, ids, scales, ranks = args
+    check(mx.lora_add(base, x, a, b, ids, scales, ranks), layer_ref.lora(*args))
+
+
+def test_waits_that_run_out_end_the_call_and_are_reported():
+    """Large enough that some wait is longer than the limit: a few hundred tokens in L2 often pass within one nanosecond."""
+    base, x, a, b, ids, scales, _ = case(4096, 7168, 64, 64, 2, none=0.0)
+    want = mx.lora_add(base, x, a, b, ids, scales)
+    torch.cuda.synchronize()
+    assert mx.get_device_error() == 0
+    mx.set_wait_limit_ns(1)
+    try:
+        mx.lora_add(base, x, a, b, ids, scales)
+        torch.cuda.synchronize()
+    finally:
+        mx.set_wait_limit_ns(0)
+    assert 80 < mx.get_device_error() < 96
+    again = mx.lora_add(base, x, a, b, ids, scales)
+    torch.cuda.synchronize()
+    assert mx.get_device_error() == 0 and torch.equal(again, want)
