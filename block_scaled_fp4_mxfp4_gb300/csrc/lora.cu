@@ -518,77 +518,94 @@ __device__ __forceinline__ uint4 keep_first(uint4 v, int n)
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// Columns 32c .. 32c + 31 of C for the tokens 16m .. 16 (m + MG) - 1: channel of column `col` of the
-// n-tile j is 32c + 8 (col / 2) + 2j + (col & 1), so lane (g, q) ends with channels 8q .. 8q + 7 of
-// tokens g and g + 8 of each 16.
+// Columns 32c .. 32c + 31 of C for the tokens of MG times 16 rows, c from c0 on: channel of column
+// `col` of the n-tile j is 32c + 8 (col / 2) + 2j + (col & 1), so lane (g, q) ends with channels
+// 8q .. 8q + 7 of tokens g and g + 8 of each 16. hi, lo: u of the first of these rows.
 template <bool F16, int MG>
-__device__ __forceinline__ void expand_block(const LoraParams &p, const uint16_t *b, int rank, const uint32_t *hi,
-                                             const uint32_t *lo, int ldu, const int *tok, int count, int m, int c)
+__device__ __forceinline__ void expand_rows(const LoraParams &p, const uint16_t *b, int rank, const uint32_t *hi,
+                                            const uint32_t *lo, int ldu, const int *tok, int count, int c0, int chunks, int step)
 {
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    float d[MG][4][4];
-    const int n = 32 * c + 8 * q;            // this lane's channels of C
-    const bool in = n < p.N;
-    int64_t row[MG][2];
-    uint4 base[MG][2];
+    const uint16_t *base[MG][2];
+    uint16_t *out[MG][2];
 #pragma unroll
     for (int i = 0; i < MG; ++i)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int t = 16 * (m + i) + 8 * h + g;
-            row[i][h] = in && t < count ? tok[t] : -1;
-            base[i][h] = make_uint4(0, 0, 0, 0);
-            if (row[i][h] >= 0) base[i][h] = *reinterpret_cast<const uint4 *>(p.base + row[i][h] * p.ldb + n);
+            const int t = 16 * i + 8 * h + g;
+            const bool has = t < count;
+            base[i][h] = has ? p.base + tok[t] * p.ldb + 8 * q : nullptr;
+            out[i][h] = has ? p.c + tok[t] * p.ldc + 8 * q : nullptr;
         }
-#pragma unroll
-    for (int i = 0; i < MG; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) d[i][j][e] = 0.0f;
-    for (int k0 = 0; k0 < rank; k0 += 32) {
-        const int k = k0 + 8 * q;
-        uint4 w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int ch = 32 * c + 8 * (g >> 1) + 2 * j + (g & 1);
-            w[j] = make_uint4(0, 0, 0, 0);
-            if (k < rank && ch < p.N) w[j] = __ldg(reinterpret_cast<const uint4 *>(b + static_cast<int64_t>(ch) * p.R + k));
-        }
-        if (k0 + 32 > rank)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = keep_first(w[j], rank - k);
+    const int first = 8 * (g >> 1) + (g & 1);            // this lane's row of B in n-tile 0 of a chunk
+    const uint16_t *brow = b + static_cast<int64_t>(32 * c0 + first) * p.R + 8 * q;
+    const uint32_t *hrow = hi + g * ldu + 4 * q, *lrow = lo + g * ldu + 4 * q;
+    for (int c = c0; c < chunks; c += step, brow += static_cast<int64_t>(32 * step) * p.R) {
+        const bool in = 32 * c + 8 * q < p.N;
+        uint4 old[MG][2];
 #pragma unroll
         for (int i = 0; i < MG; ++i)
-            // two words of hi / lo hold four k of a token
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const int at = (16 * (m + i) + g) * ldu + (k >> 1) + 2 * s;
-                const uint2 h0 = *reinterpret_cast<const uint2 *>(hi + at), h1 = *reinterpret_cast<const uint2 *>(hi + at + 8 * ldu);
-                const uint2 l0 = *reinterpret_cast<const uint2 *>(lo + at), l1 = *reinterpret_cast<const uint2 *>(lo + at + 8 * ldu);
+            for (int h = 0; h < 2; ++h)
+                if (in && base[i][h]) old[i][h] = *reinterpret_cast<const uint4 *>(base[i][h] + 32 * c);
+        float d[MG][4][4];
+#pragma unroll
+        for (int i = 0; i < MG; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) d[i][j][e] = 0.0f;
+        // whole: every lane's vector of every row of B is there
+        const bool whole_rows = 32 * c + 32 <= p.N;
+        for (int k0 = 0; k0 < rank; k0 += 32) {
+            uint4 w[4];
+            if (whole_rows && k0 + 32 <= rank) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = __ldg(reinterpret_cast<const uint4 *>(brow + 2 * j * p.R + k0));
+            } else {
+                const int left = rank - k0 - 8 * q;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint32_t b0 = s ? w[j].z : w[j].x, b1 = s ? w[j].w : w[j].y;
-                    mma_bf16(d[i][j], l0.x, l1.x, l0.y, l1.y, b0, b1);
-                    mma_bf16(d[i][j], h0.x, h1.x, h0.y, h1.y, b0, b1);
+                    w[j] = make_uint4(0, 0, 0, 0);
+                    if (left > 0 && 32 * c + first + 2 * j < p.N)
+                        w[j] = keep_first(__ldg(reinterpret_cast<const uint4 *>(brow + 2 * j * p.R + k0)), left);
                 }
             }
-    }
 #pragma unroll
-    for (int i = 0; i < MG; ++i)
+            for (int i = 0; i < MG; ++i) {
+                // four words of hi / lo hold this lane's eight k of a token
+                const int at = 16 * i * ldu + (k0 >> 1);
+                const uint4 h0 = *reinterpret_cast<const uint4 *>(hrow + at), h1 = *reinterpret_cast<const uint4 *>(hrow + at + 8 * ldu);
+                const uint4 l0 = *reinterpret_cast<const uint4 *>(lrow + at), l1 = *reinterpret_cast<const uint4 *>(lrow + at + 8 * ldu);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (row[i][h] < 0) continue;
-            const uint32_t v[4] = {base[i][h].x, base[i][h].y, base[i][h].z, base[i][h].w};
-            uint32_t o[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 f = unpack2<F16>(v[j]);
-                o[j] = pack2<F16>(f.x + d[i][j][2 * h], f.y + d[i][j][2 * h + 1]);
+                for (int j = 0; j < 4; ++j) {
+                    mma_bf16(d[i][j], l0.x, l1.x, l0.y, l1.y, w[j].x, w[j].y);
+                    mma_bf16(d[i][j], l0.z, l1.z, l0.w, l1.w, w[j].z, w[j].w);
+                    mma_bf16(d[i][j], h0.x, h1.x, h0.y, h1.y, w[j].x, w[j].y);
+                    mma_bf16(d[i][j], h0.z, h1.z, h0.w, h1.w, w[j].z, w[j].w);
+                }
             }
-            *reinterpret_cast<uint4 *>(p.c + row[i][h] * p.ldc + n) = make_uint4(o[0], o[1], o[2], o[3]);
         }
+#pragma unroll
+        for (int i = 0; i < MG; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (!in || !base[i][h]) continue;
+                const uint32_t v[4] = {old[i][h].x, old[i][h].y, old[i][h].z, old[i][h].w};
+                uint32_t o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = unpack2<F16>(v[j]);
+                    o[j] = pack2<F16>(f.x + d[i][j][2 * h], f.y + d[i][j][2 * h + 1]);
+                }
+                *reinterpret_cast<uint4 *>(out[i][h] + 32 * c) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+    }
 }
+
+// Words between rows of u in shared memory: 16 more than a multiple of 32, so that the
+// 16-byte loads of two rows' lanes take all banks.
+__host__ __device__ constexpr int u_stride(int cols) { return cols / 2 % 32 ? cols / 2 : cols / 2 + 16; }
 
 __device__ __forceinline__ void prefetch_l2(const void *p)
 {
@@ -596,7 +613,7 @@ __device__ __forceinline__ void prefetch_l2(const void *p)
 }
 
 // Grid: halves of tiles (up to kInline tokens: tiles) x blocks of channels. Shared memory: u as
-// high and low bf16, [64 tokens][ranks rounded up to 32, and 8 more against conflicts].
+// high and low bf16, [64 tokens][ranks rounded up to 32].
 template <bool INLINE, bool F16>
 __global__ void __launch_bounds__(kThreads) lora_expand_kernel(const LoraParams p)
 {
@@ -642,7 +659,7 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(const LoraParams 
     const int rank = rank_of(p, tile.adapter);
     const uint16_t *b = p.b + static_cast<int64_t>(tile.adapter) * p.N * p.R;
     const int mt = (tile.count + 15) / 16, rows = mt * 16, cols = (rank + 31) / 32 * 32;
-    const int ldu = ((p.R + 31) / 32 * 32 + 8) / 2;
+    const int ldu = u_stride((p.R + 31) / 32 * 32);
     const int c0 = blockIdx.y * kWarps + warp, step = gridDim.y * kWarps;
     // this warp's first channels go to L2 while u is made
     if (c0 < chunks) {
@@ -655,43 +672,51 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(const LoraParams 
     grid_dependency_wait();
     grid_launch_dependents();
     uint32_t *hi = ushared, *lo = ushared + kHalf * ldu;
-    for (int i = threadIdx.x; i < rows * (cols / 2); i += kThreads) {
-        const int t = i / (cols / 2), r = 2 * (i - t * (cols / 2));
-        float2 v = make_float2(0.0f, 0.0f);
-        if (t < tile.count && r < rank) {
-            const float *u = p.u + static_cast<int64_t>(tok[t]) * p.R + r;
-            for (int s0 = 0; s0 < p.splits; s0 += 8) {
-                float2 part[8];
+    // four neighbouring ranks of a token a thread
+    for (int r = 4 * (threadIdx.x & 7); r < cols; r += 32)
+        for (int t = threadIdx.x >> 3; t < rows; t += kThreads / 8) {
+            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (t < tile.count && r < rank) {
+                const float *u = p.u + static_cast<int64_t>(tok[t]) * p.R + r;
+                const int64_t split = static_cast<int64_t>(p.T) * p.R;
+                for (int s0 = 0; s0 < p.splits; s0 += 8) {
+                    float4 part[8];
 #pragma unroll
-                for (int s = 0; s < 8; ++s)
-                    part[s] = s0 + s < p.splits
-                                  ? __ldcg(reinterpret_cast<const float2 *>(u + static_cast<int64_t>(s0 + s) * p.T * p.R))
-                                  : make_float2(0.0f, 0.0f);
+                    for (int s = 0; s < 8; ++s)
+                        if (s0 + s < p.splits) part[s] = __ldcg(reinterpret_cast<const float4 *>(u + (s0 + s) * split));
 #pragma unroll
-                for (int s = 0; s < 8; ++s) {
-                    v.x += part[s].x;
-                    v.y += part[s].y;
+                    for (int s = 0; s < 8; ++s) {
+                        if (s0 + s >= p.splits) continue;
+                        v[0] += part[s].x;
+                        v[1] += part[s].y;
+                        v[2] += part[s].z;
+                        v[3] += part[s].w;
+                    }
                 }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = r + i < rank ? v[i] * scale : 0.0f;
             }
-            v.x *= scale;
-            v.y = r + 1 < rank ? v.y * scale : 0.0f;
+            uint32_t hb[2], lb[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                hb[i] = *reinterpret_cast<const uint32_t *>(&h);
+                // what rounds to infinity has no low part
+                const float hx = __uint_as_float(hb[i] << 16), hy = __uint_as_float(hb[i] & 0xFFFF0000u);
+                const __nv_bfloat162 l = __floats2bfloat162_rn(isinf(hx) ? 0.0f : v[2 * i] - hx, isinf(hy) ? 0.0f : v[2 * i + 1] - hy);
+                lb[i] = *reinterpret_cast<const uint32_t *>(&l);
+            }
+            *reinterpret_cast<uint2 *>(hi + t * ldu + r / 2) = make_uint2(hb[0], hb[1]);
+            *reinterpret_cast<uint2 *>(lo + t * ldu + r / 2) = make_uint2(lb[0], lb[1]);
         }
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
-        const uint32_t hb = *reinterpret_cast<const uint32_t *>(&h);
-        // what rounds to infinity has no low part
-        const float hx = __uint_as_float(hb << 16), hy = __uint_as_float(hb & 0xFFFF0000u);
-        const __nv_bfloat162 l = __floats2bfloat162_rn(isinf(hx) ? 0.0f : v.x - hx, isinf(hy) ? 0.0f : v.y - hy);
-        hi[t * ldu + r / 2] = hb;
-        lo[t * ldu + r / 2] = *reinterpret_cast<const uint32_t *>(&l);
-    }
     __syncthreads();
-    for (int c = c0; c < chunks; c += step)
-        for (int m = 0; m < mt; m += 2) {
-            if (m + 1 < mt)
-                expand_block<F16, 2>(p, b, rank, hi, lo, ldu, tok, tile.count, m, c);
-            else
-                expand_block<F16, 1>(p, b, rank, hi, lo, ldu, tok, tile.count, m, c);
-        }
+    for (int m = 0; m < mt; m += 2) {
+        const int at = 16 * m * ldu;
+        if (m + 1 < mt)
+            expand_rows<F16, 2>(p, b, rank, hi + at, lo + at, ldu, tok + 16 * m, tile.count - 16 * m, c0, chunks, step);
+        else
+            expand_rows<F16, 1>(p, b, rank, hi + at, lo + at, ldu, tok + 16 * m, tile.count - 16 * m, c0, chunks, step);
+    }
 }
 
 template <typename Kern, typename P>
@@ -714,11 +739,11 @@ template <bool INLINE, bool F16>
 cudaError_t launch_expand(const LoraParams &p, const LoraLayout &l, cudaStream_t stream)
 {
     static KernelOnce once;
-    constexpr size_t most = sizeof(uint32_t) * 2 * kHalf * ((kMaxRank + 8) / 2);
+    constexpr size_t most = sizeof(uint32_t) * 2 * kHalf * u_stride(kMaxRank);
     int sms = 0;
     const cudaError_t e = prepare_kernel(lora_expand_kernel<INLINE, F16>, most, once, &sms);
     if (e != cudaSuccess) return e;
-    const size_t smem = sizeof(uint32_t) * 2 * kHalf * (((p.R + 31) / 32 * 32 + 8) / 2);
+    const size_t smem = sizeof(uint32_t) * 2 * kHalf * u_stride((p.R + 31) / 32 * 32);
     // blocks of channels: as many as give every SM two blocks, no more than one chunk a warp. How
     // many halves of tiles there are the GPU alone knows: an adapter leaves one half empty on average
     const int tiles = INLINE ? l.max_tiles : 2 * l.max_tiles, chunks = (p.N + 31) / 32;

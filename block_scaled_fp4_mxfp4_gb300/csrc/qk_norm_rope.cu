@@ -9,8 +9,8 @@
 // Bound: HBM (2 bytes read, 2 written an element). A lane has two 16-byte vectors of a
 // head: in the layout of halves the two whose elements turn with each other, so that
 // nothing but the sum of squares crosses lanes. A group of LPH lanes has a head, a warp
-// the heads of one token, which share a and b; U of a group's heads are on their way at a
-// time. Arithmetic in pairs of floats (mul and fma of f32x2: one issue for two).
+// heads of one token, which share a and b; four of a group's heads are on their way at a
+// time, by cp.async, so that they hold no registers. Arithmetic in pairs of floats (mul and fma of f32x2: one issue for two).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -25,6 +25,7 @@ namespace mxfp4 {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kAhead = 4;        // heads of a lane group on their way
 
 template <bool F16>
 __device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8])
@@ -124,43 +125,57 @@ __device__ __forceinline__ float group_sum(float v)
     return v;
 }
 
-// r for heads whose squares leave fp32, or whose sum is so small that it lost bits and
-// eps does not hide it (`odd`): the values are brought to about 1 by a power of two
-// first (exact), and are left scaled by it.
-template <int LPH>
-__device__ __noinline__ float rescaled_r(Vec &x0, Vec &x1, bool odd, float eps, int D)
+// For heads whose squares leave fp32, or whose sum is so small that it lost bits and eps
+// does not hide it (`odd`): a power of two s that brings the values to about 1, and r for
+// the values times s. (By value: with references the vectors of every head went through
+// local memory, 70 us instead of 51 at 8192 tokens of 72 heads.)
+template <bool F16, int LPH>
+__device__ __noinline__ float2 rescaled(uint4 raw0, uint4 raw1, bool odd, float eps, int D)
 {
+    float x[16];
+    unpack8<F16>(raw0, *reinterpret_cast<float(*)[8]>(x));
+    unpack8<F16>(raw1, *reinterpret_cast<float(*)[8]>(x + 8));
     float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 a = floats(x0.p[i]), b = floats(x1.p[i]);
-        top = fmaxf(fmaxf(top, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(b.x), fabsf(b.y)));
-    }
+    for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[i]));
 #pragma unroll
     for (int o = LPH / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     float s = 1.0f;
     if (odd && top > 0.0f && !isinf(top)) s = exp2f(static_cast<float>(max(-126, min(126, -ilogbf(top)))));
-    const Pair s2 = pair(s, s);
     float ss = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x0.p[i] = mul(x0.p[i], s2);
-        x1.p[i] = mul(x1.p[i], s2);
-        const float2 a = floats(x0.p[i]), b = floats(x1.p[i]);
-        ss = fmaf(a.x, a.x, fmaf(a.y, a.y, fmaf(b.x, b.x, fmaf(b.y, b.y, ss))));
-    }
+    for (int i = 0; i < 16; ++i) ss = fmaf(x[i] * s, x[i] * s, ss);
     ss = group_sum<LPH>(ss);
     const double m = static_cast<double>(ss) / D + static_cast<double>(eps) * s * s;
-    return m == 0.0 ? 0.0f : static_cast<float>(1.0 / sqrt(m));
+    return make_float2(s, m == 0.0 ? 0.0f : static_cast<float>(1.0 / sqrt(m)));
 }
 
 // Heads h0 .. h1 - 1 of one token's queries or keys (which: 0, 1).
-template <bool F16, bool INTER, int LPH, int U>
+template <bool F16, bool INTER, int LPH, bool FULL>
 __device__ __forceinline__ void heads_of(const QkParams &p, int which, int64_t t, int64_t pos, int h0, int h1, int j, int hv,
-                                         int v0, int v1, bool in0, bool in1)
+                                         int v0, int v1, bool in0, bool in1, uint4 *slots)
 {
     constexpr int G = 32 / LPH;                         // heads a warp has side by side
     const int group = (threadIdx.x & 31) / LPH;
+    const int64_t in_step = 2 * G * p.sh[which], out_step = 2 * G * p.osh[which];      // bytes to a group's next head
+    const char *src0 = reinterpret_cast<const char *>(p.x[which] + t * p.st[which] + (h0 + group) * p.sh[which] + 8 * v0);
+    char *dst0 = reinterpret_cast<char *>(p.out[which] + t * p.ost[which] + (h0 + group) * p.osh[which] + 8 * v0);
+    const int far = 16 * (v1 - v0);                      // bytes to the second vector
+    // kAhead heads of a lane group are on their way to shared memory; a thread reads what it
+    // copied itself, so that nothing but its own copies is waited for
+    const uint32_t ring = smem_u32(slots) + threadIdx.x * 16;
+    constexpr uint32_t kSecond = kAhead * kThreads * 16;
+    auto request = [&](int h, int slot) {
+        if (h + group < h1) {
+            if (in0) cp_async<16>(ring + slot * (kThreads * 16), src0);
+            if (in1) cp_async<16>(ring + slot * (kThreads * 16) + kSecond, src0 + far);
+        }
+        src0 += in_step;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead - 1; ++i) request(h0 + G * i, i);
+
     // what an element is multiplied with (a), and what its partner is (b)
     Vec a0, a1, b0, b1;
 #pragma unroll
@@ -201,6 +216,7 @@ __device__ __forceinline__ void heads_of(const QkParams &p, int which, int64_t t
             }
         }
     }
+    const float least = p.eps < 1e-20f ? 1e-24f : 0.0f;
     const uint16_t *w = p.w[which];
     if (w) {
         const Vec w0 = unpack<F16>(in0 ? *reinterpret_cast<const uint4 *>(w + 8 * v0) : make_uint4(0, 0, 0, 0));
@@ -220,67 +236,71 @@ __device__ __forceinline__ void heads_of(const QkParams &p, int which, int64_t t
         }
     }
     const float inv_d = 1.0f / static_cast<float>(p.D);
-    const int64_t in_step = G * p.sh[which], out_step = G * p.osh[which];
-    const uint16_t *src = p.x[which] + t * p.st[which] + (h0 + group) * p.sh[which];
-    uint16_t *dst = p.out[which] + t * p.ost[which] + (h0 + group) * p.osh[which];
-    for (int h = h0; h < h1; h += G * U) {
-        uint4 raw[U][2];
+    // one head, in the registers of its lane group
+    auto turn = [&](const uint4 &raw0, const uint4 &raw1, bool live, uint4 &out0, uint4 &out1) {
+        Vec x0 = unpack<F16>(raw0), x1 = unpack<F16>(raw1);
+        float r = 1.0f;
+        if (w) {
+            Pair q = mul(x0.p[0], x0.p[0]), q1 = mul(x1.p[0], x1.p[0]);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            raw[u][0] = raw[u][1] = make_uint4(0, 0, 0, 0);
-            if (h + G * u + group < h1) {
-                if (in0) raw[u][0] = *reinterpret_cast<const uint4 *>(src + u * in_step + 8 * v0);
-                if (in1) raw[u][1] = *reinterpret_cast<const uint4 *>(src + u * in_step + 8 * v1);
+            for (int i = 1; i < 4; ++i) {
+                q = fma(x0.p[i], x0.p[i], q);
+                q1 = fma(x1.p[i], x1.p[i], q1);
             }
-        }
-        src += U * in_step;
+            const float2 f = floats(q), f1 = floats(q1);
+            const float ss = group_sum<LPH>((f.x + f.y) + (f1.x + f1.y));
+            r = rsqrtf(fmaf(ss, inv_d, p.eps));
+            // 1e36: the sum has not overflowed; 1e-24: squares below 2^-126 are less than 2^-24 of it
+            const bool odd = live && !(ss < 1e36f && ss >= least);
+            if (__any_sync(0xffffffffu, odd)) {
+                const float2 sr = rescaled<F16, LPH>(raw0, raw1, odd, p.eps, p.D);
+                if (odd) {
+                    r = sr.y;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const bool live = h + G * u + group < h1;
-            Vec x0 = unpack<F16>(raw[u][0]), x1 = unpack<F16>(raw[u][1]);
-            float r = 1.0f;
-            if (w) {
-                Pair q = mul(x0.p[0], x0.p[0]);
-#pragma unroll
-                for (int i = 1; i < 4; ++i) q = fma(x0.p[i], x0.p[i], q);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) q = fma(x1.p[i], x1.p[i], q);
-                const float2 f = floats(q);
-                const float ss = group_sum<LPH>(f.x + f.y);
-                r = rsqrtf(fmaf(ss, inv_d, p.eps));
-                // 1e36: the sum has not overflowed; 1e-24: squares below 2^-126 are less than 2^-24 of it
-                const bool odd = live && (!(ss < 1e36f) || (ss < 1e-24f && p.eps < 1e-20f));
-                if (__any_sync(0xffffffffu, odd)) {
-                    const float rr = rescaled_r<LPH>(x0, x1, odd, p.eps, p.D);
-                    if (odd) r = rr;
+                    for (int i = 0; i < 4; ++i) {
+                        x0.p[i] = mul(x0.p[i], pair(sr.x, sr.x));
+                        x1.p[i] = mul(x1.p[i], pair(sr.x, sr.x));
+                    }
                 }
             }
-            r += bad;
-            const Pair r2 = pair(r, r);
-            Vec o0, o1;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                Pair y0 = x1.p[i], y1 = x0.p[i];
-                if constexpr (INTER) {
-                    const float2 f0 = floats(x0.p[i]), f1 = floats(x1.p[i]);
-                    y0 = pair(f0.y, f0.x);
-                    y1 = pair(f1.y, f1.x);
-                }
-                o0.p[i] = mul(fma(y0, b0.p[i], mul(x0.p[i], a0.p[i])), r2);
-                o1.p[i] = mul(fma(y1, b1.p[i], mul(x1.p[i], a1.p[i])), r2);
-            }
-            if (live) {
-                if (in0) *reinterpret_cast<uint4 *>(dst + u * out_step + 8 * v0) = pack<F16>(o0);
-                if (in1) *reinterpret_cast<uint4 *>(dst + u * out_step + 8 * v1) = pack<F16>(o1);
-            }
         }
-        dst += U * out_step;
+        r += bad;
+        const Pair r2 = pair(r, r);
+        Vec o0, o1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            Pair y0 = x1.p[i], y1 = x0.p[i];
+            if constexpr (INTER) {
+                const float2 f0 = floats(x0.p[i]), f1 = floats(x1.p[i]);
+                y0 = pair(f0.y, f0.x);
+                y1 = pair(f1.y, f1.x);
+            }
+            o0.p[i] = mul(fma(y0, b0.p[i], mul(x0.p[i], a0.p[i])), r2);
+            o1.p[i] = mul(fma(y1, b1.p[i], mul(x1.p[i], a1.p[i])), r2);
+        }
+        out0 = pack<F16>(o0);
+        out1 = pack<F16>(o1);
+    };
+    int slot = 0;
+    for (int h = h0; h < h1; h += G) {
+        request(h + G * (kAhead - 1), (slot + kAhead - 1) % kAhead);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+        const bool live = h + group < h1;
+        uint4 raw0 = make_uint4(0, 0, 0, 0), raw1 = raw0, o0, o1;
+        if (FULL || in0) raw0 = slots[slot * kThreads + threadIdx.x];
+        if (FULL || in1) raw1 = slots[(kAhead + slot) * kThreads + threadIdx.x];
+        turn(raw0, raw1, live, o0, o1);
+        if (live && in0) *reinterpret_cast<uint4 *>(dst0) = o0;
+        if (live && in1) *reinterpret_cast<uint4 *>(dst0 + far) = o1;
+        dst0 += out_step;
+        slot = (slot + 1) % kAhead;
     }
 }
 
-template <bool F16, bool INTER, int LPH, int U>
+template <bool F16, bool INTER, int LPH, bool FULL>
 __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kernel(const QkParams p)
 {
+    __shared__ uint4 slots[2 * kAhead * kThreads];
     const int j = threadIdx.x & (LPH - 1);
     const uint32_t item = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     const uint32_t t = item / p.units, unit = item - t * p.units;
@@ -300,20 +320,18 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kernel(const QkParam
     int64_t pos = 0;
     if (p.rot) pos = p.pos64 ? static_cast<const int64_t *>(p.positions)[t] : static_cast<const int32_t *>(p.positions)[t];
     const int hq = p.heads[0];
-    if (h0 < hq) heads_of<F16, INTER, LPH, U>(p, 0, t, pos, h0, min(h1, hq), j, hv, v0, v1, in0, in1);
-    if (h1 > hq) heads_of<F16, INTER, LPH, U>(p, 1, t, pos, max(h0, hq) - hq, h1 - hq, j, hv, v0, v1, in0, in1);
+    if (h0 < hq) heads_of<F16, INTER, LPH, FULL>(p, 0, t, pos, h0, min(h1, hq), j, hv, v0, v1, in0, in1, slots);
+    if (h1 > hq) heads_of<F16, INTER, LPH, FULL>(p, 1, t, pos, max(h0, hq) - hq, h1 - hq, j, hv, v0, v1, in0, in1, slots);
 }
 
 template <bool F16, bool INTER, int LPH>
 cudaError_t launch_lph(QkParams p, int num_sms, cudaStream_t stream)
 {
-    // A warp takes as many of a token's heads, two of a lane group at a time, as still leave
-    // six rounds of 24 warps an SM; below that one head a lane group.
+    // A warp takes as many of a token's heads, as still leave
+    // three rounds of 24 warps an SM; below that one head a lane group.
     constexpr int G = 32 / LPH;
     const int heads = p.heads[0] + p.heads[1], all = (heads + G - 1) / G;
-    const int64_t each = p.T * all / (int64_t(num_sms) * 24 * 6);
-    const bool many = each >= 2;
-    p.unit_heads = G * static_cast<int>(many ? std::min<int64_t>(all, each) : 1);
+    p.unit_heads = G * static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(all, p.T * all / (int64_t(num_sms) * 24 * 3))));
     p.units = (heads + p.unit_heads - 1) / p.unit_heads;
     const int64_t items = p.T * p.units;
     cudaLaunchConfig_t cfg = {};
@@ -325,8 +343,9 @@ cudaError_t launch_lph(QkParams p, int num_sms, cudaStream_t stream)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (many) return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<F16, INTER, LPH, 2>, p);
-    return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<F16, INTER, LPH, 1>, p);
+    // every lane has two vectors of a head of 64, 128 or 256
+    if (p.D == 16 * LPH) return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<F16, INTER, LPH, true>, p);
+    return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<F16, INTER, LPH, false>, p);
 }
 
 template <bool F16, bool INTER>
