@@ -518,88 +518,99 @@ __device__ __forceinline__ uint4 keep_first(uint4 v, int n)
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// Columns 32c .. 32c + 31 of C for the tokens of MG times 16 rows, c from c0 on: channel of column
-// `col` of the n-tile j is 32c + 8 (col / 2) + 2j + (col & 1), so lane (g, q) ends with channels
-// 8q .. 8q + 7 of tokens g and g + 8 of each 16. hi, lo: u of the first of these rows.
-template <bool F16, int MG>
-__device__ __forceinline__ void expand_rows(const LoraParams &p, const uint16_t *b, int rank, const uint32_t *hi,
-                                            const uint32_t *lo, int ldu, const int *tok, int count, int c0, int chunks, int step)
+// Rows of B of one chunk of 32 channels for 32 ranks from k0 on: 8 neighbouring ranks of four
+// channels a lane. brow: this lane's first; left: channels and ranks there are from it on.
+__device__ __forceinline__ void load_b(uint4 (&w)[4], const uint16_t *brow, int R, int k0, int channels, int ranks)
+{
+    if (channels > 6 && ranks >= 8) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = __ldg(reinterpret_cast<const uint4 *>(brow + 2 * j * R + k0));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            w[j] = make_uint4(0, 0, 0, 0);
+            if (channels > 2 * j && ranks > 0)
+                w[j] = keep_first(__ldg(reinterpret_cast<const uint4 *>(brow + 2 * j * R + k0)), ranks);
+        }
+    }
+}
+
+// The update of one chunk for 16 tokens: d += (low + high part of u) B^T over 32 ranks.
+__device__ __forceinline__ void multiply(float (&d)[4][4], const uint4 (&w)[4], const uint32_t *hrow, const uint32_t *lrow,
+                                         int ldu)
+{
+    // four words of hi / lo hold this lane's eight ranks of a token
+    const uint4 h0 = *reinterpret_cast<const uint4 *>(hrow), h1 = *reinterpret_cast<const uint4 *>(hrow + 8 * ldu);
+    const uint4 l0 = *reinterpret_cast<const uint4 *>(lrow), l1 = *reinterpret_cast<const uint4 *>(lrow + 8 * ldu);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        mma_bf16(d[j], l0.x, l1.x, l0.y, l1.y, w[j].x, w[j].y);
+        mma_bf16(d[j], l0.z, l1.z, l0.w, l1.w, w[j].z, w[j].w);
+        mma_bf16(d[j], h0.x, h1.x, h0.y, h1.y, w[j].x, w[j].y);
+        mma_bf16(d[j], h0.z, h1.z, h0.w, h1.w, w[j].z, w[j].w);
+    }
+}
+
+// Columns 32c .. 32c + 31 of C for the tile's tokens, c from c0 on: channel of column `col` of the
+// n-tile j is 32c + 8 (col / 2) + 2j + (col & 1), so lane (g, q) ends with channels 8q .. 8q + 7 of
+// tokens g and g + 8 of each 16. KEPT: the ranks are at most 32 * KEPT, and a chunk's rows of B
+// stay in registers for all of the tokens (0: they are loaded again for every 16).
+template <bool F16, int KEPT>
+__device__ __forceinline__ void expand_chunks(const LoraParams &p, const uint16_t *b, int rank, const uint32_t *hi,
+                                              const uint32_t *lo, int ldu, const int *tok, int count, int c0, int chunks, int step)
 {
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    const uint16_t *base[MG][2];
-    uint16_t *out[MG][2];
-#pragma unroll
-    for (int i = 0; i < MG; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int t = 16 * i + 8 * h + g;
-            const bool has = t < count;
-            base[i][h] = has ? p.base + tok[t] * p.ldb + 8 * q : nullptr;
-            out[i][h] = has ? p.c + tok[t] * p.ldc + 8 * q : nullptr;
-        }
     const int first = 8 * (g >> 1) + (g & 1);            // this lane's row of B in n-tile 0 of a chunk
-    const uint16_t *brow = b + static_cast<int64_t>(32 * c0 + first) * p.R + 8 * q;
     const uint32_t *hrow = hi + g * ldu + 4 * q, *lrow = lo + g * ldu + 4 * q;
-    for (int c = c0; c < chunks; c += step, brow += static_cast<int64_t>(32 * step) * p.R) {
-        const bool in = 32 * c + 8 * q < p.N;
-        uint4 old[MG][2];
+    for (int c = c0; c < chunks; c += step) {
+        const int n = 32 * c + 8 * q, channels = p.N - 32 * c - first;
+        const bool in = n < p.N;
+        const uint16_t *brow = b + static_cast<int64_t>(32 * c + first) * p.R + 8 * q;
+        uint4 w[KEPT ? KEPT : 1][4];
+        if constexpr (KEPT > 0)
 #pragma unroll
-        for (int i = 0; i < MG; ++i)
+            for (int k = 0; k < KEPT; ++k) load_b(w[k], brow, p.R, 32 * k, channels, rank - 32 * k - 8 * q);
+        uint4 old[2], next[2];
+        auto fetch = [&](uint4 (&v)[2], int m) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                if (in && base[i][h]) old[i][h] = *reinterpret_cast<const uint4 *>(base[i][h] + 32 * c);
-        float d[MG][4][4];
-#pragma unroll
-        for (int i = 0; i < MG; ++i)
+            for (int h = 0; h < 2; ++h) {
+                const int t = m + 8 * h + g;
+                if (in && t < count) v[h] = *reinterpret_cast<const uint4 *>(p.base + tok[t] * p.ldb + n);
+            }
+        };
+        fetch(next, 0);
+        for (int m = 0; m < count; m += 16) {
+            old[0] = next[0];
+            old[1] = next[1];
+            fetch(next, m + 16);
+            float d[4][4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) d[i][j][e] = 0.0f;
-        // whole: every lane's vector of every row of B is there
-        const bool whole_rows = 32 * c + 32 <= p.N;
-        for (int k0 = 0; k0 < rank; k0 += 32) {
-            uint4 w[4];
-            if (whole_rows && k0 + 32 <= rank) {
+                for (int e = 0; e < 4; ++e) d[j][e] = 0.0f;
+            if constexpr (KEPT > 0) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) w[j] = __ldg(reinterpret_cast<const uint4 *>(brow + 2 * j * p.R + k0));
+                for (int k = 0; k < KEPT; ++k) multiply(d, w[k], hrow + m * ldu + 16 * k, lrow + m * ldu + 16 * k, ldu);
             } else {
-                const int left = rank - k0 - 8 * q;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    w[j] = make_uint4(0, 0, 0, 0);
-                    if (left > 0 && 32 * c + first + 2 * j < p.N)
-                        w[j] = keep_first(__ldg(reinterpret_cast<const uint4 *>(brow + 2 * j * p.R + k0)), left);
+                for (int k = 0; k < rank; k += 32) {
+                    load_b(w[0], brow, p.R, k, channels, rank - k - 8 * q);
+                    multiply(d, w[0], hrow + m * ldu + k / 2, lrow + m * ldu + k / 2, ldu);
                 }
             }
-#pragma unroll
-            for (int i = 0; i < MG; ++i) {
-                // four words of hi / lo hold this lane's eight k of a token
-                const int at = 16 * i * ldu + (k0 >> 1);
-                const uint4 h0 = *reinterpret_cast<const uint4 *>(hrow + at), h1 = *reinterpret_cast<const uint4 *>(hrow + at + 8 * ldu);
-                const uint4 l0 = *reinterpret_cast<const uint4 *>(lrow + at), l1 = *reinterpret_cast<const uint4 *>(lrow + at + 8 * ldu);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    mma_bf16(d[i][j], l0.x, l1.x, l0.y, l1.y, w[j].x, w[j].y);
-                    mma_bf16(d[i][j], l0.z, l1.z, l0.w, l1.w, w[j].z, w[j].w);
-                    mma_bf16(d[i][j], h0.x, h1.x, h0.y, h1.y, w[j].x, w[j].y);
-                    mma_bf16(d[i][j], h0.z, h1.z, h0.w, h1.w, w[j].z, w[j].w);
-                }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < MG; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                if (!in || !base[i][h]) continue;
-                const uint32_t v[4] = {old[i][h].x, old[i][h].y, old[i][h].z, old[i][h].w};
+                const int t = m + 8 * h + g;
+                if (!in || t >= count) continue;
+                const uint32_t v[4] = {old[h].x, old[h].y, old[h].z, old[h].w};
                 uint32_t o[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float2 f = unpack2<F16>(v[j]);
-                    o[j] = pack2<F16>(f.x + d[i][j][2 * h], f.y + d[i][j][2 * h + 1]);
+                    o[j] = pack2<F16>(f.x + d[j][2 * h], f.y + d[j][2 * h + 1]);
                 }
-                *reinterpret_cast<uint4 *>(out[i][h] + 32 * c) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4 *>(p.c + tok[t] * p.ldc + n) = make_uint4(o[0], o[1], o[2], o[3]);
             }
+        }
     }
 }
 
@@ -658,7 +669,7 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(const LoraParams 
     }
     const int rank = rank_of(p, tile.adapter);
     const uint16_t *b = p.b + static_cast<int64_t>(tile.adapter) * p.N * p.R;
-    const int mt = (tile.count + 15) / 16, rows = mt * 16, cols = (rank + 31) / 32 * 32;
+    const int rows = (tile.count + 15) / 16 * 16, cols = max(1, (rank + 31) / 32) * 32;   // 32 zeros of an adapter of rank 0
     const int ldu = u_stride((p.R + 31) / 32 * 32);
     const int c0 = blockIdx.y * kWarps + warp, step = gridDim.y * kWarps;
     // this warp's first channels go to L2 while u is made
@@ -710,13 +721,13 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(const LoraParams 
             *reinterpret_cast<uint2 *>(lo + t * ldu + r / 2) = make_uint2(lb[0], lb[1]);
         }
     __syncthreads();
-    for (int m = 0; m < mt; m += 2) {
-        const int at = 16 * m * ldu;
-        if (m + 1 < mt)
-            expand_rows<F16, 2>(p, b, rank, hi + at, lo + at, ldu, tok + 16 * m, tile.count - 16 * m, c0, chunks, step);
-        else
-            expand_rows<F16, 1>(p, b, rank, hi + at, lo + at, ldu, tok + 16 * m, tile.count - 16 * m, c0, chunks, step);
-    }
+    // 64 ranks of B are what the registers hold beside the rest
+    if (rank <= 32)
+        expand_chunks<F16, 1>(p, b, rank, hi, lo, ldu, tok, tile.count, c0, chunks, step);
+    else if (rank <= 64)
+        expand_chunks<F16, 2>(p, b, rank, hi, lo, ldu, tok, tile.count, c0, chunks, step);
+    else
+        expand_chunks<F16, 0>(p, b, rank, hi, lo, ldu, tok, tile.count, c0, chunks, step);
 }
 
 template <typename Kern, typename P>

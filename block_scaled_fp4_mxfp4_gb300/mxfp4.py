@@ -483,6 +483,7 @@ def nvfp4_group_quant_gemm(groups, problems=None, workspace=None, stream=None):
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 MOE_SCORES = {"softmax": 0, "sigmoid": 1}
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _stream_of(stream, t):
@@ -648,8 +649,8 @@ def _same_device(t, *others):
     for o in others:
         if o is not None and o.get_device() != i:
             raise ValueError(f"tensors on different devices: {t.device} and {o.device}")
-    if i != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if i != _current_device():
+        raise ValueError(f"tensors are on {t.device}, the current device is cuda:{_current_device()}")
 
 
 def lora_workspace_bytes(T: int, K: int, R: int, L: int) -> int:
