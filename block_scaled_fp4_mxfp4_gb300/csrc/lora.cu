@@ -44,7 +44,6 @@ constexpr int kHalf = 64;          // tokens of a block of the second product
 constexpr int kInline = 64;        // tokens up to which blocks work out the tiles themselves
 constexpr int kRanks = 64;         // ranks of one block of the first product, up to kInline tokens
 constexpr int kMaxRank = 256;
-constexpr int kSortThreads = 1024;
 
 // ------------------------------------------------------------------ tiles
 
@@ -58,20 +57,21 @@ __device__ __forceinline__ int adapter_of(int id, int L) { return id >= 0 && id 
 // sums, ranks. In which order a tile's tokens stand does not matter to their results. A
 // thread keeps its first kSortKeep ids in registers.
 constexpr int kSortKeep = 8;
-__global__ void __launch_bounds__(kSortThreads) lora_sort_kernel(const LoraParams p)
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) lora_sort_kernel(const LoraParams p)
 {
     extern __shared__ int bins[];            // [L + 1]: tokens, then the next free place
-    __shared__ int2 scan[kSortThreads / 32]; // tokens and tiles of the groups before a warp's
+    __shared__ int2 scan[THREADS / 32]; // tokens and tiles of the groups before a warp's
     __shared__ int2 all;
     const int tid = threadIdx.x, lane = tid & 31, groups = p.L + 1;
-    for (int i = tid; i < groups; i += kSortThreads) bins[i] = 0;
+    for (int i = tid; i < groups; i += THREADS) bins[i] = 0;
     __syncthreads();
     grid_dependency_wait();
     grid_launch_dependents();
     int kept[kSortKeep];
 #pragma unroll
     for (int i = 0; i < kSortKeep; ++i) {
-        const int at = i * kSortThreads + tid;
+        const int at = i * THREADS + tid;
         kept[i] = at < p.T ? p.ids[at] : 0;
     }
     // neighbours often share an adapter: one atomic for all of a warp's lanes that do
@@ -82,12 +82,12 @@ __global__ void __launch_bounds__(kSortThreads) lora_sort_kernel(const LoraParam
     };
 #pragma unroll
     for (int i = 0; i < kSortKeep; ++i)
-        if (i * kSortThreads < p.T) count(i * kSortThreads + tid, kept[i]);
-    for (int64_t base = kSortKeep * kSortThreads; base < p.T; base += kSortThreads)
+        if (i * THREADS < p.T) count(i * THREADS + tid, kept[i]);
+    for (int64_t base = kSortKeep * THREADS; base < p.T; base += THREADS)
         count(base + tid, base + tid < p.T ? p.ids[base + tid] : 0);
     __syncthreads();
     int2 before = make_int2(0, 0);           // tokens and tiles of the groups before this round's
-    for (int g0 = 0; g0 < groups; g0 += kSortThreads) {
+    for (int g0 = 0; g0 < groups; g0 += THREADS) {
         const int g = g0 + tid;
         const int n = g < groups ? bins[g] : 0;
         const int nt = g == p.L && !p.copy ? 0 : (n + kTile - 1) / kTile;
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kSortThreads) lora_sort_kernel(const LoraParam
         if (lane == 31) scan[tid >> 5] = make_int2(a, b);
         __syncthreads();
         if (tid < 32) {
-            const int2 own = scan[lane];
+            const int2 own = lane < THREADS / 32 ? scan[lane] : make_int2(0, 0);
             int2 sum = own;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kSortThreads) lora_sort_kernel(const LoraParam
                     sum.y += y;
                 }
             }
-            scan[lane] = make_int2(sum.x - own.x, sum.y - own.y);
+            if (lane < THREADS / 32) scan[lane] = make_int2(sum.x - own.x, sum.y - own.y);
             if (lane == 31) all = sum;
         }
         __syncthreads();
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kSortThreads) lora_sort_kernel(const LoraParam
         __syncthreads();
     }
     // the others of the grid's tiles are empty
-    for (int i = before.y + tid; i < p.max_tiles; i += kSortThreads) p.tiles[i] = make_int4(p.L, 0, 0, 0);
+    for (int i = before.y + tid; i < p.max_tiles; i += THREADS) p.tiles[i] = make_int4(p.L, 0, 0, 0);
     auto place = [&](int64_t at, int id) {
         const int g = at < p.T ? adapter_of(id, p.L) : -1;
         const unsigned same = __match_any_sync(0xffffffffu, g);
@@ -140,8 +140,8 @@ __global__ void __launch_bounds__(kSortThreads) lora_sort_kernel(const LoraParam
     };
 #pragma unroll
     for (int i = 0; i < kSortKeep; ++i)
-        if (i * kSortThreads < p.T) place(i * kSortThreads + tid, kept[i]);
-    for (int64_t base = kSortKeep * kSortThreads; base < p.T; base += kSortThreads)
+        if (i * THREADS < p.T) place(i * THREADS + tid, kept[i]);
+    for (int64_t base = kSortKeep * THREADS; base < p.T; base += THREADS)
         place(base + tid, base + tid < p.T ? p.ids[base + tid] : 0);
 }
 
@@ -270,22 +270,26 @@ constexpr size_t shrink_smem(int T)
     return sizeof(float) * kWarps * (T <= 8 ? 8 : (T <= 16 ? 16 : (T <= 32 ? 32 : kInline))) * (kRanks + 1);
 }
 
-template <int MT>
+template <int MT, int MOST>
 __device__ __forceinline__ void shrink_tile(const LoraParams &p, const uint16_t *a, int rows, const int *tok, int count,
                                             int kb, int ke, float *red)
 {
     if (count <= 8)
         shrink_steps<MT, 1>(p, a, rows, tok, count, kb, ke, red);
-    else if (count <= 16)
+    else if (MOST == 16 || count <= 16)
         shrink_steps<MT, 2>(p, a, rows, tok, count, kb, ke, red);
-    else if (count <= 32)
-        shrink_steps<MT, 4>(p, a, rows, tok, count, kb, ke, red);
-    else
-        shrink_steps<MT, 8>(p, a, rows, tok, count, kb, ke, red);
+    else if constexpr (MOST > 16) {
+        if (count <= 32)
+            shrink_steps<MT, 4>(p, a, rows, tok, count, kb, ke, red);
+        else
+            shrink_steps<MT, 8>(p, a, rows, tok, count, kb, ke, red);
+    }
 }
 
-// Up to kInline tokens. Grid: tiles x splits of K x blocks of 64 ranks.
-__global__ void __launch_bounds__(kThreads) lora_shrink_few_kernel(const LoraParams p)
+// Batches of up to MOST tokens (16: sums of two n-tiles leave registers for two blocks an SM).
+// Grid: tiles x splits of K x blocks of 64 ranks.
+template <int MOST>
+__global__ void __launch_bounds__(kThreads, MOST == 16 ? 2 : 1) lora_shrink_few_kernel(const LoraParams p)
 {
     extern __shared__ float red[];
     __shared__ int tok[kInline], ids[kInline], found[1];
@@ -301,11 +305,11 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_few_kernel(const LoraPar
     const int kb = static_cast<int>(min(static_cast<int64_t>(blockIdx.y) * per, static_cast<int64_t>(p.K)));
     const int ke = static_cast<int>(min(static_cast<int64_t>(kb) + per, static_cast<int64_t>(p.K)));
     if (rows <= 16)
-        shrink_tile<1>(p, a, rows, tok, tile.count, kb, ke, red);
+        shrink_tile<1, MOST>(p, a, rows, tok, tile.count, kb, ke, red);
     else if (rows <= 32)
-        shrink_tile<2>(p, a, rows, tok, tile.count, kb, ke, red);
+        shrink_tile<2, MOST>(p, a, rows, tok, tile.count, kb, ke, red);
     else
-        shrink_tile<4>(p, a, rows, tok, tile.count, kb, ke, red);
+        shrink_tile<4, MOST>(p, a, rows, tok, tile.count, kb, ke, red);
 }
 
 // More than kInline tokens, on the tensor core. Grid: tiles x splits of K x blocks of 128
@@ -771,10 +775,10 @@ LoraLayout lora_layout(int64_t T, int64_t K, int R, int L)
     LoraLayout l;
     // every group of tokens wastes less than one tile
     l.max_tiles = static_cast<int>(std::min<int64_t>(T, T / kTile + L + 1));
-    // splits of K: two blocks an SM, each with 512 elements at least (one step of every warp, or
-    // eight stages)
-    const int64_t tiles = T <= kInline ? (T + kInline - 1) / kInline : l.max_tiles;
-    l.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({304 / tiles, 32, (K + 511) / 512})));
+    // splits of K: two blocks an SM if all tiles are there (one of 17 to kInline tokens, by
+    // registers), each with 512 elements at least (one step of every warp, or eight stages)
+    const int64_t blocks = T > 16 && T <= kInline ? 152 : 304;
+    l.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({blocks / l.max_tiles, 32, (K + 511) / 512})));
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
     // splits * T is at most 32 T, and at most 304 / (T / 128) * T or T: a bound that grows with T
     const int64_t most = std::min<int64_t>(32 * T, std::max<int64_t>(304 * kTile, T));
@@ -791,15 +795,21 @@ cudaError_t launch_lora(LoraParams p, const LoraLayout &l, bool f16, cudaStream_
     p.max_tiles = l.max_tiles;
     cudaError_t e;
     if (p.T <= kInline) {
-        static KernelOnce once;
-        e = prepare_kernel(lora_shrink_few_kernel, shrink_smem(kInline), once, nullptr);
-        if (e != cudaSuccess) return e;
-        e = launch(lora_shrink_few_kernel, dim3(l.max_tiles, l.splits, (p.R + kRanks - 1) / kRanks), kThreads,
-                   shrink_smem(p.T), stream, p);
+        const dim3 grid(l.max_tiles, l.splits, (p.R + kRanks - 1) / kRanks);
+        if (p.T <= 16) {
+            e = launch(lora_shrink_few_kernel<16>, grid, kThreads, shrink_smem(p.T), stream, p);
+        } else {
+            static KernelOnce once;
+            e = prepare_kernel(lora_shrink_few_kernel<kInline>, shrink_smem(kInline), once, nullptr);
+            if (e != cudaSuccess) return e;
+            e = launch(lora_shrink_few_kernel<kInline>, grid, kThreads, shrink_smem(p.T), stream, p);
+        }
         if (e != cudaSuccess) return e;
         return f16 ? launch_expand<true, true>(p, l, stream) : launch_expand<true, false>(p, l, stream);
     }
-    e = launch(lora_sort_kernel, dim3(1), kSortThreads, sizeof(int) * (p.L + 1), stream, p);
+    // barriers of 32 warps cost more than the rounds that they save, up to what registers keep
+    e = p.T <= 256 * kSortKeep ? launch(lora_sort_kernel<256>, dim3(1), 256, sizeof(int) * (p.L + 1), stream, p)
+                               : launch(lora_sort_kernel<1024>, dim3(1), 1024, sizeof(int) * (p.L + 1), stream, p);
     if (e != cudaSuccess) return e;
     static KernelOnce once;
     e = prepare_kernel(lora_shrink_long_kernel, kLongSmem, once, nullptr);
