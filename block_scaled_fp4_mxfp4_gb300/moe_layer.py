@@ -9,7 +9,11 @@ products) around one small dense product for the router's logits (torch's, in
 bf16, so the logits are rounded to bf16). The next layer's norm adds ``out`` to
 ``h``.
 
-    python -m block_scaled_fp4_mxfp4_gb300.moe_layer [--tokens 1 16 256 4096]
+A layer made with ``few_tokens`` runs up to that many tokens (16 at most) in one
+call instead, ``mxfp4_moe_layer``, whose router reads the norm's output unrounded
+and whose logits stay in fp32.
+
+    python -m block_scaled_fp4_mxfp4_gb300.moe_layer [--tokens 1 16 256 4096] [--few-tokens 16]
 
 times a layer of random weights.
 """
@@ -29,10 +33,11 @@ class MoeLayer:
     gate, up : bf16 [E, I, H]     down : bf16 [E, H, I]
     router   : bf16 [E, H]        norm : bf16 [H]
     bias     : fp32 [E] or None, added to the scores for the choice of experts
+    few_tokens : calls of up to this many tokens take one call of the library (0: none do)
     """
 
     def __init__(self, gate, up, down, router, norm, k, max_tokens, bias=None, score="softmax", groups=1,
-                 topk_groups=1, renormalize=True, scale=1.0, eps=1e-6, group_top=2, workspace=None):
+                 topk_groups=1, renormalize=True, scale=1.0, eps=1e-6, group_top=2, workspace=None, few_tokens=0):
         E, I, H = gate.shape
         self.E, self.I, self.H, self.k = E, I, H, k
         self.router, self.norm, self.bias, self.eps = router, norm, bias, eps
@@ -52,9 +57,18 @@ class MoeLayer:
             raise ValueError(f"workspace has {workspace.numel()} bytes, {max_tokens} tokens need "
                              f"{mx.moe_experts_workspace_bytes(max_tokens, k, E, H, I)}")
         self.workspace = workspace
+        if not 0 <= few_tokens <= mx.MOE_LAYER_MAX_TOKENS:
+            raise ValueError(f"few_tokens must be 0 to {mx.MOE_LAYER_MAX_TOKENS}, got {few_tokens}")
+        self.few_tokens = few_tokens
+        self.few_workspace = mx.moe_layer_workspace(few_tokens, k, E, H, I, dev) if few_tokens else None
 
     def __call__(self, x, residual=None):
         """(out, h): the experts' sum and the residual stream, bf16 [T, H] (h = x without a residual)."""
+        if x.shape[0] <= self.few_tokens:
+            out, h, _, _ = mx.mxfp4_moe_layer(x, self.norm, self.router, self.w13, self.s13, self.w2, self.s2, self.k,
+                                              eps=self.eps, residual=residual, bias=self.bias, workspace=self.few_workspace,
+                                              **self.how)
+            return out, h
         q, sf, h, y = mx.mxfp8_add_rmsnorm_quantize(x, self.norm, self.eps, residual=residual, want_y=True)
         logits = y @ self.router.T
         ids, weights = mx.moe_route(logits, self.k, bias=self.bias, **self.how)
@@ -77,8 +91,9 @@ def main():
     ap.add_argument("--hidden", type=int, default=7168)
     ap.add_argument("--intermediate", type=int, default=2048)
     ap.add_argument("--k", type=int, default=8)
+    ap.add_argument("--few-tokens", type=int, default=0, help="tokens up to which the layer is one call of the library")
     a = ap.parse_args()
-    layer = random_layer(a.experts, a.hidden, a.intermediate, a.k, max(a.tokens))
+    layer = random_layer(a.experts, a.hidden, a.intermediate, a.k, max(a.tokens), few_tokens=a.few_tokens)
     for T in a.tokens:
         x = torch.randn((T, a.hidden), device="cuda").bfloat16()
         res = torch.randn((T, a.hidden), device="cuda").bfloat16()
