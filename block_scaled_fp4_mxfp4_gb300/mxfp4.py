@@ -699,11 +699,12 @@ def lora_add(base, X, A, B, ids, scales=None, ranks=None, C=None, workspace=None
 
 def _heads(t, name, dtype, T, D):
     """Address, heads and strides (between tokens, between heads) of a CUDA tensor [T, H, D] of this type."""
-    if not (t.dtype is dtype and t.dim() == 3 and t.shape[0] == T and t.shape[2] == D and t.is_cuda and t.stride(2) == 1):
+    shape, st = t.shape, t.stride()
+    if not (t.dtype is dtype and len(shape) == 3 and shape[0] == T and shape[2] == D and st[2] == 1 and t.is_cuda):
         _refuse(t, name, dtype, (T, "H", D), "row-major")
-    H = t.shape[1]
+    H = shape[1]
     # strides of dimensions of size one are no distances: torch may give any value
-    return t.data_ptr(), H, t.stride(0) if T > 1 else 0, t.stride(1) if H > 1 else 0
+    return t.data_ptr(), H, st[0] if T > 1 else 0, st[1] if H > 1 else 0
 
 
 def qk_norm_rope(q, k, table=None, positions=None, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -714,22 +715,29 @@ def qk_norm_rope(q, k, table=None, positions=None, q_weight=None, k_weight=None,
     and sines of every position (None: no rotation), q_weight and k_weight [D] the
     norms' weights (None: no norm). Views of a joint projection need no copy; an
     output may be its own input."""
-    if q.dim() != 3:
-        raise ValueError(f"q must have 3 dims, got {tuple(q.shape)}")
-    dtype = q.dtype
+    dtype, shape = q.dtype, q.shape
     if dtype is not torch.bfloat16 and dtype is not torch.float16:
         raise ValueError(f"q must be bf16 or fp16, got {dtype}")
-    T, _, D = q.shape
+    if len(shape) != 3:
+        raise ValueError(f"q must have 3 dims, got {tuple(shape)}")
+    T, _, D = shape
     pq, Hq, q_st, q_sh = _heads(q, "q", dtype, T, D)
     pk, Hk, k_st, k_sh = _heads(k, "k", dtype, T, D)
+    # outputs made here need no check
     if q_out is None:
         q_out = _output((T, Hq, D), dtype, q.device, stream)
+        po, qo_st, qo_sh = q_out.data_ptr(), Hq * D, D
+    else:
+        po, ho, qo_st, qo_sh = _heads(q_out, "q_out", dtype, T, D)
+        if ho != Hq:
+            raise ValueError(f"q_out has {ho} heads, q {Hq}")
     if k_out is None:
         k_out = _output((T, Hk, D), dtype, q.device, stream)
-    po, ho, qo_st, qo_sh = _heads(q_out, "q_out", dtype, T, D)
-    pp, hp, ko_st, ko_sh = _heads(k_out, "k_out", dtype, T, D)
-    if ho != Hq or hp != Hk:
-        raise ValueError(f"outputs have {ho} and {hp} heads, inputs {Hq} and {Hk}")
+        pp, ko_st, ko_sh = k_out.data_ptr(), Hk * D, D
+    else:
+        pp, hp, ko_st, ko_sh = _heads(k_out, "k_out", dtype, T, D)
+        if hp != Hk:
+            raise ValueError(f"k_out has {hp} heads, k {Hk}")
     pt, pos, P, rot, pos64 = None, None, 0, 0, 0
     if table is not None:
         if table.dim() != 2:
