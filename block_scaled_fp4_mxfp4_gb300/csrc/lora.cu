@@ -12,9 +12,9 @@
 //           and reads each x and each a once, from global memory straight into the
 //           MMA's registers (which order of K the operands take is free as long as it
 //           is the same for both: a lane holds 8 neighbouring k, one 16-byte vector).
-//           Longer batches: tcgen05.mma kind::f16 with the ranks as the 128 rows and up
-//           to 128 tokens as columns, a_a by TMA, token rows gathered by cp.async, which
-//           take a ring of shared memory at the rate of HBM.
+//           Longer batches: tcgen05.mma kind::f16 with up to 128 tokens as rows and the
+//           ranks as columns, token rows gathered by cp.async, a_a by TMA, which take a
+//           ring of shared memory at the rate of HBM.
 //   expand  u B_a^T + base, for up to 64 tokens a block. Rows of the MMA are tokens, columns
 //           are channels, chosen so that a lane ends with 8 neighbouring channels of a
 //           token: one 16-byte load of base and one store. u, summed in fp32, enters as two
@@ -312,22 +312,23 @@ __global__ void __launch_bounds__(kThreads, MOST == 16 ? 2 : 1) lora_shrink_few_
         shrink_tile<4, MOST>(p, a, rows, tok, tile.count, kb, ke, red);
 }
 
-// More than kInline tokens, on the tensor core. Grid: tiles x splits of K x blocks of 128
-// ranks. A stage is 64 elements of K: the adapter's rows (as many as it has, up to 128; the
-// MMA takes 128, and what its further rows read is whatever follows) and 128 token rows,
-// both in the 128-byte swizzle. Warps:
-//   0-3  gather token rows by cp.async; then store the sums, a rank a lane
+// More than kInline tokens, on the tensor core. Grid: tiles x splits of K. A stage is 64
+// elements of K of 128 token rows (an MMA takes 128; what its rows beyond the tile's read is
+// whatever was there) and of the adapter's rows, both in the 128-byte swizzle. Warps:
+//   0-3  gather token rows by cp.async; then store the sums, a token a lane
 //   4    lane 0 loads the adapter's rows by TMA
 //   5    issues the MMAs (an elected lane); owns TMEM
 constexpr int kLongThreads = 192;
 constexpr int kLongStages = 8;
 constexpr uint32_t kLongTokens = kTile * 128;
-constexpr uint32_t kLongSmem = 112 * 1024;       // two blocks an SM
+constexpr uint32_t kLongSmem = 112 * 1024;       // two blocks an SM,
+constexpr uint32_t kLongSmemOne = 224 * 1024;    // one, for more than 128 ranks
 
 struct LongParams {
     CUtensorMap tm_a;                // A as [L * R, K] bf16, box 64 elements x `rows`
     LoraParams l;
-    int rows, stages;                // rows of a box; stages of the ring
+    int rows, stages;                // R rounded up to 16; stages of the ring
+    uint32_t columns;                // of TMEM: a power of two
     uint64_t wait_ns;
 };
 
@@ -365,7 +366,7 @@ __global__ void __launch_bounds__(kLongThreads, 2) lora_shrink_long_kernel(const
     const LoraParams &p = lp.l;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int S = lp.stages;
-    const uint32_t a_bytes = lp.rows * 128u, stage_bytes = a_bytes + kLongTokens;
+    const uint32_t a_bytes = lp.rows * 128u, stage_bytes = kLongTokens + a_bytes;
     LongShared &sh = *reinterpret_cast<LongShared *>(smem + S * stage_bytes);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     if (tid == 0) {
@@ -382,14 +383,14 @@ __global__ void __launch_bounds__(kLongThreads, 2) lora_shrink_long_kernel(const
     grid_launch_dependents();
     // whole blocks leave here, before TMEM is theirs
     const int4 rec = __ldcg(p.tiles + blockIdx.x);
-    const int adapter = rec.x, count = rec.z, rank0 = blockIdx.z * kTile;
-    if (adapter == p.L || rank_of(p, adapter) <= rank0) return;       // nobody reads sums beyond the rank
+    const int adapter = rec.x, count = rec.z;
+    if (adapter == p.L || rank_of(p, adapter) == 0) return;
     const int per = (p.K + 64 * p.splits - 1) / (64 * p.splits) * 64;
     const int kb = static_cast<int>(min(static_cast<int64_t>(blockIdx.y) * per, static_cast<int64_t>(p.K)));
     const int ke = static_cast<int>(min(static_cast<int64_t>(kb) + per, static_cast<int64_t>(p.K)));
     const int steps = (ke - kb + 63) / 64;
     if (warp == 5) {
-        tmem_alloc(&sh.tmem, kTile);
+        tmem_alloc(&sh.tmem, lp.columns);
         tmem_relinquish();
     }
     if (tid < count) sh.tok[tid] = __ldcg(p.order + rec.y + tid);
@@ -397,7 +398,6 @@ __global__ void __launch_bounds__(kLongThreads, 2) lora_shrink_long_kernel(const
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
-    const int n = (count + 15) & ~15;
 
     if (warp == 4) {
         if (lane == 0) {
@@ -409,14 +409,14 @@ __global__ void __launch_bounds__(kLongThreads, 2) lora_shrink_long_kernel(const
                 ok = mbar_wait(&sh.empty[s], ((i / S) & 1) ^ 1u, &g_lora_error, kErrWaitEmpty, lp.wait_ns);
                 if (!ok) break;
                 mbar_arrive_expect_tx(&sh.a_full[s], a_bytes);
-                tma_load_2d(smem + s * stage_bytes, &lp.tm_a, kb + 64 * i, adapter * p.R + rank0, &sh.a_full[s], pol);
+                tma_load_2d(smem + s * stage_bytes + kLongTokens, &lp.tm_a, kb + 64 * i, adapter * p.R, &sh.a_full[s], pol);
             }
             // copies in flight land before the block leaves
             for (int j = max(0, i - S); j < i; ++j)
                 mbar_wait(&sh.a_full[j % S], (j / S) & 1, &g_lora_error, kErrWaitDrain);
         }
     } else if (warp == 5) {
-        const uint32_t idesc = idesc_bf16(n, 128);
+        const uint32_t idesc = __shfl_sync(0xffffffffu, idesc_bf16(lp.rows, 128), 0);
         bool ok = true;
         for (int i = 0; i < steps; ++i) {
             const int s = i % S;
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(kLongThreads, 2) lora_shrink_long_kernel(const
             fence_proxy_async_smem();        // cp.async wrote through the generic proxy
             tc_fence_after();
             const uint64_t ad = sdesc_sw128(smem_u32(smem + s * stage_bytes));
-            const uint64_t bd = sdesc_sw128(smem_u32(smem + s * stage_bytes + a_bytes));
+            const uint64_t bd = sdesc_sw128(smem_u32(smem + s * stage_bytes + kLongTokens));
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) mma_tc_bf16(tmem, ad + 2 * k, bd + 2 * k, idesc, i > 0 || k > 0 ? 1u : 0u);
@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(kLongThreads, 2) lora_shrink_long_kernel(const
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             src[j] = r0 + 16 * j < count ? p.x + static_cast<int64_t>(sh.tok[r0 + 16 * j]) * p.ldx : nullptr;
-        const uint32_t dst = smem_u32(smem) + a_bytes + r0 * 128 + ((c ^ (r0 & 7)) << 4);
+        const uint32_t dst = smem_u32(smem) + r0 * 128 + ((c ^ (r0 & 7)) << 4);
         bool ok = true;
         int i = 0;
         for (; i < steps; ++i) {
@@ -464,18 +464,20 @@ __global__ void __launch_bounds__(kLongThreads, 2) lora_shrink_long_kernel(const
             ok = mbar_wait_warp(&sh.empty[j % S], (j / S) & 1, &g_lora_error, kErrWaitDrain);
         const bool done = mbar_wait_warp(&sh.done, 0, &g_lora_error, kErrWaitAccum);
         tc_fence_after();
-        const int r = 32 * warp + lane;
-        if (ok && done && rank0 + 32 * warp < p.R) {
-            for (int c0 = 0; c0 < count; c0 += 32) {
+        const int t = 32 * warp + lane;              // this lane's token
+        if (ok && done && 32 * warp < count) {
+            float *u = p.u + (static_cast<int64_t>(blockIdx.y) * p.T + (t < count ? sh.tok[t] : 0)) * p.R;
+            for (int c0 = 0; c0 < p.R; c0 += 32) {
                 uint32_t v[32];
+                // 32 columns: those beyond the MMA's are not stored
                 tmem_ld32(tmem + c0 + (static_cast<uint32_t>(warp * 32) << 16), v);
                 tmem_ld_wait();
-                if (rank0 + r < p.R) {
-                    float *u = p.u + static_cast<int64_t>(blockIdx.y) * p.T * p.R + rank0 + r;
+                if (t < count)
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (c0 + j < count) u[static_cast<int64_t>(sh.tok[c0 + j]) * p.R] = steps ? __uint_as_float(v[j]) : 0.0f;
-                }
+                    for (int j = 0; j < 32; j += 4)
+                        if (c0 + j < p.R)
+                            *reinterpret_cast<uint4 *>(u + c0 + j) =
+                                steps ? make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]) : make_uint4(0, 0, 0, 0);
             }
         }
     }
@@ -484,7 +486,7 @@ __global__ void __launch_bounds__(kLongThreads, 2) lora_shrink_long_kernel(const
     __syncthreads();
     if (warp == 5) {
         tc_fence_after();
-        tmem_dealloc(tmem, kTile);
+        tmem_dealloc(tmem, lp.columns);
     }
 }
 
@@ -506,6 +508,14 @@ __device__ __forceinline__ uint32_t pack2(float x, float y)
     }
     const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
     return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// 16 bytes of a line that is read whole, soon after one another.
+__device__ __forceinline__ uint4 load_line(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.L2::128B.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
 }
 
 // The elements of a vector of 8 below `n`, zeros for the others.
@@ -539,81 +549,91 @@ __device__ __forceinline__ void load_b(uint4 (&w)[4], const uint16_t *brow, int 
     }
 }
 
-// The update of one chunk for 16 tokens: d += (low + high part of u) B^T over 32 ranks.
-__device__ __forceinline__ void multiply(float (&d)[4][4], const uint4 (&w)[4], const uint32_t *hrow, const uint32_t *lrow,
-                                         int ldu)
+// u of 16 tokens for 32 ranks in the MMAs' order: a lane's eight ranks of tokens g and g + 8,
+// high and low parts.
+struct RowsOfU {
+    uint4 h0, h1, l0, l1;
+};
+__device__ __forceinline__ RowsOfU load_u(const uint32_t *hrow, const uint32_t *lrow, int ldu)
 {
-    // four words of hi / lo hold this lane's eight ranks of a token
-    const uint4 h0 = *reinterpret_cast<const uint4 *>(hrow), h1 = *reinterpret_cast<const uint4 *>(hrow + 8 * ldu);
-    const uint4 l0 = *reinterpret_cast<const uint4 *>(lrow), l1 = *reinterpret_cast<const uint4 *>(lrow + 8 * ldu);
+    return RowsOfU{*reinterpret_cast<const uint4 *>(hrow), *reinterpret_cast<const uint4 *>(hrow + 8 * ldu),
+                   *reinterpret_cast<const uint4 *>(lrow), *reinterpret_cast<const uint4 *>(lrow + 8 * ldu)};
+}
+
+// d += u B^T over 32 ranks, for one chunk of channels and 16 tokens.
+__device__ __forceinline__ void multiply(float (&d)[4][4], const uint4 (&w)[4], const RowsOfU &u)
+{
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        mma_bf16(d[j], l0.x, l1.x, l0.y, l1.y, w[j].x, w[j].y);
-        mma_bf16(d[j], l0.z, l1.z, l0.w, l1.w, w[j].z, w[j].w);
-        mma_bf16(d[j], h0.x, h1.x, h0.y, h1.y, w[j].x, w[j].y);
-        mma_bf16(d[j], h0.z, h1.z, h0.w, h1.w, w[j].z, w[j].w);
+        mma_bf16(d[j], u.l0.x, u.l1.x, u.l0.y, u.l1.y, w[j].x, w[j].y);
+        mma_bf16(d[j], u.l0.z, u.l1.z, u.l0.w, u.l1.w, w[j].z, w[j].w);
+        mma_bf16(d[j], u.h0.x, u.h1.x, u.h0.y, u.h1.y, w[j].x, w[j].y);
+        mma_bf16(d[j], u.h0.z, u.h1.z, u.h0.w, u.h1.w, w[j].z, w[j].w);
     }
 }
 
-// Columns 32c .. 32c + 31 of C for the tile's tokens, c from c0 on: channel of column `col` of the
-// n-tile j is 32c + 8 (col / 2) + 2j + (col & 1), so lane (g, q) ends with channels 8q .. 8q + 7 of
-// tokens g and g + 8 of each 16. KEPT: the ranks are at most 32 * KEPT, and a chunk's rows of B
-// stay in registers for all of the tokens (0: they are loaded again for every 16).
+// Columns 32c .. 32c + 31 of C for 16 tokens, c0 <= c < c1: channel of column `col` of the n-tile j
+// is 32c + 8 (col / 2) + 2j + (col & 1), so lane (g, q) ends with channels 8q .. 8q + 7 of tokens g and
+// g + 8. hi, lo, tok: of the first of the tokens. KEPT: the ranks are at most 32 * KEPT, and
+// the next chunk's rows of B and base are on their way while one is multiplied (0: any
+// rank, loaded as it goes).
 template <bool F16, int KEPT>
 __device__ __forceinline__ void expand_chunks(const LoraParams &p, const uint16_t *b, int rank, const uint32_t *hi,
-                                              const uint32_t *lo, int ldu, const int *tok, int count, int c0, int chunks, int step)
+                                              const uint32_t *lo, int ldu, const int *tok, int count, int c0, int c1)
 {
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int first = 8 * (g >> 1) + (g & 1);            // this lane's row of B in n-tile 0 of a chunk
     const uint32_t *hrow = hi + g * ldu + 4 * q, *lrow = lo + g * ldu + 4 * q;
-    for (int c = c0; c < chunks; c += step) {
-        const int n = 32 * c + 8 * q, channels = p.N - 32 * c - first;
-        const bool in = n < p.N;
-        const uint16_t *brow = b + static_cast<int64_t>(32 * c + first) * p.R + 8 * q;
-        uint4 w[KEPT ? KEPT : 1][4];
+    const uint16_t *base[2];
+    uint16_t *out[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const bool has = 8 * h + g < count;
+        base[h] = has ? p.base + tok[8 * h + g] * p.ldb + 8 * q : nullptr;
+        out[h] = has ? p.c + tok[8 * h + g] * p.ldc + 8 * q : nullptr;
+    }
+    const uint16_t *brow = b + static_cast<int64_t>(32 * c0 + first) * p.R + 8 * q;
+    uint4 w[KEPT ? KEPT : 1][4], old[2];
+    auto fetch = [&](int c) {
+        if (c >= c1) return;
         if constexpr (KEPT > 0)
 #pragma unroll
-            for (int k = 0; k < KEPT; ++k) load_b(w[k], brow, p.R, 32 * k, channels, rank - 32 * k - 8 * q);
-        uint4 old[2], next[2];
-        auto fetch = [&](uint4 (&v)[2], int m) {
+            for (int k = 0; k < KEPT; ++k)
+                load_b(w[k], brow, p.R, 32 * k, p.N - 32 * c - first, rank - 32 * k - 8 * q);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int t = m + 8 * h + g;
-                if (in && t < count) v[h] = *reinterpret_cast<const uint4 *>(p.base + tok[t] * p.ldb + n);
+        for (int h = 0; h < 2; ++h)
+            if (base[h] && 32 * c + 8 * q < p.N) old[h] = load_line(base[h] + 32 * c);
+    };
+    fetch(c0);
+    for (int c = c0; c < c1; ++c) {
+        float d[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d[j][e] = 0.0f;
+        if constexpr (KEPT > 0) {
+#pragma unroll
+            for (int k = 0; k < KEPT; ++k) multiply(d, w[k], load_u(hrow + 16 * k, lrow + 16 * k, ldu));
+        } else {
+            for (int k = 0; k < rank; k += 32) {
+                load_b(w[0], brow, p.R, k, p.N - 32 * c - first, rank - k - 8 * q);
+                multiply(d, w[0], load_u(hrow + k / 2, lrow + k / 2, ldu));
             }
-        };
-        fetch(next, 0);
-        for (int m = 0; m < count; m += 16) {
-            old[0] = next[0];
-            old[1] = next[1];
-            fetch(next, m + 16);
-            float d[4][4];
+        }
+        const uint4 was[2] = {old[0], old[1]};
+        brow += 32 * p.R;
+        fetch(c + 1);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+        for (int h = 0; h < 2; ++h) {
+            if (!out[h] || 32 * c + 8 * q >= p.N) continue;
+            const uint32_t v[4] = {was[h].x, was[h].y, was[h].z, was[h].w};
+            uint32_t o[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) d[j][e] = 0.0f;
-            if constexpr (KEPT > 0) {
-#pragma unroll
-                for (int k = 0; k < KEPT; ++k) multiply(d, w[k], hrow + m * ldu + 16 * k, lrow + m * ldu + 16 * k, ldu);
-            } else {
-                for (int k = 0; k < rank; k += 32) {
-                    load_b(w[0], brow, p.R, k, channels, rank - k - 8 * q);
-                    multiply(d, w[0], hrow + m * ldu + k / 2, lrow + m * ldu + k / 2, ldu);
-                }
+            for (int j = 0; j < 4; ++j) {
+                const float2 t = unpack2<F16>(v[j]);
+                o[j] = pack2<F16>(t.x + d[j][2 * h], t.y + d[j][2 * h + 1]);
             }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int t = m + 8 * h + g;
-                if (!in || t >= count) continue;
-                const uint32_t v[4] = {old[h].x, old[h].y, old[h].z, old[h].w};
-                uint32_t o[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 f = unpack2<F16>(v[j]);
-                    o[j] = pack2<F16>(f.x + d[j][2 * h], f.y + d[j][2 * h + 1]);
-                }
-                *reinterpret_cast<uint4 *>(p.c + tok[t] * p.ldc + n) = make_uint4(o[0], o[1], o[2], o[3]);
-            }
+            *reinterpret_cast<uint4 *>(out[h] + 32 * c) = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
 }
@@ -630,7 +650,7 @@ __device__ __forceinline__ void prefetch_l2(const void *p)
 // Grid: halves of tiles (up to kInline tokens: tiles) x blocks of channels. Shared memory: u as
 // high and low bf16, [64 tokens][ranks rounded up to 32].
 template <bool INLINE, bool F16>
-__global__ void __launch_bounds__(kThreads) lora_expand_kernel(const LoraParams p)
+__global__ void __launch_bounds__(kThreads, 2) lora_expand_kernel(const LoraParams p)
 {
     extern __shared__ uint32_t ushared[];
     __shared__ int tok[kHalf], ids[kInline], found[1];
@@ -675,63 +695,84 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(const LoraParams 
     const uint16_t *b = p.b + static_cast<int64_t>(tile.adapter) * p.N * p.R;
     const int rows = (tile.count + 15) / 16 * 16, cols = max(1, (rank + 31) / 32) * 32;   // 32 zeros of an adapter of rank 0
     const int ldu = u_stride((p.R + 31) / 32 * 32);
-    const int c0 = blockIdx.y * kWarps + warp, step = gridDim.y * kWarps;
-    // this warp's first channels go to L2 while u is made
-    if (c0 < chunks) {
-        const int ch = 32 * c0 + lane;
-        if (ch < p.N)
+    // The block's warps share its 16-token parts (1, 2 or 4 of them) and, those of a part, its chunks.
+    const int parts = tile.count <= 16 ? 1 : (tile.count <= 32 ? 2 : 4), part = warp & (parts - 1);
+    // neighbouring chunks, which share lines of 128 bytes, go to one warp
+    const int lanes = gridDim.y * (kWarps / parts), mine = blockIdx.y * (kWarps / parts) + warp / parts;
+    const int c0 = static_cast<int>(static_cast<int64_t>(chunks) * mine / lanes);
+    const int c1 = static_cast<int>(static_cast<int64_t>(chunks) * (mine + 1) / lanes);
+    // this warp's part of base and, once for all parts, of B go to L2 while u is made
+    if (lane < 16 && 16 * part + lane < tile.count)
+        for (int n = 32 * c0; n < min(32 * c1, p.N); n += 64) prefetch_l2(p.base + tok[16 * part + lane] * p.ldb + n);
+    if (part == 0)
+        for (int ch = 32 * c0 + lane; ch < min(32 * c1, p.N); ch += 32)
             for (int k = 0; k < rank; k += 64) prefetch_l2(b + static_cast<int64_t>(ch) * p.R + k);
-        for (int t = lane; t < tile.count; t += 32) prefetch_l2(p.base + tok[t] * p.ldb + 32 * c0);
-    }
     const float scale = p.scales ? p.scales[tile.adapter] : 1.0f;
     grid_dependency_wait();
     grid_launch_dependents();
     uint32_t *hi = ushared, *lo = ushared + kHalf * ldu;
-    // four neighbouring ranks of a token a thread
+    // four neighbouring ranks of two tokens a thread, eight splits on their way
     for (int r = 4 * (threadIdx.x & 7); r < cols; r += 32)
-        for (int t = threadIdx.x >> 3; t < rows; t += kThreads / 8) {
-            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (t < tile.count && r < rank) {
-                const float *u = p.u + static_cast<int64_t>(tok[t]) * p.R + r;
-                const int64_t split = static_cast<int64_t>(p.T) * p.R;
-                for (int s0 = 0; s0 < p.splits; s0 += 8) {
-                    float4 part[8];
-#pragma unroll
-                    for (int s = 0; s < 8; ++s)
-                        if (s0 + s < p.splits) part[s] = __ldcg(reinterpret_cast<const float4 *>(u + (s0 + s) * split));
-#pragma unroll
-                    for (int s = 0; s < 8; ++s) {
-                        if (s0 + s >= p.splits) continue;
-                        v[0] += part[s].x;
-                        v[1] += part[s].y;
-                        v[2] += part[s].z;
-                        v[3] += part[s].w;
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = r + i < rank ? v[i] * scale : 0.0f;
-            }
-            uint32_t hb[2], lb[2];
+        for (int t0 = threadIdx.x >> 3; t0 < rows; t0 += kThreads / 4) {
+            float4 sum[2];
+            const float *u[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-                hb[i] = *reinterpret_cast<const uint32_t *>(&h);
-                // what rounds to infinity has no low part
-                const float hx = __uint_as_float(hb[i] << 16), hy = __uint_as_float(hb[i] & 0xFFFF0000u);
-                const __nv_bfloat162 l = __floats2bfloat162_rn(isinf(hx) ? 0.0f : v[2 * i] - hx, isinf(hy) ? 0.0f : v[2 * i + 1] - hy);
-                lb[i] = *reinterpret_cast<const uint32_t *>(&l);
+                const int t = t0 + i * (kThreads / 8);
+                sum[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                u[i] = t < tile.count && r < rank ? p.u + static_cast<int64_t>(tok[t]) * p.R + r : nullptr;
             }
-            *reinterpret_cast<uint2 *>(hi + t * ldu + r / 2) = make_uint2(hb[0], hb[1]);
-            *reinterpret_cast<uint2 *>(lo + t * ldu + r / 2) = make_uint2(lb[0], lb[1]);
+            const int64_t split = static_cast<int64_t>(p.T) * p.R;
+            for (int s0 = 0; s0 < p.splits; s0 += 8) {
+                float4 some[2][8];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int s = 0; s < 8; ++s)
+                        if (u[i] && s0 + s < p.splits)
+                            some[i][s] = __ldcg(reinterpret_cast<const float4 *>(u[i] + (s0 + s) * split));
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int s = 0; s < 8; ++s) {
+                        if (!u[i] || s0 + s >= p.splits) continue;
+                        sum[i].x += some[i][s].x;
+                        sum[i].y += some[i][s].y;
+                        sum[i].z += some[i][s].z;
+                        sum[i].w += some[i][s].w;
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int t = t0 + i * (kThreads / 8);
+                if (t >= rows) continue;
+                float v[4] = {sum[i].x, sum[i].y, sum[i].z, sum[i].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = r + k < rank ? v[k] * scale : 0.0f;
+                uint32_t hb[2], lb[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+                    hb[k] = *reinterpret_cast<const uint32_t *>(&h);
+                    // what rounds to infinity has no low part
+                    const float hx = __uint_as_float(hb[k] << 16), hy = __uint_as_float(hb[k] & 0xFFFF0000u);
+                    const __nv_bfloat162 l = __floats2bfloat162_rn(isinf(hx) ? 0.0f : v[2 * k] - hx, isinf(hy) ? 0.0f : v[2 * k + 1] - hy);
+                    lb[k] = *reinterpret_cast<const uint32_t *>(&l);
+                }
+                *reinterpret_cast<uint2 *>(hi + t * ldu + r / 2) = make_uint2(hb[0], hb[1]);
+                *reinterpret_cast<uint2 *>(lo + t * ldu + r / 2) = make_uint2(lb[0], lb[1]);
+            }
         }
     __syncthreads();
-    // 64 ranks of B are what the registers hold beside the rest
+    // 64 ranks of B and u are what the registers hold beside the rest
+    const int left = tile.count - 16 * part, at = 16 * part * ldu;
+    if (left <= 0) return;
     if (rank <= 32)
-        expand_chunks<F16, 1>(p, b, rank, hi, lo, ldu, tok, tile.count, c0, chunks, step);
+        expand_chunks<F16, 1>(p, b, rank, hi + at, lo + at, ldu, tok + 16 * part, left, c0, c1);
     else if (rank <= 64)
-        expand_chunks<F16, 2>(p, b, rank, hi, lo, ldu, tok, tile.count, c0, chunks, step);
+        expand_chunks<F16, 2>(p, b, rank, hi + at, lo + at, ldu, tok + 16 * part, left, c0, c1);
     else
-        expand_chunks<F16, 0>(p, b, rank, hi, lo, ldu, tok, tile.count, c0, chunks, step);
+        expand_chunks<F16, 0>(p, b, rank, hi + at, lo + at, ldu, tok + 16 * part, left, c0, c1);
 }
 
 template <typename Kern, typename P>
@@ -812,19 +853,21 @@ cudaError_t launch_lora(LoraParams p, const LoraLayout &l, bool f16, cudaStream_
                                : launch(lora_sort_kernel<1024>, dim3(1), 1024, sizeof(int) * (p.L + 1), stream, p);
     if (e != cudaSuccess) return e;
     static KernelOnce once;
-    e = prepare_kernel(lora_shrink_long_kernel, kLongSmem, once, nullptr);
+    e = prepare_kernel(lora_shrink_long_kernel, kLongSmemOne, once, nullptr);
     if (e != cudaSuccess) return e;
     LongParams lp;
     lp.l = p;
-    lp.rows = std::min(p.R, kTile);
-    lp.stages = std::min<int>(kLongStages, (kLongSmem - 1024 - sizeof(LongShared)) / (lp.rows * 128 + kLongTokens));
+    lp.rows = (p.R + 15) & ~15;
+    const uint32_t smem = lp.rows <= 128 ? kLongSmem : kLongSmemOne;
+    lp.stages = std::min<int>(kLongStages, (smem - 1024 - sizeof(LongShared)) / (kLongTokens + lp.rows * 128));
+    lp.columns = 32;
+    while (lp.columns < static_cast<uint32_t>(lp.rows)) lp.columns *= 2;
     lp.wait_ns = wait_limit_ns();
     if (!encode_map_2d(&lp.tm_a, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.a, p.K, static_cast<uint64_t>(p.L) * p.R,
                        static_cast<uint64_t>(p.K) * 2, 64u, lp.rows, CU_TENSOR_MAP_SWIZZLE_128B,
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
         return cudaErrorInvalidValue;
-    e = launch(lora_shrink_long_kernel, dim3(l.max_tiles, l.splits, (p.R + kTile - 1) / kTile), kLongThreads, kLongSmem,
-               stream, lp);
+    e = launch(lora_shrink_long_kernel, dim3(l.max_tiles, l.splits), kLongThreads, smem, stream, lp);
     if (e != cudaSuccess) return e;
     return f16 ? launch_expand<false, true>(p, l, stream) : launch_expand<false, false>(p, l, stream);
 }

@@ -31,7 +31,7 @@ def lora(**kw):
     (dict(T=0), OK), (dict(T=0, x=None, a=None, b=None, ids=None, base=None, c=None, ws=None), OK), (dict(T=-1), INVALID),
     (dict(K=0), INVALID), (dict(N=0), INVALID), (dict(R=0), INVALID), (dict(L=0), INVALID), (dict(dtype=2), INVALID),
     (dict(K=60), SHAPE), (dict(N=92), SHAPE), (dict(R=12), SHAPE), (dict(R=264), SHAPE), (dict(L=4097), SHAPE),
-    (dict(T=1 << 31), SHAPE), (dict(K=1 << 31, ldx=1 << 31), SHAPE), (dict(N=1 << 31), SHAPE),
+    (dict(T=1 << 31), SHAPE), (dict(K=(1 << 30) + 8, ldx=1 << 31), SHAPE), (dict(N=(1 << 30) + 8), SHAPE),
     (dict(x=None), INVALID), (dict(a=None), INVALID), (dict(b=None), INVALID), (dict(ids=None), INVALID),
     (dict(base=None), INVALID), (dict(c=None), INVALID), (dict(ws=None), INVALID), (dict(ldx=56), INVALID),
     (dict(ldb=88), INVALID), (dict(ldc=88), INVALID), (dict(c=16, ldc=104), INVALID), (dict(ldx=68), MISALIGNED),
@@ -150,3 +150,27 @@ def test_moe_layer_workspace_grows_with_tokens():
     sizes = [f(T, 8, 64, 2048, 768) for T in range(1, 17)]
     assert sizes == sorted(sizes) and sizes[0] > 0
     assert f(0, 8, 64, 2048, 768) == 0 and f(17, 8, 64, 2048, 768) == 0 and f(4, 8, 64, 2000, 768) == 0
+
+
+@pytest.mark.parametrize("code", range(127))
+def test_six_digits_are_the_value_of_an_e4m3_code(code):
+    """The few-token layer's form of an MXFP8 activation: its magnitude, a whole number of 2^-9, from six E2M1 digits that
+    stand 8 apart, as csrc/moe_few.cu makes them."""
+    n = int(torch.tensor([code], dtype=torch.uint8).view(torch.float8_e4m3fn).double() * 512)
+    assert n < 1 << 18
+    digits, rest = [], n
+    for _ in range(5):
+        d = ((rest + 3) & 7) - 3
+        rest = (rest - d) // 8
+        digits.append(d)
+    digits.append(rest)
+    if rest in (5, 7):
+        digits[5] = 6
+        digits[4] += -8 if rest == 5 else 8
+    # an E2M1 code for each, the value of which is half the digit
+    levels = [0, 0.5, 1, 1.5, 2, 3, 4, 6]
+    codes = [abs(d) if abs(d) <= 4 else abs(d) // 2 + 2 for d in digits]
+    assert all(2 * levels[c] == abs(d) for c, d in zip(codes, digits))
+    assert sum(d * 8 ** i for i, d in enumerate(digits)) == n
+    # scales 2^(e - 8 + 3 i) of an activation scale 2^e: half a digit of 8^i in units of 2^-9
+    assert sum((1 if d > 0 else -1) * levels[c] * 2.0 ** (3 * i - 8) for i, (c, d) in enumerate(zip(codes, digits))) == n / 512
