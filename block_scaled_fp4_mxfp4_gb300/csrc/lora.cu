@@ -42,7 +42,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kTile = 128;         // tokens of a tile
 constexpr int kHalf = 64;          // tokens of a block of the second product
 constexpr int kInline = 64;        // tokens up to which blocks work out the tiles themselves
-constexpr int kRanks = 64;         // ranks of one block of the first product, up to kInline tokens
+constexpr int kRanks = 64;         // ranks of one block of the first product, up to kInline tokens, and of the ring of the second
 constexpr int kMaxRank = 256;
 
 // ------------------------------------------------------------------ tiles
@@ -572,6 +572,20 @@ __device__ __forceinline__ void multiply(float (&d)[4][4], const uint4 (&w)[4], 
     }
 }
 
+// Eight channels of base and their sums of token g (h = 0) or g + 8, rounded once.
+template <bool F16>
+__device__ __forceinline__ uint4 updated(const uint4 &base, const float (&d)[4][4], int h)
+{
+    const uint32_t v[4] = {base.x, base.y, base.z, base.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 t = unpack2<F16>(v[j]);
+        o[j] = pack2<F16>(t.x + d[j][2 * h], t.y + d[j][2 * h + 1]);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 // Columns 32c .. 32c + 31 of C for 16 tokens, c0 <= c < c1: channel of column `col` of the n-tile j
 // is 32c + 8 (col / 2) + 2j + (col & 1), so lane (g, q) ends with channels 8q .. 8q + 7 of tokens g and
 // g + 8. hi, lo, tok: of the first of the tokens. KEPT: the ranks are at most 32 * KEPT, and
@@ -625,16 +639,89 @@ __device__ __forceinline__ void expand_chunks(const LoraParams &p, const uint16_
         fetch(c + 1);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            if (!out[h] || 32 * c + 8 * q >= p.N) continue;
-            const uint32_t v[4] = {was[h].x, was[h].y, was[h].z, was[h].w};
-            uint32_t o[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 t = unpack2<F16>(v[j]);
-                o[j] = pack2<F16>(t.x + d[j][2 * h], t.y + d[j][2 * h + 1]);
-            }
-            *reinterpret_cast<uint4 *>(out[h] + 32 * c) = make_uint4(o[0], o[1], o[2], o[3]);
+            if (out[h] && 32 * c + 8 * q < p.N) *reinterpret_cast<uint4 *>(out[h] + 32 * c) = updated<F16>(was[h], d, h);
         }
+    }
+}
+
+// The same for more than 16 tokens and adapters of up to 64 ranks (kRanks): the `parts` warps of a lane group share
+// a chunk's rows of B. kAhead chunks of B and of every warp's base are on their way to
+// shared memory, by cp.async. With both in registers one chunk ahead, a warp had 1 KB of base in
+// flight, and this part took 13 us at 4096 x 2112 where its bytes take 5.
+constexpr int kAhead = 3;
+constexpr uint32_t kRingB = 32 * 128;            // 32 channels of up to 64 ranks
+constexpr uint32_t kRingBase = 32 * 32;          // 16 tokens x 32 channels
+
+__host__ __device__ constexpr uint32_t ring_bytes() { return kAhead * (kWarps / 2 * kRingB + kWarps * kRingBase); }
+
+template <bool F16>
+__device__ __forceinline__ void expand_ring(const LoraParams &p, const uint16_t *b, int rank, const uint32_t *hi,
+                                            const uint32_t *lo, int ldu, const int *tok, int count, int c0, int c1, int part,
+                                            int parts, uint8_t *ring)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const int group = warp / parts, in_group = part * 32 + lane, blocks = (rank + 31) / 32;
+    uint8_t *bring = ring + group * kAhead * kRingB;
+    uint8_t *own = ring + kAhead * (kWarps / 2 * kRingB + warp * kRingBase) + lane * 16;
+    const uint32_t *hrow = hi + g * ldu + 4 * q, *lrow = lo + g * ldu + 4 * q;
+    const uint16_t *base[2];
+    uint16_t *out[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const bool has = 8 * h + g < count;
+        base[h] = has ? p.base + tok[8 * h + g] * p.ldb + 8 * q : nullptr;
+        out[h] = has ? p.c + tok[8 * h + g] * p.ldc + 8 * q : nullptr;
+    }
+    auto request = [&](int c, int slot) {
+        if (c < c1) {
+            // row r of the chunk, ranks 8v to 8v + 7: half a line further for odd rows, so that the
+            // rows a load takes at once lie in different banks
+            for (int i = in_group; i < 32 * 4 * blocks; i += 32 * parts) {
+                const int r = blocks == 1 ? i >> 2 : i >> 3, v = blocks == 1 ? i & 3 : i & 7;
+                if (32 * c + r < p.N && 8 * v < rank)
+                    cp_async<16>(smem_u32(bring + slot * kRingB + r * 128 + ((16 * v) ^ ((r & 1) << 6))),
+                                 b + static_cast<int64_t>(32 * c + r) * p.R + 8 * v);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (base[h] && 32 * c + 8 * q < p.N)
+                    cp_async<16>(smem_u32(own + slot * kRingBase + h * 512), base[h] + 32 * c);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead - 1; ++i) request(c0 + i, i);
+    const uint32_t first = 8 * (g >> 1) + (g & 1);
+    int slot = 0;
+    for (int c = c0; c < c1; ++c) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 2) : "memory");
+        // everyone's copies of this chunk have landed, and everyone is done with the one before
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * parts) : "memory");
+        request(c + kAhead - 1, slot == 0 ? kAhead - 1 : slot - 1);
+        float d[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d[j][e] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (k >= blocks) break;
+            uint4 w[4];
+            const uint8_t *at = bring + slot * kRingB + first * 128 + ((64 * k + 16 * q) ^ ((g & 1) << 6));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const uint4 *>(at + 256 * j);
+            if (32 * k + 32 > rank)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = keep_first(w[j], rank - 32 * k - 8 * q);
+            multiply(d, w, load_u(hrow + 16 * k, lrow + 16 * k, ldu));
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (!out[h] || 32 * c + 8 * q >= p.N) continue;
+            const uint4 was = *reinterpret_cast<const uint4 *>(own + slot * kRingBase + h * 512);
+            *reinterpret_cast<uint4 *>(out[h] + 32 * c) = updated<F16>(was, d, h);
+        }
+        slot = slot + 1 == kAhead ? 0 : slot + 1;
     }
 }
 
@@ -764,8 +851,13 @@ __global__ void __launch_bounds__(kThreads, 2) lora_expand_kernel(const LoraPara
             }
         }
     __syncthreads();
-    // 64 ranks of B and u are what the registers hold beside the rest
+    // 64 ranks of B are what the registers hold beside the rest, and the ring
     const int left = tile.count - 16 * part, at = 16 * part * ldu;
+    if (parts > 1 && p.R <= kRanks) {
+        expand_ring<F16>(p, b, rank, hi + at, lo + at, ldu, tok + 16 * part, left, c0, c1, part, parts,
+                         reinterpret_cast<uint8_t *>(lo + kHalf * ldu));
+        return;
+    }
     if (left <= 0) return;
     if (rank <= 32)
         expand_chunks<F16, 1>(p, b, rank, hi + at, lo + at, ldu, tok + 16 * part, left, c0, c1);
@@ -795,11 +887,11 @@ template <bool INLINE, bool F16>
 cudaError_t launch_expand(const LoraParams &p, const LoraLayout &l, cudaStream_t stream)
 {
     static KernelOnce once;
-    constexpr size_t most = sizeof(uint32_t) * 2 * kHalf * u_stride(kMaxRank);
+    constexpr size_t most = sizeof(uint32_t) * 2 * kHalf * u_stride(kMaxRank) + ring_bytes();
     int sms = 0;
     const cudaError_t e = prepare_kernel(lora_expand_kernel<INLINE, F16>, most, once, &sms);
     if (e != cudaSuccess) return e;
-    const size_t smem = sizeof(uint32_t) * 2 * kHalf * u_stride((p.R + 31) / 32 * 32);
+    const size_t smem = sizeof(uint32_t) * 2 * kHalf * u_stride((p.R + 31) / 32 * 32) + (p.T > 16 && p.R <= kRanks ? ring_bytes() : 0);
     // blocks of channels: as many as give every SM two blocks, no more than one chunk a warp. How
     // many halves of tiles there are the GPU alone knows: an adapter leaves one half empty on average
     const int tiles = INLINE ? l.max_tiles : 2 * l.max_tiles, chunks = (p.N + 31) / 32;
