@@ -21,7 +21,11 @@
 //           bf16 (high and low part, 2^-17 together): twice the MMAs of a product that is
 //           not bound by them, where one bf16 would cost 2^-9 of the update.
 //
-// Bound: few tokens, latency of two dependent launches; many, HBM (x once, base and C).
+// Bound: few tokens, latency of two dependent launches; many, HBM (x once, base and C) and the
+// latencies of three. Measured on the device, 7168 -> 2112: 1 token of rank 16 4.8 us, 16 tokens with
+// adapters of rank 32 of their own 7.4 us (9.9 MB, 1.5 us at the copy bandwidth), 4096 tokens of 6
+// adapters of rank 64 36.5 us (100 MB, 15 us): sort 4 us, shrink 17 us (its stream 6 TB/s), expand
+// 14 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -42,7 +46,8 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kTile = 128;         // tokens of a tile
 constexpr int kHalf = 64;          // tokens of a block of the second product
 constexpr int kInline = 64;        // tokens up to which blocks work out the tiles themselves
-constexpr int kRanks = 64;         // ranks of one block of the first product, up to kInline tokens, and of the ring of the second
+constexpr int kRanks = 64;         // ranks of a block of the first product (up to kInline tokens), and of the
+                                   // ring of the second
 constexpr int kMaxRank = 256;
 
 // ------------------------------------------------------------------ tiles
@@ -61,7 +66,7 @@ template <int THREADS>
 __global__ void __launch_bounds__(THREADS) lora_sort_kernel(const LoraParams p)
 {
     extern __shared__ int bins[];            // [L + 1]: tokens, then the next free place
-    __shared__ int2 scan[THREADS / 32]; // tokens and tiles of the groups before a warp's
+    __shared__ int2 scan[THREADS / 32];      // tokens and tiles of the groups before a warp's
     __shared__ int2 all;
     const int tid = threadIdx.x, lane = tid & 31, groups = p.L + 1;
     for (int i = tid; i < groups; i += THREADS) bins[i] = 0;
@@ -86,7 +91,7 @@ __global__ void __launch_bounds__(THREADS) lora_sort_kernel(const LoraParams p)
     for (int64_t base = kSortKeep * THREADS; base < p.T; base += THREADS)
         count(base + tid, base + tid < p.T ? p.ids[base + tid] : 0);
     __syncthreads();
-    int2 before = make_int2(0, 0);           // tokens and tiles of the groups before this round's
+    int2 before = make_int2(0, 0);           // tokens and tiles of the groups before this pass's
     for (int g0 = 0; g0 < groups; g0 += THREADS) {
         const int g = g0 + tid;
         const int n = g < groups ? bins[g] : 0;

