@@ -211,3 +211,35 @@ def test_waits_that_run_out_end_the_call_and_are_reported():
     again = mx.lora_add(base, x, a, b, ids, scales)
     torch.cuda.synchronize()
     assert mx.get_device_error() == 0 and torch.equal(again, want)
+
+
+def test_two_graphs_that_share_a_workspace():
+    cases = [case(40, 256, 128, 32, 5), case(500, 512, 64, 16, 9)]
+    size = max(mx.lora_workspace_bytes(40, 256, 32, 5), mx.lora_workspace_bytes(500, 512, 16, 9))
+    ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+    want = [mx.lora_add(*c) for c in cases]
+    graphs = []
+    for c in cases:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            o = mx.lora_add(*c, workspace=ws)
+        graphs.append((g, o))
+    for i in (0, 1, 1, 0, 1, 0, 0):
+        graphs[i][0].replay()
+        assert torch.equal(graphs[i][1], want[i])
+    assert mx.get_device_error() == 0
+
+
+@pytest.mark.parametrize("T", [16, 300])
+def test_two_streams_at_once(T):
+    cases = [case(T, 1024, 512, 32, 5, seed=i) for i in range(2)]
+    want = [mx.lora_add(*c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(10):
+        for i in range(2):
+            got[i].append(mx.lora_add(*cases[i], stream=streams[i]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want[i]) for i in range(2) for g in got[i])
+    assert mx.get_device_error() == 0

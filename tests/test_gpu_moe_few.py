@@ -164,6 +164,24 @@ def test_streams_and_graphs():
     assert mx.get_device_error() == 0
 
 
+def test_two_graphs_that_share_a_workspace():
+    """Layers that run one after another may share one: what a replay leaves there does not matter to the next."""
+    s = [make(3, 10, 512, 256, seed=1), make(16, 24, 256, 384, seed=2)]
+    size = max(mx.moe_layer_workspace_bytes(3, 3, 10, 512, 256), mx.moe_layer_workspace_bytes(16, 3, 24, 256, 384))
+    ws = torch.full((size,), 0xA5, dtype=torch.uint8, device="cuda")
+    want = [call(x, 3) for x in s]
+    graphs = []
+    for x in s:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            o = call(x, 3, workspace=ws)
+        graphs.append((g, o))
+    for i in (0, 1, 1, 0, 1, 0, 0):
+        graphs[i][0].replay()
+        assert all(torch.equal(a, b) for a, b in zip(graphs[i][1], want[i]))
+    assert mx.get_device_error() == 0
+
+
 def test_two_streams_at_once():
     """Calls of two streams share the SMs: units wait only for units that some block already has."""
     s = [make(16, 64, 1024, 512, seed=i) for i in range(2)]
