@@ -1,6 +1,7 @@
 // extern "C" entry points of include/mxfp4_layer.h: argument validation and
 // workspace layout. Nothing here allocates device memory or synchronizes.
 #include <cmath>
+#include <cstdlib>
 #include <cstring>
 
 #include "internal.h"
@@ -97,6 +98,11 @@ mxfp4_status_t qk_norm_rope(const void *q, int64_t q_st, int64_t q_sh, const voi
     const int64_t strides[8] = {q_st, q_sh, qo_st, qo_sh, k_st, k_sh, ko_st, ko_sh};
     for (int i = Hq ? 0 : 4; i < (Hk ? 8 : 4); ++i)
         if (strides[i] % 8) return MXFP4_ERR_MISALIGNED;
+    // heads of an output do not share elements
+    const int64_t ost[2] = {qo_st, ko_st}, osh[2] = {qo_sh, ko_sh};
+    const int heads[2] = {Hq, Hk};
+    for (int i = 0; i < 2; ++i)
+        if (heads[i] && ((T > 1 && std::abs(ost[i]) < D) || (heads[i] > 1 && std::abs(osh[i]) < D))) return MXFP4_ERR_INVALID_ARG;
     if ((Hq && q == q_out && (q_st != qo_st || q_sh != qo_sh)) || (Hk && k == k_out && (k_st != ko_st || k_sh != ko_sh)))
         return MXFP4_ERR_INVALID_ARG;
     if ((Hq && (!aligned(q, 16) || !aligned(q_out, 16))) || (Hk && (!aligned(k, 16) || !aligned(k_out, 16))) ||
@@ -109,7 +115,6 @@ mxfp4_status_t qk_norm_rope(const void *q, int64_t q_st, int64_t q_sh, const voi
     memset(&p, 0, sizeof(p));
     const void *x[2] = {q, k}, *w[2] = {q_weight, k_weight};
     void *o[2] = {q_out, k_out};
-    const int heads[2] = {Hq, Hk};
     for (int i = 0; i < 2; ++i) {
         p.x[i] = static_cast<const uint16_t *>(x[i]);
         p.out[i] = static_cast<uint16_t *>(o[i]);

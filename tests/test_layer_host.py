@@ -72,6 +72,7 @@ def qk(**kw):
     (dict(D=264), SHAPE), (dict(rot=24), SHAPE), (dict(rot=20, inter=1), SHAPE), (dict(T=1 << 31), SHAPE),
     (dict(T=1 << 29), SHAPE), (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(qo=None), INVALID),
     (dict(ko=None), INVALID), (dict(table=None), INVALID), (dict(pos=None), INVALID), (dict(P=0), INVALID),
+    (dict(qo_st=0), INVALID), (dict(qo_sh=0), INVALID), (dict(ko_st=-56), INVALID), (dict(Hk=2, ko_sh=56), INVALID),
     (dict(qo=16, qo_st=512), INVALID), (dict(ko=16, ko_sh=8), INVALID), (dict(q_st=260), MISALIGNED),
     (dict(q_sh=68), MISALIGNED), (dict(k_st=68), MISALIGNED), (dict(ko_sh=68), MISALIGNED), (dict(q=24), MISALIGNED),
     (dict(k=24), MISALIGNED), (dict(qo=24), MISALIGNED), (dict(ko=24), MISALIGNED), (dict(wq=24), MISALIGNED),
