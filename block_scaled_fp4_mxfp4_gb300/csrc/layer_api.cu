@@ -16,12 +16,13 @@ inline bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintp
 inline mxfp4_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MXFP4_OK : MXFP4_ERR_CUDA; }
 
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
-constexpr int64_t kMaxWidth = int64_t(1) << 30;    // of adapters: the last chunk's end is a 32-bit index
+// of adapters: the end of a group's last tile, or of the last chunk of channels, is a 32-bit index
+constexpr int64_t kMaxWidth = int64_t(1) << 30;
 
 mxfp4_status_t check_lora_sizes(int64_t T, int64_t K, int R, int L)
 {
     if (T < 0 || K < 1 || R < 1 || L < 1) return MXFP4_ERR_INVALID_ARG;
-    if (T > kMaxDim || K > kMaxWidth || K % 8 || R % 8 || R > LORA_MAX_RANK || L > LORA_MAX_ADAPTERS)
+    if (T > kMaxWidth || K > kMaxWidth || K % 8 || R % 8 || R > LORA_MAX_RANK || L > LORA_MAX_ADAPTERS)
         return MXFP4_ERR_UNSUPPORTED_SHAPE;
     return MXFP4_OK;
 }

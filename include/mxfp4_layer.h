@@ -41,7 +41,7 @@ MXFP4_API size_t lora_workspace_bytes(int64_t T, int64_t K, int R, int L);
  *   ids    : int32 [T], in any order.         scales : fp32 [L] or NULL (1).
  *   ranks  : int32 [L] or NULL (all R); taken as 0 below 0 and as R above R.
  * T >= 0; 1 <= L <= LORA_MAX_ADAPTERS; R a multiple of 8 up to LORA_MAX_RANK; K and N
- * positive multiples of 8 up to 2^30; T below 2^31. C must not overlap anything but
+ * positive multiples of 8 up to 2^30; T up to 2^30. C must not overlap anything but
  * base in its own place. Strides in elements, multiples of 8;
  * X, base, C, A, B 16-byte aligned; ids, scales, ranks 4; workspace 256. The
  * workspace needs no initialisation and keeps nothing from one call for the next;

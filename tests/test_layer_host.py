@@ -31,7 +31,7 @@ def lora(**kw):
     (dict(T=0), OK), (dict(T=0, x=None, a=None, b=None, ids=None, base=None, c=None, ws=None), OK), (dict(T=-1), INVALID),
     (dict(K=0), INVALID), (dict(N=0), INVALID), (dict(R=0), INVALID), (dict(L=0), INVALID), (dict(dtype=2), INVALID),
     (dict(K=60), SHAPE), (dict(N=92), SHAPE), (dict(R=12), SHAPE), (dict(R=264), SHAPE), (dict(L=4097), SHAPE),
-    (dict(T=1 << 31), SHAPE), (dict(K=(1 << 30) + 8, ldx=1 << 31), SHAPE), (dict(N=(1 << 30) + 8), SHAPE),
+    (dict(T=1 << 31), SHAPE), (dict(T=(1 << 30) + 1), SHAPE), (dict(K=(1 << 30) + 8, ldx=1 << 31), SHAPE), (dict(N=(1 << 30) + 8), SHAPE),
     (dict(x=None), INVALID), (dict(a=None), INVALID), (dict(b=None), INVALID), (dict(ids=None), INVALID),
     (dict(base=None), INVALID), (dict(c=None), INVALID), (dict(ws=None), INVALID), (dict(ldx=56), INVALID),
     (dict(ldb=88), INVALID), (dict(ldc=88), INVALID), (dict(c=16, ldc=104), INVALID), (dict(ldx=68), MISALIGNED),
