@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(THREADS) lora_sort_kernel(const LoraParams p)
 __device__ __forceinline__ bool find_tile(const LoraParams &p, int index, Tile &tile, int *tok, int *ids, int *found)
 {
     const int tid = threadIdx.x;
-    if (tid < kInline) ids[tid] = tid < p.T ? adapter_of(p.ids[tid], p.L) : -1;
+    if (tid < kInline) ids[tid] = tid < p.T ? adapter_of(__ldcg(p.ids + tid), p.L) : -1;
     if (tid == 0) found[0] = -1;
     __syncthreads();
     if (tid < 32) {
@@ -749,21 +749,21 @@ __global__ void __launch_bounds__(kThreads, 2) lora_expand_kernel(const LoraPara
     const int chunks = (p.N + 31) / 32, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     Tile tile;
     // The launch before let this one start when everything before it had completed: all but u
-    // is there.
+    // is there, in L2.
     if constexpr (INLINE) {
         if (!find_tile(p, blockIdx.x, tile, tok, ids, found)) {
             grid_dependency_wait();
             return;
         }
     } else {
-        const int4 r = p.tiles[blockIdx.x >> 1];
+        const int4 r = __ldcg(p.tiles + (blockIdx.x >> 1));
         const int skip = (blockIdx.x & 1) * kHalf;
         if (r.z <= skip) {
             grid_dependency_wait();
             return;
         }
         tile = Tile{r.x, r.y + skip, min(kHalf, r.z - skip)};
-        if (threadIdx.x < tile.count) tok[threadIdx.x] = p.order[tile.first + threadIdx.x];
+        if (threadIdx.x < tile.count) tok[threadIdx.x] = __ldcg(p.order + tile.first + threadIdx.x);
         __syncthreads();
     }
     if (tile.adapter == p.L) {
