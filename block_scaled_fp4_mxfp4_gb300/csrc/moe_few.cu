@@ -436,7 +436,9 @@ __global__ void __launch_bounds__(kTokenThreads) moe_few_token_kernel(const Toke
             const unsigned who = __ballot_sync(0xffffffffu, k1 == top);
             if (lane == __ffs(who) - 1) k1 = k2;
             const uint32_t second = __reduce_max_sync(0xffffffffu, k1);
-            if (lane == 0) group_key[g] = order_key(key_value(top) + (p.group_top == 2 && n > 1 ? key_value(second) : 0.0f));
+            // half of a sum of two, which cannot overflow
+            if (lane == 0)
+                group_key[g] = order_key(p.group_top == 2 && n > 1 ? 0.5f * key_value(top) + 0.5f * key_value(second) : key_value(top));
         }
         __syncthreads();
         if (tid < p.E) {

@@ -111,6 +111,25 @@ def test_rows_do_not_depend_on_one_another():
     assert mx.get_device_error() == 0
 
 
+def test_bias_of_the_lowest_value():
+    """Experts masked by fp32's lowest value go before those masked by -inf, in groups too, whose sums pass fp32."""
+    s = make(4, 8, 256, 128)
+    low, none = torch.finfo(torch.float32).min, float("-inf")
+    _, y = moe_ref.add_rmsnorm(s["x"], s["res"], s["weight"], 1e-6)
+    z = y @ s["router"].double().T
+    for bias, k, groups, topk in (([none, none, low, low, none, none, none, none], 2, 4, 1),
+                                  ([none, none, low, low, 0.0, none, none, none], 3, 4, 2),
+                                  ([none, none, none, none, none, none, none, low], 3, 1, 1)):
+        b = torch.tensor(bias, device="cuda")
+        for score in ("softmax", "sigmoid"):
+            _, _, ids, w = call(s, k, bias=b, groups=groups, topk_groups=topk, score=score)
+            ri, rw = moe_ref.route(z, k, score, b, groups, topk, 2, True, 1.0)
+            # lowest + score: equal in fp32, so the lower index comes first
+            assert torch.equal(ids.cpu().sort(-1)[0], ri.sort(-1)[0])
+            assert float((w.double().cpu().sum(-1) - rw.sum(-1)).abs().max()) <= 2.0 ** -18
+    assert mx.get_device_error() == 0
+
+
 def test_zero_rows():
     s = make(3, 4, 256, 128)
     s["x"][1], s["res"][1] = 0, 0
