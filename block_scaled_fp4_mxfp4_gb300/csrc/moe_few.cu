@@ -320,12 +320,13 @@ __global__ void __launch_bounds__(kTokenThreads) moe_few_token_kernel(const Toke
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) add(ss, __shfl_xor_sync(0xffffffffu, ss.hi, o), __shfl_xor_sync(0xffffffffu, ss.lo, o));
         if (lane == 0) {
-            // a root of fp32 and one step of Newton's method: m r^2 - 1 to 2^-40
+            // a root of fp32 and one step of Newton's method: m r^2 - 1 to 2^-40. Below 2^-125 there is
+            // no h, and r^2 may leave fp32.
             add(ss, p.heps, 0.0f);
             const float r0 = rsqrtf(ss.hi);
             const float q = r0 * r0, qe = fmaf(r0, r0, -q);
             const float e = fmaf(ss.hi, q, -1.0f) + (fmaf(ss.hi, qe, ss.lo * q));
-            r_shared = ss.hi == 0.0f || isinf(ss.hi) ? 0.0f : fmaf(r0 * p.root_h, -0.5f * e, r0 * p.root_h);
+            r_shared = ss.hi < 0x1p-125f || isinf(ss.hi) ? 0.0f : fmaf(r0 * p.root_h, -0.5f * e, r0 * p.root_h);
         }
     }
     // logits: `parts` threads an expert over interleaved slices, added in a fixed order

@@ -93,7 +93,7 @@ MXFP4_API size_t mxfp4_moe_layer_workspace_bytes(int64_t T, int k, int E, int64_
  *   out[t]  = bf16_rne( sum_j weights[t, j] * ( act_j . W2[e]^T ) ),  e = ids[t, j],
  *   act_j   = MXFP8( silu(q . G[e]^T) * (q . U[e]^T) ),  q = MXFP8(y),
  * with sums, silu and the order of the weighted sum as in mxfp4_moe_experts; the codes of y
- * and act are those of fp32 arithmetic. Magnitudes of h, and of h * weight: 0 or 2^-60 to 2^60;
+ * and act are those of fp32 arithmetic. Magnitudes of h, and of h * weight: 0 or 2^-60 to 2^50;
  * infinities and NaN stay in their tokens.
  *   X, residual, H : bf16 [T, Hd], row strides ldx, ldr, ldh. H (out, NULL: not stored)
  *                    may be X or residual itself (same pointer and stride).

@@ -139,6 +139,21 @@ def test_zero_rows():
         check(s, (out, h, ids, w), 2, eps=eps)
 
 
+@pytest.mark.parametrize("power", [47, -48])
+def test_large_and_small_magnitudes(power):
+    s = make(5, 6, 1024, 128)
+    s["x"], s["res"] = s["x"] * 2.0 ** power, s["res"] * 2.0 ** power
+    s["x"][2], s["res"][2] = 2.0 ** 49 if power > 0 else 2.0 ** -60, 0
+    check(s, call(s, 3, eps=0.0), 3, eps=0.0)
+
+
+def test_zero_row_with_an_eps_below_the_normal_numbers():
+    s = make(3, 4, 256, 128)
+    s["x"][1], s["res"][1] = 0, 0
+    out, _, ids, w = call(s, 2, eps=1e-44)
+    assert not out[1].any() and ids[1].tolist() == [0, 1] and w[1].tolist() == [0.5, 0.5]
+
+
 def test_in_place_and_strides():
     T, H = 6, 384
     s = make(T, 8, H, 128)
