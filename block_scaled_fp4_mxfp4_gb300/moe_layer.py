@@ -64,7 +64,7 @@ class MoeLayer:
 
     def __call__(self, x, residual=None):
         """(out, h): the experts' sum and the residual stream, bf16 [T, H] (h = x without a residual)."""
-        if x.shape[0] <= self.few_tokens:
+        if self.few_tokens and x.shape[0] <= self.few_tokens:
             out, h, _, _ = mx.mxfp4_moe_layer(x, self.norm, self.router, self.w13, self.s13, self.w2, self.s2, self.k,
                                               eps=self.eps, residual=residual, bias=self.bias, workspace=self.few_workspace,
                                               **self.how)

@@ -109,3 +109,14 @@ def test_layers_of_few_tokens_and_of_many_agree():
     assert torch.equal(few(x.repeat(2, 1))[0], chain(x.repeat(2, 1))[0])     # 18 tokens: the chain
     with pytest.raises(ValueError):
         moe_layer.random_layer(E, H, I, k, 16, few_tokens=17)
+
+
+def test_no_tokens(monkeypatch):
+    """A layer of zero tokens gives empty results, by the call that it would take for one."""
+    x = torch.empty((0, 512), device="cuda").bfloat16()
+    for few in (16, 0):
+        layer = moe_layer.random_layer(8, 512, 256, 2, 16, few_tokens=few)
+        if few == 0:
+            monkeypatch.setattr(mx, "mxfp4_moe_layer", None)
+        out, h = layer(x, x)
+        assert out.shape == h.shape == (0, 512) and out.dtype == h.dtype == torch.bfloat16
