@@ -243,3 +243,15 @@ def test_two_streams_at_once(T):
     torch.cuda.synchronize()
     assert all(torch.equal(g, want[i]) for i in range(2) for g in got[i])
     assert mx.get_device_error() == 0
+
+
+@pytest.mark.parametrize("T", [8192, 8193, 20011])
+def test_long_batches_of_runs_and_of_mixed_ids(T):
+    """Prompts whose tokens share an adapter, tokens without one, mixed tokens, and a run that ends inside a warp's ids."""
+    base, x, a, b, ids, scales, ranks = case(T, 64, 40, 16, 5, ragged=True)
+    ids[:3000], ids[5000:6000], ids[-2050:-7] = 2, -1, 4
+    args = base, x, a, b, ids, scales, ranks
+    c = mx.lora_add(*args)
+    check(c, layer_ref.lora(*args))
+    assert torch.equal(c[ids < 0], base[ids < 0])
+    assert torch.equal(mx.lora_add(base, x, a, b, ids, scales, ranks, C=base), c)
