@@ -18,14 +18,19 @@
 //   expand  u B_a^T + base, for up to 64 tokens a block. Rows of the MMA are tokens, columns
 //           are channels, chosen so that a lane ends with 8 neighbouring channels of a
 //           token: one 16-byte load of base and one store. u, summed in fp32, enters as two
-//           bf16 (high and low part, 2^-17 together): twice the MMAs of a product that is
-//           not bound by them, where one bf16 would cost 2^-9 of the update.
+//           bf16 (high and low part, 2^-17 together): twice the MMAs, where one bf16 would cost
+//           2^-9 of the update.
+// Batches whose tiles are filled to a half or more, of up to 64 ranks, take both products by tcgen05: the blocks
+// that share a tile's K are a cluster, add their sums in shared memory and leave u as the two bf16 that the
+// second product loads as an operand. (Sums of splits through global memory were read again by every block of
+// channels, and mma.sync took half of the second product's time: 16384 tokens 108 us, 86 now; 4096
+// tokens 37.2 and 34.6. In a tile of few tokens the 128 rows are mostly empty: 333 tokens of 20 adapters 20.7 us,
+// 19 without.)
 //
 // Bound: few tokens, latency of two dependent launches; many, HBM (x once, base and C) and the
 // latencies of three. Measured on the device, 7168 -> 2112: 1 token of rank 16 4.8 us, 16 tokens with
 // adapters of rank 32 of their own 7.4 us (9.9 MB, 1.5 us at the copy bandwidth), 4096 tokens of 6
-// adapters of rank 64 36.5 us (100 MB, 15 us): sort 4 us, shrink 17 us (its stream 6 TB/s), expand
-// 14 us.
+// adapters of rank 64 34.6 us (100 MB, 15 us), 16384 tokens 86 us (381 MB, 56 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -80,7 +85,10 @@ __global__ void __launch_bounds__(THREADS) lora_sort_kernel(const LoraParams p)
     const int64_t own = (tid >> 5) * (LONG ? kBatch : 32);
     auto load = [&](int64_t at, int (&g)[kSortKeep]) {
 #pragma unroll
-        for (int i = 0; i < kSortKeep; ++i) g[i] = at + kStep * i + lane < p.T ? adapter_of(p.ids[at + kStep * i + lane], p.L) : -1;
+        for (int i = 0; i < kSortKeep; ++i) {
+            const int64_t t = at + kStep * i + lane;
+            g[i] = t < p.T ? adapter_of(p.ids[t], p.L) : -1;
+        }
     };
     auto alike = [&](const int (&g)[kSortKeep]) {
         if (!LONG) return false;
@@ -218,7 +226,7 @@ __device__ __forceinline__ bool find_tile(const LoraParams &p, int index, Tile &
 
 __device__ __forceinline__ int rank_of(const LoraParams &p, int a)
 {
-    return p.ranks ? max(0, min(p.R, p.ranks[a])) : p.R;
+    return p.ranks ? max(0, min(p.R, __ldcg(p.ranks + a))) : p.R;
 }
 
 // ------------------------------------------------------------------- MMA
@@ -366,6 +374,8 @@ struct LongParams {
     LoraParams l;
     int rows, stages;                // R rounded up to 16; stages of the ring
     uint32_t columns;                // of TMEM: a power of two
+    int cluster;                     // blocks that share a tile's K as a cluster
+    uint8_t *parts;                  // what a cluster leaves: u as two bf16 (see sum_cluster)
     uint64_t wait_ns;
 };
 
@@ -397,6 +407,80 @@ __device__ __forceinline__ void cp_async_or_zero(uint32_t smem_dst, const void *
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(smem_dst), "l"(gsrc), "r"(bytes) : "memory");
 }
 
+// Four numbers as two bf16 each, high and low part.
+__device__ __forceinline__ void split_bf16(const float (&v)[4], uint2 &hi, uint2 &lo)
+{
+    uint32_t hb[2], lb[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+        hb[k] = *reinterpret_cast<const uint32_t *>(&h);
+        // what rounds to infinity has no low part
+        const float hx = __uint_as_float(hb[k] << 16), hy = __uint_as_float(hb[k] & 0xFFFF0000u);
+        const __nv_bfloat162 l = __floats2bfloat162_rn(isinf(hx) ? 0.0f : v[2 * k] - hx, isinf(hy) ? 0.0f : v[2 * k + 1] - hy);
+        lb[k] = *reinterpret_cast<const uint32_t *>(&l);
+    }
+    hi = make_uint2(hb[0], hb[1]);
+    lo = make_uint2(lb[0], lb[1]);
+}
+
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// Where a block keeps its sums of token t: 64 ranks, pieces of 16 bytes spread over the banks.
+__device__ __forceinline__ uint32_t sums_at(int t, int piece) { return t * 256 + ((piece ^ (t & 15)) << 4); }
+
+// The sums of a cluster's blocks, added in their order, times the adapter's scale: u of this
+// block's share of the tokens, as two bf16 a number. High parts are `parts`: a line of 64 ranks for
+// every token, tokens in the order of the tiles, pieces of 16 bytes in the order that an MMA's operand has them
+// in shared memory; then the low parts.
+__device__ __forceinline__ void sum_cluster(const LongParams &lp, const uint8_t *smem, int4 rec, int rank, int own)
+{
+    const LoraParams &p = lp.l;
+    const float scale = p.scales ? __ldcg(p.scales + rec.x) : 1.0f;
+    const int size = lp.cluster, cols = (rank + 15) / 16 * 16, per = (rec.z <= kHalf ? kHalf : kTile) / size;
+    for (int i = threadIdx.x; i < per * 8; i += 128) {
+        const int t = own * per + (i >> 3), r = 8 * (i & 7);
+        if (t >= rec.z || r >= cols) continue;
+        const uint32_t at0 = smem_u32(smem) + sums_at(t, r >> 2), at1 = smem_u32(smem) + sums_at(t, (r >> 2) + 1);
+        float4 some[8][2];
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+            if (s < size && r < p.R) {
+                some[s][0] = ld_cluster(mapa_shared(at0, s));
+                some[s][1] = ld_cluster(mapa_shared(at1, s));
+            }
+        uint2 h[2], l[2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                if (!(s < size && r < p.R)) continue;
+                v[0] += some[s][half].x;
+                v[1] += some[s][half].y;
+                v[2] += some[s][half].z;
+                v[3] += some[s][half].w;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = r + 4 * half + k < rank ? v[k] * scale : 0.0f;
+            split_bf16(v, h[half], l[half]);
+        }
+        uint8_t *to = lp.parts + (static_cast<int64_t>(rec.y) + t) * 128 + (((r >> 3) ^ (t & 7)) << 4);
+        *reinterpret_cast<uint4 *>(to) = make_uint4(h[0].x, h[0].y, h[1].x, h[1].y);
+        *reinterpret_cast<uint4 *>(to + static_cast<int64_t>(p.T) * 128) = make_uint4(l[0].x, l[0].y, l[1].x, l[1].y);
+    }
+}
+
+// CLUSTER: the blocks of a tile are a cluster and leave u; otherwise they leave its sums over their shares of K.
+template <bool CLUSTER>
 __global__ void __launch_bounds__(kLongThreads, 2) lora_shrink_long_kernel(const __grid_constant__ LongParams lp)
 {
     extern __shared__ uint8_t smem_raw[];
@@ -419,11 +503,12 @@ __global__ void __launch_bounds__(kLongThreads, 2) lora_shrink_long_kernel(const
     grid_dependency_wait();
     grid_launch_dependents();
     // whole blocks leave here, before TMEM is theirs
-    const int4 rec = __ldcg(p.tiles + blockIdx.x);
+    const int4 rec = __ldcg(p.tiles + (CLUSTER ? blockIdx.x / lp.cluster : blockIdx.x));
     const int adapter = rec.x, count = rec.z;
     if (adapter == p.L || rank_of(p, adapter) == 0) return;
-    const int per = (p.K + 64 * p.splits - 1) / (64 * p.splits) * 64;
-    const int kb = static_cast<int>(min(static_cast<int64_t>(blockIdx.y) * per, static_cast<int64_t>(p.K)));
+    const int own = CLUSTER ? static_cast<int>(cluster_ctarank()) : blockIdx.y, shares = CLUSTER ? lp.cluster : p.splits;
+    const int per = (p.K + 64 * shares - 1) / (64 * shares) * 64;
+    const int kb = static_cast<int>(min(static_cast<int64_t>(own) * per, static_cast<int64_t>(p.K)));
     const int ke = static_cast<int>(min(static_cast<int64_t>(kb) + per, static_cast<int64_t>(p.K)));
     const int steps = (ke - kb + 63) / 64;
     if (warp == 5) {
@@ -503,7 +588,7 @@ __global__ void __launch_bounds__(kLongThreads, 2) lora_shrink_long_kernel(const
         tc_fence_after();
         const int t = 32 * warp + lane;              // this lane's token
         if (ok && done && 32 * warp < count) {
-            float *u = p.u + (static_cast<int64_t>(blockIdx.y) * p.T + (t < count ? sh.tok[t] : 0)) * p.R;
+            float *u = p.u + (static_cast<int64_t>(own) * p.T + (t < count ? sh.tok[t] : 0)) * p.R;
             for (int c0 = 0; c0 < p.R; c0 += 32) {
                 uint32_t v[32];
                 // 32 columns: those beyond the MMA's are not stored
@@ -512,13 +597,24 @@ __global__ void __launch_bounds__(kLongThreads, 2) lora_shrink_long_kernel(const
                 if (t < count)
 #pragma unroll
                     for (int j = 0; j < 32; j += 4)
-                        if (c0 + j < p.R)
-                            *reinterpret_cast<uint4 *>(u + c0 + j) =
-                                steps ? make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]) : make_uint4(0, 0, 0, 0);
+                        if (c0 + j < p.R) {
+                            const uint4 sums = steps ? make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]) : make_uint4(0, 0, 0, 0);
+                            // in the place of the ring, which is empty
+                            if constexpr (CLUSTER)
+                                *reinterpret_cast<uint4 *>(smem + sums_at(t, (c0 + j) / 4)) = sums;
+                            else
+                                *reinterpret_cast<uint4 *>(u + c0 + j) = sums;
+                        }
             }
         }
     }
     __syncwarp();
+    if constexpr (CLUSTER) {
+        cluster_sync();
+        if (warp < 4) sum_cluster(lp, smem, rec, rank_of(p, adapter), own);
+        __syncwarp();
+        cluster_sync();                  // nobody leaves while others read its sums
+    }
     tc_fence_before();
     __syncthreads();
     if (warp == 5) {
@@ -771,6 +867,21 @@ __device__ __forceinline__ void prefetch_l2(const void *p)
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
+// C = base for some of a tile's tokens and the vectors of eight channels from v0 to v1 - 1, `step` apart.
+__device__ __forceinline__ void copy_rows(const LoraParams &p, const int *tok, int count, uint32_t v0, uint32_t v1, uint32_t step)
+{
+    for (uint32_t i = v0; i < v1; i += step)
+        for (int t0 = 0; t0 < count; t0 += 8) {
+            uint4 v[8];
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+                if (t0 + t < count) v[t] = reinterpret_cast<const uint4 *>(p.base + tok[t0 + t] * p.ldb)[i];
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+                if (t0 + t < count) reinterpret_cast<uint4 *>(p.c + tok[t0 + t] * p.ldc)[i] = v[t];
+        }
+}
+
 // Grid: halves of tiles (up to kInline tokens: tiles) x blocks of channels. Shared memory: u as
 // high and low bf16, [64 tokens][ranks rounded up to 32].
 template <bool INLINE, bool F16>
@@ -802,17 +913,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_expand_kernel(const LoraPara
         // no adapter: a copy of base, as it is
         grid_dependency_wait();
         grid_launch_dependents();
-        const uint32_t vectors = p.N / 8, total = gridDim.y * kThreads;
-        for (uint32_t i = blockIdx.y * kThreads + threadIdx.x; i < vectors; i += total)
-            for (int t0 = 0; t0 < tile.count; t0 += 8) {
-                uint4 v[8];
-#pragma unroll
-                for (int t = 0; t < 8; ++t)
-                    if (t0 + t < tile.count) v[t] = reinterpret_cast<const uint4 *>(p.base + tok[t0 + t] * p.ldb)[i];
-#pragma unroll
-                for (int t = 0; t < 8; ++t)
-                    if (t0 + t < tile.count) reinterpret_cast<uint4 *>(p.c + tok[t0 + t] * p.ldc)[i] = v[t];
-            }
+        copy_rows(p, tok, tile.count, blockIdx.y * kThreads + threadIdx.x, p.N / 8, gridDim.y * kThreads);
         return;
     }
     const int rank = rank_of(p, tile.adapter);
@@ -831,7 +932,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_expand_kernel(const LoraPara
     if (part == 0)
         for (int ch = 32 * c0 + lane; ch < min(32 * c1, p.N); ch += 32)
             for (int k = 0; k < rank; k += 64) prefetch_l2(b + static_cast<int64_t>(ch) * p.R + k);
-    const float scale = p.scales ? p.scales[tile.adapter] : 1.0f;
+    const float scale = p.scales ? __ldcg(p.scales + tile.adapter) : 1.0f;
     grid_dependency_wait();
     grid_launch_dependents();
     uint32_t *hi = ushared, *lo = ushared + kHalf * ldu;
@@ -873,18 +974,10 @@ __global__ void __launch_bounds__(kThreads, 2) lora_expand_kernel(const LoraPara
                 float v[4] = {sum[i].x, sum[i].y, sum[i].z, sum[i].w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[k] = r + k < rank ? v[k] * scale : 0.0f;
-                uint32_t hb[2], lb[2];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
-                    hb[k] = *reinterpret_cast<const uint32_t *>(&h);
-                    // what rounds to infinity has no low part
-                    const float hx = __uint_as_float(hb[k] << 16), hy = __uint_as_float(hb[k] & 0xFFFF0000u);
-                    const __nv_bfloat162 l = __floats2bfloat162_rn(isinf(hx) ? 0.0f : v[2 * k] - hx, isinf(hy) ? 0.0f : v[2 * k + 1] - hy);
-                    lb[k] = *reinterpret_cast<const uint32_t *>(&l);
-                }
-                *reinterpret_cast<uint2 *>(hi + t * ldu + r / 2) = make_uint2(hb[0], hb[1]);
-                *reinterpret_cast<uint2 *>(lo + t * ldu + r / 2) = make_uint2(lb[0], lb[1]);
+                uint2 h, l;
+                split_bf16(v, h, l);
+                *reinterpret_cast<uint2 *>(hi + t * ldu + r / 2) = h;
+                *reinterpret_cast<uint2 *>(lo + t * ldu + r / 2) = l;
             }
         }
     __syncthreads();
@@ -904,20 +997,280 @@ __global__ void __launch_bounds__(kThreads, 2) lora_expand_kernel(const LoraPara
         expand_chunks<F16, 0>(p, b, rank, hi + at, lo + at, ldu, tok + 16 * part, left, c0, c1);
 }
 
+// ------------------------------------------- expand, whole tiles of tokens
+
+// Batches of well filled tiles, up to 64 ranks: u B^T by tcgen05, rows are a tile's 128 tokens, columns 64 channels
+// a step. base comes to shared memory by cp.async, where a lane adds its token's sums, and leaves as C
+// from there in whole lines (a lane's own row would be 32 lines a store); steps' B (TMA) and base are three ahead.
+// Bound: what base and C take of HBM, a step's 32 KB in 1.3 us where two blocks an SM do the same.
+// Warps:
+//   0-7  base to C
+//   8    lane 0 loads B, and u as sum_cluster left it
+//   9    issues the MMAs; owns TMEM
+constexpr int kTileThreads = kThreads + 64;
+constexpr int kWide = 64;                // channels of a step
+constexpr int kSteps = 3;                // of B and base in shared memory
+constexpr uint32_t kUBytes = kTile * 128;            // of u's high parts (then of the low ones): 64 ranks a token
+constexpr uint32_t kBAt = 2 * kUBytes, kBBytes = kWide * 128;
+constexpr uint32_t kBaseAt = kBAt + kSteps * kBBytes, kBaseBytes = kTile * kWide * 2;
+constexpr uint32_t kTileShared = kBaseAt + kSteps * kBaseBytes;
+
+struct TileParams {
+    CUtensorMap tm_b;                // B as [L * N, R] bf16, box 64 elements x kWide
+    LoraParams l;
+    const uint8_t *parts;            // u, as sum_cluster leaves it
+    uint64_t wait_ns;
+};
+
+struct TileShared {
+    uint64_t u_full;
+    uint64_t b_full[kSteps], b_free[kSteps], acc_full[2], acc_empty[2];
+    uint32_t tmem;
+    int abort;
+    int tok[kTile];
+};
+constexpr uint32_t kTileSmem = kTileShared + sizeof(TileShared) + 1024;
+static_assert(kTileSmem <= 113 * 1024, "two blocks an SM");
+
+__device__ __forceinline__ void workers_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// Grid: tiles x blocks of channels.
+template <bool F16>
+__global__ void __launch_bounds__(kTileThreads, 2) lora_expand_tile_kernel(const __grid_constant__ TileParams tp)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const LoraParams &p = tp.l;
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    TileShared &sh = *reinterpret_cast<TileShared *>(smem + kTileShared);
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    // The launch before let this one start when everything before it had completed: all but u
+    // is there, in L2.
+    const int4 rec = __ldcg(p.tiles + blockIdx.x);
+    const int adapter = rec.x, count = rec.z;
+    const int rank = adapter == p.L ? 0 : rank_of(p, adapter);
+    if (tid < count) sh.tok[tid] = __ldcg(p.order + rec.y + tid);
+    if (rank == 0 || count == 0) {
+        __syncthreads();
+        grid_dependency_wait();
+        grid_launch_dependents();
+        // no update: a copy of base, as it is
+        if (p.copy) copy_rows(p, sh.tok, count, blockIdx.y * kTileThreads + tid, p.N / 8, gridDim.y * kTileThreads);
+        return;
+    }
+    if (tid == 0) {
+        for (int i = 0; i < kSteps; ++i) {
+            mbar_init(&sh.b_full[i], 1);
+            mbar_init(&sh.b_free[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.acc_full[i], 1);
+            mbar_init(&sh.acc_empty[i], kWarps);
+        }
+        mbar_init(&sh.u_full, 1);
+        sh.abort = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tp.tm_b);
+    }
+    if (warp == 9) {
+        tmem_alloc(&sh.tmem, 2 * kWide);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
+    // this block's steps of 64 channels: whole lines of C
+    const int units = (p.N + kWide - 1) / kWide;
+    const int unit = static_cast<int>(static_cast<int64_t>(units) * blockIdx.y / gridDim.y), n0 = unit * kWide;
+    const int steps = static_cast<int>(static_cast<int64_t>(units) * (blockIdx.y + 1) / gridDim.y) - unit;
+
+    if (warp == 8) {
+        if (lane == 0) {
+            const uint64_t pol = policy_evict_last();        // other tiles of the adapter read the same rows
+            int i = 0;
+            bool ok = true;
+            auto load_to = [&](int end) {
+                for (; i < end; ++i) {
+                    const int s = i % kSteps;
+                    ok = mbar_wait(&sh.b_free[s], ((i / kSteps) & 1) ^ 1u, &g_lora_error, kErrWaitEmpty, tp.wait_ns);
+                    if (!ok) return;
+                    mbar_arrive_expect_tx(&sh.b_full[s], kBBytes);
+                    tma_load_2d(smem + kBAt + s * kBBytes, &tp.tm_b, 0, adapter * p.N + n0 + i * kWide, &sh.b_full[s], pol);
+                }
+            };
+            load_to(min(steps, kSteps));
+            grid_dependency_wait();
+            const uint8_t *u = tp.parts + static_cast<int64_t>(rec.y) * 128;
+            mbar_arrive_expect_tx(&sh.u_full, 2 * count * 128);
+            bulk_load(smem, u, count * 128, &sh.u_full, pol);
+            bulk_load(smem + kUBytes, u + static_cast<int64_t>(p.T) * 128, count * 128, &sh.u_full, pol);
+            if (ok) load_to(steps);
+            // copies in flight land before the block leaves
+            mbar_wait(&sh.u_full, 0, &g_lora_error, kErrWaitDrain);
+            for (int j = max(0, i - kSteps); j < i; ++j)
+                mbar_wait(&sh.b_full[j % kSteps], (j / kSteps) & 1, &g_lora_error, kErrWaitDrain);
+        }
+        __syncwarp();
+        grid_dependency_wait();
+    } else if (warp == 9) {
+        grid_dependency_wait();
+        const uint32_t idesc = __shfl_sync(0xffffffffu, idesc_bf16(kWide, 128), 0);
+        const int ks = (rank + 15) / 16;
+        const bool there = mbar_wait_warp(&sh.u_full, 0, &g_lora_error, kErrWaitOperand, tp.wait_ns);
+        int i = 0;
+        for (; i < steps && there; ++i) {
+            const int s = i % kSteps, buf = i & 1;
+            const bool ok = mbar_wait_warp(&sh.acc_empty[buf], ((i >> 1) & 1) ^ 1u, &g_lora_error, kErrWaitAccum, tp.wait_ns) &&
+                            mbar_wait_warp(&sh.b_full[s], (i / kSteps) & 1, &g_lora_error, kErrWaitFull, tp.wait_ns);
+            if (!ok) break;
+            uint8_t *b = smem + kBAt + s * kBBytes;
+            if (rank < p.R && rank < 16 * ks)
+                // what B holds beyond the rank is not used, whatever it is
+                for (int r = lane; r < kWide; r += 32)
+                    for (int k = rank; k < 16 * ks; ++k)
+                        *reinterpret_cast<uint16_t *>(b + r * 128 + (((k >> 3) ^ (r & 7)) << 4) + 2 * (k & 7)) = 0;
+            fence_proxy_async_smem();
+            __syncwarp();
+            tc_fence_after();
+            const uint64_t hi = sdesc_sw128(smem_u32(smem)), lo = sdesc_sw128(smem_u32(smem + kUBytes));
+            const uint64_t bd = sdesc_sw128(smem_u32(b));
+            if (elect_one()) {
+                for (int k = 0; k < ks; ++k) {
+                    mma_tc_bf16(tmem + buf * kWide, lo + 2 * k, bd + 2 * k, idesc, k > 0 ? 1u : 0u);
+                    mma_tc_bf16(tmem + buf * kWide, hi + 2 * k, bd + 2 * k, idesc, 1u);
+                }
+                tc_commit(&sh.b_free[s]);
+                tc_commit(&sh.acc_full[buf]);
+            }
+            __syncwarp();
+        }
+        // nobody else waits for the arrivals of the last MMAs
+        for (int j = max(0, i - kSteps); j < i; ++j)
+            mbar_wait_warp(&sh.b_free[j % kSteps], (j / kSteps) & 1, &g_lora_error, kErrWaitDrain);
+    } else {
+        // a thread's pieces of base and C: eight channels (c) of tokens row + 32 j
+        const int c = tid & 7, row = tid >> 3;
+        auto request = [&](int i) {
+            const int n = n0 + i * kWide + 8 * c;
+            if (i < steps && n < p.N) {
+                const uint32_t to = smem_u32(smem + kBaseAt + i % kSteps * kBaseBytes) + row * 128 + ((c ^ (row & 7)) << 4);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (row + 32 * j < count) cp_async<16>(to + j * 4096, p.base + sh.tok[row + 32 * j] * p.ldb + n);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) request(i);
+        grid_dependency_wait();
+        grid_launch_dependents();
+        const int wrow = 32 * (warp & 3), t = wrow + lane, half = warp >> 2;   // this lane's token, and half of the channels
+        bool ok = true;
+        for (int i = 0; i < steps; ++i) {
+            const int buf = i & 1;
+            uint8_t *place = smem + kBaseAt + i % kSteps * kBaseBytes;
+            asm volatile("cp.async.wait_group %0;" ::"n"(kSteps - 1) : "memory");
+            ok = mbar_wait_warp(&sh.acc_full[buf], (i >> 1) & 1, &g_lora_error, kErrWaitAccum, tp.wait_ns);
+            if (!ok) *reinterpret_cast<volatile int *>(&sh.abort) = 1;
+            tc_fence_after();
+            workers_sync();                  // everyone's part of base has landed
+            if (*reinterpret_cast<volatile int *>(&sh.abort)) break;       // for all: it is set before this barrier only
+            if (wrow < count) {
+                uint32_t v[32];
+                tmem_ld32(tmem + buf * kWide + 32 * half + (static_cast<uint32_t>(wrow) << 16), v);
+                tmem_ld_wait();
+                if (t < count)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint4 *at = reinterpret_cast<uint4 *>(place + t * 128 + (((4 * half + j) ^ (t & 7)) << 4));
+                        const uint4 was = *at;
+                        const uint32_t w[4] = {was.x, was.y, was.z, was.w};
+                        uint32_t o[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 f = unpack2<F16>(w[k]);
+                            const float x = __uint_as_float(v[8 * j + 2 * k]), y = __uint_as_float(v[8 * j + 2 * k + 1]);
+                            o[k] = pack2<F16>(f.x + x, f.y + y);
+                        }
+                        *at = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
+            workers_sync();                  // all sums are added
+            const int n = n0 + i * kWide + 8 * c;
+            if (n < p.N) {
+                const uint8_t *from = place + row * 128 + ((c ^ (row & 7)) << 4);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (row + 32 * j < count)
+                        *reinterpret_cast<uint4 *>(p.c + sh.tok[row + 32 * j] * p.ldc + n) =
+                            *reinterpret_cast<const uint4 *>(from + j * 4096);
+            }
+            request(i + kSteps);             // a thread's own pieces again, which nobody else reads now
+        }
+        cp_async_wait_all();
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 2 * kWide);
+    }
+}
+
 template <typename Kern, typename P>
-cudaError_t launch(Kern kern, dim3 grid, int threads, size_t smem, cudaStream_t stream, const P &p)
+cudaError_t launch(Kern kern, dim3 grid, int threads, size_t smem, cudaStream_t stream, const P &p, int cluster = 1)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+// Tiles of a long batch that there may be (every adapter leaves half of one empty): the GPU alone knows.
+int likely_tiles(const LoraParams &p) { return std::min<int>(p.max_tiles, p.T / kTile + (p.L + 1) / 2 + 1); }
+
+template <bool F16>
+cudaError_t launch_expand_tile(const LoraParams &p, const LoraLayout &l, cudaStream_t stream)
+{
+    static KernelOnce once;
+    int sms = 0;
+    const cudaError_t e = prepare_kernel(lora_expand_tile_kernel<F16>, kTileSmem, once, &sms);
+    if (e != cudaSuccess) return e;
+    TileParams tp;
+    tp.l = p;
+    tp.parts = reinterpret_cast<const uint8_t *>(p.u);
+    tp.wait_ns = wait_limit_ns();
+    if (!encode_map_2d(&tp.tm_b, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.b, p.R, static_cast<uint64_t>(p.L) * p.N,
+                       static_cast<uint64_t>(p.R) * 2, 64u, kWide, CU_TENSOR_MAP_SWIZZLE_128B,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_128B))
+        return cudaErrorInvalidValue;
+    const int units = (p.N + kWide - 1) / kWide;
+    // blocks a tile: as many as make the waves of blocks, two an SM, shortest (a block's start takes about three steps)
+    int blocks = 1;
+    int64_t best = INT64_MAX;
+    for (int n = 1; n <= std::min(units, 2 * sms); ++n) {
+        const int64_t waves = (static_cast<int64_t>(likely_tiles(p)) * n + 2 * sms - 1) / (2 * sms);
+        const int64_t length = waves * ((units + n - 1) / n + 3);
+        if (length < best) {
+            best = length;
+            blocks = n;
+        }
+    }
+    return launch(lora_expand_tile_kernel<F16>, dim3(l.max_tiles, blocks), kTileThreads, kTileSmem, stream, tp);
 }
 
 template <bool INLINE, bool F16>
@@ -953,7 +1306,8 @@ LoraLayout lora_layout(int64_t T, int64_t K, int R, int L)
     // splits * T is at most 32 T, and at most 304 / (T / 128) * T or T: a bound that grows with T
     const int64_t most = std::min<int64_t>(32 * T, std::max<int64_t>(304 * kTile, T));
     l.u = 0;
-    l.order = l.u + up(sizeof(float) * static_cast<size_t>(most) * R);
+    // or, for up to kRanks ranks, two lines of 64 bf16 a token
+    l.order = l.u + up(std::max(sizeof(float) * static_cast<size_t>(most) * R, static_cast<size_t>(256) * T));
     l.tiles = l.order + up(sizeof(int) * static_cast<size_t>(T));
     l.total = l.tiles + up(sizeof(int4) * static_cast<size_t>(l.max_tiles));
     return l;
@@ -983,9 +1337,6 @@ cudaError_t launch_lora(LoraParams p, const LoraLayout &l, bool f16, cudaStream_
         : p.T <= 1024 * kSortKeep ? launch(lora_sort_kernel<1024, false>, dim3(1), 1024, bins, stream, p)
                                   : launch(lora_sort_kernel<1024, true>, dim3(1), 1024, bins, stream, p);
     if (e != cudaSuccess) return e;
-    static KernelOnce once;
-    e = prepare_kernel(lora_shrink_long_kernel, kLongSmemOne, once, nullptr);
-    if (e != cudaSuccess) return e;
     LongParams lp;
     lp.l = p;
     lp.rows = (p.R + 15) & ~15;
@@ -998,7 +1349,27 @@ cudaError_t launch_lora(LoraParams p, const LoraLayout &l, bool f16, cudaStream_
                        static_cast<uint64_t>(p.K) * 2, 64u, lp.rows, CU_TENSOR_MAP_SWIZZLE_128B,
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
         return cudaErrorInvalidValue;
-    e = launch(lora_shrink_long_kernel, dim3(l.max_tiles, l.splits), kLongThreads, smem, stream, lp);
+    lp.parts = reinterpret_cast<uint8_t *>(p.u);
+    lp.cluster = 1;
+    // whole tiles of tokens: ranks that one line of u holds, rows of B that TMA's 32-bit coordinates reach, and tiles that
+    // are filled well enough
+    const int likely = likely_tiles(p);
+    if (p.R <= kRanks && static_cast<int64_t>(p.L) * p.N <= (int64_t(1) << 31) - kWide && p.T >= kHalf * likely) {
+        static KernelOnce once;
+        int sms = 0;
+        e = prepare_kernel(lora_shrink_long_kernel<true>, kLongSmem, once, &sms);
+        if (e != cudaSuccess) return e;
+        // as many blocks a tile as give every SM two, with at least four stages of K each
+        lp.cluster = 8;
+        while (lp.cluster > 1 && (lp.cluster * likely > 2 * sms || lp.cluster * 256 > p.K + 255)) lp.cluster /= 2;
+        e = launch(lora_shrink_long_kernel<true>, dim3(l.max_tiles * lp.cluster), kLongThreads, smem, stream, lp, lp.cluster);
+        if (e != cudaSuccess) return e;
+        return f16 ? launch_expand_tile<true>(p, l, stream) : launch_expand_tile<false>(p, l, stream);
+    }
+    static KernelOnce once;
+    e = prepare_kernel(lora_shrink_long_kernel<false>, kLongSmemOne, once, nullptr);
+    if (e != cudaSuccess) return e;
+    e = launch(lora_shrink_long_kernel<false>, dim3(l.max_tiles, l.splits), kLongThreads, smem, stream, lp);
     if (e != cudaSuccess) return e;
     return f16 ? launch_expand<false, true>(p, l, stream) : launch_expand<false, false>(p, l, stream);
 }

@@ -255,3 +255,27 @@ def test_long_batches_of_runs_and_of_mixed_ids(T):
     check(c, layer_ref.lora(*args))
     assert torch.equal(c[ids < 0], base[ids < 0])
     assert torch.equal(mx.lora_add(base, x, a, b, ids, scales, ranks, C=base), c)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("T,K,N,R,L", [
+    (300, 8, 8, 8, 1), (257, 136, 72, 40, 1), (700, 520, 200, 24, 2), (1100, 1096, 1000, 56, 3), (1500, 2056, 64, 64, 3),
+    (2600, 4096, 328, 48, 5), (5000, 264, 136, 16, 6), (9000, 72, 264, 64, 40),
+])
+def test_batches_of_well_filled_tiles(T, K, N, R, L, dtype):
+    """Ends of K, N and ranks inside a tile's steps, ragged ranks with NaN behind them, rows that are views, in place."""
+    base, x, a, b, ids, scales, ranks = case(T, K, N, R, L, dtype, ragged=True)
+    for l in range(L):
+        a[l, int(ranks[l]):], b[l, :, int(ranks[l]):] = float("nan"), float("nan")
+    want = layer_ref.lora(base, x, torch.nan_to_num(a), torch.nan_to_num(b), ids, scales, ranks)
+    wide = torch.full((T, N + 24), 7.0, device="cuda").to(dtype)
+    c, xs = wide[:, 8:8 + N], torch.cat([x, x[:, :8]], 1)[:, :K]
+    assert mx.lora_add(base, xs, a, b, ids, scales, ranks, C=c) is c
+    check(c, want)
+    assert bool((wide[:, :8] == 7.0).all()) and bool((wide[:, 8 + N:] == 7.0).all())
+    assert torch.equal(c[ids < 0], base[ids < 0])
+    c.copy_(base)
+    first = mx.lora_add(base, x, a, b, ids, scales, ranks)
+    assert torch.equal(mx.lora_add(c, x, a, b, ids, scales, ranks, C=c), first)
+    assert bool((wide[:, :8] == 7.0).all()) and bool((wide[:, 8 + N:] == 7.0).all())
+    assert mx.get_device_error() == 0
