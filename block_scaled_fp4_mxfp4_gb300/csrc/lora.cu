@@ -401,10 +401,11 @@ __device__ __forceinline__ void mma_tc_bf16(uint32_t d_tmem, uint64_t adesc, uin
         : "memory");
 }
 
-// 16 bytes from global to shared memory, of which the first `bytes` are copied and the others zeros.
+// 16 bytes from global to shared memory, of which the first `bytes` are copied and the others zeros. L2 asks for the row's next
+// 128 bytes too (128 tokens a stage: 32768 tokens 81.9 us, 78.9 so).
 __device__ __forceinline__ void cp_async_or_zero(uint32_t smem_dst, const void *gsrc, uint32_t bytes)
 {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(smem_dst), "l"(gsrc), "r"(bytes) : "memory");
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(smem_dst), "l"(gsrc), "r"(bytes) : "memory");
 }
 
 // Four numbers as two bf16 each, high and low part.
