@@ -23,14 +23,14 @@
 // Batches whose tiles are filled to a half or more, of up to 64 ranks, take both products by tcgen05: the blocks
 // that share a tile's K are a cluster, add their sums in shared memory and leave u as the two bf16 that the
 // second product loads as an operand. (Sums of splits through global memory were read again by every block of
-// channels, and mma.sync took half of the second product's time: 16384 tokens 108 us, 86 now; 4096
-// tokens 37.2 and 34.6. In a tile of few tokens the 128 rows are mostly empty: 333 tokens of 20 adapters 20.7 us,
+// channels, and mma.sync took half of the second product's time: 16384 tokens 108 us, 87 now; 4096
+// tokens 37.2 and 31.5. In a tile of few tokens the 128 rows are mostly empty: 333 tokens of 20 adapters 20.7 us,
 // 19 without.)
 //
 // Bound: few tokens, latency of two dependent launches; many, HBM (x once, base and C) and the
 // latencies of three. Measured on the device, 7168 -> 2112: 1 token of rank 16 4.8 us, 16 tokens with
 // adapters of rank 32 of their own 7.4 us (9.9 MB, 1.5 us at the copy bandwidth), 4096 tokens of 6
-// adapters of rank 64 34.6 us (100 MB, 15 us), 16384 tokens 86 us (381 MB, 56 us).
+// adapters of rank 64 31.5 us (100 MB, 15 us), 16384 tokens 87 us (381 MB, 56 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -425,55 +425,56 @@ __device__ __forceinline__ void split_bf16(const float (&v)[4], uint2 &hi, uint2
     lo = make_uint2(lb[0], lb[1]);
 }
 
-__device__ __forceinline__ float4 ld_cluster(uint32_t addr)
+__device__ __forceinline__ void st_cluster(uint32_t addr, const uint32_t *v)
 {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
 }
 
-// Where a block keeps its sums of token t: 64 ranks, pieces of 16 bytes spread over the banks.
-__device__ __forceinline__ uint32_t sums_at(int t, int piece) { return t * 256 + ((piece ^ (t & 15)) << 4); }
+// Tokens of a tile whose sums a block of its cluster adds up.
+__device__ __forceinline__ int cluster_tokens(const LongParams &lp, int count) { return (count <= kHalf ? kHalf : kTile) / lp.cluster; }
 
-// The sums of a cluster's blocks, added in their order, times the adapter's scale: u of this
-// block's share of the tokens, as two bf16 a number. High parts are `parts`: a line of 64 ranks for
+// Where a block keeps the sums of 64 ranks that block `from` of its cluster has of its token t: pieces of 16 bytes, spread
+// over the banks.
+__device__ __forceinline__ uint32_t sums_at(int from, int per, int t, int piece)
+{
+    return (from * per + t) * 256 + ((piece ^ (t & 15)) << 4);
+}
+
+// The sums that a cluster's blocks gave this one, added in the blocks' order, times the adapter's scale: u of
+// its share of the tokens, as two bf16 a number. High parts are `parts`: a line of 64 ranks for
 // every token, tokens in the order of the tiles, pieces of 16 bytes in the order that an MMA's operand has them
 // in shared memory; then the low parts.
 __device__ __forceinline__ void sum_cluster(const LongParams &lp, const uint8_t *smem, int4 rec, int rank, int own)
 {
     const LoraParams &p = lp.l;
     const float scale = p.scales ? __ldcg(p.scales + rec.x) : 1.0f;
-    const int size = lp.cluster, cols = (rank + 15) / 16 * 16, per = (rec.z <= kHalf ? kHalf : kTile) / size;
+    const int cols = (rank + 15) / 16 * 16, per = cluster_tokens(lp, rec.z);
     for (int i = threadIdx.x; i < per * 8; i += 128) {
         const int t = own * per + (i >> 3), r = 8 * (i & 7);
         if (t >= rec.z || r >= cols) continue;
-        const uint32_t at0 = smem_u32(smem) + sums_at(t, r >> 2), at1 = smem_u32(smem) + sums_at(t, (r >> 2) + 1);
-        float4 some[8][2];
+        float v[8];
 #pragma unroll
-        for (int s = 0; s < 8; ++s)
-            if (s < size && r < p.R) {
-                some[s][0] = ld_cluster(mapa_shared(at0, s));
-                some[s][1] = ld_cluster(mapa_shared(at1, s));
-            }
-        uint2 h[2], l[2];
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int k = 0; k < 8; ++k) v[k] = 0.0f;
+        if (r < p.R)
 #pragma unroll
             for (int s = 0; s < 8; ++s) {
-                if (!(s < size && r < p.R)) continue;
-                v[0] += some[s][half].x;
-                v[1] += some[s][half].y;
-                v[2] += some[s][half].z;
-                v[3] += some[s][half].w;
+                if (s >= lp.cluster) break;
+                const float4 x = *reinterpret_cast<const float4 *>(smem + sums_at(s, per, i >> 3, r >> 2));
+                const float4 y = *reinterpret_cast<const float4 *>(smem + sums_at(s, per, i >> 3, (r >> 2) + 1));
+                v[0] += x.x;
+                v[1] += x.y;
+                v[2] += x.z;
+                v[3] += x.w;
+                v[4] += y.x;
+                v[5] += y.y;
+                v[6] += y.z;
+                v[7] += y.w;
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = r + 4 * half + k < rank ? v[k] * scale : 0.0f;
-            split_bf16(v, h[half], l[half]);
-        }
+        for (int k = 0; k < 8; ++k) v[k] = r + k < rank ? v[k] * scale : 0.0f;
+        uint2 h[2], l[2];
+        split_bf16({v[0], v[1], v[2], v[3]}, h[0], l[0]);
+        split_bf16({v[4], v[5], v[6], v[7]}, h[1], l[1]);
         uint8_t *to = lp.parts + (static_cast<int64_t>(rec.y) + t) * 128 + (((r >> 3) ^ (t & 7)) << 4);
         *reinterpret_cast<uint4 *>(to) = make_uint4(h[0].x, h[0].y, h[1].x, h[1].y);
         *reinterpret_cast<uint4 *>(to + static_cast<int64_t>(p.T) * 128) = make_uint4(l[0].x, l[0].y, l[1].x, l[1].y);
@@ -588,33 +589,47 @@ __global__ void __launch_bounds__(kLongThreads, 2) lora_shrink_long_kernel(const
         const bool done = mbar_wait_warp(&sh.done, 0, &g_lora_error, kErrWaitAccum);
         tc_fence_after();
         const int t = 32 * warp + lane;              // this lane's token
-        if (ok && done && 32 * warp < count) {
+        const uint32_t sums = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+        if constexpr (CLUSTER) {
+            uint32_t v[2 * 32];                      // up to 64 ranks
+            if (32 * warp < count) {
+                tmem_ld32(sums, *reinterpret_cast<uint32_t(*)[32]>(v));
+                if (p.R > 32) tmem_ld32(sums + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+                tmem_ld_wait();
+                if (!steps)
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) v[j] = 0;
+            }
+            __syncwarp();
+            cluster_sync();                          // every block's products are complete: the rings' memory is free
+            const int per = cluster_tokens(lp, count);
+            if (t < count)
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (4 * j < p.R) st_cluster(mapa_shared(smem_u32(smem) + sums_at(own, per, t % per, j), t / per), v + 4 * j);
+            __syncwarp();
+            cluster_sync();
+            sum_cluster(lp, smem, rec, rank_of(p, adapter), own);
+        } else if (ok && done && 32 * warp < count) {
             float *u = p.u + (static_cast<int64_t>(own) * p.T + (t < count ? sh.tok[t] : 0)) * p.R;
             for (int c0 = 0; c0 < p.R; c0 += 32) {
                 uint32_t v[32];
                 // 32 columns: those beyond the MMA's are not stored
-                tmem_ld32(tmem + c0 + (static_cast<uint32_t>(warp * 32) << 16), v);
+                tmem_ld32(sums + c0, v);
                 tmem_ld_wait();
                 if (t < count)
 #pragma unroll
                     for (int j = 0; j < 32; j += 4)
-                        if (c0 + j < p.R) {
-                            const uint4 sums = steps ? make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]) : make_uint4(0, 0, 0, 0);
-                            // in the place of the ring, which is empty
-                            if constexpr (CLUSTER)
-                                *reinterpret_cast<uint4 *>(smem + sums_at(t, (c0 + j) / 4)) = sums;
-                            else
-                                *reinterpret_cast<uint4 *>(u + c0 + j) = sums;
-                        }
+                        if (c0 + j < p.R)
+                            *reinterpret_cast<uint4 *>(u + c0 + j) =
+                                steps ? make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]) : make_uint4(0, 0, 0, 0);
             }
         }
     }
     __syncwarp();
-    if constexpr (CLUSTER) {
+    if (CLUSTER && warp >= 4) {
         cluster_sync();
-        if (warp < 4) sum_cluster(lp, smem, rec, rank_of(p, adapter), own);
-        __syncwarp();
-        cluster_sync();                  // nobody leaves while others read its sums
+        cluster_sync();
     }
     tc_fence_before();
     __syncthreads();
