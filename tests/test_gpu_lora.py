@@ -230,7 +230,7 @@ def test_two_graphs_that_share_a_workspace():
     assert mx.get_device_error() == 0
 
 
-@pytest.mark.parametrize("T", [16, 300])
+@pytest.mark.parametrize("T", [16, 300, 3000])
 def test_two_streams_at_once(T):
     cases = [case(T, 1024, 512, 32, 5, seed=i) for i in range(2)]
     want = [mx.lora_add(*c) for c in cases]
