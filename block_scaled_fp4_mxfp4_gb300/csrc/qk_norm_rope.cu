@@ -4,7 +4,7 @@
 // r = (mean x^2 + eps)^-1/2, and pairs (y_i, y_j) turned by the angle i of p. Both
 // are linear in x once r is known, so an element is
 //   out_i = r (x_i a_i + x_j b_i),  a_i = w_i cos, b_i = -+ w_j sin,
-// (a = w, b = 0 where nothing turns), and a, b are the same for all heads of a token.
+// (r x_i w_i where nothing turns), and a, b are the same for all heads of a token.
 //
 // Bound: HBM (2 bytes read, 2 written an element). A lane has two 16-byte vectors of a
 // head: in the layout of halves the two whose elements turn with each other, so that
@@ -12,7 +12,7 @@
 // heads of one token, which share a and b; four of a group's heads are on their way at a
 // time, by cp.async, so that they hold no registers. Arithmetic in pairs of floats (mul
 // and fma of f32x2: one issue for two). Measured: 8192 tokens of 64 + 8 heads of 128 51 us (302 MB,
-// 45 us at the copy bandwidth), 16 tokens of 32 + 8 2.2 us; one vector a lane with its
+// 45 us at the copy bandwidth), 53 us interleaved, 16 tokens of 32 + 8 2.2 us; one vector a lane with its
 // partner by shuffles was 105 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -97,6 +97,16 @@ __device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c)
 struct Vec {
     Pair p[4];
 };
+// c += a b where `on`.
+__device__ __forceinline__ void fma_if(bool on, const Vec &a, const Vec &b, Vec &c)
+{
+    asm("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %12, 0;\n\t"
+        "@p fma.rn.f32x2 %0, %4, %8, %0;\n\t@p fma.rn.f32x2 %1, %5, %9, %1;\n\t"
+        "@p fma.rn.f32x2 %2, %6, %10, %2;\n\t@p fma.rn.f32x2 %3, %7, %11, %3;\n\t}"
+        : "+l"(c.p[0].v), "+l"(c.p[1].v), "+l"(c.p[2].v), "+l"(c.p[3].v)
+        : "l"(a.p[0].v), "l"(a.p[1].v), "l"(a.p[2].v), "l"(a.p[3].v), "l"(b.p[0].v), "l"(b.p[1].v), "l"(b.p[2].v),
+          "l"(b.p[3].v), "r"(static_cast<int>(on)));
+}
 template <bool F16>
 __device__ __forceinline__ Vec unpack(const uint4 &v)
 {
@@ -153,8 +163,13 @@ __device__ __noinline__ float2 rescaled(uint4 raw0, uint4 raw1, bool odd, float 
     return make_float2(s, m == 0.0 ? 0.0f : static_cast<float>(1.0 / sqrt(m)));
 }
 
+// Vectors of a head that turn: none, all, or some of them. 8192 tokens of 72 heads of 128: 48.3, 50.8 and 54.6 us (half
+// of the head); the code for some took 50.3 and 54.1 for none and all. (With every product taken, those of
+// vectors that do not turn by zero, half a head was 52.4 us, but an infinity came out at its neighbour as NaN.)
+enum Turning { kNone, kAll, kSome };
+
 // Heads h0 .. h1 - 1 of one token's queries or keys (which: 0, 1).
-template <bool F16, bool INTER, int LPH, bool FULL>
+template <bool F16, bool INTER, int LPH, bool FULL, Turning TURN>
 __device__ __forceinline__ void heads_of(const QkParams &p, int which, int64_t t, int64_t pos, int h0, int h1, int j, int hv,
                                          int v0, int v1, bool in0, bool in1, uint4 *slots)
 {
@@ -179,7 +194,10 @@ __device__ __forceinline__ void heads_of(const QkParams &p, int which, int64_t t
 #pragma unroll
     for (int i = 0; i < kAhead - 1; ++i) request(h0 + G * i, i);
 
-    // what an element is multiplied with (a), and what its partner is (b)
+    // What an element is multiplied with (a), and what its partner is (b): of vectors that turn only. (A product with
+    // zero would take a partner's infinity or NaN to an element that it has nothing to do with.)
+    const bool turns0 = TURN == kAll || (TURN == kSome && (INTER ? 8 * v0 < p.rot : j < hv));
+    const bool turns1 = TURN == kAll || (TURN == kSome && (INTER ? 8 * v1 < p.rot : j < hv));
     Vec a0, a1, b0, b1;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -203,8 +221,8 @@ __device__ __forceinline__ void heads_of(const QkParams &p, int which, int64_t t
         if (pos < 0 || pos >= p.P) {
             bad = __int_as_float(0x7FC00000);
         } else if constexpr (INTER) {
-            if (in0 && 8 * v0 < p.rot) turn_pairs(v0, a0, b0);
-            if (in1 && 8 * v1 < p.rot) turn_pairs(v1, a1, b1);
+            if (in0 && turns0) turn_pairs(v0, a0, b0);
+            if (in1 && turns1) turn_pairs(v1, a1, b1);
         } else if (j < hv) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -269,17 +287,29 @@ __device__ __forceinline__ void heads_of(const QkParams &p, int which, int64_t t
         }
         r += bad;
         const Pair r2 = pair(r, r);
-        Vec o0, o1;
+        Vec o0, o1, y0 = x1, y1 = x0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            Pair y0 = x1.p[i], y1 = x0.p[i];
+            o0.p[i] = mul(x0.p[i], a0.p[i]);
+            o1.p[i] = mul(x1.p[i], a1.p[i]);
             if constexpr (INTER) {
                 const float2 f0 = floats(x0.p[i]), f1 = floats(x1.p[i]);
-                y0 = pair(f0.y, f0.x);
-                y1 = pair(f1.y, f1.x);
+                y0.p[i] = pair(f0.y, f0.x);
+                y1.p[i] = pair(f1.y, f1.x);
             }
-            o0.p[i] = mul(fma(y0, b0.p[i], mul(x0.p[i], a0.p[i])), r2);
-            o1.p[i] = mul(fma(y1, b1.p[i], mul(x1.p[i], a1.p[i])), r2);
+            if constexpr (TURN == kAll) {
+                o0.p[i] = fma(y0.p[i], b0.p[i], o0.p[i]);
+                o1.p[i] = fma(y1.p[i], b1.p[i], o1.p[i]);
+            }
+        }
+        if constexpr (TURN == kSome) {
+            fma_if(turns0, y0, b0, o0);
+            fma_if(turns1, y1, b1, o1);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            o0.p[i] = mul(o0.p[i], r2);
+            o1.p[i] = mul(o1.p[i], r2);
         }
         out0 = pack<F16>(o0);
         out1 = pack<F16>(o1);
@@ -300,7 +330,7 @@ __device__ __forceinline__ void heads_of(const QkParams &p, int which, int64_t t
     }
 }
 
-template <bool F16, bool INTER, int LPH, bool FULL>
+template <bool F16, bool INTER, int LPH, bool FULL, Turning TURN>
 __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kernel(const QkParams p)
 {
     __shared__ uint4 slots[2 * kAhead * kThreads];
@@ -323,8 +353,8 @@ __global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kernel(const QkParam
     int64_t pos = 0;
     if (p.rot) pos = p.pos64 ? static_cast<const int64_t *>(p.positions)[t] : static_cast<const int32_t *>(p.positions)[t];
     const int hq = p.heads[0];
-    if (h0 < hq) heads_of<F16, INTER, LPH, FULL>(p, 0, t, pos, h0, min(h1, hq), j, hv, v0, v1, in0, in1, slots);
-    if (h1 > hq) heads_of<F16, INTER, LPH, FULL>(p, 1, t, pos, max(h0, hq) - hq, h1 - hq, j, hv, v0, v1, in0, in1, slots);
+    if (h0 < hq) heads_of<F16, INTER, LPH, FULL, TURN>(p, 0, t, pos, h0, min(h1, hq), j, hv, v0, v1, in0, in1, slots);
+    if (h1 > hq) heads_of<F16, INTER, LPH, FULL, TURN>(p, 1, t, pos, max(h0, hq) - hq, h1 - hq, j, hv, v0, v1, in0, in1, slots);
 }
 
 template <bool F16, bool INTER, int LPH>
@@ -347,8 +377,15 @@ cudaError_t launch_lph(QkParams p, int num_sms, cudaStream_t stream)
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     // every lane has two vectors of a head of 64, 128 or 256
-    if (p.D == 16 * LPH) return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<F16, INTER, LPH, true>, p);
-    return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<F16, INTER, LPH, false>, p);
+    const bool full = p.D == 16 * LPH;
+    if (p.rot == p.D)
+        return full ? cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<F16, INTER, LPH, true, kAll>, p)
+                    : cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<F16, INTER, LPH, false, kAll>, p);
+    if (p.rot)
+        return full ? cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<F16, INTER, LPH, true, kSome>, p)
+                    : cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<F16, INTER, LPH, false, kSome>, p);
+    return full ? cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<F16, false, LPH, true, kNone>, p)
+                : cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<F16, false, LPH, false, kNone>, p);
 }
 
 template <bool F16, bool INTER>

@@ -58,7 +58,9 @@ MXFP4_API mxfp4_status_t lora_add(const void *X, int64_t ldx, const void *A, con
  *         (y_i cos - y_j sin, y_j cos + y_i sin),  j = i + rot / 2, or with `interleaved`
  *         the pair i is (2i, 2i + 1),
  * in fp32 with one rounding. Rows of any finite size are normalized; where mean + eps is 0 the
- * result is 0; an infinite x gives NaN in its place and its pair's, and zeros in the rest of its head.
+ * result is 0; an infinite x gives NaN in its place, and its pair's if it turns, and zeros in the rest of its
+ * head. Without a weight an infinity or NaN reaches no element but those two, and elements that
+ * nothing turns keep their bits (a NaN stays some NaN).
  *   table     : fp32 [P, rot], row p: the rot / 2 cosines, then the rot / 2 sines of position p.
  *   positions : int32 [T] (pos64 0) or int64 [T] (pos64 1). A position outside [0, P) gives
  *               NaN in all of its token's outputs.
