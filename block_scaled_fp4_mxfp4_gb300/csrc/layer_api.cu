@@ -3,6 +3,7 @@
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
+#include <utility>
 
 #include "internal.h"
 #include "layer.h"
@@ -25,6 +26,33 @@ mxfp4_status_t check_lora_sizes(int64_t T, int64_t K, int R, int L)
     if (T > kMaxWidth || K > kMaxWidth || K % 8 || R % 8 || R > LORA_MAX_RANK || L > LORA_MAX_ADAPTERS)
         return MXFP4_ERR_UNSUPPORTED_SHAPE;
     return MXFP4_OK;
+}
+
+// Do heads of D elements at t * st + h * sh (t < T, h < heads) share elements? They do if some |t * st + h * sh| < D
+// for a difference (t, h) other than none, |t| < T, |h| < heads.
+bool heads_overlap(int64_t T, int64_t heads, int64_t D, int64_t st, int64_t sh)
+{
+    // sizes alone matter: of h there are both signs. Beyond 2^62 a stride is no distance in memory
+    const int64_t most = int64_t(1) << 62;
+    st = st <= -most || st >= most ? most : std::abs(st);
+    sh = sh <= -most || sh >= most ? most : std::abs(sh);
+    if (T > 1 && st < D) return true;
+    if (heads > 1 && sh < D) return true;
+    if (T == 1 || heads == 1) return false;
+    // the usual layouts: all heads of a token, or all tokens of a head, before the next one
+    if (st >= sh && (st - D) / sh >= heads - 1) return false;
+    if (sh >= st && (sh - D) / st >= T - 1) return false;
+    // otherwise the dimension with fewer steps (46340 at most), against the next places of the other
+    if (T < heads) {
+        std::swap(T, heads);
+        std::swap(st, sh);
+    }
+    for (int64_t h = 1; h < heads; ++h) {
+        if (h > most / sh) return false;                 // from here on nothing in memory is that far
+        const int64_t at = h * sh, t = at / st, after = at - t * st;
+        if ((t < T && after < D) || (t + 1 < T && st - after < D)) return true;
+    }
+    return false;
 }
 
 }  // namespace
@@ -103,7 +131,7 @@ mxfp4_status_t qk_norm_rope(const void *q, int64_t q_st, int64_t q_sh, const voi
     const int64_t ost[2] = {qo_st, ko_st}, osh[2] = {qo_sh, ko_sh};
     const int heads[2] = {Hq, Hk};
     for (int i = 0; i < 2; ++i)
-        if (heads[i] && ((T > 1 && std::abs(ost[i]) < D) || (heads[i] > 1 && std::abs(osh[i]) < D))) return MXFP4_ERR_INVALID_ARG;
+        if (heads[i] && heads_overlap(T, heads[i], D, ost[i], osh[i])) return MXFP4_ERR_INVALID_ARG;
     if ((Hq && q == q_out && (q_st != qo_st || q_sh != qo_sh)) || (Hk && k == k_out && (k_st != ko_st || k_sh != ko_sh)))
         return MXFP4_ERR_INVALID_ARG;
     if ((Hq && (!aligned(q, 16) || !aligned(q_out, 16))) || (Hk && (!aligned(k, 16) || !aligned(k_out, 16))) ||

@@ -66,8 +66,9 @@ MXFP4_API mxfp4_status_t lora_add(const void *X, int64_t ldx, const void *A, con
  *               NaN in all of its token's outputs.
  *   q, k, q_out, k_out : type dtype (bf16 or fp16), rows of D; strides in elements between
  *               tokens (st) and heads (sh), any multiples of 8, so that views of a joint
- *               projection need no copy; an output's of at least D in size where there are two or
- *               more of them. An output may be its own input (same pointer and strides).
+ *               projection need no copy; an output's such that no two of its heads share elements
+ *               (refused otherwise). An output may be its own input (same pointer and strides) and
+ *               overlaps nothing else.
  *   q_weight, k_weight : type dtype [D], or NULL; elements 0 or 2^-40 to 2^40 in size.
  * T, Hq, Hk >= 0 (zero heads: that tensor is not touched); D a positive multiple of 8 up to 256;
  * 0 <= rot <= D, a multiple of 16, with `interleaved` of 8 (rot 0: no table and no positions);
