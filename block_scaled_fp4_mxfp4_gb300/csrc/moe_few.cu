@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kRouterThreads) moe_few_router_kernel(const Ro
 constexpr int kTokenThreads = 512;
 
 struct TokenParams {
-    const uint16_t *h, *w;
+    const uint16_t *h, *w, *router;
     const float *part, *part_ss;
     const float *bias;                  // [E] or null
     uint8_t *xd;                        // [T][6][H / 2] digits of y
@@ -259,7 +259,7 @@ struct TokenParams {
     int *ids_out;                       // the caller's, or null
     float *weights_out;
     int T, H, E, k, slices, groups, topk_groups, group_top, sigmoid, renorm;
-    float heps, root_h, scale;          // H eps, sqrt(H)
+    float eps, heps, root_h, scale;     // H eps, sqrt(H)
 };
 
 // A key that orders as the values do, NaN above all; 0 stands for "none".
@@ -288,14 +288,85 @@ __device__ __forceinline__ void add(Two &a, float hi, float lo)
     a.hi = s;
 }
 
+// Rows are taken as they are while the sum of their squares and H eps lie in these bounds: squares and products with
+// weights (up to 2^40) and the router's elements (up to 2^20) then stay in fp32.
+constexpr float kLeastSum = 0x1p-80f, kMostSum = 0x1p100f;
+
+// Other rows, by a whole block: a power of two s that brings the largest value to 1 or 2, and r for the values times s.
+// Rows of zeros, and such that are not finite, keep what they have (s = 0). (A pass over the row, and over the router's matrix
+// for its logits: 31 us more for a token of 7168 channels and 32 experts.)
+__device__ __noinline__ float2 rescaled(const TokenParams &p, int t, uint32_t *top, float2 *part)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint4 *row = reinterpret_cast<const uint4 *>(p.h + static_cast<int64_t>(t) * p.H);
+    uint32_t most = 0;
+    for (int v = tid; v < p.H / 8; v += kTokenThreads) {
+        const uint4 h = row[v];
+        const uint32_t a[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) most = max(most, max(a[i] & 0x7FFFu, a[i] >> 16 & 0x7FFFu));
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) top[warp] = most;
+    __syncthreads();
+    most = __reduce_max_sync(0xffffffffu, top[lane % (kTokenThreads / 32)]);
+    if (most == 0 || most >= 0x7F80u) return make_float2(0.0f, 0.0f);
+    const int e = max(-126, min(126, ilogbf(__uint_as_float(most << 16))));
+    const float s = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    Two ss{0.0f, 0.0f};
+    for (int v = tid; v < p.H / 8; v += kTokenThreads) {
+        const uint4 h = row[v];
+        const uint32_t a[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = bf16x2(a[i]);
+            add(ss, f.x * s * (f.x * s), 0.0f);
+            add(ss, f.y * s * (f.y * s), 0.0f);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) add(ss, __shfl_xor_sync(0xffffffffu, ss.hi, o), __shfl_xor_sync(0xffffffffu, ss.lo, o));
+    if (lane == 0) part[warp] = make_float2(ss.hi, ss.lo);
+    __syncthreads();
+    double m = 0.0;
+    for (int i = 0; i < kTokenThreads / 32; ++i) m += static_cast<double>(part[i].x) + part[i].y;
+    m = m / p.H + static_cast<double>(p.eps) * s * s;
+    return make_float2(s, static_cast<float>(1.0 / sqrt(m)));
+}
+
+// Their logits: a warp an expert.
+__device__ __noinline__ void rescaled_logits(const TokenParams &p, int t, float2 sr, float *logit)
+{
+    const int lane = threadIdx.x & 31;
+    const uint4 *row = reinterpret_cast<const uint4 *>(p.h + static_cast<int64_t>(t) * p.H);
+    for (int e = threadIdx.x >> 5; e < p.E; e += kTokenThreads / 32) {
+        const uint4 *weights = reinterpret_cast<const uint4 *>(p.router + static_cast<int64_t>(e) * p.H);
+        Two z{0.0f, 0.0f};
+        for (int v = lane; v < p.H / 8; v += 32) {
+            const uint4 h = row[v], w = reinterpret_cast<const uint4 *>(p.w)[v], q = weights[v];
+            const uint32_t a[4] = {h.x, h.y, h.z, h.w}, b[4] = {w.x, w.y, w.z, w.w}, c[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = bf16x2(a[i]), g = bf16x2(b[i]), k = bf16x2(c[i]);
+                add(z, f.x * sr.x * g.x * k.x, 0.0f);
+                add(z, f.y * sr.x * g.y * k.y, 0.0f);
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) add(z, __shfl_xor_sync(0xffffffffu, z.hi, o), __shfl_xor_sync(0xffffffffu, z.lo, o));
+        if (lane == 0) logit[e] = (z.hi + z.lo) * sr.y;
+    }
+}
+
 // Grid: tokens x parts of their channels; the first part of a token routes it too.
-__global__ void __launch_bounds__(kTokenThreads) moe_few_token_kernel(const TokenParams p)
+__global__ void __launch_bounds__(kTokenThreads) moe_few_token_kernel(const __grid_constant__ TokenParams p)
 {
     __shared__ float2 sums[kTokenThreads];
     __shared__ float logit[kMaxExperts], chosen_score[32];
     __shared__ uint32_t keys[kMaxExperts], group_key[kMaxExperts];
     __shared__ int rank[kMaxExperts], chosen[32];
     __shared__ float r_shared;
+    __shared__ int odd;                  // a row that is taken times a power of two
     __shared__ uint32_t table[128];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, t = blockIdx.x;
     const int v = blockIdx.y * kTokenThreads + tid;          // this thread's eight channels
@@ -320,13 +391,14 @@ __global__ void __launch_bounds__(kTokenThreads) moe_few_token_kernel(const Toke
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) add(ss, __shfl_xor_sync(0xffffffffu, ss.hi, o), __shfl_xor_sync(0xffffffffu, ss.lo, o));
         if (lane == 0) {
-            // a root of fp32 and one step of Newton's method: m r^2 - 1 to 2^-40. Below 2^-125 there is
-            // no h, and r^2 may leave fp32.
+            // a root of fp32 and one step of Newton's method: m r^2 - 1 to 2^-40. (Below 2^-125 r^2 may leave fp32; a
+            // row of zeros keeps the 0, any other is taken again.)
             add(ss, p.heps, 0.0f);
             const float r0 = rsqrtf(ss.hi);
             const float q = r0 * r0, qe = fmaf(r0, r0, -q);
             const float e = fmaf(ss.hi, q, -1.0f) + (fmaf(ss.hi, qe, ss.lo * q));
             r_shared = ss.hi < 0x1p-125f || isinf(ss.hi) ? 0.0f : fmaf(r0 * p.root_h, -0.5f * e, r0 * p.root_h);
+            odd = !(ss.hi >= kLeastSum && ss.hi <= kMostSum);
         }
     }
     // logits: `parts` threads an expert over interleaved slices, added in a fixed order
@@ -348,7 +420,16 @@ __global__ void __launch_bounds__(kTokenThreads) moe_few_token_kernel(const Toke
         sums[tid] = make_float2(z.hi, z.lo);
     }
     __syncthreads();
-    const float rf = r_shared;
+    float rf = r_shared, hs = 1.0f;
+    bool again = false;
+    if (odd) {
+        const float2 sr = rescaled(p, t, keys, sums);
+        again = sr.x != 0.0f;
+        if (again) {
+            hs = sr.x;
+            rf = sr.y;
+        }
+    }
     {
         // y in MXFP8, four lanes a block of 32
         // only now: H may be X or residual, which the launch before read
@@ -359,8 +440,8 @@ __global__ void __launch_bounds__(kTokenThreads) moe_few_token_kernel(const Toke
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 a = bf16x2(ha[i]), b = bf16x2(wa[i]);
-            y[2 * i] = a.x * b.x * rf;
-            y[2 * i + 1] = a.y * b.y * rf;
+            y[2 * i] = a.x * hs * b.x * rf;
+            y[2 * i + 1] = a.y * hs * b.y * rf;
             amax = max(amax, max(__float_as_uint(y[2 * i]) & 0x7FFFFFFFu, __float_as_uint(y[2 * i + 1]) & 0x7FFFFFFFu));
         }
         amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
@@ -380,7 +461,9 @@ __global__ void __launch_bounds__(kTokenThreads) moe_few_token_kernel(const Toke
         }
     }
     if (blockIdx.y > 0) return;
-    if (tid < p.E) {
+    if (again) {
+        rescaled_logits(p, t, make_float2(hs, rf), logit);
+    } else if (tid < p.E) {
         Two z{sums[tid].x, sums[tid].y};
         for (int i = 1; i < parts; ++i) add(z, sums[i * p.E + tid].x, sums[i * p.E + tid].y);
         logit[tid] = (z.hi + z.lo) * rf;
@@ -1124,6 +1207,7 @@ cudaError_t launch_moe_few(const MoeFewArgs &a, const MoeFewLayout &l, cudaStrea
     memset(&t, 0, sizeof(t));
     t.h = r.h;
     t.w = a.w;
+    t.router = a.router;
     t.part = r.part;
     t.part_ss = r.part_ss;
     t.bias = a.route.bias;
@@ -1145,6 +1229,7 @@ cudaError_t launch_moe_few(const MoeFewArgs &a, const MoeFewLayout &l, cudaStrea
     t.group_top = a.route.group_top;
     t.sigmoid = a.route.sigmoid;
     t.renorm = a.route.renorm;
+    t.eps = a.eps;
     t.heps = static_cast<float>(static_cast<double>(a.H) * a.eps);
     t.root_h = static_cast<float>(std::sqrt(static_cast<double>(a.H)));
     t.scale = a.route.scale;

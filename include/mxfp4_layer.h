@@ -96,11 +96,12 @@ MXFP4_API size_t mxfp4_moe_layer_workspace_bytes(int64_t T, int k, int E, int64_
  *   out[t]  = bf16_rne( sum_j weights[t, j] * ( act_j . W2[e]^T ) ),  e = ids[t, j],
  *   act_j   = MXFP8( silu(q . G[e]^T) * (q . U[e]^T) ),  q = MXFP8(y),
  * with sums, silu and the order of the weighted sum as in mxfp4_moe_experts; the codes of y
- * and act are those of fp32 arithmetic. Magnitudes of h, and of h * weight: 0 or 2^-60 to 2^50;
- * infinities and NaN stay in their tokens.
+ * and act are those of fp32 arithmetic. Rows of h of any finite size are normalized; an infinite h gives
+ * NaN in its token. Infinities and NaN stay in their tokens.
  *   X, residual, H : bf16 [T, Hd], row strides ldx, ldr, ldh. H (out, NULL: not stored)
  *                    may be X or residual itself (same pointer and stride).
- *   weight : bf16 [Hd].    router : bf16 [E, Hd], contiguous.    bias : fp32 [E] or NULL.
+ *   weight : bf16 [Hd], elements 0 or 2^-40 to 2^40 in size.    bias : fp32 [E] or NULL.
+ *   router : bf16 [E, Hd], contiguous, elements up to 2^20 in size.
  *   W13q, W13_sf, W2q, W2_sf : as in mxfp4_moe_experts, Hd and I its H and I.
  *   out    : bf16 [T, Hd], row stride ldo; may be X or residual where H is not.
  *   ids, out_weights : out, int32 and fp32 [T, k], or NULL.
