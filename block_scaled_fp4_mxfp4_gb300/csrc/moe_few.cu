@@ -226,15 +226,18 @@ __global__ void __launch_bounds__(kRouterThreads) moe_few_router_kernel(const Ro
     if ((e & ~7) < p.E) {
         for (int tk = 0; tk < p.T; ++tk) {
             const float4 *q = reinterpret_cast<const float4 *>(&hw[tk][sub * kSub]);
-            float s = 0.0f;
+            // four chains of four: a product (exact: 16 bits by 8) passes three additions there, two that join
+            // the chains and two that join the lanes. One chain lost small terms behind a large one in 15.
+            float4 s4;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float4 f = q[i];
-                s = fmaf(f.x, wr[4 * i], s);
-                s = fmaf(f.y, wr[4 * i + 1], s);
-                s = fmaf(f.z, wr[4 * i + 2], s);
-                s = fmaf(f.w, wr[4 * i + 3], s);
+                s4.x = i ? fmaf(f.x, wr[4 * i], s4.x) : f.x * wr[0];
+                s4.y = i ? fmaf(f.y, wr[4 * i + 1], s4.y) : f.y * wr[1];
+                s4.z = i ? fmaf(f.z, wr[4 * i + 2], s4.z) : f.z * wr[2];
+                s4.w = i ? fmaf(f.w, wr[4 * i + 3], s4.w) : f.w * wr[3];
             }
+            float s = (s4.x + s4.y) + (s4.z + s4.w);
             s += __shfl_xor_sync(0xffffffffu, s, 1);
             s += __shfl_xor_sync(0xffffffffu, s, 2);
             if (sub == 0 && e < p.E) p.part[(static_cast<int64_t>(blockIdx.x) * p.T + tk) * p.E + e] = s;

@@ -90,9 +90,10 @@ MXFP4_API size_t mxfp4_moe_layer_workspace_bytes(int64_t T, int k, int E, int64_
  * product, moe_route and mxfp4_moe_experts):
  *   h       = X + residual, in fp32, rounded to bf16 (residual NULL: h = X)
  *   y       = h / sqrt(mean(h^2) + eps) * weight, in fp32 (0 where mean + eps is 0)
- *   logits  = y . router^T, of y unrounded, good to 2^-22 of the sum of their terms' sizes
+ *   logits  = y . router^T, of y unrounded, good to 2^-20 of the sum of their terms' sizes
  *   ids, weights = moe_route of those logits (see there for score .. scale), but decided by
- *             scores in fp32: where two differ by less than 2^-20 either may come first
+ *             scores in fp32, good to 2^-20 beside what the logits' error makes of them: of two
+ *             choices that lie closer than these errors either may come first
  *   out[t]  = bf16_rne( sum_j weights[t, j] * ( act_j . W2[e]^T ) ),  e = ids[t, j],
  *   act_j   = MXFP8( silu(q . G[e]^T) * (q . U[e]^T) ),  q = MXFP8(y),
  * with sums, silu and the order of the weighted sum as in mxfp4_moe_experts; the codes of y
