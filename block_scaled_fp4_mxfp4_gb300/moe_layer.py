@@ -11,7 +11,9 @@ bf16, so the logits are rounded to bf16). The next layer's norm adds ``out`` to
 
 A layer made with ``few_tokens`` runs up to that many tokens (16 at most) in one
 call instead, ``mxfp4_moe_layer``, whose router reads the norm's output unrounded
-and whose logits stay in fp32.
+and whose logits stay in fp32. It decides by scores in fp32 where ``moe_route``
+decides exactly, and takes norm weights of 0 or 2^-40 to 2^40 in size and router
+elements up to 2^20; rows may be of any size in both.
 
     python -m block_scaled_fp4_mxfp4_gb300.moe_layer [--tokens 1 16 256 4096] [--few-tokens 16]
 
@@ -26,9 +28,10 @@ from . import mxfp4 as mx
 
 class MoeLayer:
     """Quantizes the experts' bf16 weights once and keeps a workspace for up to
-    ``max_tokens`` tokens (1.3 GB at 4096 of 8 choices, 7168 x 2048). Layers that
-    run one after another on one stream may share one: pass the first one's
-    ``workspace`` to the others.
+    ``max_tokens`` tokens (1.3 GB at 4096 of 8 choices, 7168 x 2048), and with
+    ``few_tokens`` a second one for those calls (6 MB at 16 of 8 choices). Layers
+    that run one after another on one stream may share them: pass the first one's
+    ``workspace`` and ``few_workspace`` to the others.
 
     gate, up : bf16 [E, I, H]     down : bf16 [E, H, I]
     router   : bf16 [E, H]        norm : bf16 [H]
@@ -37,7 +40,8 @@ class MoeLayer:
     """
 
     def __init__(self, gate, up, down, router, norm, k, max_tokens, bias=None, score="softmax", groups=1,
-                 topk_groups=1, renormalize=True, scale=1.0, eps=1e-6, group_top=2, workspace=None, few_tokens=0):
+                 topk_groups=1, renormalize=True, scale=1.0, eps=1e-6, group_top=2, workspace=None, few_tokens=0,
+                 few_workspace=None):
         E, I, H = gate.shape
         self.E, self.I, self.H, self.k = E, I, H, k
         self.router, self.norm, self.bias, self.eps = router, norm, bias, eps
@@ -51,16 +55,23 @@ class MoeLayer:
         for e in range(E):
             mx.mxfp4_quantize(torch.cat([gate[e], up[e]]), Aq=self.w13[e], A_sf=self.s13[e])
             mx.mxfp4_quantize(down[e], Aq=self.w2[e], A_sf=self.s2[e])
-        if workspace is None:
-            workspace = mx.moe_experts_workspace(max_tokens, k, E, H, I, dev)
-        elif workspace.numel() < mx.moe_experts_workspace_bytes(max_tokens, k, E, H, I):
-            raise ValueError(f"workspace has {workspace.numel()} bytes, {max_tokens} tokens need "
-                             f"{mx.moe_experts_workspace_bytes(max_tokens, k, E, H, I)}")
-        self.workspace = workspace
         if not 0 <= few_tokens <= mx.MOE_LAYER_MAX_TOKENS:
             raise ValueError(f"few_tokens must be 0 to {mx.MOE_LAYER_MAX_TOKENS}, got {few_tokens}")
         self.few_tokens = few_tokens
-        self.few_workspace = mx.moe_layer_workspace(few_tokens, k, E, H, I, dev) if few_tokens else None
+        sizes = (k, E, H, I)
+        self.workspace = self._shared(workspace, mx.moe_experts_workspace_bytes(max_tokens, *sizes), max_tokens, dev)
+        self.few_workspace = None
+        if few_tokens:
+            self.few_workspace = self._shared(few_workspace, mx.moe_layer_workspace_bytes(few_tokens, *sizes), few_tokens,
+                                              dev)
+
+    @staticmethod
+    def _shared(workspace, need, tokens, dev):
+        if workspace is None:
+            return torch.empty(max(1, need), dtype=torch.uint8, device=dev)
+        if workspace.numel() < need:
+            raise ValueError(f"workspace has {workspace.numel()} bytes, {tokens} tokens need {need}")
+        return workspace
 
     def __call__(self, x, residual=None):
         """(out, h): the experts' sum and the residual stream, bf16 [T, H] (h = x without a residual)."""
