@@ -31,10 +31,10 @@ MXFP4_API size_t lora_workspace_bytes(int64_t T, int64_t K, int R, int L);
  * token t whose adapter is a = ids[t],
  *   C[t, n] = round( base[t, n] + scales[a] * sum_{r < ranks[a]} u[r] * B[a, n, r] ),
  *   u[r]    = sum_k X[t, k] * A[a, r, k],
- * both sums in fp32 and one rounding, to C's type; between the products u is
- * held to 2^-17 of itself (as two bf16). A token whose id is outside [0, L) has
- * no adapter: its row of C is that of base. Elements of A and B at or beyond an
- * adapter's rank are not used, whatever they hold.
+ * both sums in fp32 and one rounding, to C's type; between the products scales[a] * u[r]
+ * is held to 2^-17 of itself or 2^-134 (as two bf16; infinite beyond bf16's largest, and an infinity
+ * in B may come out as NaN). A token whose id is outside [0, L) has no adapter: its row of C is that
+ * of base. Elements of A and B at or beyond an adapter's rank are not used, whatever they hold.
  *   X      : bf16 [T, K], row stride ldx.     base, C : [T, N] of type dtype (bf16 or fp16),
  *            row strides ldb and ldc; C may be base itself (same pointer and stride).
  *   A      : bf16 [L, R, K], contiguous.      B : bf16 [L, N, R], contiguous.
@@ -97,7 +97,8 @@ MXFP4_API size_t mxfp4_moe_layer_workspace_bytes(int64_t T, int k, int E, int64_
  *   out[t]  = bf16_rne( sum_j weights[t, j] * ( act_j . W2[e]^T ) ),  e = ids[t, j],
  *   act_j   = MXFP8( silu(q . G[e]^T) * (q . U[e]^T) ),  q = MXFP8(y),
  * with sums, silu and the order of the weighted sum as in mxfp4_moe_experts; the codes of y
- * and act are those of fp32 arithmetic. Rows of h of any finite size are normalized; an infinite h gives
+ * and act are those of fp32 arithmetic, and enter the products exactly, but for blocks of 32 whose
+ * largest is below 2^-111: those values to 2^-127 each. Rows of h of any finite size are normalized; an infinite h gives
  * NaN in its token. Infinities and NaN stay in their tokens.
  *   X, residual, H : bf16 [T, Hd], row strides ldx, ldr, ldh. H (out, NULL: not stored)
  *                    may be X or residual itself (same pointer and stride).
