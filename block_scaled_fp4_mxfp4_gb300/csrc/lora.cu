@@ -23,14 +23,16 @@
 // Batches whose tiles are filled to a half or more, of up to 64 ranks, take both products by tcgen05: the blocks
 // that share a tile's K are a cluster, add their sums in shared memory and leave u as the two bf16 that the
 // second product loads as an operand. (Sums of splits through global memory were read again by every block of
-// channels, and mma.sync took half of the second product's time: 16384 tokens 108 us, 87 now; 4096
-// tokens 37.2 and 31.5. In a tile of few tokens the 128 rows are mostly empty: 333 tokens of 20 adapters 20.7 us,
-// 19 without.)
+// channels, and mma.sync took half of the second product's time: 7168 -> 2112, rank 64, 16384 tokens 108 us, 87 now; 4096
+// tokens 37.2 and 31.4. In a tile of few tokens the 128 rows are mostly empty: 333 tokens of 20 adapters up to
+// rank 24, 2048 -> 7168, 23.3 us, 17.6 without.)
 //
 // Bound: few tokens, latency of two dependent launches; many, HBM (x once, base and C) and the
 // latencies of three. Measured on the device, 7168 -> 2112: 1 token of rank 16 4.8 us, 16 tokens with
 // adapters of rank 32 of their own 7.4 us (9.9 MB, 1.5 us at the copy bandwidth), 4096 tokens of 6
-// adapters of rank 64 31.5 us (100 MB, 15 us), 16384 tokens 87 us (381 MB, 56 us).
+// adapters of rank 64 31.4 us (100 MB, 15 us), of rank 128 54.6, of rank 256 94.3; 16384 tokens of rank 64 87 us (381 MB, 56 us).
+// Grids and splits go by the adapters that are held, which the host knows, not by those that a batch uses: 64 tokens
+// of one adapter (rank 16, 4096 -> 4096) 9.4 us, 19.8 where 64 or 4096 are held; 4096 tokens 29.3, 79.8 of 4096.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -67,8 +69,8 @@ __device__ __forceinline__ int adapter_of(int id, int L) { return id >= 0 && id 
 // sums, ranks. In which order a tile's tokens stand does not matter to their results. A
 // thread keeps its first kSortKeep ids in registers; more are read again for their places. LONG (more ids than
 // the block keeps): a warp takes kSortKeep * 32 neighbouring ids at a time, in a prompt all of one
-// adapter, for which one atomic is enough. 16384 tokens 9 us, 13 with an atomic for every 32; up to
-// 8192 the ids lie better spread over all warps (333 tokens 1 us).
+// adapter, for which one atomic is enough: the whole call of 32768 tokens of 6 adapters (7168 -> 2112, rank 64) 151.2 us,
+// 155.8 with an atomic for every 32; of 16384 87.2 and 88.3. Up to 8192 the ids lie better spread over all warps.
 constexpr int kSortKeep = 8;
 template <int THREADS, bool LONG>
 __global__ void __launch_bounds__(THREADS) lora_sort_kernel(const LoraParams p)
@@ -402,7 +404,8 @@ __device__ __forceinline__ void mma_tc_bf16(uint32_t d_tmem, uint64_t adesc, uin
 }
 
 // 16 bytes from global to shared memory, of which the first `bytes` are copied and the others zeros. L2 asks for the row's next
-// 128 bytes too (128 tokens a stage: 32768 tokens 81.9 us, 78.9 so).
+// 128 bytes too: the whole call of 7168 -> 2112, rank 64, 32768 tokens 151.2 us, 156.8 without; 16384 87.2 and 88.4; 4096
+// 31.4 and 31.6.
 __device__ __forceinline__ void cp_async_or_zero(uint32_t smem_dst, const void *gsrc, uint32_t bytes)
 {
     asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(smem_dst), "l"(gsrc), "r"(bytes) : "memory");
