@@ -27,11 +27,11 @@
 // token, all ended at once, and product 2 stood still for 6 us until their results were
 // published: 45.5 us, 44.8 with 32.)
 //
-// Bound: HBM, the weights of the experts that some token chose: they stream at 6 to 6.5 TB/s, for
-// two thirds of the time. Routing before them takes 8 us and the last unit and the sum
+// Bound: HBM, the weights of the experts that some token chose: they stream at 6 to 6.5 TB/s in product 1, 60 to 65 % of
+// HBM's rate over the experts' kernel. Routing before them takes 7 us and the last unit and the sum
 // 4. Measured on the device, inputs changing: 1 token x 8 of 32 experts (7168 x 2048, 187 MB, 28 us
-// at the copy bandwidth) 45 us, 16 x 8 of 128 (2048 x 768, 207 MB, 31 us) 44 us, 5 x 6 of 40 (2560 x
-// 1408, 128 MB, 19 us) 35 us; the four calls for any number of tokens 64, 62 and 51 us.
+// at the copy bandwidth) 43.8 us, 16 x 8 of 128 (2048 x 768, 207 MB, 31 us) 42.4 us, 5 x 6 of 40 (2560 x
+// 1408, 128 MB, 19 us) 34.4 us; the four calls for any number of tokens 63, 61 and 50 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
